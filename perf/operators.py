@@ -237,8 +237,9 @@ def _plain_write(s):
     x = s["latent"].float()
     a = x.abs().amax(-1).clamp(min=2.0 ** -100)
     # E4M3 codes are moved as bytes: indexing has no 8-bit float form.
-    s["all"].view(torch.uint8).view(-1, LATENT)[at] = (x * (448.0 / a)[:, None]).to(F8).view(torch.uint8)
-    s["all_scale"].view(-1)[at] = a / 448.0
+    most = torch.full_like(a, 448.0)  # a number over a tensor would be a reciprocal and a product
+    s["all"].view(torch.uint8).view(-1, LATENT)[at] = (x * (most / a)[:, None]).to(F8).view(torch.uint8)
+    s["all_scale"].view(-1)[at] = a / most
     s["all_rope"].view(-1, ROPE)[at] = s["rope"]
     return [s["cache"], s["rope_cache"], s["cache_scale"]]
 
