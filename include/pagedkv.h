@@ -606,6 +606,175 @@ PKV_API int paged_attention_verify_fp8(void *out, int32_t out_dtype, const void 
                                        size_t workspace_bytes, void *stream);
 
 /*
+ * ---- Latent attention -------------------------------------------------------------
+ * Latent attention (MLA: "注意力演进与推理流程", section 4) caches one row a token
+ * that every head shares: a compressed latent c_j (latent_dim = 512 values, the
+ * keys and values of all heads are linear maps of it) and a rotated key r_j
+ * (rope_dim = 64 values) -- 576 values a token instead of 2 n_kv 128.  Two forms
+ * of the same attention:
+ *  - absorbed: the key map is multiplied into the query and the value map into
+ *    the output projection, so a head scores and averages the cached rows
+ *    themselves:  s_j = scale (<q_latent, c_j> + <q_rope, r_j>),
+ *    out = sum_j softmax(s)_j c_j  (512 values; decode and verify);
+ *  - expanded: keys and values of every head are computed from the rows first
+ *    (the caller's matrix product over rows that latent_gather read back), and a
+ *    prefill chunk attends over them:  s_j = scale (<q_nope, k_nope_j> +
+ *    <q_rope, r_j>),  out = sum_j softmax(s)_j v_j  (128 values).
+ * Conventions as above (streams, ownership, error codes, device-side checks),
+ * except that inputs may be strided where an entry point takes strides (in
+ * elements, multiples of 8; bases 16-byte aligned; the innermost dimension is
+ * contiguous).  Layouts of the pool, all contiguous, bases 16-byte aligned:
+ *   PKV_DTYPE_BF16      cache       : bf16 [num_blocks][16][576], a row = [c | r]
+ *   PKV_DTYPE_FP8_E4M3  cache       : uint8 E4M3 codes of c [num_blocks][16][512]
+ *                       rope_cache  : bf16 [num_blocks][16][64] (r is kept as it is)
+ *                       cache_scale : fp32 [num_blocks][16], c = code * scale
+ */
+typedef struct pkv_latent_desc {
+    int32_t num_blocks;  /* physical blocks in the pool (>= 1) */
+    int32_t block_size;  /* tokens per block; must be 16 */
+    int32_t latent_dim;  /* values of the shared latent; must be 512 */
+    int32_t rope_dim;    /* values of the rotated key; must be 64 */
+    int32_t dtype;       /* PKV_DTYPE_BF16, or PKV_DTYPE_FP8_E4M3 for the *_fp8 entry points and latent_gather */
+} pkv_latent_desc;
+
+/*
+ * latent_reshape_and_cache -- append new tokens' rows to the latent pool:
+ *     slot = slot_mapping[t];  cache[slot / 16][slot % 16][:] = [latent[t] | rope[t]]
+ * Bit-exact.  latent and rope are usually slices of one projection's rows.
+ *   latent       : bf16 [num_tokens][512], row t at latent + t * latent_stride
+ *   rope         : bf16 [num_tokens][64], row t at rope + t * rope_stride
+ *   slot_mapping : int32 [num_tokens], device; slots < 0 (padding) and slots
+ *                  >= num_blocks * 16 are skipped.  Two tokens with the same slot
+ *                  in one call race (undefined).
+ *   num_tokens   : >= 0 (0 enqueues nothing)
+ * Errors: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED / PKV_ERR_CUDA.
+ */
+PKV_API int latent_reshape_and_cache(const void *latent, int64_t latent_stride, const void *rope, int64_t rope_stride,
+                                     void *cache, const int32_t *slot_mapping, int32_t num_tokens,
+                                     const pkv_latent_desc *desc, void *stream);
+
+/*
+ * latent_reshape_and_cache_fp8 -- the same into an FP8 (E4M3) pool: the latent is
+ * quantised as kv_reshape_and_cache_fp8 quantises a head's row, with x = latent[t]:
+ *     a = max(max_k |x_k|, 2^-100);  code_k = E4M3(x_k * (448 / a));  scale = a / 448
+ * (each step one correctly rounded fp32 operation, so the codes are reproducible);
+ * the rotated key is copied.
+ * Errors: as latent_reshape_and_cache.
+ */
+PKV_API int latent_reshape_and_cache_fp8(const void *latent, int64_t latent_stride, const void *rope,
+                                         int64_t rope_stride, void *cache, void *rope_cache, float *cache_scale,
+                                         const int32_t *slot_mapping, int32_t num_tokens, const pkv_latent_desc *desc,
+                                         void *stream);
+
+/*
+ * latent_gather -- read cached rows back in the order of their sequences (for the
+ * expanded form): row cu_lens[b] + i of out is [c | r] of position i of sequence b,
+ * 0 <= i < cu_lens[b + 1] - cu_lens[b].  A bf16 pool is copied bit for bit; from an
+ * FP8 pool c = code * scale, rounded once to bf16.
+ *   out          : bf16 [total_rows][576], device, contiguous, 16-byte aligned; rows
+ *                  from cu_lens[num_seqs] on are left as they were
+ *   rope_cache, cache_scale : NULL for a bf16 pool, required for an FP8 pool
+ *   block_tables : int32 [num_seqs][max_blocks_per_seq]
+ *   cu_lens      : int32 [num_seqs + 1], device, non-decreasing, cu_lens[0] = 0
+ *   total_rows   : rows of out (>= 0; 0 enqueues nothing)
+ *   status       : device uint32 into which PKV_STATUS_* bits are ORed, or NULL
+ * A row whose position passes its table, or whose block id is outside
+ * [0, num_blocks), becomes zeros (PKV_STATUS_BAD_CONTEXT_LEN, _BAD_BLOCK_ID).
+ * Errors: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED / PKV_ERR_CUDA.
+ */
+PKV_API int latent_gather(void *out, const void *cache, const void *rope_cache, const float *cache_scale,
+                          const int32_t *block_tables, const int32_t *cu_lens, int32_t num_seqs,
+                          int32_t max_blocks_per_seq, int32_t total_rows, const pkv_latent_desc *desc,
+                          uint32_t *status, void *stream);
+
+/*
+ * latent_attention_workspace_size -- bytes of device workspace that
+ * latent_attention_decode and _fp8 need for these sizes on the current device (152
+ * SMs are assumed without a GPU): the status word (byte 0) and the partials of
+ * sequences whose keys several CTAs share.  Returns 0 for invalid arguments.
+ */
+PKV_API size_t latent_attention_workspace_size(int32_t num_seqs, int32_t q_per_seq, int32_t num_q_heads,
+                                               int32_t max_blocks_per_seq, const pkv_latent_desc *desc);
+
+/*
+ * latent_attention_decode -- absorbed attention of q_per_seq query rows per
+ * sequence over a bf16 latent pool.  Sequence b owns rows b * q_per_seq + i,
+ * 0 <= i < q_per_seq; row i sits at position ctx_b - q_per_seq + i and sees keys
+ * j <= that position (q_per_seq = 1: a decode step; above: the verification of
+ * draft tokens, whose rows are cached already).  For each head h:
+ *     s_j = scale (<q_latent[row][h], c_j> + <q_rope[row][h], r_j>)
+ *     out[row][h] = sum_j softmax(s)_j c_j
+ *   out       : out_dtype [num_seqs * q_per_seq][num_q_heads][512], contiguous,
+ *               16-byte aligned; PKV_DTYPE_FLOAT32 or PKV_DTYPE_BF16
+ *   q_latent  : bf16, (row, head) at q_latent + row * q_latent_row_stride +
+ *               head * q_latent_head_stride, 512 values; q_rope: the same, 64 values
+ *   block_tables, context_lens : as paged_attention_decode
+ *   num_seqs  : 1 .. 65535;  q_per_seq : 1 .. 16;  num_q_heads : 1 .. 1024
+ *   workspace : 256-byte aligned, latent_attention_workspace_size() bytes, status
+ *               word zeroed once (it is sticky); calls that share it must not overlap
+ * A sequence with ctx < 1 (PKV_STATUS_BAD_CONTEXT_LEN) or ctx < q_per_seq
+ * (PKV_STATUS_BAD_Q_LEN) gets zero rows; a length past the table counts as the
+ * table's length (PKV_STATUS_BAD_CONTEXT_LEN); a block with an invalid id
+ * contributes nothing (PKV_STATUS_BAD_BLOCK_ID).
+ * Errors: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED /
+ *         PKV_ERR_WORKSPACE_TOO_SMALL / PKV_ERR_CUDA.
+ */
+PKV_API int latent_attention_decode(void *out, int32_t out_dtype, const void *q_latent, int64_t q_latent_row_stride,
+                                    int64_t q_latent_head_stride, const void *q_rope, int64_t q_rope_row_stride,
+                                    int64_t q_rope_head_stride, const void *cache, const int32_t *block_tables,
+                                    const int32_t *context_lens, int32_t num_seqs, int32_t q_per_seq,
+                                    int32_t num_q_heads, int32_t max_blocks_per_seq, float scale,
+                                    const pkv_latent_desc *desc, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/*
+ * latent_attention_decode_fp8 -- the same over an FP8 pool, c_j = code * scale as
+ * latent_reshape_and_cache_fp8 wrote it.
+ */
+PKV_API int latent_attention_decode_fp8(void *out, int32_t out_dtype, const void *q_latent,
+                                        int64_t q_latent_row_stride, int64_t q_latent_head_stride, const void *q_rope,
+                                        int64_t q_rope_row_stride, int64_t q_rope_head_stride, const void *cache,
+                                        const void *rope_cache, const float *cache_scale, const int32_t *block_tables,
+                                        const int32_t *context_lens, int32_t num_seqs, int32_t q_per_seq,
+                                        int32_t num_q_heads, int32_t max_blocks_per_seq, float scale,
+                                        const pkv_latent_desc *desc, void *workspace, size_t workspace_bytes,
+                                        void *stream);
+
+/*
+ * latent_attention_prefill_chunk -- expanded causal attention of a chunk of new
+ * query rows per sequence.  Sequence b owns query rows cu_q_lens[b] ..
+ * cu_q_lens[b + 1] - 1 (q_len of them) and key rows cu_k_lens[b] .. cu_k_lens[b +
+ * 1] - 1 (k_len; the cached prefix and the chunk itself); query i sits at position
+ * k_len - q_len + i and sees keys j <= that position.  For each head h:
+ *     s_j = scale (<q[i][h][0:128], k_nope[j][h]> + <q[i][h][128:192], k_rope[j]>)
+ *     out[i][h] = sum_j softmax(s)_j v[j][h]
+ *   out       : out_dtype [total_q_rows][num_heads][128], contiguous, 16-byte aligned
+ *   q         : bf16, 192 values at q + row * q_row_stride + head * q_head_stride
+ *   k_nope, v : bf16, 128 values at (row, head); both take k_row_stride and
+ *               k_head_stride (usually the two halves of one [rows][heads][256] product)
+ *   k_rope    : bf16, 64 values a row, shared by the heads, at k_rope + row * k_rope_stride
+ *   cu_q_lens, cu_k_lens : int32 [num_seqs + 1], device, non-decreasing, from 0
+ *   max_q_len : host upper bound of every q_len (sizes the launch grid)
+ *   total_q_rows, total_k_rows : rows of q / out and of the keys
+ *   workspace : 256-byte aligned, latent_attention_prefill_workspace_size() bytes
+ *               (status word at byte 0, zeroed once)
+ * A sequence with q_len > k_len or q_len > max_q_len, or whose rows lie outside
+ * the tensors, sets PKV_STATUS_BAD_Q_LEN; its rows that can be addressed become
+ * zeros.  Rows of out past cu_q_lens[num_seqs] are left as they were.
+ * Errors: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED /
+ *         PKV_ERR_WORKSPACE_TOO_SMALL / PKV_ERR_CUDA.
+ */
+PKV_API size_t latent_attention_prefill_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t max_q_len,
+                                                       int32_t total_q_rows, int32_t total_k_rows);
+PKV_API int latent_attention_prefill_chunk(void *out, int32_t out_dtype, const void *q, int64_t q_row_stride,
+                                           int64_t q_head_stride, const void *k_nope, const void *v,
+                                           int64_t k_row_stride, int64_t k_head_stride, const void *k_rope,
+                                           int64_t k_rope_stride, const int32_t *cu_q_lens, const int32_t *cu_k_lens,
+                                           int32_t num_seqs, int32_t num_heads, int32_t max_q_len,
+                                           int32_t total_q_rows, int32_t total_k_rows, float scale, void *workspace,
+                                           size_t workspace_bytes, void *stream);
+
+/*
  * ---- Host block manager ---------------------------------------------------------
  * Hands out the pool's physical blocks to sequences and emits the block tables
  * and slot mappings the kernels above consume.  Sources: "注意力演进与推理流程",

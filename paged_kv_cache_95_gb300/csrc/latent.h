@@ -1,0 +1,69 @@
+// latent.h -- internal interface between latent_api.cu and the latent-attention kernels.
+#pragma once
+
+#include "launch.h"
+
+namespace pkv {
+
+constexpr int kLatentDim = 512;                      // values of the shared latent a token
+constexpr int kRopeDim = 64;                         // values of the rotated key a token
+constexpr int kLatentRow = kLatentDim + kRopeDim;    // a bf16 pool row
+constexpr int kNopeDim = 128;                        // expanded head: key part from the latent
+constexpr int kExpandedQk = kNopeDim + kRopeDim;     // expanded head: query / key values
+constexpr int kExpandedV = 128;                      // expanded head: value values
+
+// ---- cache write and read-back ------------------------------------------------
+struct LatentWriteParams {
+    const void *latent;  // bf16 rows of 512, latent_stride elements apart
+    const void *rope;    // bf16 rows of 64, rope_stride elements apart
+    int64_t latent_stride, rope_stride;
+    void *cache;         // bf16 [slots][576], or E4M3 codes [slots][512]
+    void *rope_cache;    // FP8 pool: bf16 [slots][64]
+    float *cache_scale;  // FP8 pool: [slots]
+    const int32_t *slot_mapping;
+    int64_t num_slots;
+    int32_t num_tokens;
+};
+cudaError_t launch_latent_write(const LatentWriteParams &p, bool fp8, int sm_count, cudaStream_t stream);
+
+struct LatentGatherParams {
+    void *out;  // bf16 [total_rows][576]
+    const void *cache, *rope_cache;
+    const float *cache_scale;
+    const int32_t *block_tables;
+    const int32_t *cu_lens;
+    uint32_t *status;
+    int32_t num_seqs, max_blocks, num_blocks, total_rows;
+};
+cudaError_t launch_latent_gather(const LatentGatherParams &p, bool fp8, cudaStream_t stream);
+
+// ---- absorbed attention -----------------------------------------------------------
+struct LatentDecodeParams {
+    void *out;  // [rows][heads][512], f32 or bf16
+    const void *q_latent, *q_rope;
+    int64_t ql_row, ql_head, qr_row, qr_head;  // strides in elements
+    const void *cache, *rope_cache;            // rope_cache, cache_scale: FP8 pool only
+    const float *cache_scale;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    uint32_t *status;
+    int32_t num_seqs, q_per_seq, heads, max_blocks, num_blocks;
+    float scale_log2;
+    int32_t out_bf16;
+};
+cudaError_t launch_latent_decode(const LatentDecodeParams &p, bool fp8, cudaStream_t stream);
+
+// ---- expanded attention of a prefill chunk --------------------------------------------
+struct LatentPrefillParams {
+    void *out;  // [rows][heads][128], f32 or bf16
+    const void *q, *k_nope, *v, *k_rope;
+    int64_t q_row, q_head, k_row, k_head, r_row;  // strides in elements
+    const int32_t *cu_q_lens, *cu_k_lens;
+    uint32_t *status;
+    int32_t num_seqs, heads, max_q_len, total_q, total_k;
+    float scale_log2;
+    int32_t out_bf16;
+};
+cudaError_t launch_latent_prefill(const LatentPrefillParams &p, cudaStream_t stream);
+
+}  // namespace pkv

@@ -1,0 +1,263 @@
+// latent_api.cu -- the extern "C" entry points of the latent-attention operators
+// declared in include/pagedkv.h: argument validation before anything is enqueued,
+// then the kernel launches on the caller's stream.  No allocation, no
+// synchronisation.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/pagedkv.h"
+#include "latent.h"
+
+namespace {
+
+using pkv::kBlockSize;
+
+constexpr size_t kStatusBytes = 256;
+constexpr int32_t kMaxRowsPerSeq = 16;
+constexpr int32_t kMaxHeads = 1024;
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// The current device's SM count; 0 without a device.
+int current_sms() {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return v;
+}
+
+int check_latent(const pkv_latent_desc *d, int32_t dtype) {
+    if (!d || d->num_blocks < 1) return PKV_ERR_INVALID_ARG;
+    if (d->block_size != kBlockSize || d->latent_dim != pkv::kLatentDim || d->rope_dim != pkv::kRopeDim ||
+        d->dtype != dtype)
+        return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+// A strided bf16 input: 16-byte vectors at every row, offsets that 64 bits hold.
+bool good_stride(int64_t s) { return s >= 0 && s % 8 == 0 && s < (int64_t{1} << 40); }
+
+int write_impl(const void *latent, int64_t latent_stride, const void *rope, int64_t rope_stride, void *cache,
+               void *rope_cache, float *cache_scale, const int32_t *slot_mapping, int32_t num_tokens,
+               const pkv_latent_desc *desc, bool fp8, void *stream) {
+    if (int rc = check_latent(desc, fp8 ? PKV_DTYPE_FP8_E4M3 : PKV_DTYPE_BF16)) return rc;
+    if (num_tokens < 0 || !good_stride(latent_stride) || !good_stride(rope_stride)) return PKV_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PKV_OK;
+    if (!latent || !rope || !cache || !slot_mapping) return PKV_ERR_INVALID_ARG;
+    if (!aligned(latent, 16) || !aligned(rope, 16) || !aligned(cache, 16) || !aligned(slot_mapping, 4))
+        return PKV_ERR_INVALID_ARG;
+    if (fp8 && (!rope_cache || !cache_scale || !aligned(rope_cache, 16) || !aligned(cache_scale, 16)))
+        return PKV_ERR_INVALID_ARG;
+    const int sms = current_sms();
+    if (sms < 1) return PKV_ERR_CUDA;
+    pkv::LatentWriteParams p{};
+    p.latent = latent;
+    p.rope = rope;
+    p.latent_stride = latent_stride;
+    p.rope_stride = rope_stride;
+    p.cache = cache;
+    p.rope_cache = rope_cache;
+    p.cache_scale = cache_scale;
+    p.slot_mapping = slot_mapping;
+    p.num_slots = static_cast<int64_t>(desc->num_blocks) * kBlockSize;
+    p.num_tokens = num_tokens;
+    return pkv::launch_latent_write(p, fp8, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK
+                                                                                                   : PKV_ERR_CUDA;
+}
+
+// Sizes shared by the absorbed form's entry points and its workspace query.
+int check_decode_sizes(int32_t num_seqs, int32_t q_per_seq, int32_t heads, int32_t max_blocks) {
+    if (num_seqs < 1 || num_seqs > 65535 || q_per_seq < 1 || q_per_seq > kMaxRowsPerSeq || heads < 1 || max_blocks < 1)
+        return PKV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(max_blocks) * kBlockSize > INT32_MAX) return PKV_ERR_INVALID_ARG;
+    if (heads > kMaxHeads) return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+int decode_impl(void *out, int32_t out_dtype, const void *q_latent, int64_t ql_row, int64_t ql_head,
+                const void *q_rope, int64_t qr_row, int64_t qr_head, const void *cache, const void *rope_cache,
+                const float *cache_scale, const int32_t *block_tables, const int32_t *context_lens, int32_t num_seqs,
+                int32_t q_per_seq, int32_t heads, int32_t max_blocks, float scale, const pkv_latent_desc *desc,
+                bool fp8, void *workspace, size_t workspace_bytes, void *stream) {
+    if (int rc = check_latent(desc, fp8 ? PKV_DTYPE_FP8_E4M3 : PKV_DTYPE_BF16)) return rc;
+    if (int rc = check_decode_sizes(num_seqs, q_per_seq, heads, max_blocks)) return rc;
+    if (!out || !q_latent || !q_rope || !cache || !block_tables || !context_lens) return PKV_ERR_INVALID_ARG;
+    if (fp8 && (!rope_cache || !cache_scale || !aligned(rope_cache, 16) || !aligned(cache_scale, 16)))
+        return PKV_ERR_INVALID_ARG;
+    if (out_dtype != PKV_DTYPE_FLOAT32 && out_dtype != PKV_DTYPE_BF16) return PKV_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale)) return PKV_ERR_INVALID_ARG;
+    if (!good_stride(ql_row) || !good_stride(ql_head) || !good_stride(qr_row) || !good_stride(qr_head))
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || !aligned(q_latent, 16) || !aligned(q_rope, 16) || !aligned(cache, 16) ||
+        !aligned(block_tables, 4) || !aligned(context_lens, 4))
+        return PKV_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256)) return PKV_ERR_INVALID_ARG;
+    if (workspace_bytes < latent_attention_workspace_size(num_seqs, q_per_seq, heads, max_blocks, desc))
+        return PKV_ERR_WORKSPACE_TOO_SMALL;
+    pkv::LatentDecodeParams p{};
+    p.out = out;
+    p.q_latent = q_latent;
+    p.q_rope = q_rope;
+    p.ql_row = ql_row;
+    p.ql_head = ql_head;
+    p.qr_row = qr_row;
+    p.qr_head = qr_head;
+    p.cache = cache;
+    p.rope_cache = rope_cache;
+    p.cache_scale = cache_scale;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.status = static_cast<uint32_t *>(workspace);
+    p.num_seqs = num_seqs;
+    p.q_per_seq = q_per_seq;
+    p.heads = heads;
+    p.max_blocks = max_blocks;
+    p.num_blocks = desc->num_blocks;
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    p.out_bf16 = out_dtype == PKV_DTYPE_BF16;
+    return pkv::launch_latent_decode(p, fp8, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int latent_reshape_and_cache(const void *latent, int64_t latent_stride, const void *rope, int64_t rope_stride,
+                             void *cache, const int32_t *slot_mapping, int32_t num_tokens, const pkv_latent_desc *desc,
+                             void *stream) {
+    return write_impl(latent, latent_stride, rope, rope_stride, cache, nullptr, nullptr, slot_mapping, num_tokens, desc,
+                      false, stream);
+}
+
+int latent_reshape_and_cache_fp8(const void *latent, int64_t latent_stride, const void *rope, int64_t rope_stride,
+                                 void *cache, void *rope_cache, float *cache_scale, const int32_t *slot_mapping,
+                                 int32_t num_tokens, const pkv_latent_desc *desc, void *stream) {
+    return write_impl(latent, latent_stride, rope, rope_stride, cache, rope_cache, cache_scale, slot_mapping,
+                      num_tokens, desc, true, stream);
+}
+
+int latent_gather(void *out, const void *cache, const void *rope_cache, const float *cache_scale,
+                  const int32_t *block_tables, const int32_t *cu_lens, int32_t num_seqs, int32_t max_blocks_per_seq,
+                  int32_t total_rows, const pkv_latent_desc *desc, uint32_t *status, void *stream) {
+    if (!desc) return PKV_ERR_INVALID_ARG;
+    const bool fp8 = desc->dtype == PKV_DTYPE_FP8_E4M3;
+    if (int rc = check_latent(desc, fp8 ? PKV_DTYPE_FP8_E4M3 : PKV_DTYPE_BF16)) return rc;
+    if (num_seqs < 1 || max_blocks_per_seq < 1 || total_rows < 0) return PKV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(max_blocks_per_seq) * kBlockSize > INT32_MAX) return PKV_ERR_INVALID_ARG;
+    if (total_rows == 0) return PKV_OK;
+    if (!out || !cache || !block_tables || !cu_lens) return PKV_ERR_INVALID_ARG;
+    if (fp8 ? (!rope_cache || !cache_scale || !aligned(rope_cache, 16) || !aligned(cache_scale, 16))
+            : (rope_cache || cache_scale))
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || !aligned(cache, 16) || !aligned(block_tables, 4) || !aligned(cu_lens, 4) ||
+        !aligned(status, 4))
+        return PKV_ERR_INVALID_ARG;
+    pkv::LatentGatherParams p{};
+    p.out = out;
+    p.cache = cache;
+    p.rope_cache = rope_cache;
+    p.cache_scale = cache_scale;
+    p.block_tables = block_tables;
+    p.cu_lens = cu_lens;
+    p.status = status;
+    p.num_seqs = num_seqs;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = desc->num_blocks;
+    p.total_rows = total_rows;
+    return pkv::launch_latent_gather(p, fp8, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+size_t latent_attention_workspace_size(int32_t num_seqs, int32_t q_per_seq, int32_t num_q_heads,
+                                       int32_t max_blocks_per_seq, const pkv_latent_desc *desc) {
+    if (!desc || check_latent(desc, desc->dtype == PKV_DTYPE_FP8_E4M3 ? PKV_DTYPE_FP8_E4M3 : PKV_DTYPE_BF16) != PKV_OK)
+        return 0;
+    if (check_decode_sizes(num_seqs, q_per_seq, num_q_heads, max_blocks_per_seq) != PKV_OK) return 0;
+    return kStatusBytes;
+}
+
+int latent_attention_decode(void *out, int32_t out_dtype, const void *q_latent, int64_t q_latent_row_stride,
+                            int64_t q_latent_head_stride, const void *q_rope, int64_t q_rope_row_stride,
+                            int64_t q_rope_head_stride, const void *cache, const int32_t *block_tables,
+                            const int32_t *context_lens, int32_t num_seqs, int32_t q_per_seq, int32_t num_q_heads,
+                            int32_t max_blocks_per_seq, float scale, const pkv_latent_desc *desc, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    return decode_impl(out, out_dtype, q_latent, q_latent_row_stride, q_latent_head_stride, q_rope, q_rope_row_stride,
+                       q_rope_head_stride, cache, nullptr, nullptr, block_tables, context_lens, num_seqs, q_per_seq,
+                       num_q_heads, max_blocks_per_seq, scale, desc, false, workspace, workspace_bytes, stream);
+}
+
+int latent_attention_decode_fp8(void *out, int32_t out_dtype, const void *q_latent, int64_t q_latent_row_stride,
+                                int64_t q_latent_head_stride, const void *q_rope, int64_t q_rope_row_stride,
+                                int64_t q_rope_head_stride, const void *cache, const void *rope_cache,
+                                const float *cache_scale, const int32_t *block_tables, const int32_t *context_lens,
+                                int32_t num_seqs, int32_t q_per_seq, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                float scale, const pkv_latent_desc *desc, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+    return decode_impl(out, out_dtype, q_latent, q_latent_row_stride, q_latent_head_stride, q_rope, q_rope_row_stride,
+                       q_rope_head_stride, cache, rope_cache, cache_scale, block_tables, context_lens, num_seqs,
+                       q_per_seq, num_q_heads, max_blocks_per_seq, scale, desc, true, workspace, workspace_bytes,
+                       stream);
+}
+
+size_t latent_attention_prefill_workspace_size(int32_t num_seqs, int32_t num_heads, int32_t max_q_len,
+                                               int32_t total_q_rows, int32_t total_k_rows) {
+    if (num_seqs < 1 || num_seqs > 65535 || num_heads < 1 || num_heads > kMaxHeads || max_q_len < 0 ||
+        total_q_rows < 0 || total_k_rows < 0)
+        return 0;
+    return kStatusBytes;
+}
+
+int latent_attention_prefill_chunk(void *out, int32_t out_dtype, const void *q, int64_t q_row_stride,
+                                   int64_t q_head_stride, const void *k_nope, const void *v, int64_t k_row_stride,
+                                   int64_t k_head_stride, const void *k_rope, int64_t k_rope_stride,
+                                   const int32_t *cu_q_lens, const int32_t *cu_k_lens, int32_t num_seqs,
+                                   int32_t num_heads, int32_t max_q_len, int32_t total_q_rows, int32_t total_k_rows,
+                                   float scale, void *workspace, size_t workspace_bytes, void *stream) {
+    if (num_seqs < 1 || num_seqs > 65535 || num_heads < 1 || max_q_len < 0 || total_q_rows < 0 || total_k_rows < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (num_heads > kMaxHeads) return PKV_ERR_UNSUPPORTED;
+    if (out_dtype != PKV_DTYPE_FLOAT32 && out_dtype != PKV_DTYPE_BF16) return PKV_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale)) return PKV_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256)) return PKV_ERR_INVALID_ARG;
+    if (workspace_bytes <
+        latent_attention_prefill_workspace_size(num_seqs, num_heads, max_q_len, total_q_rows, total_k_rows))
+        return PKV_ERR_WORKSPACE_TOO_SMALL;
+    if (max_q_len == 0 || total_q_rows == 0) return PKV_OK;
+    if (!out || !q || !k_nope || !v || !k_rope || !cu_q_lens || !cu_k_lens || total_k_rows < 1)
+        return PKV_ERR_INVALID_ARG;
+    // Rows and heads are boxes of a tensor map: distinct, 16 bytes apart at least.
+    if (!good_stride(q_row_stride) || !good_stride(q_head_stride) || !good_stride(k_row_stride) ||
+        !good_stride(k_head_stride) || !good_stride(k_rope_stride) || q_row_stride < 8 || q_head_stride < 8 ||
+        k_row_stride < 8 || k_head_stride < 8 || k_rope_stride < 8)
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_nope, 16) || !aligned(v, 16) || !aligned(k_rope, 16) ||
+        !aligned(cu_q_lens, 4) || !aligned(cu_k_lens, 4))
+        return PKV_ERR_INVALID_ARG;
+    pkv::LatentPrefillParams p{};
+    p.out = out;
+    p.q = q;
+    p.k_nope = k_nope;
+    p.v = v;
+    p.k_rope = k_rope;
+    p.q_row = q_row_stride;
+    p.q_head = q_head_stride;
+    p.k_row = k_row_stride;
+    p.k_head = k_head_stride;
+    p.r_row = k_rope_stride;
+    p.cu_q_lens = cu_q_lens;
+    p.cu_k_lens = cu_k_lens;
+    p.status = static_cast<uint32_t *>(workspace);
+    p.num_seqs = num_seqs;
+    p.heads = num_heads;
+    p.max_q_len = max_q_len;
+    p.total_q = total_q_rows;
+    p.total_k = total_k_rows;
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    p.out_bf16 = out_dtype == PKV_DTYPE_BF16;
+    return pkv::launch_latent_prefill(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // extern "C"

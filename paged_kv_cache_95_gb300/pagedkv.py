@@ -37,6 +37,8 @@ PKV_VERIFY_PREFILL_KERNEL = 1
 
 HEAD_DIM = 128
 BLOCK_SIZE = 16
+LATENT_DIM = 512  # latent attention: values of the shared latent a token
+ROPE_DIM = 64     # and of its rotated key
 STATIC_SCRATCH_BYTES = 16 * 1024 * 1024  # PKV_STATIC_SCRATCH_BYTES
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpagedkv.so")
@@ -51,6 +53,13 @@ class CacheDesc(ctypes.Structure):
 
     _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class LatentDesc(ctypes.Structure):
+    """Mirror of ``pkv_latent_desc``."""
+
+    _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class PagedKVError(RuntimeError):
@@ -126,6 +135,26 @@ def _declare(lib):
     lib.kv_copy_blocks.argtypes = [P, P, P, P, P, i32, D, P]
     lib.kv_copy_blocks.restype = ctypes.c_int
     i64, I = ctypes.c_int64, ctypes.c_int
+    LD = ctypes.POINTER(LatentDesc)
+    lib.latent_reshape_and_cache.argtypes = [P, i64, P, i64, P, P, i32, LD, P]
+    lib.latent_reshape_and_cache.restype = I
+    lib.latent_reshape_and_cache_fp8.argtypes = [P, i64, P, i64, P, P, P, P, i32, LD, P]
+    lib.latent_reshape_and_cache_fp8.restype = I
+    lib.latent_gather.argtypes = [P, P, P, P, P, P, i32, i32, i32, LD, P, P]
+    lib.latent_gather.restype = I
+    lib.latent_attention_workspace_size.argtypes = [i32, i32, i32, i32, LD]
+    lib.latent_attention_workspace_size.restype = sz
+    lib.latent_attention_decode.argtypes = [P, i32, P, i64, i64, P, i64, i64, P, P, P, i32, i32, i32, i32, f32, LD, P,
+                                            sz, P]
+    lib.latent_attention_decode.restype = I
+    lib.latent_attention_decode_fp8.argtypes = [P, i32, P, i64, i64, P, i64, i64, P, P, P, P, P, i32, i32, i32, i32,
+                                                f32, LD, P, sz, P]
+    lib.latent_attention_decode_fp8.restype = I
+    lib.latent_attention_prefill_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+    lib.latent_attention_prefill_workspace_size.restype = sz
+    lib.latent_attention_prefill_chunk.argtypes = [P, i32, P, i64, i64, P, P, i64, i64, P, i64, P, P, i32, i32, i32,
+                                                   i32, i32, f32, P, sz, P]
+    lib.latent_attention_prefill_chunk.restype = I
     lib.pkv_bm_create.argtypes = [i32, ctypes.POINTER(P)]
     lib.pkv_bm_create.restype = I
     lib.pkv_bm_destroy.argtypes = [P]
@@ -654,3 +683,203 @@ def paged_attention_decode_static_scratch(out, q, k_cache, v_cache, block_tables
         int(B), int(n_q), int(block_tables.shape[1]), float(scale), int(partition_size), ctypes.byref(desc),
         _ptr(status) if status is not None else None, _stream(stream))
     _raise("paged_attention_decode_static_scratch", rc)
+
+
+# ---- latent attention ---------------------------------------------------------------
+
+def _check_rows(t, name, ndim, last, device):
+    """A bf16 input whose rows (innermost dimension) are contiguous; the outer strides are free."""
+    torch = _torch()
+    _need(isinstance(t, torch.Tensor), f"{name} must be a torch.Tensor")
+    _need(t.dtype == torch.bfloat16, f"{name} must be torch.bfloat16, got {t.dtype}")
+    _need(t.dim() == ndim and t.shape[-1] == last, f"{name} must have {ndim} dims, the last {last}: {tuple(t.shape)}")
+    _need(t.get_device() == device, f"{name} must be on the current CUDA device")
+    _need(t.stride(-1) == 1, f"{name}'s innermost dimension must be contiguous")
+
+
+def _check_on(t, name, dtype, ndim, device):
+    """A contiguous tensor on the current device."""
+    _check(t, name, dtype, ndim=ndim)
+    _need(t.get_device() == device, f"{name} must be on the current CUDA device")
+
+
+def _outer_stride(t, dim: int) -> int:
+    """The stride of an outer dimension; the packed one where its size is 1 (it is never stepped)."""
+    return int(t.stride(dim)) if t.shape[dim] > 1 else (int(t.shape[-1]) + 7) // 8 * 8
+
+
+def latent_cache_desc(cache) -> LatentDesc:
+    """Descriptor of a latent pool: bf16 [num_blocks, 16, 576], or FP8 E4M3 codes
+    (torch.float8_e4m3fn or uint8) [num_blocks, 16, 512]."""
+    torch = _torch()
+    fp8 = cache.dtype in (torch.uint8, torch.float8_e4m3fn)
+    _check(cache, "cache", cache.dtype if fp8 else torch.bfloat16, ndim=3)
+    width = LATENT_DIM if fp8 else LATENT_DIM + ROPE_DIM
+    _need(cache.shape[2] == width, f"cache rows must have {width} values, got {cache.shape[2]}")
+    return LatentDesc(int(cache.shape[0]), int(cache.shape[1]), LATENT_DIM, ROPE_DIM,
+                      PKV_DTYPE_FP8_E4M3 if fp8 else PKV_DTYPE_BF16)
+
+
+def _latent_pool(cache, rope_cache, cache_scale, device):
+    torch = _torch()
+    desc = latent_cache_desc(cache)
+    _need(cache.get_device() == device, "cache must be on the current CUDA device")
+    fp8 = desc.dtype == PKV_DTYPE_FP8_E4M3
+    _need(fp8 == (rope_cache is not None) and fp8 == (cache_scale is not None),
+          "rope_cache and cache_scale are required for an FP8 pool and not allowed otherwise")
+    if fp8:
+        _check_on(rope_cache, "rope_cache", torch.bfloat16, 3, device)
+        _check_on(cache_scale, "cache_scale", torch.float32, 2, device)
+        _need(tuple(rope_cache.shape) == (*cache.shape[:2], ROPE_DIM), "rope_cache must be [num_blocks, 16, 64]")
+        _need(tuple(cache_scale.shape) == tuple(cache.shape[:2]), "cache_scale must be [num_blocks, 16]")
+    return desc, fp8
+
+
+def _check_latent_rows(latent, rope, slot_mapping, device):
+    torch = _torch()
+    _check_rows(latent, "latent", 2, LATENT_DIM, device)
+    _check_rows(rope, "rope", 2, ROPE_DIM, device)
+    _check_on(slot_mapping, "slot_mapping", torch.int32, 1, device)
+    T = slot_mapping.shape[0]
+    _need(latent.shape[0] == T and rope.shape[0] == T, "one latent and one rope row per slot")
+    return int(T)
+
+
+def latent_reshape_and_cache(latent, rope, cache, slot_mapping, stream=None) -> None:
+    """Append rows [latent (512) | rope (64)] to the bf16 latent pool [num_blocks, 16, 576]
+    through ``slot_mapping``; ``latent`` and ``rope`` may be slices of wider rows."""
+    device = _torch().cuda.current_device()
+    desc, fp8 = _latent_pool(cache, None, None, device)
+    T = _check_latent_rows(latent, rope, slot_mapping, device)
+    rc = load_library().latent_reshape_and_cache(_ptr(latent), _outer_stride(latent, 0), _ptr(rope),
+                                                 _outer_stride(rope, 0), _ptr(cache), _ptr(slot_mapping), T,
+                                                 ctypes.byref(desc), _stream(stream))
+    _raise("latent_reshape_and_cache", rc)
+
+
+def latent_reshape_and_cache_fp8(latent, rope, cache, rope_cache, cache_scale, slot_mapping, stream=None) -> None:
+    """The same into an FP8 pool: E4M3 codes of the latent with one fp32 scale a token
+    (``cache_scale`` [num_blocks, 16]); the rotated key goes to ``rope_cache`` as it is."""
+    device = _torch().cuda.current_device()
+    desc, fp8 = _latent_pool(cache, rope_cache, cache_scale, device)
+    T = _check_latent_rows(latent, rope, slot_mapping, device)
+    rc = load_library().latent_reshape_and_cache_fp8(_ptr(latent), _outer_stride(latent, 0), _ptr(rope),
+                                                     _outer_stride(rope, 0), _ptr(cache), _ptr(rope_cache),
+                                                     _ptr(cache_scale), _ptr(slot_mapping), T, ctypes.byref(desc),
+                                                     _stream(stream))
+    _raise("latent_reshape_and_cache_fp8", rc)
+
+
+def latent_gather(out, cache, block_tables, cu_lens, rope_cache=None, cache_scale=None, status=None,
+                  stream=None) -> None:
+    """Read cached rows back in sequence order: row cu_lens[b] + i of ``out`` (bf16 [total, 576])
+    is position i of sequence b; an FP8 pool is dequantised and rounded once.  ``status`` is
+    an optional int32 CUDA tensor of one element into which status bits are ORed."""
+    torch = _torch()
+    device = torch.cuda.current_device()
+    desc, fp8 = _latent_pool(cache, rope_cache, cache_scale, device)
+    _check_on(out, "out", torch.bfloat16, 2, device)
+    _need(out.shape[1] == LATENT_DIM + ROPE_DIM, "out must be [total_rows, 576]")
+    _check_on(block_tables, "block_tables", torch.int32, 2, device)
+    _check_on(cu_lens, "cu_lens", torch.int32, 1, device)
+    B = int(block_tables.shape[0])
+    _need(cu_lens.shape[0] == B + 1, "cu_lens must be [num_seqs + 1]")
+    if status is not None:
+        _check_on(status, "status", torch.int32, 1, device)
+    rc = load_library().latent_gather(_ptr(out), _ptr(cache), _ptr(rope_cache) if fp8 else None,
+                                      _ptr(cache_scale) if fp8 else None, _ptr(block_tables), _ptr(cu_lens), B,
+                                      int(block_tables.shape[1]), int(out.shape[0]), ctypes.byref(desc),
+                                      _ptr(status) if status is not None else None, _stream(stream))
+    _raise("latent_gather", rc)
+
+
+def latent_attention_workspace_size(num_seqs: int, q_per_seq: int, num_q_heads: int, max_blocks_per_seq: int,
+                                    desc: LatentDesc) -> int:
+    return int(load_library().latent_attention_workspace_size(num_seqs, q_per_seq, num_q_heads, max_blocks_per_seq,
+                                                              ctypes.byref(desc)))
+
+
+def latent_attention_decode(out, q_latent, q_rope, cache, block_tables, context_lens, scale: float, workspace=None,
+                            q_per_seq: int = 1, rope_cache=None, cache_scale=None, stream=None):
+    """Absorbed latent attention over the paged pool: ``q_latent`` [num_seqs * q_per_seq, heads,
+    512] and ``q_rope`` [.., heads, 64] (rows and heads may be strided), ``out`` [.., heads, 512]
+    in float32 or bfloat16.  Row i of sequence b sits at position ctx_b - q_per_seq + i and
+    sees the keys up to it.  An FP8 pool comes with ``rope_cache`` and ``cache_scale``
+    (latent_attention_decode_fp8).  Returns the workspace (allocated if None)."""
+    torch = _torch()
+    device = torch.cuda.current_device()
+    desc, fp8 = _latent_pool(cache, rope_cache, cache_scale, device)
+    _check_rows(q_latent, "q_latent", 3, LATENT_DIM, device)
+    _check_rows(q_rope, "q_rope", 3, ROPE_DIM, device)
+    rows, heads, _ = q_latent.shape
+    _need(tuple(q_rope.shape[:2]) == (rows, heads), "q_rope must have q_latent's rows and heads")
+    _check_on(out, "out", out.dtype, 3, device)
+    _need(tuple(out.shape) == (rows, heads, LATENT_DIM), "out must have q_latent's shape")
+    _check_on(block_tables, "block_tables", torch.int32, 2, device)
+    _check_on(context_lens, "context_lens", torch.int32, 1, device)
+    B, k = int(context_lens.shape[0]), int(q_per_seq)
+    _need(block_tables.shape[0] == B and rows == B * k, "q_latent must hold q_per_seq rows per sequence")
+    max_blocks = int(block_tables.shape[1])
+    lib = load_library()
+    if workspace is None:
+        nbytes = int(lib.latent_attention_workspace_size(B, k, int(heads), max_blocks, ctypes.byref(desc)))
+        _need(nbytes > 0, "invalid sizes for latent_attention_decode")
+        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=out.device)  # status word starts clear
+    _check_on(workspace, "workspace", torch.uint8, 1, device)
+    ql = (_ptr(q_latent), _outer_stride(q_latent, 0), _outer_stride(q_latent, 1))
+    qr = (_ptr(q_rope), _outer_stride(q_rope, 0), _outer_stride(q_rope, 1))
+    tail = (_ptr(block_tables), _ptr(context_lens), B, k, int(heads), max_blocks, float(scale), ctypes.byref(desc),
+            _ptr(workspace), int(workspace.numel()), _stream(stream))
+    if fp8:
+        rc = lib.latent_attention_decode_fp8(_ptr(out), _out_dtype(out), *ql, *qr, _ptr(cache), _ptr(rope_cache),
+                                             _ptr(cache_scale), *tail)
+        _raise("latent_attention_decode_fp8", rc)
+    else:
+        rc = lib.latent_attention_decode(_ptr(out), _out_dtype(out), *ql, *qr, _ptr(cache), *tail)
+        _raise("latent_attention_decode", rc)
+    return workspace
+
+
+def latent_attention_prefill_workspace_size(num_seqs: int, num_heads: int, max_q_len: int, total_q_rows: int,
+                                            total_k_rows: int) -> int:
+    return int(load_library().latent_attention_prefill_workspace_size(num_seqs, num_heads, max_q_len, total_q_rows,
+                                                                      total_k_rows))
+
+
+def latent_attention_prefill_chunk(out, q, k_nope, v, k_rope, cu_q_lens, cu_k_lens, max_q_len: int, scale: float,
+                                   workspace=None, stream=None):
+    """Expanded latent attention of a causal chunk: ``q`` [total_q, heads, 192], ``k_nope`` and
+    ``v`` [total_k, heads, 128] (usually the halves of one [total_k, heads, 256] product, so of
+    equal strides), ``k_rope`` [total_k, 64] shared by the heads, ``out`` [total_q, heads, 128]
+    in float32 or bfloat16.  Returns the workspace (allocated if None)."""
+    torch = _torch()
+    device = torch.cuda.current_device()
+    _check_rows(q, "q", 3, 192, device)
+    _check_rows(k_nope, "k_nope", 3, 128, device)
+    _check_rows(v, "v", 3, 128, device)
+    _check_rows(k_rope, "k_rope", 2, ROPE_DIM, device)
+    tq, heads, _ = q.shape
+    tk = int(k_nope.shape[0])
+    _need(k_nope.shape[1] == heads and tuple(v.shape) == tuple(k_nope.shape) and k_rope.shape[0] == tk,
+          "k_nope and v must be [total_k, heads, 128], k_rope [total_k, 64]")
+    k_strides = (_outer_stride(k_nope, 0), _outer_stride(k_nope, 1))
+    _need(k_strides == (_outer_stride(v, 0), _outer_stride(v, 1)), "k_nope and v must have the same strides")
+    _check_on(out, "out", out.dtype, 3, device)
+    _need(tuple(out.shape) == (tq, heads, 128), "out must be [total_q, heads, 128]")
+    _check_on(cu_q_lens, "cu_q_lens", torch.int32, 1, device)
+    _check_on(cu_k_lens, "cu_k_lens", torch.int32, 1, device)
+    B = int(cu_q_lens.shape[0]) - 1
+    _need(cu_k_lens.shape[0] == B + 1, "cu_q_lens and cu_k_lens must be [num_seqs + 1]")
+    lib = load_library()
+    if workspace is None:
+        nbytes = int(lib.latent_attention_prefill_workspace_size(B, int(heads), int(max_q_len), int(tq), tk))
+        _need(nbytes > 0, "invalid sizes for latent_attention_prefill_chunk")
+        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=out.device)  # status word starts clear
+    _check_on(workspace, "workspace", torch.uint8, 1, device)
+    rc = lib.latent_attention_prefill_chunk(_ptr(out), _out_dtype(out), _ptr(q), _outer_stride(q, 0),
+                                            _outer_stride(q, 1), _ptr(k_nope), _ptr(v), *k_strides, _ptr(k_rope),
+                                            _outer_stride(k_rope, 0), _ptr(cu_q_lens), _ptr(cu_k_lens), B, int(heads),
+                                            int(max_q_len), int(tq), tk, float(scale), _ptr(workspace),
+                                            int(workspace.numel()), _stream(stream))
+    _raise("latent_attention_prefill_chunk", rc)
+    return workspace
