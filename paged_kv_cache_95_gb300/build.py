@@ -19,7 +19,7 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libpagedkv.so")
 SOURCES = ["api.cu", "cache_write.cu", "decode.cu", "prefill.cu", "latent_api.cu", "latent_cache.cu",
            "latent_decode.cu", "latent_prefill.cu", "block_manager.cpp"]
-HEADERS = ["launch.h", "latent.h", "ptx.cuh", "decode_core.cuh"]
+HEADERS = ["launch.h", "latent.h", "tensor_map.h", "ptx.cuh", "decode_core.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

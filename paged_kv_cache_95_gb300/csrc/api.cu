@@ -17,6 +17,7 @@
 
 #include "../../include/pagedkv.h"
 #include "launch.h"
+#include "tensor_map.h"
 
 namespace {
 
@@ -60,23 +61,8 @@ int sm_count(int dev) {
 }
 
 // ---- tensor maps -------------------------------------------------------------------
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
+using pkv::encode_fn;
+using pkv::EncodeTiledFn;
 
 // Pool tensor [num_blocks][n_kv][16][128] bf16 viewed as 4-D (dims inner->outer:
 // head_dim, slot, head, block); box = 64 dims x 16 slots, 128-byte swizzle.

@@ -50,8 +50,18 @@ struct LatentDecodeParams {
     int32_t num_seqs, q_per_seq, heads, max_blocks, num_blocks;
     float scale_log2;
     int32_t out_bf16;
+    // The split: the q_per_seq x heads columns of a sequence in col_tiles tiles of cols_per_tile
+    // (the last may hold fewer), the keys of all sequences in `ranges` ranges of tiles.
+    int32_t col_tiles, cols_per_tile, ranges;
+    int2 *record;            // [ranges]: first sequence (-1: empty), 1 if the range starts inside it
+    float *part_m, *part_l;  // [ranges][2][col_tiles * cols_per_tile]  (log2 domain, scale folded in)
+    float *part_o;           // the same x [512], unnormalised
 };
-cudaError_t launch_latent_decode(const LatentDecodeParams &p, bool fp8, cudaStream_t stream);
+constexpr int kLatentMaxRanges = 512;  // more SMs than any device has
+constexpr int kLatentMaxCols = 64;     // columns a CTA takes
+constexpr int kLatentTile = 64;        // keys a tile
+cudaError_t latent_decode_prepare_device();
+cudaError_t launch_latent_decode(const CUtensorMap &kvmap, const LatentDecodeParams &p, bool fp8, cudaStream_t stream);
 
 // ---- expanded attention of a prefill chunk --------------------------------------------
 struct LatentPrefillParams {

@@ -5,17 +5,22 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/pagedkv.h"
 #include "latent.h"
+#include "tensor_map.h"
 
 namespace {
 
 using pkv::kBlockSize;
 
 constexpr size_t kStatusBytes = 256;
+constexpr int kMaxDevices = 64;
+constexpr int kDefaultSms = 152;  // sizes asked for without a GPU
 constexpr int32_t kMaxRowsPerSeq = 16;
 constexpr int32_t kMaxHeads = 1024;
 
@@ -27,6 +32,58 @@ int current_sms() {
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
     return v;
+}
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Kernel attributes, set once per device; false on failure.
+std::once_flag g_decode_once[kMaxDevices];
+cudaError_t g_decode_err[kMaxDevices];
+bool prepare_decode() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    std::call_once(g_decode_once[dev], [&] { g_decode_err[dev] = pkv::latent_decode_prepare_device(); });
+    return g_decode_err[dev] == cudaSuccess;
+}
+
+// A bf16 pool [num_blocks][16][576] viewed so that one box is a whole block in the order
+// the tensor core wants it: dims inner -> outer are 64 values (128 bytes), 8 slots, the 9
+// chunks of 64 values, the two groups of 8 slots, the block; it lands as
+// [slot group][chunk][8 slots][128 B], eighteen 1 KB swizzle atoms.
+bool encode_latent_map(CUtensorMap *map, const void *base, int32_t num_blocks) {
+    const pkv::EncodeTiledFn fn = pkv::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[5] = {64, 8, 9, 2, static_cast<cuuint64_t>(num_blocks)};
+    const cuuint64_t strides[4] = {pkv::kLatentRow * 2, 128, pkv::kLatentRow * 16, pkv::kLatentRow * 32};
+    const cuuint32_t box[5] = {64, 8, 9, 2, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a decode call is split: one CTA per SM, column tiles of at most 64 columns of equal
+// size, and as many ranges of keys as there are SMs for a column tile (never more than
+// tiles).  Workspace: [status 256 B | records | part_m | part_l | part_o].
+struct DecodePlan {
+    int32_t col_tiles, cols_per_tile, ranges;
+    size_t off_m, off_l, off_o, total;
+};
+DecodePlan plan_decode(int32_t num_seqs, int32_t q_per_seq, int32_t heads, int32_t max_blocks, int sms) {
+    DecodePlan pl{};
+    const int32_t cols = heads * q_per_seq;
+    pl.col_tiles = (cols + pkv::kLatentMaxCols - 1) / pkv::kLatentMaxCols;
+    pl.cols_per_tile = (cols + pl.col_tiles - 1) / pl.col_tiles;
+    const int64_t tiles = static_cast<int64_t>(num_seqs) *
+                          ((static_cast<int64_t>(max_blocks) * kBlockSize + pkv::kLatentTile - 1) / pkv::kLatentTile);
+    const int64_t ranges = std::min<int64_t>(std::max(1, sms / pl.col_tiles), tiles);
+    pl.ranges = static_cast<int32_t>(std::min<int64_t>(ranges, pkv::kLatentMaxRanges));
+    const size_t rows = static_cast<size_t>(pl.ranges) * 2 * pl.col_tiles * pl.cols_per_tile;
+    pl.off_m = kStatusBytes + align_up(static_cast<size_t>(pl.ranges) * 8, 256);
+    pl.off_l = pl.off_m + align_up(rows * 4, 256);
+    pl.off_o = pl.off_l + align_up(rows * 4, 256);
+    pl.total = pl.off_o + rows * pkv::kLatentDim * 4;
+    return pl;
 }
 
 int check_latent(const pkv_latent_desc *d, int32_t dtype) {
@@ -118,7 +175,21 @@ int decode_impl(void *out, int32_t out_dtype, const void *q_latent, int64_t ql_r
     p.num_blocks = desc->num_blocks;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.out_bf16 = out_dtype == PKV_DTYPE_BF16;
-    return pkv::launch_latent_decode(p, fp8, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    const int sms = current_sms();
+    if (sms < 1 || !prepare_decode()) return PKV_ERR_CUDA;
+    const DecodePlan pl = plan_decode(num_seqs, q_per_seq, heads, max_blocks, sms);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.col_tiles = pl.col_tiles;
+    p.cols_per_tile = pl.cols_per_tile;
+    p.ranges = pl.ranges;
+    p.record = reinterpret_cast<int2 *>(ws + kStatusBytes);
+    p.part_m = reinterpret_cast<float *>(ws + pl.off_m);
+    p.part_l = reinterpret_cast<float *>(ws + pl.off_l);
+    p.part_o = reinterpret_cast<float *>(ws + pl.off_o);
+    CUtensorMap kvmap{};
+    if (!fp8 && !encode_latent_map(&kvmap, cache, desc->num_blocks)) return PKV_ERR_CUDA;
+    return pkv::launch_latent_decode(kvmap, p, fp8, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK
+                                                                                                     : PKV_ERR_CUDA;
 }
 
 }  // namespace
@@ -175,7 +246,8 @@ size_t latent_attention_workspace_size(int32_t num_seqs, int32_t q_per_seq, int3
     if (!desc || check_latent(desc, desc->dtype == PKV_DTYPE_FP8_E4M3 ? PKV_DTYPE_FP8_E4M3 : PKV_DTYPE_BF16) != PKV_OK)
         return 0;
     if (check_decode_sizes(num_seqs, q_per_seq, num_q_heads, max_blocks_per_seq) != PKV_OK) return 0;
-    return kStatusBytes;
+    const int sms = current_sms();
+    return plan_decode(num_seqs, q_per_seq, num_q_heads, max_blocks_per_seq, sms > 0 ? sms : kDefaultSms).total;
 }
 
 int latent_attention_decode(void *out, int32_t out_dtype, const void *q_latent, int64_t q_latent_row_stride,

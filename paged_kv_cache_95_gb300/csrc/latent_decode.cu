@@ -1,13 +1,38 @@
-// latent_decode.cu -- absorbed latent attention over the paged pool (decode and verify).
+// latent_decode.cu -- absorbed latent attention over the paged pool (decode and verify)
+// on the 5th-generation tensor cores.
 //
 //     s_j = scale (<q_latent, c_j> + <q_rope, r_j>),  out = sum_j softmax(s)_j c_j
 //
-// One warp per (row, head): the query lies in registers (16 latent values and 2
-// rotated ones a lane), the keys are walked one by one with a running maximum and
-// sum in fp32 (log2 domain).
+// Every (query row, head) pair of a sequence is a column that reads the same cached
+// rows, so a CTA takes up to 64 columns and reads each key once for all of them.
+//
+// Work split: the keys of all sequences are one line of 64-key tiles, cut into equal
+// ranges, one CTA per SM and column tile (context lengths are device data, so every
+// CTA sums them itself).  A range covers whole sequences and at most two parts of
+// one; whole sequences are written out, parts go to the workspace as (m, l, O) and
+// the merge kernel folds them.  No CTA waits for another.
+//
+// Per tile (64 keys = 4 blocks of 16, 72 KB, one TMA copy a block; 2 stages):
+//  * S [64 columns x 64 keys] = Q K^T: M = 64, N = 64, 36 steps of 16 values; Q stays in
+//    shared memory (128-byte swizzle, 9 chunks of 64 values).
+//  * softmax by 8 warps, one (row, half of the keys) a thread: running reference m,
+//    raised only when a score passes it by 2^8 (one vote a tile), sum l in fp32;
+//    P = 2^(s - m) rounded to bf16 (l adds the rounded weights, so numerator and
+//    denominator round alike) into shared memory as the B operand.
+//  * O^T [512 dims x columns] += V^T P^T: the same bytes as K, read as an MN-major A
+//    operand: M = 128 (4 tiles of dims), N = columns, 4 steps of 16 keys.  Transposed,
+//    because O has 512 x 64 values: as 128 lanes x 256 columns it leaves tensor memory
+//    for two S buffers, and M is full for any number of heads.
+// The tensor thread takes whichever is ready, the next S or the next P V: waiting for
+// the next tile's copy before a P V would leave no copy in flight.
+//
+// Every mbarrier wait is bounded; a role whose wait runs out raises a CTA-wide abort
+// flag, the others stop at their next wait, and the CTA records PKV_STATUS_TIMEOUT and
+// frees its tensor memory before it returns.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "latent.h"
@@ -17,11 +42,618 @@ namespace pkv {
 
 namespace {
 
+constexpr int kTile = 64;                     // keys a tile
+constexpr int kTileBlocks = kTile / kBlockSize;
+constexpr int kSoftWarps = 8;                 // warps w and w + 4 share rows 16 (w % 4) .. and split the keys
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr int kProducerWarp = kSoftWarps;
+constexpr int kMmaWarp = kSoftWarps + 1;
+constexpr int kThreads = (kSoftWarps + 2) * 32;
+constexpr int kStages = 2;
+constexpr uint32_t kBlockBytes = kBlockSize * kLatentRow * 2;  // 18 KB: [2 slot groups][9 chunks][8 slots][128 B]
+constexpr uint32_t kGroupBytes = kBlockBytes / 2;              // 8 slots
+constexpr uint32_t kStageBytes = kTileBlocks * kBlockBytes;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemS = 256;  // O^T in columns [0, 4 NCOL), S of tile i in [256 + 64 (i & 1), +64)
+constexpr float kRaise = 8.f;     // the reference follows the maximum when it is passed by 2^8
+
+enum { kBarKvFull = 0, kBarKvEmpty = kStages, kBarSFull = 2 * kStages, kBarPFull = 2 * kStages + 2, kBarPvDone, kBarQFull,
+       kNumBars };
+
+template <int NCOL>
+struct Layout {
+    static constexpr uint32_t kQ = 0;  // Q first: M = 64 reads up to 64 rows a chunk, past a smaller Q into the ring
+    static constexpr uint32_t kKv = kQ + NCOL * kLatentRow * 2;
+    static constexpr uint32_t kP = kKv + kStages * kStageBytes;
+    static constexpr uint32_t kBar = kP + NCOL * 128;
+    static constexpr uint32_t kTmemSlot = kBar + 8 * kNumBars;
+    static constexpr uint32_t kAbort = kTmemSlot + 4;
+    static constexpr uint32_t kXch = (kAbort + 4 + 15) / 16 * 16;  // [tile & 1][key half][64] maxima, later sums
+    static constexpr uint32_t kAlpha = kXch + 4 * 64 * 4;          // [64] factors of O's columns
+    static constexpr uint32_t kPlan = kAlpha + 64 * 4;             // warp totals, then the range's start
+    static constexpr uint32_t kBytes = kPlan + 16 * 8;
+    static_assert(kBytes <= 232448, "shared memory of one CTA");
+    static_assert(kKv % 1024 == 0 && kP % 1024 == 0, "swizzle atoms");
+};
+
+__host__ __device__ constexpr uint32_t idesc(int m, int n, bool a_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor of a 128-byte-swizzled operand; operands a few KB further on
+// differ in the address field alone (`+ (bytes >> 4)`).
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ bool bar_red_or(uint32_t id, uint32_t nthreads, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.or.pred q, %1, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(static_cast<uint32_t>(pred)), "r"(nthreads)
+        : "memory");
+    return r != 0;
+}
+
+// Keys of sequence b that its rows see (0: none, its rows are zeros).
+__device__ __forceinline__ int keys_of(const LatentDecodeParams &p, int b) {
+    const int ctx = __ldg(p.context_lens + b);
+    return ctx < 1 || ctx < p.q_per_seq ? 0 : min(ctx, p.max_blocks * kBlockSize);
+}
+__device__ __forceinline__ int tiles_of(const LatentDecodeParams &p, int b) {
+    return (keys_of(p, b) + kTile - 1) / kTile;
+}
+
+// A walk over the tiles of a range.
+struct Walk {
+    int b, t, keys, nt;  // tile t of the nt tiles of sequence b
+    __device__ void at(const LatentDecodeParams &p, int b0, int t0) {
+        b = b0;
+        t = t0;
+        keys = keys_of(p, b);
+        nt = (keys + kTile - 1) / kTile;
+    }
+    __device__ void next(const LatentDecodeParams &p) {  // only while another tile follows
+        if (++t < nt) return;
+        do at(p, b + 1, 0);
+        while (nt == 0 && b + 1 < p.num_seqs);
+    }
+};
+
+template <int NCOL>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const LatentDecodeParams p) {
+    using L = Layout<NCOL>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int range = blockIdx.x / p.col_tiles, ct = blockIdx.x % p.col_tiles;
+    const int cols = p.heads * p.q_per_seq;
+    const int c0 = ct * p.cols_per_tile, nc = min(p.cols_per_tile, cols - c0);
+
+    if (tid == 0) prefetch_tensormap(&kvmap);
+    griddep_launch_dependents();
+    if (sbase & 1023u) {  // operands need the 1 KB swizzle alignment
+        if (tid == 0) atomicOr(p.status, kStatusTimeout);
+        return;
+    }
+    auto bar = [&](int i) { return sbase + L::kBar + 8 * i; };
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + L::kAbort);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmemSlot);
+    int64_t *plan = reinterpret_cast<int64_t *>(smem + L::kPlan);
+    if (tid == 0) {
+        for (int i = 0; i < kNumBars; ++i)
+            mbar_init(bar(i), i == kBarPFull || i == kBarQFull ? kSoftWarps : 1);
+        *abort_flag = 0u;
+        fence_mbar_init();
+    }
+    griddep_wait();  // the producers of q and of the cache before us on the stream
+
+    // ---- the range: total tiles, then where tile `start` lies ----
+    const int seg = (p.num_seqs + kThreads - 1) / kThreads;
+    const int b_lo = min(p.num_seqs, tid * seg), b_hi = min(p.num_seqs, b_lo + seg);
+    int64_t mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(p, b);
+    int64_t upto = mine;  // inclusive prefix
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += o;
+    }
+    if (lane == 31) plan[warp] = upto;
+    __syncthreads();
+    int64_t total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += plan[w];
+        total += plan[w];
+    }
+    upto += before;
+    const int64_t ranges = min(static_cast<int64_t>(p.ranges), total);  // no range is empty
+    const int64_t start = range < ranges ? range * total / ranges : 0;
+    const int64_t stop = range < ranges ? (range + 1) * total / ranges : 0;
+    const int n = static_cast<int>(stop - start);
+    if (n > 0 && upto - mine <= start && start < upto) {
+        int64_t acc = upto - mine;
+        int b = b_lo;
+        for (; acc + tiles_of(p, b) <= start; ++b) acc += tiles_of(p, b);
+        plan[12] = b;
+        plan[13] = start - acc;
+    }
+    // Sequences without keys: zero rows, and the checks of every length, shared out over the ranges.
+    for (int b = range; b < p.num_seqs; b += p.ranges) {
+        const int ctx = __ldg(p.context_lens + b);
+        if (tid == 0 && ct == 0) {
+            uint32_t st = ctx < 1 || ctx > p.max_blocks * kBlockSize ? kStatusBadContextLen : 0u;
+            if (ctx >= 1 && ctx < p.q_per_seq) st |= kStatusBadQLen;
+            if (st) atomicOr(p.status, st);
+        }
+        if (keys_of(p, b) == 0) {
+            const size_t at = (static_cast<size_t>(b) * cols + c0) * kLatentDim * (p.out_bf16 ? 2 : 4);
+            uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + at);
+            for (int i = tid; i < nc * (p.out_bf16 ? 64 : 128); i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    if (warp == kMmaWarp && n > 0) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // The merge kernel's record of this range: its first sequence, and whether it starts inside it.
+    if (tid == 0 && ct == 0) p.record[range] = n > 0 ? make_int2(static_cast<int>(plan[12]), plan[13] > 0) : make_int2(-1, 0);
+    if (n == 0) return;
+    const uint32_t tmem = *tmem_slot;
+    const int b0 = static_cast<int>(plan[12]), t0 = static_cast<int>(plan[13]);
+
+    auto wait = [&](uint32_t b, uint32_t parity) -> bool {  // bounded; gives up at once after another role did
+        if (*abort_flag) return false;
+        if (mbar_wait(b, parity)) return true;
+        *abort_flag = 1u;
+        return false;
+    };
+    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {  // lane 0 polls for the warp
+        bool ok = false;
+        if (lane == 0) ok = wait(b, parity);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        __syncwarp();
+        return ok;
+    };
+
+    if (warp == kProducerWarp) {
+        // ---------------- TMA producer: lane j < 4 copies block j of a tile ----------------
+        Walk w;
+        w.at(p, b0, t0);
+        auto block_id = [&]() -> int {  // -1: past the context, or an invalid id (never copied)
+            const int jb = w.t * kTileBlocks + lane;
+            if (lane >= kTileBlocks || jb * kBlockSize >= w.keys) return -1;
+            const int id = __ldg(p.block_tables + static_cast<size_t>(w.b) * p.max_blocks + jb);
+            return static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks) ? id : -1;
+        };
+        int id = block_id();
+        for (int i = 0; i < n; ++i) {
+            const int cur = id;
+            if (i + 1 < n) {
+                w.next(p);
+                id = block_id();
+            }
+            const int st = i % kStages;
+            if (i >= kStages && !warp_wait(bar(kBarKvEmpty + st), ((i / kStages) - 1) & 1)) break;
+            const int count = __popc(__ballot_sync(0xffffffffu, cur >= 0));
+            if (lane == 0) mbar_arrive_expect_tx(bar(kBarKvFull + st), count * kBlockBytes);
+            __syncwarp();
+            if (cur >= 0)
+                tma_load_5d(sbase + L::kKv + st * kStageBytes + lane * kBlockBytes, &kvmap, bar(kBarKvFull + st), 0, 0, 0, 0,
+                            cur);
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------- tensor thread: the next S or the next P V, whichever is ready ----------------
+        if (lane == 0) {
+            Walk wq, wp;
+            wq.at(p, b0, t0);
+            wp = wq;
+            const uint64_t q_desc = sw128_desc(sbase + L::kQ, 16, 1024);
+            const uint64_t k_desc = sw128_desc(sbase + L::kKv, 16, kGroupBytes);
+            const uint64_t v_desc = sw128_desc(sbase + L::kKv, 1024, kGroupBytes);
+            const uint64_t p_desc = sw128_desc(sbase + L::kP, 16, 1024);
+            int qk = 0, pv = 0, pieces = 0;
+            uint64_t t_idle = 0;
+            while (pv < n) {
+                bool did = false;
+                if (qk < n && qk <= pv + 1) {  // S buffer qk & 1: its last reader was seen done before P V (qk - 2)
+                    const bool first = qk == 0 || wq.t == 0;
+                    const int st = qk % kStages;
+                    if ((!first || mbar_test_wait(bar(kBarQFull), pieces & 1)) &&
+                        mbar_test_wait(bar(kBarKvFull + st), (qk / kStages) & 1)) {
+                        tc_fence_after();
+                        const uint32_t d = tmem + kTmemS + 64 * (qk & 1);
+#pragma unroll
+                        for (int c = 0; c < 9; ++c)
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_bf16(d, q_desc + ((c * NCOL * 128 + kk * 32) >> 4),
+                                          k_desc + ((st * kStageBytes + c * 1024 + kk * 32) >> 4), idesc(64, kTile, false),
+                                          c + kk > 0);
+                        umma_commit(bar(kBarSFull + (qk & 1)));
+                        pieces += first;
+                        if (++qk < n) wq.next(p);
+                        did = true;
+                    }
+                }
+                if (!did && pv < qk && mbar_test_wait(bar(kBarPFull), pv & 1)) {
+                    tc_fence_after();
+                    const bool first = pv == 0 || wp.t == 0;
+                    const int st = pv % kStages;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+                        for (int m = 0; m < 4; ++m)
+                            umma_bf16(tmem + m * NCOL, v_desc + ((st * kStageBytes + ks * kBlockBytes + m * 2048) >> 4),
+                                      p_desc + ((ks * 32) >> 4), idesc(128, NCOL, true), !first || ks > 0);
+                    umma_commit(bar(kBarKvEmpty + st));
+                    umma_commit(bar(kBarPvDone));
+                    if (++pv < n) wp.next(p);
+                    did = true;
+                }
+                if (did) {
+                    t_idle = 0;
+                    continue;
+                }
+                if (*abort_flag) break;
+                const uint64_t now = globaltimer_ns();
+                if (t_idle == 0) t_idle = now;
+                if (now - t_idle > kWaitLimitNs) {
+                    *abort_flag = 1u;
+                    break;
+                }
+            }
+        }
+    } else {
+        // ---------------- softmax, rescaling and epilogue: 8 warps ----------------
+        const int quarter = warp & 3, half = warp >> 2;
+        const int row = quarter * 16 + lane;             // M = 64: rows 16 q .. lie in lanes 32 q .. +15
+        const bool has = lane < 16 && row < NCOL;        // this thread keeps a column's half
+        const bool warp_has = quarter * 16 < NCOL;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const int q_row = row < nc ? (c0 + row) / p.heads : p.q_per_seq - 1;
+        float *xch = reinterpret_cast<float *>(smem + L::kXch);
+        float *alpha_s = reinterpret_cast<float *>(smem + L::kAlpha);
+        auto soft_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); };
+        bool alive = true;
+
+        // Sequence b's Q: 72 vectors a column, zeros behind the last one, in the operand's swizzle.
+        auto load_q = [&](int b) {
+            for (int idx = tid; idx < NCOL * 72; idx += kSoftThreads) {
+                const int r = idx / 72, v = idx - r * 72;
+                const uint32_t dst = sbase + L::kQ + (v >> 3) * (NCOL * 128) + r * 128 + (((v & 7) ^ (r & 7)) << 4);
+                const int c = c0 + r;
+                const int64_t qr = static_cast<int64_t>(b) * p.q_per_seq + c / p.heads, h = c % p.heads;
+                const uint16_t *src = v < 64 ? static_cast<const uint16_t *>(p.q_latent) + qr * p.ql_row + h * p.ql_head + v * 8
+                                             : static_cast<const uint16_t *>(p.q_rope) + qr * p.qr_row + h * p.qr_head +
+                                                   (v - 64) * 8;
+                if (r < nc)
+                    cp_async_16(dst, src);
+                else
+                    sts128(dst, make_uint4(0u, 0u, 0u, 0u));
+            }
+        };
+        auto publish_q = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarQFull));
+        };
+
+        Walk w;
+        w.at(p, b0, t0);
+        load_q(w.b);
+        publish_q();
+        float m_ref = -INFINITY, l = 0.f;
+        bool piece_mid = t0 > 0;  // the piece does not hold its sequence's first key
+        for (int i = 0; i < n; ++i) {
+            const bool first = i == 0 || w.t == 0;
+            const bool last = i == n - 1 || w.t == w.nt - 1;
+            if (first) {
+                m_ref = -INFINITY;
+                l = 0.f;
+            }
+            // Blocks of the tile with an invalid id: flagged, their keys masked.
+            const int jb = w.t * kTileBlocks + lane;
+            const bool bad_lane =
+                lane < kTileBlocks && jb * kBlockSize < w.keys &&
+                static_cast<unsigned>(__ldg(p.block_tables + static_cast<size_t>(w.b) * p.max_blocks + jb)) >=
+                    static_cast<unsigned>(p.num_blocks);
+            const uint32_t bad = __ballot_sync(0xffffffffu, bad_lane);
+            if (bad && tid == 0) atomicOr(p.status, kStatusBadBlockId);
+            const int left = w.keys - w.t * kTile;  // keys of the tile that exist (may pass 64)
+
+            alive = alive && warp_wait(bar(kBarSFull + (i & 1)), (i >> 1) & 1);
+            float x[32];
+            float mx = -INFINITY;
+            if (alive && warp_has) {
+                tc_fence_after();
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem + lanes + kTmemS + 64 * (i & 1) + 32 * half, v);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]) * p.scale_log2;
+                // Row q_row sees keys up to keys - q_per_seq + q_row; bad blocks see none.
+                if (left - p.q_per_seq + 1 < kTile || bad) {
+                    const int limit = left - p.q_per_seq + q_row - 32 * half;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (e > limit || ((bad >> (2 * half + (e >> 4))) & 1u)) x[e] = -INFINITY;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) mx = fmax3(mx, x[e], x[e + 1]);
+            }
+            // The last S of a piece is complete: its Q can make way for the next sequence's.
+            const bool more = last && i + 1 < n;
+            Walk nx = w;
+            if (i + 1 < n) nx.next(p);
+            if (more && alive) load_q(nx.b);
+
+            float *xm = xch + (i & 1) * 128;
+            if (has) xm[half * 64 + row] = mx;
+            bool drained = false;  // this warp saw P V (i - 1) complete
+            if (bar_red_or(1, kSoftThreads, has && mx > m_ref + kRaise)) {
+                float alpha = 1.f;
+                if (has) {
+                    const float mt = fmaxf(xm[row], xm[64 + row]);
+                    if (mt > m_ref + kRaise) {
+                        alpha = fast_exp2(m_ref - mt);  // 0 from -inf
+                        m_ref = mt;
+                        l *= alpha;
+                    }
+                    if (half == 0) alpha_s[row] = alpha;
+                }
+                if (!first) {  // (the first P V of a piece overwrites O)
+                    soft_sync();
+                    alive = alive && warp_wait(bar(kBarPvDone), (i - 1) & 1);
+                    drained = true;
+                    if (alive) {
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 2 * NCOL; c += 16) {  // dim tiles 2 half, 2 half + 1
+                            uint32_t o[16];
+                            const uint32_t at = tmem + lanes + 2 * half * NCOL + c;
+                            tmem_ld_32x32b_x16(at, o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha_s[(c + e) % NCOL]);
+                            tmem_st_32x32b_x16(at, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+            }
+            // Weights, rounded to bf16 (relative 2^-8); l adds what P V will read.
+            uint32_t pk[16];
+            if (warp_has) {
+                const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    pk[e] = pack_bf16x2(fast_exp2(x[2 * e] - mu), fast_exp2(x[2 * e + 1] - mu));
+                    s0 += __uint_as_float(pk[e] << 16);
+                    s1 += __uint_as_float(pk[e] & 0xffff0000u);
+                }
+                l += s0 + s1;
+            }
+            if (i > 0 && !drained) alive = alive && warp_wait(bar(kBarPvDone), (i - 1) & 1);  // P is free again
+            if (alive) {
+                if (has) {
+                    const uint32_t dst = sbase + L::kP + row * 128;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        sts128(dst + (((4 * half + c) ^ (row & 7)) << 4),
+                               make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]));
+                }
+                // Rows that no key fills (past the context, of an invalid block) hold whatever was there:
+                // their weights are 0, their values have to be finite.
+                if (left < kTile || bad) {
+                    alive = warp_wait(bar(kBarKvFull + i % kStages), (i / kStages) & 1);
+                    const uint32_t kv = sbase + L::kKv + (i % kStages) * kStageBytes;
+                    for (int idx = tid; alive && idx < kTile * 64; idx += kSoftThreads) {
+                        const int key = idx >> 6, v = idx & 63;  // (all of a row's 16-byte chunks: the swizzle is moot)
+                        if (key >= left || ((bad >> (key >> 4)) & 1u))
+                            sts128(kv + (key >> 3) * kGroupBytes + (v >> 3) * 1024 + (key & 7) * 128 + (v & 7) * 16,
+                                   make_uint4(0u, 0u, 0u, 0u));
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (alive && lane == 0) mbar_arrive(bar(kBarPFull));
+            if (more && alive) publish_q();
+
+            if (last) {
+                // ---- the piece's columns: whole sequences to out, parts to the workspace ----
+                const bool whole = !piece_mid && w.t == w.nt - 1;
+                // Slot 0: the range's first piece when it starts inside its sequence; else slot 1.
+                const size_t slot = (static_cast<size_t>(range) * 2 + (piece_mid ? 0 : 1)) * (p.col_tiles * p.cols_per_tile) + c0;
+                soft_sync();  // the maxima have been read
+                if (has) xch[half * 64 + row] = l;
+                soft_sync();
+                if (tid < NCOL) {
+                    const float sum = xch[tid] + xch[64 + tid];
+                    alpha_s[tid] = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+                    if (!whole && tid < nc) p.part_l[slot + tid] = sum;
+                }
+                if (!whole && has && half == 0 && row < nc) p.part_m[slot + row] = m_ref;
+                soft_sync();
+                alive = alive && warp_wait(bar(kBarPvDone), i & 1);
+                if (alive) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 2 * NCOL; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld_32x32b_x16(tmem + lanes + 2 * half * NCOL + c, o);
+                        const int col = c % NCOL, dim = (2 * half + c / NCOL) * 128 + 32 * quarter + lane;
+                        if (!whole) {
+                            float *dst = p.part_o + (slot + col) * kLatentDim + dim;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (col + e < nc) dst[static_cast<size_t>(e) * kLatentDim] = __uint_as_float(o[e]);
+                        } else if (p.out_bf16) {
+                            // lanes 2 d and 2 d + 1 swap a value: each then stores two dims of one column
+                            uint32_t *dst = static_cast<uint32_t *>(p.out) +
+                                            ((static_cast<size_t>(w.b) * cols + c0 + col) * kLatentDim + (dim & ~1)) / 2;
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                const float a = __uint_as_float(o[e]) * alpha_s[col + e];
+                                const float d = __uint_as_float(o[e + 1]) * alpha_s[col + e + 1];
+                                const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : d, 1);
+                                const int ce = e + (lane & 1);
+                                if (col + ce < nc)
+                                    dst[static_cast<size_t>(ce) * (kLatentDim / 2)] =
+                                        lane & 1 ? pack_bf16x2(other, d) : pack_bf16x2(a, other);
+                            }
+                        } else {
+                            float *dst = static_cast<float *>(p.out) + (static_cast<size_t>(w.b) * cols + c0 + col) * kLatentDim + dim;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (col + e < nc)
+                                    dst[static_cast<size_t>(e) * kLatentDim] = __uint_as_float(o[e]) * alpha_s[col + e];
+                        }
+                    }
+                    tc_fence_before();
+                }
+                piece_mid = false;
+                soft_sync();  // the factors have been read
+            }
+            w = nx;
+        }
+    }
+
+    // ---- teardown: every role is done (or gave up); free tensor memory ----
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort_flag && tid == 0) {
+        atomicOr(p.status, kStatusTimeout);
+        // Copies and MMAs that are still in flight: let them finish before the CTA's memory is freed.
+        const uint64_t until = globaltimer_ns() + kWaitLimitNs;
+        while (globaltimer_ns() < until) {
+        }
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Folds the parts of the y-th split sequence: CTA x takes column x of its rows.  A sequence
+// is split where a range starts inside it; its parts are the last piece of the range before
+// the first such range (slot 1) and the first pieces (slot 0) of the ranges from there on.
+constexpr int kMergeThreads = 512;  // 4 groups of 128 threads (4 dims each) take every 4th part
+__global__ void __launch_bounds__(kMergeThreads) latent_merge_kernel(const LatentDecodeParams p) {
+    __shared__ int s_first, s_parts, s_b;
+    __shared__ float s_w[kLatentMaxRanges];
+    __shared__ float s_sum[2][kMergeThreads / 32];
+    __shared__ float4 s_o[kMergeThreads];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (warp == 0) {
+        int seen = 0, first = 0;
+        for (int base = 0; base < p.ranges && !first; base += 32) {
+            const int r = base + lane;
+            bool is = false;
+            if (r >= 1 && r < p.ranges) {
+                const int2 a = p.record[r - 1], c = p.record[r];
+                is = c.x >= 0 && c.y && !(a.y && a.x == c.x);
+            }
+            uint32_t mask = __ballot_sync(0xffffffffu, is);
+            const int here = __popc(mask);
+            if (seen + here > static_cast<int>(blockIdx.y)) {
+                for (int k = blockIdx.y - seen; k > 0; --k) mask &= mask - 1;
+                first = base + __ffs(mask) - 1;
+            }
+            seen += here;
+        }
+        int parts = 0;
+        if (first) {
+            const int b = p.record[first].x;
+            parts = 1;
+            bool go = true;
+            for (int base = first; go && base < p.ranges; base += 32) {
+                const int r = base + lane;
+                const bool same = r < p.ranges && p.record[r].x == b && p.record[r].y;
+                const uint32_t mask = __ballot_sync(0xffffffffu, same);
+                parts += mask == 0xffffffffu ? 32 : __ffs(~mask) - 1;
+                go = mask == 0xffffffffu;
+            }
+            if (lane == 0) s_b = b;
+        }
+        if (lane == 0) {
+            s_first = first;
+            s_parts = parts;
+        }
+    }
+    __syncthreads();
+    const int parts = s_parts, first = s_first;
+    if (parts == 0) return;
+    const int col = blockIdx.x, padded = p.col_tiles * p.cols_per_tile;
+    auto slot = [&](int k) {  // part k's index among the (range, slot, column) partials
+        return (static_cast<size_t>(first - 1 + k) * 2 + (k == 0 ? 1 : 0)) * padded + col;
+    };
+    float m = -INFINITY;
+    for (int k = tid; k < parts; k += kMergeThreads) m = fmaxf(m, p.part_m[slot(k)]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (lane == 0) s_sum[0][warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMergeThreads / 32; ++k) m = fmaxf(m, s_sum[0][k]);
+    float sum = 0.f;
+    for (int k = tid; k < parts; k += kMergeThreads) {
+        const float pm = p.part_m[slot(k)];
+        const float wk = pm == -INFINITY ? 0.f : exp2f(pm - m);
+        s_w[k] = wk;
+        sum += wk * p.part_l[slot(k)];
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) s_sum[1][warp] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMergeThreads / 32; ++k) sum += s_sum[1][k];
+    const int group = tid >> 7, d4 = tid & 127;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = group; k < parts; k += 4) {
+        const float wk = s_w[k];
+        if (wk == 0.f) continue;  // nothing was visible: its O was never written from finite weights
+        const float4 v = reinterpret_cast<const float4 *>(p.part_o + slot(k) * kLatentDim)[d4];
+        o.x += wk * v.x, o.y += wk * v.y, o.z += wk * v.z, o.w += wk * v.w;
+    }
+    s_o[tid] = o;
+    __syncthreads();
+    if (group != 0) return;
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    for (int k = 1; k < 4; ++k) {
+        const float4 v = s_o[k * 128 + d4];
+        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+    const size_t at = (static_cast<size_t>(s_b) * p.heads * p.q_per_seq + col) * kLatentDim + 4 * d4;
+    if (p.out_bf16)
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    else
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 template <bool FP8>
-__global__ void __launch_bounds__(128) latent_decode_kernel(const LatentDecodeParams p) {
+__global__ void __launch_bounds__(128) latent_decode_simple_kernel(const LatentDecodeParams p) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
@@ -111,10 +743,37 @@ __global__ void __launch_bounds__(128) latent_decode_kernel(const LatentDecodePa
 
 }  // namespace
 
-cudaError_t launch_latent_decode(const LatentDecodeParams &p, bool fp8, cudaStream_t stream) {
-    const int64_t units = static_cast<int64_t>(p.num_seqs) * p.q_per_seq * p.heads;
-    const dim3 grid(static_cast<unsigned>((units + 3) / 4));
-    return launch_pdl(fp8 ? latent_decode_kernel<true> : latent_decode_kernel<false>, grid, dim3(128), 0, stream, p);
+template <int NCOL>
+cudaError_t prepare_one() {
+    return cudaFuncSetAttribute(latent_decode_kernel<NCOL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Layout<NCOL>::kBytes));
+}
+
+cudaError_t latent_decode_prepare_device() {
+    cudaError_t e = prepare_one<16>();
+    if (e == cudaSuccess) e = prepare_one<32>();
+    if (e == cudaSuccess) e = prepare_one<64>();
+    return e;
+}
+
+template <int NCOL>
+cudaError_t launch_one(const CUtensorMap &kvmap, const LatentDecodeParams &p, cudaStream_t stream) {
+    return launch_pdl(latent_decode_kernel<NCOL>, dim3(p.ranges * p.col_tiles), dim3(kThreads), Layout<NCOL>::kBytes, stream,
+                      kvmap, p);
+}
+
+cudaError_t launch_latent_decode(const CUtensorMap &kvmap, const LatentDecodeParams &p, bool fp8, cudaStream_t stream) {
+    if (fp8) {
+        const int64_t units = static_cast<int64_t>(p.num_seqs) * p.q_per_seq * p.heads;
+        const dim3 grid(static_cast<unsigned>((units + 3) / 4));
+        return launch_pdl(latent_decode_simple_kernel<true>, grid, dim3(128), 0, stream, p);
+    }
+    cudaError_t e = p.cols_per_tile <= 16   ? launch_one<16>(kvmap, p, stream)
+                    : p.cols_per_tile <= 32 ? launch_one<32>(kvmap, p, stream)
+                                            : launch_one<64>(kvmap, p, stream);
+    if (e != cudaSuccess || p.ranges <= 1) return e;
+    const dim3 grid(p.heads * p.q_per_seq, std::min(p.num_seqs, p.ranges - 1));
+    return launch_pdl(latent_merge_kernel, grid, dim3(kMergeThreads), 0, stream, p);
 }
 
 }  // namespace pkv
