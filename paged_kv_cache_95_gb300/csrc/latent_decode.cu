@@ -12,10 +12,13 @@
 // one; whole sequences are written out, parts go to the workspace as (m, l, O) and
 // the merge kernel folds them.  No CTA waits for another.
 //
-// Per tile (64 keys = 4 blocks of 16, 72 KB, one TMA copy a block; 2 stages):
+// Per tile (64 keys = 4 blocks of 16, 72 KB, 2 stages):
 //  * S [64 columns x 64 keys] = Q K^T: M = 64, N = 64, 36 steps of 16 values; Q stays in
 //    shared memory (128-byte swizzle, 9 chunks of 64 values).
-//  * softmax by 8 warps, one (row, half of the keys) a thread: running reference m,
+//  * half of the blocks are copied by TMA, half by cp.async: one SM's TMA unit delivers 24
+//    bytes a clock however much is in flight (measured, from L2 as from HBM), both paths
+//    together 47; HBM's share of an SM is 23-28, so a ring on TMA alone never catches up.
+//  * softmax by 8 warps (a warp: 16 rows, half of the keys): running reference m,
 //    raised only when a score passes it by 2^8 (one vote a tile), sum l in fp32;
 //    P = 2^(s - m) rounded to bf16 (l adds the rounded weights, so numerator and
 //    denominator round alike) into shared memory as the B operand.
@@ -23,8 +26,9 @@
 //    operand: M = 128 (4 tiles of dims), N = columns, 4 steps of 16 keys.  Transposed,
 //    because O has 512 x 64 values: as 128 lanes x 256 columns it leaves tensor memory
 //    for two S buffers, and M is full for any number of heads.
-// The tensor thread takes whichever is ready, the next S or the next P V: waiting for
-// the next tile's copy before a P V would leave no copy in flight.
+// S and P V are issued by two warps, so neither waits behind the other's inputs (one
+// issuer that waits for the next tile's copy before a P V leaves no copy in flight);
+// P V frees a stage 16 keys at a time.
 //
 // Every mbarrier wait is bounded; a role whose wait runs out raises a CTA-wide abort
 // flag, the others stop at their next wait, and the CTA records PKV_STATUS_TIMEOUT and
@@ -47,9 +51,12 @@ constexpr int kTileBlocks = kTile / kBlockSize;
 constexpr int kSoftWarps = 8;                 // warps w and w + 4 share rows 16 (w % 4) .. and split the keys
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kProducerWarp = kSoftWarps;
-constexpr int kMmaWarp = kSoftWarps + 1;
-constexpr int kThreads = (kSoftWarps + 2) * 32;
+constexpr int kScoreWarp = kSoftWarps + 1;    // issues S = Q K^T
+constexpr int kValueWarp = kSoftWarps + 2;    // issues O^T += V^T P^T
+constexpr int kLoadWarp = kSoftWarps + 3;     // two pairs of copying warps, one pair a stage
+constexpr int kThreads = (kSoftWarps + 7) * 32;
 constexpr int kStages = 2;
+constexpr int kTmaBlocks = 2;                 // blocks of a tile that TMA copies; the others go through cp.async
 constexpr uint32_t kBlockBytes = kBlockSize * kLatentRow * 2;  // 18 KB: [2 slot groups][9 chunks][8 slots][128 B]
 constexpr uint32_t kGroupBytes = kBlockBytes / 2;              // 8 slots
 constexpr uint32_t kStageBytes = kTileBlocks * kBlockBytes;
@@ -57,8 +64,17 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // O^T in columns [0, 4 NCOL), S of tile i in [256 + 64 (i & 1), +64)
 constexpr float kRaise = 8.f;     // the reference follows the maximum when it is passed by 2^8
 
-enum { kBarKvFull = 0, kBarKvEmpty = kStages, kBarSFull = 2 * kStages, kBarPFull = 2 * kStages + 2, kBarPvDone, kBarQFull,
-       kNumBars };
+// kv_full[stage], kv_empty[stage][block], s_full[2], s_empty[2], p_full, pv_done, q_full
+enum {
+    kBarKvFull = 0,
+    kBarKvEmpty = kBarKvFull + kStages,
+    kBarSFull = kBarKvEmpty + kStages * kTileBlocks,
+    kBarSEmpty = kBarSFull + 2,
+    kBarPFull = kBarSEmpty + 2,
+    kBarPvDone,
+    kBarQFull,
+    kNumBars
+};
 
 template <int NCOL>
 struct Layout {
@@ -71,7 +87,7 @@ struct Layout {
     static constexpr uint32_t kXch = (kAbort + 4 + 15) / 16 * 16;  // [tile & 1][key half][64] maxima, later sums
     static constexpr uint32_t kAlpha = kXch + 4 * 64 * 4;          // [64] factors of O's columns
     static constexpr uint32_t kPlan = kAlpha + 64 * 4;             // warp totals, then the range's start
-    static constexpr uint32_t kBytes = kPlan + 16 * 8;
+    static constexpr uint32_t kBytes = kPlan + 18 * 8;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
     static_assert(kKv % 1024 == 0 && kP % 1024 == 0, "swizzle atoms");
 };
@@ -147,7 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t *plan = reinterpret_cast<int64_t *>(smem + L::kPlan);
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i)
-            mbar_init(bar(i), i == kBarPFull || i == kBarQFull ? kSoftWarps : 1);
+            mbar_init(bar(i), i < kBarKvEmpty ? kTmaBlocks + 2
+                              : i == kBarSEmpty || i == kBarSEmpty + 1 || i == kBarPFull || i == kBarQFull ? kSoftWarps : 1);
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -181,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t acc = upto - mine;
         int b = b_lo;
         for (; acc + tiles_of(p, b) <= start; ++b) acc += tiles_of(p, b);
-        plan[12] = b;
-        plan[13] = start - acc;
+        plan[16] = b;
+        plan[17] = start - acc;
     }
     // Sequences without keys: zero rows, and the checks of every length, shared out over the ranges.
     for (int b = range; b < p.num_seqs; b += p.ranges) {
@@ -198,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = tid; i < nc * (p.out_bf16 ? 64 : 128); i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    if (warp == kMmaWarp && n > 0) {
+    if (warp == kScoreWarp && n > 0) {
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
@@ -206,27 +223,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     // The merge kernel's record of this range: its first sequence, and whether it starts inside it.
-    if (tid == 0 && ct == 0) p.record[range] = n > 0 ? make_int2(static_cast<int>(plan[12]), plan[13] > 0) : make_int2(-1, 0);
+    if (tid == 0 && ct == 0) p.record[range] = n > 0 ? make_int2(static_cast<int>(plan[16]), plan[17] > 0) : make_int2(-1, 0);
     if (n == 0) return;
     const uint32_t tmem = *tmem_slot;
-    const int b0 = static_cast<int>(plan[12]), t0 = static_cast<int>(plan[13]);
+    const int b0 = static_cast<int>(plan[16]), t0 = static_cast<int>(plan[17]);
 
-    auto wait = [&](uint32_t b, uint32_t parity) -> bool {  // bounded; gives up at once after another role did
-        if (*abort_flag) return false;
-        if (mbar_wait(b, parity)) return true;
-        *abort_flag = 1u;
-        return false;
-    };
-    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {  // lane 0 polls for the warp
-        bool ok = false;
-        if (lane == 0) ok = wait(b, parity);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        __syncwarp();
-        return ok;
+    // A warp's bounded wait; it gives up soon after another role did.  The timer and the flag are
+    // read only every 64 tries: a read of %globaltimer between two tries delays the waiter by
+    // several hundred cycles.
+    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
+        uint64_t t_first = 0;
+        for (uint32_t tries = 0; !__all_sync(0xffffffffu, mbar_try_wait(b, parity)); ++tries) {
+            if ((tries & 63u) != 63u) continue;
+            const uint64_t now = globaltimer_ns();
+            if (t_first == 0) t_first = now;
+            if (__any_sync(0xffffffffu, *abort_flag != 0 || now - t_first > kWaitLimitNs)) {
+                *abort_flag = 1u;
+                return false;
+            }
+        }
+        return true;
     };
 
     if (warp == kProducerWarp) {
-        // ---------------- TMA producer: lane j < 4 copies block j of a tile ----------------
+        // ---------------- TMA producer: lane j copies block j of a tile ----------------
         Walk w;
         w.at(p, b0, t0);
         auto block_id = [&]() -> int {  // -1: past the context, or an invalid id (never copied)
@@ -243,84 +263,133 @@ __global__ void __launch_bounds__(kThreads, 1)
                 id = block_id();
             }
             const int st = i % kStages;
-            if (i >= kStages && !warp_wait(bar(kBarKvEmpty + st), ((i / kStages) - 1) & 1)) break;
-            const int count = __popc(__ballot_sync(0xffffffffu, cur >= 0));
-            if (lane == 0) mbar_arrive_expect_tx(bar(kBarKvFull + st), count * kBlockBytes);
-            __syncwarp();
-            if (cur >= 0)
-                tma_load_5d(sbase + L::kKv + st * kStageBytes + lane * kBlockBytes, &kvmap, bar(kBarKvFull + st), 0, 0, 0, 0,
-                            cur);
-        }
-    } else if (warp == kMmaWarp) {
-        // ---------------- tensor thread: the next S or the next P V, whichever is ready ----------------
-        if (lane == 0) {
-            Walk wq, wp;
-            wq.at(p, b0, t0);
-            wp = wq;
-            const uint64_t q_desc = sw128_desc(sbase + L::kQ, 16, 1024);
-            const uint64_t k_desc = sw128_desc(sbase + L::kKv, 16, kGroupBytes);
-            const uint64_t v_desc = sw128_desc(sbase + L::kKv, 1024, kGroupBytes);
-            const uint64_t p_desc = sw128_desc(sbase + L::kP, 16, 1024);
-            int qk = 0, pv = 0, pieces = 0;
-            uint64_t t_idle = 0;
-            while (pv < n) {
-                bool did = false;
-                if (qk < n && qk <= pv + 1) {  // S buffer qk & 1: its last reader was seen done before P V (qk - 2)
-                    const bool first = qk == 0 || wq.t == 0;
-                    const int st = qk % kStages;
-                    if ((!first || mbar_test_wait(bar(kBarQFull), pieces & 1)) &&
-                        mbar_test_wait(bar(kBarKvFull + st), (qk / kStages) & 1)) {
-                        tc_fence_after();
-                        const uint32_t d = tmem + kTmemS + 64 * (qk & 1);
+            bool ok = true;
 #pragma unroll
-                        for (int c = 0; c < 9; ++c)
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma_bf16(d, q_desc + ((c * NCOL * 128 + kk * 32) >> 4),
-                                          k_desc + ((st * kStageBytes + c * 1024 + kk * 32) >> 4), idesc(64, kTile, false),
-                                          c + kk > 0);
-                        umma_commit(bar(kBarSFull + (qk & 1)));
-                        pieces += first;
-                        if (++qk < n) wq.next(p);
-                        did = true;
-                    }
-                }
-                if (!did && pv < qk && mbar_test_wait(bar(kBarPFull), pv & 1)) {
-                    tc_fence_after();
-                    const bool first = pv == 0 || wp.t == 0;
-                    const int st = pv % kStages;
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-                        for (int m = 0; m < 4; ++m)
-                            umma_bf16(tmem + m * NCOL, v_desc + ((st * kStageBytes + ks * kBlockBytes + m * 2048) >> 4),
-                                      p_desc + ((ks * 32) >> 4), idesc(128, NCOL, true), !first || ks > 0);
-                    umma_commit(bar(kBarKvEmpty + st));
-                    umma_commit(bar(kBarPvDone));
-                    if (++pv < n) wp.next(p);
-                    did = true;
-                }
-                if (did) {
-                    t_idle = 0;
-                    continue;
-                }
-                if (*abort_flag) break;
-                const uint64_t now = globaltimer_ns();
-                if (t_idle == 0) t_idle = now;
-                if (now - t_idle > kWaitLimitNs) {
-                    *abort_flag = 1u;
-                    break;
+            for (int j = 0; j < kTmaBlocks; ++j) {  // P V frees a stage block by block
+                if (i >= kStages) ok = ok && warp_wait(bar(kBarKvEmpty + st * kTileBlocks + j), ((i / kStages) - 1) & 1);
+                if (ok && lane == j) {
+                    mbar_arrive_expect_tx(bar(kBarKvFull + st), cur >= 0 ? kBlockBytes : 0);
+                    if (cur >= 0)
+                        tma_load_5d(sbase + L::kKv + st * kStageBytes + j * kBlockBytes, &kvmap, bar(kBarKvFull + st), 0, 0,
+                                    0, 0, cur);
                 }
             }
+            if (!ok) break;
+        }
+    } else if (warp >= kLoadWarp) {
+        // ---------------- copying warps: the blocks from kTmaBlocks on of every second tile ----------------
+        const int st = (warp - kLoadWarp) >> 1, t = ((warp - kLoadWarp) & 1) * 32 + lane;  // 64 threads a stage
+        // 16-byte vector t + 64 k of a block (72 a slot): its place in the operand layout, k < 9 (the
+        // second group of 8 slots follows 9216 bytes on, on both sides).
+        uint32_t to[9];
+#pragma unroll
+        for (int k = 0; k < 9; ++k) {
+            const int v = t + 64 * k, r = v / 72, c = v - r * 72;
+            to[k] = (c >> 3) * 1024 + r * 128 + (((c & 7) ^ r) << 4);
+        }
+        Walk w;
+        w.at(p, b0, t0);
+        if (st == 1 && n > 1) w.next(p);
+        for (int i = st; i < n; i += kStages) {
+            int id = -1;
+            const int jb = w.t * kTileBlocks + lane;
+            if (lane < kTileBlocks && jb * kBlockSize < w.keys)
+                id = __ldg(p.block_tables + static_cast<size_t>(w.b) * p.max_blocks + jb);
+            if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) id = -1;
+            bool ok = true;
+#pragma unroll
+            for (int j = kTmaBlocks; j < kTileBlocks; ++j) {
+                const int blk = __shfl_sync(0xffffffffu, id, j);
+                if (i >= kStages) ok = ok && warp_wait(bar(kBarKvEmpty + st * kTileBlocks + j), ((i / kStages) - 1) & 1);
+                if (ok && blk >= 0) {
+                    const uint8_t *src = static_cast<const uint8_t *>(p.cache) + static_cast<size_t>(blk) * kBlockBytes + 16 * t;
+                    const uint32_t dst = sbase + L::kKv + st * kStageBytes + j * kBlockBytes;
+#pragma unroll
+                    for (int k = 0; k < 18; ++k)
+                        cp_async_16(dst + (k / 9) * kGroupBytes + to[k % 9], src + 1024 * k);
+                }
+            }
+            if (!ok) break;
+            for (int k = 0; k < kStages && i + 1 + k < n; ++k) w.next(p);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();  // generic writes -> the tensor core
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarKvFull + st));
+        }
+    } else if (warp == kScoreWarp) {
+        // ---------------- S = Q K^T ----------------
+        // (Both tensor warps run their loop whole, on warp-uniform values, and one elected lane
+        // issues: the descriptors stay in uniform registers.  Issued from a one-lane branch an
+        // MMA took 74-98 cycles to issue, against 36-52 in the pipe.)
+        Walk w;
+        w.at(p, b0, t0);
+        const uint64_t q_desc = sw128_desc(sbase + L::kQ, 16, 1024);
+        const uint64_t k_desc = sw128_desc(sbase + L::kKv, 16, kGroupBytes);
+        int pieces = 0;
+        for (int i = 0; i < n; ++i) {
+            const int st = i % kStages;
+            if (i == 0 || w.t == 0) {
+                if (!warp_wait(bar(kBarQFull), pieces & 1)) break;
+                ++pieces;
+            }
+            if (i >= 2 && !warp_wait(bar(kBarSEmpty + (i & 1)), ((i >> 1) - 1) & 1)) break;
+            if (!warp_wait(bar(kBarKvFull + st), (i / kStages) & 1)) break;
+            tc_fence_after();
+            const uint32_t d = tmem + kTmemS + 64 * (i & 1);
+            const uint64_t kd = k_desc + static_cast<uint32_t>(st) * (kStageBytes >> 4);
+            if (elect_one()) {
+#pragma unroll
+                for (int c = 0; c < 9; ++c)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16(d, q_desc + ((c * NCOL * 128 + kk * 32) >> 4), kd + ((c * 1024 + kk * 32) >> 4),
+                                  idesc(64, kTile, false), c + kk > 0);
+                umma_commit(bar(kBarSFull + (i & 1)));
+            }
+            __syncwarp();
+            if (i + 1 < n) w.next(p);
+        }
+    } else if (warp == kValueWarp) {
+        // ---------------- O^T += V^T P^T ----------------
+        Walk w;
+        w.at(p, b0, t0);
+        const uint64_t v_desc = sw128_desc(sbase + L::kKv, 1024, kGroupBytes);
+        const uint64_t p_desc = sw128_desc(sbase + L::kP, 16, 1024);
+        for (int i = 0; i < n; ++i) {
+            const int st = i % kStages;
+            const uint32_t keep = i > 0 && w.t > 0;  // a piece's first P V overwrites O
+            if (!warp_wait(bar(kBarPFull), i & 1)) break;
+            tc_fence_after();
+            const uint64_t vd = v_desc + static_cast<uint32_t>(st) * (kStageBytes >> 4);
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < kTileBlocks; ++ks) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        umma_bf16(tmem + m * NCOL, vd + ((ks * kBlockBytes + m * 2048) >> 4), p_desc + ((ks * 32) >> 4),
+                                  idesc(128, NCOL, true), ks > 0 ? 1u : keep);
+                    umma_commit(bar(kBarKvEmpty + st * kTileBlocks + ks));
+                }
+                umma_commit(bar(kBarPvDone));
+            }
+            __syncwarp();
+            if (i + 1 < n) w.next(p);
         }
     } else {
         // ---------------- softmax, rescaling and epilogue: 8 warps ----------------
         const int quarter = warp & 3, half = warp >> 2;
-        const int row = quarter * 16 + lane;             // M = 64: rows 16 q .. lie in lanes 32 q .. +15
-        const bool has = lane < 16 && row < NCOL;        // this thread keeps a column's half
+        // M = 64: rows 16 q .. of S lie in lanes 32 q .. +15.  The 16-lane load spreads them over the
+        // warp: a thread holds rows r and r + 8, of each 8 keys of every 32 (columns 8 j + 2 (lane % 4) + 0, 1).
+        const int row = quarter * 16 + (lane >> 2);
         const bool warp_has = quarter * 16 < NCOL;
+        const bool has = warp_has && (lane & 3) == 0;    // speaks for rows r and r + 8
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const int q_row = row < nc ? (c0 + row) / p.heads : p.q_per_seq - 1;
+        int q_row[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) q_row[k] = row + 8 * k < nc ? (c0 + row + 8 * k) / p.heads : p.q_per_seq - 1;
+        // P goes out as 8 x 8 matrices: this lane addresses row lane % 16 and 16-byte chunk 4 half + lane / 16 (+2).
+        const int p_row = quarter * 16 + (lane & 15);
+        const uint32_t p_at = sbase + L::kP + p_row * 128;
         float *xch = reinterpret_cast<float *>(smem + L::kXch);
         float *alpha_s = reinterpret_cast<float *>(smem + L::kAlpha);
         auto soft_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); };
@@ -353,14 +422,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.at(p, b0, t0);
         load_q(w.b);
         publish_q();
-        float m_ref = -INFINITY, l = 0.f;
+        float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         bool piece_mid = t0 > 0;  // the piece does not hold its sequence's first key
         for (int i = 0; i < n; ++i) {
             const bool first = i == 0 || w.t == 0;
             const bool last = i == n - 1 || w.t == w.nt - 1;
             if (first) {
-                m_ref = -INFINITY;
-                l = 0.f;
+                m_ref[0] = m_ref[1] = -INFINITY;
+                l[0] = l[1] = 0.f;
             }
             // Blocks of the tile with an invalid id: flagged, their keys masked.
             const int jb = w.t * kTileBlocks + lane;
@@ -373,24 +442,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int left = w.keys - w.t * kTile;  // keys of the tile that exist (may pass 64)
 
             alive = alive && warp_wait(bar(kBarSFull + (i & 1)), (i >> 1) & 1);
-            float x[32];
-            float mx = -INFINITY;
+            float x[16];  // [4 j + 2 k + e]: row r + 8 k, key 32 half + 8 j + 2 (lane % 4) + e
+            float mx[2] = {-INFINITY, -INFINITY};
             if (alive && warp_has) {
                 tc_fence_after();
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tmem + lanes + kTmemS + 64 * (i & 1) + 32 * half, v);
+                uint32_t v[16];
+                tmem_ld_16x256b_x4(tmem + lanes + kTmemS + 64 * (i & 1) + 32 * half, v);
+                tc_fence_before();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e]) * p.scale_log2;
+                for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]) * p.scale_log2;
                 // Row q_row sees keys up to keys - q_per_seq + q_row; bad blocks see none.
                 if (left - p.q_per_seq + 1 < kTile || bad) {
-                    const int limit = left - p.q_per_seq + q_row - 32 * half;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (e > limit || ((bad >> (2 * half + (e >> 4))) & 1u)) x[e] = -INFINITY;
+                    for (int e = 0; e < 16; ++e) {
+                        const int k = (e >> 1) & 1, key = 32 * half + 8 * (e >> 2) + 2 * (lane & 3) + (e & 1);
+                        if (key > left - p.q_per_seq + q_row[k] || ((bad >> (key >> 4)) & 1u)) x[e] = -INFINITY;
+                    }
                 }
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) mx = fmax3(mx, x[e], x[e + 1]);
+                for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mx[k] = fmax3(mx[k], x[4 * j + 2 * k], x[4 * j + 2 * k + 1]);
+                    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+                    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+                }
             }
+            __syncwarp();
+            if (alive && lane == 0) mbar_arrive(bar(kBarSEmpty + (i & 1)));
             // The last S of a piece is complete: its Q can make way for the next sequence's.
             const bool more = last && i + 1 < n;
             Walk nx = w;
@@ -398,18 +476,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more && alive) load_q(nx.b);
 
             float *xm = xch + (i & 1) * 128;
-            if (has) xm[half * 64 + row] = mx;
+            if (has) {
+                xm[half * 64 + row] = mx[0];
+                xm[half * 64 + row + 8] = mx[1];
+            }
             bool drained = false;  // this warp saw P V (i - 1) complete
-            if (bar_red_or(1, kSoftThreads, has && mx > m_ref + kRaise)) {
-                float alpha = 1.f;
-                if (has) {
-                    const float mt = fmaxf(xm[row], xm[64 + row]);
-                    if (mt > m_ref + kRaise) {
-                        alpha = fast_exp2(m_ref - mt);  // 0 from -inf
-                        m_ref = mt;
-                        l *= alpha;
+            if (bar_red_or(1, kSoftThreads, warp_has && (mx[0] > m_ref[0] + kRaise || mx[1] > m_ref[1] + kRaise))) {
+                if (warp_has) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float alpha = 1.f;
+                        const float mt = fmaxf(xm[row + 8 * k], xm[64 + row + 8 * k]);
+                        if (mt > m_ref[k] + kRaise) {
+                            alpha = fast_exp2(m_ref[k] - mt);  // 0 from -inf
+                            m_ref[k] = mt;
+                            l[k] *= alpha;
+                        }
+                        if (has && half == 0) alpha_s[row + 8 * k] = alpha;
                     }
-                    if (half == 0) alpha_s[row] = alpha;
                 }
                 if (!first) {  // (the first P V of a piece overwrites O)
                     soft_sync();
@@ -432,26 +516,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // Weights, rounded to bf16 (relative 2^-8); l adds what P V will read.
-            uint32_t pk[16];
+            uint32_t pk[8];  // [2 j + k]: the pair of row r + 8 k in 8-key group j
             if (warp_has) {
-                const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-                float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    pk[e] = pack_bf16x2(fast_exp2(x[2 * e] - mu), fast_exp2(x[2 * e + 1] - mu));
-                    s0 += __uint_as_float(pk[e] << 16);
-                    s1 += __uint_as_float(pk[e] & 0xffff0000u);
+                for (int k = 0; k < 2; ++k) {
+                    const float mu = m_ref[k] == -INFINITY ? 0.f : m_ref[k];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t w2 = pack_bf16x2(fast_exp2(x[4 * j + 2 * k] - mu), fast_exp2(x[4 * j + 2 * k + 1] - mu));
+                        l[k] += __uint_as_float(w2 << 16) + __uint_as_float(w2 & 0xffff0000u);
+                        pk[2 * j + k] = w2;
+                    }
                 }
-                l += s0 + s1;
             }
             if (i > 0 && !drained) alive = alive && warp_wait(bar(kBarPvDone), (i - 1) & 1);  // P is free again
             if (alive) {
-                if (has) {
-                    const uint32_t dst = sbase + L::kP + row * 128;
+                if (warp_has) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        sts128(dst + (((4 * half + c) ^ (row & 7)) << 4),
-                               make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]));
+                    for (int j = 0; j < 4; j += 2)
+                        stmatrix_x4(p_at + (((4 * half + j + (lane >> 4)) ^ (p_row & 7)) << 4), pk[2 * j], pk[2 * j + 1],
+                                    pk[2 * j + 2], pk[2 * j + 3]);
                 }
                 // Rows that no key fills (past the context, of an invalid block) hold whatever was there:
                 // their weights are 0, their values have to be finite.
@@ -478,14 +562,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Slot 0: the range's first piece when it starts inside its sequence; else slot 1.
                 const size_t slot = (static_cast<size_t>(range) * 2 + (piece_mid ? 0 : 1)) * (p.col_tiles * p.cols_per_tile) + c0;
                 soft_sync();  // the maxima have been read
-                if (has) xch[half * 64 + row] = l;
+                if (warp_has) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+                        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+                        if (has) xch[half * 64 + row + 8 * k] = l[k];
+                    }
+                }
                 soft_sync();
                 if (tid < NCOL) {
                     const float sum = xch[tid] + xch[64 + tid];
                     alpha_s[tid] = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
                     if (!whole && tid < nc) p.part_l[slot + tid] = sum;
                 }
-                if (!whole && has && half == 0 && row < nc) p.part_m[slot + row] = m_ref;
+                if (!whole && has && half == 0) {
+                    if (row < nc) p.part_m[slot + row] = m_ref[0];
+                    if (row + 8 < nc) p.part_m[slot + row + 8] = m_ref[1];
+                }
                 soft_sync();
                 alive = alive && warp_wait(bar(kBarPvDone), i & 1);
                 if (alive) {
@@ -543,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 // Folds the parts of the y-th split sequence: CTA x takes column x of its rows.  A sequence
