@@ -54,10 +54,10 @@ struct LatentDecodeParams {
     // (the last may hold fewer), the keys of all sequences in `ranges` ranges of tiles.
     int32_t col_tiles, cols_per_tile, ranges;
     int2 *record;            // [ranges]: first sequence (-1: empty), 1 if the range starts inside it
-    float *part_m, *part_l;  // [ranges][2][col_tiles * cols_per_tile]  (log2 domain, scale folded in)
+    float2 *part_ml;         // [ranges][2][col_tiles * cols_per_tile] (m, l), log2 domain, scale folded in
     float *part_o;           // the same x [512], unnormalised
 };
-constexpr int kLatentMaxRanges = 512;  // more SMs than any device has
+constexpr int kLatentMaxRanges = 160;  // at least the SMs (152); the merge keeps 5 records a lane
 constexpr int kLatentMaxCols = 64;     // columns a CTA takes
 constexpr int kLatentTile = 64;        // keys a tile
 cudaError_t latent_decode_prepare_device();

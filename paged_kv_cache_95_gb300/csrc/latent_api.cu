@@ -64,10 +64,10 @@ bool encode_latent_map(CUtensorMap *map, const void *base, int32_t num_blocks) {
 
 // How a decode call is split: one CTA per SM, column tiles of at most 64 columns of equal
 // size, and as many ranges of keys as there are SMs for a column tile (never more than
-// tiles).  Workspace: [status 256 B | records | part_m | part_l | part_o].
+// tiles).  Workspace: [status 256 B | records | part_ml | part_o].
 struct DecodePlan {
     int32_t col_tiles, cols_per_tile, ranges;
-    size_t off_m, off_l, off_o, total;
+    size_t off_ml, off_o, total;
 };
 DecodePlan plan_decode(int32_t num_seqs, int32_t q_per_seq, int32_t heads, int32_t max_blocks, int sms) {
     DecodePlan pl{};
@@ -79,9 +79,8 @@ DecodePlan plan_decode(int32_t num_seqs, int32_t q_per_seq, int32_t heads, int32
     const int64_t ranges = std::min<int64_t>(std::max(1, sms / pl.col_tiles), tiles);
     pl.ranges = static_cast<int32_t>(std::min<int64_t>(ranges, pkv::kLatentMaxRanges));
     const size_t rows = static_cast<size_t>(pl.ranges) * 2 * pl.col_tiles * pl.cols_per_tile;
-    pl.off_m = kStatusBytes + align_up(static_cast<size_t>(pl.ranges) * 8, 256);
-    pl.off_l = pl.off_m + align_up(rows * 4, 256);
-    pl.off_o = pl.off_l + align_up(rows * 4, 256);
+    pl.off_ml = kStatusBytes + align_up(static_cast<size_t>(pl.ranges) * 8, 256);
+    pl.off_o = pl.off_ml + align_up(rows * 8, 256);
     pl.total = pl.off_o + rows * pkv::kLatentDim * 4;
     return pl;
 }
@@ -183,8 +182,7 @@ int decode_impl(void *out, int32_t out_dtype, const void *q_latent, int64_t ql_r
     p.cols_per_tile = pl.cols_per_tile;
     p.ranges = pl.ranges;
     p.record = reinterpret_cast<int2 *>(ws + kStatusBytes);
-    p.part_m = reinterpret_cast<float *>(ws + pl.off_m);
-    p.part_l = reinterpret_cast<float *>(ws + pl.off_l);
+    p.part_ml = reinterpret_cast<float2 *>(ws + pl.off_ml);
     p.part_o = reinterpret_cast<float *>(ws + pl.off_o);
     CUtensorMap kvmap{};
     if (!fp8 && !encode_latent_map(&kvmap, cache, desc->num_blocks)) return PKV_ERR_CUDA;

@@ -168,6 +168,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0u;
         fence_mbar_init();
     }
+    if (warp == kScoreWarp) {  // (no other kernel's CTA waits for ours: the columns come free)
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
     griddep_wait();  // the producers of q and of the cache before us on the stream
 
     // ---- the range: total tiles, then where tile `start` lies ----
@@ -191,8 +195,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     upto += before;
     const int64_t ranges = min(static_cast<int64_t>(p.ranges), total);  // no range is empty
-    const int64_t start = range < ranges ? range * total / ranges : 0;
-    const int64_t stop = range < ranges ? (range + 1) * total / ranges : 0;
+    auto cut = [&](int r) -> int64_t {  // r total / ranges (64-bit division only where 32 bits do not hold it)
+        if (r > ranges || ranges == 0) return 0;
+        if (total < (1 << 24)) return static_cast<uint32_t>(r) * static_cast<uint32_t>(total) / static_cast<uint32_t>(ranges);
+        return r * total / ranges;
+    };
+    const int64_t start = range < ranges ? cut(range) : 0, stop = range < ranges ? cut(range + 1) : 0;
     const int n = static_cast<int>(stop - start);
     if (n > 0 && upto - mine <= start && start < upto) {
         int64_t acc = upto - mine;
@@ -201,31 +209,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         plan[16] = b;
         plan[17] = start - acc;
     }
-    // Sequences without keys: zero rows, and the checks of every length, shared out over the ranges.
-    for (int b = range; b < p.num_seqs; b += p.ranges) {
-        const int ctx = __ldg(p.context_lens + b);
-        if (tid == 0 && ct == 0) {
-            uint32_t st = ctx < 1 || ctx > p.max_blocks * kBlockSize ? kStatusBadContextLen : 0u;
-            if (ctx >= 1 && ctx < p.q_per_seq) st |= kStatusBadQLen;
-            if (st) atomicOr(p.status, st);
+    // Sequences without keys get zero rows, and every length is checked, shared out over the ranges.
+    auto empty_sequences = [&](int thread, int threads) {
+        for (int b = range; b < p.num_seqs; b += p.ranges) {
+            const int ctx = __ldg(p.context_lens + b);
+            if (thread == 0 && ct == 0) {
+                uint32_t st = ctx < 1 || ctx > p.max_blocks * kBlockSize ? kStatusBadContextLen : 0u;
+                if (ctx >= 1 && ctx < p.q_per_seq) st |= kStatusBadQLen;
+                if (st) atomicOr(p.status, st);
+            }
+            if (keys_of(p, b) == 0) {
+                const size_t at = (static_cast<size_t>(b) * cols + c0) * kLatentDim * (p.out_bf16 ? 2 : 4);
+                uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + at);
+                for (int i = thread; i < nc * (p.out_bf16 ? 64 : 128); i += threads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            }
         }
-        if (keys_of(p, b) == 0) {
-            const size_t at = (static_cast<size_t>(b) * cols + c0) * kLatentDim * (p.out_bf16 ? 2 : 4);
-            uint4 *o = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + at);
-            for (int i = tid; i < nc * (p.out_bf16 ? 64 : 128); i += kThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-    }
-    if (warp == kScoreWarp && n > 0) {
-        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-        tmem_relinquish();
-    }
+    };
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     // The merge kernel's record of this range: its first sequence, and whether it starts inside it.
     if (tid == 0 && ct == 0) p.record[range] = n > 0 ? make_int2(static_cast<int>(plan[16]), plan[17] > 0) : make_int2(-1, 0);
-    if (n == 0) return;
     const uint32_t tmem = *tmem_slot;
+    if (n == 0) {
+        empty_sequences(tid, kThreads);
+        if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
+        return;
+    }
     const int b0 = static_cast<int>(plan[16]), t0 = static_cast<int>(plan[17]);
 
     // A warp's bounded wait; it gives up soon after another role did.  The timer and the flag are
@@ -245,6 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
     };
 
+    // The first Q is asked for before the second tile: behind both tiles of every CTA (22 MB) it came 4 us late.
+    auto second_tile = [&]() { asm volatile("bar.sync 2, %0;" ::"n"(kSoftThreads + 96) : "memory"); };
     if (warp == kProducerWarp) {
         // ---------------- TMA producer: lane j copies block j of a tile ----------------
         Walk w;
@@ -274,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     0, 0, cur);
                 }
             }
+            if (i == 0) second_tile();
             if (!ok) break;
         }
     } else if (warp >= kLoadWarp) {
@@ -289,7 +302,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         Walk w;
         w.at(p, b0, t0);
-        if (st == 1 && n > 1) w.next(p);
+        if (st == 1) {
+            if (n > 1) w.next(p);
+            second_tile();
+        }
         for (int i = st; i < n; i += kStages) {
             int id = -1;
             const int jb = w.t * kTileBlocks + lane;
@@ -395,20 +411,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto soft_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); };
         bool alive = true;
 
-        // Sequence b's Q: 72 vectors a column, zeros behind the last one, in the operand's swizzle.
+        // Sequence b's Q, a row a warp: 72 vectors a column, zeros behind the last one, in the
+        // operand's swizzle.
         auto load_q = [&](int b) {
-            for (int idx = tid; idx < NCOL * 72; idx += kSoftThreads) {
-                const int r = idx / 72, v = idx - r * 72;
-                const uint32_t dst = sbase + L::kQ + (v >> 3) * (NCOL * 128) + r * 128 + (((v & 7) ^ (r & 7)) << 4);
-                const int c = c0 + r;
-                const int64_t qr = static_cast<int64_t>(b) * p.q_per_seq + c / p.heads, h = c % p.heads;
-                const uint16_t *src = v < 64 ? static_cast<const uint16_t *>(p.q_latent) + qr * p.ql_row + h * p.ql_head + v * 8
-                                             : static_cast<const uint16_t *>(p.q_rope) + qr * p.qr_row + h * p.qr_head +
-                                                   (v - 64) * 8;
-                if (r < nc)
-                    cp_async_16(dst, src);
-                else
-                    sts128(dst, make_uint4(0u, 0u, 0u, 0u));
+#pragma unroll 1
+            for (int r = warp; r < NCOL; r += kSoftWarps) {
+                const int c = c0 + r, i = c / p.heads;
+                const int64_t qr = static_cast<int64_t>(b) * p.q_per_seq + i, h = c - i * p.heads;
+                const uint16_t *ql = static_cast<const uint16_t *>(p.q_latent) + qr * p.ql_row + h * p.ql_head;
+                const uint16_t *qp = static_cast<const uint16_t *>(p.q_rope) + qr * p.qr_row + h * p.qr_head;
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const int v = lane + 32 * k;
+                    const uint32_t dst = sbase + L::kQ + (v >> 3) * (NCOL * 128) + r * 128 + (((v & 7) ^ (r & 7)) << 4);
+                    if (v >= 72) continue;
+                    if (r < nc)
+                        cp_async_16(dst, v < 64 ? ql + v * 8 : qp + (v - 64) * 8);
+                    else
+                        sts128(dst, make_uint4(0u, 0u, 0u, 0u));
+                }
             }
         };
         auto publish_q = [&]() {
@@ -421,6 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Walk w;
         w.at(p, b0, t0);
         load_q(w.b);
+        asm volatile("bar.arrive 2, %0;" ::"n"(kSoftThreads + 96) : "memory");  // Q before the second tile
+        empty_sequences(tid, kSoftThreads);
         publish_q();
         float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         bool piece_mid = t0 > 0;  // the piece does not hold its sequence's first key
@@ -571,14 +594,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 soft_sync();
-                if (tid < NCOL) {
+                if (tid < NCOL) alpha_s[tid] = [&] {
                     const float sum = xch[tid] + xch[64 + tid];
-                    alpha_s[tid] = whole ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-                    if (!whole && tid < nc) p.part_l[slot + tid] = sum;
-                }
+                    return !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+                }();
                 if (!whole && has && half == 0) {
-                    if (row < nc) p.part_m[slot + row] = m_ref[0];
-                    if (row + 8 < nc) p.part_m[slot + row + 8] = m_ref[1];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int r = row + 8 * k;
+                        if (r < nc) p.part_ml[slot + r] = make_float2(m_ref[k], xch[r] + xch[64 + r]);
+                    }
                 }
                 soft_sync();
                 alive = alive && warp_wait(bar(kBarPvDone), i & 1);
@@ -640,107 +665,109 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Folds the parts of the y-th split sequence: CTA x takes column x of its rows.  A sequence
-// is split where a range starts inside it; its parts are the last piece of the range before
-// the first such range (slot 1) and the first pieces (slot 0) of the ranges from there on.
-constexpr int kMergeThreads = 512;  // 4 groups of 128 threads (4 dims each) take every 4th part
-__global__ void __launch_bounds__(kMergeThreads) latent_merge_kernel(const LatentDecodeParams p) {
-    __shared__ int s_first, s_parts, s_b;
-    __shared__ float s_w[kLatentMaxRanges];
-    __shared__ float s_sum[2][kMergeThreads / 32];
-    __shared__ float4 s_o[kMergeThreads];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Folds the parts of the y-th split sequence, one column (of the x-th eight) a warp, 512 / z
+// of its dims (z = 1 or 4).  A sequence is split where a range starts inside it; its parts are the last
+// piece of the range before the first such range (slot 1) and the first pieces (slot 0) of
+// the ranges from there on.  Two round trips to L2: the records, then everything else.
+constexpr int kMergeWarps = 8;
+constexpr int kRecords = kLatentMaxRanges / 32;
+template <int STEPS>  // of 32 lanes x 4 dims; batches of 16 / STEPS parts
+__global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const LatentDecodeParams p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = blockIdx.x * kMergeWarps + warp;
     griddep_launch_dependents();
     griddep_wait();
-    if (warp == 0) {
-        int seen = 0, first = 0;
-        for (int base = 0; base < p.ranges && !first; base += 32) {
-            const int r = base + lane;
-            bool is = false;
-            if (r >= 1 && r < p.ranges) {
-                const int2 a = p.record[r - 1], c = p.record[r];
-                is = c.x >= 0 && c.y && !(a.y && a.x == c.x);
-            }
-            uint32_t mask = __ballot_sync(0xffffffffu, is);
-            const int here = __popc(mask);
-            if (seen + here > static_cast<int>(blockIdx.y)) {
-                for (int k = blockIdx.y - seen; k > 0; --k) mask &= mask - 1;
-                first = base + __ffs(mask) - 1;
-            }
-            seen += here;
-        }
-        int parts = 0;
-        if (first) {
-            const int b = p.record[first].x;
-            parts = 1;
-            bool go = true;
-            for (int base = first; go && base < p.ranges; base += 32) {
-                const int r = base + lane;
-                const bool same = r < p.ranges && p.record[r].x == b && p.record[r].y;
-                const uint32_t mask = __ballot_sync(0xffffffffu, same);
-                parts += mask == 0xffffffffu ? 32 : __ffs(~mask) - 1;
-                go = mask == 0xffffffffu;
-            }
-            if (lane == 0) s_b = b;
-        }
-        if (lane == 0) {
-            s_first = first;
-            s_parts = parts;
-        }
+    if (col >= p.heads * p.q_per_seq) return;
+    int2 rec[kRecords];
+#pragma unroll
+    for (int k = 0; k < kRecords; ++k) {
+        const int r = 32 * k + lane;
+        rec[k] = r < p.ranges ? p.record[r] : make_int2(-1, 0);
     }
-    __syncthreads();
-    const int parts = s_parts, first = s_first;
-    if (parts == 0) return;
-    const int col = blockIdx.x, padded = p.col_tiles * p.cols_per_tile;
-    auto slot = [&](int k) {  // part k's index among the (range, slot, column) partials
-        return (static_cast<size_t>(first - 1 + k) * 2 + (k == 0 ? 1 : 0)) * padded + col;
+    int first = 0, seen = 0, b = -1, parts = 0;
+    int2 carry = make_int2(-1, 0);
+#pragma unroll
+    for (int k = 0; k < kRecords; ++k) {
+        int2 prev = make_int2(__shfl_up_sync(0xffffffffu, rec[k].x, 1), __shfl_up_sync(0xffffffffu, rec[k].y, 1));
+        if (lane == 0) prev = carry;
+        carry = make_int2(__shfl_sync(0xffffffffu, rec[k].x, 31), __shfl_sync(0xffffffffu, rec[k].y, 31));
+        uint32_t mask = __ballot_sync(0xffffffffu, rec[k].x >= 0 && rec[k].y && !(prev.y && prev.x == rec[k].x));
+        const int here = __popc(mask), want = static_cast<int>(blockIdx.y) - seen;
+        if (!first && want < here) {
+            for (int j = want; j > 0; --j) mask &= mask - 1;
+            const int at = __ffs(mask) - 1;
+            first = 32 * k + at;
+            b = __shfl_sync(0xffffffffu, rec[k].x, at);
+        }
+        seen += here;
+    }
+    if (!first) return;
+    // The ranges that start inside sequence b follow one another: count them.
+#pragma unroll
+    for (int k = 0; k < kRecords; ++k) parts += __popc(__ballot_sync(0xffffffffu, rec[k].x == b && rec[k].y));
+    ++parts;
+    const size_t padded = static_cast<size_t>(p.col_tiles) * p.cols_per_tile;
+    // Part k among the (range, slot, column) partials: slot 1 of the range before, then slot 0 of each.
+    const size_t part0 = (static_cast<size_t>(first - 1) * 2 + 1) * padded + col;
+    const size_t part1 = static_cast<size_t>(first) * 2 * padded + col;
+    auto slot = [&](int k) { return k == 0 ? part0 : part1 + static_cast<size_t>(k - 1) * 2 * padded; };
+    constexpr int kBatch = 16 / STEPS;
+    float4 v[kBatch][STEPS], o[STEPS];
+    const int lane4 = blockIdx.z * STEPS * 32 + lane;
+    auto load = [&](int j) {
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+            const float4 *src = reinterpret_cast<const float4 *>(p.part_o + slot(j + e) * kLatentDim) + lane4;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) v[e][s] = j + e < parts ? src[32 * s] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     };
-    float m = -INFINITY;
-    for (int k = tid; k < parts; k += kMergeThreads) m = fmaxf(m, p.part_m[slot(k)]);
+    float2 ml[kRecords];
+    float w[kRecords], m = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kRecords; ++k)
+        ml[k] = 32 * k + lane < parts ? p.part_ml[slot(32 * k + lane)] : make_float2(-INFINITY, 0.f);
+    load(0);
+#pragma unroll
+    for (int k = 0; k < kRecords; ++k) m = fmaxf(m, ml[k].x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    if (lane == 0) s_sum[0][warp] = m;
-    __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kMergeThreads / 32; ++k) m = fmaxf(m, s_sum[0][k]);
-    float sum = 0.f;
-    for (int k = tid; k < parts; k += kMergeThreads) {
-        const float pm = p.part_m[slot(k)];
-        const float wk = pm == -INFINITY ? 0.f : exp2f(pm - m);
-        s_w[k] = wk;
-        sum += wk * p.part_l[slot(k)];
+    for (int k = 0; k < kRecords; ++k) {
+        w[k] = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - m);
+        sum += w[k] * ml[k].y;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) s_sum[1][warp] = sum;
-    __syncthreads();
-    sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < kMergeThreads / 32; ++k) sum += s_sum[1][k];
-    const int group = tid >> 7, d4 = tid & 127;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = group; k < parts; k += 4) {
-        const float wk = s_w[k];
-        if (wk == 0.f) continue;  // nothing was visible: its O was never written from finite weights
-        const float4 v = reinterpret_cast<const float4 *>(p.part_o + slot(k) * kLatentDim)[d4];
-        o.x += wk * v.x, o.y += wk * v.y, o.z += wk * v.z, o.w += wk * v.w;
-    }
-    s_o[tid] = o;
-    __syncthreads();
-    if (group != 0) return;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    for (int k = 1; k < 4; ++k) {
-        const float4 v = s_o[k * 128 + d4];
-        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) o[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0;;) {
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+            float wk = 0.f;  // weight of part j + e, kept by lane (j + e) % 32
+#pragma unroll
+            for (int k = 0; k < kRecords; ++k)
+                if ((j + e) >> 5 == k) wk = w[k];
+            wk = __shfl_sync(0xffffffffu, wk, (j + e) & 31);
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+                o[s].x += wk * v[e][s].x, o[s].y += wk * v[e][s].y, o[s].z += wk * v[e][s].z, o[s].w += wk * v[e][s].w;
+        }
+        j += kBatch;
+        if (j >= parts) break;
+        load(j);
     }
-    const size_t at = (static_cast<size_t>(s_b) * p.heads * p.q_per_seq + col) * kLatentDim + 4 * d4;
-    if (p.out_bf16)
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    else
-        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
-            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const size_t at = (static_cast<size_t>(b) * p.heads * p.q_per_seq + col) * kLatentDim + 4 * (lane4 + 32 * s);
+        if (p.out_bf16)
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
+                make_uint2(pack_bf16x2(o[s].x * inv, o[s].y * inv), pack_bf16x2(o[s].z * inv, o[s].w * inv));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
+                make_float4(o[s].x * inv, o[s].y * inv, o[s].z * inv, o[s].w * inv);
+    }
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -866,8 +893,11 @@ cudaError_t launch_latent_decode(const CUtensorMap &kvmap, const LatentDecodePar
                     : p.cols_per_tile <= 32 ? launch_one<32>(kvmap, p, stream)
                                             : launch_one<64>(kvmap, p, stream);
     if (e != cudaSuccess || p.ranges <= 1) return e;
-    const dim3 grid(p.heads * p.q_per_seq, std::min(p.num_seqs, p.ranges - 1));
-    return launch_pdl(latent_merge_kernel, grid, dim3(kMergeThreads), 0, stream, p);
+    // Few sequences over many ranges have many parts each: then four warps share a column's dims.
+    const int split = std::min(p.num_seqs, p.ranges - 1), x = (p.heads * p.q_per_seq + kMergeWarps - 1) / kMergeWarps;
+    if (p.ranges > 4 * split)
+        return launch_pdl(latent_merge_kernel<1>, dim3(x, split, 4), dim3(kMergeWarps * 32), 0, stream, p);
+    return launch_pdl(latent_merge_kernel<4>, dim3(x, split, 1), dim3(kMergeWarps * 32), 0, stream, p);
 }
 
 }  // namespace pkv
