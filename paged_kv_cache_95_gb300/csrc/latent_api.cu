@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -26,11 +27,19 @@ constexpr int32_t kMaxHeads = 1024;
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// The current device's SM count; 0 without a device.
+// The current device (-1: none) and its SM count (0: none), looked up once per device.
+std::atomic<int> g_sms[kMaxDevices];
+int current_device() {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices ? dev : -1;
+}
 int current_sms() {
-    int dev = 0, v = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const int dev = current_device();
+    if (dev < 0) return 0;
+    int v = g_sms[dev].load(std::memory_order_relaxed);
+    if (v > 0) return v;
     if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    g_sms[dev].store(v, std::memory_order_relaxed);
     return v;
 }
 
@@ -40,8 +49,8 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 std::once_flag g_decode_once[kMaxDevices];
 cudaError_t g_decode_err[kMaxDevices];
 bool prepare_decode() {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+    const int dev = current_device();
+    if (dev < 0) return false;
     std::call_once(g_decode_once[dev], [&] { g_decode_err[dev] = pkv::latent_decode_prepare_device(); });
     return g_decode_err[dev] == cudaSuccess;
 }

@@ -690,22 +690,36 @@ def paged_attention_decode_static_scratch(out, q, k_cache, v_cache, block_tables
 def _check_rows(t, name, ndim, last, device):
     """A bf16 input whose rows (innermost dimension) are contiguous; the outer strides are free."""
     torch = _torch()
-    _need(isinstance(t, torch.Tensor), f"{name} must be a torch.Tensor")
-    _need(t.dtype == torch.bfloat16, f"{name} must be torch.bfloat16, got {t.dtype}")
-    _need(t.dim() == ndim and t.shape[-1] == last, f"{name} must have {ndim} dims, the last {last}: {tuple(t.shape)}")
-    _need(t.get_device() == device, f"{name} must be on the current CUDA device")
-    _need(t.stride(-1) == 1, f"{name}'s innermost dimension must be contiguous")
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == ndim and t.shape[-1] == last
+            and t.get_device() == device and t.stride(-1) == 1):
+        _need(isinstance(t, torch.Tensor), f"{name} must be a torch.Tensor")
+        _need(t.dtype == torch.bfloat16, f"{name} must be torch.bfloat16, got {t.dtype}")
+        _need(t.dim() == ndim and t.shape[-1] == last, f"{name} must have {ndim} dims, the last {last}: {tuple(t.shape)}")
+        _need(t.get_device() == device, f"{name} must be on the current CUDA device")
+        _need(False, f"{name}'s innermost dimension must be contiguous")
 
 
 def _check_on(t, name, dtype, ndim, device):
     """A contiguous tensor on the current device."""
-    _check(t, name, dtype, ndim=ndim)
-    _need(t.get_device() == device, f"{name} must be on the current CUDA device")
+    if not (isinstance(t, _torch().Tensor) and t.dtype is dtype and t.dim() == ndim and t.get_device() == device
+            and t.is_contiguous()):
+        _check(t, name, dtype, ndim=ndim)
+        _need(False, f"{name} must be on the current CUDA device")
 
 
 def _outer_stride(t, dim: int) -> int:
     """The stride of an outer dimension; the packed one where its size is 1 (it is never stepped)."""
-    return int(t.stride(dim)) if t.shape[dim] > 1 else (int(t.shape[-1]) + 7) // 8 * 8
+    return t.stride(dim) if t.shape[dim] > 1 else (t.shape[-1] + 7) // 8 * 8
+
+
+def _device_and_stream(stream):
+    """The current device, and `stream` (None: the current one) as the ABI takes it."""
+    c = _torch()._C
+    if not hasattr(c, "_cuda_getDevice"):
+        raise ValueError("the latent entry points need a CUDA device")
+    _torch().cuda.init()
+    device = c._cuda_getDevice()
+    return device, c._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def latent_cache_desc(cache) -> LatentDesc:
@@ -714,24 +728,26 @@ def latent_cache_desc(cache) -> LatentDesc:
     torch = _torch()
     fp8 = cache.dtype in (torch.uint8, torch.float8_e4m3fn)
     _check(cache, "cache", cache.dtype if fp8 else torch.bfloat16, ndim=3)
-    width = LATENT_DIM if fp8 else LATENT_DIM + ROPE_DIM
-    _need(cache.shape[2] == width, f"cache rows must have {width} values, got {cache.shape[2]}")
-    return LatentDesc(int(cache.shape[0]), int(cache.shape[1]), LATENT_DIM, ROPE_DIM,
-                      PKV_DTYPE_FP8_E4M3 if fp8 else PKV_DTYPE_BF16)
+    blocks, slots, width = cache.shape
+    want = LATENT_DIM if fp8 else LATENT_DIM + ROPE_DIM
+    _need(width == want, f"cache rows must have {want} values, got {width}")
+    return LatentDesc(blocks, slots, LATENT_DIM, ROPE_DIM, PKV_DTYPE_FP8_E4M3 if fp8 else PKV_DTYPE_BF16)
 
 
 def _latent_pool(cache, rope_cache, cache_scale, device):
     torch = _torch()
     desc = latent_cache_desc(cache)
-    _need(cache.get_device() == device, "cache must be on the current CUDA device")
     fp8 = desc.dtype == PKV_DTYPE_FP8_E4M3
-    _need(fp8 == (rope_cache is not None) and fp8 == (cache_scale is not None),
-          "rope_cache and cache_scale are required for an FP8 pool and not allowed otherwise")
+    if cache.get_device() != device:
+        _need(False, "cache must be on the current CUDA device")
+    if fp8 != (rope_cache is not None) or fp8 != (cache_scale is not None):
+        _need(False, "rope_cache and cache_scale are required for an FP8 pool and not allowed otherwise")
     if fp8:
         _check_on(rope_cache, "rope_cache", torch.bfloat16, 3, device)
         _check_on(cache_scale, "cache_scale", torch.float32, 2, device)
-        _need(tuple(rope_cache.shape) == (*cache.shape[:2], ROPE_DIM), "rope_cache must be [num_blocks, 16, 64]")
-        _need(tuple(cache_scale.shape) == tuple(cache.shape[:2]), "cache_scale must be [num_blocks, 16]")
+        shape = cache.shape[:2]
+        _need(rope_cache.shape[:2] == shape and rope_cache.shape[2] == ROPE_DIM, "rope_cache must be [num_blocks, 16, 64]")
+        _need(cache_scale.shape == shape, "cache_scale must be [num_blocks, 16]")
     return desc, fp8
 
 
@@ -748,25 +764,25 @@ def _check_latent_rows(latent, rope, slot_mapping, device):
 def latent_reshape_and_cache(latent, rope, cache, slot_mapping, stream=None) -> None:
     """Append rows [latent (512) | rope (64)] to the bf16 latent pool [num_blocks, 16, 576]
     through ``slot_mapping``; ``latent`` and ``rope`` may be slices of wider rows."""
-    device = _torch().cuda.current_device()
+    device, stream = _device_and_stream(stream)
     desc, fp8 = _latent_pool(cache, None, None, device)
     T = _check_latent_rows(latent, rope, slot_mapping, device)
     rc = load_library().latent_reshape_and_cache(_ptr(latent), _outer_stride(latent, 0), _ptr(rope),
                                                  _outer_stride(rope, 0), _ptr(cache), _ptr(slot_mapping), T,
-                                                 ctypes.byref(desc), _stream(stream))
+                                                 ctypes.byref(desc), stream)
     _raise("latent_reshape_and_cache", rc)
 
 
 def latent_reshape_and_cache_fp8(latent, rope, cache, rope_cache, cache_scale, slot_mapping, stream=None) -> None:
     """The same into an FP8 pool: E4M3 codes of the latent with one fp32 scale a token
     (``cache_scale`` [num_blocks, 16]); the rotated key goes to ``rope_cache`` as it is."""
-    device = _torch().cuda.current_device()
+    device, stream = _device_and_stream(stream)
     desc, fp8 = _latent_pool(cache, rope_cache, cache_scale, device)
     T = _check_latent_rows(latent, rope, slot_mapping, device)
     rc = load_library().latent_reshape_and_cache_fp8(_ptr(latent), _outer_stride(latent, 0), _ptr(rope),
                                                      _outer_stride(rope, 0), _ptr(cache), _ptr(rope_cache),
                                                      _ptr(cache_scale), _ptr(slot_mapping), T, ctypes.byref(desc),
-                                                     _stream(stream))
+                                                     stream)
     _raise("latent_reshape_and_cache_fp8", rc)
 
 
@@ -776,7 +792,7 @@ def latent_gather(out, cache, block_tables, cu_lens, rope_cache=None, cache_scal
     is position i of sequence b; an FP8 pool is dequantised and rounded once.  ``status`` is
     an optional int32 CUDA tensor of one element into which status bits are ORed."""
     torch = _torch()
-    device = torch.cuda.current_device()
+    device, stream = _device_and_stream(stream)
     desc, fp8 = _latent_pool(cache, rope_cache, cache_scale, device)
     _check_on(out, "out", torch.bfloat16, 2, device)
     _need(out.shape[1] == LATENT_DIM + ROPE_DIM, "out must be [total_rows, 576]")
@@ -789,7 +805,7 @@ def latent_gather(out, cache, block_tables, cu_lens, rope_cache=None, cache_scal
     rc = load_library().latent_gather(_ptr(out), _ptr(cache), _ptr(rope_cache) if fp8 else None,
                                       _ptr(cache_scale) if fp8 else None, _ptr(block_tables), _ptr(cu_lens), B,
                                       int(block_tables.shape[1]), int(out.shape[0]), ctypes.byref(desc),
-                                      _ptr(status) if status is not None else None, _stream(stream))
+                                      _ptr(status) if status is not None else None, stream)
     _raise("latent_gather", rc)
 
 
@@ -807,7 +823,7 @@ def latent_attention_decode(out, q_latent, q_rope, cache, block_tables, context_
     sees the keys up to it.  An FP8 pool comes with ``rope_cache`` and ``cache_scale``
     (latent_attention_decode_fp8).  Returns the workspace (allocated if None)."""
     torch = _torch()
-    device = torch.cuda.current_device()
+    device, stream = _device_and_stream(stream)
     desc, fp8 = _latent_pool(cache, rope_cache, cache_scale, device)
     _check_rows(q_latent, "q_latent", 3, LATENT_DIM, device)
     _check_rows(q_rope, "q_rope", 3, ROPE_DIM, device)
@@ -829,7 +845,7 @@ def latent_attention_decode(out, q_latent, q_rope, cache, block_tables, context_
     ql = (_ptr(q_latent), _outer_stride(q_latent, 0), _outer_stride(q_latent, 1))
     qr = (_ptr(q_rope), _outer_stride(q_rope, 0), _outer_stride(q_rope, 1))
     tail = (_ptr(block_tables), _ptr(context_lens), B, k, int(heads), max_blocks, float(scale), ctypes.byref(desc),
-            _ptr(workspace), int(workspace.numel()), _stream(stream))
+            _ptr(workspace), int(workspace.numel()), stream)
     if fp8:
         rc = lib.latent_attention_decode_fp8(_ptr(out), _out_dtype(out), *ql, *qr, _ptr(cache), _ptr(rope_cache),
                                              _ptr(cache_scale), *tail)
@@ -853,7 +869,7 @@ def latent_attention_prefill_chunk(out, q, k_nope, v, k_rope, cu_q_lens, cu_k_le
     equal strides), ``k_rope`` [total_k, 64] shared by the heads, ``out`` [total_q, heads, 128]
     in float32 or bfloat16.  Returns the workspace (allocated if None)."""
     torch = _torch()
-    device = torch.cuda.current_device()
+    device, stream = _device_and_stream(stream)
     _check_rows(q, "q", 3, 192, device)
     _check_rows(k_nope, "k_nope", 3, 128, device)
     _check_rows(v, "v", 3, 128, device)
@@ -880,6 +896,6 @@ def latent_attention_prefill_chunk(out, q, k_nope, v, k_rope, cu_q_lens, cu_k_le
                                             _outer_stride(q, 1), _ptr(k_nope), _ptr(v), *k_strides, _ptr(k_rope),
                                             _outer_stride(k_rope, 0), _ptr(cu_q_lens), _ptr(cu_k_lens), B, int(heads),
                                             int(max_q_len), int(tq), tk, float(scale), _ptr(workspace),
-                                            int(workspace.numel()), _stream(stream))
+                                            int(workspace.numel()), stream)
     _raise("latent_attention_prefill_chunk", rc)
     return workspace
