@@ -74,6 +74,10 @@ struct LatentPrefillParams {
     float scale_log2;
     int32_t out_bf16;
 };
-cudaError_t launch_latent_prefill(const LatentPrefillParams &p, cudaStream_t stream);
+struct LatentPrefillMaps {
+    CUtensorMap q, k, rope, out;
+};
+cudaError_t latent_prefill_prepare_device();
+cudaError_t launch_latent_prefill(const LatentPrefillMaps &maps, const LatentPrefillParams &p, cudaStream_t stream);
 
 }  // namespace pkv

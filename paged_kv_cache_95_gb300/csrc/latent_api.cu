@@ -46,13 +46,45 @@ int current_sms() {
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Kernel attributes, set once per device; false on failure.
-std::once_flag g_decode_once[kMaxDevices];
-cudaError_t g_decode_err[kMaxDevices];
-bool prepare_decode() {
+std::once_flag g_prepared[kMaxDevices];
+cudaError_t g_prepare_err[kMaxDevices];
+bool prepare_device() {
     const int dev = current_device();
     if (dev < 0) return false;
-    std::call_once(g_decode_once[dev], [&] { g_decode_err[dev] = pkv::latent_decode_prepare_device(); });
-    return g_decode_err[dev] == cudaSuccess;
+    std::call_once(g_prepared[dev], [&] {
+        g_prepare_err[dev] = pkv::latent_decode_prepare_device();
+        if (g_prepare_err[dev] == cudaSuccess) g_prepare_err[dev] = pkv::latent_prefill_prepare_device();
+    });
+    return g_prepare_err[dev] == cudaSuccess;
+}
+
+// Rows [rows][heads][width] bf16 at free (row, head) strides (in elements); a box is 64
+// values of one head of box_rows rows, 128-byte swizzle: [row][128 B].
+bool encode_rows(CUtensorMap *map, const void *base, int32_t rows, int32_t heads, int32_t width, int64_t row_stride,
+                 int64_t head_stride, uint32_t box_rows) {
+    const pkv::EncodeTiledFn fn = pkv::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(row_stride) * 2};
+    const cuuint32_t box[3] = {64, 1, box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same for rows without heads: [rows][64].
+bool encode_rows_2d(CUtensorMap *map, const void *base, int32_t rows, int64_t row_stride, uint32_t box_rows) {
+    const pkv::EncodeTiledFn fn = pkv::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {64, static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_stride) * 2};
+    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A bf16 pool [num_blocks][16][576] viewed so that one box is a whole block in the order
@@ -184,7 +216,7 @@ int decode_impl(void *out, int32_t out_dtype, const void *q_latent, int64_t ql_r
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.out_bf16 = out_dtype == PKV_DTYPE_BF16;
     const int sms = current_sms();
-    if (sms < 1 || !prepare_decode()) return PKV_ERR_CUDA;
+    if (sms < 1 || !prepare_device()) return PKV_ERR_CUDA;
     const DecodePlan pl = plan_decode(num_seqs, q_per_seq, heads, max_blocks, sms);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.col_tiles = pl.col_tiles;
@@ -336,7 +368,18 @@ int latent_attention_prefill_chunk(void *out, int32_t out_dtype, const void *q, 
     p.total_k = total_k_rows;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.out_bf16 = out_dtype == PKV_DTYPE_BF16;
-    return pkv::launch_latent_prefill(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    if (p.scale_log2 == 0.f) p.scale_log2 = 1e-37f;  // the kernel hides a key by an infinite score: never 0 x infinity
+    if (!prepare_device()) return PKV_ERR_CUDA;
+    pkv::LatentPrefillMaps maps;
+    // A float32 output never leaves by TMA; its map is encoded as the bf16 view of the same memory.
+    if (!encode_rows(&maps.q, q, total_q_rows, num_heads, pkv::kExpandedQk, q_row_stride, q_head_stride, 128) ||
+        !encode_rows(&maps.k, k_nope, total_k_rows, num_heads, pkv::kNopeDim, k_row_stride, k_head_stride, 128) ||
+        !encode_rows_2d(&maps.rope, k_rope, total_k_rows, k_rope_stride, 128) ||
+        !encode_rows(&maps.out, out, total_q_rows, num_heads, pkv::kExpandedV,
+                     static_cast<int64_t>(num_heads) * pkv::kExpandedV, pkv::kExpandedV, 32))
+        return PKV_ERR_CUDA;
+    return pkv::launch_latent_prefill(maps, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK
+                                                                                                : PKV_ERR_CUDA;
 }
 
 }  // extern "C"

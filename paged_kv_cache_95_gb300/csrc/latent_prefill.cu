@@ -1,10 +1,37 @@
-// latent_prefill.cu -- expanded latent attention of a causal prefill chunk.
+// latent_prefill.cu -- expanded latent attention of a causal prefill chunk on the
+// 5th-generation tensor cores (tcgen05.mma, accumulators in tensor memory).
 //
 //     s_j = scale (<q_nope, k_nope_j> + <q_rope, r_j>), j <= k_len - q_len + i,
 //     out_i = sum_j softmax(s)_j v_j
 //
-// One warp per (row, head): 4 + 2 query values and 4 output values a lane, the keys
-// walked one by one with a running maximum and sum in fp32 (log2 domain).
+// One CTA takes two adjacent tiles of 128 query rows of one head and walks the keys in
+// tiles of 128 once for both; per key tile and row tile S = Q K^T (M = N = 128, 192 values:
+// two chunks of k_nope, one of the rotated key that all heads share) and O += P V (P from
+// tensor memory).  Tensor memory: S / P of row tile t in columns [128 t, +128), O in
+// [256 + 128 t, +128).
+//
+// What bounds it: a key tile costs two row tiles 2 x (768 + 512) cycles of the tensor pipe;
+// its operands read 2 x 128 KB of shared memory and its 80 KB of keys and values are
+// written there, 2690 cycles at 128 B a clock -- both limits are near.  One SM's TMA unit
+// delivers 24 B a clock (measured), too little for 80 KB in 2560 cycles, so K comes by TMA and
+// V by cp.async, which also fills rows past the sequence's end with zeros (a weight of 0
+// times a stranger's NaN would be NaN).
+//
+// Warps:
+//  * 0-3 softmax of row tile 0, 4-7 of row tile 1, a row a thread: 32 scores at a time, one
+//    pass, weights P = 2^(s - m) against a running reference m straight back over the
+//    consumed scores as bf16 (relative 2^-8).  m is an integer, raised when a score passes it
+//    by 2^8 (looked at before the 32 weights are written; what was written is rescaled by an
+//    exact power of two, and so are l and O); the sum l stays in fp32.
+//  * 8 TMA: Q, K.  11-14 cp.async: V.  Chunks of [128 rows][128 bytes] in a ring of 8
+//    (per key tile K K K V V): a tile's chunks are refilled as the MMAs that read them end.
+//  * 9, 10 issue the MMAs of row tile 0 and 1: S(k + 1) follows P V (k) (it overwrites the
+//    P that P V reads; the MMAs of one thread run in order), and while one tile's softmax
+//    runs the tensor pipe has the other's.
+//
+// Every mbarrier wait is bounded; a role whose wait runs out raises a CTA-wide abort
+// flag, the others stop at their next wait, and the CTA records PKV_STATUS_TIMEOUT and
+// frees its tensor memory before it returns.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -17,63 +44,402 @@ namespace pkv {
 
 namespace {
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+constexpr int kRows = 128;                    // query rows a tile
+constexpr int kKeys = 128;                    // keys a tile
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kLoadWarp = 11;
+constexpr int kLoadThreads = 128;
+constexpr int kThreads = 15 * 32;
+constexpr uint32_t kChunk = 128 * 128;        // 16 KB: 128 rows x 64 values
+constexpr int kSlots = 8;                     // ring of chunks
+constexpr int kPerTile = 5;                   // chunks a key tile: k_nope 0, 1, k_rope, v 0, 1
+constexpr uint32_t kOffQ = 0;                 // [row tile][3 chunks]
+constexpr uint32_t kOffRing = 6 * kChunk;
+constexpr uint32_t kOffBar = kOffRing + kSlots * kChunk;
+enum { kBarQ = 0, kBarFull, kBarEmpty = kBarFull + kSlots, kBarS = kBarEmpty + kSlots, kBarP = kBarS + 2, kBarO = kBarP + 2,
+       kNumBars = kBarO + 2 };
+constexpr uint32_t kOffTmem = kOffBar + 8 * kNumBars;
+constexpr uint32_t kOffAbort = kOffTmem + 4;
+constexpr uint32_t kSmemBytes = kOffAbort + 4;
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+constexpr uint32_t kTmemCols = 512, kTmemO = 256;
+constexpr float kRaise = 8.f;
 
-__global__ void __launch_bounds__(128) latent_prefill_kernel(const LatentPrefillParams p) {
+// kind::f16, D f32, A and B bf16, M = 128.
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
+constexpr uint32_t kIdescQK = kIdesc | ((128u >> 3) << 17);
+constexpr uint32_t kIdescPV = kIdesc | ((64u >> 3) << 17) | (1u << 16);  // B (V) MN-major, 64 dims
+
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// 16 bytes global -> shared; zeros where !valid (the source is not read then).
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                          const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap omap,
+                          const LatentPrefillParams p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // Pairs of row tiles in reverse: later rows see more keys, so the longest CTAs start first.
+    const int h = blockIdx.x, b = blockIdx.y, pair = static_cast<int>(gridDim.z) - 1 - static_cast<int>(blockIdx.z);
+
+    if (tid == 0) {
+        prefetch_tensormap(&qmap);
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&rmap);
+        prefetch_tensormap(&omap);
+    }
     griddep_launch_dependents();
-    griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int i = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y, b = blockIdx.z;
+    griddep_wait();  // the producers of q, keys and values before us on the stream
+    if (sbase & 1023u) {  // operands need the 1 KB swizzle alignment
+        if (tid == 0) atomicOr(p.status, kStatusTimeout);
+        return;
+    }
     const int q0 = __ldg(p.cu_q_lens + b), q_len = __ldg(p.cu_q_lens + b + 1) - q0;
     const int k0 = __ldg(p.cu_k_lens + b), k_len = __ldg(p.cu_k_lens + b + 1) - k0;
-    bool ok = q_len >= 0 && q_len <= k_len && q_len <= p.max_q_len && q0 >= 0 && k0 >= 0 &&
-              static_cast<int64_t>(q0) + q_len <= p.total_q && static_cast<int64_t>(k0) + k_len <= p.total_k;
-    if (!ok && i == 0 && h == 0 && lane == 0 && p.status) atomicOr(p.status, kStatusBadQLen);
-    if (i >= q_len || q0 < 0 || static_cast<int64_t>(q0) + i >= p.total_q) return;
-    const size_t row = static_cast<size_t>(q0) + i;
-    float q[6], o[4] = {}, m = -INFINITY, l = 0.f;
-    const uint16_t *qp = static_cast<const uint16_t *>(p.q) + row * p.q_row + h * p.q_head;
-    const uint2 qn = __ldg(reinterpret_cast<const uint2 *>(qp) + lane);
-    const uint32_t qr = __ldg(reinterpret_cast<const uint32_t *>(qp + kNopeDim) + lane);
-    q[0] = bf16_lo(qn.x), q[1] = bf16_hi(qn.x), q[2] = bf16_lo(qn.y), q[3] = bf16_hi(qn.y);
-    q[4] = bf16_lo(qr), q[5] = bf16_hi(qr);
-    const int keys = ok ? k_len - q_len + 1 + i : 0;
-    for (int j = 0; j < keys; ++j) {
-        const size_t kr = static_cast<size_t>(k0) + j;
-        const uint2 kn = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.k_nope) + kr * p.k_row +
-                                                               h * p.k_head) + lane);
-        const uint32_t r = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.k_rope) + kr * p.r_row) +
-                                 lane);
-        const uint2 vv = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.v) + kr * p.k_row +
-                                                               h * p.k_head) + lane);
-        float s = q[0] * bf16_lo(kn.x) + q[1] * bf16_hi(kn.x) + q[2] * bf16_lo(kn.y) + q[3] * bf16_hi(kn.y) +
-                  q[4] * bf16_lo(r) + q[5] * bf16_hi(r);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s);
-        const float alpha = exp2f(m - mn), e = exp2f(s - mn);
-        l = l * alpha + e;
-        o[0] = o[0] * alpha + e * bf16_lo(vv.x), o[1] = o[1] * alpha + e * bf16_hi(vv.x);
-        o[2] = o[2] * alpha + e * bf16_lo(vv.y), o[3] = o[3] * alpha + e * bf16_hi(vv.y);
-        m = mn;
+    const int r_lo = 2 * pair * kRows;  // this CTA's first row of the chunk
+    if (q_len < 0 || q_len > k_len || q_len > p.max_q_len || q0 < 0 || k0 < 0 ||
+        static_cast<int64_t>(q0) + q_len > p.total_q || static_cast<int64_t>(k0) + k_len > p.total_k) {
+        if (pair == 0 && h == 0 && tid == 0) atomicOr(p.status, kStatusBadQLen);
+        // The rows that can be addressed read as zeros; the last pair of the grid takes those past max_q_len too.
+        if (q0 >= 0) {
+            const int64_t end = min(static_cast<int64_t>(q_len), static_cast<int64_t>(p.total_q) - q0);
+            const int64_t hi = pair == static_cast<int>(gridDim.z) - 1 ? end : min(end, static_cast<int64_t>(r_lo) + 2 * kRows);
+            const int chunks = p.out_bf16 ? 16 : 32;  // 16-byte pieces of a row
+            for (int64_t idx = tid; idx < (hi - r_lo) * chunks; idx += kThreads) {
+                const size_t row = static_cast<size_t>(q0) + r_lo + idx / chunks;
+                reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) +
+                                          (row * p.heads + h) * kExpandedV * (p.out_bf16 ? 2 : 4))[idx % chunks] =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+        return;
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const size_t at = (row * p.heads + h) * kExpandedV + 4 * lane;
-    if (p.out_bf16)
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at) =
-            make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
-    else
-        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
-            make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+    const int c = k_len - q_len;
+    // Row tile t: rows i0 .. i0 + rows - 1 of the chunk, keys 0 .. c + i0 + rows - 1, nt key tiles.
+    auto tile_rows = [&](int t) { return max(0, min(kRows, q_len - r_lo - t * kRows)); };
+    auto tile_nt = [&](int t) {
+        const int rows = tile_rows(t);
+        return rows > 0 ? (c + r_lo + t * kRows + rows + kKeys - 1) / kKeys : 0;
+    };
+    const int n_tiles = max(tile_nt(0), tile_nt(1));
+    if (n_tiles == 0) return;
+
+    auto bar = [&](int i) { return sbase + kOffBar + 8 * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffTmem);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + kOffAbort);
+    if (tid == 0) {
+        for (int i = 0; i < kNumBars; ++i)
+            mbar_init(bar(i), i >= kBarFull && i < kBarEmpty ? kLoadThreads / 32
+                              : i >= kBarEmpty && i < kBarS  ? 2
+                              : i >= kBarP && i < kBarO      ? 4
+                                                             : 1);
+        *abort_flag = 0u;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // A warp's bounded wait; it gives up soon after another role did (timer and flag every 64 tries).
+    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
+        uint64_t t_first = 0;
+        for (uint32_t tries = 0; !__all_sync(0xffffffffu, mbar_try_wait(b, parity)); ++tries) {
+            if ((tries & 63u) != 63u) continue;
+            const uint64_t now = globaltimer_ns();
+            if (t_first == 0) t_first = now;
+            if (__any_sync(0xffffffffu, *abort_flag != 0 || now - t_first > kWaitLimitNs)) {
+                *abort_flag = 1u;
+                return false;
+            }
+        }
+        return true;
+    };
+    // Chunk j (5 per key tile) lies in slot j % 8, its use j / 8.
+    auto full = [&](int j) { return bar(kBarFull + j % kSlots); };
+    auto empty = [&](int j) { return bar(kBarEmpty + j % kSlots); };
+    auto slot_at = [&](int j) { return sbase + kOffRing + (j % kSlots) * kChunk; };
+    auto slot_free = [&](int j) { return j < kSlots || warp_wait(empty(j), ((j / kSlots) - 1) & 1); };
+
+    if (warp == kTmaWarp) {
+        if (elect_one()) {
+            mbar_arrive_expect_tx(bar(kBarQ), 6 * kChunk);
+            for (int t = 0; t < 2; ++t)
+                for (int i = 0; i < 3; ++i)
+                    tma_load_3d(sbase + kOffQ + (3 * t + i) * kChunk, &qmap, bar(kBarQ), 64 * i, h, q0 + r_lo + t * kRows);
+        }
+        __syncwarp();
+        bool ok = true;
+        for (int kt = 0; ok && kt < n_tiles; ++kt) {
+            for (int i = 0; i < 3; ++i) {
+                const int j = kPerTile * kt + i;
+                if (!(ok = slot_free(j))) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(full(j), kChunk);
+                    for (int k = 1; k < kLoadThreads / 32; ++k) mbar_arrive(full(j));  // (V has an arrival a warp)
+                    if (i < 2)
+                        tma_load_3d(slot_at(j), &kmap, full(j), 64 * i, h, k0 + kt * kKeys);
+                    else
+                        tma_load_2d(slot_at(j), &rmap, full(j), 0, k0 + kt * kKeys);
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp >= kLoadWarp) {
+        // V chunk i of a key tile: dims 64 i .. of keys; 8 threads a row, 16 rows at a time.
+        const int t = tid - kLoadWarp * 32, row = t >> 3, v = t & 7;
+        const uint32_t to = row * 128 + ((v ^ (row & 7)) << 4);
+        bool ok = true;
+        for (int kt = 0; ok && kt < n_tiles; ++kt) {
+            const int left = k_len - kt * kKeys;
+            const uint16_t *src = static_cast<const uint16_t *>(p.v) + (static_cast<int64_t>(k0) + kt * kKeys + row) * p.k_row +
+                                  h * p.k_head + v * 8;
+            for (int i = 0; i < 2; ++i) {
+                const int j = kPerTile * kt + 3 + i;
+                if (!(ok = slot_free(j))) break;
+                const uint32_t dst = slot_at(j) + to;
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    cp_async_16_or_zero(dst + r * 16 * 128, src + 64 * i + r * 16 * p.k_row, row + 16 * r < left);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            }
+            if (!ok) break;
+            // Landed, made visible to the tensor core, then an arrival a warp.
+            for (int i = 0; i < 2; ++i) {
+                if (i == 0)
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                else
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full(kPerTile * kt + 3 + i));
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        const int t = warp - kMmaWarp, nt = tile_nt(t);
+        const uint32_t s_at = tmem + 128 * t, o_at = tmem + kTmemO + 128 * t;
+        const uint64_t q_desc = sw128_desc(sbase + kOffQ + 3 * t * kChunk, 16, 1024);
+        const uint64_t k_desc = sw128_desc(sbase + kOffRing, 16, 1024), v_desc = sw128_desc(sbase + kOffRing, 16, 1024);
+        bool ok = warp_wait(bar(kBarQ), 0);
+        for (int kt = 0; ok && kt < n_tiles; ++kt) {
+            for (int i = 0; i < 3; ++i) {
+                const int j = kPerTile * kt + i;
+                if (!(ok = warp_wait(full(j), (j / kSlots) & 1))) break;
+                tc_fence_after();
+                const uint64_t qd = q_desc + static_cast<uint32_t>(i) * (kChunk >> 4);
+                const uint64_t kd = k_desc + static_cast<uint32_t>(j % kSlots) * (kChunk >> 4);
+                if (elect_one()) {
+                    if (kt < nt) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) umma_bf16(s_at, qd + 2 * kk, kd + 2 * kk, kIdescQK, i > 0 || kk > 0);
+                        umma_commit(empty(j));
+                        if (i == 2) umma_commit(bar(kBarS + t));
+                    } else {
+                        mbar_arrive(empty(j));  // this row tile does not see the key tile
+                    }
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            if (kt < nt && !(ok = warp_wait(bar(kBarP + t), kt & 1))) break;
+            for (int i = 0; i < 2; ++i) {
+                const int j = kPerTile * kt + 3 + i;
+                if (!(ok = warp_wait(full(j), (j / kSlots) & 1))) break;
+                tc_fence_after();
+                const uint64_t vd = v_desc + static_cast<uint32_t>(j % kSlots) * (kChunk >> 4);
+                if (elect_one()) {
+                    if (kt < nt) {
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            umma_bf16_tmem_a(o_at + 64 * i, s_at + 8 * ks, vd + ks * (2048 >> 4), kIdescPV, kt > 0 || ks > 0);
+                        umma_commit(empty(j));
+                        if (i == 1 && kt == nt - 1) umma_commit(bar(kBarO + t));
+                    } else {
+                        mbar_arrive(empty(j));
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else {
+        // ---------------- softmax: a row a thread ----------------
+        const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const int nt = tile_nt(t), rows = tile_rows(t), i0 = r_lo + t * kRows;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + kTmemO + 128 * t;
+        const float sl2 = p.scale_log2;
+        const bool neg = sl2 < 0.f;  // then the largest score is the smallest product
+        const float hidden = neg ? INFINITY : -INFINITY;
+        const int limit = c + i0 + r;  // last visible key
+        float m = -INFINITY;
+        float2 l2 = make_float2(0.f, 0.f);
+        bool alive = true;
+        for (int kt = 0; alive && kt < nt; ++kt) {
+            if (!(alive = warp_wait(bar(kBarS + t), kt & 1))) break;
+            tc_fence_after();
+            const bool mask = kt * kKeys + kKeys - 1 > c + i0;  // some row does not see some key
+            auto load = [&](int cc, uint32_t(&v)[32]) {
+                tmem_ld_32x32b_x32(s_at + 32 * cc, v);
+                if (mask) {
+                    const int last = limit - kt * kKeys - 32 * cc;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (e > last) v[e] = __float_as_uint(hidden);
+                }
+            };
+            // The largest score of 32 (log2 domain).
+            auto largest = [&](const uint32_t(&v)[32]) {
+                float x[4] = {hidden, hidden, hidden, hidden};
+                if (neg) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e & 3] = fminf(x[e & 3], __uint_as_float(v[e]));
+                    return fminf(fminf(x[0], x[1]), fminf(x[2], x[3])) * sl2;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                    x[(e >> 1) & 3] = fmax3(x[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl2;
+            };
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+                uint32_t v[32];
+                load(cc, v);
+                float mx = largest(v);
+                if (__any_sync(0xffffffffu, mx > m + kRaise)) {
+                    // Raise the references that are passed to the largest score from here on (an integer),
+                    // and rescale what was made with the old one: weights 0 .. 32 cc, l, O.
+                    uint32_t u[32];
+                    for (int k = cc + 1; k < 4; ++k) {
+                        load(k, u);
+                        mx = fmaxf(mx, largest(u));
+                    }
+                    float alpha = 1.f;
+                    if (mx > m + kRaise) {
+                        const float up = ceilf(mx);
+                        alpha = fast_exp2(m - up);  // 0 from -inf
+                        m = up;
+                    }
+                    l2 = fmul2(l2, make_float2(alpha, alpha));
+                    tmem_wait_st();  // the weights that are read back now
+                    for (int k = 0; k < cc; ++k) {
+                        uint32_t w[16];
+                        tmem_ld_32x32b_x16(s_at + 16 * k, w);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = pack_bf16x2(__uint_as_float(w[e] << 16) * alpha, __uint_as_float(w[e] & 0xffff0000u) * alpha);
+                        tmem_st_32x32b_x16(s_at + 16 * k, w);
+                    }
+                    if (kt > 0) {  // every earlier P V of this tile completed before S (kt) did
+                        for (int k = 0; k < 4; ++k) {
+                            tmem_ld_32x32b_x32(o_at + 32 * k, u);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+                            tmem_st_32x32b_x32(o_at + 32 * k, u);
+                        }
+                    }
+                    tmem_wait_st();
+                }
+                const float mu = m == -INFINITY ? 0.f : m;
+                const float2 sv = make_float2(sl2, sl2), nm = make_float2(-mu, -mu);
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 x = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sv, nm);
+                    const float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                    l2 = fadd2(l2, pr);
+                    w[e] = pack_bf16x2(pr.x, pr.y);
+                }
+                tmem_st_32x32b_x16(s_at + 16 * cc, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarP + t));
+        }
+        // ---------------- epilogue: out = O / l ----------------
+        if (nt > 0 && alive && warp_wait(bar(kBarO + t), 0)) {
+            tc_fence_after();
+            const float l = l2.x + l2.y, inv = l > 0.f ? 1.f / l : 0.f;
+            const bool staged = p.out_bf16 && rows == kRows;  // a full tile leaves by TMA from its Q's place
+            const uint32_t stage = sbase + kOffQ + 3 * t * kChunk;
+            const size_t at = ((static_cast<size_t>(q0) + i0 + r) * p.heads + h) * kExpandedV;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(o_at + 32 * k, v);
+                auto f = [&](int e) { return __uint_as_float(v[e]) * inv; };
+                if (p.out_bf16) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint4 w = make_uint4(pack_bf16x2(f(8 * e), f(8 * e + 1)), pack_bf16x2(f(8 * e + 2), f(8 * e + 3)),
+                                                   pack_bf16x2(f(8 * e + 4), f(8 * e + 5)), pack_bf16x2(f(8 * e + 6), f(8 * e + 7)));
+                        if (staged)
+                            sts128(stage + (k >> 1) * kChunk + r * 128 + (((4 * (k & 1) + e) ^ (r & 7)) << 4), w);
+                        else if (r < rows)
+                            reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at)[4 * k + e] = w;
+                    }
+                } else if (r < rows) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[8 * k + e] =
+                            make_float4(f(4 * e), f(4 * e + 1), f(4 * e + 2), f(4 * e + 3));
+                }
+            }
+            if (staged) {
+                // A warp's 32 rows are one box of their own: no barrier over the tile.
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (elect_one()) {
+                    for (int k = 0; k < 2; ++k)
+                        tma_store_3d(&omap, stage + k * kChunk + quarter * 32 * 128, 64 * k, h, q0 + i0 + quarter * 32);
+                    bulk_commit_group();
+                    bulk_wait_group_read_all();  // shared memory must outlive the reads
+                }
+                __syncwarp();
+            }
+        }
+    }
+
+    // ---- teardown: every role is done (or gave up); free tensor memory ----
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort_flag && tid == 0) {
+        atomicOr(p.status, kStatusTimeout);
+        // Copies and MMAs that are still in flight: let them finish before the CTA's memory is freed.
+        const uint64_t until = globaltimer_ns() + kWaitLimitNs;
+        while (globaltimer_ns() < until) {
+        }
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_prefill(const LatentPrefillParams &p, cudaStream_t stream) {
-    const dim3 grid((p.max_q_len + 3) / 4, p.heads, p.num_seqs);
-    return launch_pdl(latent_prefill_kernel, grid, dim3(128), 0, stream, p);
+cudaError_t latent_prefill_prepare_device() {
+    return cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kSmemBytes));
+}
+
+cudaError_t launch_latent_prefill(const LatentPrefillMaps &maps, const LatentPrefillParams &p, cudaStream_t stream) {
+    const dim3 grid(p.heads, p.num_seqs, (p.max_q_len + 2 * kRows - 1) / (2 * kRows));
+    return launch_pdl(latent_prefill_kernel, grid, dim3(kThreads), kSmemBytes, stream, maps.q, maps.k, maps.rope, maps.out,
+                      p);
 }
 
 }  // namespace pkv
