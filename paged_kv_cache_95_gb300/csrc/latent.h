@@ -61,7 +61,10 @@ constexpr int kLatentMaxRanges = 160;  // at least the SMs (152); the merge keep
 constexpr int kLatentMaxCols = 64;     // columns a CTA takes
 constexpr int kLatentTile = 64;        // keys a tile
 cudaError_t latent_decode_prepare_device();
-cudaError_t launch_latent_decode(const CUtensorMap &kvmap, const LatentDecodeParams &p, bool fp8, cudaStream_t stream);
+struct LatentDecodeMaps {
+    CUtensorMap kv, rope;  // rope: FP8 pool only
+};
+cudaError_t launch_latent_decode(const LatentDecodeMaps &maps, const LatentDecodeParams &p, bool fp8, cudaStream_t stream);
 
 // ---- expanded attention of a prefill chunk --------------------------------------------
 struct LatentPrefillParams {

@@ -103,6 +103,26 @@ bool encode_latent_map(CUtensorMap *map, const void *base, int32_t num_blocks) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// An FP8 pool: the codes [num_blocks][16][512] the same way (128 codes a chunk, 4 chunks), the
+// rotated keys [num_blocks][16][64] bf16 as [16 slots][128 B].
+bool encode_latent_maps_fp8(pkv::LatentDecodeMaps *maps, const void *codes, const void *rope, int32_t num_blocks) {
+    const pkv::EncodeTiledFn fn = pkv::encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[5] = {128, 8, 4, 2, static_cast<cuuint64_t>(num_blocks)};
+    const cuuint64_t strides[4] = {pkv::kLatentDim, 128, pkv::kLatentDim * 8, pkv::kLatentDim * 16};
+    const cuuint32_t box[5] = {128, 8, 4, 2, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    const cuuint64_t rdims[3] = {64, 16, static_cast<cuuint64_t>(num_blocks)};
+    const cuuint64_t rstrides[2] = {128, 2048};
+    const cuuint32_t rbox[3] = {64, 16, 1};
+    return fn(&maps->kv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(codes), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+           fn(&maps->rope, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(rope), rdims, rstrides, rbox, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // How a decode call is split: one CTA per SM, column tiles of at most 64 columns of equal
 // size, and as many ranges of keys as there are SMs for a column tile (never more than
 // tiles).  Workspace: [status 256 B | records | part_ml | part_o].
@@ -225,9 +245,11 @@ int decode_impl(void *out, int32_t out_dtype, const void *q_latent, int64_t ql_r
     p.record = reinterpret_cast<int2 *>(ws + kStatusBytes);
     p.part_ml = reinterpret_cast<float2 *>(ws + pl.off_ml);
     p.part_o = reinterpret_cast<float *>(ws + pl.off_o);
-    CUtensorMap kvmap{};
-    if (!fp8 && !encode_latent_map(&kvmap, cache, desc->num_blocks)) return PKV_ERR_CUDA;
-    return pkv::launch_latent_decode(kvmap, p, fp8, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK
+    pkv::LatentDecodeMaps maps{};
+    if (fp8 ? !encode_latent_maps_fp8(&maps, cache, rope_cache, desc->num_blocks)
+            : !encode_latent_map(&maps.kv, cache, desc->num_blocks))
+        return PKV_ERR_CUDA;
+    return pkv::launch_latent_decode(maps, p, fp8, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK
                                                                                                      : PKV_ERR_CUDA;
 }
 

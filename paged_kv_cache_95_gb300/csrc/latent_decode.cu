@@ -55,33 +55,35 @@ constexpr int kScoreWarp = kSoftWarps + 1;    // issues S = Q K^T
 constexpr int kValueWarp = kSoftWarps + 2;    // issues O^T += V^T P^T
 constexpr int kLoadWarp = kSoftWarps + 3;     // two pairs of copying warps, one pair a stage
 constexpr int kThreads = (kSoftWarps + 7) * 32;
-constexpr int kStages = 2;
 constexpr int kTmaBlocks = 2;                 // blocks of a tile that TMA copies; the others go through cp.async
-constexpr uint32_t kBlockBytes = kBlockSize * kLatentRow * 2;  // 18 KB: [2 slot groups][9 chunks][8 slots][128 B]
-constexpr uint32_t kGroupBytes = kBlockBytes / 2;              // 8 slots
-constexpr uint32_t kStageBytes = kTileBlocks * kBlockBytes;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemS = 256;  // O^T in columns [0, 4 NCOL), S of tile i in [256 + 64 (i & 1), +64)
-constexpr float kRaise = 8.f;     // the reference follows the maximum when it is passed by 2^8
+constexpr uint32_t kTmemS = 256;  // O^T in columns [0, 4 NCOL), the scores of tile i from 256 + (i & 1) kScoreCols on
 
-// kv_full[stage], kv_empty[stage][block], s_full[2], s_empty[2], p_full, pv_done, q_full
-enum {
-    kBarKvFull = 0,
-    kBarKvEmpty = kBarKvFull + kStages,
-    kBarSFull = kBarKvEmpty + kStages * kTileBlocks,
-    kBarSEmpty = kBarSFull + 2,
-    kBarPFull = kBarSEmpty + 2,
-    kBarPvDone,
-    kBarQFull,
-    kNumBars
-};
-
-template <int NCOL>
+// Shared memory for NCOL columns over a bf16 or an FP8 pool.
+template <int NCOL, bool FP8>
 struct Layout {
-    static constexpr uint32_t kQ = 0;  // Q first: M = 64 reads up to 64 rows a chunk, past a smaller Q into the ring
-    static constexpr uint32_t kKv = kQ + NCOL * kLatentRow * 2;
-    static constexpr uint32_t kP = kKv + kStages * kStageBytes;
-    static constexpr uint32_t kBar = kP + NCOL * 128;
+    // A block of 16 slots: [2 groups of 8 slots][chunks of 128 bytes][8 slots][128 B]; chunks are 64 bf16 values
+    // (9 of them, the last the rotated key) or 128 codes (4; the rotated keys follow the stage's codes).
+    static constexpr uint32_t kChunks = FP8 ? 4 : 9;
+    static constexpr uint32_t kGroup = kChunks * 1024;
+    static constexpr uint32_t kBlock = 2 * kGroup;
+    static constexpr uint32_t kRopeBlock = FP8 ? kBlockSize * 128 : 0;
+    static constexpr uint32_t kStage = kTileBlocks * (kBlock + kRopeBlock);
+    static constexpr int kStages = FP8 ? (NCOL == 64 ? 3 : 4) : 2;
+    // Score columns of a tile (FP8: the latent's and the rotated key's products apart, the scale goes with the first).
+    static constexpr uint32_t kScoreCols = FP8 ? 128 : 64;
+    // Q: [9 chunks][NCOL][128 B]; FP8: 4 chunks of heads, 4 of remainders (E4M3), the rotated part in bf16.  It lies
+    // first: M = 64 reads up to 64 rows a chunk, past a smaller Q into the ring.
+    static constexpr uint32_t kQ = 0;
+    static constexpr uint32_t kKv = kQ + NCOL * 9 * 128;
+    static constexpr uint32_t kP = kKv + kStages * kStage;  // [NCOL][64 bf16], or [NCOL][64 heads | 64 remainders]
+    static constexpr uint32_t kScale = kP + NCOL * 128;     // FP8: [stage][64] scales of the keys
+    static constexpr uint32_t kQf = kScale + (FP8 ? kStages * kTile * 4 : 0);  // FP8: [64] factors of the rows of Q
+    // kv_full[stage], kv_empty[stage][block], s_full[2], s_empty[2], p_full, pv_done, q_full
+    static constexpr int kBarKvFull = 0, kBarKvEmpty = kStages, kBarSFull = kBarKvEmpty + kStages * kTileBlocks,
+                         kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 2, kBarPvDone = kBarPFull + 1,
+                         kBarQFull = kBarPvDone + 1, kNumBars = kBarQFull + 1;
+    static constexpr uint32_t kBar = kQf + (FP8 ? 64 * 4 : 0);
     static constexpr uint32_t kTmemSlot = kBar + 8 * kNumBars;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kXch = (kAbort + 4 + 15) / 16 * 16;  // [tile & 1][key half][64] maxima, later sums
@@ -89,11 +91,16 @@ struct Layout {
     static constexpr uint32_t kPlan = kAlpha + 64 * 4;             // warp totals, then the range's start
     static constexpr uint32_t kBytes = kPlan + 18 * 8;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
-    static_assert(kKv % 1024 == 0 && kP % 1024 == 0, "swizzle atoms");
+    static_assert(kKv % 1024 == 0 && kP % 1024 == 0 && kStage % 1024 == 0, "swizzle atoms");
+    static_assert(kScale % 16 == 0 && kBar % 8 == 0 && kPlan % 8 == 0, "alignment");
+    // A weight may pass the reference by 2^kRaise before the reference follows.  FP8 keeps the weights as pairs of
+    // E4M3 codes: 2^4 at the reference, so 2^8 at most (448 is the largest code) and steps of 2^-9 below.
+    static constexpr float kRaise = FP8 ? 4.f : 8.f, kLift = FP8 ? 4.f : 0.f;
 };
 
-__host__ __device__ constexpr uint32_t idesc(int m, int n, bool a_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+// Instruction descriptor: D f32; A and B bf16 (kind::f16) or E4M3 (kind::f8f6f4).
+__host__ __device__ constexpr uint32_t idesc(int m, int n, bool a_mn, bool f8 = false) {
+    return (1u << 4) | (f8 ? 0u : (1u << 7) | (1u << 10)) | (a_mn ? 1u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
@@ -114,6 +121,9 @@ __device__ __forceinline__ bool bar_red_or(uint32_t id, uint32_t nthreads, bool 
         : "memory");
     return r != 0;
 }
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // Keys of sequence b that its rows see (0: none, its rows are zeros).
 __device__ __forceinline__ int keys_of(const LatentDecodeParams &p, int b) {
@@ -140,10 +150,12 @@ struct Walk {
     }
 };
 
-template <int NCOL>
+template <int NCOL, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)
-    latent_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const LatentDecodeParams p) {
-    using L = Layout<NCOL>;
+    latent_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap ropemap,
+                         const LatentDecodeParams p) {
+    using L = Layout<NCOL, FP8>;
+    constexpr int kStages = L::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -151,7 +163,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cols = p.heads * p.q_per_seq;
     const int c0 = ct * p.cols_per_tile, nc = min(p.cols_per_tile, cols - c0);
 
-    if (tid == 0) prefetch_tensormap(&kvmap);
+    if (tid == 0) {
+        prefetch_tensormap(&kvmap);
+        if (FP8) prefetch_tensormap(&ropemap);
+    }
     griddep_launch_dependents();
     if (sbase & 1023u) {  // operands need the 1 KB swizzle alignment
         if (tid == 0) atomicOr(p.status, kStatusTimeout);
@@ -162,9 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmemSlot);
     int64_t *plan = reinterpret_cast<int64_t *>(smem + L::kPlan);
     if (tid == 0) {
-        for (int i = 0; i < kNumBars; ++i)
-            mbar_init(bar(i), i < kBarKvEmpty ? kTmaBlocks + 2
-                              : i == kBarSEmpty || i == kBarSEmpty + 1 || i == kBarPFull || i == kBarQFull ? kSoftWarps : 1);
+        for (int i = 0; i < L::kNumBars; ++i)
+            mbar_init(bar(i), i < L::kBarKvEmpty ? kTmaBlocks + 2
+                              : i == L::kBarSEmpty || i == L::kBarSEmpty + 1 || i == L::kBarPFull || i == L::kBarQFull ? kSoftWarps : 1);
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -278,12 +293,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
 #pragma unroll
             for (int j = 0; j < kTmaBlocks; ++j) {  // P V frees a stage block by block
-                if (i >= kStages) ok = ok && warp_wait(bar(kBarKvEmpty + st * kTileBlocks + j), ((i / kStages) - 1) & 1);
+                if (i >= kStages) ok = ok && warp_wait(bar(L::kBarKvEmpty + st * kTileBlocks + j), ((i / kStages) - 1) & 1);
                 if (ok && lane == j) {
-                    mbar_arrive_expect_tx(bar(kBarKvFull + st), cur >= 0 ? kBlockBytes : 0);
-                    if (cur >= 0)
-                        tma_load_5d(sbase + L::kKv + st * kStageBytes + j * kBlockBytes, &kvmap, bar(kBarKvFull + st), 0, 0,
-                                    0, 0, cur);
+                    const uint32_t full = bar(L::kBarKvFull + st), stage = sbase + L::kKv + st * L::kStage;
+                    mbar_arrive_expect_tx(full, cur >= 0 ? L::kBlock + L::kRopeBlock + (FP8 ? kBlockSize * 4 : 0) : 0);
+                    if (cur >= 0) {
+                        tma_load_5d(stage + j * L::kBlock, &kvmap, full, 0, 0, 0, 0, cur);
+                        if constexpr (FP8) {
+                            tma_load_3d(stage + kTileBlocks * L::kBlock + j * L::kRopeBlock, &ropemap, full, 0, 0, cur);
+                            bulk_copy_g2s(sbase + L::kScale + (st * kTile + j * kBlockSize) * 4,
+                                          p.cache_scale + static_cast<size_t>(cur) * kBlockSize, kBlockSize * 4, full);
+                        }
+                    }
                 }
             }
             if (i == 0) second_tile();
@@ -291,22 +312,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kLoadWarp) {
         // ---------------- copying warps: the blocks from kTmaBlocks on of every second tile ----------------
-        const int st = (warp - kLoadWarp) >> 1, t = ((warp - kLoadWarp) & 1) * 32 + lane;  // 64 threads a stage
-        // 16-byte vector t + 64 k of a block (72 a slot): its place in the operand layout, k < 9 (the
-        // second group of 8 slots follows 9216 bytes on, on both sides).
-        uint32_t to[9];
+        const int g = (warp - kLoadWarp) >> 1, t = ((warp - kLoadWarp) & 1) * 32 + lane;  // 64 threads a tile
+        // Where the 16-byte vectors t + 64 k of 8 slots (72 a slot, or 32) go; the second 8 slots follow kGroup
+        // bytes on.
+        constexpr int kVec = FP8 ? 32 : 72, kSteps = kVec * 8 / 64;
+        uint32_t to[kSteps];
 #pragma unroll
-        for (int k = 0; k < 9; ++k) {
-            const int v = t + 64 * k, r = v / 72, c = v - r * 72;
+        for (int k = 0; k < kSteps; ++k) {
+            const int v = t + 64 * k, r = v / kVec, c = v - r * kVec;
             to[k] = (c >> 3) * 1024 + r * 128 + (((c & 7) ^ r) << 4);
         }
         Walk w;
         w.at(p, b0, t0);
-        if (st == 1) {
+        if (g == 1) {
             if (n > 1) w.next(p);
             second_tile();
         }
-        for (int i = st; i < n; i += kStages) {
+        for (int i = g; i < n; i += 2) {
+            const int st = i % kStages;
             int id = -1;
             const int jb = w.t * kTileBlocks + lane;
             if (lane < kTileBlocks && jb * kBlockSize < w.keys)
@@ -316,21 +339,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = kTmaBlocks; j < kTileBlocks; ++j) {
                 const int blk = __shfl_sync(0xffffffffu, id, j);
-                if (i >= kStages) ok = ok && warp_wait(bar(kBarKvEmpty + st * kTileBlocks + j), ((i / kStages) - 1) & 1);
+                if (i >= kStages) ok = ok && warp_wait(bar(L::kBarKvEmpty + st * kTileBlocks + j), ((i / kStages) - 1) & 1);
                 if (ok && blk >= 0) {
-                    const uint8_t *src = static_cast<const uint8_t *>(p.cache) + static_cast<size_t>(blk) * kBlockBytes + 16 * t;
-                    const uint32_t dst = sbase + L::kKv + st * kStageBytes + j * kBlockBytes;
+                    const uint32_t stage = sbase + L::kKv + st * L::kStage, dst = stage + j * L::kBlock;
+                    const uint8_t *src = static_cast<const uint8_t *>(p.cache) + static_cast<size_t>(blk) * L::kBlock + 16 * t;
 #pragma unroll
-                    for (int k = 0; k < 18; ++k)
-                        cp_async_16(dst + (k / 9) * kGroupBytes + to[k % 9], src + 1024 * k);
+                    for (int k = 0; k < 2 * kSteps; ++k)
+                        cp_async_16(dst + (k / kSteps) * L::kGroup + to[k % kSteps], src + 1024 * k);
+                    if constexpr (FP8) {  // 8 vectors of rotated key a slot, and the 16 scales
+                        const uint8_t *rope = static_cast<const uint8_t *>(p.rope_cache) + static_cast<size_t>(blk) * L::kRopeBlock + 16 * t;
+                        const uint32_t rdst = stage + kTileBlocks * L::kBlock + j * L::kRopeBlock + (t >> 3) * 128 +
+                                              (((t & 7) ^ (t >> 3)) << 4);
+                        cp_async_16(rdst, rope);
+                        cp_async_16(rdst + 1024, rope + 1024);
+                        if (t < 4)
+                            cp_async_16(sbase + L::kScale + (st * kTile + j * kBlockSize + 4 * t) * 4,
+                                        p.cache_scale + static_cast<size_t>(blk) * kBlockSize + 4 * t);
+                    }
                 }
             }
             if (!ok) break;
-            for (int k = 0; k < kStages && i + 1 + k < n; ++k) w.next(p);
+            for (int k = 0; k < 2 && i + 1 + k < n; ++k) w.next(p);
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();  // generic writes -> the tensor core
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarKvFull + st));
+            if (lane == 0) mbar_arrive(bar(L::kBarKvFull + st));
         }
     } else if (warp == kScoreWarp) {
         // ---------------- S = Q K^T ----------------
@@ -340,27 +373,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         Walk w;
         w.at(p, b0, t0);
         const uint64_t q_desc = sw128_desc(sbase + L::kQ, 16, 1024);
-        const uint64_t k_desc = sw128_desc(sbase + L::kKv, 16, kGroupBytes);
+        const uint64_t k_desc = sw128_desc(sbase + L::kKv, 16, L::kGroup);
+        const uint64_t r_desc = sw128_desc(sbase + L::kKv + kTileBlocks * L::kBlock, 16, 1024);
         int pieces = 0;
         for (int i = 0; i < n; ++i) {
             const int st = i % kStages;
             if (i == 0 || w.t == 0) {
-                if (!warp_wait(bar(kBarQFull), pieces & 1)) break;
+                if (!warp_wait(bar(L::kBarQFull), pieces & 1)) break;
                 ++pieces;
             }
-            if (i >= 2 && !warp_wait(bar(kBarSEmpty + (i & 1)), ((i >> 1) - 1) & 1)) break;
-            if (!warp_wait(bar(kBarKvFull + st), (i / kStages) & 1)) break;
+            if (i >= 2 && !warp_wait(bar(L::kBarSEmpty + (i & 1)), ((i >> 1) - 1) & 1)) break;
+            if (!warp_wait(bar(L::kBarKvFull + st), (i / kStages) & 1)) break;
             tc_fence_after();
-            const uint32_t d = tmem + kTmemS + 64 * (i & 1);
-            const uint64_t kd = k_desc + static_cast<uint32_t>(st) * (kStageBytes >> 4);
+            const uint32_t d = tmem + kTmemS + L::kScoreCols * (i & 1);
+            const uint64_t kd = k_desc + static_cast<uint32_t>(st) * (L::kStage >> 4);
+            const uint64_t rd = r_desc + static_cast<uint32_t>(st) * (L::kStage >> 4);
             if (elect_one()) {
 #pragma unroll
                 for (int c = 0; c < 9; ++c)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16(d, q_desc + ((c * NCOL * 128 + kk * 32) >> 4), kd + ((c * 1024 + kk * 32) >> 4),
-                                  idesc(64, kTile, false), c + kk > 0);
-                umma_commit(bar(kBarSFull + (i & 1)));
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t qd = q_desc + ((c * NCOL * 128 + kk * 32) >> 4);
+                        if constexpr (!FP8)
+                            umma_bf16(d, qd, kd + ((c * 1024 + kk * 32) >> 4), idesc(64, kTile, false), c + kk > 0);
+                        else if (c < 8)  // heads, then remainders, against the same codes
+                            umma_e4m3(d, qd, kd + (((c & 3) * 1024 + kk * 32) >> 4), idesc(64, kTile, false, true), c + kk > 0);
+                        else
+                            umma_bf16(d + 64, qd, rd + ((kk * 32) >> 4), idesc(64, kTile, false), kk > 0);
+                    }
+                umma_commit(bar(L::kBarSFull + (i & 1)));
             }
             __syncwarp();
             if (i + 1 < n) w.next(p);
@@ -369,24 +410,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- O^T += V^T P^T ----------------
         Walk w;
         w.at(p, b0, t0);
-        const uint64_t v_desc = sw128_desc(sbase + L::kKv, 1024, kGroupBytes);
+        const uint64_t v_desc = sw128_desc(sbase + L::kKv, 1024, L::kGroup);
         const uint64_t p_desc = sw128_desc(sbase + L::kP, 16, 1024);
         for (int i = 0; i < n; ++i) {
             const int st = i % kStages;
             const uint32_t keep = i > 0 && w.t > 0;  // a piece's first P V overwrites O
-            if (!warp_wait(bar(kBarPFull), i & 1)) break;
+            if (!warp_wait(bar(L::kBarPFull), i & 1)) break;
             tc_fence_after();
-            const uint64_t vd = v_desc + static_cast<uint32_t>(st) * (kStageBytes >> 4);
+            const uint64_t vd = v_desc + static_cast<uint32_t>(st) * (L::kStage >> 4);
             if (elect_one()) {
+                if constexpr (!FP8) {
 #pragma unroll
-                for (int ks = 0; ks < kTileBlocks; ++ks) {
+                    for (int ks = 0; ks < kTileBlocks; ++ks) {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        umma_bf16(tmem + m * NCOL, vd + ((ks * kBlockBytes + m * 2048) >> 4), p_desc + ((ks * 32) >> 4),
-                                  idesc(128, NCOL, true), ks > 0 ? 1u : keep);
-                    umma_commit(bar(kBarKvEmpty + st * kTileBlocks + ks));
+                        for (int m = 0; m < 4; ++m)
+                            umma_bf16(tmem + m * NCOL, vd + ((ks * L::kBlock + m * 2048) >> 4), p_desc + ((ks * 32) >> 4),
+                                      idesc(128, NCOL, true), ks > 0 ? 1u : keep);
+                        umma_commit(bar(L::kBarKvEmpty + st * kTileBlocks + ks));
+                    }
+                } else {  // 32 keys a step; heads and remainders against the same codes
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const uint64_t v = vd + ((ks * 2 * L::kBlock + m * 1024) >> 4), w8 = p_desc + ((ks * 32) >> 4);
+                            umma_e4m3(tmem + m * NCOL, v, w8, idesc(128, NCOL, true, true), ks > 0 ? 1u : keep);
+                            umma_e4m3(tmem + m * NCOL, v, w8 + (64 >> 4), idesc(128, NCOL, true, true), 1u);
+                        }
+                        umma_commit(bar(L::kBarKvEmpty + st * kTileBlocks + 2 * ks));
+                        umma_commit(bar(L::kBarKvEmpty + st * kTileBlocks + 2 * ks + 1));
+                    }
                 }
-                umma_commit(bar(kBarPvDone));
+                umma_commit(bar(L::kBarPvDone));
             }
             __syncwarp();
             if (i + 1 < n) w.next(p);
@@ -411,24 +466,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto soft_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); };
         bool alive = true;
 
-        // Sequence b's Q, a row a warp: 72 vectors a column, zeros behind the last one, in the
-        // operand's swizzle.
+        // Sequence b's Q, a row a warp, zeros behind the last one, in the operand's swizzle.  FP8: the
+        // latent part times a power of two that takes its largest value into (224, 448], as E4M3
+        // heads and remainders (a bf16 value has 8 bits, two codes hold 4 each: exact down to steps
+        // of 2^-9); the factor that undoes it in shared memory.
+        float *qf_s = reinterpret_cast<float *>(smem + L::kQf);
         auto load_q = [&](int b) {
-#pragma unroll 1
+#pragma unroll FP8 ? 4 : 1
             for (int r = warp; r < NCOL; r += kSoftWarps) {
                 const int c = c0 + r, i = c / p.heads;
                 const int64_t qr = static_cast<int64_t>(b) * p.q_per_seq + i, h = c - i * p.heads;
                 const uint16_t *ql = static_cast<const uint16_t *>(p.q_latent) + qr * p.ql_row + h * p.ql_head;
                 const uint16_t *qp = static_cast<const uint16_t *>(p.q_rope) + qr * p.qr_row + h * p.qr_head;
+                auto at = [&](int chunk, int v) { return sbase + L::kQ + chunk * (NCOL * 128) + r * 128 + ((v ^ (r & 7)) << 4); };
+                if constexpr (!FP8) {
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    const int v = lane + 32 * k;
-                    const uint32_t dst = sbase + L::kQ + (v >> 3) * (NCOL * 128) + r * 128 + (((v & 7) ^ (r & 7)) << 4);
-                    if (v >= 72) continue;
-                    if (r < nc)
-                        cp_async_16(dst, v < 64 ? ql + v * 8 : qp + (v - 64) * 8);
-                    else
-                        sts128(dst, make_uint4(0u, 0u, 0u, 0u));
+                    for (int k = 0; k < 3; ++k) {
+                        const int v = lane + 32 * k;
+                        if (v >= 72) continue;
+                        if (r < nc)
+                            cp_async_16(at(v >> 3, v & 7), v < 64 ? ql + v * 8 : qp + (v - 64) * 8);
+                        else
+                            sts128(at(v >> 3, v & 7), make_uint4(0u, 0u, 0u, 0u));
+                    }
+                } else {
+                    uint4 a = make_uint4(0u, 0u, 0u, 0u), d = a, rope = a;
+                    if (r < nc) {
+                        a = __ldg(reinterpret_cast<const uint4 *>(ql) + 2 * lane);
+                        d = __ldg(reinterpret_cast<const uint4 *>(ql) + 2 * lane + 1);
+                        if (lane < 8) rope = __ldg(reinterpret_cast<const uint4 *>(qp) + lane);
+                    }
+                    const uint32_t u[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+                    float v[16], most = 0.f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        v[2 * k] = bf16_lo(u[k]), v[2 * k + 1] = bf16_hi(u[k]);
+                        most = fmax3(most, fabsf(v[2 * k]), fabsf(v[2 * k + 1]));
+                    }
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+                    // most = f 2^e, 1 <= f < 2: times 2^(8 - e), or 2^(7 - e) when f 2^8 passes 448 (both exponents
+                    // kept within fp32's; an all-zero row keeps factor 1).
+                    const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;
+                    int lift = most > 0.f ? ((__float_as_uint(most) & 0x7fffffu) > 0x600000u ? 7 : 8) - e : 0;
+                    lift = max(-126, min(126, lift));
+                    const float up = __uint_as_float(static_cast<uint32_t>(lift + 127) << 23);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t h0 = f32x2_to_e4m3x2(v[4 * k] * up, v[4 * k + 1] * up);
+                        const uint32_t h1 = f32x2_to_e4m3x2(v[4 * k + 2] * up, v[4 * k + 3] * up);
+                        const float2 f0 = unpack_f16x2(e4m3x2_to_f16x2(h0)), f1 = unpack_f16x2(e4m3x2_to_f16x2(h1));
+                        hi[k] = h0 | h1 << 16;
+                        lo[k] = f32x2_to_e4m3x2(v[4 * k] * up - f0.x, v[4 * k + 1] * up - f0.y) |
+                                f32x2_to_e4m3x2(v[4 * k + 2] * up - f1.x, v[4 * k + 3] * up - f1.y) << 16;
+                    }
+                    sts128(at(lane >> 3, lane & 7), make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    sts128(at(4 + (lane >> 3), lane & 7), make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    if (lane < 8) sts128(at(8, lane), rope);
+                    if (lane == 0) qf_s[r] = __uint_as_float(static_cast<uint32_t>(127 - lift) << 23);
                 }
             }
         };
@@ -436,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarQFull));
+            if (lane == 0) mbar_arrive(bar(L::kBarQFull));
         };
 
         Walk w;
@@ -445,6 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("bar.arrive 2, %0;" ::"n"(kSoftThreads + 96) : "memory");  // Q before the second tile
         empty_sequences(tid, kSoftThreads);
         publish_q();
+        if constexpr (FP8) soft_sync();  // the factors of Q's rows are written
+        float q_scale[2] = {0.f, 0.f};   // FP8: those of rows r and r + 8, times the softmax scale
         float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         bool piece_mid = t0 > 0;  // the piece does not hold its sequence's first key
         for (int i = 0; i < n; ++i) {
@@ -453,6 +551,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (first) {
                 m_ref[0] = m_ref[1] = -INFINITY;
                 l[0] = l[1] = 0.f;
+            }
+            if (FP8 && warp_has && (i == 0 || w.t == 0)) {
+                q_scale[0] = qf_s[row] * p.scale_log2;
+                q_scale[1] = qf_s[row + 8] * p.scale_log2;
             }
             // Blocks of the tile with an invalid id: flagged, their keys masked.
             const int jb = w.t * kTileBlocks + lane;
@@ -464,16 +566,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (bad && tid == 0) atomicOr(p.status, kStatusBadBlockId);
             const int left = w.keys - w.t * kTile;  // keys of the tile that exist (may pass 64)
 
-            alive = alive && warp_wait(bar(kBarSFull + (i & 1)), (i >> 1) & 1);
+            alive = alive && warp_wait(bar(L::kBarSFull + (i & 1)), (i >> 1) & 1);
+            if (FP8) alive = alive && warp_wait(bar(L::kBarKvFull + i % kStages), (i / kStages) & 1);  // its scales
             float x[16];  // [4 j + 2 k + e]: row r + 8 k, key 32 half + 8 j + 2 (lane % 4) + e
+            float inv_s[8];  // FP8: [2 j + e] 1 / scale of the key
             float mx[2] = {-INFINITY, -INFINITY};
             if (alive && warp_has) {
                 tc_fence_after();
                 uint32_t v[16];
-                tmem_ld_16x256b_x4(tmem + lanes + kTmemS + 64 * (i & 1) + 32 * half, v);
-                tc_fence_before();
+                const uint32_t s_at = tmem + lanes + kTmemS + L::kScoreCols * (i & 1) + 32 * half;
+                tmem_ld_16x256b_x4(s_at, v);
+                if constexpr (!FP8) {
+                    tc_fence_before();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]) * p.scale_log2;
+                    for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]) * p.scale_log2;
+                } else {
+                    // c_j = code s_j: the score is s_j <q, code_j> + <q_rope, r_j>, and the weight that multiplies
+                    // the codes is s_j 2^score = 2^(score + log2 s_j); the sum l takes it without s_j.
+                    uint32_t u[16];
+                    tmem_ld_16x256b_x4(s_at + 64, u);
+                    tc_fence_before();
+                    const uint32_t sc = sbase + L::kScale + ((i % kStages) * kTile + 32 * half + 2 * (lane & 3)) * 4;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float s2[2] = {lds_f32(sc + 32 * j), lds_f32(sc + 32 * j + 4)};
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = 32 * half + 8 * j + 2 * (lane & 3) + e;
+                            if (key >= left || ((bad >> (key >> 4)) & 1u)) s2[e] = 1.f;  // whatever was there
+                            const float lg = __log2f(s2[e]);
+                            inv_s[2 * j + e] = __fdividef(1.f, s2[e]);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                x[4 * j + 2 * k + e] = __uint_as_float(v[4 * j + 2 * k + e]) * (q_scale[k] * s2[e]) +
+                                                       (__uint_as_float(u[4 * j + 2 * k + e]) * p.scale_log2 + lg);
+                        }
+                    }
+                }
                 // Row q_row sees keys up to keys - q_per_seq + q_row; bad blocks see none.
                 if (left - p.q_per_seq + 1 < kTile || bad) {
 #pragma unroll
@@ -491,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             __syncwarp();
-            if (alive && lane == 0) mbar_arrive(bar(kBarSEmpty + (i & 1)));
+            if (alive && lane == 0) mbar_arrive(bar(L::kBarSEmpty + (i & 1)));
             // The last S of a piece is complete: its Q can make way for the next sequence's.
             const bool more = last && i + 1 < n;
             Walk nx = w;
@@ -504,13 +633,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 xm[half * 64 + row + 8] = mx[1];
             }
             bool drained = false;  // this warp saw P V (i - 1) complete
-            if (bar_red_or(1, kSoftThreads, warp_has && (mx[0] > m_ref[0] + kRaise || mx[1] > m_ref[1] + kRaise))) {
+            if (bar_red_or(1, kSoftThreads, warp_has && (mx[0] > m_ref[0] + L::kRaise || mx[1] > m_ref[1] + L::kRaise))) {
                 if (warp_has) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         float alpha = 1.f;
                         const float mt = fmaxf(xm[row + 8 * k], xm[64 + row + 8 * k]);
-                        if (mt > m_ref[k] + kRaise) {
+                        if (mt > m_ref[k] + L::kRaise) {
                             alpha = fast_exp2(m_ref[k] - mt);  // 0 from -inf
                             m_ref[k] = mt;
                             l[k] *= alpha;
@@ -520,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!first) {  // (the first P V of a piece overwrites O)
                     soft_sync();
-                    alive = alive && warp_wait(bar(kBarPvDone), (i - 1) & 1);
+                    alive = alive && warp_wait(bar(L::kBarPvDone), (i - 1) & 1);
                     drained = true;
                     if (alive) {
                         tc_fence_after();
@@ -538,23 +667,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // Weights, rounded to bf16 (relative 2^-8); l adds what P V will read.
+            // Weights, rounded to bf16 (relative 2^-8; l adds what P V will read), or to a pair of E4M3 codes
+            // (relative 2^-8, steps of 2^-9 where the largest is at least 2^4).
             uint32_t pk[8];  // [2 j + k]: the pair of row r + 8 k in 8-key group j
             if (warp_has) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float mu = m_ref[k] == -INFINITY ? 0.f : m_ref[k];
+                    const float mu = m_ref[k] == -INFINITY ? 0.f : m_ref[k] - L::kLift;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
+                        if constexpr (FP8) {
+                            const float w0 = fast_exp2(x[4 * j + 2 * k] - mu), w1 = fast_exp2(x[4 * j + 2 * k + 1] - mu);
+                            l[k] += w0 * inv_s[2 * j] + w1 * inv_s[2 * j + 1];
+                            const uint32_t hi = f32x2_to_e4m3x2(w0, w1);
+                            const float2 f = unpack_f16x2(e4m3x2_to_f16x2(hi));
+                            pk[2 * j + k] = hi | f32x2_to_e4m3x2(w0 - f.x, w1 - f.y) << 16;
+                            continue;
+                        }
                         const uint32_t w2 = pack_bf16x2(fast_exp2(x[4 * j + 2 * k] - mu), fast_exp2(x[4 * j + 2 * k + 1] - mu));
                         l[k] += __uint_as_float(w2 << 16) + __uint_as_float(w2 & 0xffff0000u);
                         pk[2 * j + k] = w2;
                     }
                 }
             }
-            if (i > 0 && !drained) alive = alive && warp_wait(bar(kBarPvDone), (i - 1) & 1);  // P is free again
+            if (i > 0 && !drained) alive = alive && warp_wait(bar(L::kBarPvDone), (i - 1) & 1);  // P is free again
             if (alive) {
-                if (warp_has) {
+                if (FP8 && warp_has) {  // two keys of a row: 2 bytes of heads, 2 of remainders 64 bytes on
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = row + 8 * k, v = 2 * half + (j >> 1);
+                            const uint32_t at = sbase + L::kP + r * 128 + 8 * (j & 1) + 2 * (lane & 3);
+                            sts16(at + ((v ^ (r & 7)) << 4), pk[2 * j + k]);
+                            sts16(at + (((v + 4) ^ (r & 7)) << 4), pk[2 * j + k] >> 16);
+                        }
+                } else if (warp_has) {
 #pragma unroll
                     for (int j = 0; j < 4; j += 2)
                         stmatrix_x4(p_at + (((4 * half + j + (lane >> 4)) ^ (p_row & 7)) << 4), pk[2 * j], pk[2 * j + 1],
@@ -563,12 +711,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Rows that no key fills (past the context, of an invalid block) hold whatever was there:
                 // their weights are 0, their values have to be finite.
                 if (left < kTile || bad) {
-                    alive = warp_wait(bar(kBarKvFull + i % kStages), (i / kStages) & 1);
-                    const uint32_t kv = sbase + L::kKv + (i % kStages) * kStageBytes;
-                    for (int idx = tid; alive && idx < kTile * 64; idx += kSoftThreads) {
-                        const int key = idx >> 6, v = idx & 63;  // (all of a row's 16-byte chunks: the swizzle is moot)
+                    alive = warp_wait(bar(L::kBarKvFull + i % kStages), (i / kStages) & 1);
+                    const uint32_t kv = sbase + L::kKv + (i % kStages) * L::kStage;
+                    constexpr int kVec = FP8 ? 32 : 64;  // (all of a latent's 16-byte chunks: the swizzle is moot)
+                    for (int idx = tid; alive && idx < kTile * kVec; idx += kSoftThreads) {
+                        const int key = idx / kVec, v = idx % kVec;
                         if (key >= left || ((bad >> (key >> 4)) & 1u))
-                            sts128(kv + (key >> 3) * kGroupBytes + (v >> 3) * 1024 + (key & 7) * 128 + (v & 7) * 16,
+                            sts128(kv + (key >> 3) * L::kGroup + (v >> 3) * 1024 + (key & 7) * 128 + (v & 7) * 16,
                                    make_uint4(0u, 0u, 0u, 0u));
                     }
                 }
@@ -576,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
             }
             __syncwarp();
-            if (alive && lane == 0) mbar_arrive(bar(kBarPFull));
+            if (alive && lane == 0) mbar_arrive(bar(L::kBarPFull));
             if (more && alive) publish_q();
 
             if (last) {
@@ -606,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 soft_sync();
-                alive = alive && warp_wait(bar(kBarPvDone), i & 1);
+                alive = alive && warp_wait(bar(L::kBarPvDone), i & 1);
                 if (alive) {
                     tc_fence_after();
 #pragma unroll 1
@@ -770,128 +919,39 @@ __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const La
     }
 }
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-template <bool FP8>
-__global__ void __launch_bounds__(128) latent_decode_simple_kernel(const LatentDecodeParams p) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.q_per_seq;
-    if (unit >= rows * p.heads) return;
-    const int64_t row = unit / p.heads;
-    const int h = static_cast<int>(unit - row * p.heads);
-    const int b = static_cast<int>(row / p.q_per_seq), i = static_cast<int>(row - static_cast<int64_t>(b) * p.q_per_seq);
-    const int cap = p.max_blocks * kBlockSize;
-    int ctx = __ldg(p.context_lens + b);
-    uint32_t bad = ctx < 1 || ctx > cap ? kStatusBadContextLen : 0u;
-    if (ctx >= 1 && ctx < p.q_per_seq) bad |= kStatusBadQLen;
-    ctx = min(ctx, cap);
-    const int keys = ctx < 1 || ctx < p.q_per_seq ? 0 : ctx - p.q_per_seq + 1 + i;
-
-    float q[18], o[16] = {};
-    {
-        const uint4 *ql = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q_latent) + row * p.ql_row +
-                                                          h * p.ql_head);
-        const uint4 a = __ldg(ql + 2 * lane), c = __ldg(ql + 2 * lane + 1);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) q[2 * k] = bf16_lo(w[k]), q[2 * k + 1] = bf16_hi(w[k]);
-        const uint32_t r = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.q_rope) +
-                                                                    row * p.qr_row + h * p.qr_head) + lane);
-        q[16] = bf16_lo(r), q[17] = bf16_hi(r);
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int j = 0; j < keys; ++j) {
-        const int blk = __ldg(p.block_tables + static_cast<size_t>(b) * p.max_blocks + j / kBlockSize);
-        if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks)) {
-            bad |= kStatusBadBlockId;
-            continue;
-        }
-        const size_t slot = static_cast<size_t>(blk) * kBlockSize + j % kBlockSize;
-        float c[16];
-        uint32_t rw;
-        if (FP8) {
-            const uint4 a = __ldg(static_cast<const uint4 *>(p.cache) + slot * 32 + lane);
-            const float sc = __ldg(p.cache_scale + slot);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 f = unpack_f16x2(e4m3x2_to_f16x2(w[k])), g = unpack_f16x2(e4m3x2_to_f16x2(w[k] >> 16));
-                c[4 * k] = f.x * sc, c[4 * k + 1] = f.y * sc, c[4 * k + 2] = g.x * sc, c[4 * k + 3] = g.y * sc;
-            }
-            rw = __ldg(static_cast<const uint32_t *>(p.rope_cache) + slot * 32 + lane);
-        } else {
-            const uint4 *src = static_cast<const uint4 *>(p.cache) + slot * 72;
-            const uint4 a = __ldg(src + 2 * lane), d = __ldg(src + 2 * lane + 1);
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) c[2 * k] = bf16_lo(w[k]), c[2 * k + 1] = bf16_hi(w[k]);
-            rw = __ldg(reinterpret_cast<const uint32_t *>(src + 64) + lane);
-        }
-        float s = q[16] * bf16_lo(rw) + q[17] * bf16_hi(rw);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) s += q[k] * c[k];
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s);
-        const float alpha = exp2f(m - mn), e = exp2f(s - mn);
-        l = l * alpha + e;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = o[k] * alpha + e * c[k];
-        m = mn;
-    }
-    if (bad && lane == 0 && p.status) atomicOr(p.status, bad);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const size_t at = static_cast<size_t>(unit) * kLatentDim + 16 * lane;
-    if (p.out_bf16) {
-        uint32_t w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv);
-        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at);
-        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
-    }
-}
-
 }  // namespace
 
-template <int NCOL>
+template <int NCOL, bool FP8>
 cudaError_t prepare_one() {
-    return cudaFuncSetAttribute(latent_decode_kernel<NCOL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(Layout<NCOL>::kBytes));
+    return cudaFuncSetAttribute(latent_decode_kernel<NCOL, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Layout<NCOL, FP8>::kBytes));
 }
 
 cudaError_t latent_decode_prepare_device() {
-    cudaError_t e = prepare_one<16>();
-    if (e == cudaSuccess) e = prepare_one<32>();
-    if (e == cudaSuccess) e = prepare_one<64>();
+    cudaError_t e = prepare_one<16, false>();
+    if (e == cudaSuccess) e = prepare_one<32, false>();
+    if (e == cudaSuccess) e = prepare_one<64, false>();
+    if (e == cudaSuccess) e = prepare_one<16, true>();
+    if (e == cudaSuccess) e = prepare_one<32, true>();
+    if (e == cudaSuccess) e = prepare_one<64, true>();
     return e;
 }
 
-template <int NCOL>
-cudaError_t launch_one(const CUtensorMap &kvmap, const LatentDecodeParams &p, cudaStream_t stream) {
-    return launch_pdl(latent_decode_kernel<NCOL>, dim3(p.ranges * p.col_tiles), dim3(kThreads), Layout<NCOL>::kBytes, stream,
-                      kvmap, p);
+template <int NCOL, bool FP8>
+cudaError_t launch_one(const LatentDecodeMaps &maps, const LatentDecodeParams &p, cudaStream_t stream) {
+    return launch_pdl(latent_decode_kernel<NCOL, FP8>, dim3(p.ranges * p.col_tiles), dim3(kThreads),
+                      Layout<NCOL, FP8>::kBytes, stream, maps.kv, maps.rope, p);
 }
 
-cudaError_t launch_latent_decode(const CUtensorMap &kvmap, const LatentDecodeParams &p, bool fp8, cudaStream_t stream) {
-    if (fp8) {
-        const int64_t units = static_cast<int64_t>(p.num_seqs) * p.q_per_seq * p.heads;
-        const dim3 grid(static_cast<unsigned>((units + 3) / 4));
-        return launch_pdl(latent_decode_simple_kernel<true>, grid, dim3(128), 0, stream, p);
-    }
-    cudaError_t e = p.cols_per_tile <= 16   ? launch_one<16>(kvmap, p, stream)
-                    : p.cols_per_tile <= 32 ? launch_one<32>(kvmap, p, stream)
-                                            : launch_one<64>(kvmap, p, stream);
+template <bool FP8>
+cudaError_t launch_cols(const LatentDecodeMaps &maps, const LatentDecodeParams &p, cudaStream_t stream) {
+    return p.cols_per_tile <= 16   ? launch_one<16, FP8>(maps, p, stream)
+           : p.cols_per_tile <= 32 ? launch_one<32, FP8>(maps, p, stream)
+                                   : launch_one<64, FP8>(maps, p, stream);
+}
+
+cudaError_t launch_latent_decode(const LatentDecodeMaps &maps, const LatentDecodeParams &p, bool fp8, cudaStream_t stream) {
+    const cudaError_t e = fp8 ? launch_cols<true>(maps, p, stream) : launch_cols<false>(maps, p, stream);
     if (e != cudaSuccess || p.ranges <= 1) return e;
     // Few sequences over many ranges have many parts each: then four warps share a column's dims.
     const int split = std::min(p.num_seqs, p.ranges - 1), x = (p.heads * p.q_per_seq + kMergeWarps - 1) / kMergeWarps;

@@ -112,9 +112,13 @@ def decode(q_latent, q_rope, pool, q_per_seq, skip_blocks=()):
             o, size = attend(q[r], s, s[:, :LATENT], torch.full((heads,), seen))
             out[r] = o
             tol[r] = size * weight_error(q[r], s, pool.fp8)
-            if pool.fp8:  # weights below the smallest E4M3 step of a pair: 2^-18 of the largest, off at most by it
-                top = s[:, :LATENT].abs().sum(0) * 2.0 ** -17
-                tol[r] += top[None]
+            if pool.fp8:
+                # The weights that multiply the codes, w_j s_j, are pairs of E4M3 codes in which the largest is at
+                # least 2^4 and the smallest step is 2^-9: each is off by up to 2^-10 / 2^4 of the largest.
+                scale = s[:, :LATENT].abs().amax(1) / 448  # of a row that quantise() made: exact to rounding
+                w = torch.softmax((q[r] @ s.T) * SCALE, -1)
+                codes = (s[:, :LATENT].abs() / scale.clamp(min=1e-300)[:, None]).sum(0)
+                tol[r] += (w * scale).amax(-1)[:, None] * 2.0 ** -14 * 1.01 * codes[None]
     return out, tol
 
 
@@ -122,11 +126,12 @@ def weight_error(q, keys, fp8=False):
     """Relative error of a row's softmax weights, numerator and sum: each weight rounded to bf16
     (over an FP8 pool: to a pair of E4M3 codes) 2^-8, twice; exponentials 2^-12; scores
     accumulated in fp32 over n products, n 2^-24 of the sum of their sizes, twice; over an
-    FP8 pool the query held as a pair of E4M3 codes, 2^-18 of its largest value."""
+    FP8 pool the query held as a pair of E4M3 codes, the largest above 224, in steps of 2^-9:
+    2^-10 / 224 of its largest value."""
     size = SCALE * (q.abs() @ keys.abs().T).amax(-1)
     score = q.shape[-1] * 2.0 ** -24 * size
     if fp8:
-        score = score + SCALE * 2.0 ** -18 * q[:, :LATENT].abs().amax(-1) * keys[:, :LATENT].abs().sum(-1).max()
+        score = score + SCALE * 2.0 ** -10 / 224 * q[:, :LATENT].abs().amax(-1) * keys[:, :LATENT].abs().sum(-1).max()
     return (2 * 2.0 ** -8 + 2.0 ** -12 + 2 * score)[:, None]
 
 
