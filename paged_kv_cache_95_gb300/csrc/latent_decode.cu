@@ -18,7 +18,7 @@
 //  * half of the blocks are copied by TMA, half by cp.async: one SM's TMA unit delivers 24
 //    bytes a clock however much is in flight (measured, from L2 as from HBM), both paths
 //    together 47; HBM's share of an SM is 23-28, so a ring on TMA alone never catches up.
-//  * softmax by 8 warps (a warp: 16 rows, half of the keys): running reference m,
+//  * softmax by 8 warps (a warp: a quarter of the columns, half of the keys): running reference m,
 //    raised only when a score passes it by 2^8 (one vote a tile), sum l in fp32;
 //    P = 2^(s - m) rounded to bf16 (l adds the rounded weights, so numerator and
 //    denominator round alike) into shared memory as the B operand.
@@ -69,16 +69,19 @@ struct Layout {
     static constexpr uint32_t kBlock = 2 * kGroup;
     static constexpr uint32_t kRopeBlock = FP8 ? kBlockSize * 128 : 0;
     static constexpr uint32_t kStage = kTileBlocks * (kBlock + kRopeBlock);
-    static constexpr int kStages = FP8 ? (NCOL == 64 ? 3 : 4) : 2;
+    static constexpr int kStages = FP8 ? 3 : 2;
+    // M = 64: rows 16 q .. 16 q + 15 of S lie in tensor-memory lanes 32 q .., which only warps w % 4 = q reach, one
+    // scheduler's.  A quarter of the columns goes to each: column c is row 16 (c / kPerQuarter) + c % kPerQuarter.
+    static constexpr int kPerQuarter = NCOL / 4, kRowsPerThread = NCOL == 64 ? 2 : 1;
     // Score columns of a tile (FP8: the latent's and the rotated key's products apart, the scale goes with the first).
     static constexpr uint32_t kScoreCols = FP8 ? 128 : 64;
-    // Q: [9 chunks][NCOL][128 B]; FP8: 4 chunks of heads, 4 of remainders (E4M3), the rotated part in bf16.  It lies
-    // first: M = 64 reads up to 64 rows a chunk, past a smaller Q into the ring.
+    // Q: [9 chunks][64 rows][128 B]; FP8: 4 chunks of heads, 4 of remainders (E4M3), the rotated part in bf16.
+    static constexpr uint32_t kQChunk = 64 * 128;
     static constexpr uint32_t kQ = 0;
-    static constexpr uint32_t kKv = kQ + NCOL * 9 * 128;
+    static constexpr uint32_t kKv = kQ + 9 * kQChunk;
     static constexpr uint32_t kP = kKv + kStages * kStage;  // [NCOL][64 bf16], or [NCOL][64 heads | 64 remainders]
-    static constexpr uint32_t kScale = kP + NCOL * 128;     // FP8: [stage][64] scales of the keys
-    static constexpr uint32_t kQf = kScale + (FP8 ? kStages * kTile * 4 : 0);  // FP8: [64] factors of the rows of Q
+    static constexpr uint32_t kScale = kP + NCOL * 128;     // FP8: [stage][scale, its log2, its inverse][64 keys]
+    static constexpr uint32_t kQf = kScale + (FP8 ? kStages * 3 * kTile * 4 : 0);  // FP8: [64] factors of the columns
     // kv_full[stage], kv_empty[stage][block], s_full[2], s_empty[2], p_full, pv_done, q_full
     static constexpr int kBarKvFull = 0, kBarKvEmpty = kStages, kBarSFull = kBarKvEmpty + kStages * kTileBlocks,
                          kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 2, kBarPvDone = kBarPFull + 1,
@@ -94,8 +97,9 @@ struct Layout {
     static_assert(kKv % 1024 == 0 && kP % 1024 == 0 && kStage % 1024 == 0, "swizzle atoms");
     static_assert(kScale % 16 == 0 && kBar % 8 == 0 && kPlan % 8 == 0, "alignment");
     // A weight may pass the reference by 2^kRaise before the reference follows.  FP8 keeps the weights as pairs of
-    // E4M3 codes: 2^4 at the reference, so 2^8 at most (448 is the largest code) and steps of 2^-9 below.
-    static constexpr float kRaise = FP8 ? 4.f : 8.f, kLift = FP8 ? 4.f : 0.f;
+    // E4M3 codes: 2^2 at the reference, so 2^8 at most (448 is the largest code) and steps of 2^-9 below.  (2^4 and
+    // 2^4: on the verify of 64 columns a reference was raised in every second tile, 1900 cycles each.)
+    static constexpr float kRaise = FP8 ? 6.f : 8.f, kLift = FP8 ? 2.f : 0.f;
 };
 
 // Instruction descriptor: D f32; A and B bf16 (kind::f16) or E4M3 (kind::f8f6f4).
@@ -134,6 +138,14 @@ __device__ __forceinline__ int tiles_of(const LatentDecodeParams &p, int b) {
     return (keys_of(p, b) + kTile - 1) / kTile;
 }
 
+// The line of tiles that the ranges cut: every sequence with keys counts kLead tiles more, at its start --
+// what beginning another sequence costs a range (its Q, the epilogue of the one before).
+constexpr int kLead = 2;
+__device__ __forceinline__ int cost_of(const LatentDecodeParams &p, int b) {
+    const int t = tiles_of(p, b);
+    return t > 0 ? t + kLead : 0;
+}
+
 // A walk over the tiles of a range.
 struct Walk {
     int b, t, keys, nt;  // tile t of the nt tiles of sequence b
@@ -167,7 +179,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&kvmap);
         if (FP8) prefetch_tensormap(&ropemap);
     }
-    griddep_launch_dependents();
     if (sbase & 1023u) {  // operands need the 1 KB swizzle alignment
         if (tid == 0) atomicOr(p.status, kStatusTimeout);
         return;
@@ -176,11 +187,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + L::kAbort);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kTmemSlot);
     int64_t *plan = reinterpret_cast<int64_t *>(smem + L::kPlan);
+    unsigned long long *first_tile = reinterpret_cast<unsigned long long *>(plan + 16), *tile_count = first_tile + 1;
     if (tid == 0) {
         for (int i = 0; i < L::kNumBars; ++i)
             mbar_init(bar(i), i < L::kBarKvEmpty ? kTmaBlocks + 2
                               : i == L::kBarSEmpty || i == L::kBarSEmpty + 1 || i == L::kBarPFull || i == L::kBarQFull ? kSoftWarps : 1);
         *abort_flag = 0u;
+        *first_tile = ~0ull;
+        *tile_count = 0;
         fence_mbar_init();
     }
     if (warp == kScoreWarp) {  // (no other kernel's CTA waits for ours: the columns come free)
@@ -193,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int seg = (p.num_seqs + kThreads - 1) / kThreads;
     const int b_lo = min(p.num_seqs, tid * seg), b_hi = min(p.num_seqs, b_lo + seg);
     int64_t mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += tiles_of(p, b);
+    for (int b = b_lo; b < b_hi; ++b) mine += cost_of(p, b);
     int64_t upto = mine;  // inclusive prefix
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -209,21 +223,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         total += plan[w];
     }
     upto += before;
-    const int64_t ranges = min(static_cast<int64_t>(p.ranges), total);  // no range is empty
+    const int64_t ranges = min(static_cast<int64_t>(p.ranges), total);
     auto cut = [&](int r) -> int64_t {  // r total / ranges (64-bit division only where 32 bits do not hold it)
         if (r > ranges || ranges == 0) return 0;
         if (total < (1 << 24)) return static_cast<uint32_t>(r) * static_cast<uint32_t>(total) / static_cast<uint32_t>(ranges);
         return r * total / ranges;
     };
     const int64_t start = range < ranges ? cut(range) : 0, stop = range < ranges ? cut(range + 1) : 0;
-    const int n = static_cast<int>(stop - start);
-    if (n > 0 && upto - mine <= start && start < upto) {
+    // The tiles in [start, stop), by the threads whose sequences lie there (a range may hold none, when it falls
+    // into a lead): how many, and the first one.
+    int64_t tiles = 0;
+    if (upto - mine < stop && start < upto) {
         int64_t acc = upto - mine;
-        int b = b_lo;
-        for (; acc + tiles_of(p, b) <= start; ++b) acc += tiles_of(p, b);
-        plan[16] = b;
-        plan[17] = start - acc;
+        for (int b = b_lo; b < b_hi && acc < stop; ++b) {
+            const int t = tiles_of(p, b);
+            if (t == 0) continue;
+            const int64_t lo = max(static_cast<int64_t>(0), start - acc - kLead);
+            const int64_t hi = min(static_cast<int64_t>(t), stop - acc - kLead);
+            if (hi > lo) {
+                tiles += hi - lo;
+                atomicMin(first_tile, (static_cast<unsigned long long>(b) << 32) | lo);
+            }
+            acc += t + kLead;
+        }
     }
+    if (tiles > 0) atomicAdd(tile_count, static_cast<unsigned long long>(tiles));
     // Sequences without keys get zero rows, and every length is checked, shared out over the ranges.
     auto empty_sequences = [&](int thread, int threads) {
         for (int b = range; b < p.num_seqs; b += p.ranges) {
@@ -243,15 +267,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    const int n = static_cast<int>(*tile_count);
+    const int b0 = static_cast<int>(*first_tile >> 32), t0 = static_cast<int>(*first_tile & 0xffffffffu);
     // The merge kernel's record of this range: its first sequence, and whether it starts inside it.
-    if (tid == 0 && ct == 0) p.record[range] = n > 0 ? make_int2(static_cast<int>(plan[16]), plan[17] > 0) : make_int2(-1, 0);
+    if (tid == 0 && ct == 0) p.record[range] = n > 0 ? make_int2(b0, t0 > 0) : make_int2(-1, 0);
     const uint32_t tmem = *tmem_slot;
     if (n == 0) {
         empty_sequences(tid, kThreads);
         if (warp == kScoreWarp) tmem_dealloc(tmem, kTmemCols);
         return;
     }
-    const int b0 = static_cast<int>(plan[16]), t0 = static_cast<int>(plan[17]);
 
     // A warp's bounded wait; it gives up soon after another role did.  The timer and the flag are
     // read only every 64 tries: a read of %globaltimer between two tries delays the waiter by
@@ -296,14 +321,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (i >= kStages) ok = ok && warp_wait(bar(L::kBarKvEmpty + st * kTileBlocks + j), ((i / kStages) - 1) & 1);
                 if (ok && lane == j) {
                     const uint32_t full = bar(L::kBarKvFull + st), stage = sbase + L::kKv + st * L::kStage;
-                    mbar_arrive_expect_tx(full, cur >= 0 ? L::kBlock + L::kRopeBlock + (FP8 ? kBlockSize * 4 : 0) : 0);
+                    mbar_arrive_expect_tx(full, cur >= 0 ? L::kBlock + L::kRopeBlock : 0);
                     if (cur >= 0) {
                         tma_load_5d(stage + j * L::kBlock, &kvmap, full, 0, 0, 0, 0, cur);
-                        if constexpr (FP8) {
+                        if constexpr (FP8)
                             tma_load_3d(stage + kTileBlocks * L::kBlock + j * L::kRopeBlock, &ropemap, full, 0, 0, cur);
-                            bulk_copy_g2s(sbase + L::kScale + (st * kTile + j * kBlockSize) * 4,
-                                          p.cache_scale + static_cast<size_t>(cur) * kBlockSize, kBlockSize * 4, full);
-                        }
                     }
                 }
             }
@@ -352,13 +374,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               (((t & 7) ^ (t >> 3)) << 4);
                         cp_async_16(rdst, rope);
                         cp_async_16(rdst + 1024, rope + 1024);
-                        if (t < 4)
-                            cp_async_16(sbase + L::kScale + (st * kTile + j * kBlockSize + 4 * t) * 4,
-                                        p.cache_scale + static_cast<size_t>(blk) * kBlockSize + 4 * t);
                     }
                 }
             }
             if (!ok) break;
+            if constexpr (FP8) {
+                // Key t's scale, once for all columns (the stage's last reader, softmax, is behind every one of its
+                // blocks' P V): 1 for a slot without a key, whose scale may be anything.
+                const int blk = __shfl_sync(0xffffffffu, id, t >> 4), key = w.t * kTile + t;
+                const float sc = blk >= 0 && key < w.keys ? __ldg(p.cache_scale + static_cast<size_t>(blk) * kBlockSize + (t & 15)) : 1.f;
+                float *at = reinterpret_cast<float *>(smem + L::kScale) + st * 3 * kTile + t;
+                at[0] = sc;
+                at[kTile] = __log2f(sc);
+                at[2 * kTile] = __fdividef(1.f, sc);
+            }
             for (int k = 0; k < 2 && i + 1 + k < n; ++k) w.next(p);
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();  // generic writes -> the tensor core
@@ -393,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < 9; ++c)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t qd = q_desc + ((c * NCOL * 128 + kk * 32) >> 4);
+                        const uint64_t qd = q_desc + ((c * L::kQChunk + kk * 32) >> 4);
                         if constexpr (!FP8)
                             umma_bf16(d, qd, kd + ((c * 1024 + kk * 32) >> 4), idesc(64, kTile, false), c + kk > 0);
                         else if (c < 8)  // heads, then remainders, against the same codes
@@ -449,18 +478,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---------------- softmax, rescaling and epilogue: 8 warps ----------------
         const int quarter = warp & 3, half = warp >> 2;
-        // M = 64: rows 16 q .. of S lie in lanes 32 q .. +15.  The 16-lane load spreads them over the
-        // warp: a thread holds rows r and r + 8, of each 8 keys of every 32 (columns 8 j + 2 (lane % 4) + 0, 1).
-        const int row = quarter * 16 + (lane >> 2);
-        const bool warp_has = quarter * 16 < NCOL;
-        const bool has = warp_has && (lane & 3) == 0;    // speaks for rows r and r + 8
+        // The 16-lane load spreads a quarter's rows over the warp: a thread holds rows lane / 4 and (64 columns)
+        // lane / 4 + 8 of it, of each 8 keys of every 32 (columns 8 j + 2 (lane % 4) + 0, 1).
+        constexpr int kR = L::kRowsPerThread;
+        const int col0 = quarter * L::kPerQuarter + (lane >> 2);  // the column of row k is col0 + 8 k
+        const bool live = (lane >> 2) < L::kPerQuarter;
+        const bool has = live && (lane & 3) == 0;  // speaks for its columns
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        int q_row[2];
+        int q_row[kR];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) q_row[k] = row + 8 * k < nc ? (c0 + row + 8 * k) / p.heads : p.q_per_seq - 1;
-        // P goes out as 8 x 8 matrices: this lane addresses row lane % 16 and 16-byte chunk 4 half + lane / 16 (+2).
-        const int p_row = quarter * 16 + (lane & 15);
-        const uint32_t p_at = sbase + L::kP + p_row * 128;
+        for (int k = 0; k < kR; ++k) q_row[k] = col0 + 8 * k < nc ? (c0 + col0 + 8 * k) / p.heads : p.q_per_seq - 1;
+        // P: where this thread's pair of keys of 8-key group j goes, p_at[.] (+ 1024 for row k = 1).  bf16: a pair is 4
+        // bytes, group j the 16-byte chunk 4 half + j.  FP8: 2 bytes, chunk 2 half + j / 2, remainders 64 bytes on.
+        auto p_at = [&](int j) {
+            const int v = FP8 ? 2 * half + (j >> 1) : 4 * half + j;
+            return sbase + L::kP + col0 * 128 + ((v ^ (col0 & 7)) << 4) + (FP8 ? 8 * (j & 1) + 2 * (lane & 3) : 4 * (lane & 3));
+        };
         float *xch = reinterpret_cast<float *>(smem + L::kXch);
         float *alpha_s = reinterpret_cast<float *>(smem + L::kAlpha);
         auto soft_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); };
@@ -474,11 +507,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto load_q = [&](int b) {
 #pragma unroll FP8 ? 4 : 1
             for (int r = warp; r < NCOL; r += kSoftWarps) {
+                const int rq = r / L::kPerQuarter * 16 + r % L::kPerQuarter;
                 const int c = c0 + r, i = c / p.heads;
                 const int64_t qr = static_cast<int64_t>(b) * p.q_per_seq + i, h = c - i * p.heads;
                 const uint16_t *ql = static_cast<const uint16_t *>(p.q_latent) + qr * p.ql_row + h * p.ql_head;
                 const uint16_t *qp = static_cast<const uint16_t *>(p.q_rope) + qr * p.qr_row + h * p.qr_head;
-                auto at = [&](int chunk, int v) { return sbase + L::kQ + chunk * (NCOL * 128) + r * 128 + ((v ^ (r & 7)) << 4); };
+                auto at = [&](int chunk, int v) { return sbase + L::kQ + chunk * L::kQChunk + rq * 128 + ((v ^ (rq & 7)) << 4); };
                 if constexpr (!FP8) {
 #pragma unroll
                     for (int k = 0; k < 3; ++k) {
@@ -542,79 +576,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         empty_sequences(tid, kSoftThreads);
         publish_q();
         if constexpr (FP8) soft_sync();  // the factors of Q's rows are written
-        float q_scale[2] = {0.f, 0.f};   // FP8: those of rows r and r + 8, times the softmax scale
-        float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float q_scale[kR] = {};          // FP8: those of this thread's columns, times the softmax scale
+        float m_ref[kR];
+        float2 l[kR];
+        auto block_id = [&](const Walk &a) {  // lane j: the id of block j of a tile (0 past the context)
+            const int jb = a.t * kTileBlocks + lane;
+            return lane < kTileBlocks && jb * kBlockSize < a.keys
+                       ? __ldg(p.block_tables + static_cast<size_t>(a.b) * p.max_blocks + jb)
+                       : 0;
+        };
+        int id = block_id(w);     // read a tile ahead: S may be waiting already
         bool piece_mid = t0 > 0;  // the piece does not hold its sequence's first key
         for (int i = 0; i < n; ++i) {
             const bool first = i == 0 || w.t == 0;
             const bool last = i == n - 1 || w.t == w.nt - 1;
             if (first) {
-                m_ref[0] = m_ref[1] = -INFINITY;
-                l[0] = l[1] = 0.f;
-            }
-            if (FP8 && warp_has && (i == 0 || w.t == 0)) {
-                q_scale[0] = qf_s[row] * p.scale_log2;
-                q_scale[1] = qf_s[row + 8] * p.scale_log2;
+#pragma unroll
+                for (int k = 0; k < kR; ++k) {
+                    m_ref[k] = -INFINITY;
+                    l[k] = make_float2(0.f, 0.f);
+                    if constexpr (FP8) q_scale[k] = live ? qf_s[col0 + 8 * k] * p.scale_log2 : 0.f;
+                }
             }
             // Blocks of the tile with an invalid id: flagged, their keys masked.
-            const int jb = w.t * kTileBlocks + lane;
-            const bool bad_lane =
-                lane < kTileBlocks && jb * kBlockSize < w.keys &&
-                static_cast<unsigned>(__ldg(p.block_tables + static_cast<size_t>(w.b) * p.max_blocks + jb)) >=
-                    static_cast<unsigned>(p.num_blocks);
-            const uint32_t bad = __ballot_sync(0xffffffffu, bad_lane);
+            const uint32_t bad = __ballot_sync(0xffffffffu, static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks));
             if (bad && tid == 0) atomicOr(p.status, kStatusBadBlockId);
             const int left = w.keys - w.t * kTile;  // keys of the tile that exist (may pass 64)
 
+            // FP8: c_j = code s_j, so the score is s_j <q, code_j> + <q_rope, r_j>, and the weight that multiplies the
+            // codes is s_j 2^score = 2^(score + log2 s_j); the sum l takes it times 1 / s_j.
+            if (FP8) alive = alive && warp_wait(bar(L::kBarKvFull + i % kStages), (i / kStages) & 1);  // (the scales)
+            const uint32_t sc_at = sbase + L::kScale + ((i % kStages) * 3 * kTile + 32 * half + 2 * (lane & 3)) * 4;
             alive = alive && warp_wait(bar(L::kBarSFull + (i & 1)), (i >> 1) & 1);
-            if (FP8) alive = alive && warp_wait(bar(L::kBarKvFull + i % kStages), (i / kStages) & 1);  // its scales
-            float x[16];  // [4 j + 2 k + e]: row r + 8 k, key 32 half + 8 j + 2 (lane % 4) + e
-            float inv_s[8];  // FP8: [2 j + e] 1 / scale of the key
-            float mx[2] = {-INFINITY, -INFINITY};
-            if (alive && warp_has) {
+            float2 x[kR][4];  // [k][j]: row k, keys 32 half + 8 j + 2 (lane % 4) + 0, 1
+            float mx[kR];
+#pragma unroll
+            for (int k = 0; k < kR; ++k) mx[k] = -INFINITY;
+            if (alive) {
                 tc_fence_after();
                 uint32_t v[16];
                 const uint32_t s_at = tmem + lanes + kTmemS + L::kScoreCols * (i & 1) + 32 * half;
-                tmem_ld_16x256b_x4(s_at, v);
+                const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
+                auto pair = [](const uint32_t(&r)[16], int j, int k) {
+                    return make_float2(__uint_as_float(r[4 * j + 2 * k]), __uint_as_float(r[4 * j + 2 * k + 1]));
+                };
                 if constexpr (!FP8) {
-                    tc_fence_before();
+                    tmem_ld_16x256b_x4(s_at, v);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[e]) * p.scale_log2;
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int k = 0; k < kR; ++k) x[k][j] = fmul2(pair(v, j, k), sl2);
                 } else {
-                    // c_j = code s_j: the score is s_j <q, code_j> + <q_rope, r_j>, and the weight that multiplies
-                    // the codes is s_j 2^score = 2^(score + log2 s_j); the sum l takes it without s_j.
                     uint32_t u[16];
-                    tmem_ld_16x256b_x4(s_at + 64, u);
-                    tc_fence_before();
-                    const uint32_t sc = sbase + L::kScale + ((i % kStages) * kTile + 32 * half + 2 * (lane & 3)) * 4;
+                    tmem_ld_16x256b_x4_pair(s_at, v, s_at + 64, u);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        float s2[2] = {lds_f32(sc + 32 * j), lds_f32(sc + 32 * j + 4)};
+                        const float2 sc = lds_f32x2(sc_at + 32 * j), lg = lds_f32x2(sc_at + kTile * 4 + 32 * j);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int key = 32 * half + 8 * j + 2 * (lane & 3) + e;
-                            if (key >= left || ((bad >> (key >> 4)) & 1u)) s2[e] = 1.f;  // whatever was there
-                            const float lg = __log2f(s2[e]);
-                            inv_s[2 * j + e] = __fdividef(1.f, s2[e]);
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                x[4 * j + 2 * k + e] = __uint_as_float(v[4 * j + 2 * k + e]) * (q_scale[k] * s2[e]) +
-                                                       (__uint_as_float(u[4 * j + 2 * k + e]) * p.scale_log2 + lg);
-                        }
+                        for (int k = 0; k < kR; ++k)
+                            x[k][j] = ffma2(pair(v, j, k), fmul2(sc, make_float2(q_scale[k], q_scale[k])),
+                                            ffma2(pair(u, j, k), sl2, lg));
                     }
                 }
+                tc_fence_before();
                 // Row q_row sees keys up to keys - q_per_seq + q_row; bad blocks see none.
                 if (left - p.q_per_seq + 1 < kTile || bad) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int k = (e >> 1) & 1, key = 32 * half + 8 * (e >> 2) + 2 * (lane & 3) + (e & 1);
-                        if (key > left - p.q_per_seq + q_row[k] || ((bad >> (key >> 4)) & 1u)) x[e] = -INFINITY;
-                    }
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int k = 0; k < kR; ++k) {
+                            const int key = 32 * half + 8 * j + 2 * (lane & 3), end = left - p.q_per_seq + q_row[k];
+                            const bool hide = (bad >> (key >> 4)) & 1u;
+                            if (hide || key > end) x[k][j].x = -INFINITY;
+                            if (hide || key + 1 > end) x[k][j].y = -INFINITY;
+                        }
                 }
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < kR; ++k) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mx[k] = fmax3(mx[k], x[4 * j + 2 * k], x[4 * j + 2 * k + 1]);
+                    for (int j = 0; j < 4; ++j) mx[k] = fmax3(mx[k], x[k][j].x, x[k][j].y);
                     mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
                     mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
                 }
@@ -624,27 +664,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             // The last S of a piece is complete: its Q can make way for the next sequence's.
             const bool more = last && i + 1 < n;
             Walk nx = w;
-            if (i + 1 < n) nx.next(p);
+            if (i + 1 < n) {
+                nx.next(p);
+                id = block_id(nx);
+            }
             if (more && alive) load_q(nx.b);
 
             float *xm = xch + (i & 1) * 128;
-            if (has) {
-                xm[half * 64 + row] = mx[0];
-                xm[half * 64 + row + 8] = mx[1];
+            bool pass = false;
+#pragma unroll
+            for (int k = 0; k < kR; ++k) {
+                if (has) xm[half * 64 + col0 + 8 * k] = mx[k];
+                pass = pass || (live && mx[k] > m_ref[k] + L::kRaise);
             }
             bool drained = false;  // this warp saw P V (i - 1) complete
-            if (bar_red_or(1, kSoftThreads, warp_has && (mx[0] > m_ref[0] + L::kRaise || mx[1] > m_ref[1] + L::kRaise))) {
-                if (warp_has) {
+            if (bar_red_or(1, kSoftThreads, pass)) {
+                if (live) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < kR; ++k) {
                         float alpha = 1.f;
-                        const float mt = fmaxf(xm[row + 8 * k], xm[64 + row + 8 * k]);
+                        const float mt = fmaxf(xm[col0 + 8 * k], xm[64 + col0 + 8 * k]);
                         if (mt > m_ref[k] + L::kRaise) {
                             alpha = fast_exp2(m_ref[k] - mt);  // 0 from -inf
                             m_ref[k] = mt;
-                            l[k] *= alpha;
+                            l[k] = fmul2(l[k], make_float2(alpha, alpha));
                         }
-                        if (has && half == 0) alpha_s[row + 8 * k] = alpha;
+                        if (has && half == 0) alpha_s[col0 + 8 * k] = alpha;
                     }
                 }
                 if (!first) {  // (the first P V of a piece overwrites O)
@@ -667,46 +712,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // Weights, rounded to bf16 (relative 2^-8; l adds what P V will read), or to a pair of E4M3 codes
-            // (relative 2^-8, steps of 2^-9 where the largest is at least 2^4).
-            uint32_t pk[8];  // [2 j + k]: the pair of row r + 8 k in 8-key group j
-            if (warp_has) {
+            // Weights, rounded to bf16 (relative 2^-8; l adds what P V will read), or to a pair of E4M3 codes by way
+            // of fp16 (2^-11; the pair holds relative 2^-8, in steps of 2^-9 where the largest is at least 2^2).
+            uint32_t pk[kR][4];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float mu = m_ref[k] == -INFINITY ? 0.f : m_ref[k] - L::kLift;
+            for (int k = 0; k < kR; ++k) {
+                const float mu = m_ref[k] == -INFINITY ? 0.f : m_ref[k] - L::kLift;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if constexpr (FP8) {
-                            const float w0 = fast_exp2(x[4 * j + 2 * k] - mu), w1 = fast_exp2(x[4 * j + 2 * k + 1] - mu);
-                            l[k] += w0 * inv_s[2 * j] + w1 * inv_s[2 * j + 1];
-                            const uint32_t hi = f32x2_to_e4m3x2(w0, w1);
-                            const float2 f = unpack_f16x2(e4m3x2_to_f16x2(hi));
-                            pk[2 * j + k] = hi | f32x2_to_e4m3x2(w0 - f.x, w1 - f.y) << 16;
-                            continue;
-                        }
-                        const uint32_t w2 = pack_bf16x2(fast_exp2(x[4 * j + 2 * k] - mu), fast_exp2(x[4 * j + 2 * k + 1] - mu));
-                        l[k] += __uint_as_float(w2 << 16) + __uint_as_float(w2 & 0xffff0000u);
-                        pk[2 * j + k] = w2;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 y = fadd2(x[k][j], make_float2(-mu, -mu));
+                    const float2 w2 = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                    if constexpr (FP8) {
+                        l[k] = ffma2(w2, lds_f32x2(sc_at + 2 * kTile * 4 + 32 * j), l[k]);
+                        pk[k][j] = e4m3_head_and_rest(pack_f16x2(w2.x, w2.y));
+                    } else {
+                        pk[k][j] = pack_bf16x2(w2.x, w2.y);
+                        l[k] = fadd2(l[k], make_float2(bf16_lo(pk[k][j]), bf16_hi(pk[k][j])));
                     }
                 }
             }
             if (i > 0 && !drained) alive = alive && warp_wait(bar(L::kBarPvDone), (i - 1) & 1);  // P is free again
             if (alive) {
-                if (FP8 && warp_has) {  // two keys of a row: 2 bytes of heads, 2 of remainders 64 bytes on
+                if (live) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int r = row + 8 * k, v = 2 * half + (j >> 1);
-                            const uint32_t at = sbase + L::kP + r * 128 + 8 * (j & 1) + 2 * (lane & 3);
-                            sts16(at + ((v ^ (r & 7)) << 4), pk[2 * j + k]);
-                            sts16(at + (((v + 4) ^ (r & 7)) << 4), pk[2 * j + k] >> 16);
+                        for (int k = 0; k < kR; ++k) {
+                            const uint32_t at = p_at(j) + 1024 * k;
+                            if constexpr (FP8) {
+                                sts16(at, pk[k][j]);
+                                sts16(at ^ 64u, pk[k][j] >> 16);
+                            } else {
+                                sts32(at, pk[k][j]);
+                            }
                         }
-                } else if (warp_has) {
-#pragma unroll
-                    for (int j = 0; j < 4; j += 2)
-                        stmatrix_x4(p_at + (((4 * half + j + (lane >> 4)) ^ (p_row & 7)) << 4), pk[2 * j], pk[2 * j + 1],
-                                    pk[2 * j + 2], pk[2 * j + 3]);
                 }
                 // Rows that no key fills (past the context, of an invalid block) hold whatever was there:
                 // their weights are 0, their values have to be finite.
@@ -731,16 +770,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (last) {
                 // ---- the piece's columns: whole sequences to out, parts to the workspace ----
                 const bool whole = !piece_mid && w.t == w.nt - 1;
+                // (The merge's CTAs come now, when the SMs empty: launched at the start they crowd onto the first that do.)
+                if (i == n - 1) griddep_launch_dependents();
                 // Slot 0: the range's first piece when it starts inside its sequence; else slot 1.
                 const size_t slot = (static_cast<size_t>(range) * 2 + (piece_mid ? 0 : 1)) * (p.col_tiles * p.cols_per_tile) + c0;
                 soft_sync();  // the maxima have been read
-                if (warp_has) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
-                        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
-                        if (has) xch[half * 64 + row + 8 * k] = l[k];
-                    }
+                for (int k = 0; k < kR; ++k) {
+                    float sum = l[k].x + l[k].y;
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    if (has) xch[half * 64 + col0 + 8 * k] = sum;
                 }
                 soft_sync();
                 if (tid < NCOL) alpha_s[tid] = [&] {
@@ -749,8 +789,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }();
                 if (!whole && has && half == 0) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int r = row + 8 * k;
+                    for (int k = 0; k < kR; ++k) {
+                        const int r = col0 + 8 * k;
                         if (r < nc) p.part_ml[slot + r] = make_float2(m_ref[k], xch[r] + xch[64 + r]);
                     }
                 }
@@ -820,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the ranges from there on.  Two round trips to L2: the records, then everything else.
 constexpr int kMergeWarps = 8;
 constexpr int kRecords = kLatentMaxRanges / 32;
-template <int STEPS>  // of 32 lanes x 4 dims; batches of 16 / STEPS parts
+template <int STEPS>  // of 32 lanes x 4 dims; batches of 8 / STEPS parts (every warp of a call resident at once)
 __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const LatentDecodeParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * kMergeWarps + warp;
@@ -860,7 +900,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const La
     const size_t part0 = (static_cast<size_t>(first - 1) * 2 + 1) * padded + col;
     const size_t part1 = static_cast<size_t>(first) * 2 * padded + col;
     auto slot = [&](int k) { return k == 0 ? part0 : part1 + static_cast<size_t>(k - 1) * 2 * padded; };
-    constexpr int kBatch = 16 / STEPS;
+    constexpr int kBatch = 8 / STEPS;
     float4 v[kBatch][STEPS], o[STEPS];
     const int lane4 = blockIdx.z * STEPS * 32 + lane;
     auto load = [&](int j) {

@@ -136,13 +136,6 @@ constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3
 constexpr uint32_t kIdescQK = kIdescBase;               // A K-major, B K-major
 constexpr uint32_t kIdescPV = kIdescBase | (1u << 16);  // B MN-major
 
-// Two fp32 values from shared memory.
-__device__ __forceinline__ float2 lds_f32x2(uint32_t addr) {
-    float2 r;
-    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(addr));
-    return r;
-}
-
 // Sixteen E4M3 codes (dims d .. d + 15) to bf16 (exact: E4M3 values are bf16
 // values): w0 holds dims d .. d + 7, w1 dims d + 8 .. d + 15.
 __device__ __forceinline__ void e4m3x16_to_bf16(const uint4 &c, uint4 &w0, uint4 &w1) {

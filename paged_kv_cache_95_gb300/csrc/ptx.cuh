@@ -179,6 +179,11 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                  : "memory");
 }
 
+// 4-byte shared-memory store.
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // 2-byte shared-memory store of the low half of v.
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t v) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(v)) : "memory");
@@ -195,6 +200,13 @@ __device__ __forceinline__ float lds_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
     return v;
+}
+
+// Two fp32 values from shared memory.
+__device__ __forceinline__ float2 lds_f32x2(uint32_t addr) {
+    float2 r;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(addr));
+    return r;
 }
 
 // Two E4M3 codes (low byte = first element) -> packed f16x2, exactly (every
@@ -219,6 +231,20 @@ __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t four_codes, uint32_t 
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two fp16 values -> their E4M3 codes (nearest even, low 16 bits) and the codes of what they leave (high 16 bits).
+__device__ __forceinline__ uint32_t e4m3_head_and_rest(uint32_t f16x2) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 f, d;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 h, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 f, h;\n\t"
+        "sub.f16x2 d, %1, f;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 l, d;\n\t"
+        "mov.b32 %0, {h, l};\n\t}"
+        : "=r"(r)
+        : "r"(f16x2));
     return r;
 }
 
@@ -438,12 +464,20 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
         : "memory");
 }
 
-// Four 8 x 8 matrices of 16-bit values to shared memory: matrix m (register m, the accumulator
-// layout) to the rows that lanes 8 m .. 8 m + 7 address.
-__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-                 "r"(d)
-                 : "memory");
+// Two of them under one wait.
+__device__ __forceinline__ void tmem_ld_16x256b_x4_pair(uint32_t ta, uint32_t (&r)[16], uint32_t tb, uint32_t (&q)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
+          "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
+          "=&r"(q[0]), "=&r"(q[1]), "=&r"(q[2]), "=&r"(q[3]), "=&r"(q[4]), "=&r"(q[5]), "=&r"(q[6]), "=&r"(q[7]),
+          "=&r"(q[8]), "=&r"(q[9]), "=&r"(q[10]), "=&r"(q[11]), "=&r"(q[12]), "=&r"(q[13]), "=&r"(q[14]), "=&r"(q[15])
+        : "r"(ta), "r"(tb)
+        : "memory");
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }

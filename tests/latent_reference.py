@@ -114,11 +114,11 @@ def decode(q_latent, q_rope, pool, q_per_seq, skip_blocks=()):
             tol[r] = size * weight_error(q[r], s, pool.fp8)
             if pool.fp8:
                 # The weights that multiply the codes, w_j s_j, are pairs of E4M3 codes in which the largest is at
-                # least 2^4 and the smallest step is 2^-9: each is off by up to 2^-10 / 2^4 of the largest.
+                # least 2^2 and the smallest step is 2^-9: each is off by up to 2^-10 / 2^2 of the largest.
                 scale = s[:, :LATENT].abs().amax(1) / 448  # of a row that quantise() made: exact to rounding
                 w = torch.softmax((q[r] @ s.T) * SCALE, -1)
                 codes = (s[:, :LATENT].abs() / scale.clamp(min=1e-300)[:, None]).sum(0)
-                tol[r] += (w * scale).amax(-1)[:, None] * 2.0 ** -14 * 1.01 * codes[None]
+                tol[r] += (w * scale).amax(-1)[:, None] * 2.0 ** -12 * 1.01 * codes[None]
     return out, tol
 
 

@@ -186,6 +186,19 @@ def test_verify(heads, k, fp8):
     assert status_of(ws) == 0
 
 
+@pytest.mark.parametrize("lens", [[64], [500, 300], [4000]])
+def test_decode_fp8_error_in_norm(lens):
+    """The elementwise bound adds every weight's worst step; the steps are independent, so in norm the
+    result is off by about one bf16 rounding of the weights (2^-8 / sqrt 3 of it and less): 4e-3 is
+    twice what the three roundings together come to."""
+    pool = R.Pool(3, lens, True)
+    q = queries(4, len(lens), 64)
+    out, _ = run_decode(pool, *q, 1)
+    ref, _ = R.decode(*q, pool, 1)
+    err = (out.cpu().double() - ref).norm(dim=-1) / ref.norm(dim=-1)
+    assert err.max() < 8e-3 and err.mean() < 4e-3, (err.max(), err.mean())
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_decode_bf16_output(fp8):
     pool = R.Pool(4, [300, 17, 1], fp8)
