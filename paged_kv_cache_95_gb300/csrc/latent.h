@@ -53,7 +53,7 @@ struct LatentDecodeParams {
     // The split: the q_per_seq x heads columns of a sequence in col_tiles tiles of cols_per_tile
     // (the last may hold fewer), the keys of all sequences in `ranges` ranges of tiles.
     int32_t col_tiles, cols_per_tile, ranges;
-    int2 *record;            // [ranges]: first sequence (-1: empty), 1 if the range starts inside it
+    int2 *record;            // [ranges]: the split sequence that begins in the range, and its parts (0: none)
     float2 *part_ml;         // [ranges][2][col_tiles * cols_per_tile] (m, l), log2 domain, scale folded in
     float *part_o;           // the same x [512], unnormalised
 };

@@ -201,6 +201,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
     }
+    // While the kernel before us drains: the lengths, tables and queries on their way into L2 (a prefetch reads
+    // nothing: what that kernel still writes to them is written there), each CTA a share.
+    {
+        const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + tid, all = static_cast<int64_t>(gridDim.x) * kThreads;
+        const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.q_per_seq * p.heads;
+        const int64_t tables = static_cast<int64_t>(p.num_seqs) * p.max_blocks;
+        if (id * 32 < p.num_seqs) prefetch_l2(p.context_lens + id * 32);
+        if (id * 32 < tables) prefetch_l2(p.block_tables + id * 32);
+        for (int64_t k = id; k < rows * 9 && k < 4 * all; k += all) {  // 8 lines of latent part and one of rotated a row
+            const int64_t r = k / 9, line = k - 9 * r, qr = r / p.heads, h = r - qr * p.heads;
+            prefetch_l2(line < 8 ? static_cast<const uint16_t *>(p.q_latent) + qr * p.ql_row + h * p.ql_head + line * 64
+                                 : static_cast<const uint16_t *>(p.q_rope) + qr * p.qr_row + h * p.qr_head);
+        }
+    }
     griddep_wait();  // the producers of q and of the cache before us on the stream
 
     // ---- the range: total tiles, then where tile `start` lies ----
@@ -269,8 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const int n = static_cast<int>(*tile_count);
     const int b0 = static_cast<int>(*first_tile >> 32), t0 = static_cast<int>(*first_tile & 0xffffffffu);
-    // The merge kernel's record of this range: its first sequence, and whether it starts inside it.
-    if (tid == 0 && ct == 0) p.record[range] = n > 0 ? make_int2(b0, t0 > 0) : make_int2(-1, 0);
+    if (tid == 0 && ct == 0) p.record[range] = make_int2(0, 0);  // (its last piece may write it below)
     const uint32_t tmem = *tmem_slot;
     if (n == 0) {
         empty_sequences(tid, kThreads);
@@ -295,8 +308,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
     };
 
-    // The first Q is asked for before the second tile: behind both tiles of every CTA (22 MB) it came 4 us late.
-    auto second_tile = [&]() { asm volatile("bar.sync 2, %0;" ::"n"(kSoftThreads + 96) : "memory"); };
     if (warp == kProducerWarp) {
         // ---------------- TMA producer: lane j copies block j of a tile ----------------
         Walk w;
@@ -329,7 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (i == 0) second_tile();
             if (!ok) break;
         }
     } else if (warp >= kLoadWarp) {
@@ -346,10 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         Walk w;
         w.at(p, b0, t0);
-        if (g == 1) {
-            if (n > 1) w.next(p);
-            second_tile();
-        }
+        if (g == 1 && n > 1) w.next(p);
         for (int i = g; i < n; i += 2) {
             const int st = i % kStages;
             int id = -1;
@@ -572,7 +579,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         Walk w;
         w.at(p, b0, t0);
         load_q(w.b);
-        asm volatile("bar.arrive 2, %0;" ::"n"(kSoftThreads + 96) : "memory");  // Q before the second tile
         empty_sequences(tid, kSoftThreads);
         publish_q();
         if constexpr (FP8) soft_sync();  // the factors of Q's rows are written
@@ -787,6 +793,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float sum = xch[tid] + xch[64 + tid];
                     return !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
                 }();
+                if (tid == 0 && ct == 0 && !whole && !piece_mid) {
+                    // The merge's record: this sequence begins here and ends in the range that holds its last tile,
+                    // at `end - 1` on the line: the largest r with r total / ranges <= end - 1.
+                    const int64_t end = stop + w.nt - 1 - w.t;
+                    const int last_range = static_cast<int>((end * ranges - 1) / total);
+                    p.record[range] = make_int2(w.b, last_range - range + 1);
+                }
                 if (!whole && has && half == 0) {
 #pragma unroll
                     for (int k = 0; k < kR; ++k) {
@@ -855,9 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Folds the parts of the y-th split sequence, one column (of the x-th eight) a warp, 512 / z
-// of its dims (z = 1 or 4).  A sequence is split where a range starts inside it; its parts are the last
-// piece of the range before the first such range (slot 1) and the first pieces (slot 0) of
-// the ranges from there on.  Two round trips to L2: the records, then everything else.
+// of its dims (z = 1 or 4).  Its parts are the last piece (slot 1) of the range in which it begins,
+// which recorded it, and the first pieces (slot 0) of the ranges from there on.  Two round
+// trips to L2: the records, then everything else.
 constexpr int kMergeWarps = 8;
 constexpr int kRecords = kLatentMaxRanges / 32;
 template <int STEPS>  // of 32 lanes x 4 dims; batches of 8 / STEPS parts (every warp of a call resident at once)
@@ -867,38 +880,29 @@ __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const La
     griddep_launch_dependents();
     griddep_wait();
     if (col >= p.heads * p.q_per_seq) return;
+    // The y-th range in which a split sequence begins: {sequence, parts}.
+    int first = -1, b = 0, parts = 0, seen = 0;
     int2 rec[kRecords];
 #pragma unroll
-    for (int k = 0; k < kRecords; ++k) {
-        const int r = 32 * k + lane;
-        rec[k] = r < p.ranges ? p.record[r] : make_int2(-1, 0);
-    }
-    int first = 0, seen = 0, b = -1, parts = 0;
-    int2 carry = make_int2(-1, 0);
+    for (int k = 0; k < kRecords; ++k) rec[k] = 32 * k + lane < p.ranges ? p.record[32 * k + lane] : make_int2(0, 0);
 #pragma unroll
     for (int k = 0; k < kRecords; ++k) {
-        int2 prev = make_int2(__shfl_up_sync(0xffffffffu, rec[k].x, 1), __shfl_up_sync(0xffffffffu, rec[k].y, 1));
-        if (lane == 0) prev = carry;
-        carry = make_int2(__shfl_sync(0xffffffffu, rec[k].x, 31), __shfl_sync(0xffffffffu, rec[k].y, 31));
-        uint32_t mask = __ballot_sync(0xffffffffu, rec[k].x >= 0 && rec[k].y && !(prev.y && prev.x == rec[k].x));
-        const int here = __popc(mask), want = static_cast<int>(blockIdx.y) - seen;
-        if (!first && want < here) {
+        uint32_t mask = __ballot_sync(0xffffffffu, rec[k].y > 0);
+        const int want = static_cast<int>(blockIdx.y) - seen;
+        seen += __popc(mask);
+        if (first < 0 && want < __popc(mask)) {
             for (int j = want; j > 0; --j) mask &= mask - 1;
             const int at = __ffs(mask) - 1;
             first = 32 * k + at;
             b = __shfl_sync(0xffffffffu, rec[k].x, at);
+            parts = __shfl_sync(0xffffffffu, rec[k].y, at);
         }
-        seen += here;
     }
-    if (!first) return;
-    // The ranges that start inside sequence b follow one another: count them.
-#pragma unroll
-    for (int k = 0; k < kRecords; ++k) parts += __popc(__ballot_sync(0xffffffffu, rec[k].x == b && rec[k].y));
-    ++parts;
+    if (first < 0) return;
     const size_t padded = static_cast<size_t>(p.col_tiles) * p.cols_per_tile;
-    // Part k among the (range, slot, column) partials: slot 1 of the range before, then slot 0 of each.
-    const size_t part0 = (static_cast<size_t>(first - 1) * 2 + 1) * padded + col;
-    const size_t part1 = static_cast<size_t>(first) * 2 * padded + col;
+    // Part k among the (range, slot, column) partials: slot 1 of that range, then slot 0 of those behind it.
+    const size_t part0 = (static_cast<size_t>(first) * 2 + 1) * padded + col;
+    const size_t part1 = static_cast<size_t>(first + 1) * 2 * padded + col;
     auto slot = [&](int k) { return k == 0 ? part0 : part1 + static_cast<size_t>(k - 1) * 2 * padded; };
     constexpr int kBatch = 8 / STEPS;
     float4 v[kBatch][STEPS], o[STEPS];

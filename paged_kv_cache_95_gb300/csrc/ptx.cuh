@@ -70,6 +70,11 @@ __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// The line at p on its way into L2 (a hint: nothing is read into the SM).
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(p)));
+}
+
 // atomicAdd with acquire-release semantics at GPU scope: publishes the writes
 // that happen-before it (including other threads' writes ordered by a
 // preceding __syncthreads) and acquires the writes published by earlier adds.
