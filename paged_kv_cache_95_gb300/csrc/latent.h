@@ -59,7 +59,7 @@ struct LatentDecodeParams {
 };
 constexpr int kLatentMaxRanges = 160;  // at least the SMs (152); the merge keeps 5 records a lane
 constexpr int kLatentMaxCols = 64;     // columns a CTA takes
-constexpr int kLatentTile = 64;        // keys a tile
+constexpr int kLatentTile = 32;        // keys of the smallest tile
 cudaError_t latent_decode_prepare_device();
 struct LatentDecodeMaps {
     CUtensorMap kv, rope;  // rope: FP8 pool only

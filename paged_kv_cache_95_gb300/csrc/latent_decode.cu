@@ -46,8 +46,6 @@ namespace pkv {
 
 namespace {
 
-constexpr int kTile = 64;                     // keys a tile
-constexpr int kTileBlocks = kTile / kBlockSize;
 constexpr int kSoftWarps = 8;                 // warps w and w + 4 share rows 16 (w % 4) .. and split the keys
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kProducerWarp = kSoftWarps;
@@ -55,13 +53,15 @@ constexpr int kScoreWarp = kSoftWarps + 1;    // issues S = Q K^T
 constexpr int kValueWarp = kSoftWarps + 2;    // issues O^T += V^T P^T
 constexpr int kLoadWarp = kSoftWarps + 3;     // two pairs of copying warps, one pair a stage
 constexpr int kThreads = (kSoftWarps + 7) * 32;
-constexpr int kTmaBlocks = 2;                 // blocks of a tile that TMA copies; the others go through cp.async
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // O^T in columns [0, 4 NCOL), the scores of tile i from 256 + (i & 1) kScoreCols on
 
 // Shared memory for NCOL columns over a bf16 or an FP8 pool.
-template <int NCOL, bool FP8>
+template <int NCOL, bool FP8, int TILE>
 struct Layout {
+    static constexpr int kTile = TILE, kTileBlocks = TILE / kBlockSize;  // keys a tile
+    static constexpr int kTmaBlocks = kTileBlocks / 2;  // blocks of a tile that TMA copies; the others go through cp.async
+    static constexpr int kGroups = TILE / 16;           // 8-key groups of the half tile that a warp takes
     // A block of 16 slots: [2 groups of 8 slots][chunks of 128 bytes][8 slots][128 B]; chunks are 64 bf16 values
     // (9 of them, the last the rotated key) or 128 codes (4; the rotated keys follow the stage's codes).
     static constexpr uint32_t kChunks = FP8 ? 4 : 9;
@@ -69,7 +69,9 @@ struct Layout {
     static constexpr uint32_t kBlock = 2 * kGroup;
     static constexpr uint32_t kRopeBlock = FP8 ? kBlockSize * 128 : 0;
     static constexpr uint32_t kStage = kTileBlocks * (kBlock + kRopeBlock);
-    static constexpr int kStages = FP8 ? 3 : 2;
+    static constexpr int kStages = FP8 ? 3 : 128 / TILE;
+    // What beginning another sequence costs a range, in tiles: its Q, the epilogue of the one before.
+    static constexpr int kLead = FP8 ? 4 : 128 / TILE;
     // M = 64: rows 16 q .. 16 q + 15 of S lie in tensor-memory lanes 32 q .., which only warps w % 4 = q reach, one
     // scheduler's.  A quarter of the columns goes to each: column c is row 16 (c / kPerQuarter) + c % kPerQuarter.
     static constexpr int kPerQuarter = NCOL / 4, kRowsPerThread = NCOL == 64 ? 2 : 1;
@@ -81,7 +83,7 @@ struct Layout {
     static constexpr uint32_t kKv = kQ + 9 * kQChunk;
     static constexpr uint32_t kP = kKv + kStages * kStage;  // [NCOL][64 bf16], or [NCOL][64 heads | 64 remainders]
     static constexpr uint32_t kScale = kP + NCOL * 128;     // FP8: [stage][scale, its log2, its inverse][64 keys]
-    static constexpr uint32_t kQf = kScale + (FP8 ? kStages * 3 * kTile * 4 : 0);  // FP8: [64] factors of the columns
+    static constexpr uint32_t kQf = kScale + (FP8 ? kStages * 3 * TILE * 4 : 0);  // FP8: [64] factors of the columns
     // kv_full[stage], kv_empty[stage][block], s_full[2], s_empty[2], p_full, pv_done, q_full
     static constexpr int kBarKvFull = 0, kBarKvEmpty = kStages, kBarSFull = kBarKvEmpty + kStages * kTileBlocks,
                          kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 2, kBarPvDone = kBarPFull + 1,
@@ -134,26 +136,27 @@ __device__ __forceinline__ int keys_of(const LatentDecodeParams &p, int b) {
     const int ctx = __ldg(p.context_lens + b);
     return ctx < 1 || ctx < p.q_per_seq ? 0 : min(ctx, p.max_blocks * kBlockSize);
 }
+template <typename L>
 __device__ __forceinline__ int tiles_of(const LatentDecodeParams &p, int b) {
-    return (keys_of(p, b) + kTile - 1) / kTile;
+    return (keys_of(p, b) + L::kTile - 1) / L::kTile;
 }
 
-// The line of tiles that the ranges cut: every sequence with keys counts kLead tiles more, at its start --
-// what beginning another sequence costs a range (its Q, the epilogue of the one before).
-constexpr int kLead = 2;
+// The line of tiles that the ranges cut: every sequence with keys counts kLead tiles more, at its start.
+template <typename L>
 __device__ __forceinline__ int cost_of(const LatentDecodeParams &p, int b) {
-    const int t = tiles_of(p, b);
-    return t > 0 ? t + kLead : 0;
+    const int t = tiles_of<L>(p, b);
+    return t > 0 ? t + L::kLead : 0;
 }
 
 // A walk over the tiles of a range.
+template <typename L>
 struct Walk {
     int b, t, keys, nt;  // tile t of the nt tiles of sequence b
     __device__ void at(const LatentDecodeParams &p, int b0, int t0) {
         b = b0;
         t = t0;
         keys = keys_of(p, b);
-        nt = (keys + kTile - 1) / kTile;
+        nt = (keys + L::kTile - 1) / L::kTile;
     }
     __device__ void next(const LatentDecodeParams &p) {  // only while another tile follows
         if (++t < nt) return;
@@ -162,12 +165,13 @@ struct Walk {
     }
 };
 
-template <int NCOL, bool FP8>
+template <int NCOL, bool FP8, int TILE>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap kvmap, const __grid_constant__ CUtensorMap ropemap,
                          const LatentDecodeParams p) {
-    using L = Layout<NCOL, FP8>;
-    constexpr int kStages = L::kStages;
+    using L = Layout<NCOL, FP8, TILE>;
+    constexpr int kStages = L::kStages, kTile = L::kTile, kTileBlocks = L::kTileBlocks, kTmaBlocks = L::kTmaBlocks,
+                  kGroups = L::kGroups;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int seg = (p.num_seqs + kThreads - 1) / kThreads;
     const int b_lo = min(p.num_seqs, tid * seg), b_hi = min(p.num_seqs, b_lo + seg);
     int64_t mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += cost_of(p, b);
+    for (int b = b_lo; b < b_hi; ++b) mine += cost_of<L>(p, b);
     int64_t upto = mine;  // inclusive prefix
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -250,15 +254,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (upto - mine < stop && start < upto) {
         int64_t acc = upto - mine;
         for (int b = b_lo; b < b_hi && acc < stop; ++b) {
-            const int t = tiles_of(p, b);
+            const int t = tiles_of<L>(p, b);
             if (t == 0) continue;
-            const int64_t lo = max(static_cast<int64_t>(0), start - acc - kLead);
-            const int64_t hi = min(static_cast<int64_t>(t), stop - acc - kLead);
+            const int64_t lo = max(static_cast<int64_t>(0), start - acc - L::kLead);
+            const int64_t hi = min(static_cast<int64_t>(t), stop - acc - L::kLead);
             if (hi > lo) {
                 tiles += hi - lo;
                 atomicMin(first_tile, (static_cast<unsigned long long>(b) << 32) | lo);
             }
-            acc += t + kLead;
+            acc += t + L::kLead;
         }
     }
     if (tiles > 0) atomicAdd(tile_count, static_cast<unsigned long long>(tiles));
@@ -310,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kProducerWarp) {
         // ---------------- TMA producer: lane j copies block j of a tile ----------------
-        Walk w;
+        Walk<L> w;
         w.at(p, b0, t0);
         auto block_id = [&]() -> int {  // -1: past the context, or an invalid id (never copied)
             const int jb = w.t * kTileBlocks + lane;
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int v = t + 64 * k, r = v / kVec, c = v - r * kVec;
             to[k] = (c >> 3) * 1024 + r * 128 + (((c & 7) ^ r) << 4);
         }
-        Walk w;
+        Walk<L> w;
         w.at(p, b0, t0);
         if (g == 1 && n > 1) w.next(p);
         for (int i = g; i < n; i += 2) {
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (Both tensor warps run their loop whole, on warp-uniform values, and one elected lane
         // issues: the descriptors stay in uniform registers.  Issued from a one-lane branch an
         // MMA took 74-98 cycles to issue, against 36-52 in the pipe.)
-        Walk w;
+        Walk<L> w;
         w.at(p, b0, t0);
         const uint64_t q_desc = sw128_desc(sbase + L::kQ, 16, 1024);
         const uint64_t k_desc = sw128_desc(sbase + L::kKv, 16, L::kGroup);
@@ -444,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kValueWarp) {
         // ---------------- O^T += V^T P^T ----------------
-        Walk w;
+        Walk<L> w;
         w.at(p, b0, t0);
         const uint64_t v_desc = sw128_desc(sbase + L::kKv, 1024, L::kGroup);
         const uint64_t p_desc = sw128_desc(sbase + L::kP, 16, 1024);
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- softmax, rescaling and epilogue: 8 warps ----------------
         const int quarter = warp & 3, half = warp >> 2;
         // The 16-lane load spreads a quarter's rows over the warp: a thread holds rows lane / 4 and (64 columns)
-        // lane / 4 + 8 of it, of each 8 keys of every 32 (columns 8 j + 2 (lane % 4) + 0, 1).
+        // lane / 4 + 8 of it, of each 8 keys of its half tile (columns 8 j + 2 (lane % 4) + 0, 1).
         constexpr int kR = L::kRowsPerThread;
         const int col0 = quarter * L::kPerQuarter + (lane >> 2);  // the column of row k is col0 + 8 k
         const bool live = (lane >> 2) < L::kPerQuarter;
@@ -498,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P: where this thread's pair of keys of 8-key group j goes, p_at[.] (+ 1024 for row k = 1).  bf16: a pair is 4
         // bytes, group j the 16-byte chunk 4 half + j.  FP8: 2 bytes, chunk 2 half + j / 2, remainders 64 bytes on.
         auto p_at = [&](int j) {
-            const int v = FP8 ? 2 * half + (j >> 1) : 4 * half + j;
+            const int v = FP8 ? 2 * half + (j >> 1) : kGroups * half + j;
             return sbase + L::kP + col0 * 128 + ((v ^ (col0 & 7)) << 4) + (FP8 ? 8 * (j & 1) + 2 * (lane & 3) : 4 * (lane & 3));
         };
         float *xch = reinterpret_cast<float *>(smem + L::kXch);
@@ -576,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bar(L::kBarQFull));
         };
 
-        Walk w;
+        Walk<L> w;
         w.at(p, b0, t0);
         load_q(w.b);
         empty_sequences(tid, kSoftThreads);
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float q_scale[kR] = {};          // FP8: those of this thread's columns, times the softmax scale
         float m_ref[kR];
         float2 l[kR];
-        auto block_id = [&](const Walk &a) {  // lane j: the id of block j of a tile (0 past the context)
+        auto block_id = [&](const Walk<L> &a) {  // lane j: the id of block j of a tile (0 past the context)
             const int jb = a.t * kTileBlocks + lane;
             return lane < kTileBlocks && jb * kBlockSize < a.keys
                        ? __ldg(p.block_tables + static_cast<size_t>(a.b) * p.max_blocks + jb)
@@ -612,31 +616,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             // FP8: c_j = code s_j, so the score is s_j <q, code_j> + <q_rope, r_j>, and the weight that multiplies the
             // codes is s_j 2^score = 2^(score + log2 s_j); the sum l takes it times 1 / s_j.
             if (FP8) alive = alive && warp_wait(bar(L::kBarKvFull + i % kStages), (i / kStages) & 1);  // (the scales)
-            const uint32_t sc_at = sbase + L::kScale + ((i % kStages) * 3 * kTile + 32 * half + 2 * (lane & 3)) * 4;
+            const uint32_t sc_at = sbase + L::kScale + ((i % kStages) * 3 * kTile + kTile / 2 * half + 2 * (lane & 3)) * 4;
             alive = alive && warp_wait(bar(L::kBarSFull + (i & 1)), (i >> 1) & 1);
-            float2 x[kR][4];  // [k][j]: row k, keys 32 half + 8 j + 2 (lane % 4) + 0, 1
+            float2 x[kR][kGroups];  // [k][j]: row k, keys kTile / 2 half + 8 j + 2 (lane % 4) + 0, 1
             float mx[kR];
 #pragma unroll
             for (int k = 0; k < kR; ++k) mx[k] = -INFINITY;
             if (alive) {
                 tc_fence_after();
-                uint32_t v[16];
-                const uint32_t s_at = tmem + lanes + kTmemS + L::kScoreCols * (i & 1) + 32 * half;
+                uint32_t v[4 * kGroups];
+                const uint32_t s_at = tmem + lanes + kTmemS + L::kScoreCols * (i & 1) + kTile / 2 * half;
                 const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
-                auto pair = [](const uint32_t(&r)[16], int j, int k) {
+                auto pair = [](const uint32_t(&r)[4 * kGroups], int j, int k) {
                     return make_float2(__uint_as_float(r[4 * j + 2 * k]), __uint_as_float(r[4 * j + 2 * k + 1]));
                 };
                 if constexpr (!FP8) {
-                    tmem_ld_16x256b_x4(s_at, v);
+                    if constexpr (kGroups == 4)
+                        tmem_ld_16x256b_x4(s_at, v);
+                    else
+                        tmem_ld_16x256b_x2(s_at, v);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < kGroups; ++j)
 #pragma unroll
                         for (int k = 0; k < kR; ++k) x[k][j] = fmul2(pair(v, j, k), sl2);
                 } else {
                     uint32_t u[16];
                     tmem_ld_16x256b_x4_pair(s_at, v, s_at + 64, u);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < kGroups; ++j) {
                         const float2 sc = lds_f32x2(sc_at + 32 * j), lg = lds_f32x2(sc_at + kTile * 4 + 32 * j);
 #pragma unroll
                         for (int k = 0; k < kR; ++k)
@@ -648,10 +655,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Row q_row sees keys up to keys - q_per_seq + q_row; bad blocks see none.
                 if (left - p.q_per_seq + 1 < kTile || bad) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < kGroups; ++j)
 #pragma unroll
                         for (int k = 0; k < kR; ++k) {
-                            const int key = 32 * half + 8 * j + 2 * (lane & 3), end = left - p.q_per_seq + q_row[k];
+                            const int key = kTile / 2 * half + 8 * j + 2 * (lane & 3), end = left - p.q_per_seq + q_row[k];
                             const bool hide = (bad >> (key >> 4)) & 1u;
                             if (hide || key > end) x[k][j].x = -INFINITY;
                             if (hide || key + 1 > end) x[k][j].y = -INFINITY;
@@ -660,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < kR; ++k) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) mx[k] = fmax3(mx[k], x[k][j].x, x[k][j].y);
+                    for (int j = 0; j < kGroups; ++j) mx[k] = fmax3(mx[k], x[k][j].x, x[k][j].y);
                     mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
                     mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
                 }
@@ -669,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (alive && lane == 0) mbar_arrive(bar(L::kBarSEmpty + (i & 1)));
             // The last S of a piece is complete: its Q can make way for the next sequence's.
             const bool more = last && i + 1 < n;
-            Walk nx = w;
+            Walk<L> nx = w;
             if (i + 1 < n) {
                 nx.next(p);
                 id = block_id(nx);
@@ -720,12 +727,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // Weights, rounded to bf16 (relative 2^-8; l adds what P V will read), or to a pair of E4M3 codes by way
             // of fp16 (2^-11; the pair holds relative 2^-8, in steps of 2^-9 where the largest is at least 2^2).
-            uint32_t pk[kR][4];
+            uint32_t pk[kR][kGroups];
 #pragma unroll
             for (int k = 0; k < kR; ++k) {
                 const float mu = m_ref[k] == -INFINITY ? 0.f : m_ref[k] - L::kLift;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < kGroups; ++j) {
                     const float2 y = fadd2(x[k][j], make_float2(-mu, -mu));
                     const float2 w2 = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                     if constexpr (FP8) {
@@ -741,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (alive) {
                 if (live) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < kGroups; ++j)
 #pragma unroll
                         for (int k = 0; k < kR; ++k) {
                             const uint32_t at = p_at(j) + 1024 * k;
@@ -965,10 +972,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const La
 
 }  // namespace
 
+// Keys a tile.  Over a bf16 pool Q and two tiles of 64 keys fill the shared memory, and a tile stays through S,
+// softmax and P V: tiles of 32 keys in four stages are held shorter (8 x 32K tokens of 64 heads 70.9 -> 67.3 us,
+// 128 heads 81.8 -> 77.3, the ragged batch of 32 heads 43.6 -> 41.9).  With up to 16 columns 64 keys halve the parts
+// of a short context (one sequence of 1000 tokens 12.5 -> 10.4 us).
+template <int NCOL, bool FP8>
+constexpr int kTileOf = !FP8 && NCOL >= 32 ? 32 : 64;
+
 template <int NCOL, bool FP8>
 cudaError_t prepare_one() {
-    return cudaFuncSetAttribute(latent_decode_kernel<NCOL, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(Layout<NCOL, FP8>::kBytes));
+    return cudaFuncSetAttribute(latent_decode_kernel<NCOL, FP8, kTileOf<NCOL, FP8>>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Layout<NCOL, FP8, kTileOf<NCOL, FP8>>::kBytes));
 }
 
 cudaError_t latent_decode_prepare_device() {
@@ -983,8 +998,8 @@ cudaError_t latent_decode_prepare_device() {
 
 template <int NCOL, bool FP8>
 cudaError_t launch_one(const LatentDecodeMaps &maps, const LatentDecodeParams &p, cudaStream_t stream) {
-    return launch_pdl(latent_decode_kernel<NCOL, FP8>, dim3(p.ranges * p.col_tiles), dim3(kThreads),
-                      Layout<NCOL, FP8>::kBytes, stream, maps.kv, maps.rope, p);
+    return launch_pdl(latent_decode_kernel<NCOL, FP8, kTileOf<NCOL, FP8>>, dim3(p.ranges * p.col_tiles), dim3(kThreads),
+                      Layout<NCOL, FP8, kTileOf<NCOL, FP8>>::kBytes, stream, maps.kv, maps.rope, p);
 }
 
 template <bool FP8>
