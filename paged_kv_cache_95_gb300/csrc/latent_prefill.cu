@@ -18,16 +18,18 @@
 // times a stranger's NaN would be NaN).
 //
 // Warps:
-//  * 0-3 softmax of row tile 0, 4-7 of row tile 1, a row a thread: 32 scores at a time, one
+//  * 0-3 softmax of row tile 0, 4-7 of row tile 1, a row a thread: 64 scores at a time, one
 //    pass, weights P = 2^(s - m) against a running reference m straight back over the
 //    consumed scores as bf16 (relative 2^-8).  m is an integer, raised when a score passes it
-//    by 2^8 (looked at before the 32 weights are written; what was written is rescaled by an
+//    by 2^8 (looked at before the 64 weights are written; what was written is rescaled by an
 //    exact power of two, and so are l and O); the sum l stays in fp32.
-//  * 8 TMA: Q, K.  11-14 cp.async: V.  Chunks of [128 rows][128 bytes] in a ring of 8
+//  * 8 TMA: Q, K.  10-13 cp.async: V.  Chunks of [128 rows][128 bytes] in a ring of 8
 //    (per key tile K K K V V): a tile's chunks are refilled as the MMAs that read them end.
-//  * 9, 10 issue the MMAs of row tile 0 and 1: S(k + 1) follows P V (k) (it overwrites the
-//    P that P V reads; the MMAs of one thread run in order), and while one tile's softmax
-//    runs the tensor pipe has the other's.
+//  * 9 issues the MMAs in the order S0(k), P1 V(k-1), S1(k), P0 V(k): while one row tile's
+//    softmax runs the tensor pipe has the other's P V and next S (with a warp a tile they
+//    fell into step, both softmaxes at once and the pipe idle: 5400 cycles a key tile).
+//    S(k + 1) follows P V (k): it overwrites the P that P V reads, and the MMAs of one
+//    thread run in order.
 //
 // Every mbarrier wait is bounded; a role whose wait runs out raises a CTA-wide abort
 // flag, the others stop at their next wait, and the CTA records PKV_STATUS_TIMEOUT and
@@ -46,9 +48,9 @@ namespace {
 
 constexpr int kRows = 128;                    // query rows a tile
 constexpr int kKeys = 128;                    // keys a tile
-constexpr int kTmaWarp = 8, kMmaWarp = 9, kLoadWarp = 11;
+constexpr int kTmaWarp = 8, kMmaWarp = 9, kLoadWarp = 10;
 constexpr int kLoadThreads = 128;
-constexpr int kThreads = 15 * 32;
+constexpr int kThreads = 14 * 32;
 constexpr uint32_t kChunk = 128 * 128;        // 16 KB: 128 rows x 64 values
 constexpr int kSlots = 8;                     // ring of chunks
 constexpr int kPerTile = 5;                   // chunks a key tile: k_nope 0, 1, k_rope, v 0, 1
@@ -139,7 +141,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i)
             mbar_init(bar(i), i >= kBarFull && i < kBarEmpty ? kLoadThreads / 32
-                              : i >= kBarEmpty && i < kBarS  ? 2
                               : i >= kBarP && i < kBarO      ? 4
                                                              : 1);
         *abort_flag = 0u;
@@ -229,51 +230,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-        const int t = warp - kMmaWarp, nt = tile_nt(t);
-        const uint32_t s_at = tmem + 128 * t, o_at = tmem + kTmemO + 128 * t;
-        const uint64_t q_desc = sw128_desc(sbase + kOffQ + 3 * t * kChunk, 16, 1024);
-        const uint64_t k_desc = sw128_desc(sbase + kOffRing, 16, 1024), v_desc = sw128_desc(sbase + kOffRing, 16, 1024);
+    } else if (warp == kMmaWarp) {
+        // The warp runs whole on warp-uniform values, one elected lane issues: descriptors stay in uniform registers.
+        const int nt0 = tile_nt(0), nt1 = tile_nt(1);
+        const uint64_t q_desc = sw128_desc(sbase + kOffQ, 16, 1024);
+        const uint64_t kv_desc = sw128_desc(sbase + kOffRing, 16, 1024);
         bool ok = warp_wait(bar(kBarQ), 0);
-        for (int kt = 0; ok && kt < n_tiles; ++kt) {
-            for (int i = 0; i < 3; ++i) {
+        int k_seen = 0, v_seen = 0;  // key tiles whose K, V this warp has seen land
+        auto score = [&](int t, int kt) {
+            const bool last_reader = t == 1 || kt >= nt1;
+            for (int i = 0; ok && i < 3; ++i) {
                 const int j = kPerTile * kt + i;
-                if (!(ok = warp_wait(full(j), (j / kSlots) & 1))) break;
+                if (k_seen <= kt && !(ok = warp_wait(full(j), (j / kSlots) & 1))) break;
                 tc_fence_after();
-                const uint64_t qd = q_desc + static_cast<uint32_t>(i) * (kChunk >> 4);
-                const uint64_t kd = k_desc + static_cast<uint32_t>(j % kSlots) * (kChunk >> 4);
+                const uint64_t qd = q_desc + static_cast<uint32_t>(3 * t + i) * (kChunk >> 4);
+                const uint64_t kd = kv_desc + static_cast<uint32_t>(j % kSlots) * (kChunk >> 4);
                 if (elect_one()) {
-                    if (kt < nt) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) umma_bf16(s_at, qd + 2 * kk, kd + 2 * kk, kIdescQK, i > 0 || kk > 0);
-                        umma_commit(empty(j));
-                        if (i == 2) umma_commit(bar(kBarS + t));
-                    } else {
-                        mbar_arrive(empty(j));  // this row tile does not see the key tile
-                    }
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16(tmem + 128 * t, qd + 2 * kk, kd + 2 * kk, kIdescQK, i > 0 || kk > 0);
+                    if (last_reader) umma_commit(empty(j));
+                    if (i == 2) umma_commit(bar(kBarS + t));
                 }
                 __syncwarp();
             }
-            if (!ok) break;
-            if (kt < nt && !(ok = warp_wait(bar(kBarP + t), kt & 1))) break;
-            for (int i = 0; i < 2; ++i) {
+            k_seen = kt + 1;
+        };
+        auto value = [&](int t, int kt) {
+            const int nt = t == 0 ? nt0 : nt1;
+            const bool last_reader = t == 1 || kt >= nt1;
+            ok = ok && warp_wait(bar(kBarP + t), kt & 1);
+            for (int i = 0; ok && i < 2; ++i) {
                 const int j = kPerTile * kt + 3 + i;
-                if (!(ok = warp_wait(full(j), (j / kSlots) & 1))) break;
+                if (v_seen <= kt && !(ok = warp_wait(full(j), (j / kSlots) & 1))) break;
                 tc_fence_after();
-                const uint64_t vd = v_desc + static_cast<uint32_t>(j % kSlots) * (kChunk >> 4);
+                const uint64_t vd = kv_desc + static_cast<uint32_t>(j % kSlots) * (kChunk >> 4);
                 if (elect_one()) {
-                    if (kt < nt) {
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            umma_bf16_tmem_a(o_at + 64 * i, s_at + 8 * ks, vd + ks * (2048 >> 4), kIdescPV, kt > 0 || ks > 0);
-                        umma_commit(empty(j));
-                        if (i == 1 && kt == nt - 1) umma_commit(bar(kBarO + t));
-                    } else {
-                        mbar_arrive(empty(j));
-                    }
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_bf16_tmem_a(tmem + kTmemO + 128 * t + 64 * i, tmem + 128 * t + 8 * ks, vd + ks * (2048 >> 4),
+                                         kIdescPV, kt > 0 || ks > 0);
+                    if (last_reader) umma_commit(empty(j));
+                    if (i == 1 && kt == nt - 1) umma_commit(bar(kBarO + t));
                 }
                 __syncwarp();
             }
+            v_seen = kt + 1;
+        };
+        for (int kt = 0; ok && kt <= n_tiles; ++kt) {
+            if (kt < nt0) score(0, kt);
+            if (ok && kt >= 1 && kt - 1 < nt1) value(1, kt - 1);
+            if (ok && kt < nt1) score(1, kt);
+            if (ok && kt < nt0) value(0, kt);
         }
     } else {
         // ---------------- softmax: a row a thread ----------------
@@ -286,45 +294,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float hidden = neg ? INFINITY : -INFINITY;
         const int limit = c + i0 + r;  // last visible key
         float m = -INFINITY;
-        float2 l2 = make_float2(0.f, 0.f);
+        float2 l2 = make_float2(0.f, 0.f), l3 = l2;  // the sum, in four parts
         bool alive = true;
         for (int kt = 0; alive && kt < nt; ++kt) {
             if (!(alive = warp_wait(bar(kBarS + t), kt & 1))) break;
             tc_fence_after();
             const bool mask = kt * kKeys + kKeys - 1 > c + i0;  // some row does not see some key
-            auto load = [&](int cc, uint32_t(&v)[32]) {
-                tmem_ld_32x32b_x32(s_at + 32 * cc, v);
+            auto load = [&](int cc, uint32_t(&v)[64]) {
+                tmem_ld_32x32b_x64(s_at + 64 * cc, v);
                 if (mask) {
-                    const int last = limit - kt * kKeys - 32 * cc;
+                    const int last = limit - kt * kKeys - 64 * cc;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
+                    for (int e = 0; e < 64; ++e)
                         if (e > last) v[e] = __float_as_uint(hidden);
                 }
             };
-            // The largest score of 32 (log2 domain).
-            auto largest = [&](const uint32_t(&v)[32]) {
+            // The largest score of 64 (log2 domain).
+            auto largest = [&](const uint32_t(&v)[64]) {
                 float x[4] = {hidden, hidden, hidden, hidden};
                 if (neg) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e & 3] = fminf(x[e & 3], __uint_as_float(v[e]));
+                    for (int e = 0; e < 64; ++e) x[e & 3] = fminf(x[e & 3], __uint_as_float(v[e]));
                     return fminf(fminf(x[0], x[1]), fminf(x[2], x[3])) * sl2;
                 }
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
+                for (int e = 0; e < 64; e += 2)
                     x[(e >> 1) & 3] = fmax3(x[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
                 return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl2;
             };
 #pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc) {
-                uint32_t v[32];
+            for (int cc = 0; cc < 2; ++cc) {
+                uint32_t v[64];
                 load(cc, v);
                 float mx = largest(v);
                 if (__any_sync(0xffffffffu, mx > m + kRaise)) {
                     // Raise the references that are passed to the largest score from here on (an integer),
-                    // and rescale what was made with the old one: weights 0 .. 32 cc, l, O.
-                    uint32_t u[32];
-                    for (int k = cc + 1; k < 4; ++k) {
-                        load(k, u);
+                    // and rescale what was made with the old one: the weights before, l, O.
+                    if (cc == 0) {
+                        uint32_t u[64];
+                        load(1, u);
                         mx = fmaxf(mx, largest(u));
                     }
                     float alpha = 1.f;
@@ -334,8 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m = up;
                     }
                     l2 = fmul2(l2, make_float2(alpha, alpha));
+                    l3 = fmul2(l3, make_float2(alpha, alpha));
                     tmem_wait_st();  // the weights that are read back now
-                    for (int k = 0; k < cc; ++k) {
+#pragma unroll 1
+                    for (int k = 0; k < 2 * cc; ++k) {
                         uint32_t w[16];
                         tmem_ld_32x32b_x16(s_at + 16 * k, w);
 #pragma unroll
@@ -344,26 +354,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st_32x32b_x16(s_at + 16 * k, w);
                     }
                     if (kt > 0) {  // every earlier P V of this tile completed before S (kt) did
-                        for (int k = 0; k < 4; ++k) {
-                            tmem_ld_32x32b_x32(o_at + 32 * k, u);
+#pragma unroll 1
+                        for (int k = 0; k < 8; ++k) {
+                            uint32_t u[16];
+                            tmem_ld_32x32b_x16(o_at + 16 * k, u);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-                            tmem_st_32x32b_x32(o_at + 32 * k, u);
+                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+                            tmem_st_32x32b_x16(o_at + 16 * k, u);
                         }
                     }
                     tmem_wait_st();
+                    load(cc, v);  // (kept in tensor memory meanwhile, not in registers)
                 }
                 const float mu = m == -INFINITY ? 0.f : m;
                 const float2 sv = make_float2(sl2, sl2), nm = make_float2(-mu, -mu);
-                uint32_t w[16];
+                uint32_t w[32];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
+                for (int e = 0; e < 32; ++e) {
                     const float2 x = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sv, nm);
                     const float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                    l2 = fadd2(l2, pr);
+                    if (e & 1)
+                        l3 = fadd2(l3, pr);
+                    else
+                        l2 = fadd2(l2, pr);
                     w[e] = pack_bf16x2(pr.x, pr.y);
                 }
-                tmem_st_32x32b_x16(s_at + 16 * cc, w);
+                tmem_st_32x32b_x32(s_at + 32 * cc, w);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -373,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- epilogue: out = O / l ----------------
         if (nt > 0 && alive && warp_wait(bar(kBarO + t), 0)) {
             tc_fence_after();
-            const float l = l2.x + l2.y, inv = l > 0.f ? 1.f / l : 0.f;
+            const float l = (l2.x + l2.y) + (l3.x + l3.y), inv = l > 0.f ? 1.f / l : 0.f;
             const bool staged = p.out_bf16 && rows == kRows;  // a full tile leaves by TMA from its Q's place
             const uint32_t stage = sbase + kOffQ + 3 * t * kChunk;
             const size_t at = ((static_cast<size_t>(q0) + i0 + r) * p.heads + h) * kExpandedV;
