@@ -69,7 +69,8 @@ constexpr float kRaise = 8.f;
 // kind::f16, D f32, A and B bf16, M = 128.
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescQK = kIdesc | ((128u >> 3) << 17);
-constexpr uint32_t kIdescPV = kIdesc | ((64u >> 3) << 17) | (1u << 16);  // B (V) MN-major, 64 dims
+constexpr uint32_t kIdescPV = kIdesc | ((128u >> 3) << 17) | (1u << 16);  // B (V) MN-major, 128 dims
+constexpr uint32_t kIdescPVHalf = kIdesc | ((64u >> 3) << 17) | (1u << 16);
 
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
@@ -155,8 +156,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // A warp's bounded wait; it gives up soon after another role did (timer and flag every 64 tries).
-    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
+    // A warp's bounded wait, each lane for a barrier of its own; it gives up soon after another role did (timer and
+    // flag every 64 tries).
+    auto lanes_wait = [&](uint32_t b, uint32_t parity) -> bool {
         uint64_t t_first = 0;
         for (uint32_t tries = 0; !__all_sync(0xffffffffu, mbar_try_wait(b, parity)); ++tries) {
             if ((tries & 63u) != 63u) continue;
@@ -169,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
     };
+    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return lanes_wait(b, parity); };
     // Chunk j (5 per key tile) lies in slot j % 8, its use j / 8.
     auto full = [&](int j) { return bar(kBarFull + j % kSlots); };
     auto empty = [&](int j) { return bar(kBarEmpty + j % kSlots); };
@@ -235,47 +238,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nt0 = tile_nt(0), nt1 = tile_nt(1);
         const uint64_t q_desc = sw128_desc(sbase + kOffQ, 16, 1024);
         const uint64_t kv_desc = sw128_desc(sbase + kOffRing, 16, 1024);
+        const uint64_t v_desc = sw128_desc(sbase + kOffRing, kChunk, 1024);  // 128 dims: two chunks side by side
         bool ok = warp_wait(bar(kBarQ), 0);
-        int k_seen = 0, v_seen = 0;  // key tiles whose K, V this warp has seen land
+        // The warp waits for Q, K(0) and the weights only: the softmax warps look that V(k) and K(k + 1) have landed
+        // before they hand over P(k) (a wait costs this warp 100 cycles and more even when it need not wait).
+        for (int i = 0; i < 3; ++i) ok = ok && warp_wait(full(i), 0);
         auto score = [&](int t, int kt) {
-            const bool last_reader = t == 1 || kt >= nt1;
-            for (int i = 0; ok && i < 3; ++i) {
-                const int j = kPerTile * kt + i;
-                if (k_seen <= kt && !(ok = warp_wait(full(j), (j / kSlots) & 1))) break;
-                tc_fence_after();
-                const uint64_t qd = q_desc + static_cast<uint32_t>(3 * t + i) * (kChunk >> 4);
-                const uint64_t kd = kv_desc + static_cast<uint32_t>(j % kSlots) * (kChunk >> 4);
-                if (elect_one()) {
+            tc_fence_after();
+            const uint64_t qd = q_desc + static_cast<uint32_t>(3 * t) * (kChunk >> 4);
+            if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const uint64_t kd = kv_desc + static_cast<uint32_t>((kPerTile * kt + i) % kSlots) * (kChunk >> 4);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16(tmem + 128 * t, qd + 2 * kk, kd + 2 * kk, kIdescQK, i > 0 || kk > 0);
-                    if (last_reader) umma_commit(empty(j));
-                    if (i == 2) umma_commit(bar(kBarS + t));
+                        umma_bf16(tmem + 128 * t, qd + i * (kChunk >> 4) + 2 * kk, kd + 2 * kk, kIdescQK, i > 0 || kk > 0);
                 }
-                __syncwarp();
+                umma_commit(bar(kBarS + t));
+                if (t == 1 || kt >= nt1)  // K's last reader
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) umma_commit(empty(kPerTile * kt + i));
             }
-            k_seen = kt + 1;
+            __syncwarp();
         };
         auto value = [&](int t, int kt) {
-            const int nt = t == 0 ? nt0 : nt1;
-            const bool last_reader = t == 1 || kt >= nt1;
-            ok = ok && warp_wait(bar(kBarP + t), kt & 1);
-            for (int i = 0; ok && i < 2; ++i) {
-                const int j = kPerTile * kt + 3 + i;
-                if (v_seen <= kt && !(ok = warp_wait(full(j), (j / kSlots) & 1))) break;
-                tc_fence_after();
-                const uint64_t vd = kv_desc + static_cast<uint32_t>(j % kSlots) * (kChunk >> 4);
-                if (elect_one()) {
+            if (!(ok = ok && warp_wait(bar(kBarP + t), kt & 1))) return;
+            tc_fence_after();
+            const int j = kPerTile * kt + 3;
+            const uint64_t vd = v_desc + static_cast<uint32_t>(j % kSlots) * (kChunk >> 4);
+            const uint32_t o = tmem + kTmemO + 128 * t, w = tmem + 128 * t;
+            if (elect_one()) {
+                if (j % kSlots != kSlots - 1) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        umma_bf16_tmem_a(tmem + kTmemO + 128 * t + 64 * i, tmem + 128 * t + 8 * ks, vd + ks * (2048 >> 4),
-                                         kIdescPV, kt > 0 || ks > 0);
-                    if (last_reader) umma_commit(empty(j));
-                    if (i == 1 && kt == nt - 1) umma_commit(bar(kBarO + t));
+                        umma_bf16_tmem_a(o, w + 8 * ks, vd + ks * (2048 >> 4), kIdescPV, kt > 0 || ks > 0);
+                } else {  // the chunks lie at the ring's two ends: 64 dims at a time, at half the rate (66 cycles for either)
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        umma_bf16_tmem_a(o, w + 8 * ks, vd + ks * (2048 >> 4), kIdescPVHalf, kt > 0 || ks > 0);
+                        umma_bf16_tmem_a(o + 64, w + 8 * ks, v_desc + ks * (2048 >> 4), kIdescPVHalf, kt > 0 || ks > 0);
+                    }
                 }
-                __syncwarp();
+                if (t == 1 || kt >= nt1) {  // V's last reader
+                    umma_commit(empty(j));
+                    umma_commit(empty(j + 1));
+                }
+                if (kt == (t == 0 ? nt0 : nt1) - 1) umma_commit(bar(kBarO + t));
             }
-            v_seen = kt + 1;
+            __syncwarp();
         };
         for (int kt = 0; ok && kt <= n_tiles; ++kt) {
             if (kt < nt0) score(0, kt);
@@ -286,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ---------------- softmax: a row a thread ----------------
         const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-        const int nt = tile_nt(t), rows = tile_rows(t), i0 = r_lo + t * kRows;
+        const int nt = tile_nt(t), nt0 = tile_nt(0), rows = tile_rows(t), i0 = r_lo + t * kRows;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + kTmemO + 128 * t;
         const float sl2 = p.scale_log2;
@@ -382,9 +392,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st_32x32b_x32(s_at + 32 * cc, w);
             }
             tmem_wait_st();
+            if (quarter == 0 && (t == 0 || kt >= nt0)) {
+                // V(kt) and, for the S that follows, K(kt + 1): a lane a chunk.
+                const int j = kPerTile * kt + 3 + min(lane, kt + 1 < n_tiles ? 4 : 1);
+                alive = lanes_wait(full(j), (j / kSlots) & 1);
+            }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarP + t));
+            if (alive && lane == 0) mbar_arrive(bar(kBarP + t));
         }
         // ---------------- epilogue: out = O / l ----------------
         if (nt > 0 && alive && warp_wait(bar(kBarO + t), 0)) {
