@@ -23,8 +23,10 @@
 //    consumed scores as bf16 (relative 2^-8).  m is an integer, raised when a score passes it
 //    by 2^8 (looked at before the 64 weights are written; what was written is rescaled by an
 //    exact power of two, and so are l and O); the sum l stays in fp32.
-//  * 8 TMA: Q, K.  10-13 cp.async: V.  Chunks of [128 rows][128 bytes] in a ring of 8
-//    (per key tile K K K V V): a tile's chunks are refilled as the MMAs that read them end.
+//  * 8 TMA: Q, K.  10-13 cp.async: V.  Chunks of 16 KB: three a key tile of K ([128 keys]
+//    [64 values]) and two of V ([64 keys][128 dims]), each kind in a ring of 4, each refilled
+//    as the MMAs that read it end.  (One ring of 8 for both let the next K wait for this V:
+//    474 us on 8192 tokens x 32 heads.)
 //  * 9 issues the MMAs in the order S0(k), P1 V(k-1), S1(k), P0 V(k): while one row tile's
 //    softmax runs the tensor pipe has the other's P V and next S (with a warp a tile they
 //    fell into step, both softmaxes at once and the pipe idle: 5400 cycles a key tile).
@@ -52,12 +54,14 @@ constexpr int kTmaWarp = 8, kMmaWarp = 9, kLoadWarp = 10;
 constexpr int kLoadThreads = 128;
 constexpr int kThreads = 14 * 32;
 constexpr uint32_t kChunk = 128 * 128;        // 16 KB: 128 rows x 64 values
-constexpr int kSlots = 8;                     // ring of chunks
-constexpr int kPerTile = 5;                   // chunks a key tile: k_nope 0, 1, k_rope, v 0, 1
+constexpr int kSlotsK = 4, kPerTileK = 3;     // ring of K chunks; a key tile has k_nope 0, 1, k_rope
+constexpr int kSlotsV = 4, kPerTileV = 2;     // ring of V chunks; a key tile has keys 0-63, 64-127
 constexpr uint32_t kOffQ = 0;                 // [row tile][3 chunks]
-constexpr uint32_t kOffRing = 6 * kChunk;
-constexpr uint32_t kOffBar = kOffRing + kSlots * kChunk;
-enum { kBarQ = 0, kBarFull, kBarEmpty = kBarFull + kSlots, kBarS = kBarEmpty + kSlots, kBarP = kBarS + 2, kBarO = kBarP + 2,
+constexpr uint32_t kOffK = 6 * kChunk;
+constexpr uint32_t kOffV = kOffK + kSlotsK * kChunk;  // a chunk: [dim half][64 keys][128 B]
+constexpr uint32_t kOffBar = kOffV + kSlotsV * kChunk;
+enum { kBarQ = 0, kBarFullK, kBarFullV = kBarFullK + kSlotsK, kBarEmptyK = kBarFullV + kSlotsV,
+       kBarEmptyV = kBarEmptyK + kSlotsK, kBarS = kBarEmptyV + kSlotsV, kBarP = kBarS + 2, kBarO = kBarP + 2,
        kNumBars = kBarO + 2 };
 constexpr uint32_t kOffTmem = kOffBar + 8 * kNumBars;
 constexpr uint32_t kOffAbort = kOffTmem + 4;
@@ -70,7 +74,6 @@ constexpr float kRaise = 8.f;
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescQK = kIdesc | ((128u >> 3) << 17);
 constexpr uint32_t kIdescPV = kIdesc | ((128u >> 3) << 17) | (1u << 16);  // B (V) MN-major, 128 dims
-constexpr uint32_t kIdescPVHalf = kIdesc | ((64u >> 3) << 17) | (1u << 16);
 
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
     return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
@@ -141,9 +144,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + kOffAbort);
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i)
-            mbar_init(bar(i), i >= kBarFull && i < kBarEmpty ? kLoadThreads / 32
-                              : i >= kBarP && i < kBarO      ? 4
-                                                             : 1);
+            mbar_init(bar(i), i >= kBarFullV && i < kBarEmptyK ? kLoadThreads / 32
+                              : i >= kBarP && i < kBarO        ? 4
+                                                               : 1);
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -172,11 +175,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
     };
     auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool { return lanes_wait(b, parity); };
-    // Chunk j (5 per key tile) lies in slot j % 8, its use j / 8.
-    auto full = [&](int j) { return bar(kBarFull + j % kSlots); };
-    auto empty = [&](int j) { return bar(kBarEmpty + j % kSlots); };
-    auto slot_at = [&](int j) { return sbase + kOffRing + (j % kSlots) * kChunk; };
-    auto slot_free = [&](int j) { return j < kSlots || warp_wait(empty(j), ((j / kSlots) - 1) & 1); };
+    // K chunk j (three a key tile) lies in slot j % 4 as its use j / 4, V chunk j (two) the same.
+    auto full_k = [&](int j) { return bar(kBarFullK + j % kSlotsK); };
+    auto full_v = [&](int j) { return bar(kBarFullV + j % kSlotsV); };
+    auto empty_k = [&](int j) { return bar(kBarEmptyK + j % kSlotsK); };
+    auto empty_v = [&](int j) { return bar(kBarEmptyV + j % kSlotsV); };
 
     if (warp == kTmaWarp) {
         if (elect_one()) {
@@ -187,101 +190,98 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         bool ok = true;
-        for (int kt = 0; ok && kt < n_tiles; ++kt) {
-            for (int i = 0; i < 3; ++i) {
-                const int j = kPerTile * kt + i;
-                if (!(ok = slot_free(j))) break;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(full(j), kChunk);
-                    for (int k = 1; k < kLoadThreads / 32; ++k) mbar_arrive(full(j));  // (V has an arrival a warp)
-                    if (i < 2)
-                        tma_load_3d(slot_at(j), &kmap, full(j), 64 * i, h, k0 + kt * kKeys);
-                    else
-                        tma_load_2d(slot_at(j), &rmap, full(j), 0, k0 + kt * kKeys);
-                }
-                __syncwarp();
+        for (int j = 0; ok && j < kPerTileK * n_tiles; ++j) {
+            if (j >= kSlotsK && !(ok = warp_wait(empty_k(j), ((j / kSlotsK) - 1) & 1))) break;
+            const int kt = j / kPerTileK, i = j - kPerTileK * kt;
+            const uint32_t dst = sbase + kOffK + (j % kSlotsK) * kChunk;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(full_k(j), kChunk);
+                if (i < 2)
+                    tma_load_3d(dst, &kmap, full_k(j), 64 * i, h, k0 + kt * kKeys);
+                else
+                    tma_load_2d(dst, &rmap, full_k(j), 0, k0 + kt * kKeys);
             }
+            __syncwarp();
         }
     } else if (warp >= kLoadWarp) {
-        // V chunk i of a key tile: dims 64 i .. of keys; 8 threads a row, 16 rows at a time.
-        const int t = tid - kLoadWarp * 32, row = t >> 3, v = t & 7;
-        const uint32_t to = row * 128 + ((v ^ (row & 7)) << 4);
+        // V, 16 threads a row, 8 rows at a time; rows past the sequence's keys become zeros.
+        const int t = tid - kLoadWarp * 32, row = t >> 4, v = t & 15;
+        const uint32_t to = (v >> 3) * (kChunk / 2) + row * 128 + (((v & 7) ^ row) << 4);
         bool ok = true;
         for (int kt = 0; ok && kt < n_tiles; ++kt) {
-            const int left = k_len - kt * kKeys;
-            const uint16_t *src = static_cast<const uint16_t *>(p.v) + (static_cast<int64_t>(k0) + kt * kKeys + row) * p.k_row +
-                                  h * p.k_head + v * 8;
-            for (int i = 0; i < 2; ++i) {
-                const int j = kPerTile * kt + 3 + i;
-                if (!(ok = slot_free(j))) break;
-                const uint32_t dst = slot_at(j) + to;
+            for (int i = 0; i < kPerTileV; ++i) {
+                const int j = kPerTileV * kt + i, key = kt * kKeys + 64 * i + row;
+                if (j >= kSlotsV) ok = ok && warp_wait(empty_v(j), ((j / kSlotsV) - 1) & 1);
+                if (!ok) break;
+                const uint16_t *src = static_cast<const uint16_t *>(p.v) + (static_cast<int64_t>(k0) + key) * p.k_row +
+                                      h * p.k_head + v * 8;
+                const uint32_t dst = sbase + kOffV + (j % kSlotsV) * kChunk + to;
 #pragma unroll
                 for (int r = 0; r < 8; ++r)
-                    cp_async_16_or_zero(dst + r * 16 * 128, src + 64 * i + r * 16 * p.k_row, row + 16 * r < left);
+                    cp_async_16_or_zero(dst + r * 8 * 128, src + r * 8 * p.k_row, key + 8 * r < k_len);
                 asm volatile("cp.async.commit_group;" ::: "memory");
-            }
-            if (!ok) break;
-            // Landed, made visible to the tensor core, then an arrival a warp.
-            for (int i = 0; i < 2; ++i) {
-                if (i == 0)
+                // The chunk before has landed: made visible to the tensor core, an arrival a warp.
+                if (j > 0) {
                     asm volatile("cp.async.wait_group 1;" ::: "memory");
-                else
-                    asm volatile("cp.async.wait_group 0;" ::: "memory");
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full(kPerTile * kt + 3 + i));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full_v(j - 1));
+                }
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(full_v(kPerTileV * n_tiles - 1));
     } else if (warp == kMmaWarp) {
         // The warp runs whole on warp-uniform values, one elected lane issues: descriptors stay in uniform registers.
         const int nt0 = tile_nt(0), nt1 = tile_nt(1);
         const uint64_t q_desc = sw128_desc(sbase + kOffQ, 16, 1024);
-        const uint64_t kv_desc = sw128_desc(sbase + kOffRing, 16, 1024);
-        const uint64_t v_desc = sw128_desc(sbase + kOffRing, kChunk, 1024);  // 128 dims: two chunks side by side
+        const uint64_t k_desc = sw128_desc(sbase + kOffK, 16, 1024);
+        const uint64_t v_desc = sw128_desc(sbase + kOffV, kChunk / 2, 1024);  // 128 dims: two halves side by side
         bool ok = warp_wait(bar(kBarQ), 0);
-        // The warp waits for Q, K(0) and the weights only: the softmax warps look that V(k) and K(k + 1) have landed
-        // before they hand over P(k) (a wait costs this warp 100 cycles and more even when it need not wait).
-        for (int i = 0; i < 3; ++i) ok = ok && warp_wait(full(i), 0);
+        // Besides the weights the warp waits for K chunks only where it needs them first: the softmax warps look that
+        // V(k) and the first chunk of K(k + 1) have landed before they hand over P(k) (a wait costs this warp 100
+        // cycles and more even when it need not wait); the others are given until the MMAs before them are issued.
+        ok = ok && warp_wait(full_k(0), 0);
         auto score = [&](int t, int kt) {
+            const bool first_reader = t == 0 || kt >= nt0, last_reader = t == 1 || kt >= nt1;
             tc_fence_after();
             const uint64_t qd = q_desc + static_cast<uint32_t>(3 * t) * (kChunk >> 4);
-            if (elect_one()) {
+            const int j = kPerTileK * kt;
+            auto chunk = [&](int i) {
+                const uint64_t kd = k_desc + static_cast<uint32_t>((j + i) % kSlotsK) * (kChunk >> 4);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    const uint64_t kd = kv_desc + static_cast<uint32_t>((kPerTile * kt + i) % kSlots) * (kChunk >> 4);
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16(tmem + 128 * t, qd + i * (kChunk >> 4) + 2 * kk, kd + 2 * kk, kIdescQK, i > 0 || kk > 0);
+                if (last_reader) umma_commit(empty_k(j + i));
+            };
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_bf16(tmem + 128 * t, qd + i * (kChunk >> 4) + 2 * kk, kd + 2 * kk, kIdescQK, i > 0 || kk > 0);
+            for (int i = 0; i < 3; ++i) {
+                if (first_reader && i > 0) {
+                    ok = ok && warp_wait(full_k(j + i), ((j + i) / kSlotsK) & 1);
+                    tc_fence_after();
                 }
-                umma_commit(bar(kBarS + t));
-                if (t == 1 || kt >= nt1)  // K's last reader
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) umma_commit(empty(kPerTile * kt + i));
+                if (ok && elect_one()) {
+                    chunk(i);
+                    if (i == 2) umma_commit(bar(kBarS + t));
+                }
+                __syncwarp();
             }
-            __syncwarp();
         };
         auto value = [&](int t, int kt) {
             if (!(ok = ok && warp_wait(bar(kBarP + t), kt & 1))) return;
             tc_fence_after();
-            const int j = kPerTile * kt + 3;
-            const uint64_t vd = v_desc + static_cast<uint32_t>(j % kSlots) * (kChunk >> 4);
             const uint32_t o = tmem + kTmemO + 128 * t, w = tmem + 128 * t;
             if (elect_one()) {
-                if (j % kSlots != kSlots - 1) {
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        umma_bf16_tmem_a(o, w + 8 * ks, vd + ks * (2048 >> 4), kIdescPV, kt > 0 || ks > 0);
-                } else {  // the chunks lie at the ring's two ends: 64 dims at a time, at half the rate (66 cycles for either)
+                for (int i = 0; i < 2; ++i) {
+                    const int j = kPerTileV * kt + i;
+                    const uint64_t vd = v_desc + static_cast<uint32_t>(j % kSlotsV) * (kChunk >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        umma_bf16_tmem_a(o, w + 8 * ks, vd + ks * (2048 >> 4), kIdescPVHalf, kt > 0 || ks > 0);
-                        umma_bf16_tmem_a(o + 64, w + 8 * ks, v_desc + ks * (2048 >> 4), kIdescPVHalf, kt > 0 || ks > 0);
-                    }
-                }
-                if (t == 1 || kt >= nt1) {  // V's last reader
-                    umma_commit(empty(j));
-                    umma_commit(empty(j + 1));
+                    for (int ks = 0; ks < 4; ++ks)
+                        umma_bf16_tmem_a(o, w + 32 * i + 8 * ks, vd + ks * (2048 >> 4), kIdescPV, kt > 0 || i + ks > 0);
+                    if (t == 1 || kt >= nt1) umma_commit(empty_v(j));  // its last reader
                 }
                 if (kt == (t == 0 ? nt0 : nt1) - 1) umma_commit(bar(kBarO + t));
             }
@@ -393,9 +393,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_wait_st();
             if (quarter == 0 && (t == 0 || kt >= nt0)) {
-                // V(kt) and, for the S that follows, K(kt + 1): a lane a chunk.
-                const int j = kPerTile * kt + 3 + min(lane, kt + 1 < n_tiles ? 4 : 1);
-                alive = lanes_wait(full(j), (j / kSlots) & 1);
+                // V(kt) and, for the S that follows, the first chunk of K(kt + 1): a lane a chunk.
+                const int jv = kPerTileV * kt + (lane & 1), jk = kPerTileK * (kt + 1);
+                const bool of_k = lane == 2 && kt + 1 < n_tiles;
+                alive = lanes_wait(of_k ? full_k(jk) : full_v(jv), (of_k ? jk / kSlotsK : jv / kSlotsV) & 1);
             }
             tc_fence_before();
             __syncwarp();
