@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + kOffAbort);
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i)
-            mbar_init(bar(i), i >= kBarFullV && i < kBarEmptyK ? kLoadThreads / 32
+            mbar_init(bar(i), i == kBarQ || (i >= kBarFullV && i < kBarEmptyK) ? kLoadThreads / 32
                               : i >= kBarP && i < kBarO        ? 4
                                                                : 1);
         *abort_flag = 0u;
@@ -182,20 +182,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto empty_v = [&](int j) { return bar(kBarEmptyV + j % kSlotsV); };
 
     if (warp == kTmaWarp) {
-        if (elect_one()) {
-            mbar_arrive_expect_tx(bar(kBarQ), 6 * kChunk);
-            for (int t = 0; t < 2; ++t)
-                for (int i = 0; i < 3; ++i)
-                    tma_load_3d(sbase + kOffQ + (3 * t + i) * kChunk, &qmap, bar(kBarQ), 64 * i, h, q0 + r_lo + t * kRows);
-        }
-        __syncwarp();
         bool ok = true;
         for (int j = 0; ok && j < kPerTileK * n_tiles; ++j) {
             if (j >= kSlotsK && !(ok = warp_wait(empty_k(j), ((j / kSlotsK) - 1) & 1))) break;
             const int kt = j / kPerTileK, i = j - kPerTileK * kt;
             const uint32_t dst = sbase + kOffK + (j % kSlotsK) * kChunk;
             if (elect_one()) {
-                mbar_arrive_expect_tx(full_k(j), kChunk);
+                // The first row tile's Q comes with the first K, chunk by chunk: S starts after 32 KB.
+                mbar_arrive_expect_tx(full_k(j), kt == 0 ? 2 * kChunk : kChunk);
+                if (kt == 0) tma_load_3d(sbase + kOffQ + i * kChunk, &qmap, full_k(j), 64 * i, h, q0 + r_lo);
                 if (i < 2)
                     tma_load_3d(dst, &kmap, full_k(j), 64 * i, h, k0 + kt * kKeys);
                 else
@@ -204,8 +199,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
     } else if (warp >= kLoadWarp) {
+        const int t = tid - kLoadWarp * 32;
+        // The second row tile's Q: 8 threads a 64-value chunk of a row, 16 rows at a time (zeros past the last row).
+        if (tile_rows(1) > 0) {
+            const int row = t >> 3, v = t & 7, r1 = q0 + r_lo + kRows + row;
+            const uint16_t *src = static_cast<const uint16_t *>(p.q) + static_cast<int64_t>(r1) * p.q_row + h * p.q_head + v * 8;
+            const uint32_t dst = sbase + kOffQ + 3 * kChunk + row * 128 + ((v ^ (row & 7)) << 4);
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    cp_async_16_or_zero(dst + i * kChunk + r * 16 * 128, src + 64 * i + r * 16 * p.q_row, r1 + 16 * r < p.total_q);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
         // V, 16 threads a row, 8 rows at a time; rows past the sequence's keys become zeros.
-        const int t = tid - kLoadWarp * 32, row = t >> 4, v = t & 15;
+        const int row = t >> 4, v = t & 15;
         const uint32_t to = (v >> 3) * (kChunk / 2) + row * 128 + (((v & 7) ^ row) << 4);
         bool ok = true;
         for (int kt = 0; ok && kt < n_tiles; ++kt) {
@@ -220,13 +228,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int r = 0; r < 8; ++r)
                     cp_async_16_or_zero(dst + r * 8 * 128, src + r * 8 * p.k_row, key + 8 * r < k_len);
                 asm volatile("cp.async.commit_group;" ::: "memory");
-                // The chunk before has landed: made visible to the tensor core, an arrival a warp.
-                if (j > 0) {
-                    asm volatile("cp.async.wait_group 1;" ::: "memory");
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full_v(j - 1));
-                }
+                // What came before (Q, then the chunk before) has landed: made visible to the tensor core, an arrival a warp.
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(j == 0 ? bar(kBarQ) : full_v(j - 1));
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t q_desc = sw128_desc(sbase + kOffQ, 16, 1024);
         const uint64_t k_desc = sw128_desc(sbase + kOffK, 16, 1024);
         const uint64_t v_desc = sw128_desc(sbase + kOffV, kChunk / 2, 1024);  // 128 dims: two halves side by side
-        bool ok = warp_wait(bar(kBarQ), 0);
+        bool ok = true;
         // Besides the weights the warp waits for K chunks only where it needs them first: the softmax warps look that
         // V(k) and the first chunk of K(k + 1) have landed before they hand over P(k) (a wait costs this warp 100
         // cycles and more even when it need not wait); the others are given until the MMAs before them are issued.
@@ -290,6 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int kt = 0; ok && kt <= n_tiles; ++kt) {
             if (kt < nt0) score(0, kt);
             if (ok && kt >= 1 && kt - 1 < nt1) value(1, kt - 1);
+            if (kt == 0 && nt1 > 0) ok = ok && warp_wait(bar(kBarQ), 0);
             if (ok && kt < nt1) score(1, kt);
             if (ok && kt < nt0) value(0, kt);
         }

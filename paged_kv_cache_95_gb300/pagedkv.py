@@ -687,6 +687,10 @@ def paged_attention_decode_static_scratch(out, q, k_cache, v_cache, block_tables
 
 # ---- latent attention ---------------------------------------------------------------
 
+def _addr(t) -> int:
+    return t.data_ptr()
+
+
 def _check_rows(t, name, ndim, last, device):
     """A bf16 input whose rows (innermost dimension) are contiguous; the outer strides are free."""
     torch = _torch()
@@ -714,23 +718,26 @@ def _outer_stride(t, dim: int) -> int:
 
 def _device_and_stream(stream):
     """The current device, and `stream` (None: the current one) as the ABI takes it."""
-    c = _torch()._C
-    if not hasattr(c, "_cuda_getDevice"):
-        raise ValueError("the latent entry points need a CUDA device")
-    _torch().cuda.init()
-    device = c._cuda_getDevice()
-    return device, c._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    torch = _torch()
+    if not torch.cuda.is_initialized():
+        _need(torch.cuda.is_available(), "the latent entry points need a CUDA device")
+        torch.cuda.init()
+    device = torch._C._cuda_getDevice()
+    return device, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
 def latent_cache_desc(cache) -> LatentDesc:
     """Descriptor of a latent pool: bf16 [num_blocks, 16, 576], or FP8 E4M3 codes
     (torch.float8_e4m3fn or uint8) [num_blocks, 16, 512]."""
     torch = _torch()
-    fp8 = cache.dtype in (torch.uint8, torch.float8_e4m3fn)
-    _check(cache, "cache", cache.dtype if fp8 else torch.bfloat16, ndim=3)
+    dtype = cache.dtype
+    fp8 = dtype is torch.uint8 or dtype is torch.float8_e4m3fn
+    if not (cache.dim() == 3 and cache.is_cuda and cache.is_contiguous() and (fp8 or dtype is torch.bfloat16)):
+        _check(cache, "cache", dtype if fp8 else torch.bfloat16, ndim=3)
     blocks, slots, width = cache.shape
     want = LATENT_DIM if fp8 else LATENT_DIM + ROPE_DIM
-    _need(width == want, f"cache rows must have {want} values, got {width}")
+    if width != want:
+        _need(False, f"cache rows must have {want} values, got {width}")
     return LatentDesc(blocks, slots, LATENT_DIM, ROPE_DIM, PKV_DTYPE_FP8_E4M3 if fp8 else PKV_DTYPE_BF16)
 
 
@@ -746,8 +753,10 @@ def _latent_pool(cache, rope_cache, cache_scale, device):
         _check_on(rope_cache, "rope_cache", torch.bfloat16, 3, device)
         _check_on(cache_scale, "cache_scale", torch.float32, 2, device)
         shape = cache.shape[:2]
-        _need(rope_cache.shape[:2] == shape and rope_cache.shape[2] == ROPE_DIM, "rope_cache must be [num_blocks, 16, 64]")
-        _need(cache_scale.shape == shape, "cache_scale must be [num_blocks, 16]")
+        if rope_cache.shape[:2] != shape or rope_cache.shape[2] != ROPE_DIM:
+            _need(False, "rope_cache must be [num_blocks, 16, 64]")
+        if cache_scale.shape != shape:
+            _need(False, "cache_scale must be [num_blocks, 16]")
     return desc, fp8
 
 
@@ -767,8 +776,8 @@ def latent_reshape_and_cache(latent, rope, cache, slot_mapping, stream=None) -> 
     device, stream = _device_and_stream(stream)
     desc, fp8 = _latent_pool(cache, None, None, device)
     T = _check_latent_rows(latent, rope, slot_mapping, device)
-    rc = load_library().latent_reshape_and_cache(_ptr(latent), _outer_stride(latent, 0), _ptr(rope),
-                                                 _outer_stride(rope, 0), _ptr(cache), _ptr(slot_mapping), T,
+    rc = load_library().latent_reshape_and_cache(_addr(latent), _outer_stride(latent, 0), _addr(rope),
+                                                 _outer_stride(rope, 0), _addr(cache), _addr(slot_mapping), T,
                                                  ctypes.byref(desc), stream)
     _raise("latent_reshape_and_cache", rc)
 
@@ -779,9 +788,9 @@ def latent_reshape_and_cache_fp8(latent, rope, cache, rope_cache, cache_scale, s
     device, stream = _device_and_stream(stream)
     desc, fp8 = _latent_pool(cache, rope_cache, cache_scale, device)
     T = _check_latent_rows(latent, rope, slot_mapping, device)
-    rc = load_library().latent_reshape_and_cache_fp8(_ptr(latent), _outer_stride(latent, 0), _ptr(rope),
-                                                     _outer_stride(rope, 0), _ptr(cache), _ptr(rope_cache),
-                                                     _ptr(cache_scale), _ptr(slot_mapping), T, ctypes.byref(desc),
+    rc = load_library().latent_reshape_and_cache_fp8(_addr(latent), _outer_stride(latent, 0), _addr(rope),
+                                                     _outer_stride(rope, 0), _addr(cache), _addr(rope_cache),
+                                                     _addr(cache_scale), _addr(slot_mapping), T, ctypes.byref(desc),
                                                      stream)
     _raise("latent_reshape_and_cache_fp8", rc)
 
@@ -802,10 +811,10 @@ def latent_gather(out, cache, block_tables, cu_lens, rope_cache=None, cache_scal
     _need(cu_lens.shape[0] == B + 1, "cu_lens must be [num_seqs + 1]")
     if status is not None:
         _check_on(status, "status", torch.int32, 1, device)
-    rc = load_library().latent_gather(_ptr(out), _ptr(cache), _ptr(rope_cache) if fp8 else None,
-                                      _ptr(cache_scale) if fp8 else None, _ptr(block_tables), _ptr(cu_lens), B,
+    rc = load_library().latent_gather(_addr(out), _addr(cache), _addr(rope_cache) if fp8 else None,
+                                      _addr(cache_scale) if fp8 else None, _addr(block_tables), _addr(cu_lens), B,
                                       int(block_tables.shape[1]), int(out.shape[0]), ctypes.byref(desc),
-                                      _ptr(status) if status is not None else None, stream)
+                                      _addr(status) if status is not None else None, stream)
     _raise("latent_gather", rc)
 
 
@@ -842,16 +851,16 @@ def latent_attention_decode(out, q_latent, q_rope, cache, block_tables, context_
         _need(nbytes > 0, "invalid sizes for latent_attention_decode")
         workspace = torch.zeros(nbytes, dtype=torch.uint8, device=out.device)  # status word starts clear
     _check_on(workspace, "workspace", torch.uint8, 1, device)
-    ql = (_ptr(q_latent), _outer_stride(q_latent, 0), _outer_stride(q_latent, 1))
-    qr = (_ptr(q_rope), _outer_stride(q_rope, 0), _outer_stride(q_rope, 1))
-    tail = (_ptr(block_tables), _ptr(context_lens), B, k, int(heads), max_blocks, float(scale), ctypes.byref(desc),
-            _ptr(workspace), int(workspace.numel()), stream)
+    ql = (_addr(q_latent), _outer_stride(q_latent, 0), _outer_stride(q_latent, 1))
+    qr = (_addr(q_rope), _outer_stride(q_rope, 0), _outer_stride(q_rope, 1))
+    tail = (_addr(block_tables), _addr(context_lens), B, k, int(heads), max_blocks, float(scale), ctypes.byref(desc),
+            _addr(workspace), int(workspace.numel()), stream)
     if fp8:
-        rc = lib.latent_attention_decode_fp8(_ptr(out), _out_dtype(out), *ql, *qr, _ptr(cache), _ptr(rope_cache),
-                                             _ptr(cache_scale), *tail)
+        rc = lib.latent_attention_decode_fp8(_addr(out), _out_dtype(out), *ql, *qr, _addr(cache), _addr(rope_cache),
+                                             _addr(cache_scale), *tail)
         _raise("latent_attention_decode_fp8", rc)
     else:
-        rc = lib.latent_attention_decode(_ptr(out), _out_dtype(out), *ql, *qr, _ptr(cache), *tail)
+        rc = lib.latent_attention_decode(_addr(out), _out_dtype(out), *ql, *qr, _addr(cache), *tail)
         _raise("latent_attention_decode", rc)
     return workspace
 
@@ -892,10 +901,10 @@ def latent_attention_prefill_chunk(out, q, k_nope, v, k_rope, cu_q_lens, cu_k_le
         _need(nbytes > 0, "invalid sizes for latent_attention_prefill_chunk")
         workspace = torch.zeros(nbytes, dtype=torch.uint8, device=out.device)  # status word starts clear
     _check_on(workspace, "workspace", torch.uint8, 1, device)
-    rc = lib.latent_attention_prefill_chunk(_ptr(out), _out_dtype(out), _ptr(q), _outer_stride(q, 0),
-                                            _outer_stride(q, 1), _ptr(k_nope), _ptr(v), *k_strides, _ptr(k_rope),
-                                            _outer_stride(k_rope, 0), _ptr(cu_q_lens), _ptr(cu_k_lens), B, int(heads),
-                                            int(max_q_len), int(tq), tk, float(scale), _ptr(workspace),
+    rc = lib.latent_attention_prefill_chunk(_addr(out), _out_dtype(out), _addr(q), _outer_stride(q, 0),
+                                            _outer_stride(q, 1), _addr(k_nope), _addr(v), *k_strides, _addr(k_rope),
+                                            _outer_stride(k_rope, 0), _addr(cu_q_lens), _addr(cu_k_lens), B, int(heads),
+                                            int(max_q_len), int(tq), tk, float(scale), _addr(workspace),
                                             int(workspace.numel()), stream)
     _raise("latent_attention_prefill_chunk", rc)
     return workspace
