@@ -312,6 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
     };
 
+    // The pool passes through L2 once (column tiles of one range read it at about the same time): its lines go first.
+    const uint64_t policy = l2_evict_first();
+
     if (warp == kProducerWarp) {
         // ---------------- TMA producer: lane j copies block j of a tile ----------------
         Walk<L> w;
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t full = bar(L::kBarKvFull + st), stage = sbase + L::kKv + st * L::kStage;
                     mbar_arrive_expect_tx(full, cur >= 0 ? L::kBlock + L::kRopeBlock : 0);
                     if (cur >= 0) {
-                        tma_load_5d(stage + j * L::kBlock, &kvmap, full, 0, 0, 0, 0, cur);
+                        tma_load_5d(stage + j * L::kBlock, &kvmap, full, 0, 0, 0, 0, cur, policy);
                         if constexpr (FP8)
                             tma_load_3d(stage + kTileBlocks * L::kBlock + j * L::kRopeBlock, &ropemap, full, 0, 0, cur);
                     }
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint8_t *src = static_cast<const uint8_t *>(p.cache) + static_cast<size_t>(blk) * L::kBlock + 16 * t;
 #pragma unroll
                     for (int k = 0; k < 2 * kSteps; ++k)
-                        cp_async_16(dst + (k / kSteps) * L::kGroup + to[k % kSteps], src + 1024 * k);
+                        cp_async_16(dst + (k / kSteps) * L::kGroup + to[k % kSteps], src + 1024 * k, policy);
                     if constexpr (FP8) {  // 8 vectors of rotated key a slot, and the 16 scales
                         const uint8_t *rope = static_cast<const uint8_t *>(p.rope_cache) + static_cast<size_t>(blk) * L::kRopeBlock + 16 * t;
                         const uint32_t rdst = stage + kTileBlocks * L::kBlock + j * L::kRopeBlock + (t >> 3) * 128 +
