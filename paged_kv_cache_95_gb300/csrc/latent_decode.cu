@@ -69,7 +69,13 @@ struct Layout {
     static constexpr uint32_t kBlock = 2 * kGroup;
     static constexpr uint32_t kRopeBlock = FP8 ? kBlockSize * 128 : 0;
     static constexpr uint32_t kStage = kTileBlocks * (kBlock + kRopeBlock);
-    static constexpr int kStages = FP8 ? 3 : 128 / TILE;
+    // FP8, up to 32 columns: the E4M3 heads and remainders of Q are rows of one product (a remainder 8 rows behind its
+    // head, in rows that M = 64 has anyway, and in the same thread after the load), those of P columns of one product
+    // (a remainder NCOL behind): an MMA of few columns is bound by its other operand, M = 128 takes 43 cycles with N =
+    // 32 and 52 with 64.  Two products for 64 columns: O has no room for 128.
+    static constexpr bool kStack = FP8 && NCOL <= 32;
+    static constexpr int kOCols = kStack ? 2 * NCOL : NCOL;  // columns of a dim tile's O
+    static constexpr int kStages = FP8 ? (kStack ? 4 : 3) : 128 / TILE;
     // What beginning another sequence costs a range, in tiles: its Q, the epilogue of the one before.
     static constexpr int kLead = FP8 ? 4 : 128 / TILE;
     // M = 64: rows 16 q .. 16 q + 15 of S lie in tensor-memory lanes 32 q .., which only warps w % 4 = q reach, one
@@ -77,12 +83,15 @@ struct Layout {
     static constexpr int kPerQuarter = NCOL / 4, kRowsPerThread = NCOL == 64 ? 2 : 1;
     // Score columns of a tile (FP8: the latent's and the rotated key's products apart, the scale goes with the first).
     static constexpr uint32_t kScoreCols = FP8 ? 128 : 64;
-    // Q: [9 chunks][64 rows][128 B]; FP8: 4 chunks of heads, 4 of remainders (E4M3), the rotated part in bf16.
+    // Q: [chunks][64 rows][128 B]; FP8: 4 chunks of heads, 4 of remainders (E4M3; stacked: 4 of both), the rotated part
+    // in bf16.
     static constexpr uint32_t kQChunk = 64 * 128;
+    static constexpr int kQChunks = kStack ? 5 : 9;
     static constexpr uint32_t kQ = 0;
-    static constexpr uint32_t kKv = kQ + 9 * kQChunk;
-    static constexpr uint32_t kP = kKv + kStages * kStage;  // [NCOL][64 bf16], or [NCOL][64 heads | 64 remainders]
-    static constexpr uint32_t kScale = kP + NCOL * 128;     // FP8: [stage][scale, its log2, its inverse][64 keys]
+    static constexpr uint32_t kKv = kQ + kQChunks * kQChunk;
+    // P: [NCOL][64 bf16], or [NCOL][64 heads | 64 remainders], stacked [heads, remainders][NCOL][64 codes, 64 unused].
+    static constexpr uint32_t kP = kKv + kStages * kStage;
+    static constexpr uint32_t kScale = kP + kOCols * 128;  // FP8: [stage][scale, its log2, its inverse][64 keys]
     static constexpr uint32_t kQf = kScale + (FP8 ? kStages * 3 * TILE * 4 : 0);  // FP8: [64] factors of the columns
     // kv_full[stage], kv_empty[stage][block], s_full[2], s_empty[2], p_full, pv_done, q_full
     static constexpr int kBarKvFull = 0, kBarKvEmpty = kStages, kBarSFull = kBarKvEmpty + kStages * kTileBlocks,
@@ -433,13 +442,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t rd = r_desc + static_cast<uint32_t>(st) * (L::kStage >> 4);
             if (elect_one()) {
 #pragma unroll
-                for (int c = 0; c < 9; ++c)
+                for (int c = 0; c < L::kQChunks; ++c)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         const uint64_t qd = q_desc + ((c * L::kQChunk + kk * 32) >> 4);
                         if constexpr (!FP8)
                             umma_bf16(d, qd, kd + ((c * 1024 + kk * 32) >> 4), idesc(64, kTile, false), c + kk > 0);
-                        else if (c < 8)  // heads, then remainders, against the same codes
+                        else if (c < L::kQChunks - 1)  // heads (and stacked remainders), then remainders, against the same codes
                             umma_e4m3(d, qd, kd + (((c & 3) * 1024 + kk * 32) >> 4), idesc(64, kTile, false, true), c + kk > 0);
                         else
                             umma_bf16(d + 64, qd, rd + ((kk * 32) >> 4), idesc(64, kTile, false), kk > 0);
@@ -477,8 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             const uint64_t v = vd + ((ks * 2 * L::kBlock + m * 1024) >> 4), w8 = p_desc + ((ks * 32) >> 4);
-                            umma_e4m3(tmem + m * NCOL, v, w8, idesc(128, NCOL, true, true), ks > 0 ? 1u : keep);
-                            umma_e4m3(tmem + m * NCOL, v, w8 + (64 >> 4), idesc(128, NCOL, true, true), 1u);
+                            umma_e4m3(tmem + m * L::kOCols, v, w8, idesc(128, L::kOCols, true, true), ks > 0 ? 1u : keep);
+                            if constexpr (!L::kStack)
+                                umma_e4m3(tmem + m * NCOL, v, w8 + (64 >> 4), idesc(128, NCOL, true, true), 1u);
                         }
                         umma_commit(bar(L::kBarKvEmpty + st * kTileBlocks + 2 * ks));
                         umma_commit(bar(L::kBarKvEmpty + st * kTileBlocks + 2 * ks + 1));
@@ -503,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < kR; ++k) q_row[k] = col0 + 8 * k < nc ? (c0 + col0 + 8 * k) / p.heads : p.q_per_seq - 1;
         // P: where this thread's pair of keys of 8-key group j goes, p_at[.] (+ 1024 for row k = 1).  bf16: a pair is 4
-        // bytes, group j the 16-byte chunk 4 half + j.  FP8: 2 bytes, chunk 2 half + j / 2, remainders 64 bytes on.
+        // bytes, group j the 16-byte chunk 4 half + j.  FP8: 2 bytes, chunk 2 half + j / 2, remainders 64 bytes on or
+        // (stacked) NCOL rows.
         auto p_at = [&](int j) {
             const int v = FP8 ? 2 * half + (j >> 1) : kGroups * half + j;
             return sbase + L::kP + col0 * 128 + ((v ^ (col0 & 7)) << 4) + (FP8 ? 8 * (j & 1) + 2 * (lane & 3) : 4 * (lane & 3));
@@ -570,8 +581,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 f32x2_to_e4m3x2(v[4 * k + 2] * up - f1.x, v[4 * k + 3] * up - f1.y) << 16;
                     }
                     sts128(at(lane >> 3, lane & 7), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                    sts128(at(4 + (lane >> 3), lane & 7), make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                    if (lane < 8) sts128(at(8, lane), rope);
+                    sts128(L::kStack ? at(lane >> 3, lane & 7) + 8 * 128 : at(4 + (lane >> 3), lane & 7),
+                           make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    if (lane < 8) sts128(at(L::kQChunks - 1, lane), rope);
                     if (lane == 0) qf_s[r] = __uint_as_float(static_cast<uint32_t>(127 - lift) << 23);
                 }
             }
@@ -650,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float2 sc = lds_f32x2(sc_at + 32 * j), lg = lds_f32x2(sc_at + kTile * 4 + 32 * j);
 #pragma unroll
                         for (int k = 0; k < kR; ++k)
-                            x[k][j] = ffma2(pair(v, j, k), fmul2(sc, make_float2(q_scale[k], q_scale[k])),
+                            x[k][j] = ffma2(L::kStack ? fadd2(pair(v, j, 0), pair(v, j, 1)) : pair(v, j, k), fmul2(sc, make_float2(q_scale[k], q_scale[k])),
                                             ffma2(pair(u, j, k), sl2, lg));
                     }
                 }
@@ -715,9 +727,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (alive) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < 2 * NCOL; c += 16) {  // dim tiles 2 half, 2 half + 1
+                        for (int c = 0; c < 2 * L::kOCols; c += 16) {  // dim tiles 2 half, 2 half + 1
                             uint32_t o[16];
-                            const uint32_t at = tmem + lanes + 2 * half * NCOL + c;
+                            const uint32_t at = tmem + lanes + 2 * half * L::kOCols + c;
                             tmem_ld_32x32b_x16(at, o);
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
@@ -757,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const uint32_t at = p_at(j) + 1024 * k;
                             if constexpr (FP8) {
                                 sts16(at, pk[k][j]);
-                                sts16(at ^ 64u, pk[k][j] >> 16);
+                                sts16(L::kStack ? at + NCOL * 128 : at ^ 64u, pk[k][j] >> 16);
                             } else {
                                 sts32(at, pk[k][j]);
                             }
@@ -824,7 +836,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int c = 0; c < 2 * NCOL; c += 16) {
                         uint32_t o[16];
-                        tmem_ld_32x32b_x16(tmem + lanes + 2 * half * NCOL + c, o);
+                        const uint32_t o_at = tmem + lanes + (2 * half + c / NCOL) * L::kOCols + c % NCOL;
+                        tmem_ld_32x32b_x16(o_at, o);
+                        if constexpr (L::kStack) {
+                            uint32_t rest[16];
+                            tmem_ld_32x32b_x16(o_at + NCOL, rest);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(rest[e]));
+                        }
                         const int col = c % NCOL, dim = (2 * half + c / NCOL) * 128 + 32 * quarter + lane;
                         if (!whole) {
                             float *dst = p.part_o + (slot + col) * kLatentDim + dim;
