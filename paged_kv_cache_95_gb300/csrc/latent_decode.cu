@@ -53,6 +53,7 @@ constexpr int kScoreWarp = kSoftWarps + 1;    // issues S = Q K^T
 constexpr int kValueWarp = kSoftWarps + 2;    // issues O^T += V^T P^T
 constexpr int kLoadWarp = kSoftWarps + 3;     // two pairs of copying warps, one pair a stage
 constexpr int kThreads = (kSoftWarps + 7) * 32;
+constexpr int kMaxLeft = 1 << 20;  // of a tile's record; past the tile and 16 rows the keys are all the same
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // O^T in columns [0, 4 NCOL), the scores of tile i from 256 + (i & 1) kScoreCols on
 
@@ -89,24 +90,31 @@ struct Layout {
     static constexpr int kQChunks = kStack ? 5 : 9;
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kKv = kQ + kQChunks * kQChunk;
-    // P: [NCOL][64 bf16], or [NCOL][64 heads | 64 remainders], stacked [heads, remainders][NCOL][64 codes, 64 unused].
+    // P, two buffers in turn: [NCOL][64 bf16], or [NCOL][64 heads | 64 remainders]; rows of 64 bytes (32 keys, or stacked
+    // [heads, remainders][NCOL][64 codes]) lie side by side.
     static constexpr uint32_t kP = kKv + kStages * kStage;
-    static constexpr uint32_t kScale = kP + kOCols * 128;  // FP8: [stage][scale, its log2, its inverse][64 keys]
+    static constexpr bool kPHalf = kStack || (!FP8 && TILE == 32);
+    static constexpr uint32_t kPBuf = kPHalf ? 64 : NCOL * 128;
+    static constexpr uint32_t kScale = kP + (kPHalf ? 1 : 2) * kOCols * 128;  // FP8: [stage][scale, its log2, its inverse][64 keys]
     static constexpr uint32_t kQf = kScale + (FP8 ? kStages * 3 * TILE * 4 : 0);  // FP8: [64] factors of the columns
-    // kv_full[stage], kv_empty[stage][block], s_full[2], s_empty[2], p_full, pv_done, q_full
+    // kv_full[stage], kv_empty[stage][block], s_full[2], s_empty[2], p_full[2], pv_done[2], q_full
     static constexpr int kBarKvFull = 0, kBarKvEmpty = kStages, kBarSFull = kBarKvEmpty + kStages * kTileBlocks,
-                         kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 2, kBarPvDone = kBarPFull + 1,
-                         kBarQFull = kBarPvDone + 1, kNumBars = kBarQFull + 1;
+                         kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 2, kBarPvDone = kBarPFull + 2,
+                         kBarQFull = kBarPvDone + 2, kNumBars = kBarQFull + 1;
     static constexpr uint32_t kBar = kQf + (FP8 ? 64 * 4 : 0);
     static constexpr uint32_t kTmemSlot = kBar + 8 * kNumBars;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kXch = (kAbort + 4 + 15) / 16 * 16;  // [tile & 1][key half][64] maxima, later sums
     static constexpr uint32_t kAlpha = kXch + 4 * 64 * 4;          // [64] factors of O's columns
     static constexpr uint32_t kPlan = kAlpha + 64 * 4;             // warp totals, then the range's start
-    static constexpr uint32_t kBytes = kPlan + 18 * 8;
+    // What softmax has to know of a stage's tile, by the warps that copy it: {keys left and the invalid blocks, tiles
+    // left, sequence, next tile's sequence}.  (Walking the tiles itself cost softmax 240 cycles a tile, of 1600.)
+    static constexpr uint32_t kInfo = kPlan + 18 * 8;
+    static constexpr uint32_t kDead = kInfo + kStages * 16;  // [tile & 1]: a softmax warp's wait ran out
+    static constexpr uint32_t kBytes = kDead + 8;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
     static_assert(kKv % 1024 == 0 && kP % 1024 == 0 && kStage % 1024 == 0, "swizzle atoms");
-    static_assert(kScale % 16 == 0 && kBar % 8 == 0 && kPlan % 8 == 0, "alignment");
+    static_assert(kScale % 16 == 0 && kBar % 8 == 0 && kPlan % 8 == 0 && kInfo % 16 == 0, "alignment");
     // A weight may pass the reference by 2^kRaise before the reference follows.  FP8 keeps the weights as pairs of
     // E4M3 codes: 2^2 at the reference, so 2^8 at most (448 is the largest code) and steps of 2^-9 below.  (2^4 and
     // 2^4: on the verify of 64 columns a reference was raised in every second tile, 1900 cycles each.)
@@ -204,8 +212,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < L::kNumBars; ++i)
             mbar_init(bar(i), i < L::kBarKvEmpty ? kTmaBlocks + 2
-                              : i == L::kBarSEmpty || i == L::kBarSEmpty + 1 || i == L::kBarPFull || i == L::kBarQFull ? kSoftWarps : 1);
+                              : (i >= L::kBarSEmpty && i < L::kBarPvDone) || i == L::kBarQFull ? kSoftWarps : 1);
         *abort_flag = 0u;
+        *reinterpret_cast<uint2 *>(smem + L::kDead) = make_uint2(0u, 0u);
         *first_tile = ~0ull;
         *tile_count = 0;
         fence_mbar_init();
@@ -307,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A warp's bounded wait; it gives up soon after another role did.  The timer and the flag are
     // read only every 64 tries: a read of %globaltimer between two tries delays the waiter by
     // several hundred cycles.
+    // (Each lane may name a barrier of its own: one wait for several costs what one does.)
     auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
         uint64_t t_first = 0;
         for (uint32_t tries = 0; !__all_sync(0xffffffffu, mbar_try_wait(b, parity)); ++tries) {
@@ -377,9 +387,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int st = i % kStages;
             int id = -1;
             const int jb = w.t * kTileBlocks + lane;
-            if (lane < kTileBlocks && jb * kBlockSize < w.keys)
-                id = __ldg(p.block_tables + static_cast<size_t>(w.b) * p.max_blocks + jb);
+            const bool exists = lane < kTileBlocks && jb * kBlockSize < w.keys;
+            if (exists) id = __ldg(p.block_tables + static_cast<size_t>(w.b) * p.max_blocks + jb);
             if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks)) id = -1;
+            const uint32_t bad = __ballot_sync(0xffffffffu, exists && id < 0);
+            int4 info = make_int4(min(w.keys - w.t * kTile, kMaxLeft) | static_cast<int>(bad << 24), w.nt - 1 - w.t, w.b, w.b);
             bool ok = true;
 #pragma unroll
             for (int j = kTmaBlocks; j < kTileBlocks; ++j) {
@@ -411,7 +423,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 at[kTile] = __log2f(sc);
                 at[2 * kTile] = __fdividef(1.f, sc);
             }
-            for (int k = 0; k < 2 && i + 1 + k < n; ++k) w.next(p);
+            if (i + 1 < n) w.next(p);
+            info.w = w.b;
+            if (i + 2 < n) w.next(p);
+            if (t == 0) *reinterpret_cast<int4 *>(smem + L::kInfo + 16 * st) = info;
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();  // generic writes -> the tensor core
             __syncwarp();
@@ -430,12 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         int pieces = 0;
         for (int i = 0; i < n; ++i) {
             const int st = i % kStages;
-            if (i == 0 || w.t == 0) {
-                if (!warp_wait(bar(L::kBarQFull), pieces & 1)) break;
-                ++pieces;
-            }
-            if (i >= 2 && !warp_wait(bar(L::kBarSEmpty + (i & 1)), ((i >> 1) - 1) & 1)) break;
-            if (!warp_wait(bar(L::kBarKvFull + st), (i / kStages) & 1)) break;
+            // The tile; S's buffer, free after softmax (i - 2) has read it; a sequence's first tile: its Q.
+            const bool of_s = lane == 1 && i >= 2, of_q = lane == 2 && (i == 0 || w.t == 0);
+            if (!warp_wait(bar(of_s   ? L::kBarSEmpty + (i & 1)
+                               : of_q ? L::kBarQFull
+                                      : L::kBarKvFull + st),
+                           (of_s ? (i >> 1) - 1 : of_q ? pieces : i / kStages) & 1))
+                break;
+            pieces += i == 0 || w.t == 0;
             tc_fence_after();
             const uint32_t d = tmem + kTmemS + L::kScoreCols * (i & 1);
             const uint64_t kd = k_desc + static_cast<uint32_t>(st) * (L::kStage >> 4);
@@ -467,16 +484,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n; ++i) {
             const int st = i % kStages;
             const uint32_t keep = i > 0 && w.t > 0;  // a piece's first P V overwrites O
-            if (!warp_wait(bar(L::kBarPFull), i & 1)) break;
+            if (!warp_wait(bar(L::kBarPFull + (i & 1)), (i >> 1) & 1)) break;
             tc_fence_after();
             const uint64_t vd = v_desc + static_cast<uint32_t>(st) * (L::kStage >> 4);
+            const uint64_t pd = p_desc + static_cast<uint32_t>(i & 1) * (L::kPBuf >> 4);
             if (elect_one()) {
                 if constexpr (!FP8) {
 #pragma unroll
                     for (int ks = 0; ks < kTileBlocks; ++ks) {
 #pragma unroll
                         for (int m = 0; m < 4; ++m)
-                            umma_bf16(tmem + m * NCOL, vd + ((ks * L::kBlock + m * 2048) >> 4), p_desc + ((ks * 32) >> 4),
+                            umma_bf16(tmem + m * NCOL, vd + ((ks * L::kBlock + m * 2048) >> 4), pd + ((ks * 32) >> 4),
                                       idesc(128, NCOL, true), ks > 0 ? 1u : keep);
                         umma_commit(bar(L::kBarKvEmpty + st * kTileBlocks + ks));
                     }
@@ -485,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
-                            const uint64_t v = vd + ((ks * 2 * L::kBlock + m * 1024) >> 4), w8 = p_desc + ((ks * 32) >> 4);
+                            const uint64_t v = vd + ((ks * 2 * L::kBlock + m * 1024) >> 4), w8 = pd + ((ks * 32) >> 4);
                             umma_e4m3(tmem + m * L::kOCols, v, w8, idesc(128, L::kOCols, true, true), ks > 0 ? 1u : keep);
                             if constexpr (!L::kStack)
                                 umma_e4m3(tmem + m * NCOL, v, w8 + (64 >> 4), idesc(128, NCOL, true, true), 1u);
@@ -494,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         umma_commit(bar(L::kBarKvEmpty + st * kTileBlocks + 2 * ks + 1));
                     }
                 }
-                umma_commit(bar(L::kBarPvDone));
+                umma_commit(bar(L::kBarPvDone + (i & 1)));
             }
             __syncwarp();
             if (i + 1 < n) w.next(p);
@@ -595,26 +613,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bar(L::kBarQFull));
         };
 
-        Walk<L> w;
-        w.at(p, b0, t0);
-        load_q(w.b);
+        load_q(b0);
         empty_sequences(tid, kSoftThreads);
         publish_q();
         if constexpr (FP8) soft_sync();  // the factors of Q's rows are written
         float q_scale[kR] = {};          // FP8: those of this thread's columns, times the softmax scale
         float m_ref[kR];
         float2 l[kR];
-        auto block_id = [&](const Walk<L> &a) {  // lane j: the id of block j of a tile (0 past the context)
-            const int jb = a.t * kTileBlocks + lane;
-            return lane < kTileBlocks && jb * kBlockSize < a.keys
-                       ? __ldg(p.block_tables + static_cast<size_t>(a.b) * p.max_blocks + jb)
-                       : 0;
-        };
-        int id = block_id(w);     // read a tile ahead: S may be waiting already
         bool piece_mid = t0 > 0;  // the piece does not hold its sequence's first key
+        bool first = true;        // of its piece
         for (int i = 0; i < n; ++i) {
-            const bool first = i == 0 || w.t == 0;
-            const bool last = i == n - 1 || w.t == w.nt - 1;
+            // FP8: c_j = code s_j, so the score is s_j <q, code_j> + <q_rope, r_j>, and the weight that multiplies the
+            // codes is s_j 2^score = 2^(score + log2 s_j); the sum l takes it times 1 / s_j.
+            const uint32_t sc_at = sbase + L::kScale + ((i % kStages) * 3 * kTile + kTile / 2 * half + 2 * (lane & 3)) * 4;
+            // S; the tile's record and scales; P's buffer, free after P V (i - 2).
+            const bool of_kv = lane == 1, of_p = lane == 2 && i >= 2;
+            alive = alive && warp_wait(bar(of_kv  ? L::kBarKvFull + i % kStages
+                                           : of_p ? L::kBarPvDone + (i & 1)
+                                                  : L::kBarSFull + (i & 1)),
+                                       (of_kv ? i / kStages : of_p ? (i >> 1) - 1 : i >> 1) & 1);
+            const int4 info = alive ? lds_i32x4(sbase + L::kInfo + 16 * (i % kStages)) : make_int4(0, 0, 0, 0);
+            const int left = info.x & 0xffffff;  // keys of the tile that exist (may pass its size)
+            const uint32_t bad = static_cast<uint32_t>(info.x) >> 24;  // its blocks with an invalid id: flagged, their keys masked
+            const bool ends = info.y == 0, last = i == n - 1 || ends;
+            if (bad && tid == 0) atomicOr(p.status, kStatusBadBlockId);
             if (first) {
 #pragma unroll
                 for (int k = 0; k < kR; ++k) {
@@ -623,16 +645,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (FP8) q_scale[k] = live ? qf_s[col0 + 8 * k] * p.scale_log2 : 0.f;
                 }
             }
-            // Blocks of the tile with an invalid id: flagged, their keys masked.
-            const uint32_t bad = __ballot_sync(0xffffffffu, static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks));
-            if (bad && tid == 0) atomicOr(p.status, kStatusBadBlockId);
-            const int left = w.keys - w.t * kTile;  // keys of the tile that exist (may pass 64)
-
-            // FP8: c_j = code s_j, so the score is s_j <q, code_j> + <q_rope, r_j>, and the weight that multiplies the
-            // codes is s_j 2^score = 2^(score + log2 s_j); the sum l takes it times 1 / s_j.
-            if (FP8) alive = alive && warp_wait(bar(L::kBarKvFull + i % kStages), (i / kStages) & 1);  // (the scales)
-            const uint32_t sc_at = sbase + L::kScale + ((i % kStages) * 3 * kTile + kTile / 2 * half + 2 * (lane & 3)) * 4;
-            alive = alive && warp_wait(bar(L::kBarSFull + (i & 1)), (i >> 1) & 1);
             float2 x[kR][kGroups];  // [k][j]: row k, keys kTile / 2 half + 8 j + 2 (lane % 4) + 0, 1
             float mx[kR];
 #pragma unroll
@@ -691,12 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (alive && lane == 0) mbar_arrive(bar(L::kBarSEmpty + (i & 1)));
             // The last S of a piece is complete: its Q can make way for the next sequence's.
             const bool more = last && i + 1 < n;
-            Walk<L> nx = w;
-            if (i + 1 < n) {
-                nx.next(p);
-                id = block_id(nx);
-            }
-            if (more && alive) load_q(nx.b);
+            if (more && alive) load_q(info.w);
 
             float *xm = xch + (i & 1) * 128;
             bool pass = false;
@@ -705,8 +712,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (has) xm[half * 64 + col0 + 8 * k] = mx[k];
                 pass = pass || (live && mx[k] > m_ref[k] + L::kRaise);
             }
-            bool drained = false;  // this warp saw P V (i - 1) complete
-            if (bar_red_or(1, kSoftThreads, pass)) {
+            // A warp whose wait ran out does not know the tile: all of them leave here.
+            volatile uint32_t *dead = reinterpret_cast<volatile uint32_t *>(smem + L::kDead) + (i & 1);
+            if (!alive && lane == 0) *dead = 1u;
+            if (bar_red_or(1, kSoftThreads, pass || !alive)) {
+                if (*dead) break;
                 if (live) {
 #pragma unroll
                     for (int k = 0; k < kR; ++k) {
@@ -722,8 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!first) {  // (the first P V of a piece overwrites O)
                     soft_sync();
-                    alive = alive && warp_wait(bar(L::kBarPvDone), (i - 1) & 1);
-                    drained = true;
+                    alive = alive && warp_wait(bar(L::kBarPvDone + ((i - 1) & 1)), ((i - 1) >> 1) & 1);
                     if (alive) {
                         tc_fence_after();
 #pragma unroll 1
@@ -759,14 +768,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (i > 0 && !drained) alive = alive && warp_wait(bar(L::kBarPvDone), (i - 1) & 1);  // P is free again
             if (alive) {
+                const uint32_t buf = (i & 1) * L::kPBuf;
                 if (live) {
 #pragma unroll
                     for (int j = 0; j < kGroups; ++j)
 #pragma unroll
                         for (int k = 0; k < kR; ++k) {
-                            const uint32_t at = p_at(j) + 1024 * k;
+                            const uint32_t at = (L::kPHalf ? p_at(j) ^ buf : p_at(j) + buf) + 1024 * k;
                             if constexpr (FP8) {
                                 sts16(at, pk[k][j]);
                                 sts16(L::kStack ? at + NCOL * 128 : at ^ 64u, pk[k][j] >> 16);
@@ -792,12 +801,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
             }
             __syncwarp();
-            if (alive && lane == 0) mbar_arrive(bar(L::kBarPFull));
+            if (alive && lane == 0) mbar_arrive(bar(L::kBarPFull + (i & 1)));
             if (more && alive) publish_q();
 
             if (last) {
                 // ---- the piece's columns: whole sequences to out, parts to the workspace ----
-                const bool whole = !piece_mid && w.t == w.nt - 1;
+                const bool whole = !piece_mid && ends;
                 // (The merge's CTAs come now, when the SMs empty: launched at the start they crowd onto the first that do.)
                 if (i == n - 1) griddep_launch_dependents();
                 // Slot 0: the range's first piece when it starts inside its sequence; else slot 1.
@@ -818,9 +827,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (tid == 0 && ct == 0 && !whole && !piece_mid) {
                     // The merge's record: this sequence begins here and ends in the range that holds its last tile,
                     // at `end - 1` on the line: the largest r with r total / ranges <= end - 1.
-                    const int64_t end = stop + w.nt - 1 - w.t;
+                    const int64_t end = stop + info.y;
                     const int last_range = static_cast<int>((end * ranges - 1) / total);
-                    p.record[range] = make_int2(w.b, last_range - range + 1);
+                    p.record[range] = make_int2(info.z, last_range - range + 1);
                 }
                 if (!whole && has && half == 0) {
 #pragma unroll
@@ -830,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 soft_sync();
-                alive = alive && warp_wait(bar(L::kBarPvDone), i & 1);
+                alive = alive && warp_wait(bar(L::kBarPvDone + (i & 1)), (i >> 1) & 1);
                 if (alive) {
                     tc_fence_after();
 #pragma unroll 1
@@ -853,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else if (p.out_bf16) {
                             // lanes 2 d and 2 d + 1 swap a value: each then stores two dims of one column
                             uint32_t *dst = static_cast<uint32_t *>(p.out) +
-                                            ((static_cast<size_t>(w.b) * cols + c0 + col) * kLatentDim + (dim & ~1)) / 2;
+                                            ((static_cast<size_t>(info.z) * cols + c0 + col) * kLatentDim + (dim & ~1)) / 2;
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) {
                                 const float a = __uint_as_float(o[e]) * alpha_s[col + e];
@@ -865,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         lane & 1 ? pack_bf16x2(other, d) : pack_bf16x2(a, other);
                             }
                         } else {
-                            float *dst = static_cast<float *>(p.out) + (static_cast<size_t>(w.b) * cols + c0 + col) * kLatentDim + dim;
+                            float *dst = static_cast<float *>(p.out) + (static_cast<size_t>(info.z) * cols + c0 + col) * kLatentDim + dim;
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
                                 if (col + e < nc)
@@ -877,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 piece_mid = false;
                 soft_sync();  // the factors have been read
             }
-            w = nx;
+            first = last;
         }
     }
 

@@ -231,6 +231,13 @@ __device__ __forceinline__ float2 lds_f32x2(uint32_t addr) {
     return r;
 }
 
+// Four 32-bit integers from shared memory.
+__device__ __forceinline__ int4 lds_i32x4(uint32_t addr) {
+    int4 r;
+    asm volatile("ld.shared.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
+    return r;
+}
+
 // Two E4M3 codes (low byte = first element) -> packed f16x2, exactly (every
 // E4M3 value is a normal fp16 number or zero).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
