@@ -70,10 +70,11 @@ struct Layout {
     static constexpr uint32_t kBlock = 2 * kGroup;
     static constexpr uint32_t kRopeBlock = FP8 ? kBlockSize * 128 : 0;
     static constexpr uint32_t kStage = kTileBlocks * (kBlock + kRopeBlock);
-    // FP8, up to 32 columns: the E4M3 heads and remainders of Q are rows of one product (a remainder 8 rows behind its
-    // head, in rows that M = 64 has anyway, and in the same thread after the load), those of P columns of one product
-    // (a remainder NCOL behind): an MMA of few columns is bound by its other operand, M = 128 takes 43 cycles with N =
-    // 32 and 52 with 64.  Two products for 64 columns: O has no room for 128.
+    // FP8: the E4M3 heads and remainders of Q are rows of one product, those of P (up to 32 columns) columns of one: an
+    // MMA of few columns is bound by its other operand, M = 128 takes 43 cycles with N = 32 and 52 with 64, and N = 64
+    // takes 35 with M = 64 and 52 with 128.  A remainder's row is 8 behind its head's, in rows that M = 64 has anyway
+    // and in the same thread after the load; for 64 columns 16 behind, M = 128.  A remainder's column is NCOL behind
+    // (for 64 columns O has no room: two products).
     static constexpr bool kStack = FP8 && NCOL <= 32;
     static constexpr int kOCols = kStack ? 2 * NCOL : NCOL;  // columns of a dim tile's O
     static constexpr int kStages = FP8 ? (kStack ? 4 : 3) : 128 / TILE;
@@ -84,12 +85,13 @@ struct Layout {
     static constexpr int kPerQuarter = NCOL / 4, kRowsPerThread = NCOL == 64 ? 2 : 1;
     // Score columns of a tile (FP8: the latent's and the rotated key's products apart, the scale goes with the first).
     static constexpr uint32_t kScoreCols = FP8 ? 128 : 64;
-    // Q: [chunks][64 rows][128 B]; FP8: 4 chunks of heads, 4 of remainders (E4M3; stacked: 4 of both), the rotated part
-    // in bf16.
-    static constexpr uint32_t kQChunk = 64 * 128;
-    static constexpr int kQChunks = kStack ? 5 : 9;
+    // Q: 9 chunks of [64 rows][128 B]; FP8: 4 chunks of [heads and remainders][128 B] (E4M3), one of the rotated part in
+    // bf16.
+    static constexpr int kQRows = FP8 && NCOL == 64 ? 128 : 64;
+    static constexpr uint32_t kQChunk = kQRows * 128;
     static constexpr uint32_t kQ = 0;
-    static constexpr uint32_t kKv = kQ + kQChunks * kQChunk;
+    static constexpr uint32_t kQRope = kQ + (FP8 ? 4 : 8) * kQChunk;
+    static constexpr uint32_t kKv = kQRope + 64 * 128;
     // P, two buffers in turn: [NCOL][64 bf16], or [NCOL][64 heads | 64 remainders]; rows of 64 bytes (32 keys, or stacked
     // [heads, remainders][NCOL][64 codes]) lie side by side.
     static constexpr uint32_t kP = kKv + kStages * kStage;
@@ -459,17 +461,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t rd = r_desc + static_cast<uint32_t>(st) * (L::kStage >> 4);
             if (elect_one()) {
 #pragma unroll
-                for (int c = 0; c < L::kQChunks; ++c)
+                for (int c = 0; c < (FP8 ? 4 : 8); ++c)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t qd = q_desc + ((c * L::kQChunk + kk * 32) >> 4);
-                        if constexpr (!FP8)
-                            umma_bf16(d, qd, kd + ((c * 1024 + kk * 32) >> 4), idesc(64, kTile, false), c + kk > 0);
-                        else if (c < L::kQChunks - 1)  // heads (and stacked remainders), then remainders, against the same codes
-                            umma_e4m3(d, qd, kd + (((c & 3) * 1024 + kk * 32) >> 4), idesc(64, kTile, false, true), c + kk > 0);
+                        const uint64_t qd = q_desc + ((c * L::kQChunk + kk * 32) >> 4), k = kd + ((c * 1024 + kk * 32) >> 4);
+                        if constexpr (FP8)  // heads and remainders against the same codes
+                            umma_e4m3(d, qd, k, idesc(L::kQRows, kTile, false, true), c + kk > 0);
                         else
-                            umma_bf16(d + 64, qd, rd + ((kk * 32) >> 4), idesc(64, kTile, false), kk > 0);
+                            umma_bf16(d, qd, k, idesc(64, kTile, false), c + kk > 0);
                     }
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16(FP8 ? d + 64 : d, q_desc + ((L::kQRope - L::kQ + kk * 32) >> 4),
+                              (FP8 ? rd : kd + (8 * 1024 >> 4)) + ((kk * 32) >> 4), idesc(64, kTile, false), !FP8 || kk > 0);
                 umma_commit(bar(L::kBarSFull + (i & 1)));
             }
             __syncwarp();
@@ -556,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint16_t *ql = static_cast<const uint16_t *>(p.q_latent) + qr * p.ql_row + h * p.ql_head;
                 const uint16_t *qp = static_cast<const uint16_t *>(p.q_rope) + qr * p.qr_row + h * p.qr_head;
                 auto at = [&](int chunk, int v) { return sbase + L::kQ + chunk * L::kQChunk + rq * 128 + ((v ^ (rq & 7)) << 4); };
+                constexpr uint32_t kRest = L::kQRows == 128 ? 16 * 128 : 8 * 128;  // from a head to its remainder
                 if constexpr (!FP8) {
 #pragma unroll
                     for (int k = 0; k < 3; ++k) {
@@ -598,10 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         lo[k] = f32x2_to_e4m3x2(v[4 * k] * up - f0.x, v[4 * k + 1] * up - f0.y) |
                                 f32x2_to_e4m3x2(v[4 * k + 2] * up - f1.x, v[4 * k + 3] * up - f1.y) << 16;
                     }
-                    sts128(at(lane >> 3, lane & 7), make_uint4(hi[0], hi[1], hi[2], hi[3]));
-                    sts128(L::kStack ? at(lane >> 3, lane & 7) + 8 * 128 : at(4 + (lane >> 3), lane & 7),
-                           make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                    if (lane < 8) sts128(at(L::kQChunks - 1, lane), rope);
+                    const uint32_t head = at(lane >> 3, lane & 7) + (L::kQRows == 128 ? r / 16 * (16 * 128) : 0);
+                    sts128(head, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                    sts128(head + kRest, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+                    if (lane < 8) sts128(at(4, lane), rope);
                     if (lane == 0) qf_s[r] = __uint_as_float(static_cast<uint32_t>(127 - lift) << 23);
                 }
             }
@@ -668,7 +673,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < kR; ++k) x[k][j] = fmul2(pair(v, j, k), sl2);
                 } else {
                     uint32_t u[16];
-                    tmem_ld_16x256b_x4_pair(s_at, v, s_at + 64, u);
+                    if constexpr (L::kQRows == 128) {  // rows 32 q + 16 ..: the remainders
+                        tmem_ld_16x256b_x4_pair(s_at, v, s_at + (16u << 16), u);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(u[e]));
+                        tmem_ld_16x256b_x4(s_at + 64, u);
+                    } else {
+                        tmem_ld_16x256b_x4_pair(s_at, v, s_at + 64, u);
+                    }
 #pragma unroll
                     for (int j = 0; j < kGroups; ++j) {
                         const float2 sc = lds_f32x2(sc_at + 32 * j), lg = lds_f32x2(sc_at + kTile * 4 + 32 * j);
