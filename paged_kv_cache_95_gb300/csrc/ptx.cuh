@@ -75,6 +75,11 @@ __device__ __forceinline__ void prefetch_l2(const void *p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(p)));
 }
 
+// `bytes` (a multiple of 16) from the 16-byte aligned src on their way into L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(src)), "r"(bytes) : "memory");
+}
+
 // atomicAdd with acquire-release semantics at GPU scope: publishes the writes
 // that happen-before it (including other threads' writes ordered by a
 // preceding __syncthreads) and acquires the writes published by earlier adds.
