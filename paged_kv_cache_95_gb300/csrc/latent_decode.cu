@@ -571,16 +571,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         // of 2^-9); the factor that undoes it in shared memory.
         float *qf_s = reinterpret_cast<float *>(smem + L::kQf);
         auto load_q = [&](int b) {
-#pragma unroll FP8 ? 4 : 1
-            for (int r = warp; r < NCOL; r += kSoftWarps) {
-                const int rq = r / L::kPerQuarter * 16 + r % L::kPerQuarter;
+            auto q_of = [&](int r, const uint16_t *&ql, const uint16_t *&qp) {
                 const int c = c0 + r, i = c / p.heads;
                 const int64_t qr = static_cast<int64_t>(b) * p.q_per_seq + i, h = c - i * p.heads;
-                const uint16_t *ql = static_cast<const uint16_t *>(p.q_latent) + qr * p.ql_row + h * p.ql_head;
-                const uint16_t *qp = static_cast<const uint16_t *>(p.q_rope) + qr * p.qr_row + h * p.qr_head;
+                ql = static_cast<const uint16_t *>(p.q_latent) + qr * p.ql_row + h * p.ql_head;
+                qp = static_cast<const uint16_t *>(p.q_rope) + qr * p.qr_row + h * p.qr_head;
+            };
+            // FP8: a row's data, read while the row before is converted (the loop stays rolled: unrolled, its code took
+            // longer to fetch than to run).
+            uint4 a, d, rope;
+            auto fetch = [&](int r) {
+                a = d = rope = make_uint4(0u, 0u, 0u, 0u);
+                if (r < nc) {
+                    const uint16_t *ql, *qp;
+                    q_of(r, ql, qp);
+                    a = __ldg(reinterpret_cast<const uint4 *>(ql) + 2 * lane);
+                    d = __ldg(reinterpret_cast<const uint4 *>(ql) + 2 * lane + 1);
+                    if (lane < 8) rope = __ldg(reinterpret_cast<const uint4 *>(qp) + lane);
+                }
+            };
+            if constexpr (FP8) fetch(warp);
+#pragma unroll 1
+            for (int r = warp; r < NCOL; r += kSoftWarps) {
+                const int rq = r / L::kPerQuarter * 16 + r % L::kPerQuarter;
                 auto at = [&](int chunk, int v) { return sbase + L::kQ + chunk * L::kQChunk + rq * 128 + ((v ^ (rq & 7)) << 4); };
                 constexpr uint32_t kRest = L::kQRows == 128 ? 16 * 128 : 8 * 128;  // from a head to its remainder
                 if constexpr (!FP8) {
+                    const uint16_t *ql, *qp;
+                    q_of(r, ql, qp);
 #pragma unroll
                     for (int k = 0; k < 3; ++k) {
                         const int v = lane + 32 * k;
@@ -591,21 +609,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             sts128(at(v >> 3, v & 7), make_uint4(0u, 0u, 0u, 0u));
                     }
                 } else {
-                    uint4 a = make_uint4(0u, 0u, 0u, 0u), d = a, rope = a;
-                    if (r < nc) {
-                        a = __ldg(reinterpret_cast<const uint4 *>(ql) + 2 * lane);
-                        d = __ldg(reinterpret_cast<const uint4 *>(ql) + 2 * lane + 1);
-                        if (lane < 8) rope = __ldg(reinterpret_cast<const uint4 *>(qp) + lane);
-                    }
                     const uint32_t u[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+                    const uint4 rotated = rope;
+                    if (r + kSoftWarps < NCOL) fetch(r + kSoftWarps);
                     float v[16], most = 0.f;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         v[2 * k] = bf16_lo(u[k]), v[2 * k + 1] = bf16_hi(u[k]);
                         most = fmax3(most, fabsf(v[2 * k]), fabsf(v[2 * k + 1]));
                     }
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+                    most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));  // (none is negative)
                     // most = f 2^e, 1 <= f < 2: times 2^(8 - e), or 2^(7 - e) when f 2^8 passes 448 (both exponents
                     // kept within fp32's; an all-zero row keeps factor 1).
                     const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;
@@ -625,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t head = at(lane >> 3, lane & 7) + (L::kQRows == 128 ? r / 16 * (16 * 128) : 0);
                     sts128(head, make_uint4(hi[0], hi[1], hi[2], hi[3]));
                     sts128(head + kRest, make_uint4(lo[0], lo[1], lo[2], lo[3]));
-                    if (lane < 8) sts128(at(4, lane), rope);
+                    if (lane < 8) sts128(at(4, lane), rotated);
                     if (lane == 0) qf_s[r] = __uint_as_float(static_cast<uint32_t>(127 - lift) << 23);
                 }
             }
