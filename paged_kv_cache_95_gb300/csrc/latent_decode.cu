@@ -79,7 +79,7 @@ struct Layout {
     static constexpr int kOCols = kStack ? 2 * NCOL : NCOL;  // columns of a dim tile's O
     static constexpr int kStages = FP8 ? (kStack ? 4 : 3) : 128 / TILE;
     // What beginning another sequence costs a range, in tiles: its Q, the epilogue of the one before.
-    static constexpr int kLead = FP8 ? 4 : 128 / TILE;
+    static constexpr int kLead = FP8 ? 5 : 128 / TILE;
     // M = 64: rows 16 q .. 16 q + 15 of S lie in tensor-memory lanes 32 q .., which only warps w % 4 = q reach, one
     // scheduler's.  A quarter of the columns goes to each: column c is row 16 (c / kPerQuarter) + c % kPerQuarter.
     static constexpr int kPerQuarter = NCOL / 4, kRowsPerThread = NCOL == 64 ? 2 : 1;
