@@ -113,7 +113,8 @@ struct Layout {
     // left, sequence, next tile's sequence}.  (Walking the tiles itself cost softmax 240 cycles a tile, of 1600.)
     static constexpr uint32_t kInfo = kPlan + 18 * 8;
     static constexpr uint32_t kDead = kInfo + kStages * 16;  // [tile & 1]: a softmax warp's wait ran out
-    static constexpr uint32_t kBytes = kDead + 8;
+    static constexpr uint32_t kQAt = (kDead + 8 + 15) / 16 * 16;  // [NCOL] a column's places in a sequence's q_latent, q_rope
+    static constexpr uint32_t kBytes = kQAt + NCOL * 16;
     static_assert(kBytes <= 232448, "shared memory of one CTA");
     static_assert(kKv % 1024 == 0 && kP % 1024 == 0 && kStage % 1024 == 0, "swizzle atoms");
     static_assert(kScale % 16 == 0 && kBar % 8 == 0 && kPlan % 8 == 0 && kInfo % 16 == 0, "alignment");
@@ -220,6 +221,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         *first_tile = ~0ull;
         *tile_count = 0;
         fence_mbar_init();
+    }
+    longlong2 *q_at = reinterpret_cast<longlong2 *>(smem + L::kQAt);
+    if (tid < nc) {
+        const int i = (c0 + tid) / p.heads, h = c0 + tid - i * p.heads;
+        q_at[tid] = make_longlong2(i * p.ql_row + h * p.ql_head, i * p.qr_row + h * p.qr_head);
     }
     if (warp == kScoreWarp) {  // (no other kernel's CTA waits for ours: the columns come free)
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -571,11 +577,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // of 2^-9); the factor that undoes it in shared memory.
         float *qf_s = reinterpret_cast<float *>(smem + L::kQf);
         auto load_q = [&](int b) {
-            auto q_of = [&](int r, const uint16_t *&ql, const uint16_t *&qp) {
-                const int c = c0 + r, i = c / p.heads;
-                const int64_t qr = static_cast<int64_t>(b) * p.q_per_seq + i, h = c - i * p.heads;
-                ql = static_cast<const uint16_t *>(p.q_latent) + qr * p.ql_row + h * p.ql_head;
-                qp = static_cast<const uint16_t *>(p.q_rope) + qr * p.qr_row + h * p.qr_head;
+            const uint16_t *ql0 = static_cast<const uint16_t *>(p.q_latent) + static_cast<int64_t>(b) * p.q_per_seq * p.ql_row;
+            const uint16_t *qp0 = static_cast<const uint16_t *>(p.q_rope) + static_cast<int64_t>(b) * p.q_per_seq * p.qr_row;
+            auto q_of = [&](int r, const uint16_t *&ql, const uint16_t *&qp) {  // (r < nc)
+                const longlong2 to = q_at[r];
+                ql = ql0 + to.x;
+                qp = qp0 + to.y;
             };
             // FP8: a row's data, read while the row before is converted (the loop stays rolled: unrolled, its code took
             // longer to fetch than to run).
@@ -597,8 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto at = [&](int chunk, int v) { return sbase + L::kQ + chunk * L::kQChunk + rq * 128 + ((v ^ (rq & 7)) << 4); };
                 constexpr uint32_t kRest = L::kQRows == 128 ? 16 * 128 : 8 * 128;  // from a head to its remainder
                 if constexpr (!FP8) {
-                    const uint16_t *ql, *qp;
-                    q_of(r, ql, qp);
+                    const uint16_t *ql = ql0, *qp = qp0;
+                    if (r < nc) q_of(r, ql, qp);
 #pragma unroll
                     for (int k = 0; k < 3; ++k) {
                         const int v = lane + 32 * k;
