@@ -20,10 +20,13 @@
 // Warps:
 //  * 0-3 softmax of row tile 0, 4-7 of row tile 1, a row a thread: 64 scores at a time, one
 //    pass, weights P = 2^(s - m) against a running reference m straight back over the
-//    consumed scores as bf16 (relative 2^-8).  m is an integer, raised when a score passes it
-//    by 2^8 (looked at before the 64 weights are written; what was written is rescaled by an
-//    exact power of two, and so are l and O); the sum l stays in fp32.
-//  * 8 TMA: Q, K.  10-13 cp.async: V.  Chunks of 16 KB: three a key tile of K ([128 keys]
+//    consumed scores as bf16 (relative 2^-8).  m is the row's first largest score, raised by
+//    whole powers of two when a score passes it by 2^8 (looked at before the 64 weights are
+//    written; what was written is rescaled exactly, and so are l and O); the sum l stays in
+//    fp32.  (l of the rounded weights, which would round as numerator does, is two instructions
+//    more a weight: 461 -> 480 us on 8192 tokens x 32 heads; a quarter of the exponentials as
+//    polynomials on the FMA pipe 480 -> 506: the softmax warps' instructions are what counts.)
+//  * 8 TMA: the first row tile's Q, K.  10-13 cp.async: the second's Q, V.  Chunks of 16 KB: three a key tile of K ([128 keys]
 //    [64 values]) and two of V ([64 keys][128 dims]), each kind in a ring of 4, each refilled
 //    as the MMAs that read it end.  (One ring of 8 for both let the next K wait for this V:
 //    474 us on 8192 tokens x 32 heads.)
@@ -354,9 +357,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float alpha = 1.f;
                     if (mx > m + kRaise) {
-                        const float up = ceilf(mx);
-                        alpha = fast_exp2(m - up);  // 0 from -inf
-                        m = up;
+                        // The first largest score as it is, then steps of whole powers of two: the weights of the
+                        // largest scores are exact in bf16, and a row of one key is its value.
+                        const float up = m == -INFINITY ? INFINITY : ceilf(mx - m);
+                        alpha = fast_exp2(-up);
+                        m = m == -INFINITY ? mx : m + up;
                     }
                     l2 = fmul2(l2, make_float2(alpha, alpha));
                     l3 = fmul2(l3, make_float2(alpha, alpha));
