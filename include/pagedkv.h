@@ -715,7 +715,9 @@ PKV_API size_t latent_attention_workspace_size(int32_t num_seqs, int32_t q_per_s
  * A sequence with ctx < 1 (PKV_STATUS_BAD_CONTEXT_LEN) or ctx < q_per_seq
  * (PKV_STATUS_BAD_Q_LEN) gets zero rows; a length past the table counts as the
  * table's length (PKV_STATUS_BAD_CONTEXT_LEN); a block with an invalid id
- * contributes nothing (PKV_STATUS_BAD_BLOCK_ID).
+ * contributes nothing (PKV_STATUS_BAD_BLOCK_ID).  Slots that belong to no key may
+ * hold anything; a key of the sequence that is not finite makes the rows that see it
+ * NaN, and may make those before it NaN too (q_per_seq > 1: a weight of 0 times it).
  * Errors: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED /
  *         PKV_ERR_WORKSPACE_TOO_SMALL / PKV_ERR_CUDA.
  */
@@ -754,13 +756,17 @@ PKV_API int latent_attention_decode_fp8(void *out, int32_t out_dtype, const void
  *               k_head_stride (usually the two halves of one [rows][heads][256] product)
  *   k_rope    : bf16, 64 values a row, shared by the heads, at k_rope + row * k_rope_stride
  *   cu_q_lens, cu_k_lens : int32 [num_seqs + 1], device, non-decreasing, from 0
- *   max_q_len : host upper bound of every q_len (sizes the launch grid)
+ *   strides   : at least 8 here (rows and heads are boxes of a tensor map)
+ *   max_q_len : host upper bound of every q_len (sizes the launch grid; the lesser of
+ *               it and total_q_rows up to 16776960)
  *   total_q_rows, total_k_rows : rows of q / out and of the keys
  *   workspace : 256-byte aligned, latent_attention_prefill_workspace_size() bytes
  *               (status word at byte 0, zeroed once)
  * A sequence with q_len > k_len or q_len > max_q_len, or whose rows lie outside
  * the tensors, sets PKV_STATUS_BAD_Q_LEN; its rows that can be addressed become
- * zeros.  Rows of out past cu_q_lens[num_seqs] are left as they were.
+ * zeros.  Rows of out past cu_q_lens[num_seqs] are left as they were.  Rows that
+ * belong to no sequence may hold anything; a value of the sequence that is not finite
+ * may reach rows before it (a weight of 0 times it), a key only those that see it.
  * Errors: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED /
  *         PKV_ERR_WORKSPACE_TOO_SMALL / PKV_ERR_CUDA.
  */

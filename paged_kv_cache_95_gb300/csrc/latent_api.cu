@@ -24,6 +24,7 @@ constexpr int kMaxDevices = 64;
 constexpr int kDefaultSms = 152;  // sizes asked for without a GPU
 constexpr int32_t kMaxRowsPerSeq = 16;
 constexpr int32_t kMaxHeads = 1024;
+constexpr int32_t kMaxChunk = 65535 * 256;  // query rows of a prefill chunk: 256 a step of the launch grid
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -155,7 +156,16 @@ int check_latent(const pkv_latent_desc *d, int32_t dtype) {
 }
 
 // A strided bf16 input: 16-byte vectors at every row, offsets that 64 bits hold.
-bool good_stride(int64_t s) { return s >= 0 && s % 8 == 0 && s < (int64_t{1} << 40); }
+bool good_stride(int64_t s) { return s >= 0 && s % 8 == 0 && s < (int64_t{1} << 38); }
+
+// The softmax scale in the log2 domain, which has to be finite too.
+bool log2_scale(float scale, float *out) {
+    *out = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    return std::isfinite(*out);
+}
+
+// Lengths that the kernels may round up to whole tiles within 32 bits.
+constexpr int64_t kMaxLength = INT32_MAX - 4096;
 
 int write_impl(const void *latent, int64_t latent_stride, const void *rope, int64_t rope_stride, void *cache,
                void *rope_cache, float *cache_scale, const int32_t *slot_mapping, int32_t num_tokens,
@@ -189,7 +199,7 @@ int write_impl(const void *latent, int64_t latent_stride, const void *rope, int6
 int check_decode_sizes(int32_t num_seqs, int32_t q_per_seq, int32_t heads, int32_t max_blocks) {
     if (num_seqs < 1 || num_seqs > 65535 || q_per_seq < 1 || q_per_seq > kMaxRowsPerSeq || heads < 1 || max_blocks < 1)
         return PKV_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(max_blocks) * kBlockSize > INT32_MAX) return PKV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(max_blocks) * kBlockSize > kMaxLength) return PKV_ERR_INVALID_ARG;
     if (heads > kMaxHeads) return PKV_ERR_UNSUPPORTED;
     return PKV_OK;
 }
@@ -205,7 +215,8 @@ int decode_impl(void *out, int32_t out_dtype, const void *q_latent, int64_t ql_r
     if (fp8 && (!rope_cache || !cache_scale || !aligned(rope_cache, 16) || !aligned(cache_scale, 16)))
         return PKV_ERR_INVALID_ARG;
     if (out_dtype != PKV_DTYPE_FLOAT32 && out_dtype != PKV_DTYPE_BF16) return PKV_ERR_UNSUPPORTED;
-    if (!std::isfinite(scale)) return PKV_ERR_INVALID_ARG;
+    pkv::LatentDecodeParams p{};
+    if (!log2_scale(scale, &p.scale_log2)) return PKV_ERR_INVALID_ARG;
     if (!good_stride(ql_row) || !good_stride(ql_head) || !good_stride(qr_row) || !good_stride(qr_head))
         return PKV_ERR_INVALID_ARG;
     if (!aligned(out, 16) || !aligned(q_latent, 16) || !aligned(q_rope, 16) || !aligned(cache, 16) ||
@@ -214,7 +225,6 @@ int decode_impl(void *out, int32_t out_dtype, const void *q_latent, int64_t ql_r
     if (!workspace || !aligned(workspace, 256)) return PKV_ERR_INVALID_ARG;
     if (workspace_bytes < latent_attention_workspace_size(num_seqs, q_per_seq, heads, max_blocks, desc))
         return PKV_ERR_WORKSPACE_TOO_SMALL;
-    pkv::LatentDecodeParams p{};
     p.out = out;
     p.q_latent = q_latent;
     p.q_rope = q_rope;
@@ -233,7 +243,6 @@ int decode_impl(void *out, int32_t out_dtype, const void *q_latent, int64_t ql_r
     p.heads = heads;
     p.max_blocks = max_blocks;
     p.num_blocks = desc->num_blocks;
-    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.out_bf16 = out_dtype == PKV_DTYPE_BF16;
     const int sms = current_sms();
     if (sms < 1 || !prepare_device()) return PKV_ERR_CUDA;
@@ -278,7 +287,8 @@ int latent_gather(void *out, const void *cache, const void *rope_cache, const fl
     const bool fp8 = desc->dtype == PKV_DTYPE_FP8_E4M3;
     if (int rc = check_latent(desc, fp8 ? PKV_DTYPE_FP8_E4M3 : PKV_DTYPE_BF16)) return rc;
     if (num_seqs < 1 || max_blocks_per_seq < 1 || total_rows < 0) return PKV_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(max_blocks_per_seq) * kBlockSize > INT32_MAX) return PKV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(max_blocks_per_seq) * kBlockSize > kMaxLength || total_rows > kMaxLength)
+        return PKV_ERR_INVALID_ARG;
     if (total_rows == 0) return PKV_OK;
     if (!out || !cache || !block_tables || !cu_lens) return PKV_ERR_INVALID_ARG;
     if (fp8 ? (!rope_cache || !cache_scale || !aligned(rope_cache, 16) || !aligned(cache_scale, 16))
@@ -351,9 +361,11 @@ int latent_attention_prefill_chunk(void *out, int32_t out_dtype, const void *q, 
                                    float scale, void *workspace, size_t workspace_bytes, void *stream) {
     if (num_seqs < 1 || num_seqs > 65535 || num_heads < 1 || max_q_len < 0 || total_q_rows < 0 || total_k_rows < 0)
         return PKV_ERR_INVALID_ARG;
-    if (num_heads > kMaxHeads) return PKV_ERR_UNSUPPORTED;
+    if (total_q_rows > kMaxLength || total_k_rows > kMaxLength) return PKV_ERR_INVALID_ARG;
+    if (num_heads > kMaxHeads || std::min(max_q_len, total_q_rows) > kMaxChunk) return PKV_ERR_UNSUPPORTED;
     if (out_dtype != PKV_DTYPE_FLOAT32 && out_dtype != PKV_DTYPE_BF16) return PKV_ERR_UNSUPPORTED;
-    if (!std::isfinite(scale)) return PKV_ERR_INVALID_ARG;
+    pkv::LatentPrefillParams p{};
+    if (!log2_scale(scale, &p.scale_log2)) return PKV_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256)) return PKV_ERR_INVALID_ARG;
     if (workspace_bytes <
         latent_attention_prefill_workspace_size(num_seqs, num_heads, max_q_len, total_q_rows, total_k_rows))
@@ -369,7 +381,6 @@ int latent_attention_prefill_chunk(void *out, int32_t out_dtype, const void *q, 
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_nope, 16) || !aligned(v, 16) || !aligned(k_rope, 16) ||
         !aligned(cu_q_lens, 4) || !aligned(cu_k_lens, 4))
         return PKV_ERR_INVALID_ARG;
-    pkv::LatentPrefillParams p{};
     p.out = out;
     p.q = q;
     p.k_nope = k_nope;
@@ -388,7 +399,6 @@ int latent_attention_prefill_chunk(void *out, int32_t out_dtype, const void *q, 
     p.max_q_len = max_q_len;
     p.total_q = total_q_rows;
     p.total_k = total_k_rows;
-    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.out_bf16 = out_dtype == PKV_DTYPE_BF16;
     if (p.scale_log2 == 0.f) p.scale_log2 = 1e-37f;  // the kernel hides a key by an infinite score: never 0 x infinity
     if (!prepare_device()) return PKV_ERR_CUDA;

@@ -204,7 +204,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (FP8) prefetch_tensormap(&ropemap);
     }
     if (sbase & 1023u) {  // operands need the 1 KB swizzle alignment
+        griddep_wait();
         if (tid == 0) atomicOr(p.status, kStatusTimeout);
+        if (tid == 0 && ct == 0) p.record[range] = make_int2(0, 0);
         return;
     }
     auto bar = [&](int i) { return sbase + L::kBar + 8 * i; };
@@ -646,7 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sts128(head, make_uint4(hi[0], hi[1], hi[2], hi[3]));
                     sts128(head + kRest, make_uint4(lo[0], lo[1], lo[2], lo[3]));
                     if (lane < 8) sts128(at(4, lane), rotated);
-                    if (lane == 0) qf_s[r] = __uint_as_float(static_cast<uint32_t>(127 - lift) << 23);
+                    // (E4M3 has no infinity: a row that holds one scores NaN.)
+                    if (lane == 0) qf_s[r] = __uint_as_float(most == INFINITY ? 0x7fffffffu : static_cast<uint32_t>(127 - lift) << 23);
                 }
             }
         };

@@ -481,7 +481,8 @@ cudaError_t latent_prefill_prepare_device() {
 }
 
 cudaError_t launch_latent_prefill(const LatentPrefillMaps &maps, const LatentPrefillParams &p, cudaStream_t stream) {
-    const dim3 grid(p.heads, p.num_seqs, (p.max_q_len + 2 * kRows - 1) / (2 * kRows));
+    const int longest = p.max_q_len < p.total_q ? p.max_q_len : p.total_q;
+    const dim3 grid(p.heads, p.num_seqs, (longest + 2 * kRows - 1) / (2 * kRows));
     return launch_pdl(latent_prefill_kernel, grid, dim3(kThreads), kSmemBytes, stream, maps.q, maps.k, maps.rope, maps.out,
                       p);
 }

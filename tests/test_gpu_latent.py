@@ -481,6 +481,113 @@ def test_prefill_bad_lengths():
     assert (out[20:] == 0).all() and status_of(ws) == P.PKV_STATUS_BAD_Q_LEN
 
 
+@pytest.mark.parametrize("factor", [0.0, -1.0])
+def test_scales_of_zero_and_below(factor):
+    """A scale of -s is a query of the other sign; a scale of 0 is the mean of what a row sees."""
+    for fp8 in (False, True):
+        pool = R.Pool(60, [900, 65, 3], fp8)
+        q = queries(61, 3, 20)
+        out = torch.empty(3, 20, 512, device="cuda")
+        P.latent_attention_decode(out, q[0].cuda(), q[1].cuda(), block_tables=pool.tables.cuda(), context_lens=i32(pool.lens),
+                                  scale=factor * R.SCALE, **pool.device())
+        R.assert_within(out, *R.decode(*(x * factor for x in q), pool, 1), f"scale x {factor}")
+    q, kv, rows = prefill_inputs(62, [150, 3], [300, 3], 3, spare=0)
+    out = torch.empty(153, 3, 128, device="cuda")
+    P.latent_attention_prefill_chunk(out, q.cuda(), kv.cuda()[..., :128], kv.cuda()[..., 128:], rows.cuda()[:, 512:],
+                                     i32([0, 150, 153]), i32([0, 300, 303]), 150, factor * R.SCALE)
+    R.assert_within(out, *R.expanded(q * factor, kv[..., :128], kv[..., 128:], rows[:, 512:], [150, 3], [300, 3]),
+                    f"prefill, scale x {factor}")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_more_columns_than_the_gpu_holds(fp8):
+    """1024 heads x 3 rows are 48 column tiles; x 16 rows 256, more than there are SMs."""
+    pool = R.Pool(63, [130, 20], fp8)
+    for k in (3, 16):
+        q = queries(64, 2 * k, 1024)
+        out, ws = run_decode(pool, *q, k, dtype=torch.bfloat16)
+        R.assert_within(out, *R.decode(*q, pool, k), f"{k} rows of 1024 heads")
+        assert status_of(ws) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_one_block_of_many_sequences(fp8):
+    """Sequences that share their pages (a common prefix) and one that names a block twice."""
+    pool = R.Pool(65, [320] * 6, fp8, table_pad=0)
+    pool.tables[:] = pool.tables[0]
+    pool.tables[3, 7] = pool.tables[3, 2]
+    q = queries(66, 6, 32)
+    out, _ = run_decode(pool, *q, 1)
+    R.assert_within(out, *R.decode(*q, pool, 1), "shared blocks")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_query_that_is_not_finite_stays_alone(fp8):
+    pool = R.Pool(67, [200, 90], fp8)
+    q = queries(68, 2, 24)
+    want, _ = run_decode(pool, *q, 1)
+    q[0][0, 5, 17], q[0][1, 7, 300], q[1][1, 2, 9] = float("inf"), R.NAN, R.NAN
+    out, ws = run_decode(pool, *q, 1)
+    broken = torch.zeros(2, 24, dtype=torch.bool)
+    broken[0, 5] = broken[1, 7] = broken[1, 2] = True
+    assert torch.equal(out.cpu()[~broken], want.cpu()[~broken])
+    assert out.cpu()[broken].isnan().all()
+    assert status_of(ws) == 0
+
+
+def test_prefill_queries_and_keys_that_are_not_finite():
+    """A query spoils its own row; a key only the rows that see it."""
+    q, kv, rows = prefill_inputs(69, [300], [300], 2, spare=0)
+    want, _ = run_prefill(q, kv, rows, [300], [300])
+    q[7, 1, 40], kv[250, 0, 3] = R.NAN, R.NAN
+    out, ws = run_prefill(q, kv, rows, [300], [300])
+    broken = torch.zeros(300, 2, dtype=torch.bool)
+    broken[7, 1] = broken[250:, 0] = True
+    assert torch.equal(out.cpu()[~broken], want.cpu()[~broken])
+    assert out.cpu()[broken].isnan().all()
+    assert status_of(ws) == 0
+
+
+def test_prefill_on_two_streams_and_in_a_graph():
+    """Calls at once on two streams, then captured one behind the other over one workspace."""
+    sizes = [([200, 65], [400, 65]), ([300], [301])]
+    calls, refs = [], []
+    for i, (ql, kl) in enumerate(sizes):
+        q, kv, rows = prefill_inputs(70 + i, ql, kl, 3, spare=0)
+        refs.append(R.expanded(q, kv[..., :128], kv[..., 128:], rows[:, 512:], ql, kl))
+        d = dict(q=q.cuda(), kv=kv.cuda(), rows=rows.cuda(), cq=i32(starts(ql)), ck=i32(starts(kl)), n=max(ql),
+                 out=torch.full((sum(ql), 3, 128), R.NAN, device="cuda"), ws=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+        calls.append(d)
+    shared = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+
+    def run(d, ws):
+        P.latent_attention_prefill_chunk(d["out"], d["q"], d["kv"][..., :128], d["kv"][..., 128:], d["rows"][:, 512:], d["cq"],
+                                         d["ck"], d["n"], R.SCALE, workspace=ws)
+
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(4):
+        for d, s in zip(calls, streams):
+            with torch.cuda.stream(s):
+                run(d, d["ws"])
+    torch.cuda.synchronize()
+    want = [d["out"].clone() for d in calls]
+    for w, ref in zip(want, refs):
+        R.assert_within(w, *ref, "two streams")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for d in calls:
+            run(d, shared)
+    for d in calls:
+        d["out"].fill_(R.NAN)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    for d, w in zip(calls, want):
+        assert torch.equal(d["out"], w)
+    assert status_of(shared) == 0
+
+
 # ---- refusals of the binding ------------------------------------------------------------------------
 
 def test_binding_refusals():

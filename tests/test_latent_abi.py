@@ -148,3 +148,29 @@ def test_reference_absorbed_equals_expanded():
     v = torch.einsum("jc,hdc->jhd", rows[:, :512], wv)
     want, _ = R.expanded(q, k_nope, v, rows[:, 512:], [4], [n])
     assert torch.allclose(torch.einsum("rhc,hdc->rhd", out, wv), want, atol=1e-12)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(mb=(1 << 27) - 1), INV), (dict(scale=3e38), INV), (dict(scale=-3e38), INV), (dict(qlr=1 << 38), INV),
+    (dict(qlh=1 << 40), INV),
+])
+def test_decode_refuses_what_overflows(lib, kw, want):
+    """Lengths that do not round up to a tile in 32 bits, scales infinite in the log2 domain, strides past a tensor."""
+    for fp8 in (False, True):
+        assert _decode(lib, _decode_args(d=desc(dtype=2 if fp8 else 0), **kw), fp8) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(mq=65535 * 256 + 1, tq=(1 << 30)), UNS), (dict(mq=1 << 30, tq=65535 * 256 + 1), UNS), (dict(tq=2 ** 31 - 1), INV),
+    (dict(tk=2 ** 31 - 1), INV), (dict(scale=3e38), INV), (dict(qs=1 << 38), INV),
+])
+def test_prefill_refuses_what_overflows(lib, kw, want):
+    a = dict(qs=192 * 8, mq=16, tq=20, tk=40, scale=0.07)
+    a.update(kw)
+    assert lib.latent_attention_prefill_chunk(FAKE, 1, FAKE, a["qs"], 192, FAKE, FAKE, 256 * 8, 256, FAKE, 576, FAKE, FAKE, 2, 8,
+                                              a["mq"], a["tq"], a["tk"], a["scale"], FAKE, 1 << 30, None) == want
+
+
+def test_gather_refuses_what_overflows(lib):
+    for mb, n in (((1 << 27) - 1, 10), (8, 2 ** 31 - 1)):
+        assert lib.latent_gather(FAKE, FAKE, None, None, FAKE, FAKE, 2, mb, n, ctypes.byref(desc()), None, None) == INV
