@@ -6,29 +6,42 @@
 // Every (query row, head) pair of a sequence is a column that reads the same cached
 // rows, so a CTA takes up to 64 columns and reads each key once for all of them.
 //
-// Work split: the keys of all sequences are one line of 64-key tiles, cut into equal
-// ranges, one CTA per SM and column tile (context lengths are device data, so every
-// CTA sums them itself).  A range covers whole sequences and at most two parts of
-// one; whole sequences are written out, parts go to the workspace as (m, l, O) and
-// the merge kernel folds them.  No CTA waits for another.
+// Work split: the keys of all sequences are one line of tiles, cut into equal ranges,
+// one CTA per SM and column tile (context lengths are device data, so every CTA sums
+// them itself; a sequence's start counts a few tiles more, for its Q and the epilogue).
+// A range covers whole sequences and at most two parts of one; whole sequences are
+// written out, parts go to the workspace as (m, l, O) and the merge kernel folds them.
+// No CTA waits for another.
 //
-// Per tile (64 keys = 4 blocks of 16, 72 KB, 2 stages):
-//  * S [64 columns x 64 keys] = Q K^T: M = 64, N = 64, 36 steps of 16 values; Q stays in
-//    shared memory (128-byte swizzle, 9 chunks of 64 values).
+// Per tile (bf16: 32 keys, four stages of 36 KB; up to 16 columns 64 keys, two stages;
+// FP8: 64 keys, 40 KB, four stages, with 64 columns three):
+//  * S [columns x keys] = Q K^T: M = 64 (FP8 with 64 columns 128), N = keys; Q stays in
+//    shared memory (128-byte swizzle).  Over an FP8 pool Q and P are pairs of E4M3 codes.
 //  * half of the blocks are copied by TMA, half by cp.async: one SM's TMA unit delivers 24
 //    bytes a clock however much is in flight (measured, from L2 as from HBM), both paths
 //    together 47; HBM's share of an SM is 23-28, so a ring on TMA alone never catches up.
 //  * softmax by 8 warps (a warp: a quarter of the columns, half of the keys): running reference m,
 //    raised only when a score passes it by 2^8 (one vote a tile), sum l in fp32;
 //    P = 2^(s - m) rounded to bf16 (l adds the rounded weights, so numerator and
-//    denominator round alike) into shared memory as the B operand.
+//    denominator round alike) into shared memory as the B operand, two buffers in turn.
 //  * O^T [512 dims x columns] += V^T P^T: the same bytes as K, read as an MN-major A
-//    operand: M = 128 (4 tiles of dims), N = columns, 4 steps of 16 keys.  Transposed,
+//    operand: M = 128 (4 tiles of dims), N = columns, 16 keys a step (FP8: 32).  Transposed,
 //    because O has 512 x 64 values: as 128 lanes x 256 columns it leaves tensor memory
 //    for two S buffers, and M is full for any number of heads.
 // S and P V are issued by two warps, so neither waits behind the other's inputs (one
 // issuer that waits for the next tile's copy before a P V leaves no copy in flight);
-// P V frees a stage 16 keys at a time.
+// P V frees a stage block by block.
+//
+// What bounds it (cycles of one CTA, 1.9 GHz): a tile of 32 keys takes 1550-1650.  With 32
+// columns that is HBM's rate (23 bytes a clock and SM: 6.6 TB/s; the ragged batch of 64
+// sequences and 32 heads 39.0 us, 25.5 of them bytes); with 64 the tensor pipe, 36 MMAs of
+// 28 cycles for S and 16 of 52 for P V, whose operands come from shared memory (8 x 32K
+// tokens of 64 heads 65.5 us, 128 heads over 32 sequences 72.6).  FP8: 64 keys in 1850 with
+// 32 columns, the ring's four stages held from S to P V (30 us, 14.5 of bytes), 2400 with 64
+// (three stages; 4 rows x 64 heads over 16 sequences 91.5 us, 39.9 of operations).  Around
+// the tiles: launch, plan and first copies 5 us, Q of another sequence and the epilogue of
+// the one before 2-4 us (72 KB of Q come in at 47 bytes a clock, 128 KB of O go out), the
+// merge 4-6 us.
 //
 // Every mbarrier wait is bounded; a role whose wait runs out raises a CTA-wide abort
 // flag, the others stop at their next wait, and the CTA records PKV_STATUS_TIMEOUT and

@@ -36,6 +36,11 @@
 //    S(k + 1) follows P V (k): it overwrites the P that P V reads, and the MMAs of one
 //    thread run in order.
 //
+// 8192 tokens x 32 heads: 461 us, 1.49 PFLOP/s.  Short chunks (4 of 162-417 rows behind
+// 179-791 cached ones, 32 heads): 36.8 us; 224 CTAs of 4 to 9 key tiles on 152 SMs, each with
+// 5-6 us of launch, first copies and epilogue.  (CTAs that take the next unit themselves,
+// its copies issued early: 36.7 us there, 471 on the long prompt, whose loop got 6% slower.)
+//
 // Every mbarrier wait is bounded; a role whose wait runs out raises a CTA-wide abort
 // flag, the others stop at their next wait, and the CTA records PKV_STATUS_TIMEOUT and
 // frees its tensor memory before it returns.
