@@ -12,34 +12,38 @@
 //
 // What bounds it: a key tile costs two row tiles 2 x (768 + 512) cycles of the tensor pipe;
 // its operands read 2 x 128 KB of shared memory and its 80 KB of keys and values are
-// written there, 2690 cycles at 128 B a clock -- both limits are near.  One SM's TMA unit
-// delivers 24 B a clock (measured), too little for 80 KB in 2560 cycles, so K comes by TMA and
-// V by cp.async, which also fills rows past the sequence's end with zeros (a weight of 0
-// times a stranger's NaN would be NaN).
+// written there, 2690 cycles at 128 B a clock.  Shared memory is the nearer limit: the S
+// MMAs (8 KB of operands in 64 cycles) leave nothing for the copies and take 85 cycles each
+// beside them; a tile takes 3300-3600 cycles, in which the pipe is hardly ever idle.  One SM's
+// TMA unit delivers 24 B a clock (measured), too little for 80 KB in 2560 cycles, so K comes by
+// TMA and V by cp.async, which also fills rows past the sequence's end with zeros (a weight of
+// 0 times a stranger's NaN would be NaN).
 //
 // Warps:
 //  * 0-3 softmax of row tile 0, 4-7 of row tile 1, a row a thread: 64 scores at a time, one
-//    pass, weights P = 2^(s - m) against a running reference m straight back over the
-//    consumed scores as bf16 (relative 2^-8).  m is the row's first largest score, raised by
-//    whole powers of two when a score passes it by 2^8 (looked at before the 64 weights are
-//    written; what was written is rescaled exactly, and so are l and O); the sum l stays in
-//    fp32.  (l of the rounded weights, which would round as numerator does, is two instructions
-//    more a weight: 461 -> 480 us on 8192 tokens x 32 heads; a quarter of the exponentials as
-//    polynomials on the FMA pipe 480 -> 506: the softmax warps' instructions are what counts.)
-//  * 8 TMA: the first row tile's Q, K.  10-13 cp.async: the second's Q, V.  Chunks of 16 KB: three a key tile of K ([128 keys]
-//    [64 values]) and two of V ([64 keys][128 dims]), each kind in a ring of 4, each refilled
-//    as the MMAs that read it end.  (One ring of 8 for both let the next K wait for this V:
-//    474 us on 8192 tokens x 32 heads.)
+//    pass, weights P = 2^(s - m) against a reference m straight back over the consumed scores
+//    as bf16 (relative 2^-8).  m is the row's first largest score; only where the weights of 64
+//    scores add up to more than 64 x 2^8 is the largest one looked for, m raised by a whole power
+//    of two, and what was made with the old one (weights, l, O) rescaled exactly: bf16 and fp32
+//    hold weights above 1 as they hold those below (462 -> 452 us on 8192 tokens x 32 heads
+//    against a maximum over every 64 scores).  The sum l stays in fp32.  (l of the rounded
+//    weights, which would round as the numerator does, is two instructions more a weight: 461 ->
+//    480 us; a quarter of the exponentials as polynomials on the FMA pipe 480 -> 506; scores 32 at
+//    a time with the next ones on their way spill: 452 -> 480.)
+//  * 8 TMA: the first row tile's Q, K.  10-13 cp.async: the second's Q, V.  Chunks of 16 KB:
+//    three a key tile of K ([128 keys][64 values]) and two of V ([64 keys][128 dims]), each kind
+//    in a ring of 4, each refilled as the MMAs that read it end.  (One ring of 8 for both let the
+//    next K wait for this V: 474 us.)
 //  * 9 issues the MMAs in the order S0(k), P1 V(k-1), S1(k), P0 V(k): while one row tile's
 //    softmax runs the tensor pipe has the other's P V and next S (with a warp a tile they
 //    fell into step, both softmaxes at once and the pipe idle: 5400 cycles a key tile).
 //    S(k + 1) follows P V (k): it overwrites the P that P V reads, and the MMAs of one
 //    thread run in order.
 //
-// 8192 tokens x 32 heads: 461 us, 1.49 PFLOP/s.  Short chunks (4 of 162-417 rows behind
-// 179-791 cached ones, 32 heads): 36.8 us; 224 CTAs of 4 to 9 key tiles on 152 SMs, each with
+// 8192 tokens x 32 heads: 452 us, 1.52 PFLOP/s.  Short chunks (4 of 162-417 rows behind
+// 179-791 cached ones, 32 heads): 36.6 us; 224 CTAs of 4 to 9 key tiles on 152 SMs, each with
 // 5-6 us of launch, first copies and epilogue.  (CTAs that take the next unit themselves,
-// its copies issued early: 36.7 us there, 471 on the long prompt, whose loop got 6% slower.)
+// its copies issued early: no gain there, and the long prompt's loop got 6% slower.)
 //
 // Every mbarrier wait is bounded; a role whose wait runs out raises a CTA-wide abort
 // flag, the others stop at their next wait, and the CTA records PKV_STATUS_TIMEOUT and
@@ -76,7 +80,7 @@ constexpr uint32_t kOffAbort = kOffTmem + 4;
 constexpr uint32_t kSmemBytes = kOffAbort + 4;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;
-constexpr float kRaise = 8.f;
+constexpr float kRaise = 8.f, kTooMuch = 64.f * 256.f;
 
 // kind::f16, D f32, A and B bf16, M = 128.
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
@@ -349,63 +353,73 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
 #pragma unroll 1
             for (int cc = 0; cc < 2; ++cc) {
-                uint32_t v[64];
+                uint32_t v[64], w[32];
                 load(cc, v);
-                float mx = largest(v);
-                if (__any_sync(0xffffffffu, mx > m + kRaise)) {
-                    // Raise the references that are passed to the largest score from here on (an integer),
-                    // and rescale what was made with the old one: the weights before, l, O.
-                    if (cc == 0) {
-                        uint32_t u[64];
-                        load(1, u);
-                        mx = fmaxf(mx, largest(u));
-                    }
-                    float alpha = 1.f;
-                    if (mx > m + kRaise) {
-                        // The first largest score as it is, then steps of whole powers of two: the weights of the
-                        // largest scores are exact in bf16, and a row of one key is its value.
-                        const float up = m == -INFINITY ? INFINITY : ceilf(mx - m);
-                        alpha = fast_exp2(-up);
-                        m = m == -INFINITY ? mx : m + up;
-                    }
-                    l2 = fmul2(l2, make_float2(alpha, alpha));
-                    l3 = fmul2(l3, make_float2(alpha, alpha));
-                    tmem_wait_st();  // the weights that are read back now
-#pragma unroll 1
-                    for (int k = 0; k < 2 * cc; ++k) {
-                        uint32_t w[16];
-                        tmem_ld_32x32b_x16(s_at + 16 * k, w);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            w[e] = pack_bf16x2(__uint_as_float(w[e] << 16) * alpha, __uint_as_float(w[e] & 0xffff0000u) * alpha);
-                        tmem_st_32x32b_x16(s_at + 16 * k, w);
-                    }
-                    if (kt > 0) {  // every earlier P V of this tile completed before S (kt) did
-#pragma unroll 1
-                        for (int k = 0; k < 8; ++k) {
-                            uint32_t u[16];
-                            tmem_ld_32x32b_x16(o_at + 16 * k, u);
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-                            tmem_st_32x32b_x16(o_at + 16 * k, u);
+                float2 a2, a3;  // the chunk's sum, in four parts
+                // The reference is looked at only where it has to be: for a row's first keys, and again where weights against
+                // the old one add up to more than 64 x 2^8.
+                for (bool raise = __any_sync(0xffffffffu, m == -INFINITY);;) {
+                    if (raise) {
+                        // Raise the references that are passed to the largest score from here on, and rescale what was made
+                        // with the old one: the weights before, l, O.
+                        float mx = largest(v);
+                        if (cc == 0) {
+                            uint32_t u[64];
+                            load(1, u);
+                            mx = fmaxf(mx, largest(u));
                         }
-                    }
-                    tmem_wait_st();
-                    load(cc, v);  // (kept in tensor memory meanwhile, not in registers)
-                }
-                const float mu = m == -INFINITY ? 0.f : m;
-                const float2 sv = make_float2(sl2, sl2), nm = make_float2(-mu, -mu);
-                uint32_t w[32];
+                        float alpha = 1.f;
+                        if (mx > m + kRaise) {
+                            // The first largest score as it is, then steps of whole powers of two: the weights of the
+                            // largest scores are exact in bf16, and a row of one key is its value.
+                            const float up = m == -INFINITY ? INFINITY : ceilf(mx - m);
+                            alpha = fast_exp2(-up);
+                            m = m == -INFINITY ? mx : m + up;
+                        }
+                        l2 = fmul2(l2, make_float2(alpha, alpha));
+                        l3 = fmul2(l3, make_float2(alpha, alpha));
+                        tmem_wait_st();  // the weights that are read back now
+#pragma unroll 1
+                        for (int k = 0; k < 2 * cc; ++k) {
+                            uint32_t wt[16];
+                            tmem_ld_32x32b_x16(s_at + 16 * k, wt);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const float2 x = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sv, nm);
-                    const float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                    if (e & 1)
-                        l3 = fadd2(l3, pr);
-                    else
-                        l2 = fadd2(l2, pr);
-                    w[e] = pack_bf16x2(pr.x, pr.y);
+                            for (int e = 0; e < 16; ++e)
+                                wt[e] = pack_bf16x2(__uint_as_float(wt[e] << 16) * alpha, __uint_as_float(wt[e] & 0xffff0000u) * alpha);
+                            tmem_st_32x32b_x16(s_at + 16 * k, wt);
+                        }
+                        if (kt > 0) {  // every earlier P V of this tile completed before S (kt) did
+#pragma unroll 1
+                            for (int k = 0; k < 8; ++k) {
+                                uint32_t u[16];
+                                tmem_ld_32x32b_x16(o_at + 16 * k, u);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+                                tmem_st_32x32b_x16(o_at + 16 * k, u);
+                            }
+                        }
+                        tmem_wait_st();
+                        load(cc, v);  // (kept in tensor memory meanwhile, not in registers)
+                    }
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    const float2 sv = make_float2(sl2, sl2), nm = make_float2(-mu, -mu);
+                    a2 = a3 = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float2 x = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sv, nm);
+                        const float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        if (e & 1)
+                            a3 = fadd2(a3, pr);
+                        else
+                            a2 = fadd2(a2, pr);
+                        w[e] = pack_bf16x2(pr.x, pr.y);
+                    }
+                    if (raise || !__any_sync(0xffffffffu, (a2.x + a2.y) + (a3.x + a3.y) > kTooMuch)) break;
+                    raise = true;
+                    load(cc, v);
                 }
+                l2 = fadd2(l2, a2);
+                l3 = fadd2(l3, a3);
                 tmem_st_32x32b_x32(s_at + 32 * cc, w);
             }
             tmem_wait_st();
