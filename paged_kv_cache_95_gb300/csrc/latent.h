@@ -78,7 +78,7 @@ struct LatentPrefillParams {
     int32_t out_bf16;
 };
 struct LatentPrefillMaps {
-    CUtensorMap q, k, rope, out;
+    CUtensorMap q, k, rope;
 };
 cudaError_t latent_prefill_prepare_device();
 cudaError_t launch_latent_prefill(const LatentPrefillMaps &maps, const LatentPrefillParams &p, cudaStream_t stream);

@@ -403,12 +403,9 @@ int latent_attention_prefill_chunk(void *out, int32_t out_dtype, const void *q, 
     if (p.scale_log2 == 0.f) p.scale_log2 = 1e-37f;  // the kernel hides a key by an infinite score: never 0 x infinity
     if (!prepare_device()) return PKV_ERR_CUDA;
     pkv::LatentPrefillMaps maps;
-    // A float32 output never leaves by TMA; its map is encoded as the bf16 view of the same memory.
     if (!encode_rows(&maps.q, q, total_q_rows, num_heads, pkv::kExpandedQk, q_row_stride, q_head_stride, 128) ||
         !encode_rows(&maps.k, k_nope, total_k_rows, num_heads, pkv::kNopeDim, k_row_stride, k_head_stride, 128) ||
-        !encode_rows_2d(&maps.rope, k_rope, total_k_rows, k_rope_stride, 128) ||
-        !encode_rows(&maps.out, out, total_q_rows, num_heads, pkv::kExpandedV,
-                     static_cast<int64_t>(num_heads) * pkv::kExpandedV, pkv::kExpandedV, 32))
+        !encode_rows_2d(&maps.rope, k_rope, total_k_rows, k_rope_stride, 128))
         return PKV_ERR_CUDA;
     return pkv::launch_latent_prefill(maps, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK
                                                                                                 : PKV_ERR_CUDA;

@@ -40,8 +40,8 @@
 //    S(k + 1) follows P V (k): it overwrites the P that P V reads, and the MMAs of one
 //    thread run in order.
 //
-// 8192 tokens x 32 heads: 452 us, 1.52 PFLOP/s.  Short chunks (4 of 162-417 rows behind
-// 179-791 cached ones, 32 heads): 36.6 us; 224 CTAs of 4 to 9 key tiles on 152 SMs, each with
+// 8192 tokens x 32 heads: 447 us, 1.54 PFLOP/s.  Short chunks (4 of 162-417 rows behind
+// 179-791 cached ones, 32 heads): 36.2 us; 224 CTAs of 4 to 9 key tiles on 152 SMs, each with
 // 5-6 us of launch, first copies and epilogue.  (CTAs that take the next unit themselves,
 // its copies issued early: no gain there, and the long prompt's loop got 6% slower.)
 //
@@ -101,7 +101,7 @@ __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *sr
 
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                          const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap omap,
+                          const __grid_constant__ CUtensorMap rmap,
                           const LatentPrefillParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -113,7 +113,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&qmap);
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&rmap);
-        prefetch_tensormap(&omap);
     }
     griddep_launch_dependents();
     griddep_wait();  // the producers of q, keys and values before us on the stream
@@ -437,7 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (nt > 0 && alive && warp_wait(bar(kBarO + t), 0)) {
             tc_fence_after();
             const float l = (l2.x + l2.y) + (l3.x + l3.y), inv = l > 0.f ? 1.f / l : 0.f;
-            const bool staged = p.out_bf16 && rows == kRows;  // a full tile leaves by TMA from its Q's place
+            // bf16: a warp's 32 rows through its part of Q's place, then out in runs of 256 bytes (by TMA, at 24 bytes a clock,
+            // two full row tiles took 2 us longer).
             const uint32_t stage = sbase + kOffQ + 3 * t * kChunk;
             const size_t at = ((static_cast<size_t>(q0) + i0 + r) * p.heads + h) * kExpandedV;
 #pragma unroll 1
@@ -450,10 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 4; ++e) {
                         const uint4 w = make_uint4(pack_bf16x2(f(8 * e), f(8 * e + 1)), pack_bf16x2(f(8 * e + 2), f(8 * e + 3)),
                                                    pack_bf16x2(f(8 * e + 4), f(8 * e + 5)), pack_bf16x2(f(8 * e + 6), f(8 * e + 7)));
-                        if (staged)
-                            sts128(stage + (k >> 1) * kChunk + r * 128 + (((4 * (k & 1) + e) ^ (r & 7)) << 4), w);
-                        else if (r < rows)
-                            reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at)[4 * k + e] = w;
+                        sts128(stage + (k >> 1) * kChunk + r * 128 + (((4 * (k & 1) + e) ^ (r & 7)) << 4), w);
                     }
                 } else if (r < rows) {
 #pragma unroll
@@ -462,17 +459,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                             make_float4(f(4 * e), f(4 * e + 1), f(4 * e + 2), f(4 * e + 3));
                 }
             }
-            if (staged) {
-                // A warp's 32 rows are one box of their own: no barrier over the tile.
-                fence_proxy_async_smem();
+            if (p.out_bf16) {
                 __syncwarp();
-                if (elect_one()) {
-                    for (int k = 0; k < 2; ++k)
-                        tma_store_3d(&omap, stage + k * kChunk + quarter * 32 * 128, 64 * k, h, q0 + i0 + quarter * 32);
-                    bulk_commit_group();
-                    bulk_wait_group_read_all();  // shared memory must outlive the reads
+                const int c = lane & 15;
+                uint4 *out = static_cast<uint4 *>(p.out) + ((static_cast<size_t>(q0) + i0) * p.heads + h) * (kExpandedV / 8) + c;
+#pragma unroll 4
+                for (int k = 0; k < 16; ++k) {
+                    const int row = quarter * 32 + 2 * k + (lane >> 4);
+                    const uint4 w = lds128(stage + (c >> 3) * kChunk + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+                    if (row < rows) out[static_cast<size_t>(row) * p.heads * (kExpandedV / 8)] = w;
                 }
-                __syncwarp();
             }
         }
     }
@@ -502,8 +498,7 @@ cudaError_t latent_prefill_prepare_device() {
 cudaError_t launch_latent_prefill(const LatentPrefillMaps &maps, const LatentPrefillParams &p, cudaStream_t stream) {
     const int longest = p.max_q_len < p.total_q ? p.max_q_len : p.total_q;
     const dim3 grid(p.heads, p.num_seqs, (longest + 2 * kRows - 1) / (2 * kRows));
-    return launch_pdl(latent_prefill_kernel, grid, dim3(kThreads), kSmemBytes, stream, maps.q, maps.k, maps.rope, maps.out,
-                      p);
+    return launch_pdl(latent_prefill_kernel, grid, dim3(kThreads), kSmemBytes, stream, maps.q, maps.k, maps.rope, p);
 }
 
 }  // namespace pkv
