@@ -40,8 +40,8 @@
 //    S(k + 1) follows P V (k): it overwrites the P that P V reads, and the MMAs of one
 //    thread run in order.
 //
-// 8192 tokens x 32 heads: 447 us, 1.54 PFLOP/s.  Short chunks (4 of 162-417 rows behind
-// 179-791 cached ones, 32 heads): 36.2 us; 224 CTAs of 4 to 9 key tiles on 152 SMs, each with
+// 8192 tokens x 32 heads: 451 us, 1.52 PFLOP/s.  Short chunks (4 of 162-417 rows behind
+// 179-791 cached ones, 32 heads): 35.0 us; 224 CTAs of 4 to 9 key tiles on 152 SMs, each with
 // 5-6 us of launch, first copies and epilogue.  (CTAs that take the next unit themselves,
 // its copies issued early: no gain there, and the long prompt's loop got 6% slower.)
 //
@@ -52,6 +52,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "latent.h"
 #include "ptx.cuh"
@@ -74,7 +75,7 @@ constexpr uint32_t kOffV = kOffK + kSlotsK * kChunk;  // a chunk: [dim half][64 
 constexpr uint32_t kOffBar = kOffV + kSlotsV * kChunk;
 enum { kBarQ = 0, kBarFullK, kBarFullV = kBarFullK + kSlotsK, kBarEmptyK = kBarFullV + kSlotsV,
        kBarEmptyV = kBarEmptyK + kSlotsK, kBarS = kBarEmptyV + kSlotsV, kBarP = kBarS + 2, kBarO = kBarP + 2,
-       kNumBars = kBarO + 2 };
+       kBarMerge = kBarO + 2, kNumBars };
 constexpr uint32_t kOffTmem = kOffBar + 8 * kNumBars;
 constexpr uint32_t kOffAbort = kOffTmem + 4;
 constexpr uint32_t kSmemBytes = kOffAbort + 4;
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i)
             mbar_init(bar(i), i == kBarQ || (i >= kBarFullV && i < kBarEmptyK) ? kLoadThreads / 32
-                              : i >= kBarP && i < kBarO        ? 4
+                              : (i >= kBarP && i < kBarO) || i == kBarMerge ? 4
                                                                : 1);
         *abort_flag = 0u;
         fence_mbar_init();
@@ -192,286 +193,340 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto empty_k = [&](int j) { return bar(kBarEmptyK + j % kSlotsK); };
     auto empty_v = [&](int j) { return bar(kBarEmptyV + j % kSlotsV); };
 
-    if (warp == kTmaWarp) {
-        bool ok = true;
-        for (int j = 0; ok && j < kPerTileK * n_tiles; ++j) {
-            if (j >= kSlotsK && !(ok = warp_wait(empty_k(j), ((j / kSlotsK) - 1) & 1))) break;
-            const int kt = j / kPerTileK, i = j - kPerTileK * kt;
-            const uint32_t dst = sbase + kOffK + (j % kSlotsK) * kChunk;
-            if (elect_one()) {
-                // The first row tile's Q comes with the first K, chunk by chunk: S starts after 32 KB.
-                mbar_arrive_expect_tx(full_k(j), kt == 0 ? 2 * kChunk : kChunk);
-                if (kt == 0) tma_load_3d(sbase + kOffQ + i * kChunk, &qmap, full_k(j), 64 * i, h, q0 + r_lo);
-                if (i < 2)
-                    tma_load_3d(dst, &kmap, full_k(j), 64 * i, h, k0 + kt * kKeys);
-                else
-                    tma_load_2d(dst, &rmap, full_k(j), 0, k0 + kt * kKeys);
-            }
-            __syncwarp();
-        }
-    } else if (warp >= kLoadWarp) {
-        const int t = tid - kLoadWarp * 32;
-        // The second row tile's Q: 8 threads a 64-value chunk of a row, 16 rows at a time (zeros past the last row).
-        if (tile_rows(1) > 0) {
-            const int row = t >> 3, v = t & 7, r1 = q0 + r_lo + kRows + row;
-            const uint16_t *src = static_cast<const uint16_t *>(p.q) + static_cast<int64_t>(r1) * p.q_row + h * p.q_head + v * 8;
-            const uint32_t dst = sbase + kOffQ + 3 * kChunk + row * 128 + ((v ^ (row & 7)) << 4);
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    cp_async_16_or_zero(dst + i * kChunk + r * 16 * 128, src + 64 * i + r * 16 * p.q_row, r1 + 16 * r < p.total_q);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        // V, 16 threads a row, 8 rows at a time; rows past the sequence's keys become zeros.
-        const int row = t >> 4, v = t & 15;
-        const uint32_t to = (v >> 3) * (kChunk / 2) + row * 128 + (((v & 7) ^ row) << 4);
-        bool ok = true;
-        for (int kt = 0; ok && kt < n_tiles; ++kt) {
-            for (int i = 0; i < kPerTileV; ++i) {
-                const int j = kPerTileV * kt + i, key = kt * kKeys + 64 * i + row;
-                if (j >= kSlotsV) ok = ok && warp_wait(empty_v(j), ((j / kSlotsV) - 1) & 1);
-                if (!ok) break;
-                const uint16_t *src = static_cast<const uint16_t *>(p.v) + (static_cast<int64_t>(k0) + key) * p.k_row +
-                                      h * p.k_head + v * 8;
-                const uint32_t dst = sbase + kOffV + (j % kSlotsV) * kChunk + to;
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    cp_async_16_or_zero(dst + r * 8 * 128, src + r * 8 * p.k_row, key + 8 * r < k_len);
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                // What came before (Q, then the chunk before) has landed: made visible to the tensor core, an arrival a warp.
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(j == 0 ? bar(kBarQ) : full_v(j - 1));
-            }
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(full_v(kPerTileV * n_tiles - 1));
-    } else if (warp == kMmaWarp) {
-        // The warp runs whole on warp-uniform values, one elected lane issues: descriptors stay in uniform registers.
-        const int nt0 = tile_nt(0), nt1 = tile_nt(1);
-        const uint64_t q_desc = sw128_desc(sbase + kOffQ, 16, 1024);
-        const uint64_t k_desc = sw128_desc(sbase + kOffK, 16, 1024);
-        const uint64_t v_desc = sw128_desc(sbase + kOffV, kChunk / 2, 1024);  // 128 dims: two halves side by side
-        bool ok = true;
-        // Besides the weights the warp waits for K chunks only where it needs them first: the softmax warps look that
-        // V(k) and the first chunk of K(k + 1) have landed before they hand over P(k) (a wait costs this warp 100
-        // cycles and more even when it need not wait); the others are given until the MMAs before them are issued.
-        ok = ok && warp_wait(full_k(0), 0);
-        auto score = [&](int t, int kt) {
-            const bool first_reader = t == 0 || kt >= nt0, last_reader = t == 1 || kt >= nt1;
-            tc_fence_after();
-            const uint64_t qd = q_desc + static_cast<uint32_t>(3 * t) * (kChunk >> 4);
-            const int j = kPerTileK * kt;
-            auto chunk = [&](int i) {
-                const uint64_t kd = k_desc + static_cast<uint32_t>((j + i) % kSlotsK) * (kChunk >> 4);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    umma_bf16(tmem + 128 * t, qd + i * (kChunk >> 4) + 2 * kk, kd + 2 * kk, kIdescQK, i > 0 || kk > 0);
-                if (last_reader) umma_commit(empty_k(j + i));
-            };
-#pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                if (first_reader && i > 0) {
-                    ok = ok && warp_wait(full_k(j + i), ((j + i) / kSlotsK) & 1);
-                    tc_fence_after();
-                }
-                if (ok && elect_one()) {
-                    chunk(i);
-                    if (i == 2) umma_commit(bar(kBarS + t));
+    // One row tile (short chunks, a chunk's last rows) leaves the other's warps and tensor memory free: its keys are split,
+    // even tiles to the first group, odd ones to the second, and the first joins their O: a tile of keys in 1900 instead of
+    // 3100 cycles (4 chunks of up to 110 rows over 5.6K keys, 32 heads: 81 -> 55 us).  Else each group has a row tile.
+    auto roles = [&](auto split) {
+        constexpr bool kSplit = decltype(split)::value;
+        auto steps = [&](int t) { return kSplit ? (n_tiles + 1 - t) >> 1 : tile_nt(t); };  // key tiles that group t takes
+        auto key_tile = [&](int t, int i) { return kSplit ? 2 * i + t : i; };
+        if (warp == kTmaWarp) {
+            bool ok = true;
+            for (int j = 0; ok && j < kPerTileK * n_tiles; ++j) {
+                if (j >= kSlotsK && !(ok = warp_wait(empty_k(j), ((j / kSlotsK) - 1) & 1))) break;
+                const int kt = j / kPerTileK, i = j - kPerTileK * kt;
+                const uint32_t dst = sbase + kOffK + (j % kSlotsK) * kChunk;
+                if (elect_one()) {
+                    // The first row tile's Q comes with the first K, chunk by chunk: S starts after 32 KB.
+                    mbar_arrive_expect_tx(full_k(j), kt == 0 ? 2 * kChunk : kChunk);
+                    if (kt == 0) tma_load_3d(sbase + kOffQ + i * kChunk, &qmap, full_k(j), 64 * i, h, q0 + r_lo);
+                    if (i < 2)
+                        tma_load_3d(dst, &kmap, full_k(j), 64 * i, h, k0 + kt * kKeys);
+                    else
+                        tma_load_2d(dst, &rmap, full_k(j), 0, k0 + kt * kKeys);
                 }
                 __syncwarp();
             }
-        };
-        auto value = [&](int t, int kt) {
-            if (!(ok = ok && warp_wait(bar(kBarP + t), kt & 1))) return;
-            tc_fence_after();
-            const uint32_t o = tmem + kTmemO + 128 * t, w = tmem + 128 * t;
-            if (elect_one()) {
+        } else if (warp >= kLoadWarp) {
+            const int t = tid - kLoadWarp * 32;
+            // The second row tile's Q: 8 threads a 64-value chunk of a row, 16 rows at a time (zeros past the last row).
+            if (tile_rows(1) > 0) {
+                const int row = t >> 3, v = t & 7, r1 = q0 + r_lo + kRows + row;
+                const uint16_t *src = static_cast<const uint16_t *>(p.q) + static_cast<int64_t>(r1) * p.q_row + h * p.q_head + v * 8;
+                const uint32_t dst = sbase + kOffQ + 3 * kChunk + row * 128 + ((v ^ (row & 7)) << 4);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int j = kPerTileV * kt + i;
-                    const uint64_t vd = v_desc + static_cast<uint32_t>(j % kSlotsV) * (kChunk >> 4);
+                for (int i = 0; i < 3; ++i)
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        umma_bf16_tmem_a(o, w + 32 * i + 8 * ks, vd + ks * (2048 >> 4), kIdescPV, kt > 0 || i + ks > 0);
-                    if (t == 1 || kt >= nt1) umma_commit(empty_v(j));  // its last reader
-                }
-                if (kt == (t == 0 ? nt0 : nt1) - 1) umma_commit(bar(kBarO + t));
+                    for (int r = 0; r < 8; ++r)
+                        cp_async_16_or_zero(dst + i * kChunk + r * 16 * 128, src + 64 * i + r * 16 * p.q_row, r1 + 16 * r < p.total_q);
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            // V, 16 threads a row, 8 rows at a time; rows past the sequence's keys become zeros.
+            const int row = t >> 4, v = t & 15;
+            const uint32_t to = (v >> 3) * (kChunk / 2) + row * 128 + (((v & 7) ^ row) << 4);
+            bool ok = true;
+            for (int kt = 0; ok && kt < n_tiles; ++kt) {
+                for (int i = 0; i < kPerTileV; ++i) {
+                    const int j = kPerTileV * kt + i, key = kt * kKeys + 64 * i + row;
+                    if (j >= kSlotsV) ok = ok && warp_wait(empty_v(j), ((j / kSlotsV) - 1) & 1);
+                    if (!ok) break;
+                    const uint16_t *src = static_cast<const uint16_t *>(p.v) + (static_cast<int64_t>(k0) + key) * p.k_row +
+                                          h * p.k_head + v * 8;
+                    const uint32_t dst = sbase + kOffV + (j % kSlotsV) * kChunk + to;
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        cp_async_16_or_zero(dst + r * 8 * 128, src + r * 8 * p.k_row, key + 8 * r < k_len);
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+                    // What came before (Q, then the chunk before) has landed: made visible to the tensor core, an arrival a warp.
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(j == 0 ? bar(kBarQ) : full_v(j - 1));
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
             __syncwarp();
-        };
-        for (int kt = 0; ok && kt <= n_tiles; ++kt) {
-            if (kt < nt0) score(0, kt);
-            if (ok && kt >= 1 && kt - 1 < nt1) value(1, kt - 1);
-            if (kt == 0 && nt1 > 0) ok = ok && warp_wait(bar(kBarQ), 0);
-            if (ok && kt < nt1) score(1, kt);
-            if (ok && kt < nt0) value(0, kt);
-        }
-    } else {
-        // ---------------- softmax: a row a thread ----------------
-        const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-        const int nt = tile_nt(t), nt0 = tile_nt(0), rows = tile_rows(t), i0 = r_lo + t * kRows;
-        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        const uint32_t s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + kTmemO + 128 * t;
-        const float sl2 = p.scale_log2;
-        const bool neg = sl2 < 0.f;  // then the largest score is the smallest product
-        const float hidden = neg ? INFINITY : -INFINITY;
-        const int limit = c + i0 + r;  // last visible key
-        float m = -INFINITY;
-        float2 l2 = make_float2(0.f, 0.f), l3 = l2;  // the sum, in four parts
-        bool alive = true;
-        for (int kt = 0; alive && kt < nt; ++kt) {
-            if (!(alive = warp_wait(bar(kBarS + t), kt & 1))) break;
-            tc_fence_after();
-            const bool mask = kt * kKeys + kKeys - 1 > c + i0;  // some row does not see some key
-            auto load = [&](int cc, uint32_t(&v)[64]) {
-                tmem_ld_32x32b_x64(s_at + 64 * cc, v);
-                if (mask) {
-                    const int last = limit - kt * kKeys - 64 * cc;
+            if (ok && lane == 0) mbar_arrive(full_v(kPerTileV * n_tiles - 1));
+        } else if (warp == kMmaWarp) {
+            // The warp runs whole on warp-uniform values, one elected lane issues: descriptors stay in uniform registers.
+            const int nt0 = steps(0), nt1 = steps(1);
+            const uint64_t q_desc = sw128_desc(sbase + kOffQ, 16, 1024);
+            const uint64_t k_desc = sw128_desc(sbase + kOffK, 16, 1024);
+            const uint64_t v_desc = sw128_desc(sbase + kOffV, kChunk / 2, 1024);  // 128 dims: two halves side by side
+            bool ok = true;
+            // Besides the weights the warp waits for K chunks only where it needs them first: the softmax warps look that
+            // V(k) and the first chunk of K(k + 1) have landed before they hand over P(k) (a wait costs this warp 100
+            // cycles and more even when it need not wait); the others are given until the MMAs before them are issued.
+            ok = ok && warp_wait(full_k(0), 0);
+            auto score = [&](int t, int i) {
+                const int kt = key_tile(t, i);
+                const bool first_reader = kSplit || t == 0 || kt >= nt0, last_reader = kSplit || t == 1 || kt >= nt1;
+                tc_fence_after();
+                const uint64_t qd = q_desc + static_cast<uint32_t>(kSplit ? 0 : 3 * t) * (kChunk >> 4);
+                const int j = kPerTileK * kt;
+                auto chunk = [&](int i) {
+                    const uint64_t kd = k_desc + static_cast<uint32_t>((j + i) % kSlotsK) * (kChunk >> 4);
 #pragma unroll
-                    for (int e = 0; e < 64; ++e)
-                        if (e > last) v[e] = __float_as_uint(hidden);
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16(tmem + 128 * t, qd + i * (kChunk >> 4) + 2 * kk, kd + 2 * kk, kIdescQK, i > 0 || kk > 0);
+                    if (last_reader) umma_commit(empty_k(j + i));
+                };
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    if (first_reader && (kSplit || i > 0)) {
+                        ok = ok && warp_wait(full_k(j + i), ((j + i) / kSlotsK) & 1);
+                        tc_fence_after();
+                    }
+                    if (ok && elect_one()) {
+                        chunk(i);
+                        if (i == 2) umma_commit(bar(kBarS + t));
+                    }
+                    __syncwarp();
                 }
             };
-            // The largest score of 64 (log2 domain).
-            auto largest = [&](const uint32_t(&v)[64]) {
-                float x[4] = {hidden, hidden, hidden, hidden};
-                if (neg) {
+            auto value = [&](int t, int step) {
+                const int kt = key_tile(t, step);
+                const bool of_v = kSplit && (lane == 1 || lane == 2);  // (else the softmax warps looked)
+                const int jv = kPerTileV * kt + (lane & 1);
+                if (!(ok = ok && lanes_wait(of_v ? full_v(jv) : bar(kBarP + t), (of_v ? jv / kSlotsV : step) & 1))) return;
+                tc_fence_after();
+                const uint32_t o = tmem + kTmemO + 128 * t, w = tmem + 128 * t;
+                if (elect_one()) {
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) x[e & 3] = fminf(x[e & 3], __uint_as_float(v[e]));
-                    return fminf(fminf(x[0], x[1]), fminf(x[2], x[3])) * sl2;
+                    for (int i = 0; i < 2; ++i) {
+                        const int j = kPerTileV * kt + i;
+                        const uint64_t vd = v_desc + static_cast<uint32_t>(j % kSlotsV) * (kChunk >> 4);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            umma_bf16_tmem_a(o, w + 32 * i + 8 * ks, vd + ks * (2048 >> 4), kIdescPV, step > 0 || i + ks > 0);
+                        if (kSplit || t == 1 || kt >= nt1) umma_commit(empty_v(j));  // its last reader
+                    }
+                    if (step == (t == 0 ? nt0 : nt1) - 1) umma_commit(bar(kBarO + t));
                 }
-#pragma unroll
-                for (int e = 0; e < 64; e += 2)
-                    x[(e >> 1) & 3] = fmax3(x[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-                return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl2;
+                __syncwarp();
             };
-#pragma unroll 1
-            for (int cc = 0; cc < 2; ++cc) {
-                uint32_t v[64], w[32];
-                load(cc, v);
-                float2 a2, a3;  // the chunk's sum, in four parts
-                // The reference is looked at only where it has to be: for a row's first keys, and again where weights against
-                // the old one add up to more than 64 x 2^8.
-                for (bool raise = __any_sync(0xffffffffu, m == -INFINITY);;) {
-                    if (raise) {
-                        // Raise the references that are passed to the largest score from here on, and rescale what was made
-                        // with the old one: the weights before, l, O.
-                        float mx = largest(v);
-                        if (cc == 0) {
-                            uint32_t u[64];
-                            load(1, u);
-                            mx = fmaxf(mx, largest(u));
-                        }
-                        float alpha = 1.f;
-                        if (mx > m + kRaise) {
-                            // The first largest score as it is, then steps of whole powers of two: the weights of the
-                            // largest scores are exact in bf16, and a row of one key is its value.
-                            const float up = m == -INFINITY ? INFINITY : ceilf(mx - m);
-                            alpha = fast_exp2(-up);
-                            m = m == -INFINITY ? mx : m + up;
-                        }
-                        l2 = fmul2(l2, make_float2(alpha, alpha));
-                        l3 = fmul2(l3, make_float2(alpha, alpha));
-                        tmem_wait_st();  // the weights that are read back now
-#pragma unroll 1
-                        for (int k = 0; k < 2 * cc; ++k) {
-                            uint32_t wt[16];
-                            tmem_ld_32x32b_x16(s_at + 16 * k, wt);
+            for (int i = 0; ok && i <= max(nt0, nt1); ++i) {
+                if (i < nt0) score(0, i);
+                if (ok && i >= 1 && i - 1 < nt1) value(1, i - 1);
+                if (!kSplit && i == 0 && nt1 > 0) ok = ok && warp_wait(bar(kBarQ), 0);
+                if (ok && i < nt1) score(1, i);
+                if (ok && i < nt0) value(0, i);
+            }
+        } else {
+            // ---------------- softmax: a row a thread ----------------
+            const int t = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+            const int nt = steps(t), nt0 = tile_nt(0), rows = tile_rows(kSplit ? 0 : t), i0 = r_lo + (kSplit ? 0 : t * kRows);
+            const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+            const uint32_t s_at = tmem + lanes + 128 * t, o_at = tmem + lanes + kTmemO + 128 * t;
+            const float sl2 = p.scale_log2;
+            const bool neg = sl2 < 0.f;  // then the largest score is the smallest product
+            const float hidden = neg ? INFINITY : -INFINITY;
+            const int limit = c + i0 + r;  // last visible key
+            float m = -INFINITY;
+            float2 l2 = make_float2(0.f, 0.f), l3 = l2;  // the sum, in four parts
+            bool alive = true;
+            for (int i = 0; alive && i < nt; ++i) {
+                const int kt = key_tile(t, i);
+                if (!(alive = warp_wait(bar(kBarS + t), i & 1))) break;
+                tc_fence_after();
+                const bool mask = kt * kKeys + kKeys - 1 > c + i0;  // some row does not see some key
+                auto load = [&](int cc, uint32_t(&v)[64]) {
+                    tmem_ld_32x32b_x64(s_at + 64 * cc, v);
+                    if (mask) {
+                        const int last = limit - kt * kKeys - 64 * cc;
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                wt[e] = pack_bf16x2(__uint_as_float(wt[e] << 16) * alpha, __uint_as_float(wt[e] & 0xffff0000u) * alpha);
-                            tmem_st_32x32b_x16(s_at + 16 * k, wt);
-                        }
-                        if (kt > 0) {  // every earlier P V of this tile completed before S (kt) did
-#pragma unroll 1
-                            for (int k = 0; k < 8; ++k) {
-                                uint32_t u[16];
-                                tmem_ld_32x32b_x16(o_at + 16 * k, u);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
-                                tmem_st_32x32b_x16(o_at + 16 * k, u);
-                            }
-                        }
-                        tmem_wait_st();
-                        load(cc, v);  // (kept in tensor memory meanwhile, not in registers)
+                        for (int e = 0; e < 64; ++e)
+                            if (e > last) v[e] = __float_as_uint(hidden);
                     }
-                    const float mu = m == -INFINITY ? 0.f : m;
-                    const float2 sv = make_float2(sl2, sl2), nm = make_float2(-mu, -mu);
-                    a2 = a3 = make_float2(0.f, 0.f);
+                };
+                // The largest score of 64 (log2 domain).
+                auto largest = [&](const uint32_t(&v)[64]) {
+                    float x[4] = {hidden, hidden, hidden, hidden};
+                    if (neg) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float2 x = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sv, nm);
-                        const float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                        if (e & 1)
-                            a3 = fadd2(a3, pr);
-                        else
-                            a2 = fadd2(a2, pr);
-                        w[e] = pack_bf16x2(pr.x, pr.y);
+                        for (int e = 0; e < 64; ++e) x[e & 3] = fminf(x[e & 3], __uint_as_float(v[e]));
+                        return fminf(fminf(x[0], x[1]), fminf(x[2], x[3])) * sl2;
                     }
-                    if (raise || !__any_sync(0xffffffffu, (a2.x + a2.y) + (a3.x + a3.y) > kTooMuch)) break;
-                    raise = true;
+#pragma unroll
+                    for (int e = 0; e < 64; e += 2)
+                        x[(e >> 1) & 3] = fmax3(x[(e >> 1) & 3], __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl2;
+                };
+#pragma unroll 1
+                for (int cc = 0; cc < 2; ++cc) {
+                    uint32_t v[64], w[32];
                     load(cc, v);
-                }
-                l2 = fadd2(l2, a2);
-                l3 = fadd2(l3, a3);
-                tmem_st_32x32b_x32(s_at + 32 * cc, w);
-            }
-            tmem_wait_st();
-            if (quarter == 0 && (t == 0 || kt >= nt0)) {
-                // V(kt) and, for the S that follows, the first chunk of K(kt + 1): a lane a chunk.
-                const int jv = kPerTileV * kt + (lane & 1), jk = kPerTileK * (kt + 1);
-                const bool of_k = lane == 2 && kt + 1 < n_tiles;
-                alive = lanes_wait(of_k ? full_k(jk) : full_v(jv), (of_k ? jk / kSlotsK : jv / kSlotsV) & 1);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (alive && lane == 0) mbar_arrive(bar(kBarP + t));
-        }
-        // ---------------- epilogue: out = O / l ----------------
-        if (nt > 0 && alive && warp_wait(bar(kBarO + t), 0)) {
-            tc_fence_after();
-            const float l = (l2.x + l2.y) + (l3.x + l3.y), inv = l > 0.f ? 1.f / l : 0.f;
-            // bf16: a warp's 32 rows through its part of Q's place, then out in runs of 256 bytes (by TMA, at 24 bytes a clock,
-            // two full row tiles took 2 us longer).
-            const uint32_t stage = sbase + kOffQ + 3 * t * kChunk;
-            const size_t at = ((static_cast<size_t>(q0) + i0 + r) * p.heads + h) * kExpandedV;
+                    float2 a2, a3;  // the chunk's sum, in four parts
+                    // The reference is looked at only where it has to be: for a row's first keys, and again where weights against
+                    // the old one add up to more than 64 x 2^8.
+                    for (bool raise = __any_sync(0xffffffffu, m == -INFINITY);;) {
+                        if (raise) {
+                            // Raise the references that are passed to the largest score from here on, and rescale what was made
+                            // with the old one: the weights before, l, O.
+                            float mx = largest(v);
+                            if (cc == 0) {
+                                uint32_t u[64];
+                                load(1, u);
+                                mx = fmaxf(mx, largest(u));
+                            }
+                            float alpha = 1.f;
+                            if (mx > m + kRaise) {
+                                // The first largest score as it is, then steps of whole powers of two: the weights of the
+                                // largest scores are exact in bf16, and a row of one key is its value.
+                                const float up = m == -INFINITY ? INFINITY : ceilf(mx - m);
+                                alpha = fast_exp2(-up);
+                                m = m == -INFINITY ? mx : m + up;
+                            }
+                            l2 = fmul2(l2, make_float2(alpha, alpha));
+                            l3 = fmul2(l3, make_float2(alpha, alpha));
+                            tmem_wait_st();  // the weights that are read back now
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(o_at + 32 * k, v);
-                auto f = [&](int e) { return __uint_as_float(v[e]) * inv; };
-                if (p.out_bf16) {
+                            for (int k = 0; k < 2 * cc; ++k) {
+                                uint32_t wt[16];
+                                tmem_ld_32x32b_x16(s_at + 16 * k, wt);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint4 w = make_uint4(pack_bf16x2(f(8 * e), f(8 * e + 1)), pack_bf16x2(f(8 * e + 2), f(8 * e + 3)),
-                                                   pack_bf16x2(f(8 * e + 4), f(8 * e + 5)), pack_bf16x2(f(8 * e + 6), f(8 * e + 7)));
-                        sts128(stage + (k >> 1) * kChunk + r * 128 + (((4 * (k & 1) + e) ^ (r & 7)) << 4), w);
+                                for (int e = 0; e < 16; ++e)
+                                    wt[e] = pack_bf16x2(__uint_as_float(wt[e] << 16) * alpha, __uint_as_float(wt[e] & 0xffff0000u) * alpha);
+                                tmem_st_32x32b_x16(s_at + 16 * k, wt);
+                            }
+                            if (i > 0) {  // every earlier P V of this tile completed before S (kt) did
+#pragma unroll 1
+                                for (int k = 0; k < 8; ++k) {
+                                    uint32_t u[16];
+                                    tmem_ld_32x32b_x16(o_at + 16 * k, u);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+                                    tmem_st_32x32b_x16(o_at + 16 * k, u);
+                                }
+                            }
+                            tmem_wait_st();
+                            load(cc, v);  // (kept in tensor memory meanwhile, not in registers)
+                        }
+                        const float mu = m == -INFINITY ? 0.f : m;
+                        const float2 sv = make_float2(sl2, sl2), nm = make_float2(-mu, -mu);
+                        a2 = a3 = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float2 x = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sv, nm);
+                            const float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                            if (e & 1)
+                                a3 = fadd2(a3, pr);
+                            else
+                                a2 = fadd2(a2, pr);
+                            w[e] = pack_bf16x2(pr.x, pr.y);
+                        }
+                        if (raise || !__any_sync(0xffffffffu, (a2.x + a2.y) + (a3.x + a3.y) > kTooMuch)) break;
+                        raise = true;
+                        load(cc, v);
                     }
-                } else if (r < rows) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[8 * k + e] =
-                            make_float4(f(4 * e), f(4 * e + 1), f(4 * e + 2), f(4 * e + 3));
+                    l2 = fadd2(l2, a2);
+                    l3 = fadd2(l3, a3);
+                    tmem_st_32x32b_x32(s_at + 32 * cc, w);
                 }
-            }
-            if (p.out_bf16) {
+                tmem_wait_st();
+                if (!kSplit && quarter == 0 && (t == 0 || kt >= nt0)) {
+                    // V(kt) and, for the S that follows, the first chunk of K(kt + 1): a lane a chunk.
+                    const int jv = kPerTileV * kt + (lane & 1), jk = kPerTileK * (kt + 1);
+                    const bool of_k = lane == 2 && kt + 1 < n_tiles;
+                    alive = lanes_wait(of_k ? full_k(jk) : full_v(jv), (of_k ? jk / kSlotsK : jv / kSlotsV) & 1);
+                }
+                tc_fence_before();
                 __syncwarp();
-                const int c = lane & 15;
-                uint4 *out = static_cast<uint4 *>(p.out) + ((static_cast<size_t>(q0) + i0) * p.heads + h) * (kExpandedV / 8) + c;
+                if (alive && lane == 0) mbar_arrive(bar(kBarP + t));
+            }
+            // ---------------- epilogue: out = O / l ----------------
+            if (nt > 0 && alive && warp_wait(bar(kBarO + t), 0)) {
+                tc_fence_after();
+                float l = (l2.x + l2.y) + (l3.x + l3.y), w0 = 1.f, w1 = 0.f;
+                // Split keys: the second group's (m, l) in the place of a second row tile's Q, its O in K's ring, which every S is
+                // done with ([128 rows][32 vectors], a row's vectors turned by the row).
+                const uint32_t other_ml = sbase + kOffQ + 3 * kChunk + 8 * r, other_o = sbase + kOffK + 512 * r;
+                if (kSplit && t == 1) {
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(o_at + 32 * k, v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            sts128(other_o + (((8 * k + e) ^ lane) << 4), make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+                    }
+                    sts32(other_ml, __float_as_uint(m));
+                    sts32(other_ml + 4, __float_as_uint(l));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(kBarMerge));
+                    return;
+                }
+                if (kSplit) {
+                    if (!warp_wait(bar(kBarMerge), 0)) return;
+                    const float2 ml = lds_f32x2(other_ml);
+                    const float all = fmaxf(m, ml.x);
+                    w0 = m == -INFINITY ? 0.f : fast_exp2(m - all);
+                    w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - all);
+                    l = w0 * l + w1 * ml.y;
+                }
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                // bf16: a warp's 32 rows through its part of Q's place, then out in runs of 256 bytes (by TMA, at 24 bytes a clock,
+                // two full row tiles took 2 us longer).
+                const uint32_t stage = sbase + kOffQ + 3 * t * kChunk;
+                const size_t at = ((static_cast<size_t>(q0) + i0 + r) * p.heads + h) * kExpandedV;
+#pragma unroll 1
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(o_at + 32 * k, v);
+                    if (kSplit) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint4 u = lds128(other_o + (((8 * k + e) ^ lane) << 4));
+                            auto join = [&](int x, uint32_t y) {
+                                v[4 * e + x] = __float_as_uint(w0 * __uint_as_float(v[4 * e + x]) + (w1 > 0.f ? w1 * __uint_as_float(y) : 0.f));
+                            };
+                            join(0, u.x), join(1, u.y), join(2, u.z), join(3, u.w);
+                        }
+                    }
+                    auto f = [&](int e) { return __uint_as_float(v[e]) * inv; };
+                    if (p.out_bf16) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint4 w = make_uint4(pack_bf16x2(f(8 * e), f(8 * e + 1)), pack_bf16x2(f(8 * e + 2), f(8 * e + 3)),
+                                                       pack_bf16x2(f(8 * e + 4), f(8 * e + 5)), pack_bf16x2(f(8 * e + 6), f(8 * e + 7)));
+                            sts128(stage + (k >> 1) * kChunk + r * 128 + (((4 * (k & 1) + e) ^ (r & 7)) << 4), w);
+                        }
+                    } else if (r < rows) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[8 * k + e] =
+                                make_float4(f(4 * e), f(4 * e + 1), f(4 * e + 2), f(4 * e + 3));
+                    }
+                }
+                if (p.out_bf16) {
+                    __syncwarp();
+                    const int c = lane & 15;
+                    uint4 *out = static_cast<uint4 *>(p.out) + ((static_cast<size_t>(q0) + i0) * p.heads + h) * (kExpandedV / 8) + c;
 #pragma unroll 4
-                for (int k = 0; k < 16; ++k) {
-                    const int row = quarter * 32 + 2 * k + (lane >> 4);
-                    const uint4 w = lds128(stage + (c >> 3) * kChunk + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-                    if (row < rows) out[static_cast<size_t>(row) * p.heads * (kExpandedV / 8)] = w;
+                    for (int k = 0; k < 16; ++k) {
+                        const int row = quarter * 32 + 2 * k + (lane >> 4);
+                        const uint4 w = lds128(stage + (c >> 3) * kChunk + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+                        if (row < rows) out[static_cast<size_t>(row) * p.heads * (kExpandedV / 8)] = w;
+                    }
                 }
             }
         }
-    }
+    };
+    if (tile_rows(1) == 0 && n_tiles > 1)
+        roles(std::true_type{});
+    else
+        roles(std::false_type{});
 
     // ---- teardown: every role is done (or gave up); free tensor memory ----
     tc_fence_before();

@@ -448,6 +448,14 @@ def test_prefill_many_sequences():
     check_prefill(*prefill_inputs(3, q_lens, k_lens, 2), q_lens, k_lens)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("k_lens", [[1000, 897, 128, 140], [129, 256, 257, 1153], [385, 1, 4000, 512]])
+def test_prefill_one_row_tile(k_lens, dtype):
+    """Up to 128 rows over one, even and odd numbers of key tiles."""
+    q_lens = [100, 1, 128, 7]
+    check_prefill(*prefill_inputs(sum(k_lens), q_lens, k_lens, 3), q_lens, k_lens, dtype=dtype)
+
+
 def test_prefill_strides():
     """Heads outermost, and packed keys and values of their own."""
     g = R.gen(4)
