@@ -760,8 +760,10 @@ PKV_API int latent_attention_decode_fp8(void *out, int32_t out_dtype, const void
  *   max_q_len : host upper bound of every q_len (sizes the launch grid; the lesser of
  *               it and total_q_rows up to 16776960)
  *   total_q_rows, total_k_rows : rows of q / out and of the keys
- *   workspace : 256-byte aligned, latent_attention_prefill_workspace_size() bytes
- *               (status word at byte 0, zeroed once)
+ *   workspace : 256-byte aligned, status word at byte 0, zeroed once.  With
+ *               latent_attention_prefill_workspace_size() bytes (for the current device;
+ *               152 SMs are assumed without a GPU) the keys of few rows are shared by
+ *               several CTAs; with the status word alone (256 bytes) never
  * A sequence with q_len > k_len or q_len > max_q_len, or whose rows lie outside
  * the tensors, sets PKV_STATUS_BAD_Q_LEN; its rows that can be addressed become
  * zeros.  Rows of out past cu_q_lens[num_seqs] are left as they were.  Rows that

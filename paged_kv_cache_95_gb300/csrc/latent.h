@@ -76,7 +76,12 @@ struct LatentPrefillParams {
     int32_t num_seqs, heads, max_q_len, total_q, total_k;
     float scale_log2;
     int32_t out_bf16;
+    int32_t pairs;   // of row tiles in the longest chunk
+    int32_t splits;  // parts of a pair's key tiles (1: no partials)
+    float2 *part_ml;  // [splits][total_q][heads] (m, l), log2 domain, scale folded in
+    float *part_o;    // the same x [128], unnormalised
 };
+constexpr int kLatentMaxSplits = 32;  // the merge keeps a split a lane
 struct LatentPrefillMaps {
     CUtensorMap q, k, rope;
 };

@@ -24,6 +24,7 @@ constexpr int kMaxDevices = 64;
 constexpr int kDefaultSms = 152;  // sizes asked for without a GPU
 constexpr int32_t kMaxRowsPerSeq = 16;
 constexpr int32_t kMaxHeads = 1024;
+constexpr int64_t kMinSplitTiles = 6;  // key tiles from which a pair's are split (4 tiles: 10.1 us whole, 11.8 in parts)
 constexpr int32_t kMaxChunk = 65535 * 256;  // query rows of a prefill chunk: 256 a step of the launch grid
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -144,6 +145,30 @@ DecodePlan plan_decode(int32_t num_seqs, int32_t q_per_seq, int32_t heads, int32
     pl.off_ml = kStatusBytes + align_up(static_cast<size_t>(pl.ranges) * 8, 256);
     pl.off_o = pl.off_ml + align_up(rows * 8, 256);
     pl.total = pl.off_o + rows * pkv::kLatentDim * 4;
+    return pl;
+}
+
+// How a prefill call is split: pairs of row tiles (256 rows) over the grid, and where those do not fill the GPU their key
+// tiles in parts (the lengths are device data: the parts follow from the totals).  Workspace: [status 256 B | part_ml |
+// part_o].
+struct PrefillPlan {
+    int32_t pairs, splits;
+    size_t off_o, total;
+};
+PrefillPlan plan_prefill(int32_t num_seqs, int32_t heads, int32_t max_q_len, int32_t total_q, int32_t total_k, int sms) {
+    PrefillPlan pl{};
+    pl.pairs = (std::min(max_q_len, total_q) + 255) / 256;
+    const int64_t units = static_cast<int64_t>(heads) *
+                          std::min<int64_t>(static_cast<int64_t>(num_seqs) * pl.pairs, (static_cast<int64_t>(total_q) + 255) / 256 + num_seqs);
+    const int64_t tiles = (static_cast<int64_t>(total_k) / num_seqs + 127) / 128;
+    // A part costs its tiles (1 us each) and its share of the merge (0.4 us): sqrt(2.5 tiles) parts are least.  100 rows x 8
+    // heads over 1000 / 2000 / 4000 keys: 14.1 -> 11.7, 22.3 -> 12.9, 38.5 -> 14.3 us; 512 rows x 16 heads over 4000: 64.7 -> 31.
+    const int64_t best = static_cast<int64_t>(std::sqrt(2.5 * static_cast<double>(tiles)));
+    const int64_t splits = units > 0 && tiles >= kMinSplitTiles ? std::min<int64_t>({sms / units, best, pkv::kLatentMaxSplits}) : 1;
+    pl.splits = static_cast<int32_t>(std::max<int64_t>(splits, 1));
+    const size_t rows = pl.splits > 1 ? static_cast<size_t>(pl.splits) * total_q * heads : 0;
+    pl.off_o = kStatusBytes + align_up(rows * 8, 256);
+    pl.total = pl.off_o + rows * pkv::kExpandedV * 4;
     return pl;
 }
 
@@ -350,7 +375,8 @@ size_t latent_attention_prefill_workspace_size(int32_t num_seqs, int32_t num_hea
     if (num_seqs < 1 || num_seqs > 65535 || num_heads < 1 || num_heads > kMaxHeads || max_q_len < 0 ||
         total_q_rows < 0 || total_k_rows < 0)
         return 0;
-    return kStatusBytes;
+    const int sms = current_sms();
+    return plan_prefill(num_seqs, num_heads, max_q_len, total_q_rows, total_k_rows, sms > 0 ? sms : kDefaultSms).total;
 }
 
 int latent_attention_prefill_chunk(void *out, int32_t out_dtype, const void *q, int64_t q_row_stride,
@@ -367,9 +393,7 @@ int latent_attention_prefill_chunk(void *out, int32_t out_dtype, const void *q, 
     pkv::LatentPrefillParams p{};
     if (!log2_scale(scale, &p.scale_log2)) return PKV_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256)) return PKV_ERR_INVALID_ARG;
-    if (workspace_bytes <
-        latent_attention_prefill_workspace_size(num_seqs, num_heads, max_q_len, total_q_rows, total_k_rows))
-        return PKV_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < kStatusBytes) return PKV_ERR_WORKSPACE_TOO_SMALL;
     if (max_q_len == 0 || total_q_rows == 0) return PKV_OK;
     if (!out || !q || !k_nope || !v || !k_rope || !cu_q_lens || !cu_k_lens || total_k_rows < 1)
         return PKV_ERR_INVALID_ARG;
@@ -401,7 +425,14 @@ int latent_attention_prefill_chunk(void *out, int32_t out_dtype, const void *q, 
     p.total_k = total_k_rows;
     p.out_bf16 = out_dtype == PKV_DTYPE_BF16;
     if (p.scale_log2 == 0.f) p.scale_log2 = 1e-37f;  // the kernel hides a key by an infinite score: never 0 x infinity
-    if (!prepare_device()) return PKV_ERR_CUDA;
+    const int sms = current_sms();
+    if (sms < 1 || !prepare_device()) return PKV_ERR_CUDA;
+    PrefillPlan pl = plan_prefill(num_seqs, num_heads, max_q_len, total_q_rows, total_k_rows, sms);
+    if (workspace_bytes < pl.total) pl.splits = 1;  // the status word alone
+    p.pairs = pl.pairs;
+    p.splits = pl.splits;
+    p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + kStatusBytes);
+    p.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + pl.off_o);
     pkv::LatentPrefillMaps maps;
     if (!encode_rows(&maps.q, q, total_q_rows, num_heads, pkv::kExpandedQk, q_row_stride, q_head_stride, 128) ||
         !encode_rows(&maps.k, k_nope, total_k_rows, num_heads, pkv::kNopeDim, k_row_stride, k_head_stride, 128) ||

@@ -5,7 +5,8 @@
 //     out_i = sum_j softmax(s)_j v_j
 //
 // One CTA takes two adjacent tiles of 128 query rows of one head and walks the keys in
-// tiles of 128 once for both; per key tile and row tile S = Q K^T (M = N = 128, 192 values:
+// tiles of 128 once for both (where such pairs do not fill the GPU, each walks a part of the
+// keys, and a second kernel joins the parts (m, l, O)); per key tile and row tile S = Q K^T (M = N = 128, 192 values:
 // two chunks of k_nope, one of the rotated key that all heads share) and O += P V (P from
 // tensor memory).  Tensor memory: S / P of row tile t in columns [128 t, +128), O in
 // [256 + 128 t, +128).
@@ -100,6 +101,7 @@ __device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *sr
                  : "memory");
 }
 
+template <bool kParts>  // the key tiles of a pair of row tiles in p.splits parts
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap rmap,
@@ -107,8 +109,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // Pairs of row tiles in reverse: later rows see more keys, so the longest CTAs start first.
-    const int h = blockIdx.x, b = blockIdx.y, pair = static_cast<int>(gridDim.z) - 1 - static_cast<int>(blockIdx.z);
+    // Pairs of row tiles in reverse: later rows see more keys, so the longest CTAs start first.  Split `sp` of a pair takes
+    // the sp-th part of its key tiles.
+    const int h = blockIdx.x, b = blockIdx.y, sp = kParts ? blockIdx.z / p.pairs : 0,
+              pair = p.pairs - 1 - static_cast<int>(kParts ? blockIdx.z % p.pairs : blockIdx.z);
 
     if (tid == 0) {
         prefetch_tensormap(&qmap);
@@ -122,15 +126,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     const int q0 = __ldg(p.cu_q_lens + b), q_len = __ldg(p.cu_q_lens + b + 1) - q0;
-    const int k0 = __ldg(p.cu_k_lens + b), k_len = __ldg(p.cu_k_lens + b + 1) - k0;
+    const int k_first = __ldg(p.cu_k_lens + b), k_all = __ldg(p.cu_k_lens + b + 1) - k_first;
     const int r_lo = 2 * pair * kRows;  // this CTA's first row of the chunk
-    if (q_len < 0 || q_len > k_len || q_len > p.max_q_len || q0 < 0 || k0 < 0 ||
-        static_cast<int64_t>(q0) + q_len > p.total_q || static_cast<int64_t>(k0) + k_len > p.total_k) {
-        if (pair == 0 && h == 0 && tid == 0) atomicOr(p.status, kStatusBadQLen);
+    auto part_at = [&](int64_t row) { return (static_cast<size_t>(sp) * p.total_q + row) * p.heads + h; };
+    auto part_of = [&](int64_t row) -> float2 & { return p.part_ml[part_at(row)]; };
+    if (q_len < 0 || q_len > k_all || q_len > p.max_q_len || q0 < 0 || k_first < 0 ||
+        static_cast<int64_t>(q0) + q_len > p.total_q || static_cast<int64_t>(k_first) + k_all > p.total_k) {
+        if (pair == 0 && h == 0 && sp == 0 && tid == 0) atomicOr(p.status, kStatusBadQLen);
         // The rows that can be addressed read as zeros; the last pair of the grid takes those past max_q_len too.
         if (q0 >= 0) {
             const int64_t end = min(static_cast<int64_t>(q_len), static_cast<int64_t>(p.total_q) - q0);
-            const int64_t hi = pair == static_cast<int>(gridDim.z) - 1 ? end : min(end, static_cast<int64_t>(r_lo) + 2 * kRows);
+            const int64_t hi = pair == p.pairs - 1 ? end : min(end, static_cast<int64_t>(r_lo) + 2 * kRows);
+            if (kParts) {  // (the merge writes the zeros)
+                for (int64_t i = r_lo + tid; i < hi; i += kThreads) part_of(q0 + i) = make_float2(-INFINITY, 0.f);
+                return;
+            }
             const int chunks = p.out_bf16 ? 16 : 32;  // 16-byte pieces of a row
             for (int64_t idx = tid; idx < (hi - r_lo) * chunks; idx += kThreads) {
                 const size_t row = static_cast<size_t>(q0) + r_lo + idx / chunks;
@@ -141,15 +151,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return;
     }
-    const int c = k_len - q_len;
-    // Row tile t: rows i0 .. i0 + rows - 1 of the chunk, keys 0 .. c + i0 + rows - 1, nt key tiles.
+    // Row tile t: rows i0 .. i0 + rows - 1 of the chunk, keys 0 .. k_all - q_len + i0 + rows - 1, in key tiles.
     auto tile_rows = [&](int t) { return max(0, min(kRows, q_len - r_lo - t * kRows)); };
-    auto tile_nt = [&](int t) {
+    auto tiles_of = [&](int t) {
         const int rows = tile_rows(t);
-        return rows > 0 ? (c + r_lo + t * kRows + rows + kKeys - 1) / kKeys : 0;
+        return rows > 0 ? (k_all - q_len + r_lo + t * kRows + rows + kKeys - 1) / kKeys : 0;
     };
+    // This part's key tiles; the keys from its first one on are as if they were the sequence's.
+    const int per = kParts ? (max(tiles_of(0), tiles_of(1)) + p.splits - 1) / p.splits : 0, skipped = sp * per * kKeys;
+    auto tile_nt = [&](int t) { return kParts ? max(0, min(tiles_of(t) - sp * per, per)) : tiles_of(t); };
+    const int k0 = k_first + skipped, k_len = k_all - skipped, c = k_len - q_len;
     const int n_tiles = max(tile_nt(0), tile_nt(1));
-    if (n_tiles == 0) return;
+    if (n_tiles == 0) {
+        if (kParts)
+            for (int i = tid; i < min(2 * kRows, q_len - r_lo); i += kThreads) part_of(q0 + r_lo + i) = make_float2(-INFINITY, 0.f);
+        return;
+    }
 
     auto bar = [&](int i) { return sbase + kOffBar + 8 * i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffTmem);
@@ -474,12 +491,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w0 = m == -INFINITY ? 0.f : fast_exp2(m - all);
                     w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - all);
                     l = w0 * l + w1 * ml.y;
+                    m = all;
                 }
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = kParts ? 1.f : l > 0.f ? 1.f / l : 0.f;
                 // bf16: a warp's 32 rows through its part of Q's place, then out in runs of 256 bytes (by TMA, at 24 bytes a clock,
                 // two full row tiles took 2 us longer).
                 const uint32_t stage = sbase + kOffQ + 3 * t * kChunk;
-                const size_t at = ((static_cast<size_t>(q0) + i0 + r) * p.heads + h) * kExpandedV;
+                const bool bf16 = p.out_bf16 && !kParts;
+                float *out = kParts ? p.part_o + part_at(q0 + i0 + r) * kExpandedV
+                                    : static_cast<float *>(p.out) + ((static_cast<size_t>(q0) + i0 + r) * p.heads + h) * kExpandedV;
+                if (kParts && r < rows) part_of(q0 + i0 + r) = make_float2(m, l);
 #pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
                     uint32_t v[32];
@@ -495,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     auto f = [&](int e) { return __uint_as_float(v[e]) * inv; };
-                    if (p.out_bf16) {
+                    if (bf16) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const uint4 w = make_uint4(pack_bf16x2(f(8 * e), f(8 * e + 1)), pack_bf16x2(f(8 * e + 2), f(8 * e + 3)),
@@ -505,21 +526,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else if (r < rows) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[8 * k + e] =
-                                make_float4(f(4 * e), f(4 * e + 1), f(4 * e + 2), f(4 * e + 3));
+                            reinterpret_cast<float4 *>(out)[8 * k + e] = make_float4(f(4 * e), f(4 * e + 1), f(4 * e + 2), f(4 * e + 3));
                     }
                 }
-                if (p.out_bf16) {
+                if (bf16) {
                     __syncwarp();
                     const int c = lane & 15;
-                    uint4 *out = static_cast<uint4 *>(p.out) + ((static_cast<size_t>(q0) + i0) * p.heads + h) * (kExpandedV / 8) + c;
+                    uint4 *dst = static_cast<uint4 *>(p.out) + ((static_cast<size_t>(q0) + i0) * p.heads + h) * (kExpandedV / 8) + c;
 #pragma unroll 4
                     for (int k = 0; k < 16; ++k) {
                         const int row = quarter * 32 + 2 * k + (lane >> 4);
                         const uint4 w = lds128(stage + (c >> 3) * kChunk + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-                        if (row < rows) out[static_cast<size_t>(row) * p.heads * (kExpandedV / 8)] = w;
+                        if (row < rows) dst[static_cast<size_t>(row) * p.heads * (kExpandedV / 8)] = w;
                     }
                 }
+            } else if (kParts && nt == 0 && r < rows) {
+                part_of(q0 + i0 + r) = make_float2(-INFINITY, 0.f);
             }
         }
     };
@@ -543,17 +565,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
+// Joins the splits of a (row, head): out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s, a warp each, four values a lane.
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(kMergeWarps * 32) latent_prefill_merge_kernel(const LatentPrefillParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5), all = static_cast<int64_t>(p.total_q) * p.heads;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (at >= min(all, static_cast<int64_t>(__ldg(p.cu_q_lens + p.num_seqs)) * p.heads)) return;
+    const float2 ml = lane < p.splits ? p.part_ml[lane * all + at] : make_float2(-INFINITY, 0.f);
+    const float4 *src = reinterpret_cast<const float4 *>(p.part_o) + at * (kExpandedV / 4) + lane;
+    float m = ml.x;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    // (A part without a weight may hold anything; l is NaN where a query or a key was.)
+    const float w = ml.x == -INFINITY && ml.y == 0.f ? 0.f : exp2f(ml.x - (m == -INFINITY ? 0.f : m));
+    float sum = ml.x == -INFINITY && ml.y == 0.f ? 0.f : w * ml.y;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint32_t used = __ballot_sync(0xffffffffu, !(ml.x == -INFINITY && ml.y == 0.f));
+#pragma unroll 4
+    for (int k = 0; k < p.splits; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        if (!((used >> k) & 1u)) continue;
+        const float4 v = src[k * all * (kExpandedV / 4)];
+        o.x += wk * v.x, o.y += wk * v.y, o.z += wk * v.z, o.w += wk * v.w;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // NaN stays
+    if (p.out_bf16)
+        reinterpret_cast<uint2 *>(p.out)[at * (kExpandedV / 4) + lane] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    else
+        reinterpret_cast<float4 *>(p.out)[at * (kExpandedV / 4) + lane] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
 }  // namespace
 
 cudaError_t latent_prefill_prepare_device() {
-    return cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(kSmemBytes));
+    const int bytes = static_cast<int>(kSmemBytes);
+    const cudaError_t e = cudaFuncSetAttribute(latent_prefill_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(latent_prefill_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 cudaError_t launch_latent_prefill(const LatentPrefillMaps &maps, const LatentPrefillParams &p, cudaStream_t stream) {
-    const int longest = p.max_q_len < p.total_q ? p.max_q_len : p.total_q;
-    const dim3 grid(p.heads, p.num_seqs, (longest + 2 * kRows - 1) / (2 * kRows));
-    return launch_pdl(latent_prefill_kernel, grid, dim3(kThreads), kSmemBytes, stream, maps.q, maps.k, maps.rope, p);
+    const cudaError_t e = launch_pdl(p.splits > 1 ? latent_prefill_kernel<true> : latent_prefill_kernel<false>, dim3(p.heads, p.num_seqs, p.pairs * p.splits), dim3(kThreads), kSmemBytes,
+                                     stream, maps.q, maps.k, maps.rope, p);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    const int64_t blocks = (static_cast<int64_t>(p.total_q) * p.heads + kMergeWarps - 1) / kMergeWarps;
+    return launch_pdl(latent_prefill_merge_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kMergeWarps * 32), 0, stream, p);
 }
 
 }  // namespace pkv

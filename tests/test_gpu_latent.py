@@ -456,6 +456,77 @@ def test_prefill_one_row_tile(k_lens, dtype):
     check_prefill(*prefill_inputs(sum(k_lens), q_lens, k_lens, 3), q_lens, k_lens, dtype=dtype)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("q_lens,k_lens", [
+    ([100], [2500]), ([1], [9000]), ([300, 20], [2900, 1500]), ([128, 0, 129], [3000, 700, 4100]), ([700], [4000]),
+    ([5, 260], [5, 6000]),
+])
+def test_prefill_keys_over_several_ctas(q_lens, k_lens, dtype):
+    """Few rows over many keys: parts of the keys, joined; rows and tiles that see nothing of a part."""
+    for heads in (1, 5):
+        args = prefill_inputs(sum(k_lens) + heads, q_lens, k_lens, heads)
+        assert P.latent_attention_prefill_workspace_size(len(q_lens), heads, max(q_lens), args[0].shape[0], args[1].shape[0]) > 256
+        check_prefill(*args, q_lens, k_lens, dtype=dtype)
+
+
+def test_prefill_parts_in_a_graph_share_a_workspace():
+    """Two calls whose parts lie in one workspace, one behind the other, replayed: the same bits."""
+    calls = []
+    for i, (ql, kl, heads) in enumerate([(100, 3000, 4), (260, 1800, 2)]):
+        q, kv, rows = prefill_inputs(90 + i, [ql], [kl], heads, spare=0)
+        calls.append((dict(out=torch.full((ql, heads, 128), R.NAN, dtype=torch.bfloat16, device="cuda"), q=q.cuda(), kv=kv.cuda(),
+                           rows=rows.cuda(), cq=i32([0, ql]), ck=i32([0, kl]), n=ql),
+                      R.expanded(q, kv[..., :128], kv[..., 128:], rows[:, 512:], [ql], [kl])))
+    ws = torch.zeros(max(P.latent_attention_prefill_workspace_size(1, d["out"].shape[1], d["n"], d["n"], d["kv"].shape[0])
+                         for d, _ in calls), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+
+    def run(d):
+        P.latent_attention_prefill_chunk(d["out"], d["q"], d["kv"][..., :128], d["kv"][..., 128:], d["rows"][:, 512:], d["cq"],
+                                         d["ck"], d["n"], R.SCALE, workspace=ws)
+
+    for d, ref in calls:
+        run(d)
+        R.assert_within(d["out"], *ref, "parts")
+    want = [d["out"].clone() for d, _ in calls]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for d, _ in calls:
+            run(d)
+    for d, _ in calls:
+        d["out"].fill_(R.NAN)
+    ws[256:] = 0xFF  # parts of an earlier call are not read
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    for (d, _), w in zip(calls, want):
+        assert torch.equal(bits(d["out"]), bits(w))
+    assert status_of(ws) == 0
+
+
+def test_prefill_split_bad_lengths_and_values():
+    """With the keys in parts: a sequence with more queries than keys, one whose keys lie outside, a query and a key
+    that are not finite, and a workspace that has room for the status word alone."""
+    q_lens, k_lens = [20, 30, 150], [4000, 10, 4000]
+    q, kv, rows = prefill_inputs(80, q_lens, k_lens, 2, spare=0)
+    ref, tol = R.expanded(q, kv[..., :128], kv[..., 128:], rows[:, 512:], q_lens, k_lens)  # (of rows that see neither NaN)
+    q[3, 1, 7], kv[3995, 0, 3] = R.NAN, R.NAN
+    broken = torch.zeros(200, 2, dtype=torch.bool)
+    broken[3, 1] = broken[15:20, 0] = True  # (key 3995 is row 15's own)
+    for ws in (None, torch.zeros(256, dtype=torch.uint8, device="cuda")):
+        out = torch.full((200, 2, 128), 5.0, device="cuda")
+        ws = P.latent_attention_prefill_chunk(out, q.cuda(), kv.cuda()[..., :128], kv.cuda()[..., 128:], rows.cuda()[:, 512:],
+                                              i32(starts(q_lens)), i32(starts(k_lens)), 150, R.SCALE, workspace=ws)
+        assert status_of(ws) == P.PKV_STATUS_BAD_Q_LEN
+        o = out.cpu()
+        assert o[broken].isnan().all() and (o[20:50] == 0).all()
+        R.assert_within(o[~broken], ref[~broken], tol[~broken], "the others")
+    out, ws = run_prefill(q, kv, rows, [20, 0, 180], [4000, 10, 4010])  # key rows past the tensor
+    assert (out[20:] == 0).all() and status_of(ws) == P.PKV_STATUS_BAD_Q_LEN
+    out, ws = run_prefill(q, kv, rows, [20, 30, 150], k_lens, max_q=100)  # a chunk longer than its bound
+    assert (out[20:] == 0).all() and status_of(ws) == P.PKV_STATUS_BAD_Q_LEN
+
+
 def test_prefill_strides():
     """Heads outermost, and packed keys and values of their own."""
     g = R.gen(4)

@@ -174,3 +174,14 @@ def test_prefill_refuses_what_overflows(lib, kw, want):
 def test_gather_refuses_what_overflows(lib):
     for mb, n in (((1 << 27) - 1, 10), (8, 2 ** 31 - 1)):
         assert lib.latent_gather(FAKE, FAKE, None, None, FAKE, FAKE, 2, mb, n, ctypes.byref(desc()), None, None) == INV
+
+
+def test_prefill_workspace_size(lib):
+    """Parts of the keys need room only where few rows meet many keys; the status word alone is accepted."""
+    size = lib.latent_attention_prefill_workspace_size
+    assert size(1, 32, 8192, 8192, 8192) == 256 and size(4, 32, 400, 1200, 2000) == 256 and size(1, 8, 100, 100, 500) == 256
+    need = size(1, 8, 100, 100, 4000)
+    assert need > 256 and (need - 256) % 256 == 0
+    assert size(1, 8, 0, 0, 0) == 256
+    for bad in ((0, 8, 1, 1, 1), (65536, 8, 1, 1, 1), (1, 0, 1, 1, 1), (1, 1025, 1, 1, 1), (1, 8, -1, 1, 1), (1, 8, 1, -1, 1)):
+        assert size(*bad) == 0
