@@ -818,6 +818,13 @@ def latent_gather(out, cache, block_tables, cu_lens, rope_cache=None, cache_scal
     _raise("latent_gather", rc)
 
 
+def _latent_workspace(nbytes, device):
+    """Device scratch whose status word starts clear (the rest is written before it is read)."""
+    workspace = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+    workspace[:256].zero_()
+    return workspace
+
+
 def latent_attention_workspace_size(num_seqs: int, q_per_seq: int, num_q_heads: int, max_blocks_per_seq: int,
                                     desc: LatentDesc) -> int:
     return int(load_library().latent_attention_workspace_size(num_seqs, q_per_seq, num_q_heads, max_blocks_per_seq,
@@ -849,7 +856,7 @@ def latent_attention_decode(out, q_latent, q_rope, cache, block_tables, context_
     if workspace is None:
         nbytes = int(lib.latent_attention_workspace_size(B, k, int(heads), max_blocks, ctypes.byref(desc)))
         _need(nbytes > 0, "invalid sizes for latent_attention_decode")
-        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=out.device)  # status word starts clear
+        workspace = _latent_workspace(nbytes, out.device)
     _check_on(workspace, "workspace", torch.uint8, 1, device)
     ql = (_addr(q_latent), _outer_stride(q_latent, 0), _outer_stride(q_latent, 1))
     qr = (_addr(q_rope), _outer_stride(q_rope, 0), _outer_stride(q_rope, 1))
@@ -899,7 +906,7 @@ def latent_attention_prefill_chunk(out, q, k_nope, v, k_rope, cu_q_lens, cu_k_le
     if workspace is None:
         nbytes = int(lib.latent_attention_prefill_workspace_size(B, int(heads), int(max_q_len), int(tq), tk))
         _need(nbytes > 0, "invalid sizes for latent_attention_prefill_chunk")
-        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=out.device)  # status word starts clear
+        workspace = _latent_workspace(nbytes, out.device)
     _check_on(workspace, "workspace", torch.uint8, 1, device)
     rc = lib.latent_attention_prefill_chunk(_addr(out), _out_dtype(out), _addr(q), _outer_stride(q, 0),
                                             _outer_stride(q, 1), _addr(k_nope), _addr(v), *k_strides, _addr(k_rope),

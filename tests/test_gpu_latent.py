@@ -125,6 +125,13 @@ def test_gather(lens, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("count", [32, 33, 1025, 2100])
+def test_gather_many_sequences(count, fp8):
+    """More than 32 and 1024 lengths to search, empty sequences among them, first and last."""
+    test_gather([(i * 7) % 4 for i in range(count - 1)] + [0], fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_gather_bad_blocks_and_lengths(fp8):
     pool = R.Pool(3, [40, 20], fp8, table_pad=0)
     pool.tables[0, 1] = pool.num_blocks
