@@ -978,8 +978,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // trips to L2: the records, then everything else.
 constexpr int kMergeWarps = 8;
 constexpr int kRecords = kLatentMaxRanges / 32;
-template <int STEPS>  // of 32 lanes x 4 dims; batches of 8 / STEPS parts (every warp of a call resident at once)
-__global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const LatentDecodeParams p) {
+template <int STEPS, int BATCH>  // steps of 32 lanes x 4 dims, batches of parts read at once
+__global__ void __launch_bounds__(kMergeWarps * 32, BATCH > 2 ? 2 : 3) latent_merge_kernel(const LatentDecodeParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * kMergeWarps + warp;
     griddep_launch_dependents();
@@ -1009,7 +1009,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) latent_merge_kernel(const La
     const size_t part0 = (static_cast<size_t>(first) * 2 + 1) * padded + col;
     const size_t part1 = static_cast<size_t>(first + 1) * 2 * padded + col;
     auto slot = [&](int k) { return k == 0 ? part0 : part1 + static_cast<size_t>(k - 1) * 2 * padded; };
-    constexpr int kBatch = 8 / STEPS;
+    constexpr int kBatch = BATCH;
     float4 v[kBatch][STEPS], o[STEPS];
     const int lane4 = blockIdx.z * STEPS * 32 + lane;
     auto load = [&](int j) {
@@ -1110,11 +1110,14 @@ cudaError_t launch_cols(const LatentDecodeMaps &maps, const LatentDecodeParams &
 cudaError_t launch_latent_decode(const LatentDecodeMaps &maps, const LatentDecodeParams &p, bool fp8, cudaStream_t stream) {
     const cudaError_t e = fp8 ? launch_cols<true>(maps, p, stream) : launch_cols<false>(maps, p, stream);
     if (e != cudaSuccess || p.ranges <= 1) return e;
-    // Few sequences over many ranges have many parts each: then four warps share a column's dims.
+    // Few sequences over many ranges have many parts each: then four warps share a column's dims, and read 12 parts at once
+    // (8 sequences of 32K tokens 65.5 -> 63.9 us against 8, 4 of 16K 33.5 -> 28.9), or all of up to 16 (one sequence of 1000
+    // tokens: 12 and 4 10.9, 16 10.3 us).
     const int split = std::min(p.num_seqs, p.ranges - 1), x = (p.heads * p.q_per_seq + kMergeWarps - 1) / kMergeWarps;
     if (p.ranges > 4 * split)
-        return launch_pdl(latent_merge_kernel<1>, dim3(x, split, 4), dim3(kMergeWarps * 32), 0, stream, p);
-    return launch_pdl(latent_merge_kernel<4>, dim3(x, split, 1), dim3(kMergeWarps * 32), 0, stream, p);
+        return launch_pdl(p.ranges <= 16 ? latent_merge_kernel<1, 16> : latent_merge_kernel<1, 12>, dim3(x, split, 4),
+                          dim3(kMergeWarps * 32), 0, stream, p);
+    return launch_pdl(latent_merge_kernel<4, 2>, dim3(x, split, 1), dim3(kMergeWarps * 32), 0, stream, p);
 }
 
 }  // namespace pkv
