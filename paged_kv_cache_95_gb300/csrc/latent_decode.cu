@@ -1111,11 +1111,11 @@ cudaError_t launch_latent_decode(const LatentDecodeMaps &maps, const LatentDecod
     const cudaError_t e = fp8 ? launch_cols<true>(maps, p, stream) : launch_cols<false>(maps, p, stream);
     if (e != cudaSuccess || p.ranges <= 1) return e;
     // Few sequences over many ranges have many parts each: then four warps share a column's dims, and read 12 parts at once
-    // (8 sequences of 32K tokens 65.5 -> 63.9 us against 8, 4 of 16K 33.5 -> 28.9), or all of up to 16 (one sequence of 1000
-    // tokens: 12 and 4 10.9, 16 10.3 us).
+    // (8 sequences of 32K tokens 65.5 -> 63.9 us against 8, 4 of 16K 33.5 -> 28.9; 16: 65.1, 29.5), over few ranges 16 (one
+    // sequence of 1000 tokens, 16 parts: 10.3 us, 12 and 4 10.9).
     const int split = std::min(p.num_seqs, p.ranges - 1), x = (p.heads * p.q_per_seq + kMergeWarps - 1) / kMergeWarps;
     if (p.ranges > 4 * split)
-        return launch_pdl(p.ranges <= 16 ? latent_merge_kernel<1, 16> : latent_merge_kernel<1, 12>, dim3(x, split, 4),
+        return launch_pdl(p.ranges <= 32 ? latent_merge_kernel<1, 16> : latent_merge_kernel<1, 12>, dim3(x, split, 4),
                           dim3(kMergeWarps * 32), 0, stream, p);
     return launch_pdl(latent_merge_kernel<4, 2>, dim3(x, split, 1), dim3(kMergeWarps * 32), 0, stream, p);
 }
