@@ -36,7 +36,7 @@
 // columns that is HBM's rate (23 bytes a clock and SM: 6.6 TB/s; the ragged batch of 64
 // sequences and 32 heads 39.0 us, 25.5 of them bytes); with 64 the tensor pipe, 36 MMAs of
 // 28 cycles for S and 16 of 52 for P V, whose operands come from shared memory (8 x 32K
-// tokens of 64 heads 65.5 us, 128 heads over 32 sequences 72.6).  FP8: 64 keys in 1850 with
+// tokens of 64 heads 63.9 us, 128 heads over 32 sequences 72.6).  FP8: 64 keys in 1850 with
 // 32 columns, the ring's four stages held from S to P V (30 us, 14.5 of bytes), 2400 with 64
 // (three stages; 4 rows x 64 heads over 16 sequences 91.5 us, 39.9 of operations).  Around
 // the tiles: launch, plan and first copies 5 us, Q of another sequence and the epilogue of
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     upto += before;
     // Of few and short sequences not every SM takes a range: a part costs about as much in the epilogue and the merge as an
     // eighth of a tile per part of its sequence, so sqrt(8 tiles sequences) ranges are least (one sequence of 4000 tokens, 64
-    // heads: 125 ranges 29.3 us, 33 17.3; 8000: 35.1, 20.7; two of 8000: 27.5, 22.5); up to 24 tiles a sequence each has its own.
+    // heads: 129 ranges 29.2 us, 32 17.7; 8000: 35.2, 20.0; two of 8000: 27.4, 20.8); up to 24 tiles a sequence each has its own.
     const int64_t few = 24 * static_cast<int64_t>(p.num_seqs);
     const int64_t best = static_cast<int64_t>(sqrtf(8.f * static_cast<float>(total) * static_cast<float>(p.num_seqs)));
     const int64_t ranges = min(static_cast<int64_t>(p.ranges), total <= few ? total : max(few, best));
