@@ -983,6 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // trips to L2: the records, then everything else.
 constexpr int kMergeWarps = 8;
 constexpr int kRecords = kLatentMaxRanges / 32;
+constexpr int kMergeResident = 2 * 152;  // CTAs
 template <int STEPS, int BATCH>  // steps of 32 lanes x 4 dims, batches of parts read at once
 __global__ void __launch_bounds__(kMergeWarps * 32, BATCH > 2 ? 2 : 3) latent_merge_kernel(const LatentDecodeParams p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1115,14 +1116,17 @@ cudaError_t launch_cols(const LatentDecodeMaps &maps, const LatentDecodeParams &
 cudaError_t launch_latent_decode(const LatentDecodeMaps &maps, const LatentDecodeParams &p, bool fp8, cudaStream_t stream) {
     const cudaError_t e = fp8 ? launch_cols<true>(maps, p, stream) : launch_cols<false>(maps, p, stream);
     if (e != cudaSuccess || p.ranges <= 1) return e;
-    // Few sequences over many ranges have many parts each: then four warps share a column's dims, and read 12 parts at once
-    // (8 sequences of 32K tokens 65.5 -> 63.9 us against 8, 4 of 16K 33.5 -> 28.9; 16: 65.1, 29.5), over few ranges 16 (one
-    // sequence of 1000 tokens, 16 parts: 10.3 us, 12 and 4 10.9).
+    // Few sequences over many ranges have many parts each: then as many warps share a column's dims as leave all CTAs resident
+    // (two an SM; 32 sequences of 1000 tokens, 64 heads: four warps in 1024 CTAs 27.4 us, one 21.2), and read as many parts at
+    // once as registers hold (8 sequences of 32K tokens: 8 65.5 us, 12 63.9, 16 65.1); over few ranges 16 (one sequence of 1000
+    // tokens, 16 parts: 10.3 us, 12 and 4 10.9).
     const int split = std::min(p.num_seqs, p.ranges - 1), x = (p.heads * p.q_per_seq + kMergeWarps - 1) / kMergeWarps;
-    if (p.ranges > 4 * split)
-        return launch_pdl(p.ranges <= 32 ? latent_merge_kernel<1, 16> : latent_merge_kernel<1, 12>, dim3(x, split, 4),
-                          dim3(kMergeWarps * 32), 0, stream, p);
-    return launch_pdl(latent_merge_kernel<4, 2>, dim3(x, split, 1), dim3(kMergeWarps * 32), 0, stream, p);
+    auto merge = [&](auto kernel, int z) { return launch_pdl(kernel, dim3(x, split, z), dim3(kMergeWarps * 32), 0, stream, p); };
+    if (p.ranges > 4 * split) {
+        if (x * split * 4 <= kMergeResident) return p.ranges <= 32 ? merge(latent_merge_kernel<1, 16>, 4) : merge(latent_merge_kernel<1, 12>, 4);
+        return x * split * 2 <= kMergeResident ? merge(latent_merge_kernel<2, 6>, 2) : merge(latent_merge_kernel<4, 4>, 1);
+    }
+    return merge(latent_merge_kernel<4, 2>, 1);
 }
 
 }  // namespace pkv
