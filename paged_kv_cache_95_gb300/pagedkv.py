@@ -11,6 +11,7 @@ or ``python -m paged_kv_cache_95_gb300.build``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -201,9 +202,15 @@ def version() -> int:
 
 # ---- tensor marshalling ----------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> int:
@@ -686,42 +693,71 @@ def paged_attention_decode_static_scratch(out, q, k_cache, v_cache, block_tables
 
 
 # ---- latent attention ---------------------------------------------------------------
-
-def _addr(t) -> int:
-    return t.data_ptr()
-
+# (A decode of few tokens takes 10 us on the GPU: an argument is looked at once, and its error put into words only where
+# something is wrong with it.  The tensors keep their names to the end of a call: an address alone would let a temporary
+# be freed, and its memory handed out, before the launch.)
 
 def _check_rows(t, name, ndim, last, device):
-    """A bf16 input whose rows (innermost dimension) are contiguous; the outer strides are free."""
+    """Raises what is wrong with a bf16 input of contiguous rows."""
     torch = _torch()
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == ndim and t.shape[-1] == last
-            and t.get_device() == device and t.stride(-1) == 1):
-        _need(isinstance(t, torch.Tensor), f"{name} must be a torch.Tensor")
-        _need(t.dtype == torch.bfloat16, f"{name} must be torch.bfloat16, got {t.dtype}")
-        _need(t.dim() == ndim and t.shape[-1] == last, f"{name} must have {ndim} dims, the last {last}: {tuple(t.shape)}")
-        _need(t.get_device() == device, f"{name} must be on the current CUDA device")
-        _need(False, f"{name}'s innermost dimension must be contiguous")
+    _need(isinstance(t, torch.Tensor), f"{name} must be a torch.Tensor")
+    _need(t.dtype == torch.bfloat16, f"{name} must be torch.bfloat16, got {t.dtype}")
+    _need(t.dim() == ndim and t.shape[-1] == last, f"{name} must have {ndim} dims, the last {last}: {tuple(t.shape)}")
+    _need(t.get_device() == device, f"{name} must be on the current CUDA device")
+    _need(False, f"{name}'s innermost dimension must be contiguous")
 
 
-def _check_on(t, name, dtype, ndim, device):
-    """A contiguous tensor on the current device."""
-    if not (isinstance(t, _torch().Tensor) and t.dtype is dtype and t.dim() == ndim and t.get_device() == device
-            and t.is_contiguous()):
-        _check(t, name, dtype, ndim=ndim)
-        _need(False, f"{name} must be on the current CUDA device")
+def _rows(t, name, ndim, last, device):
+    """Shape, strides and address of a bf16 input whose rows (innermost dimension) are contiguous; the outer strides are
+    free, and packed where a dimension is never stepped (size 1)."""
+    try:
+        shape, strides = t.shape, t.stride()
+        if (t.dtype is _torch().bfloat16 and len(strides) == ndim and shape[-1] == last and strides[-1] == 1
+                and t.get_device() == device):
+            if 1 in shape:
+                strides = [n if size > 1 else last for size, n in zip(shape, strides)]
+            return shape, strides, t.data_ptr()
+    except AttributeError:
+        pass
+    return _check_rows(t, name, ndim, last, device)
 
 
-def _outer_stride(t, dim: int) -> int:
-    """The stride of an outer dimension; the packed one where its size is 1 (it is never stepped)."""
-    return t.stride(dim) if t.shape[dim] > 1 else (t.shape[-1] + 7) // 8 * 8
+def _flat(t, name, dtype, ndim, device):
+    """Shape and address of a contiguous tensor on the current device."""
+    try:
+        if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+            shape = t.shape
+            if len(shape) == ndim:
+                return shape, t.data_ptr()
+    except AttributeError:
+        pass
+    _check(t, name, dtype, ndim=ndim)
+    raise ValueError(f"{name} must be on the current CUDA device")
+
+
+def _latent_out(out, device):
+    torch = _torch()
+    dtype = getattr(out, "dtype", None)
+    if dtype is torch.bfloat16:
+        code = PKV_DTYPE_BF16
+    elif dtype is torch.float32:
+        code = PKV_DTYPE_FLOAT32
+    else:
+        raise ValueError(f"out must be float32 or bfloat16, got {dtype}")
+    return code, *_flat(out, "out", dtype, 3, device)
+
+
+_cuda_started = False
 
 
 def _device_and_stream(stream):
     """The current device, and `stream` (None: the current one) as the ABI takes it."""
+    global _cuda_started
     torch = _torch()
-    if not torch.cuda.is_initialized():
+    if not _cuda_started:
         _need(torch.cuda.is_available(), "the latent entry points need a CUDA device")
         torch.cuda.init()
+        _cuda_started = True
     device = torch._C._cuda_getDevice()
     return device, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
@@ -732,53 +768,54 @@ def latent_cache_desc(cache) -> LatentDesc:
     torch = _torch()
     dtype = cache.dtype
     fp8 = dtype is torch.uint8 or dtype is torch.float8_e4m3fn
-    if not (cache.dim() == 3 and cache.is_cuda and cache.is_contiguous() and (fp8 or dtype is torch.bfloat16)):
-        _check(cache, "cache", dtype if fp8 else torch.bfloat16, ndim=3)
+    _check(cache, "cache", dtype if fp8 else torch.bfloat16, ndim=3)
     blocks, slots, width = cache.shape
     want = LATENT_DIM if fp8 else LATENT_DIM + ROPE_DIM
-    if width != want:
-        _need(False, f"cache rows must have {want} values, got {width}")
+    _need(width == want, f"cache rows must have {want} values, got {width}")
     return LatentDesc(blocks, slots, LATENT_DIM, ROPE_DIM, PKV_DTYPE_FP8_E4M3 if fp8 else PKV_DTYPE_BF16)
 
 
+@functools.lru_cache(maxsize=64)
+def _latent_desc(blocks, slots, dtype):
+    return ctypes.byref(LatentDesc(blocks, slots, LATENT_DIM, ROPE_DIM, dtype))
+
+
 def _latent_pool(cache, rope_cache, cache_scale, device):
+    """(descriptor, FP8, addresses of cache, rope_cache and cache_scale)."""
     torch = _torch()
-    desc = latent_cache_desc(cache)
-    fp8 = desc.dtype == PKV_DTYPE_FP8_E4M3
-    if cache.get_device() != device:
-        _need(False, "cache must be on the current CUDA device")
+    dtype = getattr(cache, "dtype", None)
+    fp8 = dtype is torch.uint8 or dtype is torch.float8_e4m3fn
+    (blocks, slots, width), address = _flat(cache, "cache", dtype if fp8 else torch.bfloat16, 3, device)
+    if width != (LATENT_DIM if fp8 else LATENT_DIM + ROPE_DIM):
+        latent_cache_desc(cache)
     if fp8 != (rope_cache is not None) or fp8 != (cache_scale is not None):
-        _need(False, "rope_cache and cache_scale are required for an FP8 pool and not allowed otherwise")
-    if fp8:
-        _check_on(rope_cache, "rope_cache", torch.bfloat16, 3, device)
-        _check_on(cache_scale, "cache_scale", torch.float32, 2, device)
-        shape = cache.shape[:2]
-        if rope_cache.shape[:2] != shape or rope_cache.shape[2] != ROPE_DIM:
-            _need(False, "rope_cache must be [num_blocks, 16, 64]")
-        if cache_scale.shape != shape:
-            _need(False, "cache_scale must be [num_blocks, 16]")
-    return desc, fp8
+        raise ValueError("rope_cache and cache_scale are required for an FP8 pool and not allowed otherwise")
+    if not fp8:
+        return _latent_desc(blocks, slots, PKV_DTYPE_BF16), False, address, None, None
+    shape, rope = _flat(rope_cache, "rope_cache", torch.bfloat16, 3, device)
+    _need(shape == (blocks, slots, ROPE_DIM), "rope_cache must be [num_blocks, 16, 64]")
+    shape, scale = _flat(cache_scale, "cache_scale", torch.float32, 2, device)
+    _need(shape == (blocks, slots), "cache_scale must be [num_blocks, 16]")
+    return _latent_desc(blocks, slots, PKV_DTYPE_FP8_E4M3), True, address, rope, scale
 
 
-def _check_latent_rows(latent, rope, slot_mapping, device):
-    torch = _torch()
-    _check_rows(latent, "latent", 2, LATENT_DIM, device)
-    _check_rows(rope, "rope", 2, ROPE_DIM, device)
-    _check_on(slot_mapping, "slot_mapping", torch.int32, 1, device)
-    T = slot_mapping.shape[0]
-    _need(latent.shape[0] == T and rope.shape[0] == T, "one latent and one rope row per slot")
-    return int(T)
+def _latent_rows(latent, rope, slot_mapping, device):
+    """(latent, its stride, rope, its stride, slots, tokens) of a write."""
+    latent_shape, latent_strides, latent_at = _rows(latent, "latent", 2, LATENT_DIM, device)
+    rope_shape, rope_strides, rope_at = _rows(rope, "rope", 2, ROPE_DIM, device)
+    (tokens,), slots = _flat(slot_mapping, "slot_mapping", _torch().int32, 1, device)
+    if latent_shape[0] != tokens or rope_shape[0] != tokens:
+        raise ValueError("one latent and one rope row per slot")
+    return latent_at, latent_strides[0], rope_at, rope_strides[0], slots, tokens
 
 
 def latent_reshape_and_cache(latent, rope, cache, slot_mapping, stream=None) -> None:
     """Append rows [latent (512) | rope (64)] to the bf16 latent pool [num_blocks, 16, 576]
     through ``slot_mapping``; ``latent`` and ``rope`` may be slices of wider rows."""
     device, stream = _device_and_stream(stream)
-    desc, fp8 = _latent_pool(cache, None, None, device)
-    T = _check_latent_rows(latent, rope, slot_mapping, device)
-    rc = load_library().latent_reshape_and_cache(_addr(latent), _outer_stride(latent, 0), _addr(rope),
-                                                 _outer_stride(rope, 0), _addr(cache), _addr(slot_mapping), T,
-                                                 ctypes.byref(desc), stream)
+    desc, _, pool, _, _ = _latent_pool(cache, None, None, device)
+    rows = _latent_rows(latent, rope, slot_mapping, device)
+    rc = (_lib or load_library()).latent_reshape_and_cache(*rows[:4], pool, *rows[4:], desc, stream)
     _raise("latent_reshape_and_cache", rc)
 
 
@@ -786,12 +823,9 @@ def latent_reshape_and_cache_fp8(latent, rope, cache, rope_cache, cache_scale, s
     """The same into an FP8 pool: E4M3 codes of the latent with one fp32 scale a token
     (``cache_scale`` [num_blocks, 16]); the rotated key goes to ``rope_cache`` as it is."""
     device, stream = _device_and_stream(stream)
-    desc, fp8 = _latent_pool(cache, rope_cache, cache_scale, device)
-    T = _check_latent_rows(latent, rope, slot_mapping, device)
-    rc = load_library().latent_reshape_and_cache_fp8(_addr(latent), _outer_stride(latent, 0), _addr(rope),
-                                                     _outer_stride(rope, 0), _addr(cache), _addr(rope_cache),
-                                                     _addr(cache_scale), _addr(slot_mapping), T, ctypes.byref(desc),
-                                                     stream)
+    desc, _, pool, rope_pool, scales = _latent_pool(cache, rope_cache, cache_scale, device)
+    rows = _latent_rows(latent, rope, slot_mapping, device)
+    rc = (_lib or load_library()).latent_reshape_and_cache_fp8(*rows[:4], pool, rope_pool, scales, *rows[4:], desc, stream)
     _raise("latent_reshape_and_cache_fp8", rc)
 
 
@@ -802,27 +836,29 @@ def latent_gather(out, cache, block_tables, cu_lens, rope_cache=None, cache_scal
     an optional int32 CUDA tensor of one element into which status bits are ORed."""
     torch = _torch()
     device, stream = _device_and_stream(stream)
-    desc, fp8 = _latent_pool(cache, rope_cache, cache_scale, device)
-    _check_on(out, "out", torch.bfloat16, 2, device)
-    _need(out.shape[1] == LATENT_DIM + ROPE_DIM, "out must be [total_rows, 576]")
-    _check_on(block_tables, "block_tables", torch.int32, 2, device)
-    _check_on(cu_lens, "cu_lens", torch.int32, 1, device)
-    B = int(block_tables.shape[0])
-    _need(cu_lens.shape[0] == B + 1, "cu_lens must be [num_seqs + 1]")
-    if status is not None:
-        _check_on(status, "status", torch.int32, 1, device)
-    rc = load_library().latent_gather(_addr(out), _addr(cache), _addr(rope_cache) if fp8 else None,
-                                      _addr(cache_scale) if fp8 else None, _addr(block_tables), _addr(cu_lens), B,
-                                      int(block_tables.shape[1]), int(out.shape[0]), ctypes.byref(desc),
-                                      _addr(status) if status is not None else None, stream)
+    desc, _, pool, rope_pool, scales = _latent_pool(cache, rope_cache, cache_scale, device)
+    (rows, width), out_at = _flat(out, "out", torch.bfloat16, 2, device)
+    _need(width == LATENT_DIM + ROPE_DIM, "out must be [total_rows, 576]")
+    (B, max_blocks), tables = _flat(block_tables, "block_tables", torch.int32, 2, device)
+    (n,), lens_at = _flat(cu_lens, "cu_lens", torch.int32, 1, device)
+    _need(n == B + 1, "cu_lens must be [num_seqs + 1]")
+    status_at = None if status is None else _flat(status, "status", torch.int32, 1, device)[1]
+    rc = (_lib or load_library()).latent_gather(out_at, pool, rope_pool, scales, tables, lens_at, B, max_blocks, rows, desc,
+                                                status_at, stream)
     _raise("latent_gather", rc)
 
 
-def _latent_workspace(nbytes, device):
-    """Device scratch whose status word starts clear (the rest is written before it is read)."""
-    workspace = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
-    workspace[:256].zero_()
-    return workspace
+def _latent_workspace(workspace, nbytes, what, like, device):
+    """Address and size of the caller's workspace, or of a new one whose status word starts clear (the rest is written
+    before it is read); and the tensor."""
+    torch = _torch()
+    if workspace is None:
+        nbytes = nbytes()
+        _need(nbytes > 0, f"invalid sizes for {what}")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        workspace[:256].zero_()
+    (size,), address = _flat(workspace, "workspace", torch.uint8, 1, device)
+    return address, size, workspace
 
 
 def latent_attention_workspace_size(num_seqs: int, q_per_seq: int, num_q_heads: int, max_blocks_per_seq: int,
@@ -840,34 +876,28 @@ def latent_attention_decode(out, q_latent, q_rope, cache, block_tables, context_
     (latent_attention_decode_fp8).  Returns the workspace (allocated if None)."""
     torch = _torch()
     device, stream = _device_and_stream(stream)
-    desc, fp8 = _latent_pool(cache, rope_cache, cache_scale, device)
-    _check_rows(q_latent, "q_latent", 3, LATENT_DIM, device)
-    _check_rows(q_rope, "q_rope", 3, ROPE_DIM, device)
-    rows, heads, _ = q_latent.shape
-    _need(tuple(q_rope.shape[:2]) == (rows, heads), "q_rope must have q_latent's rows and heads")
-    _check_on(out, "out", out.dtype, 3, device)
-    _need(tuple(out.shape) == (rows, heads, LATENT_DIM), "out must have q_latent's shape")
-    _check_on(block_tables, "block_tables", torch.int32, 2, device)
-    _check_on(context_lens, "context_lens", torch.int32, 1, device)
-    B, k = int(context_lens.shape[0]), int(q_per_seq)
-    _need(block_tables.shape[0] == B and rows == B * k, "q_latent must hold q_per_seq rows per sequence")
-    max_blocks = int(block_tables.shape[1])
-    lib = load_library()
-    if workspace is None:
-        nbytes = int(lib.latent_attention_workspace_size(B, k, int(heads), max_blocks, ctypes.byref(desc)))
-        _need(nbytes > 0, "invalid sizes for latent_attention_decode")
-        workspace = _latent_workspace(nbytes, out.device)
-    _check_on(workspace, "workspace", torch.uint8, 1, device)
-    ql = (_addr(q_latent), _outer_stride(q_latent, 0), _outer_stride(q_latent, 1))
-    qr = (_addr(q_rope), _outer_stride(q_rope, 0), _outer_stride(q_rope, 1))
-    tail = (_addr(block_tables), _addr(context_lens), B, k, int(heads), max_blocks, float(scale), ctypes.byref(desc),
-            _addr(workspace), int(workspace.numel()), stream)
+    desc, fp8, pool, rope_pool, scales = _latent_pool(cache, rope_cache, cache_scale, device)
+    (rows, heads, _), ql_strides, ql = _rows(q_latent, "q_latent", 3, LATENT_DIM, device)
+    shape, qr_strides, qr = _rows(q_rope, "q_rope", 3, ROPE_DIM, device)
+    _need(shape == (rows, heads, ROPE_DIM), "q_rope must have q_latent's rows and heads")
+    code, shape, out_at = _latent_out(out, device)
+    _need(shape == (rows, heads, LATENT_DIM), "out must have q_latent's shape")
+    (B, max_blocks), tables = _flat(block_tables, "block_tables", torch.int32, 2, device)
+    (n,), lens = _flat(context_lens, "context_lens", torch.int32, 1, device)
+    k = int(q_per_seq)
+    _need(n == B and rows == B * k, "q_latent must hold q_per_seq rows per sequence")
+    lib = _lib or load_library()
+    space, size, workspace = _latent_workspace(
+        workspace, lambda: lib.latent_attention_workspace_size(B, k, heads, max_blocks, desc), "latent_attention_decode", out,
+        device)
     if fp8:
-        rc = lib.latent_attention_decode_fp8(_addr(out), _out_dtype(out), *ql, *qr, _addr(cache), _addr(rope_cache),
-                                             _addr(cache_scale), *tail)
+        rc = lib.latent_attention_decode_fp8(out_at, code, ql, ql_strides[0], ql_strides[1], qr, qr_strides[0], qr_strides[1],
+                                             pool, rope_pool, scales, tables, lens, B, k, heads, max_blocks, scale, desc, space,
+                                             size, stream)
         _raise("latent_attention_decode_fp8", rc)
     else:
-        rc = lib.latent_attention_decode(_addr(out), _out_dtype(out), *ql, *qr, _addr(cache), *tail)
+        rc = lib.latent_attention_decode(out_at, code, ql, ql_strides[0], ql_strides[1], qr, qr_strides[0], qr_strides[1],
+                                         pool, tables, lens, B, k, heads, max_blocks, scale, desc, space, size, stream)
         _raise("latent_attention_decode", rc)
     return workspace
 
@@ -886,32 +916,26 @@ def latent_attention_prefill_chunk(out, q, k_nope, v, k_rope, cu_q_lens, cu_k_le
     in float32 or bfloat16.  Returns the workspace (allocated if None)."""
     torch = _torch()
     device, stream = _device_and_stream(stream)
-    _check_rows(q, "q", 3, 192, device)
-    _check_rows(k_nope, "k_nope", 3, 128, device)
-    _check_rows(v, "v", 3, 128, device)
-    _check_rows(k_rope, "k_rope", 2, ROPE_DIM, device)
-    tq, heads, _ = q.shape
-    tk = int(k_nope.shape[0])
-    _need(k_nope.shape[1] == heads and tuple(v.shape) == tuple(k_nope.shape) and k_rope.shape[0] == tk,
+    (tq, heads, _), q_strides, q_at = _rows(q, "q", 3, 192, device)
+    k_shape, k_strides, k_at = _rows(k_nope, "k_nope", 3, 128, device)
+    v_shape, v_strides, v_at = _rows(v, "v", 3, 128, device)
+    rope_shape, rope_strides, rope_at = _rows(k_rope, "k_rope", 2, ROPE_DIM, device)
+    tk = k_shape[0]
+    _need(k_shape[1] == heads and v_shape == k_shape and rope_shape[0] == tk,
           "k_nope and v must be [total_k, heads, 128], k_rope [total_k, 64]")
-    k_strides = (_outer_stride(k_nope, 0), _outer_stride(k_nope, 1))
-    _need(k_strides == (_outer_stride(v, 0), _outer_stride(v, 1)), "k_nope and v must have the same strides")
-    _check_on(out, "out", out.dtype, 3, device)
-    _need(tuple(out.shape) == (tq, heads, 128), "out must be [total_q, heads, 128]")
-    _check_on(cu_q_lens, "cu_q_lens", torch.int32, 1, device)
-    _check_on(cu_k_lens, "cu_k_lens", torch.int32, 1, device)
-    B = int(cu_q_lens.shape[0]) - 1
-    _need(cu_k_lens.shape[0] == B + 1, "cu_q_lens and cu_k_lens must be [num_seqs + 1]")
-    lib = load_library()
-    if workspace is None:
-        nbytes = int(lib.latent_attention_prefill_workspace_size(B, int(heads), int(max_q_len), int(tq), tk))
-        _need(nbytes > 0, "invalid sizes for latent_attention_prefill_chunk")
-        workspace = _latent_workspace(nbytes, out.device)
-    _check_on(workspace, "workspace", torch.uint8, 1, device)
-    rc = lib.latent_attention_prefill_chunk(_addr(out), _out_dtype(out), _addr(q), _outer_stride(q, 0),
-                                            _outer_stride(q, 1), _addr(k_nope), _addr(v), *k_strides, _addr(k_rope),
-                                            _outer_stride(k_rope, 0), _addr(cu_q_lens), _addr(cu_k_lens), B, int(heads),
-                                            int(max_q_len), int(tq), tk, float(scale), _addr(workspace),
-                                            int(workspace.numel()), stream)
+    _need(tuple(k_strides) == tuple(v_strides), "k_nope and v must have the same strides")
+    code, shape, out_at = _latent_out(out, device)
+    _need(shape == (tq, heads, 128), "out must be [total_q, heads, 128]")
+    (n,), cu_q = _flat(cu_q_lens, "cu_q_lens", torch.int32, 1, device)
+    (m,), cu_k = _flat(cu_k_lens, "cu_k_lens", torch.int32, 1, device)
+    _need(m == n, "cu_q_lens and cu_k_lens must be [num_seqs + 1]")
+    B, max_q_len = n - 1, int(max_q_len)
+    lib = _lib or load_library()
+    space, size, workspace = _latent_workspace(
+        workspace, lambda: lib.latent_attention_prefill_workspace_size(B, heads, max_q_len, tq, tk),
+        "latent_attention_prefill_chunk", out, device)
+    rc = lib.latent_attention_prefill_chunk(out_at, code, q_at, q_strides[0], q_strides[1], k_at, v_at, k_strides[0], k_strides[1],
+                                            rope_at, rope_strides[0], cu_q, cu_k, B, heads, max_q_len, tq, tk, scale, space, size,
+                                            stream)
     _raise("latent_attention_prefill_chunk", rc)
     return workspace
