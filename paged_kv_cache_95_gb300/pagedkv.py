@@ -714,8 +714,8 @@ def _rows(t, name, ndim, last, device):
         shape, strides = t.shape, t.stride()
         if (t.dtype is _torch().bfloat16 and len(strides) == ndim and shape[-1] == last and strides[-1] == 1
                 and t.get_device() == device):
-            if 1 in shape:
-                strides = [n if size > 1 else last for size, n in zip(shape, strides)]
+            if shape[0] == 1 or shape[-2] == 1:
+                strides = tuple(n if size > 1 else last for size, n in zip(shape, strides))
             return shape, strides, t.data_ptr()
     except AttributeError:
         pass
@@ -793,9 +793,11 @@ def _latent_pool(cache, rope_cache, cache_scale, device):
     if not fp8:
         return _latent_desc(blocks, slots, PKV_DTYPE_BF16), False, address, None, None
     shape, rope = _flat(rope_cache, "rope_cache", torch.bfloat16, 3, device)
-    _need(shape == (blocks, slots, ROPE_DIM), "rope_cache must be [num_blocks, 16, 64]")
+    if shape != (blocks, slots, ROPE_DIM):
+        raise ValueError("rope_cache must be [num_blocks, 16, 64]")
     shape, scale = _flat(cache_scale, "cache_scale", torch.float32, 2, device)
-    _need(shape == (blocks, slots), "cache_scale must be [num_blocks, 16]")
+    if shape != (blocks, slots):
+        raise ValueError("cache_scale must be [num_blocks, 16]")
     return _latent_desc(blocks, slots, PKV_DTYPE_FP8_E4M3), True, address, rope, scale
 
 
@@ -838,27 +840,24 @@ def latent_gather(out, cache, block_tables, cu_lens, rope_cache=None, cache_scal
     device, stream = _device_and_stream(stream)
     desc, _, pool, rope_pool, scales = _latent_pool(cache, rope_cache, cache_scale, device)
     (rows, width), out_at = _flat(out, "out", torch.bfloat16, 2, device)
-    _need(width == LATENT_DIM + ROPE_DIM, "out must be [total_rows, 576]")
+    if width != LATENT_DIM + ROPE_DIM:
+        raise ValueError("out must be [total_rows, 576]")
     (B, max_blocks), tables = _flat(block_tables, "block_tables", torch.int32, 2, device)
     (n,), lens_at = _flat(cu_lens, "cu_lens", torch.int32, 1, device)
-    _need(n == B + 1, "cu_lens must be [num_seqs + 1]")
+    if n != B + 1:
+        raise ValueError("cu_lens must be [num_seqs + 1]")
     status_at = None if status is None else _flat(status, "status", torch.int32, 1, device)[1]
     rc = (_lib or load_library()).latent_gather(out_at, pool, rope_pool, scales, tables, lens_at, B, max_blocks, rows, desc,
                                                 status_at, stream)
     _raise("latent_gather", rc)
 
 
-def _latent_workspace(workspace, nbytes, what, like, device):
-    """Address and size of the caller's workspace, or of a new one whose status word starts clear (the rest is written
-    before it is read); and the tensor."""
-    torch = _torch()
-    if workspace is None:
-        nbytes = nbytes()
-        _need(nbytes > 0, f"invalid sizes for {what}")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-        workspace[:256].zero_()
-    (size,), address = _flat(workspace, "workspace", torch.uint8, 1, device)
-    return address, size, workspace
+def _new_workspace(nbytes, what, like):
+    """Device scratch whose status word starts clear (the rest is written before it is read)."""
+    _need(nbytes > 0, f"invalid sizes for {what}")
+    workspace = _torch().empty(nbytes, dtype=_torch().uint8, device=like.device)
+    workspace[:256].zero_()
+    return workspace
 
 
 def latent_attention_workspace_size(num_seqs: int, q_per_seq: int, num_q_heads: int, max_blocks_per_seq: int,
@@ -879,17 +878,20 @@ def latent_attention_decode(out, q_latent, q_rope, cache, block_tables, context_
     desc, fp8, pool, rope_pool, scales = _latent_pool(cache, rope_cache, cache_scale, device)
     (rows, heads, _), ql_strides, ql = _rows(q_latent, "q_latent", 3, LATENT_DIM, device)
     shape, qr_strides, qr = _rows(q_rope, "q_rope", 3, ROPE_DIM, device)
-    _need(shape == (rows, heads, ROPE_DIM), "q_rope must have q_latent's rows and heads")
+    if shape != (rows, heads, ROPE_DIM):
+        raise ValueError("q_rope must have q_latent's rows and heads")
     code, shape, out_at = _latent_out(out, device)
-    _need(shape == (rows, heads, LATENT_DIM), "out must have q_latent's shape")
+    if shape != (rows, heads, LATENT_DIM):
+        raise ValueError("out must have q_latent's shape")
     (B, max_blocks), tables = _flat(block_tables, "block_tables", torch.int32, 2, device)
     (n,), lens = _flat(context_lens, "context_lens", torch.int32, 1, device)
     k = int(q_per_seq)
-    _need(n == B and rows == B * k, "q_latent must hold q_per_seq rows per sequence")
+    if n != B or rows != B * k:
+        raise ValueError("q_latent must hold q_per_seq rows per sequence")
     lib = _lib or load_library()
-    space, size, workspace = _latent_workspace(
-        workspace, lambda: lib.latent_attention_workspace_size(B, k, heads, max_blocks, desc), "latent_attention_decode", out,
-        device)
+    if workspace is None:
+        workspace = _new_workspace(lib.latent_attention_workspace_size(B, k, heads, max_blocks, desc), "latent_attention_decode", out)
+    (size,), space = _flat(workspace, "workspace", torch.uint8, 1, device)
     if fp8:
         rc = lib.latent_attention_decode_fp8(out_at, code, ql, ql_strides[0], ql_strides[1], qr, qr_strides[0], qr_strides[1],
                                              pool, rope_pool, scales, tables, lens, B, k, heads, max_blocks, scale, desc, space,
@@ -921,19 +923,23 @@ def latent_attention_prefill_chunk(out, q, k_nope, v, k_rope, cu_q_lens, cu_k_le
     v_shape, v_strides, v_at = _rows(v, "v", 3, 128, device)
     rope_shape, rope_strides, rope_at = _rows(k_rope, "k_rope", 2, ROPE_DIM, device)
     tk = k_shape[0]
-    _need(k_shape[1] == heads and v_shape == k_shape and rope_shape[0] == tk,
-          "k_nope and v must be [total_k, heads, 128], k_rope [total_k, 64]")
-    _need(tuple(k_strides) == tuple(v_strides), "k_nope and v must have the same strides")
+    if k_shape[1] != heads or v_shape != k_shape or rope_shape[0] != tk:
+        raise ValueError("k_nope and v must be [total_k, heads, 128], k_rope [total_k, 64]")
+    if k_strides != v_strides:
+        raise ValueError("k_nope and v must have the same strides")
     code, shape, out_at = _latent_out(out, device)
-    _need(shape == (tq, heads, 128), "out must be [total_q, heads, 128]")
+    if shape != (tq, heads, 128):
+        raise ValueError("out must be [total_q, heads, 128]")
     (n,), cu_q = _flat(cu_q_lens, "cu_q_lens", torch.int32, 1, device)
     (m,), cu_k = _flat(cu_k_lens, "cu_k_lens", torch.int32, 1, device)
-    _need(m == n, "cu_q_lens and cu_k_lens must be [num_seqs + 1]")
+    if m != n:
+        raise ValueError("cu_q_lens and cu_k_lens must be [num_seqs + 1]")
     B, max_q_len = n - 1, int(max_q_len)
     lib = _lib or load_library()
-    space, size, workspace = _latent_workspace(
-        workspace, lambda: lib.latent_attention_prefill_workspace_size(B, heads, max_q_len, tq, tk),
-        "latent_attention_prefill_chunk", out, device)
+    if workspace is None:
+        workspace = _new_workspace(lib.latent_attention_prefill_workspace_size(B, heads, max_q_len, tq, tk),
+                                   "latent_attention_prefill_chunk", out)
+    (size,), space = _flat(workspace, "workspace", torch.uint8, 1, device)
     rc = lib.latent_attention_prefill_chunk(out_at, code, q_at, q_strides[0], q_strides[1], k_at, v_at, k_strides[0], k_strides[1],
                                             rope_at, rope_strides[0], cu_q, cu_k, B, heads, max_q_len, tq, tk, scale, space, size,
                                             stream)
