@@ -69,8 +69,8 @@ cudaError_t launch_latent_decode(const LatentDecodeMaps &maps, const LatentDecod
 // ---- expanded attention of a prefill chunk --------------------------------------------
 struct LatentPrefillParams {
     void *out;  // [rows][heads][128], f32 or bf16
-    const void *q, *k_nope, *v, *k_rope;
-    int64_t q_row, q_head, k_row, k_head, r_row;  // strides in elements
+    const void *q, *v;                      // (keys and the first row tile's q come by their tensor maps)
+    int64_t q_row, q_head, k_row, k_head;  // strides in elements
     const int32_t *cu_q_lens, *cu_k_lens;
     uint32_t *status;
     int32_t num_seqs, heads, max_q_len, total_q, total_k;

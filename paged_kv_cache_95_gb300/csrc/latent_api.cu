@@ -407,14 +407,11 @@ int latent_attention_prefill_chunk(void *out, int32_t out_dtype, const void *q, 
         return PKV_ERR_INVALID_ARG;
     p.out = out;
     p.q = q;
-    p.k_nope = k_nope;
     p.v = v;
-    p.k_rope = k_rope;
     p.q_row = q_row_stride;
     p.q_head = q_head_stride;
     p.k_row = k_row_stride;
     p.k_head = k_head_stride;
-    p.r_row = k_rope_stride;
     p.cu_q_lens = cu_q_lens;
     p.cu_k_lens = cu_k_lens;
     p.status = static_cast<uint32_t *>(workspace);
