@@ -111,12 +111,12 @@ struct Layout {
     static constexpr bool kPHalf = kStack || (!FP8 && TILE == 32);
     static constexpr uint32_t kPBuf = kPHalf ? 64 : NCOL * 128;
     static constexpr uint32_t kScale = kP + (kPHalf ? 1 : 2) * kOCols * 128;  // FP8: [stage][scale, its log2, its inverse][64 keys]
-    static constexpr uint32_t kQf = kScale + (FP8 ? kStages * 3 * TILE * 4 : 0);  // FP8: [64] factors of the columns
+    static constexpr uint32_t kQf = kScale + (FP8 ? kStages * 3 * TILE * 4 : 0);  // FP8: [a piece's first tile & 1][64] factors of the columns
     // kv_full[stage], kv_empty[stage][block], s_full[2], s_empty[2], p_full[2], pv_done[2], q_full
     static constexpr int kBarKvFull = 0, kBarKvEmpty = kStages, kBarSFull = kBarKvEmpty + kStages * kTileBlocks,
                          kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 2, kBarPvDone = kBarPFull + 2,
                          kBarQFull = kBarPvDone + 2, kNumBars = kBarQFull + 1;
-    static constexpr uint32_t kBar = kQf + (FP8 ? 64 * 4 : 0);
+    static constexpr uint32_t kBar = kQf + (FP8 ? 2 * 64 * 4 : 0);
     static constexpr uint32_t kTmemSlot = kBar + 8 * kNumBars;
     static constexpr uint32_t kAbort = kTmemSlot + 4;
     static constexpr uint32_t kXch = (kAbort + 4 + 15) / 16 * 16;  // [tile & 1][key half][64] maxima, later sums
@@ -594,9 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Sequence b's Q, a row a warp, zeros behind the last one, in the operand's swizzle.  FP8: the
         // latent part times a power of two that takes its largest value into (224, 448], as E4M3
         // heads and remainders (a bf16 value has 8 bits, two codes hold 4 each: exact down to steps
-        // of 2^-9); the factor that undoes it in shared memory.
+        // of 2^-9); the factor that undoes it in shared memory, in two buffers by the parity of the tile that
+        // reads it, the piece's first: where a piece is one tile a warp writes the next piece's factors while another still
+        // has to read this one's.  (A write to the same buffer comes two tiles on at least, behind the barrier of a tile.)
         float *qf_s = reinterpret_cast<float *>(smem + L::kQf);
-        auto load_q = [&](int b) {
+        auto load_q = [&](int b, int first_tile) {
             const uint16_t *ql0 = static_cast<const uint16_t *>(p.q_latent) + static_cast<int64_t>(b) * p.q_per_seq * p.ql_row;
             const uint16_t *qp0 = static_cast<const uint16_t *>(p.q_rope) + static_cast<int64_t>(b) * p.q_per_seq * p.qr_row;
             auto q_of = [&](int r, const uint16_t *&ql, const uint16_t *&qp) {  // (r < nc)
@@ -667,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     sts128(head + kRest, make_uint4(lo[0], lo[1], lo[2], lo[3]));
                     if (lane < 8) sts128(at(4, lane), rotated);
                     // (E4M3 has no infinity: a row that holds one scores NaN.)
-                    if (lane == 0) qf_s[r] = __uint_as_float(most == INFINITY ? 0x7fffffffu : static_cast<uint32_t>(127 - lift) << 23);
+                    if (lane == 0) qf_s[64 * (first_tile & 1) + r] = __uint_as_float(most == INFINITY ? 0x7fffffffu : static_cast<uint32_t>(127 - lift) << 23);
                 }
             }
         };
@@ -678,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(bar(L::kBarQFull));
         };
 
-        load_q(b0);
+        load_q(b0, 0);
         empty_sequences(tid, kSoftThreads);
         publish_q();
         if constexpr (FP8) soft_sync();  // the factors of Q's rows are written
@@ -707,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < kR; ++k) {
                     m_ref[k] = -INFINITY;
                     l[k] = make_float2(0.f, 0.f);
-                    if constexpr (FP8) q_scale[k] = live ? qf_s[col0 + 8 * k] * p.scale_log2 : 0.f;
+                    if constexpr (FP8) q_scale[k] = live ? qf_s[64 * (i & 1) + col0 + 8 * k] * p.scale_log2 : 0.f;
                 }
             }
             float2 x[kR][kGroups];  // [k][j]: row k, keys kTile / 2 half + 8 j + 2 (lane % 4) + 0, 1
@@ -775,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (alive && lane == 0) mbar_arrive(bar(L::kBarSEmpty + (i & 1)));
             // The last S of a piece is complete: its Q can make way for the next sequence's.
             const bool more = last && i + 1 < n;
-            if (more && alive) load_q(info.w);
+            if (more && alive) load_q(info.w, i + 1);
 
             float *xm = xch + (i & 1) * 128;
             bool pass = false;
