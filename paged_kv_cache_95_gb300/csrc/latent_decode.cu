@@ -16,7 +16,7 @@
 // Per tile (bf16: 32 keys, four stages of 36 KB; up to 16 columns 64 keys, two stages;
 // FP8: 64 keys, 40 KB, four stages, with 64 columns three):
 //  * S [columns x keys] = Q K^T: M = 64 (FP8 with 64 columns 128), N = keys; Q stays in
-//    shared memory (128-byte swizzle).  Over an FP8 pool Q and P are pairs of E4M3 codes.
+//    shared memory (128-byte swizzle).  Over an FP8 pool Q is pairs of E4M3 codes, P three E5M2 codes a weight.
 //  * half of the blocks are copied by TMA, half by cp.async: one SM's TMA unit delivers 24
 //    bytes a clock however much is in flight (measured, from L2 as from HBM), both paths
 //    together 47; HBM's share of an SM is 23-28, so a ring on TMA alone never catches up.
@@ -36,9 +36,10 @@
 // columns that is HBM's rate (23 bytes a clock and SM: 6.6 TB/s; the ragged batch of 64
 // sequences and 32 heads 39.0 us, 25.5 of them bytes); with 64 the tensor pipe, 36 MMAs of
 // 28 cycles for S and 16 of 52 for P V, whose operands come from shared memory (8 x 32K
-// tokens of 64 heads 63.9 us, 128 heads over 32 sequences 72.6).  FP8: 64 keys in 1850 with
-// 32 columns, the ring's four stages held from S to P V (30 us, 14.5 of bytes), 2400 with 64
-// (three stages; 4 rows x 64 heads over 16 sequences 91.5 us, 39.9 of operations).  Around
+// tokens of 64 heads 63.9 us, 128 heads over 32 sequences 72.6).  FP8: 64 keys a tile,
+// with 32 columns the ring's four stages held from S to P V (32.2 us, 14.5 of bytes; 30.2 with P
+// as two codes), with 64 the tensor pipe and three stages (4 rows x 64 heads over 16 sequences
+// 100.9 us, 39.9 of operations; 90.8 with two codes).  Around
 // the tiles: launch, plan and first copies 5 us, Q of another sequence and the epilogue of
 // the one before 2-4 us (72 KB of Q come in at 47 bytes a clock, 128 KB of O go out), the
 // merge 4-6 us.
@@ -86,8 +87,9 @@ struct Layout {
     // FP8: the E4M3 heads and remainders of Q are rows of one product, those of P (up to 32 columns) columns of one: an
     // MMA of few columns is bound by its other operand, M = 128 takes 43 cycles with N = 32 and 52 with 64, and N = 64
     // takes 35 with M = 64 and 52 with 128.  A remainder's row is 8 behind its head's, in rows that M = 64 has anyway
-    // and in the same thread after the load; for 64 columns 16 behind, M = 128.  A remainder's column is NCOL behind
-    // (for 64 columns O has no room: two products).
+    // and in the same thread after the load; for 64 columns 16 behind, M = 128.  P is three E5M2 codes a weight, what
+    // each leaves in the next: the second's column is NCOL behind the first's (for 64 columns O has no room: a product of
+    // its own), the third's product adds to the first's columns.
     static constexpr bool kStack = FP8 && NCOL <= 32;
     static constexpr int kOCols = kStack ? 2 * NCOL : NCOL;  // columns of a dim tile's O
     static constexpr int kStages = FP8 ? (kStack ? 4 : 3) : 128 / TILE;
@@ -105,12 +107,13 @@ struct Layout {
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kQRope = kQ + (FP8 ? 4 : 8) * kQChunk;
     static constexpr uint32_t kKv = kQRope + 64 * 128;
-    // P, two buffers in turn: [NCOL][64 bf16], or [NCOL][64 heads | 64 remainders]; rows of 64 bytes (32 keys, or stacked
-    // [heads, remainders][NCOL][64 codes]) lie side by side.
+    // P, two buffers in turn: [NCOL][64 bf16], or [NCOL][64 first | 64 second codes]; rows of 64 bytes (32 keys, or stacked
+    // [first, second][NCOL][64 codes]) lie side by side.
     static constexpr uint32_t kP = kKv + kStages * kStage;
     static constexpr bool kPHalf = kStack || (!FP8 && TILE == 32);
     static constexpr uint32_t kPBuf = kPHalf ? 64 : NCOL * 128;
-    static constexpr uint32_t kScale = kP + (kPHalf ? 1 : 2) * kOCols * 128;  // FP8: [stage][scale, its log2, its inverse][64 keys]
+    static constexpr uint32_t kP3 = kP + (kPHalf ? 1 : 2) * kOCols * 128;  // FP8: third codes, [NCOL][two buffers of 64]
+    static constexpr uint32_t kScale = kP3 + (FP8 ? NCOL * 128 : 0);  // FP8: [stage][scale, its log2, its inverse][64 keys]
     static constexpr uint32_t kQf = kScale + (FP8 ? kStages * 3 * TILE * 4 : 0);  // FP8: [a piece's first tile & 1][64] factors of the columns
     // kv_full[stage], kv_empty[stage][block], s_full[2], s_empty[2], p_full[2], pv_done[2], q_full
     static constexpr int kBarKvFull = 0, kBarKvEmpty = kStages, kBarSFull = kBarKvEmpty + kStages * kTileBlocks,
@@ -131,15 +134,18 @@ struct Layout {
     static_assert(kBytes <= 232448, "shared memory of one CTA");
     static_assert(kKv % 1024 == 0 && kP % 1024 == 0 && kStage % 1024 == 0, "swizzle atoms");
     static_assert(kScale % 16 == 0 && kBar % 8 == 0 && kPlan % 8 == 0 && kInfo % 16 == 0, "alignment");
-    // A weight may pass the reference by 2^kRaise before the reference follows.  FP8 keeps the weights as pairs of
-    // E4M3 codes: 2^2 at the reference, so 2^8 at most (448 is the largest code) and steps of 2^-9 below.  (2^4 and
-    // 2^4: on the verify of 64 columns a reference was raised in every second tile, 1900 cycles each.)
-    static constexpr float kRaise = FP8 ? 6.f : 8.f, kLift = FP8 ? 2.f : 0.f;
+    // A weight may pass the reference by 2^kRaise before the reference follows.  FP8 keeps a weight as three E5M2 codes:
+    // 2^9 at the reference, so 2^15 at most (57344 is the largest code), and half of the smallest step is 2^-17, 2^-26 of
+    // the reference: a million keys that small come to 2^-6 of it.  (Pairs of E4M3 codes, 2^2 at the reference and steps of
+    // 2^-9, lost every key below 2^-12 of the largest: with one key of 0.3 of the weight and 14000 more up to 94% of
+    // the output.  A raise of 2^4: on the verify of 64 columns a reference was raised in every second tile, 1900 cycles each.)
+    static constexpr float kRaise = FP8 ? 6.f : 8.f, kLift = FP8 ? 9.f : 0.f;
 };
 
-// Instruction descriptor: D f32; A and B bf16 (kind::f16) or E4M3 (kind::f8f6f4).
-__host__ __device__ constexpr uint32_t idesc(int m, int n, bool a_mn, bool f8 = false) {
-    return (1u << 4) | (f8 ? 0u : (1u << 7) | (1u << 10)) | (a_mn ? 1u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+// Instruction descriptor: D f32; A and B bf16 (kind::f16), or A E4M3 and B E4M3 or E5M2 (kind::f8f6f4).
+enum class Kind : uint32_t { kBf16 = (1u << 7) | (1u << 10), kE4m3 = 0, kE4m3E5m2 = 1u << 10 };
+__host__ __device__ constexpr uint32_t idesc(int m, int n, bool a_mn, Kind kind = Kind::kBf16) {
+    return (1u << 4) | static_cast<uint32_t>(kind) | (a_mn ? 1u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int kk = 0; kk < 4; ++kk) {
                         const uint64_t qd = q_desc + ((c * L::kQChunk + kk * 32) >> 4), k = kd + ((c * 1024 + kk * 32) >> 4);
                         if constexpr (FP8)  // heads and remainders against the same codes
-                            umma_e4m3(d, qd, k, idesc(L::kQRows, kTile, false, true), c + kk > 0);
+                            umma_f8(d, qd, k, idesc(L::kQRows, kTile, false, Kind::kE4m3), c + kk > 0);
                         else
                             umma_bf16(d, qd, k, idesc(64, kTile, false), c + kk > 0);
                     }
@@ -547,15 +553,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       idesc(128, NCOL, true), ks > 0 ? 1u : keep);
                         umma_commit(bar(L::kBarKvEmpty + st * kTileBlocks + ks));
                     }
-                } else {  // 32 keys a step; heads and remainders against the same codes
+                } else {  // 32 keys a step; a weight's three codes against the same key
+                    const uint64_t p3 = p_desc + ((L::kP3 - L::kP + static_cast<uint32_t>(i & 1) * 64) >> 4);
 #pragma unroll
                     for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
                         for (int m = 0; m < 4; ++m) {
                             const uint64_t v = vd + ((ks * 2 * L::kBlock + m * 1024) >> 4), w8 = pd + ((ks * 32) >> 4);
-                            umma_e4m3(tmem + m * L::kOCols, v, w8, idesc(128, L::kOCols, true, true), ks > 0 ? 1u : keep);
-                            if constexpr (!L::kStack)
-                                umma_e4m3(tmem + m * NCOL, v, w8 + (64 >> 4), idesc(128, NCOL, true, true), 1u);
+                            const uint32_t o = tmem + m * L::kOCols;
+                            umma_f8(o, v, w8, idesc(128, L::kOCols, true, Kind::kE4m3E5m2), ks > 0 ? 1u : keep);
+                            if constexpr (!L::kStack) umma_f8(o, v, w8 + (64 >> 4), idesc(128, NCOL, true, Kind::kE4m3E5m2), 1u);
+                            umma_f8(o, v, p3 + ((ks * 32) >> 4), idesc(128, NCOL, true, Kind::kE4m3E5m2), 1u);
                         }
                         umma_commit(bar(L::kBarKvEmpty + st * kTileBlocks + 2 * ks));
                         umma_commit(bar(L::kBarKvEmpty + st * kTileBlocks + 2 * ks + 1));
@@ -580,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < kR; ++k) q_row[k] = col0 + 8 * k < nc ? (c0 + col0 + 8 * k) / p.heads : p.q_per_seq - 1;
         // P: where this thread's pair of keys of 8-key group j goes, p_at[.] (+ 1024 for row k = 1).  bf16: a pair is 4
-        // bytes, group j the 16-byte chunk 4 half + j.  FP8: 2 bytes, chunk 2 half + j / 2, remainders 64 bytes on or
-        // (stacked) NCOL rows.
+        // bytes, group j the 16-byte chunk 4 half + j.  FP8: 2 bytes, chunk 2 half + j / 2, second codes 64 bytes on or
+        // (stacked) NCOL rows, third codes in rows of their own.
         auto p_at = [&](int j) {
             const int v = FP8 ? 2 * half + (j >> 1) : kGroups * half + j;
             return sbase + L::kP + col0 * 128 + ((v ^ (col0 & 7)) << 4) + (FP8 ? 8 * (j & 1) + 2 * (lane & 3) : 4 * (lane & 3));
@@ -823,9 +831,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            // Weights, rounded to bf16 (relative 2^-8; l adds what P V will read), or to a pair of E4M3 codes by way
-            // of fp16 (2^-11; the pair holds relative 2^-8, in steps of 2^-9 where the largest is at least 2^2).
-            uint32_t pk[kR][kGroups];
+            // Weights, rounded to bf16 (relative 2^-8; l adds what P V will read), or to three E5M2 codes by way of fp16
+            // (2^-11; each code is off by 2^-3 of what it rounds, so three by 2^-9, or by 2^-17; l adds the unrounded
+            // weights).
+            uint32_t pk[kR][kGroups], pk3[kR][FP8 ? kGroups : 1];
 #pragma unroll
             for (int k = 0; k < kR; ++k) {
                 const float mu = m_ref[k] == -INFINITY ? 0.f : m_ref[k] - L::kLift;
@@ -835,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 w2 = make_float2(fast_exp2(y.x), fast_exp2(y.y));
                     if constexpr (FP8) {
                         l[k] = ffma2(w2, lds_f32x2(sc_at + 2 * kTile * 4 + 32 * j), l[k]);
-                        pk[k][j] = e4m3_head_and_rest(pack_f16x2(w2.x, w2.y));
+                        e5m2_codes(pack_f16x2(w2.x, w2.y), pk[k][j], pk3[k][j]);
                     } else {
                         pk[k][j] = pack_bf16x2(w2.x, w2.y);
                         l[k] = fadd2(l[k], make_float2(bf16_lo(pk[k][j]), bf16_hi(pk[k][j])));
@@ -853,6 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if constexpr (FP8) {
                                 sts16(at, pk[k][j]);
                                 sts16(L::kStack ? at + NCOL * 128 : at ^ 64u, pk[k][j] >> 16);
+                                sts16((p_at(j) ^ ((i & 1) * 64u)) + (L::kP3 - L::kP) + 1024 * k, pk3[k][j]);
                             } else {
                                 sts32(at, pk[k][j]);
                             }

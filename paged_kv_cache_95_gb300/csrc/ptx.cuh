@@ -268,18 +268,23 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
     return r;
 }
 
-// Two fp16 values -> their E4M3 codes (nearest even, low 16 bits) and the codes of what they leave (high 16 bits).
-__device__ __forceinline__ uint32_t e4m3_head_and_rest(uint32_t f16x2) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 h, l;\n\t.reg .b32 f, d;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 h, %1;\n\t"
-        "cvt.rn.f16x2.e4m3x2 f, h;\n\t"
-        "sub.f16x2 d, %1, f;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 l, d;\n\t"
-        "mov.b32 %0, {h, l};\n\t}"
-        : "=r"(r)
+// Two fp16 values -> three E5M2 codes each (nearest even), each of what the ones before leave: the first in the low 16 bits
+// of ab, the second in the high 16, the third in c.  (An E5M2 code is the high byte of its fp16 value.)
+__device__ __forceinline__ void e5m2_codes(uint32_t f16x2, uint32_t &ab, uint32_t &c) {
+    asm("{\n\t.reg .b16 h, l, t;\n\t.reg .b32 f, d, x;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 h, %2;\n\t"
+        "cvt.u32.u16 x, h;\n\t"
+        "prmt.b32 f, x, 0, 0x1404;\n\t"
+        "sub.f16x2 d, %2, f;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 l, d;\n\t"
+        "cvt.u32.u16 x, l;\n\t"
+        "prmt.b32 f, x, 0, 0x1404;\n\t"
+        "sub.f16x2 d, d, f;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f16x2 t, d;\n\t"
+        "mov.b32 %0, {h, l};\n\t"
+        "cvt.u32.u16 %1, t;\n\t}"
+        : "=r"(ab), "=r"(c)
         : "r"(f16x2));
-    return r;
 }
 
 // Two floats -> packed f16x2 (round to nearest even); `lo` in the low half.
@@ -411,8 +416,8 @@ __device__ __forceinline__ void umma_bf16(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// D[tmem] (+)= A[smem desc] * B[smem desc]; kind::f8f6f4 (E4M3 inputs, f32 accumulate; K = 32).
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// D[tmem] (+)= A[smem desc] * B[smem desc]; kind::f8f6f4 (8-bit inputs of the descriptor's types, f32 accumulate; K = 32).
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
