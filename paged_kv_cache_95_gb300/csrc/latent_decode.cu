@@ -113,7 +113,7 @@ struct Layout {
     static constexpr bool kPHalf = kStack || (!FP8 && TILE == 32);
     static constexpr uint32_t kPBuf = kPHalf ? 64 : NCOL * 128;
     static constexpr uint32_t kP3 = kP + (kPHalf ? 1 : 2) * kOCols * 128;  // FP8: third codes, [NCOL][two buffers of 64]
-    static constexpr uint32_t kScale = kP3 + (FP8 ? NCOL * 128 : 0);  // FP8: [stage][scale, its log2, its inverse][64 keys]
+    static constexpr uint32_t kScale = kP3 + (FP8 ? NCOL * 128 : 0);  // FP8: [stage][scale, its log2, its inverse in kUnit][64 keys]
     static constexpr uint32_t kQf = kScale + (FP8 ? kStages * 3 * TILE * 4 : 0);  // FP8: [a piece's first tile & 1][64] factors of the columns
     // kv_full[stage], kv_empty[stage][block], s_full[2], s_empty[2], p_full[2], pv_done[2], q_full
     static constexpr int kBarKvFull = 0, kBarKvEmpty = kStages, kBarSFull = kBarKvEmpty + kStages * kTileBlocks,
@@ -140,6 +140,9 @@ struct Layout {
     // 2^-9, lost every key below 2^-12 of the largest: with one key of 0.3 of the weight and 14000 more up to 94% of
     // the output.  A raise of 2^4: on the verify of 64 columns a reference was raised in every second tile, 1900 cycles each.)
     static constexpr float kRaise = FP8 ? 6.f : 8.f, kLift = FP8 ? 9.f : 0.f;
+    // FP8: the sum l takes a weight times 1 / s_j, 2^109 for a row of zeros (s = 2^-100 / 448): in units of 2^15, a thousand
+    // of those would be infinite at 2^9.  (At the other end s is 2^120, and l 2^-126.)  O leaves in the same units.
+    static constexpr float kUnit = FP8 ? 0x1p-15f : 1.f;
 };
 
 // Instruction descriptor: D f32; A and B bf16 (kind::f16), or A E4M3 and B E4M3 or E5M2 (kind::f8f6f4).
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float *at = reinterpret_cast<float *>(smem + L::kScale) + st * 3 * kTile + t;
                 at[0] = sc;
                 at[kTile] = __log2f(sc);
-                at[2 * kTile] = __fdividef(1.f, sc);
+                at[2 * kTile] = __fdividef(L::kUnit, sc);
             }
             if (i + 1 < n) w.next(p);
             info.w = w.b;
@@ -699,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool first = true;        // of its piece
         for (int i = 0; i < n; ++i) {
             // FP8: c_j = code s_j, so the score is s_j <q, code_j> + <q_rope, r_j>, and the weight that multiplies the
-            // codes is s_j 2^score = 2^(score + log2 s_j); the sum l takes it times 1 / s_j.
+            // codes is s_j 2^score = 2^(score + log2 s_j); the sum l takes it times 1 / s_j (in kUnit).
             const uint32_t sc_at = sbase + L::kScale + ((i % kStages) * 3 * kTile + kTile / 2 * half + 2 * (lane & 3)) * 4;
             // S; the tile's record and scales; P's buffer, free after P V (i - 2).
             const bool of_kv = lane == 1, of_p = lane == 2 && i >= 2;
@@ -906,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 soft_sync();
                 if (tid < NCOL) alpha_s[tid] = [&] {
                     const float sum = xch[tid] + xch[64 + tid];
-                    return !whole ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+                    return !whole ? 1.f : sum > 0.f ? L::kUnit / sum : 0.f;
                 }();
                 if (tid == 0 && ct == 0 && !whole && !piece_mid) {
                     // The merge's record: this sequence begins here and ends in the range that holds its last tile,
@@ -942,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float *dst = p.part_o + (slot + col) * kLatentDim + dim;
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
-                                if (col + e < nc) dst[static_cast<size_t>(e) * kLatentDim] = __uint_as_float(o[e]);
+                                if (col + e < nc) dst[static_cast<size_t>(e) * kLatentDim] = __uint_as_float(o[e]) * L::kUnit;
                         } else if (p.out_bf16) {
                             // lanes 2 d and 2 d + 1 swap a value: each then stores two dims of one column
                             uint32_t *dst = static_cast<uint32_t *>(p.out) +

@@ -80,8 +80,9 @@ def _reference(pool, ql, qr):
     32 bits; sums over n keys in 32 bits (each addition 2^-23, three products a key and 32 keys an addition)."""
     n, (k, heads, _) = pool.lens[0], ql.shape
     keys, q = pool.sequence(0), torch.cat([ql, qr], -1).double()
-    scale = keys[:, :512].abs().amax(1) / 448
-    codes = keys[:, :512].abs() / scale[:, None]
+    slots = (pool.tables[0].long()[:, None] * 16 + torch.arange(16)).flatten()[:n]
+    scale = pool.cache_scale.view(-1)[slots].double()
+    codes = pool.cache.view(-1, 512)[slots].view(torch.float8_e4m3fn).double().abs()
     out, tol, weights = [], [], []
     for i in range(k):
         seen = n - k + 1 + i
@@ -97,12 +98,9 @@ def _reference(pool, ql, qr):
     return torch.stack(out), torch.stack(tol), weights
 
 
-def _check_peaked(n, heads, weight, where, common, tail, k=1, seqs=None):
-    """As many sequences over the same pages as the GPU has ranges, so that every one lies in a range, whole."""
-    pool, ql, qr = _peaked(n + heads, n, heads, weight, where, common, tail, k)
-    ref, tol, w = _reference(pool, ql, qr)
-    got = torch.stack([x[:, where] for x in w])
-    assert 0.4 * weight < got.mean() < min(1.0, 1.5 * weight)  # (the case is what it says)
+def _run_shared(pool, ql, qr, seqs=None):
+    """The sequence many times over the same pages, as often as the GPU has ranges (every one lies in a range, whole)."""
+    (k, heads, _), n = ql.shape, pool.lens[0]
     if seqs is None:
         tiles = -(-heads * k // 64)
         seqs = torch.cuda.get_device_properties(0).multi_processor_count // tiles
@@ -111,7 +109,16 @@ def _check_peaked(n, heads, weight, where, common, tail, k=1, seqs=None):
                                    block_tables=pool.tables.cuda().repeat(seqs, 1), context_lens=i32([n] * seqs),
                                    scale=R.SCALE, **pool.device())
     assert status_of(ws) == 0
-    out = out.view(seqs, k, heads, 512)
+    return out.view(seqs, k, heads, 512)
+
+
+def _check_peaked(n, heads, weight, where, common, tail, k=1, seqs=None):
+    pool, ql, qr = _peaked(n + heads, n, heads, weight, where, common, tail, k)
+    ref, tol, w = _reference(pool, ql, qr)
+    got = torch.stack([x[:, where] for x in w])
+    assert 0.4 * weight < got.mean() < min(1.0, 1.5 * weight)  # (the case is what it says)
+    out = _run_shared(pool, ql, qr, seqs)
+    seqs = out.shape[0]
     for b in {0, seqs // 2, seqs - 1}:
         err = (out[b].cpu().double() - ref).norm(dim=-1) / ref.norm(dim=-1)
         assert err.max() < 1e-2 and err.mean() < 3e-3, (b, err.max(), err.mean())
@@ -138,3 +145,33 @@ def test_one_key_has_most_of_the_weight_of_a_long_range(heads, k, weight, where,
 def test_one_key_has_most_of_the_weight_of_a_split_sequence(seqs, tail):
     for weight, where in ((0.3, 0), (0.9, 20000)):
         _check_peaked(32000, 64, weight, where, 0.5, tail, seqs=seqs)
+
+
+# ---- scales at their least ------------------------------------------------------------------
+
+def _with_rows(seed, n, latent):
+    """A sequence of n tokens with these latents."""
+    pool = R.Pool(seed, [n], True, spare=0)
+    slots = (pool.tables[0].long()[:, None] * 16 + torch.arange(16)).flatten()[:n]
+    codes, scale = R.quantise(latent)
+    pool.cache.view(-1, 512)[slots], pool.cache_scale.view(-1)[slots] = codes.view(torch.uint8), scale
+    pool.rows[slots, :512] = codes.double() * scale.double()[:, None]
+    return pool
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -10])
+@pytest.mark.parametrize("n,seqs,live", [(3000, None, [0]), (3000, 2, [1500, 2000]), (3000, None, []), (40000, None, [39999]),
+                                         (120000, 1, [119000]), (120000, 1, [])])
+def test_rows_of_zeros_keep_their_weight(n, seqs, live, size, heads):
+    """Tokens whose latents are zeros, written with the least scale there is, but for a few: the zeros weigh as much as the
+    others in the sum, and thousands of them of equal weight (small queries) do not make it infinite."""
+    latent = torch.zeros(n, 512, dtype=torch.bfloat16)
+    latent[live] = R.normal(R.gen(heads), len(live), 512)
+    pool = _with_rows(heads + 1, n, latent)
+    g = R.gen(heads + 2)
+    ql, qr = R.normal(g, 1, heads, 512, scale=size), R.normal(g, 1, heads, 64, scale=size)
+    ref, tol, _ = _reference(pool, ql, qr)
+    out = _run_shared(pool, ql, qr, seqs)
+    R.assert_within(out[0], ref, tol, "zeros")
+    R.assert_within(out[-1], ref, tol, "zeros")
