@@ -733,7 +733,8 @@ PKV_API int latent_attention_decode(void *out, int32_t out_dtype, const void *q_
  * latent_attention_decode_fp8 -- the same over an FP8 pool, c_j = code * scale as
  * latent_reshape_and_cache_fp8 wrote it.  Beyond the codes themselves: softmax weights are
  * rounded to 2^-9 (each, relative; those below 2^-17 of the largest to 2^-26 of it), the
- * latent part of a query to 2^-17 of its row's largest value.
+ * latent part of a query to 2^-17 of its row's largest value, scales below 2^-100 / 448 (a
+ * cleared pool's 0 among them) count as that.
  */
 PKV_API int latent_attention_decode_fp8(void *out, int32_t out_dtype, const void *q_latent,
                                         int64_t q_latent_row_stride, int64_t q_latent_head_stride, const void *q_rope,

@@ -67,6 +67,7 @@ constexpr int kScoreWarp = kSoftWarps + 1;    // issues S = Q K^T
 constexpr int kValueWarp = kSoftWarps + 2;    // issues O^T += V^T P^T
 constexpr int kLoadWarp = kSoftWarps + 3;     // two pairs of copying warps, one pair a stage
 constexpr int kThreads = (kSoftWarps + 7) * 32;
+constexpr float kLeastScale = 0x1p-100f / 448.f;  // of an FP8 row, as latent_write_fp8_kernel makes it of zeros
 constexpr int kMaxLeft = 1 << 20;  // of a tile's record; past the tile and 16 rows the keys are all the same
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;  // O^T in columns [0, 4 NCOL), the scores of tile i from 256 + (i & 1) kScoreCols on
@@ -450,6 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // blocks' P V): 1 for a slot without a key, whose scale may be anything.
                 const int blk = __shfl_sync(0xffffffffu, id, t >> 4);
                 if (blk >= 0 && w.t * kTile + t < w.keys) sc = __ldg(p.cache_scale + static_cast<size_t>(blk) * kBlockSize + (t & 15));
+                // A slot of a cleared pool has scale 0, whose logarithm and inverse are infinite: the least that a write
+                // makes instead (NaN stays).
+                if (fabsf(sc) < kLeastScale) sc = kLeastScale;
             }
             bool ok = true;
 #pragma unroll

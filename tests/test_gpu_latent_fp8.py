@@ -175,3 +175,33 @@ def test_rows_of_zeros_keep_their_weight(n, seqs, live, size, heads):
     out = _run_shared(pool, ql, qr, seqs)
     R.assert_within(out[0], ref, tol, "zeros")
     R.assert_within(out[-1], ref, tol, "zeros")
+
+
+@pytest.mark.parametrize("heads", [16, 32, 64])
+@pytest.mark.parametrize("cleared", [[5], [0, 1, 2, 64, 130], range(300)])
+def test_scales_of_zero(cleared, heads):
+    """Tokens with a scale of 0 are c = 0 whatever their codes, as the read-back has them; among others, and a pool that
+    was cleared and never written."""
+    n = 300
+    pool = _with_rows(heads, n, R.normal(R.gen(heads + 1), n, 512))
+    slots = (pool.tables[0].long()[:, None] * 16 + torch.arange(16)).flatten()[:n][list(cleared)]
+    pool.cache_scale.view(-1)[slots], pool.rows[slots, :512] = 0.0, 0.0
+    if len(cleared) == n:
+        pool.cache.zero_()
+    g = R.gen(heads + 2)
+    ql, qr = R.normal(g, 1, heads, 512), R.normal(g, 1, heads, 64)
+    ref, tol, _ = _reference(pool, ql, qr)
+    for seqs in (1, None):
+        out = _run_shared(pool, ql, qr, seqs)
+        R.assert_within(out[0], ref, tol, "cleared scales")
+        R.assert_within(out[-1], ref, tol, "cleared scales")
+    rows = torch.empty(n, 576, dtype=torch.bfloat16, device="cuda")
+    P.latent_gather(rows, block_tables=pool.tables.cuda(), cu_lens=i32([0, n]), **pool.device())
+    assert (rows[list(cleared), :512] == 0).all()
+
+
+def test_a_scale_that_is_not_finite_spoils_its_sequence():
+    pool = _with_rows(1, 200, R.normal(R.gen(2), 200, 512))
+    q = R.normal(R.gen(3), 1, 16, 512), R.normal(R.gen(4), 1, 16, 64)
+    pool.cache_scale.view(-1)[int(pool.tables[0, 1]) * 16 + 3] = R.NAN
+    assert _run_shared(pool, *q, 1).isnan().all()
