@@ -488,8 +488,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!warp_wait(bar(kBarMerge), 0)) return;
                     const float2 ml = lds_f32x2(other_ml);
                     const float all = fmaxf(m, ml.x);
-                    w0 = m == -INFINITY ? 0.f : fast_exp2(m - all);
-                    w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - all);
+                    // (A side that a row sees nothing of weighs 0.  One whose scores are all NaN has m = -infinity too, but its l
+                    // is NaN, and so is its weight; the difference of two infinities is NaN as well.)
+                    w0 = m == -INFINITY ? l : fast_exp2(m - all);
+                    w1 = ml.x == -INFINITY ? ml.y : fast_exp2(ml.x - all);
                     l = w0 * l + w1 * ml.y;
                     m = all;
                 }
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 8; ++e) {
                             const uint4 u = lds128(other_o + (((8 * k + e) ^ lane) << 4));
                             auto join = [&](int x, uint32_t y) {
-                                v[4 * e + x] = __float_as_uint(w0 * __uint_as_float(v[4 * e + x]) + (w1 > 0.f ? w1 * __uint_as_float(y) : 0.f));
+                                v[4 * e + x] = __float_as_uint(w0 * __uint_as_float(v[4 * e + x]) + (w1 == 0.f ? 0.f : w1 * __uint_as_float(y)));
                             };
                             join(0, u.x), join(1, u.y), join(2, u.z), join(3, u.w);
                         }

@@ -752,3 +752,22 @@ def test_a_served_sequence(fp8):
                                   q_per_seq=k, **d)
         R.assert_within(out, *R.decode(*q, pool, k), f"decode of {k}")
     bm.close()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("value", [R.NAN, float("inf")])
+@pytest.mark.parametrize("q_len,k_len,keys", [(1, 129, [128]), (3, 131, [128]), (100, 400, range(128, 256)), (1, 200, range(128)),
+                                              (40, 300, range(256)), (2, 2000, range(1920, 2000))])
+def test_prefill_split_keys_that_are_not_finite(q_len, k_len, keys, value, dtype):
+    """One row tile, whose even and odd key tiles are joined: keys that fill what one side sees, NaN or with scores of
+    infinity, make every row that sees one NaN, as they do where nothing is split."""
+    heads = 3
+    q, kv, rows = prefill_inputs(k_len, [q_len], [k_len], heads, spare=0)
+    q = q.abs() + 0.1  # (scores of an infinite key are +infinity, never NaN)
+    keys = list(keys)
+    kv[keys, 1, 5] = value
+    out, ws = run_prefill(q, kv, rows, [q_len], [k_len], dtype=dtype)
+    sees = torch.arange(q_len) + k_len - q_len >= keys[0]
+    assert out[:, 1].cpu()[sees].isnan().all()
+    assert torch.isfinite(out[:, 1].cpu()[~sees]).all() and torch.isfinite(out[:, [0, 2]]).all()
+    assert status_of(ws) == 0
