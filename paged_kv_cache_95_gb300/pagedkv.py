@@ -852,12 +852,22 @@ def latent_gather(out, cache, block_tables, cu_lens, rope_cache=None, cache_scal
     _raise("latent_gather", rc)
 
 
-def _new_workspace(nbytes, what, like):
-    """Device scratch whose status word starts clear (the rest is written before it is read)."""
+def _new_workspace(nbytes, what, like, stream):
+    """Device scratch whose status word starts clear (the rest is written before it is read), allocated and cleared on the
+    call's stream (its handle): on another one the clear could come behind the kernel, and the memory still be in use."""
+    torch = _torch()
     _need(nbytes > 0, f"invalid sizes for {what}")
-    workspace = _torch().empty(nbytes, dtype=_torch().uint8, device=like.device)
-    workspace[:256].zero_()
-    return workspace
+
+    def new():
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        workspace[:256].zero_()
+        return workspace
+
+    if stream == torch.cuda.current_stream(like.device).cuda_stream:
+        return new()
+    # (A handle of 0 is the default stream, which ExternalStream would take for a new one.)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, like.device) if stream else torch.cuda.default_stream(like.device)):
+        return new()
 
 
 def latent_attention_workspace_size(num_seqs: int, q_per_seq: int, num_q_heads: int, max_blocks_per_seq: int,
@@ -890,7 +900,8 @@ def latent_attention_decode(out, q_latent, q_rope, cache, block_tables, context_
         raise ValueError("q_latent must hold q_per_seq rows per sequence")
     lib = _lib or load_library()
     if workspace is None:
-        workspace = _new_workspace(lib.latent_attention_workspace_size(B, k, heads, max_blocks, desc), "latent_attention_decode", out)
+        workspace = _new_workspace(lib.latent_attention_workspace_size(B, k, heads, max_blocks, desc), "latent_attention_decode", out,
+                                   stream)
     (size,), space = _flat(workspace, "workspace", torch.uint8, 1, device)
     if fp8:
         rc = lib.latent_attention_decode_fp8(out_at, code, ql, ql_strides[0], ql_strides[1], qr, qr_strides[0], qr_strides[1],
@@ -938,7 +949,7 @@ def latent_attention_prefill_chunk(out, q, k_nope, v, k_rope, cu_q_lens, cu_k_le
     lib = _lib or load_library()
     if workspace is None:
         workspace = _new_workspace(lib.latent_attention_prefill_workspace_size(B, heads, max_q_len, tq, tk),
-                                   "latent_attention_prefill_chunk", out)
+                                   "latent_attention_prefill_chunk", out, stream)
     (size,), space = _flat(workspace, "workspace", torch.uint8, 1, device)
     rc = lib.latent_attention_prefill_chunk(out_at, code, q_at, q_strides[0], q_strides[1], k_at, v_at, k_strides[0], k_strides[1],
                                             rope_at, rope_strides[0], cu_q, cu_k, B, heads, max_q_len, tq, tk, scale, space, size,

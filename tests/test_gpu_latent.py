@@ -771,3 +771,58 @@ def test_prefill_split_keys_that_are_not_finite(q_len, k_len, keys, value, dtype
     assert out[:, 1].cpu()[sees].isnan().all()
     assert torch.isfinite(out[:, 1].cpu()[~sees]).all() and torch.isfinite(out[:, [0, 2]]).all()
     assert status_of(ws) == 0
+
+
+def _busy():
+    """Work of a tenth of a second on the current stream."""
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_allocates_its_workspace_on_the_stream_it_is_given(fp8, handle):
+    """The current stream is busy: the call on another one neither waits for it nor loses its status to a clear there."""
+    pool = R.Pool(95, [0, 700, 90], fp8)
+    q = queries(96, 3, 16)
+    d, ql, qr, tables, lens = pool.device(), q[0].cuda(), q[1].cuda(), pool.tables.cuda(), i32(pool.lens)
+    out = torch.full((3, 16, 512), R.NAN, device="cuda")
+    s = torch.cuda.Stream()
+    _busy()
+    ws = P.latent_attention_decode(out, ql, qr, block_tables=tables, context_lens=lens, scale=R.SCALE,
+                                   stream=s.cuda_stream if handle else s, **d)
+    s.synchronize()
+    assert not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    R.assert_within(out, *R.decode(*q, pool, 1), "another stream")
+    assert status_of(ws) == P.PKV_STATUS_BAD_CONTEXT_LEN  # (of the empty sequence)
+
+
+def test_decode_on_the_default_stream_by_its_handle():
+    pool = R.Pool(97, [0, 300])
+    q = queries(98, 2, 16)
+    d, ql, qr, tables, lens = pool.device(), q[0].cuda(), q[1].cuda(), pool.tables.cuda(), i32(pool.lens)
+    out = torch.full((2, 16, 512), R.NAN, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        ws = P.latent_attention_decode(out, ql, qr, block_tables=tables, context_lens=lens, scale=R.SCALE, stream=0, **d)
+    torch.cuda.synchronize()
+    R.assert_within(out, *R.decode(*q, pool, 1), "default stream")
+    assert status_of(ws) == P.PKV_STATUS_BAD_CONTEXT_LEN
+
+
+def test_prefill_allocates_its_workspace_on_the_stream_it_is_given():
+    q_lens, k_lens = [100, 5], [3000, 3]  # parts of the keys, and a sequence with more queries than keys
+    q, kv, rows = prefill_inputs(99, q_lens, k_lens, 2, spare=0)
+    ref, tol = R.expanded(q, kv[..., :128], kv[..., 128:], rows[:, 512:], q_lens, k_lens)
+    qd, kvd, rowsd, cq, ck = q.cuda(), kv.cuda(), rows.cuda(), i32(starts(q_lens)), i32(starts(k_lens))
+    out = torch.full((105, 2, 128), R.NAN, device="cuda")
+    s = torch.cuda.Stream()
+    _busy()
+    ws = P.latent_attention_prefill_chunk(out, qd, kvd[..., :128], kvd[..., 128:], rowsd[:, 512:], cq, ck, 100, R.SCALE, stream=s)
+    s.synchronize()
+    assert not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    R.assert_within(out, ref, tol, "another stream")
+    assert status_of(ws) == P.PKV_STATUS_BAD_Q_LEN
