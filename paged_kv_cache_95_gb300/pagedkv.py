@@ -229,6 +229,24 @@ def _need(cond: bool, msg: str):
         raise ValueError(msg)
 
 
+def _new_workspace(nbytes, what, like, stream, clear=None):
+    """Device scratch whose first ``clear`` bytes are zero (None: all), allocated and cleared on the call's stream (its
+    handle): on another one the clear could come behind the kernel, and the memory still be in use."""
+    torch = _torch()
+    _need(nbytes > 0, f"invalid sizes for {what}")
+
+    def new():
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        (workspace if clear is None else workspace[:clear]).zero_()
+        return workspace
+
+    if stream == torch.cuda.current_stream(like.device).cuda_stream:
+        return new()
+    # (A handle of 0 is the default stream, which ExternalStream would take for a new one.)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, like.device) if stream else torch.cuda.default_stream(like.device)):
+        return new()
+
+
 def _check(t, name, dtype, ndim=None, last=None):
     torch = _torch()
     _need(isinstance(t, torch.Tensor), f"{name} must be a torch.Tensor")
@@ -475,8 +493,7 @@ def paged_attention_decode(out, q, k_cache, v_cache, block_tables, context_lens,
     max_blocks = int(block_tables.shape[1])
     if workspace is None:
         nbytes = paged_attention_workspace_size(B, n_q, max_blocks, partition_size, desc)
-        _need(nbytes > 0, "invalid sizes for paged_attention_decode")
-        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)  # status word starts clear
+        workspace = _new_workspace(nbytes, "paged_attention_decode", q, _stream(stream))  # status word starts clear
     _check(workspace, "workspace", torch.uint8, ndim=1)
     lib = load_library()
     if fp8:
@@ -532,8 +549,7 @@ def paged_attention_verify(out, q, q_per_seq: int, k_cache, v_cache, block_table
     if workspace is None:
         nbytes = int(lib.paged_attention_verify_workspace_size_on(int(kernel), B, int(q_per_seq), n_q, max_blocks,
                                                                   int(partition_size), ctypes.byref(desc)))
-        _need(nbytes > 0, "invalid sizes for paged_attention_verify")
-        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
+        workspace = _new_workspace(nbytes, "paged_attention_verify", q, _stream(stream))
     _check(workspace, "workspace", torch.uint8, ndim=1)
     if kernel != PKV_VERIFY_AUTO:
         rc = lib.paged_attention_verify_on(int(kernel), _ptr(out), _out_dtype(out), _ptr(q), int(q_per_seq),
@@ -606,8 +622,7 @@ def paged_attention_prefill_chunk(out, q, cu_q_lens, max_q_len: int, k_cache, v_
     if workspace is None:
         nbytes = paged_attention_prefill_chunk_workspace_size(B, n_q, int(rows), int(max_q_len),
                                                               int(block_tables.shape[1]), desc)
-        _need(nbytes > 0, "invalid sizes for paged_attention_prefill_chunk")
-        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)  # status word starts clear
+        workspace = _new_workspace(nbytes, "paged_attention_prefill_chunk", q, _stream(stream))  # status word starts clear
     _check(workspace, "workspace", torch.uint8, ndim=1)
     lib = load_library()
     if fp8:
@@ -656,8 +671,7 @@ def paged_attention_decode_append(out, q, key, value, k_cache, v_cache, block_ta
     max_blocks = int(block_tables.shape[1])
     if workspace is None:
         nbytes = paged_attention_workspace_size(B, n_q, max_blocks, partition_size, desc)
-        _need(nbytes > 0, "invalid sizes for paged_attention_decode_append")
-        workspace = torch.zeros(nbytes, dtype=torch.uint8, device=q.device)
+        workspace = _new_workspace(nbytes, "paged_attention_decode_append", q, _stream(stream))
     _check(workspace, "workspace", torch.uint8, ndim=1)
     rc = load_library().paged_attention_decode_append(
         _ptr(out), _out_dtype(out), _ptr(q), _ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache),
@@ -852,24 +866,6 @@ def latent_gather(out, cache, block_tables, cu_lens, rope_cache=None, cache_scal
     _raise("latent_gather", rc)
 
 
-def _new_workspace(nbytes, what, like, stream):
-    """Device scratch whose status word starts clear (the rest is written before it is read), allocated and cleared on the
-    call's stream (its handle): on another one the clear could come behind the kernel, and the memory still be in use."""
-    torch = _torch()
-    _need(nbytes > 0, f"invalid sizes for {what}")
-
-    def new():
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-        workspace[:256].zero_()
-        return workspace
-
-    if stream == torch.cuda.current_stream(like.device).cuda_stream:
-        return new()
-    # (A handle of 0 is the default stream, which ExternalStream would take for a new one.)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, like.device) if stream else torch.cuda.default_stream(like.device)):
-        return new()
-
-
 def latent_attention_workspace_size(num_seqs: int, q_per_seq: int, num_q_heads: int, max_blocks_per_seq: int,
                                     desc: LatentDesc) -> int:
     return int(load_library().latent_attention_workspace_size(num_seqs, q_per_seq, num_q_heads, max_blocks_per_seq,
@@ -901,7 +897,7 @@ def latent_attention_decode(out, q_latent, q_rope, cache, block_tables, context_
     lib = _lib or load_library()
     if workspace is None:
         workspace = _new_workspace(lib.latent_attention_workspace_size(B, k, heads, max_blocks, desc), "latent_attention_decode", out,
-                                   stream)
+                                   stream, clear=256)
     (size,), space = _flat(workspace, "workspace", torch.uint8, 1, device)
     if fp8:
         rc = lib.latent_attention_decode_fp8(out_at, code, ql, ql_strides[0], ql_strides[1], qr, qr_strides[0], qr_strides[1],
@@ -949,7 +945,7 @@ def latent_attention_prefill_chunk(out, q, k_nope, v, k_rope, cu_q_lens, cu_k_le
     lib = _lib or load_library()
     if workspace is None:
         workspace = _new_workspace(lib.latent_attention_prefill_workspace_size(B, heads, max_q_len, tq, tk),
-                                   "latent_attention_prefill_chunk", out, stream)
+                                   "latent_attention_prefill_chunk", out, stream, clear=256)
     (size,), space = _flat(workspace, "workspace", torch.uint8, 1, device)
     rc = lib.latent_attention_prefill_chunk(out_at, code, q_at, q_strides[0], q_strides[1], k_at, v_at, k_strides[0], k_strides[1],
                                             rope_at, rope_strides[0], cu_q, cu_k, B, heads, max_q_len, tq, tk, scale, space, size,
