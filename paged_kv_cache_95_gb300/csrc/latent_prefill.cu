@@ -400,10 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float alpha = 1.f;
                             if (mx > m + kRaise) {
                                 // The first largest score as it is, then steps of whole powers of two: the weights of the
-                                // largest scores are exact in bf16, and a row of one key is its value.
-                                const float up = m == -INFINITY ? INFINITY : ceilf(mx - m);
+                                // largest scores are exact in bf16, and a row of one key is its value.  (From 2^256 on
+                                // nothing is left of what was: the new score itself, for a step from a mask's -1e10 or
+                                // less is rounded by more than the scores that follow.)
+                                const float up = ceilf(mx - m);
                                 alpha = fast_exp2(-up);
-                                m = m == -INFINITY ? mx : m + up;
+                                m = up < 256.f ? m + up : mx;
                             }
                             l2 = fmul2(l2, make_float2(alpha, alpha));
                             l3 = fmul2(l3, make_float2(alpha, alpha));

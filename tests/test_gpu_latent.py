@@ -826,3 +826,19 @@ def test_prefill_allocates_its_workspace_on_the_stream_it_is_given():
     torch.cuda.synchronize()
     R.assert_within(out, ref, tol, "another stream")
     assert status_of(ws) == P.PKV_STATUS_BAD_Q_LEN
+
+
+@pytest.mark.parametrize("size", [1.0, 100.0])
+@pytest.mark.parametrize("low", [-1e6, -3e12, torch.finfo(torch.bfloat16).min, -float("inf")])
+@pytest.mark.parametrize("q_len,k_len,first", [(1, 400, 130), (100, 600, 260), (300, 900, 300), (2, 4000, 3000)])
+def test_prefill_first_keys_masked_by_low_scores(q_len, k_len, first, low, size):
+    """The keys that a row sees first have a score of a large negative number or -infinity (a mask that the caller put into
+    the rotated key): those behind them are weighed as if the first were not there."""
+    q, kv, rows = prefill_inputs(k_len, [q_len], [k_len], 2, spare=0, scale=size)
+    q[..., 128] = 1.0
+    rows[:, 512] = 0
+    rows[:first, 512] = low
+    out, ws = run_prefill(q, kv, rows, [q_len], [k_len])
+    R.assert_within(out, *R.expanded(q, kv[first:, :, :128], kv[first:, :, 128:], rows[first:, 512:], [q_len], [k_len - first]),
+                    f"low {low}")
+    assert status_of(ws) == 0
