@@ -913,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 soft_sync();
                 if (tid < NCOL) alpha_s[tid] = [&] {
                     const float sum = xch[tid] + xch[64 + tid];
-                    return !whole ? 1.f : sum > 0.f ? L::kUnit / sum : 0.f;
+                    return !whole ? 1.f : sum > 0.f ? L::kUnit / sum : sum;  // (0, or NaN: never a finite row from a sum that is none)
                 }();
                 if (tid == 0 && ct == 0 && !whole && !piece_mid) {
                     // The merge's record: this sequence begins here and ends in the range that holds its last tile,
@@ -1062,7 +1062,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, BATCH > 2 ? 2 : 3) latent_me
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum > 0.f ? 1.f / sum : sum;  // (0 or NaN)
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) o[s] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int j = 0;;) {

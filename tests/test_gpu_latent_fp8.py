@@ -205,3 +205,18 @@ def test_a_scale_that_is_not_finite_spoils_its_sequence():
     q = R.normal(R.gen(3), 1, 16, 512), R.normal(R.gen(4), 1, 16, 64)
     pool.cache_scale.view(-1)[int(pool.tables[0, 1]) * 16 + 3] = R.NAN
     assert _run_shared(pool, *q, 1).isnan().all()
+
+
+@pytest.mark.parametrize("heads", [8, 64])
+@pytest.mark.parametrize("n", [40, 130, 9000])
+def test_a_scale_that_is_not_finite_never_makes_zeros(n, heads):
+    """The last key's scale is NaN: its own row is NaN, and the row before it, which does not see the key, is either right or NaN."""
+    pool = _with_rows(n, n, R.normal(R.gen(n + 1), n, 512))
+    g = R.gen(n + 2)
+    ql, qr = R.normal(g, 2, heads, 512), R.normal(g, 2, heads, 64)
+    ref, tol, _ = _reference(pool, ql, qr)
+    pool.cache_scale.view(-1)[int(pool.tables[0, (n - 1) // 16]) * 16 + (n - 1) % 16] = R.NAN
+    out = _run_shared(pool, ql, qr, 1)[0].cpu()
+    assert out[1].isnan().all()
+    if not out[0].isnan().all():
+        R.assert_within(out[0], ref[0], tol[0], "the row before")
