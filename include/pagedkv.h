@@ -657,8 +657,8 @@ PKV_API int latent_reshape_and_cache(const void *latent, int64_t latent_stride, 
  * latent_reshape_and_cache_fp8 -- the same into an FP8 (E4M3) pool: the latent is
  * quantised as kv_reshape_and_cache_fp8 quantises a head's row, with x = latent[t]:
  *     a = max(max_k |x_k|, 2^-100);  code_k = E4M3(x_k * (448 / a));  scale = a / 448
- * (each step one correctly rounded fp32 operation, so the codes are reproducible);
- * the rotated key is copied.
+ * (each step one correctly rounded fp32 operation, so the codes are reproducible; the
+ * maximum passes over a NaN, whose own code is NaN); the rotated key is copied.
  * Errors: as latent_reshape_and_cache.
  */
 PKV_API int latent_reshape_and_cache_fp8(const void *latent, int64_t latent_stride, const void *rope,
@@ -761,7 +761,7 @@ PKV_API int latent_attention_decode_fp8(void *out, int32_t out_dtype, const void
  *   cu_q_lens, cu_k_lens : int32 [num_seqs + 1], device, non-decreasing, from 0
  *   strides   : at least 8 here (rows and heads are boxes of a tensor map)
  *   max_q_len : host upper bound of every q_len (sizes the launch grid; the lesser of
- *               it and total_q_rows up to 16776960)
+ *               it and total_q_rows up to 16776960; 0 enqueues nothing)
  *   total_q_rows, total_k_rows : rows of q / out and of the keys
  *   workspace : 256-byte aligned, status word at byte 0, zeroed once.  With
  *               latent_attention_prefill_workspace_size() bytes (for the current device;

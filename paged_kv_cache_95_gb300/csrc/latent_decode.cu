@@ -37,7 +37,7 @@
 // sequences and 32 heads 39.0 us, 25.5 of them bytes); with 64 the tensor pipe, 36 MMAs of
 // 28 cycles for S and 16 of 52 for P V, whose operands come from shared memory (8 x 32K
 // tokens of 64 heads 63.9 us, 128 heads over 32 sequences 72.6).  FP8: 64 keys a tile,
-// with 32 columns the ring's four stages held from S to P V (32.2 us, 14.5 of bytes; 30.2 with P
+// with 32 columns the ring's four stages held from S to P V (32.3 us, 14.5 of bytes; 30.2 with P
 // as two codes), with 64 the tensor pipe and three stages (4 rows x 64 heads over 16 sequences
 // 100.9 us, 39.9 of operations; 90.8 with two codes).  Around
 // the tiles: launch, plan and first copies 5 us, Q of another sequence and the epilogue of
@@ -85,8 +85,8 @@ struct Layout {
     static constexpr uint32_t kBlock = 2 * kGroup;
     static constexpr uint32_t kRopeBlock = FP8 ? kBlockSize * 128 : 0;
     static constexpr uint32_t kStage = kTileBlocks * (kBlock + kRopeBlock);
-    // FP8: the E4M3 heads and remainders of Q are rows of one product, those of P (up to 32 columns) columns of one: an
-    // MMA of few columns is bound by its other operand, M = 128 takes 43 cycles with N = 32 and 52 with 64, and N = 64
+    // FP8: the E4M3 heads and remainders of Q are rows of one product, two of P's codes (up to 32 columns) columns of one:
+    // an MMA of few columns is bound by its other operand, M = 128 takes 43 cycles with N = 32 and 52 with 64, and N = 64
     // takes 35 with M = 64 and 52 with 128.  A remainder's row is 8 behind its head's, in rows that M = 64 has anyway
     // and in the same thread after the load; for 64 columns 16 behind, M = 128.  P is three E5M2 codes a weight, what
     // each leaves in the next: the second's column is NCOL behind the first's (for 64 columns O has no room: a product of

@@ -41,7 +41,7 @@
 //    S(k + 1) follows P V (k): it overwrites the P that P V reads, and the MMAs of one
 //    thread run in order.
 //
-// 8192 tokens x 32 heads: 450 us, 1.53 PFLOP/s.  Short chunks (4 of 162-417 rows behind
+// 8192 tokens x 32 heads: 450 us, 1.53 PFLOP/s (487, 1.41, in a run of seconds under the power cap).  Short chunks (4 of 162-417 rows behind
 // 179-791 cached ones, 32 heads): 35.1 us; 224 CTAs of 4 to 9 key tiles on 152 SMs, each with
 // 5-6 us of launch, first copies and epilogue.  (CTAs that take the next unit themselves,
 // its copies issued early: no gain there, and the long prompt's loop got 6% slower.)
