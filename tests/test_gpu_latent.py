@@ -788,6 +788,7 @@ def test_decode_allocates_its_workspace_on_the_stream_it_is_given(fp8, handle):
     d, ql, qr, tables, lens = pool.device(), q[0].cuda(), q[1].cuda(), pool.tables.cuda(), i32(pool.lens)
     out = torch.full((3, 16, 512), R.NAN, device="cuda")
     s = torch.cuda.Stream()
+    run_decode(pool, *q, 1)  # (the kernels are loaded)
     _busy()
     ws = P.latent_attention_decode(out, ql, qr, block_tables=tables, context_lens=lens, scale=R.SCALE,
                                    stream=s.cuda_stream if handle else s, **d)
@@ -819,6 +820,7 @@ def test_prefill_allocates_its_workspace_on_the_stream_it_is_given():
     qd, kvd, rowsd, cq, ck = q.cuda(), kv.cuda(), rows.cuda(), i32(starts(q_lens)), i32(starts(k_lens))
     out = torch.full((105, 2, 128), R.NAN, device="cuda")
     s = torch.cuda.Stream()
+    run_prefill(q, kv, rows, q_lens, k_lens)  # (the kernels are loaded)
     _busy()
     ws = P.latent_attention_prefill_chunk(out, qd, kvd[..., :128], kvd[..., 128:], rowsd[:, 512:], cq, ck, 100, R.SCALE, stream=s)
     s.synchronize()
