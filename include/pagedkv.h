@@ -502,7 +502,7 @@ PKV_API int paged_attention_prefill_chunk_fp8(void *out, int32_t out_dtype, cons
  * are appended first, so ctx_b counts them; row i (0 <= i < k) of sequence b
  * sits at position ctx_b - k + i and sees keys j <= ctx_b - k + i (the causal
  * rule among the draft tokens; row k - 1 is an ordinary decode row).  The
- * acceptance rule itself (sampling) is not part of this library.
+ * acceptance rule is speculative_verify.
  *
  *   q, out    : [num_seqs * q_per_seq][num_q_heads][head_dim]; sequence b owns
  *               rows b * q_per_seq .. b * q_per_seq + q_per_seq - 1
@@ -784,6 +784,175 @@ PKV_API int latent_attention_prefill_chunk(void *out, int32_t out_dtype, const v
                                            int32_t num_seqs, int32_t num_heads, int32_t max_q_len,
                                            int32_t total_q_rows, int32_t total_k_rows, float scale, void *workspace,
                                            size_t workspace_bytes, void *stream);
+
+/*
+ * ---- A step of speculative decoding ------------------------------------------------
+ * The target model checks drafted tokens in one pass ("LLM 推理全过程的维度变化与核心公式",
+ * section "工程优化怎么嵌进公式", Speculative Decoding; xinc.fun archive 233, section 7).
+ * Here the drafts of a sequence are a tree (a chain is one): node 0 is the token sampled
+ * last, whose K and V are not cached yet, the others are drafts, each behind its parent
+ * (parents[j] < j).  Sequence b owns rows cu_q_lens[b] .. cu_q_lens[b + 1] - 1 of the
+ * step's tensors, one a node, 64 at most.  A step, with c the tokens cached before it:
+ *   1. rotary_reshape_and_cache: node j's key turned to position c + depth(j) and
+ *      written to the slot of position c + j;
+ *   2. paged_attention_tree: every node over the c cached tokens and its own ancestors;
+ *   3. speculative_verify: the path of accepted nodes, and one token more;
+ *   4. kv_compact_path: the path's rows to the slots of positions c, c + 1, ..
+ * after which c + counts[b] tokens are cached.
+ */
+#define PKV_MAX_TREE_NODES 64
+
+/*
+ * Rotary positions: pair i of a head's first rotary_dim values turns by the angle
+ * position * w_i,   (a, b) -> magnitude * (a cos - b sin, b cos + a sin);
+ * the values behind them stay as they are.  A pair is (i, i + rotary_dim / 2) or
+ * (2 i, 2 i + 1).
+ */
+#define PKV_ROTARY_HALF 0
+#define PKV_ROTARY_INTERLEAVED 1
+
+/* How w_i = base^(-2 i / rotary_dim) is stretched for contexts longer than the trained ones. */
+#define PKV_ROTARY_SCALING_NONE 0
+#define PKV_ROTARY_SCALING_LINEAR 1        /* w / factor */
+#define PKV_ROTARY_SCALING_NTK 2           /* base * factor^(d / (d - 2)) for base, d = rotary_dim */
+#define PKV_ROTARY_SCALING_BY_PARTS 3      /* w / factor for pairs that turn less than `low` times over original_length, w
+                                              for those that turn more than `high` times, between them a ramp over the
+                                              pairs' numbers (ends rounded outwards to whole numbers); the
+                                              magnitude is 0.1 ln(factor) + 1 (1 for a factor up to 1) */
+#define PKV_ROTARY_SCALING_BY_WAVELENGTH 4 /* the same ends, between them a ramp over the number of turns; magnitude 1 */
+typedef struct pkv_rotary_scaling {
+    int32_t kind;            /* PKV_ROTARY_SCALING_* */
+    int32_t original_length; /* by parts, by wavelength: tokens of the contexts trained on (>= 1) */
+    double factor;           /* > 0 (not read for NONE) */
+    double low, high;        /* by parts, by wavelength: turns, 0 < low < high */
+} pkv_rotary_scaling;
+
+/*
+ * rotary_frequencies -- the w_i as the entry points below take them: turns a position,
+ * modulo one turn, in units of 2^-64.  The product with a position in 64-bit whole
+ * numbers is then the angle without a rounding, however far the position.  Host
+ * memory; needs no GPU.
+ *   frequencies : HOST array of rotary_dim / 2;  magnitude : receives the magnitude
+ *   base        : above 1;  scaling : NULL for none
+ * Errors: PKV_ERR_INVALID_ARG.
+ */
+PKV_API int rotary_frequencies(uint64_t *frequencies, float *magnitude, int32_t rotary_dim, double base,
+                               const pkv_rotary_scaling *scaling);
+
+/*
+ * rotary_embedding -- rows turned to their positions, rounded once.
+ *   out, x      : bf16, (token, head) at base + token * row_stride + head * head_stride,
+ *                 head_dim values, 16-byte aligned; strides in elements, multiples of 8.
+ *                 In place with out == x and equal strides; other overlaps are the
+ *                 caller's error
+ *   positions   : int32 [num_tokens], device; a position below 0 turns back (the gradient
+ *                 of a turn by p is a turn by -p)
+ *   frequencies : DEVICE copy of rotary_frequencies()'s, [rotary_dim / 2], 8-byte aligned
+ *   head_dim    : a multiple of 16, up to 1024;  rotary_dim : a multiple of 16, up to head_dim
+ *   num_tokens  : >= 0 (0 enqueues nothing)
+ * Errors: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED / PKV_ERR_CUDA.
+ */
+PKV_API int rotary_embedding(void *out, int64_t out_row_stride, int64_t out_head_stride, const void *x,
+                             int64_t x_row_stride, int64_t x_head_stride, const int32_t *positions,
+                             const uint64_t *frequencies, int32_t num_tokens, int32_t num_heads, int32_t head_dim,
+                             int32_t rotary_dim, int32_t layout, float magnitude, void *stream);
+
+/*
+ * rotary_reshape_and_cache -- queries and keys turned to their positions, the keys (and
+ * the values as they are) written to the pool, in one launch:
+ *     q_out[t][h] = turn(q[t][h], positions[t])
+ *     slot = slot_mapping[t]:  k_cache[slot] = turn(key[t], positions[t]),  v_cache[slot] = value[t]
+ * The same bits as rotary_embedding of q and key followed by kv_reshape_and_cache.
+ *   q           : bf16, (token, head) at q + token * q_row_stride + head * q_head_stride, 128
+ *                 values; key, value: the same, cache->num_kv_heads heads (usually slices of
+ *                 one projection's rows).  16-byte aligned, strides multiples of 8
+ *   q_out       : bf16 [num_tokens][num_q_heads][128], contiguous, 16-byte aligned; q itself
+ *                 where q is contiguous
+ *   num_q_heads : 0 for keys and values alone (q and q_out are not read)
+ *   slot_mapping: as kv_reshape_and_cache: a token without a slot (padding) writes no key
+ *                 and value; its query is turned all the same
+ * Errors: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED / PKV_ERR_CUDA.
+ */
+PKV_API int rotary_reshape_and_cache(void *q_out, const void *q, int64_t q_row_stride, int64_t q_head_stride,
+                                     const void *key, int64_t k_row_stride, int64_t k_head_stride, const void *value,
+                                     int64_t v_row_stride, int64_t v_head_stride, void *k_cache, void *v_cache,
+                                     const int32_t *positions, const int32_t *slot_mapping,
+                                     const uint64_t *frequencies, int32_t num_tokens, int32_t num_q_heads,
+                                     int32_t rotary_dim, int32_t layout, float magnitude, const pkv_cache_desc *cache,
+                                     void *stream);
+
+/*
+ * rotary_reshape_and_cache_fp8 -- the same into an FP8 (E4M3) pool, quantised as
+ * kv_reshape_and_cache_fp8 quantises a row, the turned keys from fp32 (not rounded to
+ * bf16 between).
+ */
+PKV_API int rotary_reshape_and_cache_fp8(void *q_out, const void *q, int64_t q_row_stride, int64_t q_head_stride,
+                                         const void *key, int64_t k_row_stride, int64_t k_head_stride,
+                                         const void *value, int64_t v_row_stride, int64_t v_head_stride,
+                                         void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                                         const int32_t *positions, const int32_t *slot_mapping,
+                                         const uint64_t *frequencies, int32_t num_tokens, int32_t num_q_heads,
+                                         int32_t rotary_dim, int32_t layout, float magnitude,
+                                         const pkv_cache_desc *cache, void *stream);
+
+/*
+ * speculative_verify -- which drafted tokens stand, and the token behind them (Leviathan et
+ * al., "Fast Inference from Transformers via Speculative Decoding").  p_i is row
+ * cu_q_lens[b] + i of target_probs: the target's distribution behind node i.  From node 0
+ * on, the children of the current node i are looked at in the order of their numbers.
+ * Child j, token x = tokens[j], u_j = uniforms[j], is accepted when
+ *     u_j q_i(x) < p_i(x)    with draft_probs (q_i: what j was drawn from; chains only)
+ *     u_j r < p_i(x)         without: r = 1 - the p_i of the siblings refused before it (a
+ *                            token that was refused there has no probability left)
+ * and is then the current node.  Where no child is accepted the walk ends, and the last
+ * token is the least v with  w(0) + .. + w(v) > u_0 (sum of w),  w(v) being
+ *     max(p_i(v) - q_i(v), 0)  with draft_probs where a child was refused
+ *     p_i(v)                   else, without draft_probs 0 for the refused children's tokens
+ * and p_i where that is 0 everywhere (should p_i be too, the token is -1).  Products are
+ * exact, sums are kept to 2^-48.  Probabilities that are NaN or below 0 count as 0, above 1
+ * as 1; a draft outside [0, vocab_size), or whose parent is no node before it, is refused.
+ *   tokens_out   : int32 [num_seqs][max_q_len], device: the accepted tokens, the last token, then -1
+ *   path         : int32 [num_seqs][max_q_len], device: 0, the accepted nodes, then -1
+ *   counts       : int32 [num_seqs], device: entries of path and of tokens_out (0 for a
+ *                  sequence without nodes)
+ *   target_probs, draft_probs : fp32, row r at base + r * row_stride, vocab_size values (4-byte
+ *                  aligned; 16-byte aligned rows are read faster); draft_probs may be NULL
+ *   tokens       : int32 [total_q_rows], device (node 0's is not read)
+ *   parents      : int32 [total_q_rows], device: node numbers within the sequence; NULL: chains.
+ *                  Not together with draft_probs (PKV_ERR_UNSUPPORTED)
+ *   uniforms     : fp32 [total_q_rows], device, in [0, 1); node 0's draws the last token
+ *   cu_q_lens    : int32 [num_seqs + 1], device, non-decreasing, from 0
+ *   max_q_len    : host upper bound of the nodes a sequence, 1 .. PKV_MAX_TREE_NODES
+ *   status       : device uint32 into which PKV_STATUS_BAD_Q_LEN is ORed for a sequence whose rows
+ *                  lie outside the tensors or are more than max_q_len (count 0), or NULL
+ *   num_seqs     : 1 .. 65535;  vocab_size : 1 .. 2^24
+ * Errors: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED / PKV_ERR_CUDA.
+ */
+PKV_API int speculative_verify(int32_t *tokens_out, int32_t *path, int32_t *counts, const float *target_probs,
+                               int64_t target_row_stride, const float *draft_probs, int64_t draft_row_stride,
+                               const int32_t *tokens, const int32_t *parents, const float *uniforms,
+                               const int32_t *cu_q_lens, int32_t num_seqs, int32_t max_q_len, int32_t total_q_rows,
+                               int32_t vocab_size, uint32_t *status, void *stream);
+
+/*
+ * kv_compact_path -- the rows of an accepted path moved together.  With n = cu_q_lens[b + 1] -
+ * cu_q_lens[b] nodes and c = context_lens[b] - n (context_lens counts the nodes, as for
+ * paged_attention_tree):  for 0 < i < counts[b], in this order,
+ *     position c + i := position c + path[b][i]   in k_cache, v_cache (and the scales)
+ * path and counts are speculative_verify's (path[i] >= i).  Bit-exact.
+ *   k_scale, v_scale : NULL for a bf16 cache; required for PKV_DTYPE_FP8_E4M3 (16-byte aligned)
+ *   path             : int32 [num_seqs][path_len], device;  path_len : 1 .. PKV_MAX_TREE_NODES
+ *   status           : device uint32 into which PKV_STATUS_* bits are ORed, or NULL
+ * A sequence whose lengths do not fit (more path than nodes, more nodes than context, a
+ * context past its table) moves nothing, a node before its place or past the tree is skipped
+ * (PKV_STATUS_BAD_Q_LEN, _BAD_CONTEXT_LEN), as is one in a block with an invalid id
+ * (PKV_STATUS_BAD_BLOCK_ID).
+ * Errors: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED / PKV_ERR_CUDA.
+ */
+PKV_API int kv_compact_path(void *k_cache, void *v_cache, float *k_scale, float *v_scale, const int32_t *block_tables,
+                            const int32_t *context_lens, const int32_t *cu_q_lens, const int32_t *path,
+                            const int32_t *counts, int32_t num_seqs, int32_t max_blocks_per_seq, int32_t path_len,
+                            const pkv_cache_desc *cache, uint32_t *status, void *stream);
 
 /*
  * ---- Host block manager ---------------------------------------------------------

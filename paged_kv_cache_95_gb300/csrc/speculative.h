@@ -1,0 +1,65 @@
+// speculative.h -- internal interface between speculative_api.cu and the kernels of a
+// speculative decoding step (rotary positions, tree attention, verification, compaction).
+#pragma once
+
+#include "launch.h"
+
+namespace pkv {
+
+// ---- rotary positions ------------------------------------------------------------
+constexpr int kRotaryUnit = 16;  // values a thread turns: 8 pairs
+
+struct RotaryParams {
+    void *out;
+    const void *x;
+    int64_t out_row, out_head, x_row, x_head;  // strides in elements
+    const int32_t *positions;
+    const uint64_t *frequencies;  // [rotary_dim / 2], turns a position in units of 2^-64
+    int32_t num_tokens, num_heads, head_dim, rotary_dim;
+    float magnitude;
+};
+cudaError_t launch_rotary(const RotaryParams &p, bool interleaved, int sm_count, cudaStream_t stream);
+
+struct RotaryWriteParams {
+    void *q_out;  // bf16 [tokens][heads][128]
+    const void *q, *key, *value;
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;  // strides in elements
+    void *k_cache, *v_cache;
+    float *k_scale, *v_scale;  // FP8 pool only
+    const int32_t *positions, *slot_mapping;
+    const uint64_t *frequencies;
+    int64_t num_slots;
+    int32_t num_tokens, n_q, n_kv, rotary_dim;
+    float magnitude;
+};
+cudaError_t launch_rotary_write(const RotaryWriteParams &p, bool interleaved, bool fp8, int sm_count,
+                                cudaStream_t stream);
+
+// ---- verification of drafted tokens, compaction of the accepted path -----------------
+constexpr int kMaxTreeNodes = 64;  // nodes of a sequence's tree: the bits of a mask
+
+struct SpecVerifyParams {
+    int32_t *tokens_out, *path;  // [num_seqs][max_q_len]
+    int32_t *counts;             // [num_seqs]
+    const float *target, *draft;  // rows of vocab probabilities
+    int64_t target_row, draft_row;
+    const int32_t *tokens, *parents, *cu_q_lens;
+    const float *uniforms;
+    uint32_t *status;
+    int32_t num_seqs, max_q_len, total_rows, vocab;
+    int32_t segment;  // vocabulary entries a warp sums
+};
+cudaError_t launch_speculative_verify(const SpecVerifyParams &p, int cluster, cudaStream_t stream);
+constexpr int kVerifyWarps = 16;
+constexpr int kVerifyMaxCluster = 8;
+
+struct CompactParams {
+    void *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    const int32_t *block_tables, *context_lens, *cu_q_lens, *path, *counts;
+    uint32_t *status;
+    int32_t num_seqs, max_blocks, num_blocks, n_kv, path_len;
+};
+cudaError_t launch_kv_compact_path(const CompactParams &p, bool fp8, cudaStream_t stream);
+
+}  // namespace pkv

@@ -36,6 +36,12 @@ PKV_VERIFY_AUTO = -1
 PKV_VERIFY_DECODE_KERNEL = 0
 PKV_VERIFY_PREFILL_KERNEL = 1
 
+PKV_ROTARY_HALF = 0
+PKV_ROTARY_INTERLEAVED = 1
+ROTARY_LAYOUTS = {"half": PKV_ROTARY_HALF, "interleaved": PKV_ROTARY_INTERLEAVED}
+ROTARY_SCALINGS = ("none", "linear", "ntk", "by_parts", "by_wavelength")  # PKV_ROTARY_SCALING_*, in their order
+MAX_TREE_NODES = 64  # PKV_MAX_TREE_NODES
+
 HEAD_DIM = 128
 BLOCK_SIZE = 16
 LATENT_DIM = 512  # latent attention: values of the shared latent a token
@@ -61,6 +67,13 @@ class LatentDesc(ctypes.Structure):
 
     _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32), ("latent_dim", ctypes.c_int32),
                 ("rope_dim", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class RotaryScaling(ctypes.Structure):
+    """Mirror of ``pkv_rotary_scaling``."""
+
+    _fields_ = [("kind", ctypes.c_int32), ("original_length", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
 
 
 class PagedKVError(RuntimeError):
@@ -156,6 +169,20 @@ def _declare(lib):
     lib.latent_attention_prefill_chunk.argtypes = [P, i32, P, i64, i64, P, P, i64, i64, P, i64, P, P, i32, i32, i32,
                                                    i32, i32, f32, P, sz, P]
     lib.latent_attention_prefill_chunk.restype = I
+    lib.rotary_frequencies.argtypes = [P, P, i32, ctypes.c_double, ctypes.POINTER(RotaryScaling)]
+    lib.rotary_frequencies.restype = I
+    lib.rotary_embedding.argtypes = [P, i64, i64, P, i64, i64, P, P, i32, i32, i32, i32, i32, f32, P]
+    lib.rotary_embedding.restype = I
+    lib.rotary_reshape_and_cache.argtypes = [P, P, i64, i64, P, i64, i64, P, i64, i64, P, P, P, P, P, i32, i32, i32, i32,
+                                             f32, D, P]
+    lib.rotary_reshape_and_cache.restype = I
+    lib.rotary_reshape_and_cache_fp8.argtypes = [P, P, i64, i64, P, i64, i64, P, i64, i64, P, P, P, P, P, P, P, i32, i32,
+                                                 i32, i32, f32, D, P]
+    lib.rotary_reshape_and_cache_fp8.restype = I
+    lib.speculative_verify.argtypes = [P, P, P, P, i64, P, i64, P, P, P, P, i32, i32, i32, i32, P, P]
+    lib.speculative_verify.restype = I
+    lib.kv_compact_path.argtypes = [P, P, P, P, P, P, P, P, P, i32, i32, i32, D, P, P]
+    lib.kv_compact_path.restype = I
     lib.pkv_bm_create.argtypes = [i32, ctypes.POINTER(P)]
     lib.pkv_bm_create.restype = I
     lib.pkv_bm_destroy.argtypes = [P]
@@ -769,7 +796,7 @@ def _device_and_stream(stream):
     global _cuda_started
     torch = _torch()
     if not _cuda_started:
-        _need(torch.cuda.is_available(), "the latent entry points need a CUDA device")
+        _need(torch.cuda.is_available(), "the entry points need a CUDA device")
         torch.cuda.init()
         _cuda_started = True
     device = torch._C._cuda_getDevice()
@@ -952,3 +979,202 @@ def latent_attention_prefill_chunk(out, q, k_nope, v, k_rope, cu_q_lens, cu_k_le
                                             stream)
     _raise("latent_attention_prefill_chunk", rc)
     return workspace
+
+
+# ---- a step of speculative decoding --------------------------------------------------
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       original_length: int = 0, low: float = 1.0, high: float = 32.0, device=None):
+    """The angles per position of a head's rotated pairs, as the rotary entry points take them
+    (int64 tensor [rotary_dim / 2]: turns in units of 2^-64), and the magnitude that goes with
+    them.  ``scaling``: "none", "linear", "ntk", "by_parts" (with ``original_length`` and the
+    turns ``low`` and ``high`` over it) or "by_wavelength" (the same).  ``device``: the current
+    CUDA device if None ("cpu" needs no GPU)."""
+    torch = _torch()
+    _need(scaling in ROTARY_SCALINGS, f"scaling must be one of {ROTARY_SCALINGS}, got {scaling!r}")
+    _need(int(rotary_dim) >= 2, "rotary_dim must be at least 2")
+    freqs = torch.zeros(int(rotary_dim) // 2, dtype=torch.int64)
+    magnitude = ctypes.c_float()
+    how = RotaryScaling(ROTARY_SCALINGS.index(scaling), int(original_length), float(factor), float(low), float(high))
+    rc = load_library().rotary_frequencies(freqs.data_ptr(), ctypes.byref(magnitude), int(rotary_dim), float(base),
+                                           ctypes.byref(how))
+    _raise("rotary_frequencies", rc)
+    return freqs.to("cuda" if device is None else device), magnitude.value
+
+
+def _turn(positions, frequencies, layout, tokens, device):
+    """(positions, frequencies, rotary_dim, layout) as the ABI takes them."""
+    torch = _torch()
+    (n,), pos = _flat(positions, "positions", torch.int32, 1, device)
+    if n != tokens:
+        raise ValueError("one position per token")
+    (pairs,), freqs = _flat(frequencies, "frequencies", torch.int64, 1, device)
+    code = ROTARY_LAYOUTS.get(layout)
+    if code is None:
+        raise ValueError(f"layout must be one of {tuple(ROTARY_LAYOUTS)}, got {layout!r}")
+    return pos, freqs, 2 * pairs, code
+
+
+def rotary_embedding(out, x, positions, frequencies, layout: str = "half", magnitude: float = 1.0, stream=None) -> None:
+    """Turn the first 2 * len(frequencies) values of every head of ``x`` (bf16 [tokens, heads,
+    head_dim], tokens and heads may be strided) to its token's position (int32 [tokens]) into
+    ``out`` (the same shape; ``x`` itself for in place).  ``layout``: pairs (i, i + half) or
+    interleaved (2 i, 2 i + 1).  ``frequencies`` and ``magnitude``: :func:`rotary_frequencies`."""
+    device, stream = _device_and_stream(stream)
+    width = x.shape[-1] if getattr(x, "shape", None) else 0
+    (tokens, heads, dim), xs, x_at = _rows(x, "x", 3, width, device)
+    shape, outs, out_at = _rows(out, "out", 3, width, device)
+    if shape != (tokens, heads, dim):
+        raise ValueError("out must have x's shape")
+    pos, freqs, rotary, code = _turn(positions, frequencies, layout, tokens, device)
+    rc = (_lib or load_library()).rotary_embedding(out_at, outs[0], outs[1], x_at, xs[0], xs[1], pos, freqs, tokens, heads,
+                                                   dim, rotary, code, magnitude, stream)
+    _raise("rotary_embedding", rc)
+
+
+@functools.lru_cache(maxsize=64)
+def _cache_desc(blocks, kv, slots, dtype):
+    return ctypes.byref(CacheDesc(blocks, slots, kv, HEAD_DIM, dtype))
+
+
+def _kv_pool(k_cache, v_cache, k_scale, v_scale, device):
+    """(descriptor, FP8, KV heads, addresses of the K and V caches and their scales)."""
+    torch = _torch()
+    dtype = getattr(k_cache, "dtype", None)
+    fp8 = dtype is torch.uint8 or dtype is torch.float8_e4m3fn
+    dtype = dtype if fp8 else torch.bfloat16
+    shape, k = _flat(k_cache, "k_cache", dtype, 4, device)
+    v_shape, v = _flat(v_cache, "v_cache", dtype, 4, device)
+    if shape[3] != HEAD_DIM or v_shape != shape:
+        raise ValueError("k_cache and v_cache must be [num_blocks, n_kv, 16, 128]")
+    if fp8 != (k_scale is not None) or fp8 != (v_scale is not None):
+        raise ValueError("k_scale and v_scale are required for an FP8 cache and not allowed otherwise")
+    blocks, kv, slots, _ = shape
+    if not fp8:
+        return _cache_desc(blocks, kv, slots, PKV_DTYPE_BF16), False, kv, k, v, None, None
+    ks_shape, ks = _flat(k_scale, "k_scale", torch.float32, 3, device)
+    vs_shape, vs = _flat(v_scale, "v_scale", torch.float32, 3, device)
+    if ks_shape != shape[:3] or vs_shape != shape[:3]:
+        raise ValueError("k_scale and v_scale must be [num_blocks, n_kv, 16]")
+    return _cache_desc(blocks, kv, slots, PKV_DTYPE_FP8_E4M3), True, kv, k, v, ks, vs
+
+
+def _rotary_write(fp8, q_out, q, key, value, k_cache, v_cache, k_scale, v_scale, positions, slot_mapping, frequencies,
+                  layout, magnitude, stream):
+    torch = _torch()
+    device, stream = _device_and_stream(stream)
+    desc, is_fp8, kv, k_at, v_at, ks, vs = _kv_pool(k_cache, v_cache, k_scale, v_scale, device)
+    if is_fp8 != fp8:
+        raise ValueError("rotary_reshape_and_cache takes bf16 caches, rotary_reshape_and_cache_fp8 E4M3 codes")
+    (tokens,), slots = _flat(slot_mapping, "slot_mapping", torch.int32, 1, device)
+    k_shape, k_strides, key_at = _rows(key, "key", 3, HEAD_DIM, device)
+    v_shape, v_strides, value_at = _rows(value, "value", 3, HEAD_DIM, device)
+    if k_shape != (tokens, kv, HEAD_DIM) or v_shape != k_shape:
+        raise ValueError("key and value must be [num_tokens, n_kv, 128]")
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        heads, q_at, q_strides, out_at = 0, None, (0, 0), None
+    else:
+        (n, heads, _), q_strides, q_at = _rows(q, "q", 3, HEAD_DIM, device)
+        shape, out_at = _flat(q_out, "q_out", torch.bfloat16, 3, device)
+        if n != tokens or shape != (tokens, heads, HEAD_DIM):
+            raise ValueError("q and q_out must be [num_tokens, n_q, 128]")
+    pos, freqs, rotary, code = _turn(positions, frequencies, layout, tokens, device)
+    lib = _lib or load_library()
+    head = (out_at, q_at, q_strides[0], q_strides[1], key_at, k_strides[0], k_strides[1], value_at, v_strides[0],
+            v_strides[1], k_at, v_at)
+    tail = (pos, slots, freqs, tokens, heads, rotary, code, magnitude, desc, stream)
+    if fp8:
+        _raise("rotary_reshape_and_cache_fp8", lib.rotary_reshape_and_cache_fp8(*head, ks, vs, *tail))
+    else:
+        _raise("rotary_reshape_and_cache", lib.rotary_reshape_and_cache(*head, *tail))
+
+
+def rotary_reshape_and_cache(q_out, q, key, value, k_cache, v_cache, positions, slot_mapping, frequencies,
+                             layout: str = "half", magnitude: float = 1.0, stream=None) -> None:
+    """Turn ``q`` [tokens, n_q, 128] into ``q_out`` (contiguous; ``q`` itself where it is) and
+    ``key`` [tokens, n_kv, 128] into the bf16 pool, and append ``value``, through
+    ``slot_mapping``; q, key and value may be slices of wider rows.  ``q`` and ``q_out`` None:
+    keys and values alone."""
+    _rotary_write(False, q_out, q, key, value, k_cache, v_cache, None, None, positions, slot_mapping, frequencies, layout,
+                  magnitude, stream)
+
+
+def rotary_reshape_and_cache_fp8(q_out, q, key, value, k_cache, v_cache, k_scale, v_scale, positions, slot_mapping,
+                                 frequencies, layout: str = "half", magnitude: float = 1.0, stream=None) -> None:
+    """The same into an FP8 pool: the turned keys and the values as E4M3 codes with one fp32
+    scale per token and head."""
+    _rotary_write(True, q_out, q, key, value, k_cache, v_cache, k_scale, v_scale, positions, slot_mapping, frequencies,
+                  layout, magnitude, stream)
+
+
+def _probabilities(t, name, rows, device):
+    """(vocabulary, row stride, address) of fp32 rows whose values are contiguous."""
+    torch = _torch()
+    try:
+        shape, strides = t.shape, t.stride()
+        if (t.dtype is torch.float32 and len(shape) == 2 and shape[0] == rows and t.get_device() == device
+                and (strides[1] == 1 or shape[1] == 1)):
+            return shape[1], strides[0] if shape[0] > 1 else shape[1], t.data_ptr()
+    except AttributeError:
+        pass
+    raise ValueError(f"{name} must be float32 [total_rows, vocab] on the current CUDA device, its rows contiguous")
+
+
+def speculative_verify(tokens_out, path, counts, target_probs, tokens, cu_q_lens, max_q_len: int, uniforms, parents=None,
+                       draft_probs=None, status=None, stream=None) -> None:
+    """Accept drafted tokens against the target's probabilities with given random numbers, and
+    draw the token behind them.  ``target_probs`` fp32 [total_rows, vocab], ``tokens`` int32
+    [total_rows], ``uniforms`` fp32 [total_rows], a row per node; ``parents`` int32 [total_rows]
+    (None: chains) or ``draft_probs`` like ``target_probs`` (chains: what each node's child was
+    drawn from).  Results: ``tokens_out`` and ``path`` int32 [num_seqs, max_q_len] (padded with
+    -1) and ``counts`` int32 [num_seqs]."""
+    torch = _torch()
+    device, stream = _device_and_stream(stream)
+    (n,), cu = _flat(cu_q_lens, "cu_q_lens", torch.int32, 1, device)
+    B, most = n - 1, int(max_q_len)
+    out_shape, out_at = _flat(tokens_out, "tokens_out", torch.int32, 2, device)
+    path_shape, path_at = _flat(path, "path", torch.int32, 2, device)
+    (m,), counts_at = _flat(counts, "counts", torch.int32, 1, device)
+    if out_shape != (B, most) or path_shape != out_shape or m != B:
+        raise ValueError("tokens_out and path must be [num_seqs, max_q_len], counts [num_seqs]")
+    (rows,), tokens_at = _flat(tokens, "tokens", torch.int32, 1, device)
+    (m,), u = _flat(uniforms, "uniforms", torch.float32, 1, device)
+    if m != rows:
+        raise ValueError("one uniform per row")
+    vocab, stride, target = _probabilities(target_probs, "target_probs", rows, device)
+    draft, draft_stride, up = None, 0, None
+    if draft_probs is not None:
+        width, draft_stride, draft = _probabilities(draft_probs, "draft_probs", rows, device)
+        if width != vocab:
+            raise ValueError("draft_probs must have target_probs' shape")
+    if parents is not None:
+        (m,), up = _flat(parents, "parents", torch.int32, 1, device)
+        if m != rows:
+            raise ValueError("one parent per row")
+    status_at = None if status is None else _flat(status, "status", torch.int32, 1, device)[1]
+    rc = (_lib or load_library()).speculative_verify(out_at, path_at, counts_at, target, stride, draft, draft_stride,
+                                                     tokens_at, up, u, cu, B, most, rows, vocab, status_at, stream)
+    _raise("speculative_verify", rc)
+
+
+def kv_compact_path(k_cache, v_cache, block_tables, context_lens, cu_q_lens, path, counts, k_scale=None, v_scale=None,
+                    status=None, stream=None) -> None:
+    """Move the accepted path's rows to consecutive places: position c + path[b, i] to c + i for
+    0 < i < counts[b], c = context_lens[b] less the sequence's nodes, in both caches (and, for an
+    FP8 cache, in both scale arrays).  ``path`` and ``counts``: :func:`speculative_verify`."""
+    torch = _torch()
+    device, stream = _device_and_stream(stream)
+    desc, _, _, k_at, v_at, ks, vs = _kv_pool(k_cache, v_cache, k_scale, v_scale, device)
+    (B, max_blocks), tables = _flat(block_tables, "block_tables", torch.int32, 2, device)
+    (n,), lens = _flat(context_lens, "context_lens", torch.int32, 1, device)
+    (m,), cu = _flat(cu_q_lens, "cu_q_lens", torch.int32, 1, device)
+    (rows, width), path_at = _flat(path, "path", torch.int32, 2, device)
+    (c,), counts_at = _flat(counts, "counts", torch.int32, 1, device)
+    if n != B or m != B + 1 or rows != B or c != B:
+        raise ValueError("context_lens, path and counts must have a row per sequence, cu_q_lens one more")
+    status_at = None if status is None else _flat(status, "status", torch.int32, 1, device)[1]
+    rc = (_lib or load_library()).kv_compact_path(k_at, v_at, ks, vs, tables, lens, cu, path_at, counts_at, B, max_blocks,
+                                                  width, desc, status_at, stream)
+    _raise("kv_compact_path", rc)
