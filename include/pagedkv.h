@@ -896,6 +896,44 @@ PKV_API int rotary_reshape_and_cache_fp8(void *q_out, const void *q, int64_t q_r
                                          const pkv_cache_desc *cache, void *stream);
 
 /*
+ * paged_attention_tree -- attention of every node of a tree over the cached tokens and the
+ * nodes that its mask names.  Sequence b has n = cu_q_lens[b + 1] - cu_q_lens[b] nodes, whose K
+ * and V are the last n of its ctx = context_lens[b] positions; with c = ctx - n, row
+ * cu_q_lens[b] + i sees the keys j < c, and of those behind them the keys c + j whose bit j
+ * of tree_mask[row] is set (of a tree: the node's ancestors and the node itself; any mask will
+ * do):
+ *     s_j = scale * <q[row][h], K_b[j][g]>,   out[row][h] = sum_j softmax(s)_j V_b[j][g]
+ * n = 1 with bit 0 is a decode row, masks of all lower bits are paged_attention_verify.
+ *   out        : out_dtype [total_q_rows][num_q_heads][128], device, 16-byte aligned; rows from
+ *                cu_q_lens[num_seqs] on are left as they were
+ *   q          : bf16 [total_q_rows][num_q_heads][128], device, 16-byte aligned
+ *   tree_mask  : uint64 [total_q_rows], device, 8-byte aligned; bits from n on are not looked at
+ *   cu_q_lens  : int32 [num_seqs + 1], device, non-decreasing, from 0
+ *   max_q_len  : host upper bound of the nodes a sequence, 1 .. PKV_MAX_TREE_NODES
+ *   k_cache, v_cache, k_scale, v_scale : a bf16 pool (scales NULL) or an FP8 (E4M3) pool, as cache->dtype
+ *                says; attention is over code * scale
+ *   num_q_heads: any multiple of cache->num_kv_heads (to 65536)
+ *   workspace  : 256-byte aligned, paged_attention_tree_workspace_size() bytes (for the current
+ *                device; 152 SMs are assumed without a GPU), status word zeroed once (it is
+ *                sticky); calls that share it must not overlap
+ * A row that sees no key is zero.  A sequence with ctx < 1 or past its table
+ * (PKV_STATUS_BAD_CONTEXT_LEN), ctx < n or n > max_q_len (PKV_STATUS_BAD_Q_LEN) gets zero rows; one whose
+ * rows lie outside the tensors none (PKV_STATUS_BAD_Q_LEN).  A block with an invalid id
+ * contributes nothing (PKV_STATUS_BAD_BLOCK_ID).  Slots that belong to no key may hold anything; a
+ * node whose V is not finite may make rows NaN that do not see it (a weight of 0 times it).
+ * Errors: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED /
+ *         PKV_ERR_WORKSPACE_TOO_SMALL / PKV_ERR_CUDA.
+ */
+PKV_API size_t paged_attention_tree_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t max_q_len,
+                                                   const pkv_cache_desc *cache);
+PKV_API int paged_attention_tree(void *out, int32_t out_dtype, const void *q, const uint64_t *tree_mask,
+                                 const int32_t *cu_q_lens, int32_t max_q_len, int32_t total_q_rows, const void *k_cache,
+                                 const void *v_cache, const float *k_scale, const float *v_scale,
+                                 const int32_t *block_tables, const int32_t *context_lens, int32_t num_seqs,
+                                 int32_t num_q_heads, int32_t max_blocks_per_seq, float scale,
+                                 const pkv_cache_desc *cache, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * speculative_verify -- which drafted tokens stand, and the token behind them (Leviathan et
  * al., "Fast Inference from Transformers via Speculative Decoding").  p_i is row
  * cu_q_lens[b] + i of target_probs: the target's distribution behind node i.  From node 0

@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libpagedkv.so")
 SOURCES = ["api.cu", "cache_write.cu", "decode.cu", "prefill.cu", "latent_api.cu", "latent_cache.cu",
-           "latent_decode.cu", "latent_prefill.cu", "speculative_api.cu", "rotary.cu", "speculate.cu",
+           "latent_decode.cu", "latent_prefill.cu", "speculative_api.cu", "rotary.cu", "tree_attention.cu", "speculate.cu",
            "block_manager.cpp"]
 HEADERS = ["launch.h", "latent.h", "speculative.h", "tensor_map.h", "ptx.cuh", "decode_core.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -35,9 +35,30 @@ struct RotaryWriteParams {
 cudaError_t launch_rotary_write(const RotaryWriteParams &p, bool interleaved, bool fp8, int sm_count,
                                 cudaStream_t stream);
 
-// ---- verification of drafted tokens, compaction of the accepted path -----------------
+// ---- attention of a tree's rows over the cache ---------------------------------------
 constexpr int kMaxTreeNodes = 64;  // nodes of a sequence's tree: the bits of a mask
 
+struct TreeParams {
+    const void *q;  // bf16 [total_rows][n_q][128]
+    void *out;      // [total_rows][n_q][128], f32 or bf16
+    const uint64_t *mask;  // [total_rows]
+    const int32_t *cu_q_lens, *block_tables, *context_lens;
+    const void *v_cache;             // (K comes by its tensor map)
+    const float *k_scale, *v_scale;  // FP8 pool only
+    uint32_t *status;
+    int32_t num_seqs, n_q, n_kv, group, max_blocks, num_blocks, total_rows, max_q_len;
+    float scale_log2;
+    int32_t out_bf16;
+    // The split: all (sequence, KV head, 128-row tile) units' key tiles in `ranges` equal ranges, one a CTA.
+    int32_t ranges, part_rows;  // part_rows: rows of a partial (the most a row tile holds)
+    int4 *record;               // [ranges]: the split unit that begins in the range (sequence, unit, parts; 0 parts: none)
+    float2 *part_ml;            // [ranges][2][part_rows] (m, l), log2 domain, scale folded in
+    float *part_o;              // the same x [128], unnormalised
+};
+cudaError_t tree_prepare_device();
+cudaError_t launch_tree_attention(const CUtensorMap &kmap, const TreeParams &p, bool fp8, cudaStream_t stream);
+
+// ---- verification of drafted tokens, compaction of the accepted path -----------------
 struct SpecVerifyParams {
     int32_t *tokens_out, *path;  // [num_seqs][max_q_len]
     int32_t *counts;             // [num_seqs]

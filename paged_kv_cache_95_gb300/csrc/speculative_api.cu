@@ -8,6 +8,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/pagedkv.h"
 #include "speculative.h"
@@ -55,6 +56,49 @@ int check_rotation(int32_t head_dim, int32_t rotary_dim, int32_t layout, float m
     if (head_dim % pkv::kRotaryUnit != 0 || rotary_dim % pkv::kRotaryUnit != 0) return PKV_ERR_UNSUPPORTED;
     return PKV_OK;
 }
+
+// The softmax scale in the log2 domain, which has to be finite too.
+bool log2_scale(float scale, float *out) {
+    *out = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    return std::isfinite(*out);
+}
+
+constexpr size_t kStatusBytes = 256;
+constexpr int kDefaultSms = 152;  // sizes asked for without a GPU
+// Lengths that the kernels may round up to whole tiles within 32 bits.
+constexpr int64_t kMaxLength = INT32_MAX - 4096;
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Tree attention: one range of key tiles for each SM.  Workspace: [status 256 B | records | part_ml | part_o].
+struct TreePlan {
+    int32_t ranges, part_rows;
+    size_t off_ml, off_o, total;
+};
+TreePlan plan_tree(int32_t group, int32_t max_q_len, int sms) {
+    TreePlan pl{};
+    pl.ranges = sms;
+    pl.part_rows = static_cast<int32_t>(std::min<int64_t>(128, static_cast<int64_t>(group) * max_q_len));
+    const size_t rows = static_cast<size_t>(pl.ranges) * 2 * pl.part_rows;
+    pl.off_ml = kStatusBytes + align_up(static_cast<size_t>(pl.ranges) * 16, 256);
+    pl.off_o = pl.off_ml + align_up(rows * 8, 256);
+    pl.total = pl.off_o + rows * kHeadDim * 4;
+    return pl;
+}
+
+int check_tree_sizes(int32_t num_seqs, int32_t num_q_heads, int32_t max_q_len, const pkv_cache_desc *cache) {
+    const bool fp8 = cache && cache->dtype == PKV_DTYPE_FP8_E4M3;
+    if (int rc = check_pool(cache, fp8)) return rc;
+    if (num_seqs < 1 || num_seqs > 65535 || max_q_len < 1 || max_q_len > PKV_MAX_TREE_NODES) return PKV_ERR_INVALID_ARG;
+    if (num_q_heads < 1 || num_q_heads % cache->num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
+    if (num_q_heads > 65536) return PKV_ERR_UNSUPPORTED;
+    // K/V tiles are addressed by the 32-bit index block * n_kv + head.
+    if (static_cast<int64_t>(cache->num_blocks) * cache->num_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+std::once_flag g_tree_prepared[kMaxDevices];
+cudaError_t g_tree_prep_err[kMaxDevices];
 
 int finish(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
 
@@ -224,6 +268,74 @@ int rotary_reshape_and_cache_fp8(void *q_out, const void *q, int64_t q_row_strid
     return rotary_write(q_out, q, q_row_stride, q_head_stride, key, k_row_stride, k_head_stride, value, v_row_stride,
                         v_head_stride, k_cache, v_cache, k_scale, v_scale, positions, slot_mapping, frequencies,
                         num_tokens, num_q_heads, rotary_dim, layout, magnitude, cache, true, stream);
+}
+
+size_t paged_attention_tree_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t max_q_len,
+                                           const pkv_cache_desc *cache) {
+    if (check_tree_sizes(num_seqs, num_q_heads, max_q_len, cache) != PKV_OK) return 0;
+    const int sms = current_sms();
+    return plan_tree(num_q_heads / cache->num_kv_heads, max_q_len, sms > 0 ? sms : kDefaultSms).total;
+}
+
+int paged_attention_tree(void *out, int32_t out_dtype, const void *q, const uint64_t *tree_mask, const int32_t *cu_q_lens,
+                         int32_t max_q_len, int32_t total_q_rows, const void *k_cache, const void *v_cache,
+                         const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                         const int32_t *context_lens, int32_t num_seqs, int32_t num_q_heads, int32_t max_blocks_per_seq,
+                         float scale, const pkv_cache_desc *cache, void *workspace, size_t workspace_bytes, void *stream) {
+    if (int rc = check_tree_sizes(num_seqs, num_q_heads, max_q_len, cache)) return rc;
+    const bool fp8 = cache->dtype == PKV_DTYPE_FP8_E4M3;
+    if (out_dtype != PKV_DTYPE_FLOAT32 && out_dtype != PKV_DTYPE_BF16) return PKV_ERR_UNSUPPORTED;
+    if (total_q_rows < 0 || max_blocks_per_seq < 1 || static_cast<int64_t>(max_blocks_per_seq) * kBlockSize > kMaxLength)
+        return PKV_ERR_INVALID_ARG;
+    pkv::TreeParams p{};
+    if (!log2_scale(scale, &p.scale_log2)) return PKV_ERR_INVALID_ARG;
+    if (total_q_rows == 0) return PKV_OK;
+    if (!out || !q || !tree_mask || !cu_q_lens || !k_cache || !v_cache || !block_tables || !context_lens)
+        return PKV_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(tree_mask, 8) || !aligned(cu_q_lens, 4) || !aligned(k_cache, 16) ||
+        !aligned(v_cache, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4))
+        return PKV_ERR_INVALID_ARG;
+    if (fp8 ? (!k_scale || !v_scale || !aligned(k_scale, 16) || !aligned(v_scale, 16)) : (k_scale || v_scale))
+        return PKV_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256)) return PKV_ERR_INVALID_ARG;
+    if (workspace_bytes < paged_attention_tree_workspace_size(num_seqs, num_q_heads, max_q_len, cache))
+        return PKV_ERR_WORKSPACE_TOO_SMALL;
+    const int sms = current_sms(), dev = current_device();
+    if (sms < 1) return PKV_ERR_CUDA;
+    std::call_once(g_tree_prepared[dev], [&] { g_tree_prep_err[dev] = pkv::tree_prepare_device(); });
+    if (g_tree_prep_err[dev] != cudaSuccess) return PKV_ERR_CUDA;
+    const int32_t n_kv = cache->num_kv_heads;
+    CUtensorMap kmap;
+    if (!(fp8 ? pkv::encode_pool_map_fp8(&kmap, k_cache, cache->num_blocks, n_kv)
+              : pkv::encode_pool_tile_map(&kmap, k_cache, cache->num_blocks, n_kv)))
+        return PKV_ERR_CUDA;
+    const TreePlan pl = plan_tree(num_q_heads / n_kv, max_q_len, sms);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.q = q;
+    p.out = out;
+    p.mask = tree_mask;
+    p.cu_q_lens = cu_q_lens;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.status = reinterpret_cast<uint32_t *>(ws);
+    p.num_seqs = num_seqs;
+    p.n_q = num_q_heads;
+    p.n_kv = n_kv;
+    p.group = num_q_heads / n_kv;
+    p.max_blocks = max_blocks_per_seq;
+    p.num_blocks = cache->num_blocks;
+    p.total_rows = total_q_rows;
+    p.max_q_len = max_q_len;
+    p.out_bf16 = out_dtype == PKV_DTYPE_BF16;
+    p.ranges = pl.ranges;
+    p.part_rows = pl.part_rows;
+    p.record = reinterpret_cast<int4 *>(ws + kStatusBytes);
+    p.part_ml = reinterpret_cast<float2 *>(ws + pl.off_ml);
+    p.part_o = reinterpret_cast<float *>(ws + pl.off_o);
+    return finish(pkv::launch_tree_attention(kmap, p, fp8, static_cast<cudaStream_t>(stream)));
 }
 
 int speculative_verify(int32_t *tokens_out, int32_t *path, int32_t *counts, const float *target_probs,

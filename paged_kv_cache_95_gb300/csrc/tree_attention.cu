@@ -1,0 +1,1024 @@
+// tree_attention.cu -- attention of a tree of drafted tokens over the paged cache, on the
+// 5th-generation tensor cores (tcgen05.mma, accumulators in tensor memory).
+//
+// Sequence b has n nodes whose K and V stand behind its c = ctx - n cached tokens.  Node i's
+// row of head h sees the keys j < c and the nodes j - c whose bits are set in its mask:
+//     s_j = scale <q[i][h], K_j,g>,  g = floor(h / G),   out[i][h] = sum softmax(s)_j V_j,g
+//
+// Every row of a (sequence, KV head) sees the same prefix, so the G heads of its n nodes are the
+// rows of one MMA tile (row r = node r / G, head r % G; 128 rows, more in several tiles) and
+// each K and V tile is read once for all of them: HBM bound up to 128 rows.  Masks touch
+// the last key tiles only: a thread holds a row, its mask shifted to a key chunk gives the
+// chunk's 32 visible bits.
+//
+// Split.  The units (sequence, KV head, row tile) have as many key tiles (64 keys) as their
+// sequence; all tiles in this order are cut into equal ranges, one for each SM's one CTA (the
+// lengths are device data: every CTA finds its range from them).  A CTA walks the pieces of
+// units in its range; a unit that lies in several ranges leaves (m, l, O) partials, which
+// a second kernel joins.
+//
+// A CTA's warps (hand-offs through mbarriers, every wait bounded):
+//  * 8 fetches K by TMA (one copy for each of a tile's four paged blocks); 12 and 13 fetch V by
+//    16-byte asynchronous copies: one SM's TMA unit delivers 24 bytes a clock, HBM's share of an SM
+//    is 23-28, so a ring on TMA alone never catches up.  The rings run ahead of the pieces.  V rows
+//    of keys that are not the sequence's, or of blocks with an invalid id, come as zeros.
+//  * 11 plans the CTA's range and fetches the pieces' Q rows (any G); pieces of up to 64 rows have
+//    two places for them in turn.  The next piece's rows are on their way into L2 meanwhile (behind
+//    two full rings a read from HBM takes 5 us).
+//  * 9 issues S = Q K^T, 10 P V (run whole, one elected lane issues: descriptors stay in uniform
+//    registers; one warp for both took 3500 cycles for 128 keys, of which HBM leaves 2800).  Tensor
+//    memory: S of tile j in [64 (j & 3), +64), O of the even and of the odd tiles in [256, +128) and
+//    [384, +128).  With four places for S the next scores are there when a tile's weights are
+//    done (with tiles of 128 keys in two places a tile waited for the P V of the one before
+//    it: 3400 cycles for 128 keys).
+//  * 0-3 and 4-7 are two groups of softmax threads, for the even and the odd tiles; thread r of
+//    a group holds row r: maximum, weights 2^(s - m) and their sum need no exchange.  The
+//    exponent reference m is raised when a maximum passes it by more than 2^8 (then the row's O is
+//    rescaled).  P goes back over S as bf16 heads (truncated) and remainders (rounded), P V =
+//    P_hi V + P_lo V: weights to 2^-16.  At a piece's end the groups' (m, l, O) are joined, each
+//    group storing half of the values.
+//  * Keys past ctx and of blocks with an invalid id are masked by index, so stale bytes reach no
+//    result.
+//
+// FP8 pool (E4M3 codes, one scale per key and head).  K's codes are the B operand as they are; a row of Q
+// is two rows of E4M3 codes, what the first leaves in the second, scaled by the power of two that
+// puts the row's largest value in [2^7, 2^8): exact down to 2^-9 of that value, 2^-17 of it below.
+// 12-15 take every fourth tile of V each: its codes by asynchronous copies, expanded to bf16
+// (exact) into the V ring.  K's scale multiplies the scores, V's the weights that enter P V.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "ptx.cuh"
+#include "speculative.h"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kRows = 128;         // of a row tile
+constexpr int kKeys = 64;          // of a tile
+constexpr int kTileBlocks = kKeys / kBlockSize;
+constexpr int kGroupWarps = 4;     // softmax warps of a group
+constexpr int kPlaces = 4;         // of S in tensor memory
+constexpr int kWarpK = 8, kWarpS = 9, kWarpPv = 10, kWarpQ = 11, kWarpV = 12;
+
+constexpr uint32_t kHalfTile = kRows * 128;      // 16 KB: 128 rows x 128 bytes
+constexpr uint32_t kVTile = kKeys * 256;         // 16 KB: 64 bf16 rows of V
+constexpr uint32_t kBlkBytes = 4096;             // one paged (block, head) tile of bf16 values
+constexpr uint32_t kCodeBytes = 2048;            // the same of codes
+constexpr uint32_t kTmemCols = 512, kTmemO = 256;
+
+template <bool FP8>
+struct Layout {
+    static constexpr int kCopyWarps = FP8 ? 4 : 2;  // that fetch V
+    static constexpr int kThreads = (kWarpV + kCopyWarps) * 32;
+    static constexpr int kStagesK = 6, kStagesV = FP8 ? 4 : 6;
+    static constexpr int kRaw = 2;         // FP8: tiles of codes that a copying warp has on their way
+    static constexpr int kScaleTiles = 16;  // FP8: places of a tile's scales (its reader is behind by less than 12 tiles)
+    static constexpr uint32_t kBlk = FP8 ? kCodeBytes : kBlkBytes;  // of the pool
+    static constexpr uint32_t kKTile = kTileBlocks * kBlk;
+    static constexpr uint32_t kOffQ = 0;  // [value half][128 rows][128 B], FP8: [codes, remainders' codes][128 rows][128 B]
+    static constexpr uint32_t kOffK = kOffQ + 2 * kHalfTile;
+    static constexpr uint32_t kOffV = kOffK + kStagesK * kKTile;
+    static constexpr uint32_t kOffRaw = kOffV + kStagesV * kVTile;  // FP8: [copying warp][kRaw] tiles of codes
+    static constexpr uint32_t kOffScale = kOffRaw + (FP8 ? kCopyWarps * kRaw * kTileBlocks * kCodeBytes : 0);  // [K, V][64]
+    static constexpr uint32_t kOffRow = kOffScale + (FP8 ? kScaleTiles * 2 * kKeys * 4 : 0);  // FP8: factors of Q's rows, two places
+    static constexpr uint32_t kOffMl = kOffRow + (FP8 ? 2 * kRows * 4 : 0);  // (m, l) of the groups' rows
+    static constexpr uint32_t kOffBar = kOffMl + 2 * kRows * 8;
+    static constexpr int kBars = 2 * kStagesK + 2 * kStagesV + 4 + 3 * kPlaces + 3;
+    static constexpr uint32_t kOffPlan = kOffBar + 8 * kBars;
+    static constexpr uint32_t kBytes = kOffPlan + 64;
+    static_assert(kBytes <= 232448, "shared memory of a CTA");
+    static_assert(kOffK % 1024 == 0 && kKTile % 1024 == 0 && kOffV % 1024 == 0 && kOffPlan % 8 == 0, "alignment");
+};
+
+// Instruction descriptors: D f32; M = 128, N = 64 (S) or 128 (P V).
+constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((64u >> 3) << 17) | ((128u >> 4) << 24);  // bf16
+constexpr uint32_t kIdescS8 = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);                         // E4M3
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);  // V MN-major
+
+// Shared-memory matrix descriptor for a 128-byte-swizzled canonical layout.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Whether the phase with the given parity is complete, at once.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// 16 bytes asynchronously, or zeros.
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+                 "r"(valid ? 16 : 0)
+                 : "memory");
+}
+
+// P - head for a pair, head = the packed bf16 pair `h`: exact, since head is P truncated.
+__device__ __forceinline__ float2 minus_bf16x2(float2 p, uint32_t h) {
+    float2 d;
+    asm("{\n\t.reg .b16 lo, hi, m;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b16 m, 0xBF80;\n\t"
+        "fma.rn.f32.bf16 %0, lo, m, %3;\n\tfma.rn.f32.bf16 %1, hi, m, %4;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "r"(h), "f"(p.x), "f"(p.y));
+    return d;
+}
+
+// A sequence as the split sees it (device data: checked).  units is 0 for one without rows, or whose
+// rows lie outside the tensors; one whose lengths do not fit has one tile that no row sees, so its rows become zeros.
+struct Sequence {
+    int row0, n, ctx, row_tiles, units, tiles;
+    uint32_t wrong;  // status bits
+};
+__device__ __forceinline__ Sequence load_sequence(const TreeParams &p, int b) {
+    Sequence s;
+    s.row0 = __ldg(p.cu_q_lens + b);
+    s.n = __ldg(p.cu_q_lens + b + 1) - s.row0;
+    s.ctx = __ldg(p.context_lens + b);
+    s.wrong = 0;
+    const int64_t most = static_cast<int64_t>(p.max_blocks) * kBlockSize;
+    if (s.n < 0 || s.row0 < 0 || s.n > p.total_rows - s.row0) {
+        s.wrong = kStatusBadQLen;
+        s.n = 0;
+    } else if (s.n > 0) {
+        if (s.ctx < 1 || s.ctx > most) s.wrong = kStatusBadContextLen;
+        if (s.n > p.max_q_len || (s.ctx >= 1 && s.ctx < s.n)) s.wrong |= kStatusBadQLen;
+        if (s.wrong) s.ctx = 0;
+    }
+    s.row_tiles = static_cast<int>((static_cast<int64_t>(s.n) * p.group + kRows - 1) / kRows);
+    s.units = s.n > 0 ? s.row_tiles * p.n_kv : 0;
+    s.tiles = max(1, (s.ctx + kKeys - 1) / kKeys);
+    return s;
+}
+
+// A CTA's range of tiles: the unit it starts in, and its length.
+struct Plan {
+    int b, unit, tile, count;
+    int64_t begin, total;  // of the range; tiles of the whole call
+    int ranges;            // that are not empty
+};
+
+// The pieces of a range, one after the other; every role walks them by itself.
+struct Walk {
+    Sequence s;
+    int b, unit, t0, t1, left;
+    __device__ __forceinline__ void start(const TreeParams &p, const Plan &plan) {
+        b = plan.b;
+        unit = plan.unit;
+        t0 = plan.tile;
+        left = plan.count;
+        if (left > 0) s = load_sequence(p, b);
+        t1 = min(s.tiles, t0 + left);
+    }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void next(const TreeParams &p) {
+        left -= t1 - t0;
+        if (left <= 0) return;
+        t0 = 0;
+        if (++unit >= s.units) {
+            unit = 0;
+            do s = load_sequence(p, ++b);
+            while (s.units == 0);
+        }
+        t1 = min(s.tiles, left);
+    }
+    __device__ __forceinline__ int kv_head() const { return unit / s.row_tiles; }
+    __device__ __forceinline__ int row_tile() const { return unit % s.row_tiles; }
+    __device__ __forceinline__ int rows(const TreeParams &p) const { return min(kRows, s.n * p.group - row_tile() * kRows); }
+};
+
+// The range of this CTA, by one warp: tiles of all sequences, then the sequence that the range starts in.  (The
+// first 128 sequences are looked at once; dividends that fit 32 bits are divided in them: a plan of 64 sequences is
+// on the way of every call.)
+constexpr int kPlanHeld = 4;
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
+}
+__device__ Plan make_plan(const TreeParams &p, int lane) {
+    Plan plan{};
+    uint32_t wrong = 0;
+    auto load = [&](int b, int &tiles) -> int64_t {  // tiles of all of a sequence's units
+        tiles = 1;
+        if (b >= p.num_seqs) return 0;
+        const Sequence s = load_sequence(p, b);
+        wrong |= s.wrong;
+        tiles = s.tiles;
+        return static_cast<int64_t>(s.units) * s.tiles;
+    };
+    int64_t held[kPlanHeld], total = 0;
+    int held_tiles[kPlanHeld];
+#pragma unroll
+    for (int i = 0; i < kPlanHeld; ++i) total += held[i] = load(32 * i + lane, held_tiles[i]);
+    for (int b = 32 * kPlanHeld + lane; b < p.num_seqs; b += 32) {
+        int tiles;
+        total += load(b, tiles);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    if (wrong && blockIdx.x == 0 && p.status) atomicOr(p.status, wrong);
+    plan.total = total;
+    plan.ranges = static_cast<int>(min(static_cast<int64_t>(p.ranges), total));
+    if (static_cast<int>(blockIdx.x) >= plan.ranges) return plan;
+    plan.begin = divide(total * blockIdx.x, plan.ranges);
+    plan.count = static_cast<int>(divide(total * (blockIdx.x + 1), plan.ranges) - plan.begin);
+    int64_t before = 0;
+    auto find = [&](int b0, int64_t mine, int tiles) -> bool {  // the range starts in one of the 32 sequences from b0 on
+        int64_t upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += y;
+        }
+        upto += before;
+        const uint32_t past = __ballot_sync(0xffffffffu, upto > plan.begin);
+        before = __shfl_sync(0xffffffffu, upto, 31);
+        if (!past) return false;
+        const int who = __ffs(past) - 1;
+        const int64_t inside = __shfl_sync(0xffffffffu, plan.begin - (upto - mine), who);
+        tiles = __shfl_sync(0xffffffffu, tiles, who);
+        plan.b = b0 + who;
+        plan.unit = static_cast<int>(divide(inside, tiles));
+        plan.tile = static_cast<int>(inside - static_cast<int64_t>(plan.unit) * tiles);
+        return true;
+    };
+#pragma unroll
+    for (int i = 0; i < kPlanHeld; ++i)
+        if (32 * i < p.num_seqs && find(32 * i, held[i], held_tiles[i])) return plan;
+    for (int b0 = 32 * kPlanHeld; b0 < p.num_seqs; b0 += 32) {
+        int tiles;
+        const int64_t mine = load(b0 + lane, tiles);
+        if (find(b0, mine, tiles)) return plan;
+    }
+    plan.count = 0;  // (not reached: begin < total)
+    return plan;
+}
+
+// Sixteen E4M3 codes to bf16 (exact: E4M3 values are bf16 values): a holds values 0 .. 7, b 8 .. 15.
+__device__ __forceinline__ void e4m3x16_to_bf16(const uint4 &c, uint4 &a, uint4 &b) {
+    auto two = [](uint32_t f16x2) {
+        const float2 f = unpack_f16x2(f16x2);
+        return pack_bf16x2(f.x, f.y);
+    };
+    uint32_t x, y;
+    e4m3x4_to_f16x2x2(c.x, x, y);
+    a.x = two(x);
+    a.y = two(y);
+    e4m3x4_to_f16x2x2(c.y, x, y);
+    a.z = two(x);
+    a.w = two(y);
+    e4m3x4_to_f16x2x2(c.z, x, y);
+    b.x = two(x);
+    b.y = two(y);
+    e4m3x4_to_f16x2x2(c.w, x, y);
+    b.z = two(x);
+    b.w = two(y);
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap kmap, const TreeParams p) {
+    using L = Layout<FP8>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.group;
+    auto bar = [&](int i) { return sbase + L::kOffBar + 8 * i; };
+    auto k_full = [&](int st) { return bar(st); };
+    auto k_empty = [&](int st) { return bar(L::kStagesK + st); };
+    auto v_full = [&](int st) { return bar(2 * L::kStagesK + st); };
+    auto v_empty = [&](int st) { return bar(2 * L::kStagesK + L::kStagesV + st); };
+    constexpr int kBarQ = 2 * L::kStagesK + 2 * L::kStagesV;
+    auto q_full = [&](int place) { return bar(kBarQ + place); };
+    auto q_empty = [&](int place) { return bar(kBarQ + 2 + place); };
+    // of tile j: place j % kPlaces, phase j / kPlaces
+    auto s_full = [&](int j) { return bar(kBarQ + 4 + j % kPlaces); };
+    auto p_full = [&](int j) { return bar(kBarQ + 4 + kPlaces + j % kPlaces); };
+    auto pv_done = [&](int j) { return bar(kBarQ + 4 + 2 * kPlaces + j % kPlaces); };
+    auto phase = [](int j) -> uint32_t { return (j / kPlaces) & 1; };
+    const uint32_t o_free = bar(kBarQ + 4 + 3 * kPlaces), drained = o_free + 8;  // (drained: one of each issuing warp)
+    const bool two_q = p.part_rows <= kRows / 2;  // two places for Q: rows 0 .. 63 and 64 .. 127 of the tile
+    Plan *plan_slot = reinterpret_cast<Plan *>(smem + L::kOffPlan);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffPlan + 48);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + L::kOffPlan + 56);
+    static_assert(sizeof(Plan) <= 48, "plan area");
+
+    if (tid == 0) {
+        prefetch_tensormap(&kmap);
+        for (int st = 0; st < L::kStagesK; ++st) {
+            mbar_init(k_full(st), 1);
+            mbar_init(k_empty(st), 1);
+        }
+        for (int st = 0; st < L::kStagesV; ++st) {
+            mbar_init(v_full(st), FP8 ? 1 : L::kCopyWarps);
+            mbar_init(v_empty(st), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(q_full(i), 1);
+            mbar_init(q_empty(i), 1);
+        }
+        for (int i = 0; i < kPlaces; ++i) {
+            mbar_init(s_full(i), 1);
+            mbar_init(p_full(i), kGroupWarps);
+            mbar_init(pv_done(i), 1);
+        }
+        mbar_init(o_free, 2 * kGroupWarps);
+        mbar_init(drained, 1);
+        mbar_init(drained + 8, 1);
+        *abort_flag = 0u;
+        fence_mbar_init();
+    }
+    if (warp == kWarpS) {
+        tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish();
+    }
+    griddep_launch_dependents();
+    griddep_wait();
+    if (warp == kWarpQ) {
+        const Plan plan = make_plan(p, lane);
+        if (lane == 0) *plan_slot = plan;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const Plan plan = *plan_slot;
+    const uint32_t tmem = *tmem_slot;
+
+    // A whole warp waits for a barrier's phase, within a bound, and gives up at once after another role gave up.
+    // (What is complete already costs one test; then lane 0 alone polls.)
+    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
+        if (__any_sync(0xffffffffu, mbar_test_wait(b, parity))) return true;
+        bool ok = false;
+        if (lane == 0 && !*abort_flag) {
+            ok = mbar_wait(b, parity);
+            if (!ok) *abort_flag = 1u;
+        }
+        return __any_sync(0xffffffffu, ok);
+    };
+
+    Walk w;
+    w.start(p, plan);
+    // Place and use (its number there) of piece i's Q.
+    auto q_place = [&](int i) { return two_q ? i & 1 : 0; };
+    auto q_use = [&](int i) { return two_q ? i >> 1 : i; };
+    // Lane k < 4: the id of block k of tile t (-1: none).
+    auto block_id = [&](int t) -> int {
+        const int blocks = (w.s.ctx + kBlockSize - 1) / kBlockSize, at = t * kTileBlocks + lane;
+        return lane < kTileBlocks && at < blocks ? __ldg(p.block_tables + static_cast<int64_t>(w.b) * p.max_blocks + at) : -1;
+    };
+    if (warp == kWarpK) {
+        // ---------------- K: lane k < 4 sends for block k of a tile ----------------
+        int j = 0;  // tile of the range
+        bool ok = true;
+        for (; ok && w.more(); w.next(p)) {
+            const int blocks = (w.s.ctx + kBlockSize - 1) / kBlockSize, g = w.kv_head();
+            int next = block_id(w.t0);
+            for (int t = w.t0; t < w.t1; ++t, ++j) {
+                // (an invalid id fetches block 0; its keys are masked)
+                const int id = static_cast<unsigned>(next) < static_cast<unsigned>(p.num_blocks) ? next : 0;
+                if (t + 1 < w.t1) next = block_id(t + 1);
+                const int st = j % L::kStagesK;
+                if (j >= L::kStagesK && !(ok = warp_wait(k_empty(st), ((j / L::kStagesK) - 1) & 1))) break;
+                const int load = max(0, min(kTileBlocks, blocks - t * kTileBlocks));
+                if (lane == 0) {
+                    if (load > 0)
+                        mbar_arrive_expect_tx(k_full(st), load * L::kBlk);
+                    else
+                        mbar_arrive(k_full(st));
+                }
+                __syncwarp();
+                const uint32_t dst = sbase + L::kOffK + st * L::kKTile + lane * L::kBlk;
+                if (lane < load) {
+                    if constexpr (FP8)
+                        tma_load_4d(dst, &kmap, k_full(st), 0, 0, g, id);
+                    else
+                        tma_load_5d(dst, &kmap, k_full(st), 0, 0, 0, 0, id * p.n_kv + g);
+                }
+            }
+        }
+        // (given up: the copies still on their way land before the CTA ends)
+        if (!ok && lane == 0)
+            for (int i = max(0, j - L::kStagesK); i < j; ++i) mbar_wait(k_full(i % L::kStagesK), (i / L::kStagesK) & 1);
+    } else if (!FP8 && warp >= kWarpV) {
+        // ---------------- V: 16 threads a row, four rows a step ----------------
+        const int t16 = (warp - kWarpV) * 32 + lane, row4 = t16 >> 4, c = t16 & 15;
+        uint32_t to[4];  // of rows row4 + 4 i of a block
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = row4 + 4 * i;
+            to[i] = (r >> 3) * 2048 + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
+        }
+        int j = 0, landed = 0;  // tiles sent for; tiles handed on
+        bool ok = true;
+        auto hand_on = [&]() {  // a tile has landed: made visible to the tensor core, an arrival a warp
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_full(landed % L::kStagesV));
+            ++landed;
+        };
+        for (; ok && w.more(); w.next(p)) {
+            const int g = w.kv_head();
+            int next = block_id(w.t0);
+            for (int t = w.t0; t < w.t1; ++t, ++j) {
+                const int mine = next;
+                if (t + 1 < w.t1) next = block_id(t + 1);
+                const int st = j % L::kStagesV;
+                if (j >= L::kStagesV) {
+                    const uint32_t parity = ((j / L::kStagesV) - 1) & 1;
+                    // A place not free yet: what was sent for is handed on as it lands.
+                    while (landed < j && !__any_sync(0xffffffffu, mbar_test_wait(v_empty(st), parity))) {
+                        if (j - landed >= 3)
+                            asm volatile("cp.async.wait_group 2;" ::: "memory");
+                        else if (j - landed == 2)
+                            asm volatile("cp.async.wait_group 1;" ::: "memory");
+                        else
+                            asm volatile("cp.async.wait_group 0;" ::: "memory");
+                        hand_on();
+                    }
+                    if (!(ok = warp_wait(v_empty(st), parity))) break;
+                }
+                const int keys = w.s.ctx - t * kKeys;
+#pragma unroll
+                for (int k = 0; k < kTileBlocks; ++k) {
+                    const int id = __shfl_sync(0xffffffffu, mine, k);
+                    const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
+                    const uint8_t *src = static_cast<const uint8_t *>(p.v_cache) +
+                                         (static_cast<int64_t>(good ? id : 0) * p.n_kv + g) * kBlkBytes + row4 * 256 + c * 16;
+                    const uint32_t dst = sbase + L::kOffV + st * kVTile + k * kBlkBytes;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        cp_async_16_or_zero(dst + to[i], src + i * 1024, good && k * kBlockSize + row4 + 4 * i < keys);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (landed + 2 < j) {  // (three tiles on their way)
+                    asm volatile("cp.async.wait_group 3;" ::: "memory");
+                    hand_on();
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        while (ok && landed < j) hand_on();
+    } else if (FP8 && warp >= kWarpV) {
+        // ---------------- V's codes: every fourth tile, expanded to bf16; its scales and K's ----------------
+        const int x = warp - kWarpV;
+        const uint32_t raw0 = sbase + L::kOffRaw + x * L::kRaw * kTileBlocks * kCodeBytes;
+        // This lane's 16-byte pieces of a block: row (lane >> 3) + 4 i, chunk lane & 7.
+        const int row = lane >> 3, c = lane & 7;
+        Walk ahead = w;  // of the tile sent for next
+        int ta = ahead.t0, ja = 0;
+        auto skip = [&](Walk &walk, int &t, int &j, int n) {  // n tiles on
+            while (n > 0 && walk.more()) {
+                const int step = min(n, walk.t1 - t);
+                t += step;
+                j += step;
+                n -= step;
+                if (t == walk.t1) {
+                    walk.next(p);
+                    t = walk.t0;
+                }
+            }
+        };
+        auto send = [&]() {  // the codes and scales of tile ja, then on to this warp's next
+            if (ahead.more()) {
+                const int g = ahead.kv_head(), blocks = (ahead.s.ctx + kBlockSize - 1) / kBlockSize;
+                const int at = ta * kTileBlocks + lane;
+                const int mine = lane < kTileBlocks && at < blocks
+                                     ? __ldg(p.block_tables + static_cast<int64_t>(ahead.b) * p.max_blocks + at)
+                                     : -1;
+                const uint32_t raw = raw0 + ((ja >> 2) % L::kRaw) * kTileBlocks * kCodeBytes;
+                const uint32_t scale = sbase + L::kOffScale + (ja % L::kScaleTiles) * 2 * kKeys * 4;
+#pragma unroll
+                for (int k = 0; k < kTileBlocks; ++k) {
+                    const int id = __shfl_sync(0xffffffffu, mine, k);
+                    const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
+                    const int64_t tile = static_cast<int64_t>(good ? id : 0) * p.n_kv + g;
+                    const uint8_t *src = static_cast<const uint8_t *>(p.v_cache) + tile * kCodeBytes + lane * 16;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cp_async_16(raw + k * kCodeBytes + i * 512 + lane * 16, src + i * 512);
+                    if (lane < 8)
+                        cp_async_16(scale + (lane >> 2) * kKeys * 4 + k * 64 + (lane & 3) * 16,
+                                    (lane < 4 ? p.k_scale : p.v_scale) + tile * kBlockSize + (lane & 3) * 4);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            skip(ahead, ta, ja, L::kCopyWarps);
+        };
+        int t = w.t0, j = 0;
+        skip(ahead, ta, ja, x);
+        skip(w, t, j, x);
+        for (int i = 0; i < L::kRaw; ++i) send();
+        bool ok = true;
+        while (ok && w.more()) {
+            const int st = j % L::kStagesV;
+            const int mine = block_id(t);
+            const int keys = w.s.ctx - t * kKeys;
+            if (j >= L::kStagesV && !(ok = warp_wait(v_empty(st), ((j / L::kStagesV) - 1) & 1))) break;
+            asm volatile("cp.async.wait_group %0;" ::"n"(L::kRaw - 1) : "memory");
+            __syncwarp();
+            const uint32_t raw = raw0 + ((j >> 2) % L::kRaw) * kTileBlocks * kCodeBytes;
+            const uint32_t scale = sbase + L::kOffScale + (j % L::kScaleTiles) * 2 * kKeys * 4;
+#pragma unroll
+            for (int k = 0; k < kTileBlocks; ++k) {
+                const int id = __shfl_sync(0xffffffffu, mine, k);
+                const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
+                // a key that is not the sequence's: scales 0, values 0
+                if (lane < kBlockSize && (!good || k * kBlockSize + lane >= keys)) {
+                    sts32(scale + (k * kBlockSize + lane) * 4, 0u);
+                    sts32(scale + (kKeys + k * kBlockSize + lane) * 4, 0u);
+                }
+                const uint32_t dst = sbase + L::kOffV + st * kVTile + k * kBlkBytes;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = row + 4 * i;
+                    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+                    const uint4 code = lds128(raw + k * kCodeBytes + i * 512 + lane * 16);
+                    if (good && k * kBlockSize + r < keys) e4m3x16_to_bf16(code, a, b);
+                    // values 16 c .. 16 c + 15 of row r: bf16 chunks 2 c and 2 c + 1 of 16
+                    const uint32_t at = dst + (r >> 3) * 2048 + (c >> 2) * 1024 + (r & 7) * 128;
+                    sts128(at + (((2 * (c & 3)) ^ (r & 7)) << 4), a);
+                    sts128(at + (((2 * (c & 3) + 1) ^ (r & 7)) << 4), b);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v_full(st));
+            send();
+            skip(w, t, j, L::kCopyWarps);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == kWarpQ) {
+        // ---------------- the pieces' Q rows: 16 lanes a row, two rows a step ----------------
+        const int c = lane & 15;
+        for (int piece = 0; w.more(); ++piece) {
+            const int place = q_place(piece);
+            if (q_use(piece) > 0 && !warp_wait(q_empty(place), (q_use(piece) - 1) & 1)) break;
+            // f(row, address of this lane's 8 values) for the rows of the piece at hand
+            auto each_row = [&](auto f) {
+                const int rows = w.rows(p), first = w.row_tile() * kRows;
+                int r = lane >> 4, h = (first + r) % G;
+                const __nv_bfloat16 *src =
+                    static_cast<const __nv_bfloat16 *>(p.q) + 8 * c +
+                    ((static_cast<int64_t>(w.s.row0) + (first + r) / G) * p.n_q + static_cast<int64_t>(w.kv_head()) * G + h) * kHeadDim;
+                const int64_t node_step = static_cast<int64_t>(p.n_q - G) * kHeadDim;  // from behind a node's heads to the next's
+                for (; r < rows; r += 2) {
+                    f(r, src);
+                    src += 2 * kHeadDim;
+                    for (h += 2; h >= G; h -= G) src += node_step;
+                }
+            };
+            const uint32_t at = sbase + L::kOffQ + place * (kHalfTile / 2);
+            if constexpr (FP8) {
+                float *factor = reinterpret_cast<float *>(smem + L::kOffRow) + place * kRows;
+                const int rows = w.rows(p);
+                // (both halves of the warp take as many steps: the maximum goes by shuffles)
+                const int first = w.row_tile() * kRows;
+                const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(p.q) + 8 * c +
+                                            (static_cast<int64_t>(w.s.row0) * p.n_q + static_cast<int64_t>(w.kv_head()) * G) * kHeadDim;
+                auto read = [&](int r) -> uint4 {
+                    const int at_row = first + min(r, rows - 1);
+                    return __ldg(reinterpret_cast<const uint4 *>(
+                        base + (static_cast<int64_t>(at_row / G) * p.n_q + at_row % G) * kHeadDim));
+                };
+                uint4 x[4];
+                for (int r0 = 0; r0 < rows; r0 += 8) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = read(r0 + 2 * i + (lane >> 4));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = r0 + 2 * i + (lane >> 4);
+                        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                        float v[8], most = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            v[2 * k] = __uint_as_float(u[k] << 16);
+                            v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+                            most = fmaxf(most, fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
+                        }
+#pragma unroll
+                        for (int off = 8; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+                        // 2^e puts the largest value in [2^7, 2^8) (both powers are normal numbers)
+                        const int e = min(126, max(-119, 7 - (static_cast<int>(__float_as_uint(most) >> 23) - 127)));
+                        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                        uint32_t hi[2], lo[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float s4[4], rest[4];
+#pragma unroll
+                            for (int i4 = 0; i4 < 4; ++i4) s4[i4] = v[4 * k + i4] * up;
+                            hi[k] = f32x2_to_e4m3x2(s4[0], s4[1]) | (f32x2_to_e4m3x2(s4[2], s4[3]) << 16);
+                            uint32_t f0, f1;
+                            e4m3x4_to_f16x2x2(hi[k], f0, f1);
+                            const float2 h0 = unpack_f16x2(f0), h1 = unpack_f16x2(f1);
+                            rest[0] = s4[0] - h0.x;
+                            rest[1] = s4[1] - h0.y;
+                            rest[2] = s4[2] - h1.x;
+                            rest[3] = s4[3] - h1.y;
+                            lo[k] = f32x2_to_e4m3x2(rest[0], rest[1]) | (f32x2_to_e4m3x2(rest[2], rest[3]) << 16);
+                        }
+                        if (r < rows) {
+                            const uint32_t to = at + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+                            sts32(to, hi[0]);
+                            sts32(to + 4, hi[1]);
+                            sts32(to + kHalfTile, lo[0]);
+                            sts32(to + kHalfTile + 4, lo[1]);
+                            // (a row with an infinity has no finite scores: NaN, as code x 448 would not say)
+                            if (c == 0)
+                                factor[r] = most > 3.4e38f ? __uint_as_float(0x7fc00000u)
+                                                           : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                        }
+                    }
+                }
+            } else {
+                const uint32_t dst = at + (c >> 3) * kHalfTile;
+                each_row([&](int r, const __nv_bfloat16 *src) { cp_async_16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), src); });
+                asm volatile("cp.async.wait_all;" ::: "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full(place));
+            w.next(p);
+            if (w.more()) each_row([&](int, const __nv_bfloat16 *src) {
+                if ((c & 7) == 0) prefetch_l2(src);
+            });
+        }
+    } else if (warp == kWarpS) {
+        // ---------------- S = Q K^T ----------------
+        int j = 0;
+        bool ok = true;
+        for (int piece = 0; ok && w.more(); w.next(p), ++piece) {
+            const int place = q_place(piece);
+            if (!(ok = warp_wait(q_full(place), q_use(piece) & 1))) break;
+            for (int t = w.t0; t < w.t1; ++t, ++j) {
+                const int st = j % L::kStagesK;
+                ok = warp_wait(k_full(st), (j / L::kStagesK) & 1);
+                if (ok && j >= kPlaces) ok = warp_wait(pv_done(j), phase(j - kPlaces));  // the weights there have been read
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    // (the second place's rows begin 64 rows down; what lies behind them is read and not used)
+                    const uint32_t kb = sbase + L::kOffK + st * L::kKTile, qb = sbase + L::kOffQ + place * (kHalfTile / 2);
+                    const uint32_t d = tmem + kKeys * (j % kPlaces);
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)  // 32 values per step: codes, then the remainders'
+                            umma_f8(d, sw128_desc(qb + (kk >> 2) * kHalfTile + (kk & 3) * 32, 16, 1024),
+                                    sw128_desc(kb + (kk & 3) * 32, 16, 1024), kIdescS8, kk > 0);
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)  // 16 values per step: half kk / 4, 32 B into the row
+                            umma_bf16(d, sw128_desc(qb + (kk >> 2) * kHalfTile + (kk & 3) * 32, 16, 1024),
+                                      sw128_desc(kb + (kk >> 2) * 1024 + (kk & 3) * 32, 16, 2048), kIdescS, kk > 0);
+                    }
+                    umma_commit(s_full(j));
+                    umma_commit(k_empty(st));
+                    if (t + 1 == w.t1) umma_commit(q_empty(place));
+                }
+                __syncwarp();
+            }
+        }
+    } else if (warp == kWarpPv) {
+        // ---------------- O += P V ----------------
+        int j = 0;
+        bool ok = true;
+        for (int piece = 0; ok && w.more(); w.next(p), ++piece) {
+            for (int t = w.t0; t < w.t1; ++t, ++j) {
+                const int st = j % L::kStagesV;
+                ok = warp_wait(v_full(st), (j / L::kStagesV) & 1);
+                // O of the piece before has been read
+                if (ok && piece > 0 && t - w.t0 < 2) ok = warp_wait(o_free, (piece - 1) & 1);
+                ok = ok && warp_wait(p_full(j), phase(j));
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t vb = sbase + L::kOffV + st * kVTile, d = tmem + kTmemO + 128 * (j & 1);
+                    const uint32_t first = t - w.t0 < 2 ? 0u : 1u;
+#pragma unroll
+                    for (int s4 = 0; s4 < 4; ++s4) {  // keys 16 s4 ..: of each 32 keys [16 columns heads | 16 remainders]
+                        const uint32_t a_hi = tmem + kKeys * (j % kPlaces) + (s4 >> 1) * 32 + (s4 & 1) * 8;
+                        const uint64_t bd = sw128_desc(vb + s4 * kBlkBytes, 1024, 2048);
+                        umma_bf16_tmem_a(d, a_hi, bd, kIdescPV, s4 > 0 ? 1u : first);
+                        umma_bf16_tmem_a(d, a_hi + 16, bd, kIdescPV, 1u);
+                    }
+                    umma_commit(pv_done(j));
+                    umma_commit(v_empty(st));
+                }
+                __syncwarp();
+            }
+        }
+    } else {
+        // ---------------- softmax: group a takes the tiles j with j & 1 == a, thread r the row r ----------------
+        const int a = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t t_o = lane_base + kTmemO + 128 * a;
+        float2 *ml = reinterpret_cast<float2 *>(smem + L::kOffMl);
+        auto both_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(2 * kGroupWarps * 32) : "memory"); };
+        bool alive = true;
+        int j0 = 0;  // tiles before the piece
+        for (int piece = 0; w.more(); w.next(p), ++piece) {
+            const int rows = w.rows(p), first_row = w.row_tile() * kRows, g = w.kv_head();
+            const bool busy = quarter * 32 < rows;  // (warp-uniform: a warp without rows only keeps step)
+            const int prefix = w.s.ctx - w.s.n;
+            const int64_t row = static_cast<int64_t>(w.s.row0) + (first_row + r) / G;
+            uint64_t mask = 0;
+            if (r < rows && w.s.ctx > 0) {
+                mask = __ldg(reinterpret_cast<const unsigned long long *>(p.mask) + row);
+                if (w.s.n < 64) mask &= (1ull << w.s.n) - 1;
+            }
+            float sl2 = p.scale_log2;
+            float m = -INFINITY, l = 0.f;
+            const int t_first = w.t0 + ((j0 ^ a) & 1);
+            int id = t_first < w.t1 ? block_id(t_first) : -1;  // read a tile ahead
+            for (int t = t_first; t < w.t1; t += 2) {
+                const int j = j0 + t - w.t0;
+                // blocks of this tile with an invalid id
+                const bool wrong = lane < kTileBlocks && (t * kTileBlocks + lane) * kBlockSize < w.s.ctx &&
+                                   static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks);
+                const uint32_t bad = __ballot_sync(0xffffffffu, wrong);
+                if (t + 2 < w.t1) id = block_id(t + 2);
+                if (bad && quarter == 0 && lane == 0 && p.status) atomicOr(p.status, kStatusBadBlockId);
+                if constexpr (FP8) alive = alive && warp_wait(v_full(j % L::kStagesV), (j / L::kStagesV) & 1);  // (the scales)
+                alive = alive && warp_wait(s_full(j), phase(j));
+                if (!alive) continue;
+                tc_fence_after();
+                const uint32_t t_s = lane_base + kKeys * (j % kPlaces);
+                if (busy) {
+                    if constexpr (FP8) {
+                        if (t == t_first)
+                            sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::kOffRow)[q_place(piece) * kRows + r];
+                    }
+                    const uint32_t scales = sbase + L::kOffScale + (j % L::kScaleTiles) * 2 * kKeys * 4;
+                    const bool whole = t * kKeys + kKeys <= prefix && !bad;  // every row sees every key (CTA-uniform)
+                    uint32_t v[64];
+                    tmem_ld_32x32b_x64(t_s, v);
+                    if constexpr (FP8) {  // scores times each key's K scale
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const uint4 f = lds128(scales + 16 * i);
+                            const float2 x = fmul2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
+                                                   make_float2(__uint_as_float(f.x), __uint_as_float(f.y)));
+                            const float2 y = fmul2(make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])),
+                                                   make_float2(__uint_as_float(f.z), __uint_as_float(f.w)));
+                            v[4 * i] = __float_as_uint(x.x);
+                            v[4 * i + 1] = __float_as_uint(x.y);
+                            v[4 * i + 2] = __float_as_uint(y.x);
+                            v[4 * i + 3] = __float_as_uint(y.y);
+                        }
+                    }
+                    // bits of the visible keys
+                    uint64_t seen = ~0ull;
+                    if (!whole) {
+                        const int at = t * kKeys - prefix;  // node of the tile's first key
+                        if (at >= 0)
+                            seen = at < 64 ? mask >> at : 0;
+                        else if (at > -64)
+                            seen = ((1ull << -at) - 1) | (mask << -at);
+#pragma unroll
+                        for (int k = 0; k < kTileBlocks; ++k)
+                            if ((bad >> k) & 1) seen &= ~(0xffffull << (16 * k));
+                    }
+                    // the row's largest score (the least, should the scale be below 0)
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if (whole && p.scale_log2 >= 0.f) {
+#pragma unroll
+                        for (int k = 0; k < 64; k += 2)
+                            mx[(k >> 1) & 3] = fmax3(mx[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                    } else {
+                        const uint32_t flip = p.scale_log2 < 0.f ? 0x80000000u : 0u;
+#pragma unroll
+                        for (int k = 0; k < 64; ++k)
+                            mx[k & 3] = fmaxf(mx[k & 3], (seen >> k) & 1 ? __uint_as_float(v[k] ^ flip) : -INFINITY);
+                    }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const float mt = top == -INFINITY ? -INFINITY : top * fabsf(sl2);
+                    float alpha = 1.f;
+                    if (mt > m + 8.f) {
+                        alpha = fast_exp2(m - mt);  // (0 where m is -inf)
+                        m = mt;
+                    }
+                    // O rescaled, behind the P V of this group's tile before
+                    if (t >= w.t0 + 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        alive = warp_wait(pv_done(j - 2), phase(j - 2));
+                        tc_fence_after();
+                        if (alive) {
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t o[16];
+                                tmem_ld_32x32b_x16(t_o + 16 * c, o);
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                                tmem_st_32x32b_x16(t_o + 16 * c, o);
+                            }
+                        }
+                    }
+                    // P = 2^(s scale log2(e) - m) over S, and the row's sum
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    const float2 sl2v = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
+                    float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int k = 32 * c + 2 * e;
+                            const float2 x = ffma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), sl2v, nmu);
+                            float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                            if (!whole) {
+                                if (!((seen >> k) & 1)) pr.x = 0.f;
+                                if (!((seen >> (k + 1)) & 1)) pr.y = 0.f;
+                            }
+                            if (e & 1)
+                                rs1 = fadd2(rs1, pr);
+                            else
+                                rs0 = fadd2(rs0, pr);
+                            if constexpr (FP8) pr = fmul2(pr, lds_f32x2(scales + (kKeys + k) * 4));  // (the sum keeps the plain weights)
+                            pk[e] = __byte_perm(__float_as_uint(pr.x), __float_as_uint(pr.y), 0x7632);
+                            const float2 rest = minus_bf16x2(pr, pk[e]);
+                            pk[16 + e] = pack_bf16x2(rest.x, rest.y);
+                        }
+                        tmem_st_32x32b_x32(t_s + 32 * c, pk);
+                    }
+                    const float2 rs = fadd2(rs0, rs1);
+                    l = l * alpha + (rs.x + rs.y);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(j));
+            }
+            // ---- the piece's end: both groups' parts joined; group a stores the values 64 a .. 64 a + 63 ----
+            const int tiles = w.t1 - w.t0;
+            const bool had[2] = {tiles > 1 || (j0 & 1) == 0, tiles > 1 || (j0 & 1) == 1};
+            j0 += tiles;
+            const int last = j0 - 1 - ((j0 - 1 - a) & 1), other = j0 - 1 - ((j0 - a) & 1);  // the groups' last tiles
+            if (had[a]) alive = alive && warp_wait(pv_done(last), phase(last));
+            ml[a * kRows + r] = make_float2(m, l);
+            tc_fence_before();
+            both_sync();
+            tc_fence_after();
+            if (had[1 - a]) {  // (complete: the other group waited for it; this orders its data for this warp)
+                alive = alive && warp_wait(pv_done(other), phase(other));
+                tc_fence_after();
+            }
+            if (alive && busy) {
+                const float2 x0 = ml[r], x1 = ml[kRows + r];
+                const float top = fmaxf(x0.x, x1.x);
+                const float mu = top == -INFINITY ? 0.f : top;
+                float f[2] = {fast_exp2(x0.x - mu), fast_exp2(x1.x - mu)};
+                const float sum = f[0] * x0.y + f[1] * x1.y;
+                const bool direct = tiles == w.s.tiles;
+                if (direct) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (a row that sees nothing is zero)
+                    f[0] *= inv;
+                    f[1] *= inv;
+                }
+                const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1);
+                const int64_t pr = slot * p.part_rows + r;
+                const int64_t head = row * p.n_q + static_cast<int64_t>(g) * G + (first_row + r) % G;
+                if (!direct && a == 0 && r < rows) p.part_ml[pr] = make_float2(top, sum);
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    const int col = 64 * a + 32 * c;
+                    uint32_t o[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = 0u;
+                    if (had[0]) {
+                        uint32_t x[32];
+                        tmem_ld_32x32b_x32(lane_base + kTmemO + col, x);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(f[0] == 0.f ? 0.f : __uint_as_float(x[k]) * f[0]);
+                    }
+                    if (had[1]) {
+                        uint32_t x[32];
+                        tmem_ld_32x32b_x32(lane_base + kTmemO + 128 + col, x);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            o[k] = __float_as_uint(f[1] == 0.f ? __uint_as_float(o[k])
+                                                               : fmaf(__uint_as_float(x[k]), f[1], __uint_as_float(o[k])));
+                    }
+                    if (r >= rows) {
+                    } else if (!direct || !p.out_bf16) {
+                        uint4 *dst = reinterpret_cast<uint4 *>((direct ? static_cast<float *>(p.out) + head * kHeadDim
+                                                                       : p.part_o + pr * kHeadDim) + col);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    } else {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + head * kHeadDim + col);
+                        auto two = [&](int k) { return pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])); };
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            dst[k] = make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6));
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(o_free);
+            both_sync();  // (m, l) have been read
+            // A unit that begins here and goes on in the next ranges is joined by the second kernel.
+            if (tid == 0 && w.left == tiles) {
+                int4 rec = make_int4(0, 0, 0, 0);
+                if (w.t0 == 0 && tiles < w.s.tiles) {
+                    const int64_t end = plan.begin + plan.count - tiles + w.s.tiles;  // behind the unit's last tile
+                    const int64_t cta = (end * plan.ranges + plan.total - 1) / plan.total - 1;
+                    rec = make_int4(w.b, w.unit, static_cast<int>(cta) - static_cast<int>(blockIdx.x) + 1, 0);
+                }
+                p.record[blockIdx.x] = rec;
+            }
+        }
+        if (tid == 0 && plan.count == 0) p.record[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
+
+    // ---- every role is done (or gave up): tensor memory is freed ----
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort_flag) {
+        if (tid == 0 && p.status) atomicOr(p.status, kStatusTimeout);
+        if ((warp == kWarpS || warp == kWarpPv) && elect_one()) {  // MMAs on their way end before the columns are freed
+            const uint32_t b = drained + (warp == kWarpS ? 0 : 8);
+            umma_commit(b);
+            mbar_wait(b, 0);
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == kWarpS) tmem_dealloc(tmem, kTmemCols);
+}
+
+// out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i over the parts of a split unit: a warp takes a
+// row, lane k its values 4 k .. 4 k + 3.  The unit's first part lies in the range that it begins in (slot
+// 1), the others in slot 0 of the ranges behind.
+constexpr int kMergeRows = 8;  // rows (warps) of a CTA
+__global__ void __launch_bounds__(kMergeRows * 32) tree_merge_kernel(const TreeParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int c = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
+    const int4 rec = p.record[c];
+    const int parts = rec.z;
+    if (parts < 2) return;
+    const Sequence s = load_sequence(p, rec.x);
+    const int g = rec.y / s.row_tiles, first_row = rec.y % s.row_tiles * kRows;
+    if (r >= min(kRows, s.n * p.group - first_row)) return;
+    auto part = [&](int i) -> int64_t { return (static_cast<int64_t>(c + i) * 2 + (i == 0 ? 1 : 0)) * p.part_rows + r; };
+    float top = -INFINITY;
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(p.part_ml + part(i)).x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float mu = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const float2 x = __ldcg(p.part_ml + part(i));
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + part(i) * kHeadDim) + lane);
+        const float f = fast_exp2(x.x - mu);
+        sum = fmaf(f, x.y, sum);
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t head = (static_cast<int64_t>(s.row0) + (first_row + r) / p.group) * p.n_q + static_cast<int64_t>(g) * p.group +
+                         (first_row + r) % p.group;
+    if (p.out_bf16)
+        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + head * kHeadDim)[lane] =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    else
+        reinterpret_cast<float4 *>(static_cast<float *>(p.out) + head * kHeadDim)[lane] =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
+}  // namespace
+
+cudaError_t tree_prepare_device() {
+    const cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(Layout<false>::kBytes));
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(tree_attention_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(Layout<true>::kBytes));
+}
+
+cudaError_t launch_tree_attention(const CUtensorMap &kmap, const TreeParams &p, bool fp8, cudaStream_t stream) {
+    const cudaError_t e = fp8 ? launch_pdl(tree_attention_kernel<true>, dim3(p.ranges), dim3(Layout<true>::kThreads),
+                                           Layout<true>::kBytes, stream, kmap, p)
+                              : launch_pdl(tree_attention_kernel<false>, dim3(p.ranges), dim3(Layout<false>::kThreads),
+                                           Layout<false>::kBytes, stream, kmap, p);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(tree_merge_kernel, dim3(p.ranges, (p.part_rows + kMergeRows - 1) / kMergeRows), dim3(kMergeRows * 32), 0,
+                      stream, p);
+}
+
+}  // namespace pkv

@@ -179,6 +179,10 @@ def _declare(lib):
     lib.rotary_reshape_and_cache_fp8.argtypes = [P, P, i64, i64, P, i64, i64, P, i64, i64, P, P, P, P, P, P, P, i32, i32,
                                                  i32, i32, f32, D, P]
     lib.rotary_reshape_and_cache_fp8.restype = I
+    lib.paged_attention_tree_workspace_size.argtypes = [i32, i32, i32, D]
+    lib.paged_attention_tree_workspace_size.restype = sz
+    lib.paged_attention_tree.argtypes = [P, i32, P, P, P, i32, i32, P, P, P, P, P, P, i32, i32, i32, f32, D, P, sz, P]
+    lib.paged_attention_tree.restype = I
     lib.speculative_verify.argtypes = [P, P, P, P, i64, P, i64, P, P, P, P, i32, i32, i32, i32, P, P]
     lib.speculative_verify.restype = I
     lib.kv_compact_path.argtypes = [P, P, P, P, P, P, P, P, P, i32, i32, i32, D, P, P]
@@ -1107,6 +1111,44 @@ def rotary_reshape_and_cache_fp8(q_out, q, key, value, k_cache, v_cache, k_scale
     scale per token and head."""
     _rotary_write(True, q_out, q, key, value, k_cache, v_cache, k_scale, v_scale, positions, slot_mapping, frequencies,
                   layout, magnitude, stream)
+
+
+def paged_attention_tree_workspace_size(num_seqs: int, num_q_heads: int, max_q_len: int, cache: CacheDesc) -> int:
+    return int(load_library().paged_attention_tree_workspace_size(num_seqs, num_q_heads, max_q_len, ctypes.byref(cache)))
+
+
+def paged_attention_tree(out, q, tree_mask, cu_q_lens, max_q_len: int, k_cache, v_cache, block_tables, context_lens,
+                         scale: float, workspace=None, k_scale=None, v_scale=None, stream=None):
+    """Attention of every node of each sequence's tree over its cached prefix and the nodes that its
+    mask names: ``q`` bf16 [total_rows, n_q, 128], ``out`` the same in float32 or bfloat16, ``tree_mask``
+    int64 [total_rows] (bit j: node j of the sequence is seen), ``cu_q_lens`` int32 [num_seqs + 1]; ``context_lens``
+    counts the nodes, whose K and V are cached already.  An FP8 cache comes with ``k_scale`` and
+    ``v_scale``.  Returns the workspace (allocated if None)."""
+    torch = _torch()
+    device, stream = _device_and_stream(stream)
+    desc, _, kv, k_at, v_at, ks, vs = _kv_pool(k_cache, v_cache, k_scale, v_scale, device)
+    (rows, heads, width), q_at = _flat(q, "q", torch.bfloat16, 3, device)
+    code, shape, out_at = _latent_out(out, device)
+    if width != HEAD_DIM or shape != (rows, heads, width):
+        raise ValueError("q and out must be [total_rows, n_q, 128]")
+    (m,), mask = _flat(tree_mask, "tree_mask", torch.int64, 1, device)
+    if m != rows:
+        raise ValueError("one mask per row")
+    (n,), cu = _flat(cu_q_lens, "cu_q_lens", torch.int32, 1, device)
+    (B, max_blocks), tables = _flat(block_tables, "block_tables", torch.int32, 2, device)
+    (m,), lens = _flat(context_lens, "context_lens", torch.int32, 1, device)
+    if n != B + 1 or m != B:
+        raise ValueError("context_lens must be [num_seqs], cu_q_lens [num_seqs + 1]")
+    most = int(max_q_len)
+    lib = _lib or load_library()
+    if workspace is None:
+        workspace = _new_workspace(lib.paged_attention_tree_workspace_size(B, heads, most, desc), "paged_attention_tree", out,
+                                   stream, clear=256)
+    (size,), space = _flat(workspace, "workspace", torch.uint8, 1, device)
+    rc = lib.paged_attention_tree(out_at, code, q_at, mask, cu, most, rows, k_at, v_at, ks, vs, tables, lens, B, heads,
+                                  max_blocks, scale, desc, space, size, stream)
+    _raise("paged_attention_tree", rc)
+    return workspace
 
 
 def _probabilities(t, name, rows, device):

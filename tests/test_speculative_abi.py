@@ -155,3 +155,33 @@ def test_reference_rotation_turns_back():
     for layout in ("half", "interleaved"):
         y = R.rotate(R.rotate(x, [5, 70, 1000], w, layout), [-5, -70, -1000], w, layout)
         assert torch.allclose(x, y, atol=1e-12, rtol=0)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(out=None), INV), (dict(q=None), INV), (dict(m=None), INV), (dict(cu=None), INV), (dict(kc=None), INV),
+    (dict(vc=None), INV), (dict(bt=None), INV), (dict(cl=None), INV), (dict(ws=None), INV), (dict(out=FAKE + 8), INV),
+    (dict(q=FAKE + 8), INV), (dict(m=FAKE + 4), INV), (dict(kc=FAKE + 8), INV), (dict(cu=FAKE + 2), INV),
+    (dict(ws=FAKE + 128), INV), (dict(wb=256), WS), (dict(od=2), UNS), (dict(B=0), INV), (dict(B=65536), INV),
+    (dict(most=0), INV), (dict(most=65), INV), (dict(rows=-1), INV), (dict(h=0), INV), (dict(h=12), INV),
+    (dict(h=80000), UNS), (dict(mb=0), INV), (dict(mb=1 << 27), INV), (dict(s=NAN), INV), (dict(s=INF), INV),
+    (dict(s=3e38), INV), (dict(ks=FAKE), INV), (dict(c=dict(dtype=2)), INV), (dict(c=dict(dtype=2), ks=FAKE, vs=FAKE + 4), INV),
+    (dict(c=dict(num_blocks=1 << 30)), UNS), (dict(rows=0), 0), *[(dict(c=k), w) for k, w in BAD_DESC],
+])
+def test_tree_refusals(lib, kw, want):
+    a = dict(out=FAKE, od=0, q=FAKE, m=FAKE, cu=FAKE, most=8, rows=16, kc=FAKE, vc=FAKE, ks=None, vs=None, bt=FAKE, cl=FAKE,
+             B=2, h=32, mb=8, s=0.1, c={}, ws=FAKE, wb=1 << 30)
+    a.update(kw)
+    c = desc(**a["c"])
+    assert lib.paged_attention_tree(a["out"], a["od"], a["q"], a["m"], a["cu"], a["most"], a["rows"], a["kc"], a["vc"],
+                                    a["ks"], a["vs"], a["bt"], a["cl"], a["B"], a["h"], a["mb"], a["s"], ctypes.byref(c),
+                                    a["ws"], a["wb"], None) == want
+
+
+def test_tree_workspace(lib):
+    size = lambda *a, **k: lib.paged_attention_tree_workspace_size(*a, ctypes.byref(desc(**k)))  # noqa: E731
+    assert size(0, 32, 8) == size(2, 12, 8) == size(2, 32, 65) == size(2, 32, 8, bs=8) == 0
+    # a status word, a record a range, and per range two partials of the rows of a tile: (m, l) and 128 values
+    for heads, most, rows in ((32, 8, 32), (64, 64, 128), (8, 1, 1), (40, 3, 15)):
+        n = size(2, heads, most)
+        assert 304 * rows * 520 <= n <= 304 * rows * 520 + 4096
+        assert n == size(60000, heads, most) == size(2, heads, most, dtype=2)
