@@ -43,7 +43,6 @@ struct TreeParams {
     void *out;      // [total_rows][n_q][128], f32 or bf16
     const uint64_t *mask;  // [total_rows]
     const int32_t *cu_q_lens, *block_tables, *context_lens;
-    const void *v_cache;             // (K comes by its tensor map)
     const float *k_scale, *v_scale;  // FP8 pool only
     uint32_t *status;
     int32_t num_seqs, n_q, n_kv, group, max_blocks, num_blocks, total_rows, max_q_len;
@@ -56,7 +55,8 @@ struct TreeParams {
     float *part_o;              // the same x [128], unnormalised
 };
 cudaError_t tree_prepare_device();
-cudaError_t launch_tree_attention(const CUtensorMap &kmap, const TreeParams &p, bool fp8, cudaStream_t stream);
+cudaError_t launch_tree_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, const TreeParams &p, bool fp8,
+                                  cudaStream_t stream);
 
 // ---- verification of drafted tokens, compaction of the accepted path -----------------
 struct SpecVerifyParams {

@@ -305,9 +305,11 @@ int paged_attention_tree(void *out, int32_t out_dtype, const void *q, const uint
     std::call_once(g_tree_prepared[dev], [&] { g_tree_prep_err[dev] = pkv::tree_prepare_device(); });
     if (g_tree_prep_err[dev] != cudaSuccess) return PKV_ERR_CUDA;
     const int32_t n_kv = cache->num_kv_heads;
-    CUtensorMap kmap;
+    CUtensorMap kmap, vmap;
     if (!(fp8 ? pkv::encode_pool_map_fp8(&kmap, k_cache, cache->num_blocks, n_kv)
-              : pkv::encode_pool_tile_map(&kmap, k_cache, cache->num_blocks, n_kv)))
+              : pkv::encode_pool_tile_map(&kmap, k_cache, cache->num_blocks, n_kv)) ||
+        !(fp8 ? pkv::encode_pool_map_fp8(&vmap, v_cache, cache->num_blocks, n_kv)
+              : pkv::encode_pool_tile_map(&vmap, v_cache, cache->num_blocks, n_kv)))
         return PKV_ERR_CUDA;
     const TreePlan pl = plan_tree(num_q_heads / n_kv, max_q_len, sms);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -317,7 +319,6 @@ int paged_attention_tree(void *out, int32_t out_dtype, const void *q, const uint
     p.cu_q_lens = cu_q_lens;
     p.block_tables = block_tables;
     p.context_lens = context_lens;
-    p.v_cache = v_cache;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.status = reinterpret_cast<uint32_t *>(ws);
@@ -335,7 +336,7 @@ int paged_attention_tree(void *out, int32_t out_dtype, const void *q, const uint
     p.record = reinterpret_cast<int4 *>(ws + kStatusBytes);
     p.part_ml = reinterpret_cast<float2 *>(ws + pl.off_ml);
     p.part_o = reinterpret_cast<float *>(ws + pl.off_o);
-    return finish(pkv::launch_tree_attention(kmap, p, fp8, static_cast<cudaStream_t>(stream)));
+    return finish(pkv::launch_tree_attention(kmap, vmap, p, fp8, static_cast<cudaStream_t>(stream)));
 }
 
 int speculative_verify(int32_t *tokens_out, int32_t *path, int32_t *counts, const float *target_probs,

@@ -18,10 +18,10 @@
 // a second kernel joins.
 //
 // A CTA's warps (hand-offs through mbarriers, every wait bounded):
-//  * 8 fetches K by TMA (one copy for each of a tile's four paged blocks); 12 and 13 fetch V by
-//    16-byte asynchronous copies: one SM's TMA unit delivers 24 bytes a clock, HBM's share of an SM
-//    is 23-28, so a ring on TMA alone never catches up.  The rings run ahead of the pieces.  V rows
-//    of keys that are not the sequence's, or of blocks with an invalid id, come as zeros.
+//  * 8 fetches K and 12 V by TMA (one copy for each of a tile's four paged blocks) into rings that run
+//    ahead of the pieces.  (One warp for both takes 2700 cycles for 64 keys, of which HBM leaves 1400;
+//    V by 16-byte asynchronous copies instead: what any warp reads then waits behind them, a
+//    piece's 128 rows of Q 6 us.)
 //  * 11 plans the CTA's range and fetches the pieces' Q rows (any G); pieces of up to 64 rows have
 //    two places for them in turn.  The next piece's rows are on their way into L2 meanwhile (behind
 //    two full rings a read from HBM takes 5 us).
@@ -37,14 +37,15 @@
 //    rescaled).  P goes back over S as bf16 heads (truncated) and remainders (rounded), P V =
 //    P_hi V + P_lo V: weights to 2^-16.  At a piece's end the groups' (m, l, O) are joined, each
 //    group storing half of the values.
-//  * Keys past ctx and of blocks with an invalid id are masked by index, so stale bytes reach no
-//    result.
+//  * Keys past ctx and of blocks with an invalid id are masked by index and their V rows zeroed in
+//    shared memory, so stale bytes reach no result.
 //
 // FP8 pool (E4M3 codes, one scale per key and head).  K's codes are the B operand as they are; a row of Q
 // is two rows of E4M3 codes, what the first leaves in the second, scaled by the power of two that
 // puts the row's largest value in [2^7, 2^8): exact down to 2^-9 of that value, 2^-17 of it below.
-// 12-15 take every fourth tile of V each: its codes by asynchronous copies, expanded to bf16
-// (exact) into the V ring.  K's scale multiplies the scores, V's the weights that enter P V.
+// V's codes come into a ring of their own, with both scales; 13-15 take every third tile each
+// and expand it to bf16 (exact) into the V ring.  K's scale multiplies the scores, V's the weights that
+// enter P V.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -62,7 +63,7 @@ constexpr int kKeys = 64;          // of a tile
 constexpr int kTileBlocks = kKeys / kBlockSize;
 constexpr int kGroupWarps = 4;     // softmax warps of a group
 constexpr int kPlaces = 4;         // of S in tensor memory
-constexpr int kWarpK = 8, kWarpS = 9, kWarpPv = 10, kWarpQ = 11, kWarpV = 12;
+constexpr int kWarpK = 8, kWarpS = 9, kWarpPv = 10, kWarpQ = 11, kWarpV = 12, kWarpExpand = 13;
 
 constexpr uint32_t kHalfTile = kRows * 128;      // 16 KB: 128 rows x 128 bytes
 constexpr uint32_t kVTile = kKeys * 256;         // 16 KB: 64 bf16 rows of V
@@ -72,22 +73,22 @@ constexpr uint32_t kTmemCols = 512, kTmemO = 256;
 
 template <bool FP8>
 struct Layout {
-    static constexpr int kCopyWarps = FP8 ? 4 : 2;  // that fetch V
-    static constexpr int kThreads = (kWarpV + kCopyWarps) * 32;
+    static constexpr int kExpandWarps = FP8 ? 3 : 0;
+    static constexpr int kThreads = (kWarpExpand + kExpandWarps) * 32;
     static constexpr int kStagesK = 6, kStagesV = FP8 ? 4 : 6;
-    static constexpr int kRaw = 2;         // FP8: tiles of codes that a copying warp has on their way
-    static constexpr int kScaleTiles = 16;  // FP8: places of a tile's scales (its reader is behind by less than 12 tiles)
+    static constexpr int kStagesRaw = FP8 ? 8 : 0;  // of V's codes and both scales
     static constexpr uint32_t kBlk = FP8 ? kCodeBytes : kBlkBytes;  // of the pool
     static constexpr uint32_t kKTile = kTileBlocks * kBlk;
     static constexpr uint32_t kOffQ = 0;  // [value half][128 rows][128 B], FP8: [codes, remainders' codes][128 rows][128 B]
     static constexpr uint32_t kOffK = kOffQ + 2 * kHalfTile;
     static constexpr uint32_t kOffV = kOffK + kStagesK * kKTile;
-    static constexpr uint32_t kOffRaw = kOffV + kStagesV * kVTile;  // FP8: [copying warp][kRaw] tiles of codes
-    static constexpr uint32_t kOffScale = kOffRaw + (FP8 ? kCopyWarps * kRaw * kTileBlocks * kCodeBytes : 0);  // [K, V][64]
-    static constexpr uint32_t kOffRow = kOffScale + (FP8 ? kScaleTiles * 2 * kKeys * 4 : 0);  // FP8: factors of Q's rows, two places
+    static constexpr uint32_t kOffRaw = kOffV + kStagesV * kVTile;
+    static constexpr uint32_t kOffScale = kOffRaw + kStagesRaw * kTileBlocks * kCodeBytes;  // FP8: [tile][K, V][64]
+    static constexpr uint32_t kOffOnes = kOffScale + kStagesRaw * 2 * kKeys * 4;  // FP8: a tile's K scales, all 1
+    static constexpr uint32_t kOffRow = kOffOnes + (FP8 ? kKeys * 4 : 0);  // FP8: factors of Q's rows, two places
     static constexpr uint32_t kOffMl = kOffRow + (FP8 ? 2 * kRows * 4 : 0);  // (m, l) of the groups' rows
     static constexpr uint32_t kOffBar = kOffMl + 2 * kRows * 8;
-    static constexpr int kBars = 2 * kStagesK + 2 * kStagesV + 4 + 3 * kPlaces + 3;
+    static constexpr int kBars = 2 * kStagesK + 2 * kStagesV + 2 * kStagesRaw + 4 + 3 * kPlaces + 3;
     static constexpr uint32_t kOffPlan = kOffBar + 8 * kBars;
     static constexpr uint32_t kBytes = kOffPlan + 64;
     static_assert(kBytes <= 232448, "shared memory of a CTA");
@@ -118,11 +119,21 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
-// 16 bytes asynchronously, or zeros.
-__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void *src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
-                 "r"(valid ? 16 : 0)
-                 : "memory");
+// The bounded wait of mbar_wait, asleep up to 20 us at a time (a poller takes issue slots from the softmax).
+__device__ __forceinline__ bool mbar_sleep_wait(uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    }
 }
 
 // P - head for a pair, head = the packed bf16 pair `h`: exact, since head is P truncated.
@@ -288,7 +299,8 @@ __device__ __forceinline__ void e4m3x16_to_bf16(const uint4 &c, uint4 &a, uint4 
 
 template <bool FP8>
 __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
-    tree_attention_kernel(const __grid_constant__ CUtensorMap kmap, const TreeParams p) {
+    tree_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                          const TreeParams p) {
     using L = Layout<FP8>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -299,7 +311,9 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     auto k_empty = [&](int st) { return bar(L::kStagesK + st); };
     auto v_full = [&](int st) { return bar(2 * L::kStagesK + st); };
     auto v_empty = [&](int st) { return bar(2 * L::kStagesK + L::kStagesV + st); };
-    constexpr int kBarQ = 2 * L::kStagesK + 2 * L::kStagesV;
+    constexpr int kBarRaw = 2 * L::kStagesK + 2 * L::kStagesV, kBarQ = kBarRaw + 2 * L::kStagesRaw;
+    auto raw_full = [&](int st) { return bar(kBarRaw + st); };
+    auto raw_empty = [&](int st) { return bar(kBarRaw + L::kStagesRaw + st); };
     auto q_full = [&](int place) { return bar(kBarQ + place); };
     auto q_empty = [&](int place) { return bar(kBarQ + 2 + place); };
     // of tile j: place j % kPlaces, phase j / kPlaces
@@ -316,13 +330,18 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
 
     if (tid == 0) {
         prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
         for (int st = 0; st < L::kStagesK; ++st) {
             mbar_init(k_full(st), 1);
             mbar_init(k_empty(st), 1);
         }
         for (int st = 0; st < L::kStagesV; ++st) {
-            mbar_init(v_full(st), FP8 ? 1 : L::kCopyWarps);
+            mbar_init(v_full(st), 1);
             mbar_init(v_empty(st), 1);
+        }
+        for (int st = 0; st < L::kStagesRaw; ++st) {
+            mbar_init(raw_full(st), 1);
+            mbar_init(raw_empty(st), 1 + kGroupWarps);  // the expansion, and the softmax of the tile
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full(i), 1);
@@ -339,6 +358,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         *abort_flag = 0u;
         fence_mbar_init();
     }
+    if (FP8 && tid < kKeys) reinterpret_cast<float *>(smem + L::kOffOnes)[tid] = 1.f;
     if (warp == kWarpS) {
         tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tmem_relinquish();
@@ -361,7 +381,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         if (__any_sync(0xffffffffu, mbar_test_wait(b, parity))) return true;
         bool ok = false;
         if (lane == 0 && !*abort_flag) {
-            ok = mbar_wait(b, parity);
+            ok = mbar_sleep_wait(b, parity);
             if (!ok) *abort_flag = 1u;
         }
         return __any_sync(0xffffffffu, ok);
@@ -377,9 +397,16 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         const int blocks = (w.s.ctx + kBlockSize - 1) / kBlockSize, at = t * kTileBlocks + lane;
         return lane < kTileBlocks && at < blocks ? __ldg(p.block_tables + static_cast<int64_t>(w.b) * p.max_blocks + at) : -1;
     };
-    if (warp == kWarpK) {
-        // ---------------- K: lane k < 4 sends for block k of a tile ----------------
-        int j = 0;  // tile of the range
+    if (warp == kWarpK || warp == kWarpV) {
+        // ---------------- copies: lane k < 4 sends for block k of a tile (FP8: with V, for its scales too) ----------------
+        const bool is_k = warp == kWarpK;
+        const bool raw = FP8 && !is_k;
+        const int stages = is_k ? L::kStagesK : raw ? L::kStagesRaw : L::kStagesV;
+        const uint32_t ring = sbase + (is_k ? L::kOffK : raw ? L::kOffRaw : L::kOffV);
+        const uint32_t full0 = is_k ? k_full(0) : raw ? raw_full(0) : v_full(0);
+        const uint32_t empty0 = is_k ? k_empty(0) : raw ? raw_empty(0) : v_empty(0);
+        const CUtensorMap *map = is_k ? &kmap : &vmap;
+        int j = 0, st = 0, use = 0;  // tile of the range; its stage, and the stage's use
         bool ok = true;
         for (; ok && w.more(); w.next(p)) {
             const int blocks = (w.s.ctx + kBlockSize - 1) / kBlockSize, g = w.kv_head();
@@ -388,175 +415,82 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 // (an invalid id fetches block 0; its keys are masked)
                 const int id = static_cast<unsigned>(next) < static_cast<unsigned>(p.num_blocks) ? next : 0;
                 if (t + 1 < w.t1) next = block_id(t + 1);
-                const int st = j % L::kStagesK;
-                if (j >= L::kStagesK && !(ok = warp_wait(k_empty(st), ((j / L::kStagesK) - 1) & 1))) break;
+                if (use > 0 && !(ok = warp_wait(empty0 + 8 * st, (use - 1) & 1))) break;
                 const int load = max(0, min(kTileBlocks, blocks - t * kTileBlocks));
+                const uint32_t full = full0 + 8 * st;
                 if (lane == 0) {
                     if (load > 0)
-                        mbar_arrive_expect_tx(k_full(st), load * L::kBlk);
+                        mbar_arrive_expect_tx(full, load * (L::kBlk + (raw ? 2 * kBlockSize * 4 : 0)));
                     else
-                        mbar_arrive(k_full(st));
+                        mbar_arrive(full);
                 }
                 __syncwarp();
-                const uint32_t dst = sbase + L::kOffK + st * L::kKTile + lane * L::kBlk;
+                const uint32_t dst = ring + (st * kTileBlocks + lane) * L::kBlk;
                 if (lane < load) {
-                    if constexpr (FP8)
-                        tma_load_4d(dst, &kmap, k_full(st), 0, 0, g, id);
-                    else
-                        tma_load_5d(dst, &kmap, k_full(st), 0, 0, 0, 0, id * p.n_kv + g);
+                    if constexpr (FP8) {
+                        tma_load_4d(dst, map, full, 0, 0, g, id);
+                        if (raw) {
+                            const uint32_t scale = sbase + L::kOffScale + (st * 2 * kKeys + lane * kBlockSize) * 4;
+                            const int64_t at = (static_cast<int64_t>(id) * p.n_kv + g) * kBlockSize;
+                            bulk_copy_g2s(scale, p.k_scale + at, kBlockSize * 4, full);
+                            bulk_copy_g2s(scale + kKeys * 4, p.v_scale + at, kBlockSize * 4, full);
+                        }
+                    } else {
+                        tma_load_5d(dst, map, full, 0, 0, 0, 0, id * p.n_kv + g);
+                    }
+                }
+                if (++st == stages) {
+                    st = 0;
+                    ++use;
                 }
             }
         }
         // (given up: the copies still on their way land before the CTA ends)
         if (!ok && lane == 0)
-            for (int i = max(0, j - L::kStagesK); i < j; ++i) mbar_wait(k_full(i % L::kStagesK), (i / L::kStagesK) & 1);
-    } else if (!FP8 && warp >= kWarpV) {
-        // ---------------- V: 16 threads a row, four rows a step ----------------
-        const int t16 = (warp - kWarpV) * 32 + lane, row4 = t16 >> 4, c = t16 & 15;
-        uint32_t to[4];  // of rows row4 + 4 i of a block
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = row4 + 4 * i;
-            to[i] = (r >> 3) * 2048 + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4);
-        }
-        int j = 0, landed = 0;  // tiles sent for; tiles handed on
+            for (int i = max(0, j - stages); i < j; ++i) mbar_wait(full0 + 8 * (i % stages), (i / stages) & 1);
+    } else if (FP8 && warp >= kWarpExpand) {
+        // ---------------- V's codes of every third tile expanded to bf16 ----------------
+        const int x = warp - kWarpExpand;
+        const int row = lane >> 3, c = lane & 7;  // of a block: rows row + 4 i, codes 16 c .. 16 c + 15
+        int j = 0;
         bool ok = true;
-        auto hand_on = [&]() {  // a tile has landed: made visible to the tensor core, an arrival a warp
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(v_full(landed % L::kStagesV));
-            ++landed;
-        };
         for (; ok && w.more(); w.next(p)) {
-            const int g = w.kv_head();
-            int next = block_id(w.t0);
-            for (int t = w.t0; t < w.t1; ++t, ++j) {
-                const int mine = next;
-                if (t + 1 < w.t1) next = block_id(t + 1);
-                const int st = j % L::kStagesV;
-                if (j >= L::kStagesV) {
-                    const uint32_t parity = ((j / L::kStagesV) - 1) & 1;
-                    // A place not free yet: what was sent for is handed on as it lands.
-                    while (landed < j && !__any_sync(0xffffffffu, mbar_test_wait(v_empty(st), parity))) {
-                        if (j - landed >= 3)
-                            asm volatile("cp.async.wait_group 2;" ::: "memory");
-                        else if (j - landed == 2)
-                            asm volatile("cp.async.wait_group 1;" ::: "memory");
-                        else
-                            asm volatile("cp.async.wait_group 0;" ::: "memory");
-                        hand_on();
-                    }
-                    if (!(ok = warp_wait(v_empty(st), parity))) break;
-                }
+            int t = w.t0 + (x + 2 * j) % 3;  // the piece's first tile whose number j + t - t0 is x modulo 3
+            int next = t < w.t1 ? block_id(t) : -1;
+            for (; t < w.t1; t += 3) {
+                const int mine = next, i = j + t - w.t0, raw_st = i % (FP8 ? L::kStagesRaw : 1), st = i % L::kStagesV;
+                if (t + 3 < w.t1) next = block_id(t + 3);
                 const int keys = w.s.ctx - t * kKeys;
-#pragma unroll
+                ok = warp_wait(raw_full(raw_st), (i / (FP8 ? L::kStagesRaw : 1)) & 1);
+                if (ok && i >= L::kStagesV) ok = warp_wait(v_empty(st), ((i / L::kStagesV) - 1) & 1);
+                if (!ok) break;
+#pragma unroll 1
                 for (int k = 0; k < kTileBlocks; ++k) {
                     const int id = __shfl_sync(0xffffffffu, mine, k);
                     const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
-                    const uint8_t *src = static_cast<const uint8_t *>(p.v_cache) +
-                                         (static_cast<int64_t>(good ? id : 0) * p.n_kv + g) * kBlkBytes + row4 * 256 + c * 16;
+                    const uint32_t src = sbase + L::kOffRaw + (raw_st * kTileBlocks + k) * kCodeBytes;
                     const uint32_t dst = sbase + L::kOffV + st * kVTile + k * kBlkBytes;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        cp_async_16_or_zero(dst + to[i], src + i * 1024, good && k * kBlockSize + row4 + 4 * i < keys);
+                    for (int n = 0; n < 4; ++n) {
+                        const int r = row + 4 * n;
+                        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+                        const uint4 code = lds128(src + r * 128 + ((c ^ (r & 7)) << 4));
+                        if (good && k * kBlockSize + r < keys) e4m3x16_to_bf16(code, a, b);
+                        // bf16 chunks 2 c and 2 c + 1 of the row's 16
+                        const uint32_t at = dst + (r >> 3) * 2048 + (c >> 2) * 1024 + (r & 7) * 128;
+                        sts128(at + (((2 * (c & 3)) ^ (r & 7)) << 4), a);
+                        sts128(at + (((2 * (c & 3) + 1) ^ (r & 7)) << 4), b);
+                    }
                 }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                if (landed + 2 < j) {  // (three tiles on their way)
-                    asm volatile("cp.async.wait_group 3;" ::: "memory");
-                    hand_on();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(v_full(st));
+                    mbar_arrive(raw_empty(raw_st));
                 }
             }
+            j += w.t1 - w.t0;
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        while (ok && landed < j) hand_on();
-    } else if (FP8 && warp >= kWarpV) {
-        // ---------------- V's codes: every fourth tile, expanded to bf16; its scales and K's ----------------
-        const int x = warp - kWarpV;
-        const uint32_t raw0 = sbase + L::kOffRaw + x * L::kRaw * kTileBlocks * kCodeBytes;
-        // This lane's 16-byte pieces of a block: row (lane >> 3) + 4 i, chunk lane & 7.
-        const int row = lane >> 3, c = lane & 7;
-        Walk ahead = w;  // of the tile sent for next
-        int ta = ahead.t0, ja = 0;
-        auto skip = [&](Walk &walk, int &t, int &j, int n) {  // n tiles on
-            while (n > 0 && walk.more()) {
-                const int step = min(n, walk.t1 - t);
-                t += step;
-                j += step;
-                n -= step;
-                if (t == walk.t1) {
-                    walk.next(p);
-                    t = walk.t0;
-                }
-            }
-        };
-        auto send = [&]() {  // the codes and scales of tile ja, then on to this warp's next
-            if (ahead.more()) {
-                const int g = ahead.kv_head(), blocks = (ahead.s.ctx + kBlockSize - 1) / kBlockSize;
-                const int at = ta * kTileBlocks + lane;
-                const int mine = lane < kTileBlocks && at < blocks
-                                     ? __ldg(p.block_tables + static_cast<int64_t>(ahead.b) * p.max_blocks + at)
-                                     : -1;
-                const uint32_t raw = raw0 + ((ja >> 2) % L::kRaw) * kTileBlocks * kCodeBytes;
-                const uint32_t scale = sbase + L::kOffScale + (ja % L::kScaleTiles) * 2 * kKeys * 4;
-#pragma unroll
-                for (int k = 0; k < kTileBlocks; ++k) {
-                    const int id = __shfl_sync(0xffffffffu, mine, k);
-                    const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
-                    const int64_t tile = static_cast<int64_t>(good ? id : 0) * p.n_kv + g;
-                    const uint8_t *src = static_cast<const uint8_t *>(p.v_cache) + tile * kCodeBytes + lane * 16;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) cp_async_16(raw + k * kCodeBytes + i * 512 + lane * 16, src + i * 512);
-                    if (lane < 8)
-                        cp_async_16(scale + (lane >> 2) * kKeys * 4 + k * 64 + (lane & 3) * 16,
-                                    (lane < 4 ? p.k_scale : p.v_scale) + tile * kBlockSize + (lane & 3) * 4);
-                }
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-            skip(ahead, ta, ja, L::kCopyWarps);
-        };
-        int t = w.t0, j = 0;
-        skip(ahead, ta, ja, x);
-        skip(w, t, j, x);
-        for (int i = 0; i < L::kRaw; ++i) send();
-        bool ok = true;
-        while (ok && w.more()) {
-            const int st = j % L::kStagesV;
-            const int mine = block_id(t);
-            const int keys = w.s.ctx - t * kKeys;
-            if (j >= L::kStagesV && !(ok = warp_wait(v_empty(st), ((j / L::kStagesV) - 1) & 1))) break;
-            asm volatile("cp.async.wait_group %0;" ::"n"(L::kRaw - 1) : "memory");
-            __syncwarp();
-            const uint32_t raw = raw0 + ((j >> 2) % L::kRaw) * kTileBlocks * kCodeBytes;
-            const uint32_t scale = sbase + L::kOffScale + (j % L::kScaleTiles) * 2 * kKeys * 4;
-#pragma unroll
-            for (int k = 0; k < kTileBlocks; ++k) {
-                const int id = __shfl_sync(0xffffffffu, mine, k);
-                const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
-                // a key that is not the sequence's: scales 0, values 0
-                if (lane < kBlockSize && (!good || k * kBlockSize + lane >= keys)) {
-                    sts32(scale + (k * kBlockSize + lane) * 4, 0u);
-                    sts32(scale + (kKeys + k * kBlockSize + lane) * 4, 0u);
-                }
-                const uint32_t dst = sbase + L::kOffV + st * kVTile + k * kBlkBytes;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = row + 4 * i;
-                    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-                    const uint4 code = lds128(raw + k * kCodeBytes + i * 512 + lane * 16);
-                    if (good && k * kBlockSize + r < keys) e4m3x16_to_bf16(code, a, b);
-                    // values 16 c .. 16 c + 15 of row r: bf16 chunks 2 c and 2 c + 1 of 16
-                    const uint32_t at = dst + (r >> 3) * 2048 + (c >> 2) * 1024 + (r & 7) * 128;
-                    sts128(at + (((2 * (c & 3)) ^ (r & 7)) << 4), a);
-                    sts128(at + (((2 * (c & 3) + 1) ^ (r & 7)) << 4), b);
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(v_full(st));
-            send();
-            skip(w, t, j, L::kCopyWarps);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (warp == kWarpQ) {
         // ---------------- the pieces' Q rows: 16 lanes a row, two rows a step ----------------
         const int c = lane & 15;
@@ -590,14 +524,18 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     return __ldg(reinterpret_cast<const uint4 *>(
                         base + (static_cast<int64_t>(at_row / G) * p.n_q + at_row % G) * kHeadDim));
                 };
-                uint4 x[4];
-                for (int r0 = 0; r0 < rows; r0 += 8) {
+                uint4 ahead[4];  // the rows of the next four steps
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = read(r0 + 2 * i + (lane >> 4));
+                for (int i = 0; i < 4; ++i) ahead[i] = read(2 * i + (lane >> 4));
+#pragma unroll 1
+                for (int r0 = 0; r0 < rows; r0 += 2) {
+                    const uint4 x = ahead[0];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = r0 + 2 * i + (lane >> 4);
-                        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    for (int i = 0; i < 3; ++i) ahead[i] = ahead[i + 1];
+                    ahead[3] = read(r0 + 8 + (lane >> 4));
+                    {
+                        const int r = r0 + (lane >> 4);
+                        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
                         float v[8], most = 0.f;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -747,60 +685,72 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 const uint32_t bad = __ballot_sync(0xffffffffu, wrong);
                 if (t + 2 < w.t1) id = block_id(t + 2);
                 if (bad && quarter == 0 && lane == 0 && p.status) atomicOr(p.status, kStatusBadBlockId);
-                if constexpr (FP8) alive = alive && warp_wait(v_full(j % L::kStagesV), (j / L::kStagesV) & 1);  // (the scales)
+                if constexpr (FP8) alive = alive && warp_wait(raw_full(j % L::kStagesRaw), (j / L::kStagesRaw) & 1);  // (the scales)
                 alive = alive && warp_wait(s_full(j), phase(j));
                 if (!alive) continue;
                 tc_fence_after();
                 const uint32_t t_s = lane_base + kKeys * (j % kPlaces);
                 if (busy) {
                     if constexpr (FP8) {
-                        if (t == t_first)
-                            sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::kOffRow)[q_place(piece) * kRows + r];
+                        if (t == t_first) sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::kOffRow)[q_place(piece) * kRows + r];
                     }
-                    const uint32_t scales = sbase + L::kOffScale + (j % L::kScaleTiles) * 2 * kKeys * 4;
-                    const bool whole = t * kKeys + kKeys <= prefix && !bad;  // every row sees every key (CTA-uniform)
-                    uint32_t v[64];
-                    tmem_ld_32x32b_x64(t_s, v);
-                    if constexpr (FP8) {  // scores times each key's K scale
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const uint4 f = lds128(scales + 16 * i);
-                            const float2 x = fmul2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])),
-                                                   make_float2(__uint_as_float(f.x), __uint_as_float(f.y)));
-                            const float2 y = fmul2(make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])),
-                                                   make_float2(__uint_as_float(f.z), __uint_as_float(f.w)));
-                            v[4 * i] = __float_as_uint(x.x);
-                            v[4 * i + 1] = __float_as_uint(x.y);
-                            v[4 * i + 2] = __float_as_uint(y.x);
-                            v[4 * i + 3] = __float_as_uint(y.y);
-                        }
-                    }
-                    // bits of the visible keys
-                    uint64_t seen = ~0ull;
-                    if (!whole) {
+                    const uint32_t scales = sbase + L::kOffScale + (j % (FP8 ? L::kStagesRaw : 1)) * 2 * kKeys * 4;
+                    float2 sl2v = make_float2(sl2, sl2);
+                    uint32_t k_scales = scales;
+                    // Tiles that not every row sees whole: the scores are scaled and the hidden ones -inf before the pass below,
+                    // which then scales them by 1.  (A loop of its own, once or twice a sequence: in the pass, whose code the
+                    // instruction caches have to hold beside six other roles', selects cost every tile.)
+                    if (t * kKeys + kKeys > prefix || bad) {
                         const int at = t * kKeys - prefix;  // node of the tile's first key
-                        if (at >= 0)
-                            seen = at < 64 ? mask >> at : 0;
-                        else if (at > -64)
-                            seen = ((1ull << -at) - 1) | (mask << -at);
-#pragma unroll
+                        uint64_t seen = at >= 0 ? (at < 64 ? mask >> at : 0) : at > -64 ? ((1ull << -at) - 1) | (mask << -at) : ~0ull;
                         for (int k = 0; k < kTileBlocks; ++k)
                             if ((bad >> k) & 1) seen &= ~(0xffffull << (16 * k));
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t x[16];
+                            tmem_ld_32x32b_x16(t_s + 16 * c, x);
+                            const uint32_t bits = static_cast<uint32_t>(seen >> (16 * c));
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                float f = sl2;
+                                if constexpr (FP8) f *= lds_f32(scales + 4 * (16 * c + k));
+                                x[k] = (bits >> k) & 1 ? __float_as_uint(__uint_as_float(x[k]) * f) : 0xff800000u;
+                            }
+                            tmem_st_32x32b_x16(t_s + 16 * c, x);
+                        }
+                        tmem_wait_st();
+                        sl2v = make_float2(1.f, 1.f);
+                        if constexpr (FP8) {
+                            k_scales = sbase + L::kOffOnes;
+                            // V scales that belong to no key may be anything: 1 (every warp writes the same)
+                            for (int k = lane; k < kKeys; k += 32)
+                                if (t * kKeys + k >= w.s.ctx || ((bad >> (k >> 4)) & 1)) sts32(scales + 4 * (kKeys + k), 0x3f800000u);
+                            fence_proxy_async_smem();  // (the next copy there comes behind)
+                            __syncwarp();
+                        }
                     }
-                    // the row's largest score (the least, should the scale be below 0)
+                    uint32_t v[64];
+                    tmem_ld_32x32b_x64(t_s, v);
+                    // scores in the log2 domain (FP8: times each key's K scale), and the row's largest
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    if (whole && p.scale_log2 >= 0.f) {
 #pragma unroll
-                        for (int k = 0; k < 64; k += 2)
-                            mx[(k >> 1) & 3] = fmax3(mx[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                    } else {
-                        const uint32_t flip = p.scale_log2 < 0.f ? 0x80000000u : 0u;
-#pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            mx[k & 3] = fmaxf(mx[k & 3], (seen >> k) & 1 ? __uint_as_float(v[k] ^ flip) : -INFINITY);
+                    for (int i = 0; i < 32; i += 2) {
+                        float2 f0 = sl2v, f1 = sl2v;
+                        if constexpr (FP8) {
+                            const uint4 f = lds128(k_scales + 8 * i);
+                            f0 = fmul2(make_float2(__uint_as_float(f.x), __uint_as_float(f.y)), sl2v);
+                            f1 = fmul2(make_float2(__uint_as_float(f.z), __uint_as_float(f.w)), sl2v);
+                        }
+                        const float2 x = fmul2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f0);
+                        const float2 y = fmul2(make_float2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3])), f1);
+                        v[2 * i] = __float_as_uint(x.x);
+                        v[2 * i + 1] = __float_as_uint(x.y);
+                        v[2 * i + 2] = __float_as_uint(y.x);
+                        v[2 * i + 3] = __float_as_uint(y.y);
+                        mx[i & 2] = fmax3(mx[i & 2], x.x, x.y);
+                        mx[(i & 2) + 1] = fmax3(mx[(i & 2) + 1], y.x, y.y);
                     }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    const float mt = top == -INFINITY ? -INFINITY : top * fabsf(sl2);
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     float alpha = 1.f;
                     if (mt > m + 8.f) {
                         alpha = fast_exp2(m - mt);  // (0 where m is -inf)
@@ -821,30 +771,31 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                             }
                         }
                     }
-                    // P = 2^(s scale log2(e) - m) over S, and the row's sum
+                    // P = 2^(s - m) over S, and the row's sum
                     const float mu = m == -INFINITY ? 0.f : m;
-                    const float2 sl2v = make_float2(sl2, sl2), nmu = make_float2(-mu, -mu);
+                    const float2 nmu = make_float2(-mu, -mu);
                     float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t pk[32];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
+                        for (int e = 0; e < 16; e += 2) {
                             const int k = 32 * c + 2 * e;
-                            const float2 x = ffma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), sl2v, nmu);
-                            float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                            if (!whole) {
-                                if (!((seen >> k) & 1)) pr.x = 0.f;
-                                if (!((seen >> (k + 1)) & 1)) pr.y = 0.f;
+                            const float2 x = fadd2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), nmu);
+                            const float2 y = fadd2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), nmu);
+                            float2 px = make_float2(fast_exp2(x.x), fast_exp2(x.y)), py = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                            rs0 = fadd2(rs0, px);
+                            rs1 = fadd2(rs1, py);
+                            if constexpr (FP8) {  // (the sum keeps the plain weights)
+                                const uint4 f = lds128(scales + (kKeys + k) * 4);
+                                px = fmul2(px, make_float2(__uint_as_float(f.x), __uint_as_float(f.y)));
+                                py = fmul2(py, make_float2(__uint_as_float(f.z), __uint_as_float(f.w)));
                             }
-                            if (e & 1)
-                                rs1 = fadd2(rs1, pr);
-                            else
-                                rs0 = fadd2(rs0, pr);
-                            if constexpr (FP8) pr = fmul2(pr, lds_f32x2(scales + (kKeys + k) * 4));  // (the sum keeps the plain weights)
-                            pk[e] = __byte_perm(__float_as_uint(pr.x), __float_as_uint(pr.y), 0x7632);
-                            const float2 rest = minus_bf16x2(pr, pk[e]);
-                            pk[16 + e] = pack_bf16x2(rest.x, rest.y);
+                            pk[e] = __byte_perm(__float_as_uint(px.x), __float_as_uint(px.y), 0x7632);
+                            pk[e + 1] = __byte_perm(__float_as_uint(py.x), __float_as_uint(py.y), 0x7632);
+                            const float2 ex = minus_bf16x2(px, pk[e]), ey = minus_bf16x2(py, pk[e + 1]);
+                            pk[16 + e] = pack_bf16x2(ex.x, ex.y);
+                            pk[17 + e] = pack_bf16x2(ey.x, ey.y);
                         }
                         tmem_st_32x32b_x32(t_s + 32 * c, pk);
                     }
@@ -852,9 +803,28 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     l = l * alpha + (rs.x + rs.y);
                     tmem_wait_st();
                 }
+                // V rows of keys that are not the sequence's, or of a bad block: zeros before the P V reads them (FP8: by the
+                // expansion)
+                const int past = w.s.ctx - t * kKeys;
+                if (!FP8 && (past < kKeys || bad)) {
+                    alive = warp_wait(v_full(j % L::kStagesV), (j / L::kStagesV) & 1);
+                    if (!alive) continue;
+                    const uint32_t vb = sbase + L::kOffV + (j % L::kStagesV) * kVTile;
+                    for (int i = r; i < kKeys * 16; i += kGroupWarps * 32) {
+                        const int key = i >> 4, ch = i & 15;  // (all 16 chunks of a row: the swizzle is moot)
+                        if (key >= past || ((bad >> (key >> 4)) & 1u))
+                            sts128(vb + (key >> 4) * kBlkBytes + ((key >> 3) & 1) * 2048 + (ch >> 3) * 1024 + (key & 7) * 128 +
+                                       (ch & 7) * 16,
+                                   make_uint4(0u, 0u, 0u, 0u));
+                    }
+                    fence_proxy_async_smem();
+                }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(j));
+                if (lane == 0) {
+                    mbar_arrive(p_full(j));
+                    if constexpr (FP8) mbar_arrive(raw_empty(j % L::kStagesRaw));  // (the scales have been read)
+                }
             }
             // ---- the piece's end: both groups' parts joined; group a stores the values 64 a .. 64 a + 63 ----
             const int tiles = w.t1 - w.t0;
@@ -1011,11 +981,12 @@ cudaError_t tree_prepare_device() {
                                 static_cast<int>(Layout<true>::kBytes));
 }
 
-cudaError_t launch_tree_attention(const CUtensorMap &kmap, const TreeParams &p, bool fp8, cudaStream_t stream) {
+cudaError_t launch_tree_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, const TreeParams &p, bool fp8,
+                                  cudaStream_t stream) {
     const cudaError_t e = fp8 ? launch_pdl(tree_attention_kernel<true>, dim3(p.ranges), dim3(Layout<true>::kThreads),
-                                           Layout<true>::kBytes, stream, kmap, p)
+                                           Layout<true>::kBytes, stream, kmap, vmap, p)
                               : launch_pdl(tree_attention_kernel<false>, dim3(p.ranges), dim3(Layout<false>::kThreads),
-                                           Layout<false>::kBytes, stream, kmap, p);
+                                           Layout<false>::kBytes, stream, kmap, vmap, p);
     if (e != cudaSuccess) return e;
     return launch_pdl(tree_merge_kernel, dim3(p.ranges, (p.part_rows + kMergeRows - 1) / kMergeRows), dim3(kMergeRows * 32), 0,
                       stream, p);
