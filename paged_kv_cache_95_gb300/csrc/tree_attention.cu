@@ -22,9 +22,9 @@
 //    ahead of the pieces.  (One warp for both takes 2700 cycles for 64 keys, of which HBM leaves 1400;
 //    V by 16-byte asynchronous copies instead: what any warp reads then waits behind them, a
 //    piece's 128 rows of Q 6 us.)
-//  * 11 plans the CTA's range and fetches the pieces' Q rows (any G); pieces of up to 64 rows have
-//    two places for them in turn.  The next piece's rows are on their way into L2 meanwhile (behind
-//    two full rings a read from HBM takes 5 us).
+//  * 11 plans the CTA's range and fetches the pieces' Q rows (any G), a piece ahead into two places
+//    in turn; the first piece's come by the softmax warps, before the rings fill (behind full rings
+//    any read takes 5 us).
 //  * 9 issues S = Q K^T, 10 P V (run whole, one elected lane issues: descriptors stay in uniform
 //    registers; one warp for both took 3500 cycles for 128 keys, of which HBM leaves 2800).  Tensor
 //    memory: S of tile j in [64 (j & 3), +64), O of the even and of the odd tiles in [256, +128) and
@@ -44,8 +44,10 @@
 // is two rows of E4M3 codes, what the first leaves in the second, scaled by the power of two that
 // puts the row's largest value in [2^7, 2^8): exact down to 2^-9 of that value, 2^-17 of it below.
 // V's codes come into a ring of their own, with both scales; 13-15 take every third tile each
-// and expand it to bf16 (exact) into the V ring.  K's scale multiplies the scores, V's the weights that
-// enter P V.
+// and expand it to fp16 (exact) into the V ring.  K's scale multiplies the scores, V's the weights,
+// which enter P V rounded to fp16 (2^-12; as bf16 heads and remainders of V in bf16 a tile took
+// 1.4 times the instructions).  The reference m counts the exponent of a tile's largest V scale in, so that
+// weights times scales stay below 2^9.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -71,16 +73,23 @@ constexpr uint32_t kBlkBytes = 4096;             // one paged (block, head) tile
 constexpr uint32_t kCodeBytes = 2048;            // the same of codes
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;
 
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 template <bool FP8>
 struct Layout {
     static constexpr int kExpandWarps = FP8 ? 3 : 0;
     static constexpr int kThreads = (kWarpExpand + kExpandWarps) * 32;
-    static constexpr int kStagesK = 6, kStagesV = FP8 ? 4 : 6;
-    static constexpr int kStagesRaw = FP8 ? 8 : 0;  // of V's codes and both scales
+    static constexpr int kStagesK = FP8 ? 6 : 5, kStagesV = FP8 ? 4 : 5;
+    static constexpr int kStagesRaw = FP8 ? 5 : 0;  // of V's codes and both scales
     static constexpr uint32_t kBlk = FP8 ? kCodeBytes : kBlkBytes;  // of the pool
     static constexpr uint32_t kKTile = kTileBlocks * kBlk;
-    static constexpr uint32_t kOffQ = 0;  // [value half][128 rows][128 B], FP8: [codes, remainders' codes][128 rows][128 B]
-    static constexpr uint32_t kOffK = kOffQ + 2 * kHalfTile;
+    // Two places of [value half][128 rows][128 B], FP8: [codes, remainders' codes][128 rows][128 B]
+    static constexpr uint32_t kOffQ = 0, kQTile = 2 * kHalfTile;
+    static constexpr uint32_t kOffK = kOffQ + 2 * kQTile;
     static constexpr uint32_t kOffV = kOffK + kStagesK * kKTile;
     static constexpr uint32_t kOffRaw = kOffV + kStagesV * kVTile;
     static constexpr uint32_t kOffScale = kOffRaw + kStagesRaw * kTileBlocks * kCodeBytes;  // FP8: [tile][K, V][64]
@@ -88,9 +97,10 @@ struct Layout {
     static constexpr uint32_t kOffRow = kOffOnes + (FP8 ? kKeys * 4 : 0);  // FP8: factors of Q's rows, two places
     static constexpr uint32_t kOffMl = kOffRow + (FP8 ? 2 * kRows * 4 : 0);  // (m, l) of the groups' rows
     static constexpr uint32_t kOffBar = kOffMl + 2 * kRows * 8;
-    static constexpr int kBars = 2 * kStagesK + 2 * kStagesV + 2 * kStagesRaw + 4 + 3 * kPlaces + 3;
+    static constexpr int kBarRaw = 2 * kStagesK + 2 * kStagesV, kBarQ = kBarRaw + 2 * kStagesRaw, kBarS = kBarQ + 4;
+    static constexpr int kBarOFree = kBarS + 3 * kPlaces, kBarOReady = kBarOFree + 1, kBars = kBarOFree + 5;
     static constexpr uint32_t kOffPlan = kOffBar + 8 * kBars;
-    static constexpr uint32_t kBytes = kOffPlan + 64;
+    static constexpr uint32_t kBytes = kOffPlan + 96;
     static_assert(kBytes <= 232448, "shared memory of a CTA");
     static_assert(kOffK % 1024 == 0 && kKTile % 1024 == 0 && kOffV % 1024 == 0 && kOffPlan % 8 == 0, "alignment");
 };
@@ -98,7 +108,8 @@ struct Layout {
 // Instruction descriptors: D f32; M = 128, N = 64 (S) or 128 (P V).
 constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | ((64u >> 3) << 17) | ((128u >> 4) << 24);  // bf16
 constexpr uint32_t kIdescS8 = (1u << 4) | ((64u >> 3) << 17) | ((128u >> 4) << 24);                         // E4M3
-constexpr uint32_t kIdescPV = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);  // V MN-major
+constexpr uint32_t kIdescPV = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);  // bf16, V MN-major
+constexpr uint32_t kIdescPV16 = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);               // the same in fp16
 
 // Shared-memory matrix descriptor for a 128-byte-swizzled canonical layout.
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -134,6 +145,23 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint32_t bar, uint32_t parity) {
         if (ok) return true;
         if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
     }
+}
+
+// A whole warp waits for a barrier's phase, within a bound, and gives up at once after another role gave up.
+// (What is complete already costs one test; then lane 0 alone polls.)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag) {
+    if (__any_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    bool ok = false;
+    if ((threadIdx.x & 31) == 0 && !*abort_flag) {
+        ok = mbar_sleep_wait(bar, parity);
+        if (!ok) *abort_flag = 1u;
+    }
+    return __any_sync(0xffffffffu, ok);
+}
+
+// The softmax warps of both groups.
+__device__ __forceinline__ void softmax_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(2 * kGroupWarps * 32) : "memory");
 }
 
 // P - head for a pair, head = the packed bf16 pair `h`: exact, since head is P truncated.
@@ -175,9 +203,10 @@ __device__ __forceinline__ Sequence load_sequence(const TreeParams &p, int b) {
 
 // A CTA's range of tiles: the unit it starts in, and its length.
 struct Plan {
-    int b, unit, tile, count;
     int64_t begin, total;  // of the range; tiles of the whole call
-    int ranges;            // that are not empty
+    int b, unit, tile, count;
+    int ranges;  // that are not empty
+    Sequence s;  // b's
 };
 
 // The pieces of a range, one after the other; every role walks them by itself.
@@ -189,7 +218,7 @@ struct Walk {
         unit = plan.unit;
         t0 = plan.tile;
         left = plan.count;
-        if (left > 0) s = load_sequence(p, b);
+        s = plan.s;
         t1 = min(s.tiles, t0 + left);
     }
     __device__ __forceinline__ bool more() const { return left > 0; }
@@ -209,34 +238,29 @@ struct Walk {
     __device__ __forceinline__ int rows(const TreeParams &p) const { return min(kRows, s.n * p.group - row_tile() * kRows); }
 };
 
-// The range of this CTA, by one warp: tiles of all sequences, then the sequence that the range starts in.  (The
-// first 128 sequences are looked at once; dividends that fit 32 bits are divided in them: a plan of 64 sequences is
-// on the way of every call.)
-constexpr int kPlanHeld = 4;
+// The range of this CTA, by one warp: tiles of all sequences, then the sequence that the range starts in.  (On the way
+// of every call, with cold instruction caches: short code, and dividends that fit 32 bits divided in them.)
 __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
     if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
     return x / y;
 }
 __device__ Plan make_plan(const TreeParams &p, int lane) {
     Plan plan{};
-    uint32_t wrong = 0;
-    auto load = [&](int b, int &tiles) -> int64_t {  // tiles of all of a sequence's units
-        tiles = 1;
-        if (b >= p.num_seqs) return 0;
-        const Sequence s = load_sequence(p, b);
-        wrong |= s.wrong;
-        tiles = s.tiles;
+    Sequence s{};
+    auto load = [&](int b) -> int64_t {  // tiles of all of a sequence's units
+        s.tiles = 1;
+        s.units = 0;
+        if (b < p.num_seqs) s = load_sequence(p, b);
         return static_cast<int64_t>(s.units) * s.tiles;
     };
-    int64_t held[kPlanHeld], total = 0;
-    int held_tiles[kPlanHeld];
-#pragma unroll
-    for (int i = 0; i < kPlanHeld; ++i) total += held[i] = load(32 * i + lane, held_tiles[i]);
-    for (int b = 32 * kPlanHeld + lane; b < p.num_seqs; b += 32) {
-        int tiles;
-        total += load(b, tiles);
+    int64_t mine = 0, total = 0;
+    uint32_t wrong = 0;
+#pragma unroll 1
+    for (int b = lane; b < p.num_seqs; b += 32) {
+        total += mine = load(b);
+        wrong |= s.wrong;
     }
-#pragma unroll
+#pragma unroll 1
     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
     if (wrong && blockIdx.x == 0 && p.status) atomicOr(p.status, wrong);
     plan.total = total;
@@ -245,9 +269,11 @@ __device__ Plan make_plan(const TreeParams &p, int lane) {
     plan.begin = divide(total * blockIdx.x, plan.ranges);
     plan.count = static_cast<int>(divide(total * (blockIdx.x + 1), plan.ranges) - plan.begin);
     int64_t before = 0;
-    auto find = [&](int b0, int64_t mine, int tiles) -> bool {  // the range starts in one of the 32 sequences from b0 on
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+        if (p.num_seqs > 32) mine = load(b0 + lane);  // (else it is there)
         int64_t upto = mine;
-#pragma unroll
+#pragma unroll 1
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
             if (lane >= off) upto += y;
@@ -255,52 +281,199 @@ __device__ Plan make_plan(const TreeParams &p, int lane) {
         upto += before;
         const uint32_t past = __ballot_sync(0xffffffffu, upto > plan.begin);
         before = __shfl_sync(0xffffffffu, upto, 31);
-        if (!past) return false;
-        const int who = __ffs(past) - 1;
-        const int64_t inside = __shfl_sync(0xffffffffu, plan.begin - (upto - mine), who);
-        tiles = __shfl_sync(0xffffffffu, tiles, who);
-        plan.b = b0 + who;
-        plan.unit = static_cast<int>(divide(inside, tiles));
-        plan.tile = static_cast<int>(inside - static_cast<int64_t>(plan.unit) * tiles);
-        return true;
-    };
-#pragma unroll
-    for (int i = 0; i < kPlanHeld; ++i)
-        if (32 * i < p.num_seqs && find(32 * i, held[i], held_tiles[i])) return plan;
-    for (int b0 = 32 * kPlanHeld; b0 < p.num_seqs; b0 += 32) {
-        int tiles;
-        const int64_t mine = load(b0 + lane, tiles);
-        if (find(b0, mine, tiles)) return plan;
+        if (past) {  // the range starts in one of these 32 sequences
+            const int who = __ffs(past) - 1;
+            plan.b = b0 + who;
+            if (lane == who) {
+                const int64_t inside = plan.begin - (upto - mine);
+                plan.unit = static_cast<int>(divide(inside, s.tiles));
+                plan.tile = static_cast<int>(inside - static_cast<int64_t>(plan.unit) * s.tiles);
+                plan.s = s;
+            }
+            return plan;
+        }
     }
     plan.count = 0;  // (not reached: begin < total)
     return plan;
 }
 
-// Sixteen E4M3 codes to bf16 (exact: E4M3 values are bf16 values): a holds values 0 .. 7, b 8 .. 15.
-__device__ __forceinline__ void e4m3x16_to_bf16(const uint4 &c, uint4 &a, uint4 &b) {
-    auto two = [](uint32_t f16x2) {
-        const float2 f = unpack_f16x2(f16x2);
-        return pack_bf16x2(f.x, f.y);
+// Sixteen E4M3 codes to fp16 (exact): a holds values 0 .. 7, b 8 .. 15.
+__device__ __forceinline__ void e4m3x16_to_f16(const uint4 &c, uint4 &a, uint4 &b) {
+    e4m3x4_to_f16x2x2(c.x, a.x, a.y);
+    e4m3x4_to_f16x2x2(c.y, a.z, a.w);
+    e4m3x4_to_f16x2x2(c.z, b.x, b.y);
+    e4m3x4_to_f16x2x2(c.w, b.z, b.w);
+}
+
+// The Q rows first .. first + rows - 1 of a (sequence, KV head) into the tile at dst, 16 lanes a row: the rows 2 part, 2 part + 1,
+// 2 (part + parts), .. by one warp.  FP8: as two rows of E4M3 codes (dst, dst + 16 KB), and the factor that undoes the
+// row's power of two.  (Not inlined: two roles call it.)
+template <bool FP8>
+__device__ __noinline__ void load_q(const TreeParams &p, int row0, int first, int rows, int head0, uint32_t dst, float *factor,
+                                    int part, int parts) {
+    const int lane = threadIdx.x & 31, c = lane & 15, G = p.group;
+    const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(p.q) + 8 * c +
+                                (static_cast<int64_t>(row0) * p.n_q + head0) * kHeadDim;
+    auto source = [&](int r) -> const __nv_bfloat16 * {  // (rows past the last are read as the last)
+        const int at = first + min(r, rows - 1), node = at / G;
+        return base + (static_cast<int64_t>(node) * p.n_q + (at - node * G)) * kHeadDim;
     };
-    uint32_t x, y;
-    e4m3x4_to_f16x2x2(c.x, x, y);
-    a.x = two(x);
-    a.y = two(y);
-    e4m3x4_to_f16x2x2(c.y, x, y);
-    a.z = two(x);
-    a.w = two(y);
-    e4m3x4_to_f16x2x2(c.z, x, y);
-    b.x = two(x);
-    b.y = two(y);
-    e4m3x4_to_f16x2x2(c.w, x, y);
-    b.z = two(x);
-    b.w = two(y);
+    const int step = 2 * parts, first_r = 2 * part + (lane >> 4);
+    // Row r's 16-byte chunk c: half c / 8 (FP8: of the raw values too, whose place the codes take).
+    auto place = [&](int r) { return dst + (c >> 3) * kHalfTile + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+#pragma unroll 4
+    for (int r = first_r; r < rows; r += step) cp_async_16(place(r), source(r));
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (FP8) {
+        // (both halves of the warp take as many steps: the maximum goes by shuffles; a lane reads what it fetched)
+#pragma unroll 1
+        for (int r = first_r; r - (lane >> 4) < rows; r += step) {
+            const uint4 raw = lds128(place(min(r, kRows - 1)));
+            const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+            float v[8], most = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[2 * k] = __uint_as_float(u[k] << 16);
+                v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+                most = fmaxf(most, fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
+            }
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+            // 2^e puts the largest value in [2^7, 2^8) (both powers are normal numbers)
+            const int e = min(126, max(-119, 7 - (static_cast<int>(__float_as_uint(most) >> 23) - 127)));
+            // (a scale below 0 negates the row: the softmax's is above)
+            const float up = __uint_as_float((static_cast<uint32_t>(127 + e) << 23) | (p.scale_log2 < 0.f ? 0x80000000u : 0u));
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = v[4 * k + i] * up;
+                hi[k] = f32x2_to_e4m3x2(x[0], x[1]) | (f32x2_to_e4m3x2(x[2], x[3]) << 16);
+                uint32_t f0, f1;
+                e4m3x4_to_f16x2x2(hi[k], f0, f1);
+                const float2 h0 = unpack_f16x2(f0), h1 = unpack_f16x2(f1);
+                lo[k] = f32x2_to_e4m3x2(x[0] - h0.x, x[1] - h0.y) | (f32x2_to_e4m3x2(x[2] - h1.x, x[3] - h1.y) << 16);
+            }
+            if (r < rows) {
+                const uint32_t to = dst + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+                sts32(to, hi[0]);
+                sts32(to + 4, hi[1]);
+                sts32(to + kHalfTile, lo[0]);
+                sts32(to + kHalfTile + 4, lo[1]);
+                // (a row with an infinity has no finite scores: NaN, as a code of 448 would not say)
+                if (c == 0)
+                    factor[r] = most > 3.4e38f ? __uint_as_float(0x7fc00000u)
+                                               : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            }
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// The end of a piece: the groups' parts joined, values 64 a .. 64 a + 63 stored by group a; by a softmax warp whose lanes'
+// tensor memory begins at lane_base.  It runs behind the group's first tile of the next piece, whose scores are
+// there long before the last P V of this one.  False where the wait for that ran out.  (Not inlined: one copy, for the
+// instruction caches.)
+struct End {
+    int64_t to;  // this lane's row among the heads' rows of out, or among the partials
+    int piece, rows;
+    bool had0, had1, direct;  // the groups' tiles; a whole unit
+};
+template <bool FP8>
+__device__ __noinline__ bool finish_piece(const TreeParams &p, const End end, uint32_t sbase, uint32_t lane_base, bool alive) {
+    using L = Layout<FP8>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, a = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const float2 *ml = reinterpret_cast<const float2 *>(smem + L::kOffMl);
+    const uint32_t o_free = sbase + L::kOffBar + 8 * L::kBarOFree, o_ready = sbase + L::kOffBar + 8 * L::kBarOReady;
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + L::kOffPlan + 88);
+    softmax_sync();  // (m, l) of both groups
+    alive = alive && warp_wait(o_ready, end.piece & 1, abort_flag);
+    tc_fence_after();
+    if (alive && quarter * 32 < end.rows) {
+        const float2 x0 = ml[r], x1 = ml[kRows + r];
+        const float top = fmaxf(x0.x, x1.x);
+        const float mu = top == -INFINITY ? 0.f : top;
+        float f0 = fast_exp2(x0.x - mu), f1 = fast_exp2(x1.x - mu);
+        const float sum = f0 * x0.y + f1 * x1.y;
+        if (end.direct) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (a row that sees nothing is zero)
+            f0 *= inv;
+            f1 *= inv;
+        } else if (a == 0 && r < end.rows) {
+            p.part_ml[end.to] = make_float2(top, sum);
+        }
+        // Through the piece's place of Q, 4 KB a warp (128 bytes of 32 rows), so that a store writes whole lines: 4 rows of
+        // 128 bytes (a row a thread they take the SM 2000 cycles).
+        const bool narrow = end.direct && p.out_bf16;
+        const uint32_t stage = sbase + L::kOffQ + (end.piece & 1) * L::kQTile + warp * 4096;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {  // 32 values; bf16 leaves as 64, fp32 as 32
+            uint32_t o[32], x[32];
+            const uint32_t from = lane_base + kTmemO + 64 * a + 32 * half;
+            if (end.had0) {
+                tmem_ld_32x32b_x32(from, o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f0);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = 0u;
+            }
+            if (end.had1) {
+                tmem_ld_32x32b_x32(from + 128, x);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(fmaf(__uint_as_float(x[k]), f1, __uint_as_float(o[k])));
+            }
+            if (half == 1) {  // O has been read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(o_free);
+            }
+            const uint32_t at = stage + lane * 128;
+            if (narrow) {
+                auto two = [&](int k) { return pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])); };
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    sts128(at + (((4 * half + k) ^ (lane & 7)) << 4),
+                           make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6)));
+                if (half == 0) continue;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    sts128(at + ((k ^ (lane & 7)) << 4), make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const int rr = 4 * i + (lane >> 3), ch = lane & 7;
+                const int64_t to = __shfl_sync(0xffffffffu, end.to, rr) * kHeadDim + 64 * a;
+                const uint4 y = lds128(stage + rr * 128 + ((ch ^ (rr & 7)) << 4));
+                if (quarter * 32 + rr < end.rows) {
+                    if (narrow)
+                        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + to + 8 * ch) = y;
+                    else
+                        *reinterpret_cast<uint4 *>((end.direct ? static_cast<float *>(p.out) : p.part_o) + to + 32 * half + 4 * ch) = y;
+                }
+            }
+            __syncwarp();
+        }
+        fence_proxy_async_smem();  // (the place's next Q comes behind)
+    } else {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
+    }
+    softmax_sync();  // (m, l) have been read, and the place of Q
+    if (threadIdx.x == 0) mbar_arrive(sbase + L::kOffBar + 8 * (L::kBarQ + 2 + (end.piece & 1)));
+    return alive;
 }
 
 template <bool FP8>
 __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                          const TreeParams p) {
+                          const __grid_constant__ TreeParams p) {
     using L = Layout<FP8>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
@@ -311,22 +484,22 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     auto k_empty = [&](int st) { return bar(L::kStagesK + st); };
     auto v_full = [&](int st) { return bar(2 * L::kStagesK + st); };
     auto v_empty = [&](int st) { return bar(2 * L::kStagesK + L::kStagesV + st); };
-    constexpr int kBarRaw = 2 * L::kStagesK + 2 * L::kStagesV, kBarQ = kBarRaw + 2 * L::kStagesRaw;
-    auto raw_full = [&](int st) { return bar(kBarRaw + st); };
-    auto raw_empty = [&](int st) { return bar(kBarRaw + L::kStagesRaw + st); };
-    auto q_full = [&](int place) { return bar(kBarQ + place); };
-    auto q_empty = [&](int place) { return bar(kBarQ + 2 + place); };
+    auto raw_full = [&](int st) { return bar(L::kBarRaw + st); };
+    auto raw_empty = [&](int st) { return bar(L::kBarRaw + L::kStagesRaw + st); };
+    auto q_full = [&](int place) { return bar(L::kBarQ + place); };
+    auto q_empty = [&](int place) { return bar(L::kBarQ + 2 + place); };
     // of tile j: place j % kPlaces, phase j / kPlaces
-    auto s_full = [&](int j) { return bar(kBarQ + 4 + j % kPlaces); };
-    auto p_full = [&](int j) { return bar(kBarQ + 4 + kPlaces + j % kPlaces); };
-    auto pv_done = [&](int j) { return bar(kBarQ + 4 + 2 * kPlaces + j % kPlaces); };
+    auto s_full = [&](int j) { return bar(L::kBarS + j % kPlaces); };
+    auto p_full = [&](int j) { return bar(L::kBarS + kPlaces + j % kPlaces); };
+    auto pv_done = [&](int j) { return bar(L::kBarS + 2 * kPlaces + j % kPlaces); };
     auto phase = [](int j) -> uint32_t { return (j / kPlaces) & 1; };
-    const uint32_t o_free = bar(kBarQ + 4 + 3 * kPlaces), drained = o_free + 8;  // (drained: one of each issuing warp)
-    const bool two_q = p.part_rows <= kRows / 2;  // two places for Q: rows 0 .. 63 and 64 .. 127 of the tile
+    const uint32_t o_free = bar(L::kBarOFree), o_ready = bar(L::kBarOReady);  // O has been read; a piece's last P V is done
+    const uint32_t q_first = bar(L::kBarOReady + 1);                          // the first piece's Q is there
+    const uint32_t drained = bar(L::kBarOReady + 2);                          // one of each issuing warp
     Plan *plan_slot = reinterpret_cast<Plan *>(smem + L::kOffPlan);
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffPlan + 48);
-    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + L::kOffPlan + 56);
-    static_assert(sizeof(Plan) <= 48, "plan area");
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffPlan + 80);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + L::kOffPlan + 88);
+    static_assert(sizeof(Plan) <= 80, "plan area");
 
     if (tid == 0) {
         prefetch_tensormap(&kmap);
@@ -340,12 +513,12 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
             mbar_init(v_empty(st), 1);
         }
         for (int st = 0; st < L::kStagesRaw; ++st) {
-            mbar_init(raw_full(st), 1);
+            mbar_init(raw_full(st), 1 + 32);  // the codes, and a lane's share of the scales each
             mbar_init(raw_empty(st), 1 + kGroupWarps);  // the expansion, and the softmax of the tile
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full(i), 1);
-            mbar_init(q_empty(i), 1);
+            mbar_init(q_empty(i), 2);  // the last S of a piece, and its end
         }
         for (int i = 0; i < kPlaces; ++i) {
             mbar_init(s_full(i), 1);
@@ -355,6 +528,8 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         mbar_init(o_free, 2 * kGroupWarps);
         mbar_init(drained, 1);
         mbar_init(drained + 8, 1);
+        mbar_init(q_first, 1);
+        mbar_init(o_ready, 1);
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -367,7 +542,8 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     griddep_wait();
     if (warp == kWarpQ) {
         const Plan plan = make_plan(p, lane);
-        if (lane == 0) *plan_slot = plan;
+        // (the lane that holds the sequence; any, where the range is empty)
+        if (plan.count > 0 ? plan.s.units > 0 : lane == 0) *plan_slot = plan;
     }
     tc_fence_before();
     __syncthreads();
@@ -375,30 +551,17 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     const Plan plan = *plan_slot;
     const uint32_t tmem = *tmem_slot;
 
-    // A whole warp waits for a barrier's phase, within a bound, and gives up at once after another role gave up.
-    // (What is complete already costs one test; then lane 0 alone polls.)
-    auto warp_wait = [&](uint32_t b, uint32_t parity) -> bool {
-        if (__any_sync(0xffffffffu, mbar_test_wait(b, parity))) return true;
-        bool ok = false;
-        if (lane == 0 && !*abort_flag) {
-            ok = mbar_sleep_wait(b, parity);
-            if (!ok) *abort_flag = 1u;
-        }
-        return __any_sync(0xffffffffu, ok);
-    };
+    auto warp_wait = [&](uint32_t b, uint32_t parity) { return pkv::warp_wait(b, parity, abort_flag); };
 
     Walk w;
     w.start(p, plan);
-    // Place and use (its number there) of piece i's Q.
-    auto q_place = [&](int i) { return two_q ? i & 1 : 0; };
-    auto q_use = [&](int i) { return two_q ? i >> 1 : i; };
     // Lane k < 4: the id of block k of tile t (-1: none).
     auto block_id = [&](int t) -> int {
         const int blocks = (w.s.ctx + kBlockSize - 1) / kBlockSize, at = t * kTileBlocks + lane;
         return lane < kTileBlocks && at < blocks ? __ldg(p.block_tables + static_cast<int64_t>(w.b) * p.max_blocks + at) : -1;
     };
     if (warp == kWarpK || warp == kWarpV) {
-        // ---------------- copies: lane k < 4 sends for block k of a tile (FP8: with V, for its scales too) ----------------
+        // ---------------- copies: lane k < 4 sends for block k of a tile (FP8: with V, every lane for scales) ----------------
         const bool is_k = warp == kWarpK;
         const bool raw = FP8 && !is_k;
         const int stages = is_k ? L::kStagesK : raw ? L::kStagesRaw : L::kStagesV;
@@ -415,12 +578,14 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 // (an invalid id fetches block 0; its keys are masked)
                 const int id = static_cast<unsigned>(next) < static_cast<unsigned>(p.num_blocks) ? next : 0;
                 if (t + 1 < w.t1) next = block_id(t + 1);
+                // (behind full rings a read takes 5 us: the first piece's Q before them)
+                if (j == 2 && !(ok = warp_wait(q_first, 0))) break;
                 if (use > 0 && !(ok = warp_wait(empty0 + 8 * st, (use - 1) & 1))) break;
                 const int load = max(0, min(kTileBlocks, blocks - t * kTileBlocks));
                 const uint32_t full = full0 + 8 * st;
                 if (lane == 0) {
                     if (load > 0)
-                        mbar_arrive_expect_tx(full, load * (L::kBlk + (raw ? 2 * kBlockSize * 4 : 0)));
+                        mbar_arrive_expect_tx(full, load * L::kBlk);
                     else
                         mbar_arrive(full);
                 }
@@ -429,14 +594,20 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 if (lane < load) {
                     if constexpr (FP8) {
                         tma_load_4d(dst, map, full, 0, 0, g, id);
-                        if (raw) {
-                            const uint32_t scale = sbase + L::kOffScale + (st * 2 * kKeys + lane * kBlockSize) * 4;
-                            const int64_t at = (static_cast<int64_t>(id) * p.n_kv + g) * kBlockSize;
-                            bulk_copy_g2s(scale, p.k_scale + at, kBlockSize * 4, full);
-                            bulk_copy_g2s(scale + kKeys * 4, p.v_scale + at, kBlockSize * 4, full);
-                        }
                     } else {
                         tma_load_5d(dst, map, full, 0, 0, 0, 0, id * p.n_kv + g);
+                    }
+                }
+                if constexpr (FP8) {
+                    // The scales, 16 bytes a lane (8 lanes a block): off the TMA unit, whose copies take 100 cycles and more each.
+                    if (raw) {
+                        const int k = lane >> 3, part = lane & 3;
+                        const int block = __shfl_sync(0xffffffffu, id, k);
+                        if (k < load)
+                            cp_async_16(sbase + L::kOffScale + (st * 2 * kKeys + ((lane >> 2) & 1) * kKeys + k * kBlockSize + 4 * part) * 4,
+                                        ((lane >> 2) & 1 ? p.v_scale : p.k_scale) +
+                                            (static_cast<int64_t>(block) * p.n_kv + g) * kBlockSize + 4 * part);
+                        cp_async_mbar_arrive_noinc(full);
                     }
                 }
                 if (++st == stages) {
@@ -445,11 +616,12 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 }
             }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         // (given up: the copies still on their way land before the CTA ends)
         if (!ok && lane == 0)
             for (int i = max(0, j - stages); i < j; ++i) mbar_wait(full0 + 8 * (i % stages), (i / stages) & 1);
     } else if (FP8 && warp >= kWarpExpand) {
-        // ---------------- V's codes of every third tile expanded to bf16 ----------------
+        // ---------------- V's codes of every third tile expanded to fp16 ----------------
         const int x = warp - kWarpExpand;
         const int row = lane >> 3, c = lane & 7;  // of a block: rows row + 4 i, codes 16 c .. 16 c + 15
         int j = 0;
@@ -464,22 +636,31 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 ok = warp_wait(raw_full(raw_st), (i / (FP8 ? L::kStagesRaw : 1)) & 1);
                 if (ok && i >= L::kStagesV) ok = warp_wait(v_empty(st), ((i / L::kStagesV) - 1) & 1);
                 if (!ok) break;
+                uint4 code[4];  // a block ahead
+                auto read = [&](int k) {
+                    const uint32_t src = sbase + L::kOffRaw + (raw_st * kTileBlocks + k) * kCodeBytes + row * 128;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) code[n] = lds128(src + n * 512 + ((c ^ ((row + 4 * n) & 7)) << 4));
+                };
+                read(0);
 #pragma unroll 1
                 for (int k = 0; k < kTileBlocks; ++k) {
                     const int id = __shfl_sync(0xffffffffu, mine, k);
                     const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
-                    const uint32_t src = sbase + L::kOffRaw + (raw_st * kTileBlocks + k) * kCodeBytes;
-                    const uint32_t dst = sbase + L::kOffV + st * kVTile + k * kBlkBytes;
+                    const uint32_t dst = sbase + L::kOffV + st * kVTile + k * kBlkBytes + (c >> 2) * 1024;
+                    uint4 a[4], b[4];
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
+                        e4m3x16_to_f16(code[n], a[n], b[n]);
+                        if (!good || k * kBlockSize + row + 4 * n >= keys) a[n] = b[n] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    if (k + 1 < kTileBlocks) read(k + 1);
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {  // 16-byte chunks 2 c and 2 c + 1 of the row's 16
                         const int r = row + 4 * n;
-                        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-                        const uint4 code = lds128(src + r * 128 + ((c ^ (r & 7)) << 4));
-                        if (good && k * kBlockSize + r < keys) e4m3x16_to_bf16(code, a, b);
-                        // bf16 chunks 2 c and 2 c + 1 of the row's 16
-                        const uint32_t at = dst + (r >> 3) * 2048 + (c >> 2) * 1024 + (r & 7) * 128;
-                        sts128(at + (((2 * (c & 3)) ^ (r & 7)) << 4), a);
-                        sts128(at + (((2 * (c & 3) + 1) ^ (r & 7)) << 4), b);
+                        const uint32_t at = dst + (r >> 3) * 2048 + (r & 7) * 128;
+                        sts128(at + (((2 * (c & 3)) ^ (r & 7)) << 4), a[n]);
+                        sts128(at + (((2 * (c & 3) + 1) ^ (r & 7)) << 4), b[n]);
                     }
                 }
                 fence_proxy_async_smem();
@@ -492,111 +673,22 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
             j += w.t1 - w.t0;
         }
     } else if (warp == kWarpQ) {
-        // ---------------- the pieces' Q rows: 16 lanes a row, two rows a step ----------------
-        const int c = lane & 15;
-        for (int piece = 0; w.more(); ++piece) {
-            const int place = q_place(piece);
-            if (q_use(piece) > 0 && !warp_wait(q_empty(place), (q_use(piece) - 1) & 1)) break;
-            // f(row, address of this lane's 8 values) for the rows of the piece at hand
-            auto each_row = [&](auto f) {
-                const int rows = w.rows(p), first = w.row_tile() * kRows;
-                int r = lane >> 4, h = (first + r) % G;
-                const __nv_bfloat16 *src =
-                    static_cast<const __nv_bfloat16 *>(p.q) + 8 * c +
-                    ((static_cast<int64_t>(w.s.row0) + (first + r) / G) * p.n_q + static_cast<int64_t>(w.kv_head()) * G + h) * kHeadDim;
-                const int64_t node_step = static_cast<int64_t>(p.n_q - G) * kHeadDim;  // from behind a node's heads to the next's
-                for (; r < rows; r += 2) {
-                    f(r, src);
-                    src += 2 * kHeadDim;
-                    for (h += 2; h >= G; h -= G) src += node_step;
-                }
-            };
-            const uint32_t at = sbase + L::kOffQ + place * (kHalfTile / 2);
-            if constexpr (FP8) {
-                float *factor = reinterpret_cast<float *>(smem + L::kOffRow) + place * kRows;
-                const int rows = w.rows(p);
-                // (both halves of the warp take as many steps: the maximum goes by shuffles)
-                const int first = w.row_tile() * kRows;
-                const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(p.q) + 8 * c +
-                                            (static_cast<int64_t>(w.s.row0) * p.n_q + static_cast<int64_t>(w.kv_head()) * G) * kHeadDim;
-                auto read = [&](int r) -> uint4 {
-                    const int at_row = first + min(r, rows - 1);
-                    return __ldg(reinterpret_cast<const uint4 *>(
-                        base + (static_cast<int64_t>(at_row / G) * p.n_q + at_row % G) * kHeadDim));
-                };
-                uint4 ahead[4];  // the rows of the next four steps
-#pragma unroll
-                for (int i = 0; i < 4; ++i) ahead[i] = read(2 * i + (lane >> 4));
-#pragma unroll 1
-                for (int r0 = 0; r0 < rows; r0 += 2) {
-                    const uint4 x = ahead[0];
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) ahead[i] = ahead[i + 1];
-                    ahead[3] = read(r0 + 8 + (lane >> 4));
-                    {
-                        const int r = r0 + (lane >> 4);
-                        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-                        float v[8], most = 0.f;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            v[2 * k] = __uint_as_float(u[k] << 16);
-                            v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-                            most = fmaxf(most, fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
-                        }
-#pragma unroll
-                        for (int off = 8; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-                        // 2^e puts the largest value in [2^7, 2^8) (both powers are normal numbers)
-                        const int e = min(126, max(-119, 7 - (static_cast<int>(__float_as_uint(most) >> 23) - 127)));
-                        const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                        uint32_t hi[2], lo[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float s4[4], rest[4];
-#pragma unroll
-                            for (int i4 = 0; i4 < 4; ++i4) s4[i4] = v[4 * k + i4] * up;
-                            hi[k] = f32x2_to_e4m3x2(s4[0], s4[1]) | (f32x2_to_e4m3x2(s4[2], s4[3]) << 16);
-                            uint32_t f0, f1;
-                            e4m3x4_to_f16x2x2(hi[k], f0, f1);
-                            const float2 h0 = unpack_f16x2(f0), h1 = unpack_f16x2(f1);
-                            rest[0] = s4[0] - h0.x;
-                            rest[1] = s4[1] - h0.y;
-                            rest[2] = s4[2] - h1.x;
-                            rest[3] = s4[3] - h1.y;
-                            lo[k] = f32x2_to_e4m3x2(rest[0], rest[1]) | (f32x2_to_e4m3x2(rest[2], rest[3]) << 16);
-                        }
-                        if (r < rows) {
-                            const uint32_t to = at + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-                            sts32(to, hi[0]);
-                            sts32(to + 4, hi[1]);
-                            sts32(to + kHalfTile, lo[0]);
-                            sts32(to + kHalfTile + 4, lo[1]);
-                            // (a row with an infinity has no finite scores: NaN, as code x 448 would not say)
-                            if (c == 0)
-                                factor[r] = most > 3.4e38f ? __uint_as_float(0x7fc00000u)
-                                                           : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                        }
-                    }
-                }
-            } else {
-                const uint32_t dst = at + (c >> 3) * kHalfTile;
-                each_row([&](int r, const __nv_bfloat16 *src) { cp_async_16(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4), src); });
-                asm volatile("cp.async.wait_all;" ::: "memory");
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
+        // ---------------- the Q rows of the pieces from the second on ----------------
+        if (w.more()) w.next(p);
+        for (int piece = 1; w.more(); w.next(p), ++piece) {
+            const int place = piece & 1;
+            if (piece > 1 && !warp_wait(q_empty(place), ((piece >> 1) - 1) & 1)) break;
+            load_q<FP8>(p, w.s.row0, w.row_tile() * kRows, w.rows(p), w.kv_head() * G, sbase + L::kOffQ + place * L::kQTile,
+                        reinterpret_cast<float *>(smem + L::kOffRow) + place * kRows, 0, 1);
             if (lane == 0) mbar_arrive(q_full(place));
-            w.next(p);
-            if (w.more()) each_row([&](int, const __nv_bfloat16 *src) {
-                if ((c & 7) == 0) prefetch_l2(src);
-            });
         }
     } else if (warp == kWarpS) {
         // ---------------- S = Q K^T ----------------
         int j = 0;
         bool ok = true;
         for (int piece = 0; ok && w.more(); w.next(p), ++piece) {
-            const int place = q_place(piece);
-            if (!(ok = warp_wait(q_full(place), q_use(piece) & 1))) break;
+            const int place = piece & 1;
+            if (!(ok = warp_wait(q_full(place), (piece >> 1) & 1))) break;
             for (int t = w.t0; t < w.t1; ++t, ++j) {
                 const int st = j % L::kStagesK;
                 ok = warp_wait(k_full(st), (j / L::kStagesK) & 1);
@@ -604,8 +696,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
-                    // (the second place's rows begin 64 rows down; what lies behind them is read and not used)
-                    const uint32_t kb = sbase + L::kOffK + st * L::kKTile, qb = sbase + L::kOffQ + place * (kHalfTile / 2);
+                    const uint32_t kb = sbase + L::kOffK + st * L::kKTile, qb = sbase + L::kOffQ + place * L::kQTile;
                     const uint32_t d = tmem + kKeys * (j % kPlaces);
                     if constexpr (FP8) {
 #pragma unroll
@@ -642,14 +733,15 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     const uint32_t vb = sbase + L::kOffV + st * kVTile, d = tmem + kTmemO + 128 * (j & 1);
                     const uint32_t first = t - w.t0 < 2 ? 0u : 1u;
 #pragma unroll
-                    for (int s4 = 0; s4 < 4; ++s4) {  // keys 16 s4 ..: of each 32 keys [16 columns heads | 16 remainders]
-                        const uint32_t a_hi = tmem + kKeys * (j % kPlaces) + (s4 >> 1) * 32 + (s4 & 1) * 8;
+                    for (int s4 = 0; s4 < 4; ++s4) {  // keys 16 s4 ..: [8 columns heads | 8 remainders], FP8 8 columns in all
+                        const uint32_t at = tmem + kKeys * (j % kPlaces) + 16 * s4;
                         const uint64_t bd = sw128_desc(vb + s4 * kBlkBytes, 1024, 2048);
-                        umma_bf16_tmem_a(d, a_hi, bd, kIdescPV, s4 > 0 ? 1u : first);
-                        umma_bf16_tmem_a(d, a_hi + 16, bd, kIdescPV, 1u);
+                        umma_bf16_tmem_a(d, at, bd, FP8 ? kIdescPV16 : kIdescPV, s4 > 0 ? 1u : first);
+                        if constexpr (!FP8) umma_bf16_tmem_a(d, at + 8, bd, kIdescPV, 1u);
                     }
                     umma_commit(pv_done(j));
                     umma_commit(v_empty(st));
+                    if (t + 1 == w.t1) umma_commit(o_ready);
                 }
                 __syncwarp();
             }
@@ -660,9 +752,24 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t t_o = lane_base + kTmemO + 128 * a;
         float2 *ml = reinterpret_cast<float2 *>(smem + L::kOffMl);
-        auto both_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(2 * kGroupWarps * 32) : "memory"); };
+        if (w.more()) {  // the first piece's Q, by all of these warps
+            load_q<FP8>(p, w.s.row0, w.row_tile() * kRows, w.rows(p), w.kv_head() * G, sbase + L::kOffQ,
+                        reinterpret_cast<float *>(smem + L::kOffRow), warp, 2 * kGroupWarps);
+            softmax_sync();
+            if (tid == 0) {
+                mbar_arrive(q_full(0));
+                mbar_arrive(q_first);
+            }
+        }
         bool alive = true;
         int j0 = 0;  // tiles before the piece
+
+        End end{};
+        bool pending = false;  // a piece's end is still to come
+        auto finish = [&]() {
+            alive = finish_piece<FP8>(p, end, sbase, lane_base, alive);
+            pending = false;
+        };
         for (int piece = 0; w.more(); w.next(p), ++piece) {
             const int rows = w.rows(p), first_row = w.row_tile() * kRows, g = w.kv_head();
             const bool busy = quarter * 32 < rows;  // (warp-uniform: a warp without rows only keeps step)
@@ -670,8 +777,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
             const int64_t row = static_cast<int64_t>(w.s.row0) + (first_row + r) / G;
             uint64_t mask = 0;
             if (r < rows && w.s.ctx > 0) {
-                mask = __ldg(reinterpret_cast<const unsigned long long *>(p.mask) + row);
-                if (w.s.n < 64) mask &= (1ull << w.s.n) - 1;
+                mask = __ldg(reinterpret_cast<const unsigned long long *>(p.mask) + row);  // (not looked at before the tree's tiles)
             }
             float sl2 = p.scale_log2;
             float m = -INFINITY, l = 0.f;
@@ -692,17 +798,22 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 const uint32_t t_s = lane_base + kKeys * (j % kPlaces);
                 if (busy) {
                     if constexpr (FP8) {
-                        if (t == t_first) sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::kOffRow)[q_place(piece) * kRows + r];
+                        // (a factor of 0 counts as the least normal number: a hidden key's -inf times it stays one)
+                        if (t == t_first) {
+                            sl2 = fabsf(p.scale_log2) * reinterpret_cast<const float *>(smem + L::kOffRow)[(piece & 1) * kRows + r];
+                            if (sl2 < 0x1p-126f) sl2 = 0x1p-126f;
+                        }
                     }
                     const uint32_t scales = sbase + L::kOffScale + (j % (FP8 ? L::kStagesRaw : 1)) * 2 * kKeys * 4;
-                    float2 sl2v = make_float2(sl2, sl2);
+                    float2 sl2v = make_float2(sl2, sl2);  // (bf16)
                     uint32_t k_scales = scales;
                     // Tiles that not every row sees whole: the scores are scaled and the hidden ones -inf before the pass below,
                     // which then scales them by 1.  (A loop of its own, once or twice a sequence: in the pass, whose code the
                     // instruction caches have to hold beside six other roles', selects cost every tile.)
                     if (t * kKeys + kKeys > prefix || bad) {
                         const int at = t * kKeys - prefix;  // node of the tile's first key
-                        uint64_t seen = at >= 0 ? (at < 64 ? mask >> at : 0) : at > -64 ? ((1ull << -at) - 1) | (mask << -at) : ~0ull;
+                        const uint64_t nodes = w.s.n < 64 ? mask & ((1ull << w.s.n) - 1) : mask;
+                        uint64_t seen = at >= 0 ? (at < 64 ? nodes >> at : 0) : at > -64 ? ((1ull << -at) - 1) | (nodes << -at) : ~0ull;
                         for (int k = 0; k < kTileBlocks; ++k)
                             if ((bad >> k) & 1) seen &= ~(0xffffull << (16 * k));
 #pragma unroll 1
@@ -712,8 +823,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                             const uint32_t bits = static_cast<uint32_t>(seen >> (16 * c));
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
-                                float f = sl2;
-                                if constexpr (FP8) f *= lds_f32(scales + 4 * (16 * c + k));
+                                const float f = FP8 ? lds_f32(scales + 4 * (16 * c + k)) : sl2;
                                 x[k] = (bits >> k) & 1 ? __float_as_uint(__uint_as_float(x[k]) * f) : 0xff800000u;
                             }
                             tmem_st_32x32b_x16(t_s + 16 * c, x);
@@ -731,26 +841,42 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     }
                     uint32_t v[64];
                     tmem_ld_32x32b_x64(t_s, v);
-                    // scores in the log2 domain (FP8: times each key's K scale), and the row's largest
+                    // scores in the log2 domain (FP8: times each key's K scale, before the row's factor), and the row's largest
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float2 f4[8];  // FP8: scales of 16 keys
+                    auto load_scales = [&](uint32_t from) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        float2 f0 = sl2v, f1 = sl2v;
-                        if constexpr (FP8) {
-                            const uint4 f = lds128(k_scales + 8 * i);
-                            f0 = fmul2(make_float2(__uint_as_float(f.x), __uint_as_float(f.y)), sl2v);
-                            f1 = fmul2(make_float2(__uint_as_float(f.z), __uint_as_float(f.w)), sl2v);
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 f = lds128(from + 16 * i);
+                            f4[2 * i] = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
+                            f4[2 * i + 1] = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
                         }
-                        const float2 x = fmul2(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f0);
-                        const float2 y = fmul2(make_float2(__uint_as_float(v[2 * i + 2]), __uint_as_float(v[2 * i + 3])), f1);
-                        v[2 * i] = __float_as_uint(x.x);
-                        v[2 * i + 1] = __float_as_uint(x.y);
-                        v[2 * i + 2] = __float_as_uint(y.x);
-                        v[2 * i + 3] = __float_as_uint(y.y);
-                        mx[i & 2] = fmax3(mx[i & 2], x.x, x.y);
-                        mx[(i & 2) + 1] = fmax3(mx[(i & 2) + 1], y.x, y.y);
+                    };
+                    if constexpr (FP8) load_scales(k_scales);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float2 f[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = FP8 ? f4[i] : sl2v;
+                        if constexpr (FP8) load_scales(c < 3 ? k_scales + 64 * (c + 1) : scales + kKeys * 4);  // (the next ones, at last V's first)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int k = 16 * c + 2 * i;
+                            const float2 x = fmul2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), f[i]);
+                            v[k] = __float_as_uint(x.x);
+                            v[k + 1] = __float_as_uint(x.y);
+                            mx[i & 3] = fmax3(mx[i & 3], x.x, x.y);
+                        }
                     }
-                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if constexpr (FP8) {
+                        // and the exponent of the tile's largest V scale (a sum of weights of scales below 2^-90 would
+                        // leave fp32)
+                        const float2 sv = lds_f32x2(scales + (kKeys + 2 * lane) * 4);
+                        const uint32_t most = __reduce_max_sync(
+                            0xffffffffu, max(__float_as_uint(sv.x) & 0x7fffffffu, __float_as_uint(sv.y) & 0x7fffffffu));
+                        mt = fmaf(mt, sl2, static_cast<float>(min(max(static_cast<int>(most >> 23) - 127, -90), 100)));
+                    }
                     float alpha = 1.f;
                     if (mt > m + 8.f) {
                         alpha = fast_exp2(m - mt);  // (0 where m is -inf)
@@ -776,28 +902,37 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     const float2 nmu = make_float2(-mu, -mu);
                     float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t pk[32];
+                    for (int c = 0; c < 4; ++c) {  // 16 keys: 8 columns of heads, 8 of remainders
+                        uint32_t pk[FP8 ? 8 : 16];
+                        float2 f[8];
+                        if constexpr (FP8) {
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const int k = 32 * c + 2 * e;
-                            const float2 x = fadd2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), nmu);
-                            const float2 y = fadd2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), nmu);
-                            float2 px = make_float2(fast_exp2(x.x), fast_exp2(x.y)), py = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-                            rs0 = fadd2(rs0, px);
-                            rs1 = fadd2(rs1, py);
-                            if constexpr (FP8) {  // (the sum keeps the plain weights)
-                                const uint4 f = lds128(scales + (kKeys + k) * 4);
-                                px = fmul2(px, make_float2(__uint_as_float(f.x), __uint_as_float(f.y)));
-                                py = fmul2(py, make_float2(__uint_as_float(f.z), __uint_as_float(f.w)));
-                            }
-                            pk[e] = __byte_perm(__float_as_uint(px.x), __float_as_uint(px.y), 0x7632);
-                            pk[e + 1] = __byte_perm(__float_as_uint(py.x), __float_as_uint(py.y), 0x7632);
-                            const float2 ex = minus_bf16x2(px, pk[e]), ey = minus_bf16x2(py, pk[e + 1]);
-                            pk[16 + e] = pack_bf16x2(ex.x, ex.y);
-                            pk[17 + e] = pack_bf16x2(ey.x, ey.y);
+                            for (int i = 0; i < 8; ++i) f[i] = f4[i];
+                            if (c < 3) load_scales(scales + kKeys * 4 + 64 * (c + 1));
                         }
-                        tmem_st_32x32b_x32(t_s + 32 * c, pk);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int k = 16 * c + 2 * e;
+                            const float2 s2 = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+                            const float2 x = FP8 ? ffma2(s2, make_float2(sl2, sl2), nmu) : fadd2(s2, nmu);
+                            float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                            if (e & 1)
+                                rs1 = fadd2(rs1, pr);
+                            else
+                                rs0 = fadd2(rs0, pr);
+                            if constexpr (FP8) {  // (the sum keeps the plain weights)
+                                pr = fmul2(pr, f[e]);
+                                pk[e] = pack_f16x2(pr.x, pr.y);
+                            } else {
+                                pk[e] = __byte_perm(__float_as_uint(pr.x), __float_as_uint(pr.y), 0x7632);
+                                const float2 rest = minus_bf16x2(pr, pk[e]);
+                                pk[8 + e] = pack_bf16x2(rest.x, rest.y);
+                            }
+                        }
+                        if constexpr (FP8)
+                            tmem_st_32x32b_x8(t_s + 16 * c, pk);
+                        else
+                            tmem_st_32x32b_x16(t_s + 16 * c, pk);
                     }
                     const float2 rs = fadd2(rs0, rs1);
                     l = l * alpha + (rs.x + rs.y);
@@ -825,77 +960,21 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     mbar_arrive(p_full(j));
                     if constexpr (FP8) mbar_arrive(raw_empty(j % L::kStagesRaw));  // (the scales have been read)
                 }
+                if (pending) finish();
             }
-            // ---- the piece's end: both groups' parts joined; group a stores the values 64 a .. 64 a + 63 ----
+            // ---- the piece's end ----
             const int tiles = w.t1 - w.t0;
-            const bool had[2] = {tiles > 1 || (j0 & 1) == 0, tiles > 1 || (j0 & 1) == 1};
-            j0 += tiles;
-            const int last = j0 - 1 - ((j0 - 1 - a) & 1), other = j0 - 1 - ((j0 - a) & 1);  // the groups' last tiles
-            if (had[a]) alive = alive && warp_wait(pv_done(last), phase(last));
+            if (pending) finish();
             ml[a * kRows + r] = make_float2(m, l);
-            tc_fence_before();
-            both_sync();
-            tc_fence_after();
-            if (had[1 - a]) {  // (complete: the other group waited for it; this orders its data for this warp)
-                alive = alive && warp_wait(pv_done(other), phase(other));
-                tc_fence_after();
-            }
-            if (alive && busy) {
-                const float2 x0 = ml[r], x1 = ml[kRows + r];
-                const float top = fmaxf(x0.x, x1.x);
-                const float mu = top == -INFINITY ? 0.f : top;
-                float f[2] = {fast_exp2(x0.x - mu), fast_exp2(x1.x - mu)};
-                const float sum = f[0] * x0.y + f[1] * x1.y;
-                const bool direct = tiles == w.s.tiles;
-                if (direct) {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (a row that sees nothing is zero)
-                    f[0] *= inv;
-                    f[1] *= inv;
-                }
-                const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1);
-                const int64_t pr = slot * p.part_rows + r;
-                const int64_t head = row * p.n_q + static_cast<int64_t>(g) * G + (first_row + r) % G;
-                if (!direct && a == 0 && r < rows) p.part_ml[pr] = make_float2(top, sum);
-#pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    const int col = 64 * a + 32 * c;
-                    uint32_t o[32];
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = 0u;
-                    if (had[0]) {
-                        uint32_t x[32];
-                        tmem_ld_32x32b_x32(lane_base + kTmemO + col, x);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(f[0] == 0.f ? 0.f : __uint_as_float(x[k]) * f[0]);
-                    }
-                    if (had[1]) {
-                        uint32_t x[32];
-                        tmem_ld_32x32b_x32(lane_base + kTmemO + 128 + col, x);
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            o[k] = __float_as_uint(f[1] == 0.f ? __uint_as_float(o[k])
-                                                               : fmaf(__uint_as_float(x[k]), f[1], __uint_as_float(o[k])));
-                    }
-                    if (r >= rows) {
-                    } else if (!direct || !p.out_bf16) {
-                        uint4 *dst = reinterpret_cast<uint4 *>((direct ? static_cast<float *>(p.out) + head * kHeadDim
-                                                                       : p.part_o + pr * kHeadDim) + col);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                    } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + head * kHeadDim + col);
-                        auto two = [&](int k) { return pack_bf16x2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])); };
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            dst[k] = make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6));
-                    }
-                    __syncwarp();
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(o_free);
-            both_sync();  // (m, l) have been read
+            pending = true;
+            end.piece = piece;
+            end.rows = busy ? rows : 0;
+            end.had0 = tiles > 1 || (j0 & 1) == 0;
+            end.had1 = tiles > 1 || (j0 & 1) == 1;
+            end.direct = tiles == w.s.tiles;
+            end.to = end.direct ? row * p.n_q + static_cast<int64_t>(g) * G + (first_row + r) % G
+                                : (static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1)) * p.part_rows + r;
+            j0 += tiles;
             // A unit that begins here and goes on in the next ranges is joined by the second kernel.
             if (tid == 0 && w.left == tiles) {
                 int4 rec = make_int4(0, 0, 0, 0);
@@ -907,6 +986,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 p.record[blockIdx.x] = rec;
             }
         }
+        if (pending) finish();
         if (tid == 0 && plan.count == 0) p.record[blockIdx.x] = make_int4(0, 0, 0, 0);
     }
 
