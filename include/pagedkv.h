@@ -912,7 +912,7 @@ PKV_API int rotary_reshape_and_cache_fp8(void *q_out, const void *q, int64_t q_r
  *   max_q_len  : host upper bound of the nodes a sequence, 1 .. PKV_MAX_TREE_NODES
  *   k_cache, v_cache, k_scale, v_scale : a bf16 pool (scales NULL) or an FP8 (E4M3) pool, as cache->dtype
  *                says; attention is over code * scale
- *   num_q_heads: any multiple of cache->num_kv_heads (to 65536)
+ *   num_q_heads: any multiple of cache->num_kv_heads (to 1024)
  *   workspace  : 256-byte aligned, paged_attention_tree_workspace_size() bytes (for the current
  *                device; 152 SMs are assumed without a GPU), status word zeroed once (it is
  *                sticky); calls that share it must not overlap

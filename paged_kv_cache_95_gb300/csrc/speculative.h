@@ -46,6 +46,7 @@ struct TreeParams {
     const float *k_scale, *v_scale;  // FP8 pool only
     uint32_t *status;
     int32_t num_seqs, n_q, n_kv, group, max_blocks, num_blocks, total_rows, max_q_len;
+    uint32_t group_magic;  // 2^32 / group rounded up (0 for a group of 1)
     float scale_log2;
     int32_t out_bf16;
     // The split: all (sequence, KV head, 128-row tile) units' key tiles in `ranges` equal ranges, one a CTA.

@@ -64,6 +64,7 @@ bool log2_scale(float scale, float *out) {
 }
 
 constexpr size_t kStatusBytes = 256;
+constexpr int32_t kMaxTreeHeads = 1024;
 constexpr int kDefaultSms = 152;  // sizes asked for without a GPU
 // Lengths that the kernels may round up to whole tiles within 32 bits.
 constexpr int64_t kMaxLength = INT32_MAX - 4096;
@@ -91,7 +92,7 @@ int check_tree_sizes(int32_t num_seqs, int32_t num_q_heads, int32_t max_q_len, c
     if (int rc = check_pool(cache, fp8)) return rc;
     if (num_seqs < 1 || num_seqs > 65535 || max_q_len < 1 || max_q_len > PKV_MAX_TREE_NODES) return PKV_ERR_INVALID_ARG;
     if (num_q_heads < 1 || num_q_heads % cache->num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
-    if (num_q_heads > 65536) return PKV_ERR_UNSUPPORTED;
+    if (num_q_heads > kMaxTreeHeads) return PKV_ERR_UNSUPPORTED;
     // K/V tiles are addressed by the 32-bit index block * n_kv + head.
     if (static_cast<int64_t>(cache->num_blocks) * cache->num_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     return PKV_OK;
@@ -326,6 +327,7 @@ int paged_attention_tree(void *out, int32_t out_dtype, const void *q, const uint
     p.n_q = num_q_heads;
     p.n_kv = n_kv;
     p.group = num_q_heads / n_kv;
+    p.group_magic = p.group > 1 ? static_cast<uint32_t>(((uint64_t{1} << 32) + p.group - 1) / p.group) : 0;
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = cache->num_blocks;
     p.total_rows = total_q_rows;

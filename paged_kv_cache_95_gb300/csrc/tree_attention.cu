@@ -95,12 +95,14 @@ struct Layout {
     static constexpr uint32_t kOffScale = kOffRaw + kStagesRaw * kTileBlocks * kCodeBytes;  // FP8: [tile][K, V][64]
     static constexpr uint32_t kOffOnes = kOffScale + kStagesRaw * 2 * kKeys * 4;  // FP8: a tile's K scales, all 1
     static constexpr uint32_t kOffRow = kOffOnes + (FP8 ? kKeys * 4 : 0);  // FP8: factors of Q's rows, two places
-    static constexpr uint32_t kOffMl = kOffRow + (FP8 ? 2 * kRows * 4 : 0);  // (m, l) of the groups' rows
+    static constexpr uint32_t kOffBad = kOffRow + (FP8 ? 2 * kRows * 4 : 0);  // [tile modulo 16]: blocks with an invalid id
+    static constexpr uint32_t kOffMl = kOffBad + 16 * 4;  // (m, l) of the groups' rows
     static constexpr uint32_t kOffBar = kOffMl + 2 * kRows * 8;
     static constexpr int kBarRaw = 2 * kStagesK + 2 * kStagesV, kBarQ = kBarRaw + 2 * kStagesRaw, kBarS = kBarQ + 4;
     static constexpr int kBarOFree = kBarS + 3 * kPlaces, kBarOReady = kBarOFree + 1, kBars = kBarOFree + 5;
     static constexpr uint32_t kOffPlan = kOffBar + 8 * kBars;
-    static constexpr uint32_t kBytes = kOffPlan + 96;
+    static constexpr uint32_t kOffSequences = kOffPlan + 96;
+    static constexpr uint32_t kBytes = kOffSequences + 32 * sizeof(int) * 3;
     static_assert(kBytes <= 232448, "shared memory of a CTA");
     static_assert(kOffK % 1024 == 0 && kKTile % 1024 == 0 && kOffV % 1024 == 0 && kOffPlan % 8 == 0, "alignment");
 };
@@ -148,8 +150,25 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint32_t bar, uint32_t parity) {
 }
 
 // A whole warp waits for a barrier's phase, within a bound, and gives up at once after another role gave up.
-// (What is complete already costs one test; then lane 0 alone polls.)
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag) {
+// (What is complete already costs one test; then lane 0 alone polls, in code that is not repeated at every wait: the
+// roles' loops share the instruction caches.)
+__device__ __noinline__ bool warp_wait_on(uint32_t bar, uint32_t parity, uint32_t abort_at) {
+    bool ok = false;
+    if ((threadIdx.x & 31) == 0) {
+        uint32_t gave_up;
+        asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(gave_up) : "r"(abort_at) : "memory");
+        if (!gave_up) {
+            ok = mbar_sleep_wait(bar, parity);
+            if (!ok) asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(abort_at), "r"(1u) : "memory");
+        }
+    }
+    return __any_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort_at) {
+    return __any_sync(0xffffffffu, mbar_test_wait(bar, parity)) || warp_wait_on(bar, parity, abort_at);
+}
+// The same without a call, for the softmax warps: what they hold would have to be saved around one.
+__device__ __forceinline__ bool softmax_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag) {
     if (__any_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
     bool ok = false;
     if ((threadIdx.x & 31) == 0 && !*abort_flag) {
@@ -174,13 +193,26 @@ __device__ __forceinline__ float2 minus_bf16x2(float2 p, uint32_t h) {
     return d;
 }
 
+// x / group for a row x of a tree (magic: 2^32 / group rounded up; exact for 64 nodes of up to 1024 heads).
+__device__ __forceinline__ int by_group(int x, uint32_t magic) {
+    return magic == 0 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), magic));  // (0: a group of 1)
+}
+
 // A sequence as the split sees it (device data: checked).  units is 0 for one without rows, or whose
 // rows lie outside the tensors; one whose lengths do not fit has one tile that no row sees, so its rows become zeros.
 struct Sequence {
     int row0, n, ctx, row_tiles, units, tiles;
     uint32_t wrong;  // status bits
 };
-__device__ __forceinline__ Sequence load_sequence(const TreeParams &p, int b) {
+struct Lengths {
+    int row0, n, ctx;
+};
+__device__ __forceinline__ void count_tiles(const TreeParams &p, Sequence &s) {
+    s.row_tiles = static_cast<int>((static_cast<int64_t>(s.n) * p.group + kRows - 1) / kRows);
+    s.units = s.n > 0 ? s.row_tiles * p.n_kv : 0;
+    s.tiles = max(1, (s.ctx + kKeys - 1) / kKeys);
+}
+__device__ __noinline__ Sequence load_sequence(const TreeParams &p, int b) {
     Sequence s;
     s.row0 = __ldg(p.cu_q_lens + b);
     s.n = __ldg(p.cu_q_lens + b + 1) - s.row0;
@@ -195,9 +227,7 @@ __device__ __forceinline__ Sequence load_sequence(const TreeParams &p, int b) {
         if (s.n > p.max_q_len || (s.ctx >= 1 && s.ctx < s.n)) s.wrong |= kStatusBadQLen;
         if (s.wrong) s.ctx = 0;
     }
-    s.row_tiles = static_cast<int>((static_cast<int64_t>(s.n) * p.group + kRows - 1) / kRows);
-    s.units = s.n > 0 ? s.row_tiles * p.n_kv : 0;
-    s.tiles = max(1, (s.ctx + kKeys - 1) / kKeys);
+    count_tiles(p, s);
     return s;
 }
 
@@ -209,33 +239,47 @@ struct Plan {
     Sequence s;  // b's
 };
 
-// The pieces of a range, one after the other; every role walks them by itself.
+// The pieces of a range, one after the other; every role walks them by itself.  The sequences (rows, nodes, context) of
+// the 32 with plan.b stand in shared memory: behind full rings a read of memory takes 5 us.
 struct Walk {
     Sequence s;
-    int b, unit, t0, t1, left;
+    int b, g, row_tile, t0, t1, left;
+    bool far;  // past those
     __device__ __forceinline__ void start(const TreeParams &p, const Plan &plan) {
+        far = false;
         b = plan.b;
-        unit = plan.unit;
         t0 = plan.tile;
         left = plan.count;
         s = plan.s;
+        g = left > 0 ? plan.unit / s.row_tiles : 0;
+        row_tile = plan.unit - g * s.row_tiles;
         t1 = min(s.tiles, t0 + left);
     }
     __device__ __forceinline__ bool more() const { return left > 0; }
-    __device__ __forceinline__ void next(const TreeParams &p) {
+    __device__ __forceinline__ void next(const TreeParams &p, const Lengths *known) {
         left -= t1 - t0;
         if (left <= 0) return;
         t0 = 0;
-        if (++unit >= s.units) {
-            unit = 0;
-            do s = load_sequence(p, ++b);
-            while (s.units == 0);
+        if (++row_tile == s.row_tiles) {
+            row_tile = 0;
+            if (++g == p.n_kv) {
+                g = 0;
+                do {
+                    if ((++b & 31) == 0) far = true;
+                    if (!far) {
+                        s.row0 = known[b & 31].row0;
+                        s.n = known[b & 31].n;
+                        s.ctx = known[b & 31].ctx;
+                        count_tiles(p, s);
+                    } else {
+                        s = load_sequence(p, b);
+                    }
+                } while (s.units == 0);
+            }
         }
         t1 = min(s.tiles, left);
     }
-    __device__ __forceinline__ int kv_head() const { return unit / s.row_tiles; }
-    __device__ __forceinline__ int row_tile() const { return unit % s.row_tiles; }
-    __device__ __forceinline__ int rows(const TreeParams &p) const { return min(kRows, s.n * p.group - row_tile() * kRows); }
+    __device__ __forceinline__ int rows(const TreeParams &p) const { return min(kRows, s.n * p.group - row_tile * kRows); }
 };
 
 // The range of this CTA, by one warp: tiles of all sequences, then the sequence that the range starts in.  (On the way
@@ -244,7 +288,7 @@ __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
     if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
     return x / y;
 }
-__device__ Plan make_plan(const TreeParams &p, int lane) {
+__device__ __noinline__ Plan make_plan(const TreeParams &p, int lane, Lengths *known) {
     Plan plan{};
     Sequence s{};
     auto load = [&](int b) -> int64_t {  // tiles of all of a sequence's units
@@ -290,6 +334,7 @@ __device__ Plan make_plan(const TreeParams &p, int lane) {
                 plan.tile = static_cast<int>(inside - static_cast<int64_t>(plan.unit) * s.tiles);
                 plan.s = s;
             }
+            known[lane] = {s.row0, s.n, s.ctx};
             return plan;
         }
     }
@@ -312,16 +357,17 @@ template <bool FP8>
 __device__ __noinline__ void load_q(const TreeParams &p, int row0, int first, int rows, int head0, uint32_t dst, float *factor,
                                     int part, int parts) {
     const int lane = threadIdx.x & 31, c = lane & 15, G = p.group;
+    const uint32_t magic = p.group_magic;
     const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(p.q) + 8 * c +
                                 (static_cast<int64_t>(row0) * p.n_q + head0) * kHeadDim;
     auto source = [&](int r) -> const __nv_bfloat16 * {  // (rows past the last are read as the last)
-        const int at = first + min(r, rows - 1), node = at / G;
+        const int at = first + min(r, rows - 1), node = by_group(at, magic);
         return base + (static_cast<int64_t>(node) * p.n_q + (at - node * G)) * kHeadDim;
     };
     const int step = 2 * parts, first_r = 2 * part + (lane >> 4);
     // Row r's 16-byte chunk c: half c / 8 (FP8: of the raw values too, whose place the codes take).
     auto place = [&](int r) { return dst + (c >> 3) * kHalfTile + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
-#pragma unroll 4
+#pragma unroll 1
     for (int r = first_r; r < rows; r += step) cp_async_16(place(r), source(r));
     asm volatile("cp.async.wait_all;" ::: "memory");
     if constexpr (FP8) {
@@ -390,7 +436,7 @@ __device__ __noinline__ bool finish_piece(const TreeParams &p, const End end, ui
     const uint32_t o_free = sbase + L::kOffBar + 8 * L::kBarOFree, o_ready = sbase + L::kOffBar + 8 * L::kBarOReady;
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + L::kOffPlan + 88);
     softmax_sync();  // (m, l) of both groups
-    alive = alive && warp_wait(o_ready, end.piece & 1, abort_flag);
+    alive = alive && softmax_wait(o_ready, end.piece & 1, abort_flag);
     tc_fence_after();
     if (alive && quarter * 32 < end.rows) {
         const float2 x0 = ml[r], x1 = ml[kRows + r];
@@ -497,6 +543,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     const uint32_t q_first = bar(L::kBarOReady + 1);                          // the first piece's Q is there
     const uint32_t drained = bar(L::kBarOReady + 2);                          // one of each issuing warp
     Plan *plan_slot = reinterpret_cast<Plan *>(smem + L::kOffPlan);
+    Lengths *known = reinterpret_cast<Lengths *>(smem + L::kOffSequences);  // of the 32 sequences with the range's first
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kOffPlan + 80);
     volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + L::kOffPlan + 88);
     static_assert(sizeof(Plan) <= 80, "plan area");
@@ -541,7 +588,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     griddep_launch_dependents();
     griddep_wait();
     if (warp == kWarpQ) {
-        const Plan plan = make_plan(p, lane);
+        const Plan plan = make_plan(p, lane, known);
         // (the lane that holds the sequence; any, where the range is empty)
         if (plan.count > 0 ? plan.s.units > 0 : lane == 0) *plan_slot = plan;
     }
@@ -551,7 +598,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     const Plan plan = *plan_slot;
     const uint32_t tmem = *tmem_slot;
 
-    auto warp_wait = [&](uint32_t b, uint32_t parity) { return pkv::warp_wait(b, parity, abort_flag); };
+    auto warp_wait = [&](uint32_t b, uint32_t parity) { return pkv::warp_wait(b, parity, sbase + L::kOffPlan + 88); };
 
     Walk w;
     w.start(p, plan);
@@ -571,18 +618,28 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         const CUtensorMap *map = is_k ? &kmap : &vmap;
         int j = 0, st = 0, use = 0;  // tile of the range; its stage, and the stage's use
         bool ok = true;
-        for (; ok && w.more(); w.next(p)) {
-            const int blocks = (w.s.ctx + kBlockSize - 1) / kBlockSize, g = w.kv_head();
+#pragma unroll 1
+        for (; ok && w.more(); w.next(p, known)) {
+            const int blocks = (w.s.ctx + kBlockSize - 1) / kBlockSize, g = w.g;
             int next = block_id(w.t0);
+#pragma unroll 1
             for (int t = w.t0; t < w.t1; ++t, ++j) {
                 // (an invalid id fetches block 0; its keys are masked)
-                const int id = static_cast<unsigned>(next) < static_cast<unsigned>(p.num_blocks) ? next : 0;
+                const int now = next, id = static_cast<unsigned>(now) < static_cast<unsigned>(p.num_blocks) ? now : 0;
                 if (t + 1 < w.t1) next = block_id(t + 1);
                 // (behind full rings a read takes 5 us: the first piece's Q before them)
                 if (j == 2 && !(ok = warp_wait(q_first, 0))) break;
                 if (use > 0 && !(ok = warp_wait(empty0 + 8 * st, (use - 1) & 1))) break;
                 const int load = max(0, min(kTileBlocks, blocks - t * kTileBlocks));
                 const uint32_t full = full0 + 8 * st;
+                if (is_k) {
+                    // Blocks with an invalid id, for the softmax (which is behind by less than 12 tiles: the place is free).
+                    const uint32_t bad = __ballot_sync(0xffffffffu, lane < load && now != id);
+                    if (lane == 0) {
+                        sts32(sbase + L::kOffBad + 4 * (j & 15), bad);
+                        if (bad && p.status) atomicOr(p.status, kStatusBadBlockId);
+                    }
+                }
                 if (lane == 0) {
                     if (load > 0)
                         mbar_arrive_expect_tx(full, load * L::kBlk);
@@ -619,6 +676,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         asm volatile("cp.async.wait_all;" ::: "memory");
         // (given up: the copies still on their way land before the CTA ends)
         if (!ok && lane == 0)
+#pragma unroll 1
             for (int i = max(0, j - stages); i < j; ++i) mbar_wait(full0 + 8 * (i % stages), (i / stages) & 1);
     } else if (FP8 && warp >= kWarpExpand) {
         // ---------------- V's codes of every third tile expanded to fp16 ----------------
@@ -626,9 +684,11 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         const int row = lane >> 3, c = lane & 7;  // of a block: rows row + 4 i, codes 16 c .. 16 c + 15
         int j = 0;
         bool ok = true;
-        for (; ok && w.more(); w.next(p)) {
+#pragma unroll 1
+        for (; ok && w.more(); w.next(p, known)) {
             int t = w.t0 + (x + 2 * j) % 3;  // the piece's first tile whose number j + t - t0 is x modulo 3
             int next = t < w.t1 ? block_id(t) : -1;
+#pragma unroll 1
             for (; t < w.t1; t += 3) {
                 const int mine = next, i = j + t - w.t0, raw_st = i % (FP8 ? L::kStagesRaw : 1), st = i % L::kStagesV;
                 if (t + 3 < w.t1) next = block_id(t + 3);
@@ -674,21 +734,36 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         }
     } else if (warp == kWarpQ) {
         // ---------------- the Q rows of the pieces from the second on ----------------
-        if (w.more()) w.next(p);
-        for (int piece = 1; w.more(); w.next(p), ++piece) {
+        int4 rec = make_int4(0, 0, 0, 0);  // a unit that begins in the last piece and goes on in the next ranges: for the second kernel
+        auto note = [&]() {
+            if (w.t0 > 0 || w.left != w.t1 - w.t0 || w.t1 == w.s.tiles) return;
+            const int64_t end = plan.begin + plan.count - w.t1 + w.s.tiles;  // behind the unit's last tile
+            const int64_t cta = (end * plan.ranges + plan.total - 1) / plan.total - 1;
+            rec = make_int4(w.b, w.g * w.s.row_tiles + w.row_tile, static_cast<int>(cta) - static_cast<int>(blockIdx.x) + 1, 0);
+        };
+        if (w.more()) {
+            note();
+            w.next(p, known);
+        }
+#pragma unroll 1
+        for (int piece = 1; w.more(); w.next(p, known), ++piece) {
+            note();
             const int place = piece & 1;
             if (piece > 1 && !warp_wait(q_empty(place), ((piece >> 1) - 1) & 1)) break;
-            load_q<FP8>(p, w.s.row0, w.row_tile() * kRows, w.rows(p), w.kv_head() * G, sbase + L::kOffQ + place * L::kQTile,
+            load_q<FP8>(p, w.s.row0, w.row_tile * kRows, w.rows(p), w.g * G, sbase + L::kOffQ + place * L::kQTile,
                         reinterpret_cast<float *>(smem + L::kOffRow) + place * kRows, 0, 1);
             if (lane == 0) mbar_arrive(q_full(place));
         }
+        if (lane == 0) p.record[blockIdx.x] = rec;
     } else if (warp == kWarpS) {
         // ---------------- S = Q K^T ----------------
         int j = 0;
         bool ok = true;
-        for (int piece = 0; ok && w.more(); w.next(p), ++piece) {
+#pragma unroll 1
+        for (int piece = 0; ok && w.more(); w.next(p, known), ++piece) {
             const int place = piece & 1;
             if (!(ok = warp_wait(q_full(place), (piece >> 1) & 1))) break;
+#pragma unroll 1
             for (int t = w.t0; t < w.t1; ++t, ++j) {
                 const int st = j % L::kStagesK;
                 ok = warp_wait(k_full(st), (j / L::kStagesK) & 1);
@@ -720,7 +795,9 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         // ---------------- O += P V ----------------
         int j = 0;
         bool ok = true;
-        for (int piece = 0; ok && w.more(); w.next(p), ++piece) {
+#pragma unroll 1
+        for (int piece = 0; ok && w.more(); w.next(p, known), ++piece) {
+#pragma unroll 1
             for (int t = w.t0; t < w.t1; ++t, ++j) {
                 const int st = j % L::kStagesV;
                 ok = warp_wait(v_full(st), (j / L::kStagesV) & 1);
@@ -753,7 +830,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         const uint32_t t_o = lane_base + kTmemO + 128 * a;
         float2 *ml = reinterpret_cast<float2 *>(smem + L::kOffMl);
         if (w.more()) {  // the first piece's Q, by all of these warps
-            load_q<FP8>(p, w.s.row0, w.row_tile() * kRows, w.rows(p), w.kv_head() * G, sbase + L::kOffQ,
+            load_q<FP8>(p, w.s.row0, w.row_tile * kRows, w.rows(p), w.g * G, sbase + L::kOffQ,
                         reinterpret_cast<float *>(smem + L::kOffRow), warp, 2 * kGroupWarps);
             softmax_sync();
             if (tid == 0) {
@@ -770,11 +847,13 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
             alive = finish_piece<FP8>(p, end, sbase, lane_base, alive);
             pending = false;
         };
-        for (int piece = 0; w.more(); w.next(p), ++piece) {
-            const int rows = w.rows(p), first_row = w.row_tile() * kRows, g = w.kv_head();
+#pragma unroll 1
+        for (int piece = 0; w.more(); w.next(p, known), ++piece) {
+            const int rows = w.rows(p), first_row = w.row_tile * kRows, g = w.g;
             const bool busy = quarter * 32 < rows;  // (warp-uniform: a warp without rows only keeps step)
             const int prefix = w.s.ctx - w.s.n;
-            const int64_t row = static_cast<int64_t>(w.s.row0) + (first_row + r) / G;
+            const int node = by_group(first_row + r, p.group_magic);
+            const int64_t row = static_cast<int64_t>(w.s.row0) + node;
             uint64_t mask = 0;
             if (r < rows && w.s.ctx > 0) {
                 mask = __ldg(reinterpret_cast<const unsigned long long *>(p.mask) + row);  // (not looked at before the tree's tiles)
@@ -782,20 +861,15 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
             float sl2 = p.scale_log2;
             float m = -INFINITY, l = 0.f;
             const int t_first = w.t0 + ((j0 ^ a) & 1);
-            int id = t_first < w.t1 ? block_id(t_first) : -1;  // read a tile ahead
+#pragma unroll 1
             for (int t = t_first; t < w.t1; t += 2) {
                 const int j = j0 + t - w.t0;
-                // blocks of this tile with an invalid id
-                const bool wrong = lane < kTileBlocks && (t * kTileBlocks + lane) * kBlockSize < w.s.ctx &&
-                                   static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks);
-                const uint32_t bad = __ballot_sync(0xffffffffu, wrong);
-                if (t + 2 < w.t1) id = block_id(t + 2);
-                if (bad && quarter == 0 && lane == 0 && p.status) atomicOr(p.status, kStatusBadBlockId);
-                if constexpr (FP8) alive = alive && warp_wait(raw_full(j % L::kStagesRaw), (j / L::kStagesRaw) & 1);  // (the scales)
-                alive = alive && warp_wait(s_full(j), phase(j));
+                if constexpr (FP8) alive = alive && softmax_wait(raw_full(j % L::kStagesRaw), (j / L::kStagesRaw) & 1, abort_flag);  // (the scales)
+                alive = alive && softmax_wait(s_full(j), phase(j), abort_flag);
                 if (!alive) continue;
                 tc_fence_after();
                 const uint32_t t_s = lane_base + kKeys * (j % kPlaces);
+                const uint32_t bad = reinterpret_cast<const volatile uint32_t *>(smem + L::kOffBad)[j & 15];
                 if (busy) {
                     if constexpr (FP8) {
                         // (a factor of 0 counts as the least normal number: a hidden key's -inf times it stays one)
@@ -810,10 +884,11 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     // Tiles that not every row sees whole: the scores are scaled and the hidden ones -inf before the pass below,
                     // which then scales them by 1.  (A loop of its own, once or twice a sequence: in the pass, whose code the
                     // instruction caches have to hold beside six other roles', selects cost every tile.)
-                    if (t * kKeys + kKeys > prefix || bad) {
+                    if (__builtin_expect(t * kKeys + kKeys > prefix || bad, 0)) {
                         const int at = t * kKeys - prefix;  // node of the tile's first key
                         const uint64_t nodes = w.s.n < 64 ? mask & ((1ull << w.s.n) - 1) : mask;
                         uint64_t seen = at >= 0 ? (at < 64 ? nodes >> at : 0) : at > -64 ? ((1ull << -at) - 1) | (nodes << -at) : ~0ull;
+#pragma unroll 1
                         for (int k = 0; k < kTileBlocks; ++k)
                             if ((bad >> k) & 1) seen &= ~(0xffffull << (16 * k));
 #pragma unroll 1
@@ -833,40 +908,45 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                         if constexpr (FP8) {
                             k_scales = sbase + L::kOffOnes;
                             // V scales that belong to no key may be anything: 1 (every warp writes the same)
+#pragma unroll 1
                             for (int k = lane; k < kKeys; k += 32)
                                 if (t * kKeys + k >= w.s.ctx || ((bad >> (k >> 4)) & 1)) sts32(scales + 4 * (kKeys + k), 0x3f800000u);
                             fence_proxy_async_smem();  // (the next copy there comes behind)
                             __syncwarp();
                         }
                     }
-                    uint32_t v[64];
-                    tmem_ld_32x32b_x64(t_s, v);
-                    // scores in the log2 domain (FP8: times each key's K scale, before the row's factor), and the row's largest
+                    // The row's largest score in the log2 domain.  (FP8: 32 keys at a time, scaled by each key's K scale and put
+                    // back; the row's factor comes behind.  All 64 at once leave no registers for the scales: spilled
+                    // ones come back through the L1 that 200 KB of shared memory leave, 403 us for 211.)
+                    constexpr int kPass = FP8 ? 32 : kKeys;
+                    uint32_t v[kPass];
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    float2 f4[8];  // FP8: scales of 16 keys
-                    auto load_scales = [&](uint32_t from) {
+#pragma unroll 1
+                    for (int c = 0; c < kKeys / kPass; ++c) {
+                        if constexpr (FP8)
+                            tmem_ld_32x32b_x32(t_s + kPass * c, v);
+                        else
+                            tmem_ld_32x32b_x64(t_s, v);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 f = lds128(from + 16 * i);
-                            f4[2 * i] = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
-                            f4[2 * i + 1] = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
+                        for (int i = 0; i < kPass / 4; ++i) {
+                            float2 f0 = sl2v, f1 = sl2v;
+                            if constexpr (FP8) {
+                                const uint4 f = lds128(k_scales + 128 * c + 16 * i);
+                                f0 = make_float2(__uint_as_float(f.x), __uint_as_float(f.y));
+                                f1 = make_float2(__uint_as_float(f.z), __uint_as_float(f.w));
+                            }
+                            const float2 x = fmul2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), f0);
+                            const float2 y = fmul2(make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), f1);
+                            mx[2 * (i & 1)] = fmax3(mx[2 * (i & 1)], x.x, x.y);
+                            mx[2 * (i & 1) + 1] = fmax3(mx[2 * (i & 1) + 1], y.x, y.y);
+                            if constexpr (FP8) {
+                                v[4 * i] = __float_as_uint(x.x);
+                                v[4 * i + 1] = __float_as_uint(x.y);
+                                v[4 * i + 2] = __float_as_uint(y.x);
+                                v[4 * i + 3] = __float_as_uint(y.y);
+                            }
                         }
-                    };
-                    if constexpr (FP8) load_scales(k_scales);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float2 f[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) f[i] = FP8 ? f4[i] : sl2v;
-                        if constexpr (FP8) load_scales(c < 3 ? k_scales + 64 * (c + 1) : scales + kKeys * 4);  // (the next ones, at last V's first)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int k = 16 * c + 2 * i;
-                            const float2 x = fmul2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), f[i]);
-                            v[k] = __float_as_uint(x.x);
-                            v[k + 1] = __float_as_uint(x.y);
-                            mx[i & 3] = fmax3(mx[i & 3], x.x, x.y);
-                        }
+                        if constexpr (FP8) tmem_st_32x32b_x32(t_s + kPass * c, v);
                     }
                     float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if constexpr (FP8) {
@@ -876,6 +956,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                         const uint32_t most = __reduce_max_sync(
                             0xffffffffu, max(__float_as_uint(sv.x) & 0x7fffffffu, __float_as_uint(sv.y) & 0x7fffffffu));
                         mt = fmaf(mt, sl2, static_cast<float>(min(max(static_cast<int>(most >> 23) - 127, -90), 100)));
+                        tmem_wait_st();
                     }
                     float alpha = 1.f;
                     if (mt > m + 8.f) {
@@ -883,8 +964,8 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                         m = mt;
                     }
                     // O rescaled, behind the P V of this group's tile before
-                    if (t >= w.t0 + 2 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                        alive = warp_wait(pv_done(j - 2), phase(j - 2));
+                    if (__builtin_expect(t >= w.t0 + 2 && __any_sync(0xffffffffu, alpha != 1.f), 0)) {
+                        alive = softmax_wait(pv_done(j - 2), phase(j - 2), abort_flag);
                         tc_fence_after();
                         if (alive) {
 #pragma unroll 1
@@ -901,38 +982,40 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     const float mu = m == -INFINITY ? 0.f : m;
                     const float2 nmu = make_float2(-mu, -mu);
                     float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
+                    const float2 slope = FP8 ? make_float2(sl2, sl2) : sl2v;
+#pragma unroll 1
+                    for (int c = 0; c < kKeys / kPass; ++c) {
+                        if constexpr (FP8) tmem_ld_32x32b_x32(t_s + kPass * c, v);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {  // 16 keys: 8 columns of heads, 8 of remainders
-                        uint32_t pk[FP8 ? 8 : 16];
-                        float2 f[8];
-                        if constexpr (FP8) {
+                        for (int h = 0; h < kPass / 16; ++h) {  // 16 keys: 8 columns of heads, 8 of remainders
+                            uint32_t pk[FP8 ? 8 : 16];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) f[i] = f4[i];
-                            if (c < 3) load_scales(scales + kKeys * 4 + 64 * (c + 1));
-                        }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int k = 16 * c + 2 * e;
-                            const float2 s2 = make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-                            const float2 x = FP8 ? ffma2(s2, make_float2(sl2, sl2), nmu) : fadd2(s2, nmu);
-                            float2 pr = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                            if (e & 1)
-                                rs1 = fadd2(rs1, pr);
-                            else
-                                rs0 = fadd2(rs0, pr);
-                            if constexpr (FP8) {  // (the sum keeps the plain weights)
-                                pr = fmul2(pr, f[e]);
-                                pk[e] = pack_f16x2(pr.x, pr.y);
-                            } else {
-                                pk[e] = __byte_perm(__float_as_uint(pr.x), __float_as_uint(pr.y), 0x7632);
-                                const float2 rest = minus_bf16x2(pr, pk[e]);
-                                pk[8 + e] = pack_bf16x2(rest.x, rest.y);
+                            for (int e = 0; e < 8; e += 2) {
+                                const int k = 16 * h + 2 * e;
+                                const float2 x = ffma2(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), slope, nmu);
+                                const float2 y = ffma2(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), slope, nmu);
+                                float2 px = make_float2(fast_exp2(x.x), fast_exp2(x.y)), py = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                                rs0 = fadd2(rs0, px);
+                                rs1 = fadd2(rs1, py);
+                                if constexpr (FP8) {  // (the sum keeps the plain weights)
+                                    const uint4 f = lds128(scales + (kKeys + kPass * c + k) * 4);
+                                    px = fmul2(px, make_float2(__uint_as_float(f.x), __uint_as_float(f.y)));
+                                    py = fmul2(py, make_float2(__uint_as_float(f.z), __uint_as_float(f.w)));
+                                    pk[e] = pack_f16x2(px.x, px.y);
+                                    pk[e + 1] = pack_f16x2(py.x, py.y);
+                                } else {
+                                    pk[e] = __byte_perm(__float_as_uint(px.x), __float_as_uint(px.y), 0x7632);
+                                    pk[e + 1] = __byte_perm(__float_as_uint(py.x), __float_as_uint(py.y), 0x7632);
+                                    const float2 ex = minus_bf16x2(px, pk[e]), ey = minus_bf16x2(py, pk[e + 1]);
+                                    pk[8 + e] = pack_bf16x2(ex.x, ex.y);
+                                    pk[9 + e] = pack_bf16x2(ey.x, ey.y);
+                                }
                             }
+                            if constexpr (FP8)
+                                tmem_st_32x32b_x8(t_s + kPass * c + 16 * h, pk);
+                            else
+                                tmem_st_32x32b_x16(t_s + kPass * c + 16 * h, pk);
                         }
-                        if constexpr (FP8)
-                            tmem_st_32x32b_x8(t_s + 16 * c, pk);
-                        else
-                            tmem_st_32x32b_x16(t_s + 16 * c, pk);
                     }
                     const float2 rs = fadd2(rs0, rs1);
                     l = l * alpha + (rs.x + rs.y);
@@ -941,10 +1024,11 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 // V rows of keys that are not the sequence's, or of a bad block: zeros before the P V reads them (FP8: by the
                 // expansion)
                 const int past = w.s.ctx - t * kKeys;
-                if (!FP8 && (past < kKeys || bad)) {
-                    alive = warp_wait(v_full(j % L::kStagesV), (j / L::kStagesV) & 1);
+                if (__builtin_expect(!FP8 && (past < kKeys || bad), 0)) {
+                    alive = softmax_wait(v_full(j % L::kStagesV), (j / L::kStagesV) & 1, abort_flag);
                     if (!alive) continue;
                     const uint32_t vb = sbase + L::kOffV + (j % L::kStagesV) * kVTile;
+#pragma unroll 1
                     for (int i = r; i < kKeys * 16; i += kGroupWarps * 32) {
                         const int key = i >> 4, ch = i & 15;  // (all 16 chunks of a row: the swizzle is moot)
                         if (key >= past || ((bad >> (key >> 4)) & 1u))
@@ -972,22 +1056,11 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
             end.had0 = tiles > 1 || (j0 & 1) == 0;
             end.had1 = tiles > 1 || (j0 & 1) == 1;
             end.direct = tiles == w.s.tiles;
-            end.to = end.direct ? row * p.n_q + static_cast<int64_t>(g) * G + (first_row + r) % G
+            end.to = end.direct ? row * p.n_q + static_cast<int64_t>(g) * G + (first_row + r - node * G)
                                 : (static_cast<int64_t>(blockIdx.x) * 2 + (w.t0 > 0 ? 0 : 1)) * p.part_rows + r;
             j0 += tiles;
-            // A unit that begins here and goes on in the next ranges is joined by the second kernel.
-            if (tid == 0 && w.left == tiles) {
-                int4 rec = make_int4(0, 0, 0, 0);
-                if (w.t0 == 0 && tiles < w.s.tiles) {
-                    const int64_t end = plan.begin + plan.count - tiles + w.s.tiles;  // behind the unit's last tile
-                    const int64_t cta = (end * plan.ranges + plan.total - 1) / plan.total - 1;
-                    rec = make_int4(w.b, w.unit, static_cast<int>(cta) - static_cast<int>(blockIdx.x) + 1, 0);
-                }
-                p.record[blockIdx.x] = rec;
-            }
         }
         if (pending) finish();
-        if (tid == 0 && plan.count == 0) p.record[blockIdx.x] = make_int4(0, 0, 0, 0);
     }
 
     // ---- every role is done (or gave up): tensor memory is freed ----

@@ -163,7 +163,7 @@ def test_reference_rotation_turns_back():
     (dict(q=FAKE + 8), INV), (dict(m=FAKE + 4), INV), (dict(kc=FAKE + 8), INV), (dict(cu=FAKE + 2), INV),
     (dict(ws=FAKE + 128), INV), (dict(wb=256), WS), (dict(od=2), UNS), (dict(B=0), INV), (dict(B=65536), INV),
     (dict(most=0), INV), (dict(most=65), INV), (dict(rows=-1), INV), (dict(h=0), INV), (dict(h=12), INV),
-    (dict(h=80000), UNS), (dict(mb=0), INV), (dict(mb=1 << 27), INV), (dict(s=NAN), INV), (dict(s=INF), INV),
+    (dict(h=1032), UNS), (dict(mb=0), INV), (dict(mb=1 << 27), INV), (dict(s=NAN), INV), (dict(s=INF), INV),
     (dict(s=3e38), INV), (dict(ks=FAKE), INV), (dict(c=dict(dtype=2)), INV), (dict(c=dict(dtype=2), ks=FAKE, vs=FAKE + 4), INV),
     (dict(c=dict(num_blocks=1 << 30)), UNS), (dict(rows=0), 0), *[(dict(c=k), w) for k, w in BAD_DESC],
 ])
