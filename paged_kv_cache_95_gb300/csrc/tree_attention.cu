@@ -84,7 +84,8 @@ struct Layout {
     static constexpr int kExpandWarps = FP8 ? 3 : 0;
     static constexpr int kThreads = (kWarpExpand + kExpandWarps) * 32;
     static constexpr int kStagesK = FP8 ? 6 : 5, kStagesV = FP8 ? 4 : 5;
-    static constexpr int kStagesRaw = FP8 ? 5 : 0;  // of V's codes and both scales
+    static constexpr int kStagesRaw = FP8 ? 5 : 0;     // of V's codes
+    static constexpr int kStagesScale = FP8 ? 12 : 0;  // of both scales, which stay until the softmax is done with the tile
     static constexpr uint32_t kBlk = FP8 ? kCodeBytes : kBlkBytes;  // of the pool
     static constexpr uint32_t kKTile = kTileBlocks * kBlk;
     // Two places of [value half][128 rows][128 B], FP8: [codes, remainders' codes][128 rows][128 B]
@@ -93,12 +94,13 @@ struct Layout {
     static constexpr uint32_t kOffV = kOffK + kStagesK * kKTile;
     static constexpr uint32_t kOffRaw = kOffV + kStagesV * kVTile;
     static constexpr uint32_t kOffScale = kOffRaw + kStagesRaw * kTileBlocks * kCodeBytes;  // FP8: [tile][K, V][64]
-    static constexpr uint32_t kOffOnes = kOffScale + kStagesRaw * 2 * kKeys * 4;  // FP8: a tile's K scales, all 1
+    static constexpr uint32_t kOffOnes = kOffScale + kStagesScale * 2 * kKeys * 4;  // FP8: a tile's K scales, all 1
     static constexpr uint32_t kOffRow = kOffOnes + (FP8 ? kKeys * 4 : 0);  // FP8: factors of Q's rows, two places
     static constexpr uint32_t kOffBad = kOffRow + (FP8 ? 2 * kRows * 4 : 0);  // [tile modulo 16]: blocks with an invalid id
-    static constexpr uint32_t kOffMl = kOffBad + 16 * 4;  // (m, l) of the groups' rows
+    static constexpr uint32_t kOffMl = kOffBad + (FP8 ? 2 : 1) * 16 * 4;  // (m, l) of the groups' rows
     static constexpr uint32_t kOffBar = kOffMl + 2 * kRows * 8;
-    static constexpr int kBarRaw = 2 * kStagesK + 2 * kStagesV, kBarQ = kBarRaw + 2 * kStagesRaw, kBarS = kBarQ + 4;
+    static constexpr int kBarRaw = 2 * kStagesK + 2 * kStagesV, kBarScale = kBarRaw + 2 * kStagesRaw;
+    static constexpr int kBarQ = kBarScale + 2 * kStagesScale, kBarS = kBarQ + 4;
     static constexpr int kBarOFree = kBarS + 3 * kPlaces, kBarOReady = kBarOFree + 1, kBars = kBarOFree + 5;
     static constexpr uint32_t kOffPlan = kOffBar + 8 * kBars;
     static constexpr uint32_t kOffSequences = kOffPlan + 96;
@@ -150,9 +152,12 @@ __device__ __forceinline__ bool mbar_sleep_wait(uint32_t bar, uint32_t parity) {
 }
 
 // A whole warp waits for a barrier's phase, within a bound, and gives up at once after another role gave up.
-// (What is complete already costs one test; then lane 0 alone polls, in code that is not repeated at every wait: the
-// roles' loops share the instruction caches.)
+// (What is complete already costs one test; then come some polls, asleep in code that is not repeated at every wait: the
+// roles' loops share the instruction caches.  Without the polls a waking costs what makes FP8 225 us for 191.)
 __device__ __noinline__ bool warp_wait_on(uint32_t bar, uint32_t parity, uint32_t abort_at) {
+#pragma unroll 1
+    for (int i = 0; i < 40; ++i)
+        if (__any_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
     bool ok = false;
     if ((threadIdx.x & 31) == 0) {
         uint32_t gave_up;
@@ -532,6 +537,8 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     auto v_empty = [&](int st) { return bar(2 * L::kStagesK + L::kStagesV + st); };
     auto raw_full = [&](int st) { return bar(L::kBarRaw + st); };
     auto raw_empty = [&](int st) { return bar(L::kBarRaw + L::kStagesRaw + st); };
+    auto scale_full = [&](int st) { return bar(L::kBarScale + st); };
+    auto scale_empty = [&](int st) { return bar(L::kBarScale + L::kStagesScale + st); };
     auto q_full = [&](int place) { return bar(L::kBarQ + place); };
     auto q_empty = [&](int place) { return bar(L::kBarQ + 2 + place); };
     // of tile j: place j % kPlaces, phase j / kPlaces
@@ -560,8 +567,12 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
             mbar_init(v_empty(st), 1);
         }
         for (int st = 0; st < L::kStagesRaw; ++st) {
-            mbar_init(raw_full(st), 1 + 32);  // the codes, and a lane's share of the scales each
-            mbar_init(raw_empty(st), 1 + kGroupWarps);  // the expansion, and the softmax of the tile
+            mbar_init(raw_full(st), 1);
+            mbar_init(raw_empty(st), 1);
+        }
+        for (int st = 0; st < L::kStagesScale; ++st) {
+            mbar_init(scale_full(st), 32);  // a lane's share each
+            mbar_init(scale_empty(st), kGroupWarps);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full(i), 1);
@@ -602,13 +613,15 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
 
     Walk w;
     w.start(p, plan);
-    // Lane k < 4: the id of block k of tile t (-1: none).
-    auto block_id = [&](int t) -> int {
-        const int blocks = (w.s.ctx + kBlockSize - 1) / kBlockSize, at = t * kTileBlocks + lane;
-        return lane < kTileBlocks && at < blocks ? __ldg(p.block_tables + static_cast<int64_t>(w.b) * p.max_blocks + at) : -1;
+    // A lane's block id of the eight tiles from t on (-1: none), read eight tiles ahead: a read behind full rings takes longer
+    // than a tile.
+    constexpr int kAhead = 32 / kTileBlocks;
+    auto block_ids = [&](int t) -> int {
+        const int at = t * kTileBlocks + lane;
+        return at < (w.s.ctx + kBlockSize - 1) / kBlockSize ? __ldg(p.block_tables + static_cast<int64_t>(w.b) * p.max_blocks + at) : -1;
     };
     if (warp == kWarpK || warp == kWarpV) {
-        // ---------------- copies: lane k < 4 sends for block k of a tile (FP8: with V, every lane for scales) ----------------
+        // ---------------- copies: one for each of a tile's blocks ----------------
         const bool is_k = warp == kWarpK;
         const bool raw = FP8 && !is_k;
         const int stages = is_k ? L::kStagesK : raw ? L::kStagesRaw : L::kStagesV;
@@ -621,50 +634,62 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
 #pragma unroll 1
         for (; ok && w.more(); w.next(p, known)) {
             const int blocks = (w.s.ctx + kBlockSize - 1) / kBlockSize, g = w.g;
-            int next = block_id(w.t0);
+            int ids = -1, next = block_ids(w.t0);
 #pragma unroll 1
             for (int t = w.t0; t < w.t1; ++t, ++j) {
                 // (an invalid id fetches block 0; its keys are masked)
-                const int now = next, id = static_cast<unsigned>(now) < static_cast<unsigned>(p.num_blocks) ? now : 0;
-                if (t + 1 < w.t1) next = block_id(t + 1);
+                const int turn = (t - w.t0) & (kAhead - 1);
+                if (turn == 0) {
+                    ids = next;
+                    if (t + kAhead < w.t1) next = block_ids(t + kAhead);
+                }
+                const int now = __shfl_sync(0xffffffffu, ids, turn * kTileBlocks + (lane & (kTileBlocks - 1)));
+                const int id = static_cast<unsigned>(now) < static_cast<unsigned>(p.num_blocks) ? now : 0;
                 // (behind full rings a read takes 5 us: the first piece's Q before them)
                 if (j == 2 && !(ok = warp_wait(q_first, 0))) break;
                 if (use > 0 && !(ok = warp_wait(empty0 + 8 * st, (use - 1) & 1))) break;
                 const int load = max(0, min(kTileBlocks, blocks - t * kTileBlocks));
                 const uint32_t full = full0 + 8 * st;
-                if (is_k) {
-                    // Blocks with an invalid id, for the softmax (which is behind by less than 12 tiles: the place is free).
+                if (is_k || FP8) {
+                    // Blocks with an invalid id, for the softmax (which is behind by less than 12 tiles: the place is free)
+                    // and, FP8, for the expansion.
                     const uint32_t bad = __ballot_sync(0xffffffffu, lane < load && now != id);
                     if (lane == 0) {
-                        sts32(sbase + L::kOffBad + 4 * (j & 15), bad);
-                        if (bad && p.status) atomicOr(p.status, kStatusBadBlockId);
+                        sts32(sbase + L::kOffBad + 4 * (j & 15) + (is_k ? 0 : 64), bad);
+                        if (is_k && bad && p.status) atomicOr(p.status, kStatusBadBlockId);
                     }
                 }
-                if (lane == 0) {
+                int block[kTileBlocks];
+#pragma unroll
+                for (int k = 0; k < kTileBlocks; ++k) block[k] = __shfl_sync(0xffffffffu, id, k);
+                if (elect_one()) {
                     if (load > 0)
                         mbar_arrive_expect_tx(full, load * L::kBlk);
                     else
                         mbar_arrive(full);
-                }
-                __syncwarp();
-                const uint32_t dst = ring + (st * kTileBlocks + lane) * L::kBlk;
-                if (lane < load) {
-                    if constexpr (FP8) {
-                        tma_load_4d(dst, map, full, 0, 0, g, id);
-                    } else {
-                        tma_load_5d(dst, map, full, 0, 0, 0, 0, id * p.n_kv + g);
+                    const uint32_t dst = ring + st * kTileBlocks * L::kBlk;
+#pragma unroll
+                    for (int k = 0; k < kTileBlocks; ++k) {
+                        if (k < load) {
+                            if constexpr (FP8)
+                                tma_load_4d(dst + k * L::kBlk, map, full, 0, 0, g, block[k]);
+                            else
+                                tma_load_5d(dst + k * L::kBlk, map, full, 0, 0, 0, 0, block[k] * p.n_kv + g);
+                        }
                     }
                 }
+                __syncwarp();
                 if constexpr (FP8) {
-                    // The scales, 16 bytes a lane (8 lanes a block): off the TMA unit, whose copies take 100 cycles and more each.
-                    if (raw) {
-                        const int k = lane >> 3, part = lane & 3;
-                        const int block = __shfl_sync(0xffffffffu, id, k);
+                    // The scales, 16 bytes a lane (4 lanes a block's K scales, 4 its V scales): off the TMA unit.  (By the K warp: the
+                    // V warp runs less far ahead, and Q's fetches would hold them up.)
+                    if (is_k) {
+                        const int place = j % L::kStagesScale, part = lane & 3, k = lane >> 3, of_v = (lane >> 2) & 1;
+                        const int from = __shfl_sync(0xffffffffu, id, k);
+                        if (j >= L::kStagesScale && !(ok = warp_wait(scale_empty(place), ((j / L::kStagesScale) - 1) & 1))) break;
                         if (k < load)
-                            cp_async_16(sbase + L::kOffScale + (st * 2 * kKeys + ((lane >> 2) & 1) * kKeys + k * kBlockSize + 4 * part) * 4,
-                                        ((lane >> 2) & 1 ? p.v_scale : p.k_scale) +
-                                            (static_cast<int64_t>(block) * p.n_kv + g) * kBlockSize + 4 * part);
-                        cp_async_mbar_arrive_noinc(full);
+                            cp_async_16(sbase + L::kOffScale + (place * 2 * kKeys + of_v * kKeys + k * kBlockSize + 4 * part) * 4,
+                                        (of_v ? p.v_scale : p.k_scale) + (static_cast<int64_t>(from) * p.n_kv + g) * kBlockSize + 4 * part);
+                        cp_async_mbar_arrive_noinc(scale_full(place));
                     }
                 }
                 if (++st == stages) {
@@ -687,15 +712,14 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
 #pragma unroll 1
         for (; ok && w.more(); w.next(p, known)) {
             int t = w.t0 + (x + 2 * j) % 3;  // the piece's first tile whose number j + t - t0 is x modulo 3
-            int next = t < w.t1 ? block_id(t) : -1;
 #pragma unroll 1
             for (; t < w.t1; t += 3) {
-                const int mine = next, i = j + t - w.t0, raw_st = i % (FP8 ? L::kStagesRaw : 1), st = i % L::kStagesV;
-                if (t + 3 < w.t1) next = block_id(t + 3);
+                const int i = j + t - w.t0, raw_st = i % (FP8 ? L::kStagesRaw : 1), st = i % L::kStagesV;
                 const int keys = w.s.ctx - t * kKeys;
                 ok = warp_wait(raw_full(raw_st), (i / (FP8 ? L::kStagesRaw : 1)) & 1);
                 if (ok && i >= L::kStagesV) ok = warp_wait(v_empty(st), ((i / L::kStagesV) - 1) & 1);
                 if (!ok) break;
+                const uint32_t bad = reinterpret_cast<const volatile uint32_t *>(smem + L::kOffBad)[16 + (i & 15)];
                 uint4 code[4];  // a block ahead
                 auto read = [&](int k) {
                     const uint32_t src = sbase + L::kOffRaw + (raw_st * kTileBlocks + k) * kCodeBytes + row * 128;
@@ -705,8 +729,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 read(0);
 #pragma unroll 1
                 for (int k = 0; k < kTileBlocks; ++k) {
-                    const int id = __shfl_sync(0xffffffffu, mine, k);
-                    const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
+                    const bool good = ((bad >> k) & 1) == 0;
                     const uint32_t dst = sbase + L::kOffV + st * kVTile + k * kBlkBytes + (c >> 2) * 1024;
                     uint4 a[4], b[4];
 #pragma unroll
@@ -864,7 +887,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
 #pragma unroll 1
             for (int t = t_first; t < w.t1; t += 2) {
                 const int j = j0 + t - w.t0;
-                if constexpr (FP8) alive = alive && softmax_wait(raw_full(j % L::kStagesRaw), (j / L::kStagesRaw) & 1, abort_flag);  // (the scales)
+                if constexpr (FP8) alive = alive && softmax_wait(scale_full(j % L::kStagesScale), (j / L::kStagesScale) & 1, abort_flag);
                 alive = alive && softmax_wait(s_full(j), phase(j), abort_flag);
                 if (!alive) continue;
                 tc_fence_after();
@@ -878,7 +901,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                             if (sl2 < 0x1p-126f) sl2 = 0x1p-126f;
                         }
                     }
-                    const uint32_t scales = sbase + L::kOffScale + (j % (FP8 ? L::kStagesRaw : 1)) * 2 * kKeys * 4;
+                    const uint32_t scales = sbase + L::kOffScale + (j % (FP8 ? L::kStagesScale : 1)) * 2 * kKeys * 4;
                     float2 sl2v = make_float2(sl2, sl2);  // (bf16)
                     uint32_t k_scales = scales;
                     // Tiles that not every row sees whole: the scores are scaled and the hidden ones -inf before the pass below,
@@ -1042,7 +1065,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(p_full(j));
-                    if constexpr (FP8) mbar_arrive(raw_empty(j % L::kStagesRaw));  // (the scales have been read)
+                    if constexpr (FP8) mbar_arrive(scale_empty(j % L::kStagesScale));
                 }
                 if (pending) finish();
             }
