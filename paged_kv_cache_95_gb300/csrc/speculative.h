@@ -46,6 +46,7 @@ struct TreeParams {
     const float *k_scale, *v_scale;  // FP8 pool only
     uint32_t *status;
     int32_t num_seqs, n_q, n_kv, group, max_blocks, num_blocks, total_rows, max_q_len;
+    int32_t whole_nodes;   // 128 / group where that is whole (Q by copies of whole nodes), else 0
     uint32_t group_magic;  // 2^32 / group rounded up (0 for a group of 1)
     float scale_log2;
     int32_t out_bf16;
@@ -56,7 +57,7 @@ struct TreeParams {
     float *part_o;              // the same x [128], unnormalised
 };
 cudaError_t tree_prepare_device();
-cudaError_t launch_tree_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, const TreeParams &p, bool fp8,
+cudaError_t launch_tree_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &qmap, const TreeParams &p, bool fp8,
                                   cudaStream_t stream);
 
 // ---- verification of drafted tokens, compaction of the accepted path -----------------

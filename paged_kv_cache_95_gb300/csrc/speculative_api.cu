@@ -306,13 +306,15 @@ int paged_attention_tree(void *out, int32_t out_dtype, const void *q, const uint
     std::call_once(g_tree_prepared[dev], [&] { g_tree_prep_err[dev] = pkv::tree_prepare_device(); });
     if (g_tree_prep_err[dev] != cudaSuccess) return PKV_ERR_CUDA;
     const int32_t n_kv = cache->num_kv_heads;
-    CUtensorMap kmap, vmap;
+    const int32_t group = num_q_heads / n_kv, whole_nodes = 128 % group == 0 ? 128 / group : 0;
+    CUtensorMap kmap, vmap, qmap{};
     if (!(fp8 ? pkv::encode_pool_map_fp8(&kmap, k_cache, cache->num_blocks, n_kv)
               : pkv::encode_pool_tile_map(&kmap, k_cache, cache->num_blocks, n_kv)) ||
         !(fp8 ? pkv::encode_pool_map_fp8(&vmap, v_cache, cache->num_blocks, n_kv)
-              : pkv::encode_pool_tile_map(&vmap, v_cache, cache->num_blocks, n_kv)))
+              : pkv::encode_pool_tile_map(&vmap, v_cache, cache->num_blocks, n_kv)) ||
+        (whole_nodes && !pkv::encode_query_group_map(&qmap, q, total_q_rows, num_q_heads, group)))
         return PKV_ERR_CUDA;
-    const TreePlan pl = plan_tree(num_q_heads / n_kv, max_q_len, sms);
+    const TreePlan pl = plan_tree(group, max_q_len, sms);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.q = q;
     p.out = out;
@@ -326,7 +328,8 @@ int paged_attention_tree(void *out, int32_t out_dtype, const void *q, const uint
     p.num_seqs = num_seqs;
     p.n_q = num_q_heads;
     p.n_kv = n_kv;
-    p.group = num_q_heads / n_kv;
+    p.group = group;
+    p.whole_nodes = whole_nodes;
     p.group_magic = p.group > 1 ? static_cast<uint32_t>(((uint64_t{1} << 32) + p.group - 1) / p.group) : 0;
     p.max_blocks = max_blocks_per_seq;
     p.num_blocks = cache->num_blocks;
@@ -338,7 +341,7 @@ int paged_attention_tree(void *out, int32_t out_dtype, const void *q, const uint
     p.record = reinterpret_cast<int4 *>(ws + kStatusBytes);
     p.part_ml = reinterpret_cast<float2 *>(ws + pl.off_ml);
     p.part_o = reinterpret_cast<float *>(ws + pl.off_o);
-    return finish(pkv::launch_tree_attention(kmap, vmap, p, fp8, static_cast<cudaStream_t>(stream)));
+    return finish(pkv::launch_tree_attention(kmap, vmap, qmap, p, fp8, static_cast<cudaStream_t>(stream)));
 }
 
 int speculative_verify(int32_t *tokens_out, int32_t *path, int32_t *counts, const float *target_probs,

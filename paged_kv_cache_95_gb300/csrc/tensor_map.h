@@ -65,4 +65,18 @@ inline bool encode_pool_tile_map(CUtensorMap *map, const void *base, int32_t num
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Query rows [rows][n_q][128] of bf16; a box (64 values, `group` heads, 128 / group rows) lands as 128 lines of 128 bytes,
+// 128-byte swizzle: one value half of the heads of a KV head, row after row.
+inline bool encode_query_group_map(CUtensorMap *map, const void *base, int32_t rows, int32_t n_q, int32_t group) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(n_q), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {2ull * kHeadDim, 2ull * kHeadDim * n_q};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(128 / group)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace pkv

@@ -22,9 +22,11 @@
 //    ahead of the pieces.  (One warp for both takes 2700 cycles for 64 keys, of which HBM leaves 1400;
 //    V by 16-byte asynchronous copies instead: what any warp reads then waits behind them, a
 //    piece's 128 rows of Q 6 us.)
-//  * 11 plans the CTA's range and fetches the pieces' Q rows (any G), a piece ahead into two places
-//    in turn; the first piece's come by the softmax warps, before the rings fill (behind full rings
-//    any read takes 5 us).
+//  * 11 plans the CTA's range and fetches the pieces' Q rows, a piece ahead into two places in turn: by two
+//    TMA copies where a tile holds whole nodes (G divides 128), else row by row, which takes the warp
+//    9000 cycles for 128 rows (FP8, 64 sequences of 512 .. 4096 tokens: 221 us, 168 with the copies); the first
+//    piece's rows then come by the softmax warps, before the rings fill (behind full rings any
+//    read takes 5 us).  FP8: it also makes them codes, and fetches every tile's scales.
 //  * 9 issues S = Q K^T, 10 P V (run whole, one elected lane issues: descriptors stay in uniform
 //    registers; one warp for both took 3500 cycles for 128 keys, of which HBM leaves 2800).  Tensor
 //    memory: S of tile j in [64 (j & 3), +64), O of the even and of the odd tiles in [256, +128) and
@@ -43,7 +45,7 @@
 // FP8 pool (E4M3 codes, one scale per key and head).  K's codes are the B operand as they are; a row of Q
 // is two rows of E4M3 codes, what the first leaves in the second, scaled by the power of two that
 // puts the row's largest value in [2^7, 2^8): exact down to 2^-9 of that value, 2^-17 of it below.
-// V's codes come into a ring of their own, with both scales; 13-15 take every third tile each
+// V's codes come into a ring of their own; 13-15 take every third tile each
 // and expand it to fp16 (exact) into the V ring.  K's scale multiplies the scores, V's the weights,
 // which enter P V rounded to fp16 (2^-12; as bf16 heads and remainders of V in bf16 a tile took
 // 1.4 times the instructions).  The reference m counts the exponent of a tile's largest V scale in, so that
@@ -100,7 +102,7 @@ struct Layout {
     static constexpr uint32_t kOffMl = kOffBad + (FP8 ? 2 : 1) * 16 * 4;  // (m, l) of the groups' rows
     static constexpr uint32_t kOffBar = kOffMl + 2 * kRows * 8;
     static constexpr int kBarRaw = 2 * kStagesK + 2 * kStagesV, kBarScale = kBarRaw + 2 * kStagesRaw;
-    static constexpr int kBarQ = kBarScale + 2 * kStagesScale, kBarS = kBarQ + 4;
+    static constexpr int kBarQ = kBarScale + 2 * kStagesScale, kBarS = kBarQ + 6;
     static constexpr int kBarOFree = kBarS + 3 * kPlaces, kBarOReady = kBarOFree + 1, kBars = kBarOFree + 5;
     static constexpr uint32_t kOffPlan = kOffBar + 8 * kBars;
     static constexpr uint32_t kOffSequences = kOffPlan + 96;
@@ -174,7 +176,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_
 }
 // The same without a call, for the softmax warps: what they hold would have to be saved around one.
 __device__ __forceinline__ bool softmax_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag) {
-    if (__any_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+#pragma unroll 1
+    for (int i = 0; i < 20; ++i)
+        if (__any_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
     bool ok = false;
     if ((threadIdx.x & 31) == 0 && !*abort_flag) {
         ok = mbar_sleep_wait(bar, parity);
@@ -355,68 +359,91 @@ __device__ __forceinline__ void e4m3x16_to_f16(const uint4 &c, uint4 &a, uint4 &
     e4m3x4_to_f16x2x2(c.w, b.z, b.w);
 }
 
-// The Q rows first .. first + rows - 1 of a (sequence, KV head) into the tile at dst, 16 lanes a row: the rows 2 part, 2 part + 1,
-// 2 (part + parts), .. by one warp.  FP8: as two rows of E4M3 codes (dst, dst + 16 KB), and the factor that undoes the
+// A pair of fp16 values to E4M3 codes (in the low 16 bits), to the nearest.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t x) {
+    uint16_t y;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t x, uint32_t y) {
+    uint32_t z;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    return z;
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t x, uint32_t y) {
+    uint32_t z;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    return z;
+}
+
+// The Q rows first .. first + rows - 1 of a (sequence, KV head) into the tile at dst, unless they are there: the eight rows
+// 8 part .., 8 (part + parts) .., .. by one warp.  FP8: as two rows of E4M3 codes (dst, dst + 16 KB), and the factor that undoes the
 // row's power of two.  (Not inlined: two roles call it.)
 template <bool FP8>
 __device__ __noinline__ void load_q(const TreeParams &p, int row0, int first, int rows, int head0, uint32_t dst, float *factor,
-                                    int part, int parts) {
-    const int lane = threadIdx.x & 31, c = lane & 15, G = p.group;
+                                    int part, int parts, bool there) {
+    const int lane = threadIdx.x & 31, G = p.group;
     const uint32_t magic = p.group_magic;
-    const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(p.q) + 8 * c +
+    const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(p.q) + 8 * (lane & 15) +
                                 (static_cast<int64_t>(row0) * p.n_q + head0) * kHeadDim;
-    auto source = [&](int r) -> const __nv_bfloat16 * {  // (rows past the last are read as the last)
-        const int at = first + min(r, rows - 1), node = by_group(at, magic);
-        return base + (static_cast<int64_t>(node) * p.n_q + (at - node * G)) * kHeadDim;
-    };
-    const int step = 2 * parts, first_r = 2 * part + (lane >> 4);
     // Row r's 16-byte chunk c: half c / 8 (FP8: of the raw values too, whose place the codes take).
-    auto place = [&](int r) { return dst + (c >> 3) * kHalfTile + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+    auto place = [&](int r, int c) { return dst + (c >> 3) * kHalfTile + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
 #pragma unroll 1
-    for (int r = first_r; r < rows; r += step) cp_async_16(place(r), source(r));
+    for (int r0 = there ? rows : 8 * part; r0 < rows; r0 += 8 * parts) {
+#pragma unroll 1
+        for (int i = 0; i < 8; i += 2) {  // (16 lanes a row; rows past the last are read as the last)
+            const int r = r0 + i + (lane >> 4), at = first + min(r, rows - 1), node = by_group(at, magic);
+            cp_async_16(place(r, lane & 15), base + (static_cast<int64_t>(node) * p.n_q + (at - node * G)) * kHeadDim);
+        }
+    }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if constexpr (FP8) {
-        // (both halves of the warp take as many steps: the maximum goes by shuffles; a lane reads what it fetched)
+        __syncwarp();
 #pragma unroll 1
-        for (int r = first_r; r - (lane >> 4) < rows; r += step) {
-            const uint4 raw = lds128(place(min(r, kRows - 1)));
-            const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-            float v[8], most = 0.f;
+        for (int r0 = 8 * part; r0 < rows; r0 += 8 * parts) {  // four lanes a row, 32 values each
+            const int r = r0 + (lane >> 2), c = lane & 3;
+            uint32_t u[16], most2 = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                v[2 * k] = __uint_as_float(u[k] << 16);
-                v[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-                most = fmaxf(most, fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
+                const uint4 raw = lds128(place(r, 4 * c + k));
+                u[4 * k] = raw.x;
+                u[4 * k + 1] = raw.y;
+                u[4 * k + 2] = raw.z;
+                u[4 * k + 3] = raw.w;
             }
 #pragma unroll
-            for (int off = 8; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+            for (int k = 0; k < 16; ++k) most2 = max_u16x2(most2, u[k] & 0x7fff7fffu);
+            most2 = max_u16x2(most2, __shfl_xor_sync(0xffffffffu, most2, 1));
+            most2 = max_u16x2(most2, __shfl_xor_sync(0xffffffffu, most2, 2));  // (and every lane has its values)
+            const uint32_t most = max(most2 << 16, most2 & 0xffff0000u);  // as fp32
             // 2^e puts the largest value in [2^7, 2^8) (both powers are normal numbers)
-            const int e = min(126, max(-119, 7 - (static_cast<int>(__float_as_uint(most) >> 23) - 127)));
+            const int e = min(126, max(-119, 7 - (static_cast<int>(most >> 23) - 127)));
             // (a scale below 0 negates the row: the softmax's is above)
             const float up = __uint_as_float((static_cast<uint32_t>(127 + e) << 23) | (p.scale_log2 < 0.f ? 0x80000000u : 0u));
-            uint32_t hi[2], lo[2];
+            const float2 up2 = make_float2(up, up);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float x[4];
+            for (int h = 0; h < 2; ++h) {
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = v[4 * k + i] * up;
-                hi[k] = f32x2_to_e4m3x2(x[0], x[1]) | (f32x2_to_e4m3x2(x[2], x[3]) << 16);
-                uint32_t f0, f1;
-                e4m3x4_to_f16x2x2(hi[k], f0, f1);
-                const float2 h0 = unpack_f16x2(f0), h1 = unpack_f16x2(f1);
-                lo[k] = f32x2_to_e4m3x2(x[0] - h0.x, x[1] - h0.y) | (f32x2_to_e4m3x2(x[2] - h1.x, x[3] - h1.y) << 16);
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t x[2];  // (fp16 holds the 8 bits down to 2^-17, of which E4M3 keeps those down to 2^-10)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t w = u[8 * h + 2 * k + i];
+                        const float2 y = fmul2(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), up2);
+                        x[i] = pack_f16x2(y.x, y.y);
+                    }
+                    hi[k] = f16x2_to_e4m3x2(x[0]) | (f16x2_to_e4m3x2(x[1]) << 16);
+                    uint32_t f0, f1;
+                    e4m3x4_to_f16x2x2(hi[k], f0, f1);
+                    lo[k] = f16x2_to_e4m3x2(sub_f16x2(x[0], f0)) | (f16x2_to_e4m3x2(sub_f16x2(x[1], f1)) << 16);
+                }
+                const uint32_t to = dst + r * 128 + (((2 * c + h) ^ (r & 7)) << 4);
+                sts128(to, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                sts128(to + kHalfTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
             }
-            if (r < rows) {
-                const uint32_t to = dst + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
-                sts32(to, hi[0]);
-                sts32(to + 4, hi[1]);
-                sts32(to + kHalfTile, lo[0]);
-                sts32(to + kHalfTile + 4, lo[1]);
-                // (a row with an infinity has no finite scores: NaN, as a code of 448 would not say)
-                if (c == 0)
-                    factor[r] = most > 3.4e38f ? __uint_as_float(0x7fc00000u)
-                                               : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            }
+            // (a row with an infinity has no finite scores: NaN, as a code of 448 would not say)
+            if (c == 0) factor[r] = most == 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         }
     }
     fence_proxy_async_smem();
@@ -524,6 +551,7 @@ __device__ __noinline__ bool finish_piece(const TreeParams &p, const End end, ui
 template <bool FP8>
 __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                          const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ TreeParams p) {
     using L = Layout<FP8>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -541,6 +569,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     auto scale_empty = [&](int st) { return bar(L::kBarScale + L::kStagesScale + st); };
     auto q_full = [&](int place) { return bar(L::kBarQ + place); };
     auto q_empty = [&](int place) { return bar(L::kBarQ + 2 + place); };
+    auto q_raw = [&](int place) { return bar(L::kBarQ + 4 + place); };  // FP8: before it is codes
     // of tile j: place j % kPlaces, phase j / kPlaces
     auto s_full = [&](int j) { return bar(L::kBarS + j % kPlaces); };
     auto p_full = [&](int j) { return bar(L::kBarS + kPlaces + j % kPlaces); };
@@ -558,6 +587,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     if (tid == 0) {
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
+        if (p.whole_nodes) prefetch_tensormap(&qmap);
         for (int st = 0; st < L::kStagesK; ++st) {
             mbar_init(k_full(st), 1);
             mbar_init(k_empty(st), 1);
@@ -576,6 +606,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(q_full(i), 1);
+            mbar_init(q_raw(i), 1);
             mbar_init(q_empty(i), 2);  // the last S of a piece, and its end
         }
         for (int i = 0; i < kPlaces; ++i) {
@@ -679,19 +710,6 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     }
                 }
                 __syncwarp();
-                if constexpr (FP8) {
-                    // The scales, 16 bytes a lane (4 lanes a block's K scales, 4 its V scales): off the TMA unit.  (By the K warp: the
-                    // V warp runs less far ahead, and Q's fetches would hold them up.)
-                    if (is_k) {
-                        const int place = j % L::kStagesScale, part = lane & 3, k = lane >> 3, of_v = (lane >> 2) & 1;
-                        const int from = __shfl_sync(0xffffffffu, id, k);
-                        if (j >= L::kStagesScale && !(ok = warp_wait(scale_empty(place), ((j / L::kStagesScale) - 1) & 1))) break;
-                        if (k < load)
-                            cp_async_16(sbase + L::kOffScale + (place * 2 * kKeys + of_v * kKeys + k * kBlockSize + 4 * part) * 4,
-                                        (of_v ? p.v_scale : p.k_scale) + (static_cast<int64_t>(from) * p.n_kv + g) * kBlockSize + 4 * part);
-                        cp_async_mbar_arrive_noinc(scale_full(place));
-                    }
-                }
                 if (++st == stages) {
                     st = 0;
                     ++use;
@@ -764,19 +782,60 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
             const int64_t cta = (end * plan.ranges + plan.total - 1) / plan.total - 1;
             rec = make_int4(w.b, w.g * w.s.row_tiles + w.row_tile, static_cast<int>(cta) - static_cast<int>(blockIdx.x) + 1, 0);
         };
-        if (w.more()) {
-            note();
-            w.next(p, known);
-        }
+        int j = 0, sent = 0;
+        bool ok = true;
+        auto arrives = [&](int piece) { return FP8 ? q_raw(piece & 1) : q_full(piece & 1); };  // what the copies complete
 #pragma unroll 1
-        for (int piece = 1; w.more(); w.next(p, known), ++piece) {
+        for (int piece = 0; ok && w.more(); w.next(p, known), ++piece) {
             note();
             const int place = piece & 1;
-            if (piece > 1 && !warp_wait(q_empty(place), ((piece >> 1) - 1) & 1)) break;
-            load_q<FP8>(p, w.s.row0, w.row_tile * kRows, w.rows(p), w.g * G, sbase + L::kOffQ + place * L::kQTile,
-                        reinterpret_cast<float *>(smem + L::kOffRow) + place * kRows, 0, 1);
-            if (lane == 0) mbar_arrive(q_full(place));
+            const uint32_t dst = sbase + L::kOffQ + place * L::kQTile;
+            if (piece > 1 && !(ok = warp_wait(q_empty(place), ((piece >> 1) - 1) & 1))) break;
+            if (p.whole_nodes) {
+                // One copy for each value half: a tile's rows are the G heads of 128 / G nodes.  (Row by row by 16-byte
+                // asynchronous copies the warp takes 9000 cycles for 128 rows.)
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(arrives(piece), L::kQTile);
+                    tma_load_3d(dst, &qmap, arrives(piece), 0, w.g * G, w.s.row0 + w.row_tile * p.whole_nodes);
+                    tma_load_3d(dst + kHalfTile, &qmap, arrives(piece), 64, w.g * G, w.s.row0 + w.row_tile * p.whole_nodes);
+                    if (piece == 0) mbar_arrive(q_first);
+                }
+                __syncwarp();
+                sent = piece + 1;
+            }
+            if (piece > 0 && (FP8 || !p.whole_nodes)) {  // (the first piece's by the softmax warps)
+                if (p.whole_nodes && !(ok = warp_wait(q_raw(place), (piece >> 1) & 1))) break;
+                load_q<FP8>(p, w.s.row0, w.row_tile * kRows, w.rows(p), w.g * G, dst,
+                            reinterpret_cast<float *>(smem + L::kOffRow) + place * kRows, 0, 1, p.whole_nodes != 0);
+                if (lane == 0) mbar_arrive(q_full(place));
+            }
+            if constexpr (FP8) {
+                const int64_t at = static_cast<int64_t>(w.g) * kBlockSize + 4 * (lane & 3);
+                const float *from = ((lane >> 2) & 1) ? p.v_scale : p.k_scale;
+                const uint32_t to = sbase + L::kOffScale + (((lane >> 2) & 1) * kKeys + (lane >> 3) * kBlockSize + 4 * (lane & 3)) * 4;
+                int ids = -1, next = block_ids(w.t0);
+                if (piece == 0 && !(ok = warp_wait(q_first, 0))) break;
+#pragma unroll 1
+                for (int t = w.t0; t < w.t1; ++t, ++j) {
+                    const int turn = (t - w.t0) & (kAhead - 1), place = j % L::kStagesScale;
+                    if (turn == 0) {
+                        ids = next;
+                        if (t + kAhead < w.t1) next = block_ids(t + kAhead);
+                    }
+                    const int now = __shfl_sync(0xffffffffu, ids, turn * kTileBlocks + (lane >> 3));
+                    const int id = static_cast<unsigned>(now) < static_cast<unsigned>(p.num_blocks) ? now : 0;
+                    if (j >= L::kStagesScale && !(ok = warp_wait(scale_empty(place), ((j / L::kStagesScale) - 1) & 1))) break;
+                    if ((t * kTileBlocks + (lane >> 3)) * kBlockSize < w.s.ctx)
+                        cp_async_16(to + place * 2 * kKeys * 4, from + static_cast<int64_t>(id) * p.n_kv * kBlockSize + at);
+                    cp_async_mbar_arrive_noinc(scale_full(place));
+                }
+            }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        // (given up: the copies still on their way land before the CTA ends)
+        if (!ok && lane == 0)
+#pragma unroll 1
+            for (int i = max(0, sent - 2); i < sent; ++i) mbar_wait(arrives(i), (i >> 1) & 1);
         if (lane == 0) p.record[blockIdx.x] = rec;
     } else if (warp == kWarpS) {
         // ---------------- S = Q K^T ----------------
@@ -852,16 +911,17 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t t_o = lane_base + kTmemO + 128 * a;
         float2 *ml = reinterpret_cast<float2 *>(smem + L::kOffMl);
-        if (w.more()) {  // the first piece's Q, by all of these warps
+        bool alive = true;
+        if (w.more() && (FP8 || !p.whole_nodes)) {  // the first piece's Q, by all of these warps
+            if (p.whole_nodes) alive = softmax_wait(q_raw(0), 0, abort_flag);
             load_q<FP8>(p, w.s.row0, w.row_tile * kRows, w.rows(p), w.g * G, sbase + L::kOffQ,
-                        reinterpret_cast<float *>(smem + L::kOffRow), warp, 2 * kGroupWarps);
+                        reinterpret_cast<float *>(smem + L::kOffRow), warp, 2 * kGroupWarps, p.whole_nodes != 0);
             softmax_sync();
             if (tid == 0) {
                 mbar_arrive(q_full(0));
-                mbar_arrive(q_first);
+                if (!p.whole_nodes) mbar_arrive(q_first);
             }
         }
-        bool alive = true;
         int j0 = 0;  // tiles before the piece
 
         End end{};
@@ -1157,12 +1217,12 @@ cudaError_t tree_prepare_device() {
                                 static_cast<int>(Layout<true>::kBytes));
 }
 
-cudaError_t launch_tree_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, const TreeParams &p, bool fp8,
+cudaError_t launch_tree_attention(const CUtensorMap &kmap, const CUtensorMap &vmap, const CUtensorMap &qmap, const TreeParams &p, bool fp8,
                                   cudaStream_t stream) {
     const cudaError_t e = fp8 ? launch_pdl(tree_attention_kernel<true>, dim3(p.ranges), dim3(Layout<true>::kThreads),
-                                           Layout<true>::kBytes, stream, kmap, vmap, p)
+                                           Layout<true>::kBytes, stream, kmap, vmap, qmap, p)
                               : launch_pdl(tree_attention_kernel<false>, dim3(p.ranges), dim3(Layout<false>::kThreads),
-                                           Layout<false>::kBytes, stream, kmap, vmap, p);
+                                           Layout<false>::kBytes, stream, kmap, vmap, qmap, p);
     if (e != cudaSuccess) return e;
     return launch_pdl(tree_merge_kernel, dim3(p.ranges, (p.part_rows + kMergeRows - 1) / kMergeRows), dim3(kMergeRows * 32), 0,
                       stream, p);
