@@ -15,13 +15,13 @@
 // draws from p_i and follows the draw as long as it is among the children.)
 //
 // The products next to a border (24 bits each) and the few sums of the walk are fp64: exact, or
-// nearly.  The sums over the vocabulary are error-free pairs of fp32 (high part and
-// remainder, 2^-48), joined in fp64: the same token as sums in fp64 but for borders closer than
-// that, without the slow fp64 pipe (two additions a clock and SM: 64 rows of 128000 would take
-// it 14 us).
+// nearly.  The sums over the vocabulary are pairs of fp32 (high part and remainder, right to
+// 2^-46): the same token as sums in fp64 but for borders closer than that, without the slow fp64
+// pipe (two additions a clock and SM: 64 rows of 128000 would take it 14 us, and the search within
+// a segment of 2000 entries 10 us).
 //
 // One cluster of up to 8 CTAs takes a sequence: each warp sums one segment of the vocabulary, the
-// segment sums are exchanged through distributed shared memory, and the one warp whose segment
+// segment sums are exchanged through distributed shared memory, and the CTA whose segment
 // holds the drawn token reads that segment (a few KB, in cache) a second time.  HBM bound for
 // batches (one row of p and one of q a sequence), latency bound for few sequences: three
 // dependent reads (lengths, tokens, probabilities) come before the row.
@@ -51,42 +51,66 @@ __device__ __forceinline__ uint32_t cluster_size() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// A double into another CTA's copy of this CTA's shared-memory address.
-__device__ __forceinline__ void store_remote(uint32_t addr, uint32_t rank, double v) {
+// A pair into another CTA's copy of this CTA's shared-memory address.
+__device__ __forceinline__ void store_remote(uint32_t addr, uint32_t rank, float2 v) {
     uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote), "d"(v) : "memory");
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.x), "f"(v.y) : "memory");
 }
 
 // A probability as it counts: NaN and below 0 as 0, above 1 as 1 (so sums stay finite).
 __device__ __forceinline__ float weigh(float p) { return fminf(fmaxf(p, 0.f), 1.f); }
 
-// hi + lo += x without error in hi (the error of each addition goes to lo).
-__device__ __forceinline__ void add_exact(float &hi, float &lo, float x) {
-    const float sum = __fadd_rn(hi, x);
-    const float part = __fsub_rn(sum, hi);
-    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(sum, part)), __fsub_rn(x, part)));
-    hi = sum;
+// Pairs (x the sum rounded to fp32, y what that leaves) of weights: each sum is right to 2^-46.
+__device__ __forceinline__ float2 renormal(float h, float l) {
+    const float x = __fadd_rn(h, l);
+    return make_float2(x, __fsub_rn(l, __fsub_rn(x, h)));
+}
+__device__ __forceinline__ float2 plus(float2 a, float2 b) {
+    const float sum = __fadd_rn(a.x, b.x), part = __fsub_rn(sum, a.x);
+    const float rest = __fadd_rn(__fsub_rn(a.x, __fsub_rn(sum, part)), __fsub_rn(b.x, part));
+    return renormal(sum, __fadd_rn(rest, __fadd_rn(a.y, b.y)));
+}
+__device__ __forceinline__ float2 pair(double x) {
+    const float h = static_cast<float>(x);
+    return make_float2(h, static_cast<float>(x - static_cast<double>(h)));
+}
+__device__ __forceinline__ bool above(float2 a, float2 b) { return a.x > b.x || (a.x == b.x && a.y > b.y); }
+__device__ __forceinline__ float2 shuffle_up(float2 a, int off) {
+    return make_float2(__shfl_up_sync(0xffffffffu, a.x, off), __shfl_up_sync(0xffffffffu, a.y, off));
+}
+// This lane's value and those of the lanes before, over a power of two of lanes.
+__device__ __forceinline__ float2 scan_lanes(float2 a, int lane, int lanes) {
+#pragma unroll
+    for (int off = 1; off < lanes; off <<= 1) {
+        const float2 y = shuffle_up(a, off), z = plus(a, y);
+        a = make_float2(lane >= off ? z.x : a.x, lane >= off ? z.y : a.y);
+    }
+    return a;
 }
 
-// The weight of entry v in fp64 (exact: a difference of two fp32 numbers of [0, 1] that are
-// not tiny against each other; else its rounding is below 2^-53 of the larger).
-__device__ __forceinline__ double weight64(const float *p, const float *q, int v) {
-    const double w = static_cast<double>(weigh(__ldg(p + v)));
-    if (!q) return w;
-    const double d = w - static_cast<double>(weigh(__ldg(q + v)));
-    return d > 0.0 ? d : 0.0;
+// The weight of entry v (exact: p > q, so p - (p - q rounded) - q has no rounding).
+__device__ __forceinline__ float2 weight(const float *p, const float *q, int v) {
+    const float x = weigh(__ldg(p + v));
+    if (!q) return make_float2(x, 0.f);
+    const float y = weigh(__ldg(q + v));
+    if (!(x > y)) return make_float2(0.f, 0.f);
+    const float d = __fsub_rn(x, y);
+    return make_float2(d, __fsub_rn(__fsub_rn(x, d), y));
 }
 
 struct VerifyShared {
-    double sums[kSegments];  // of every segment of the cluster
-    double p[kMaxTreeNodes], q[kMaxTreeNodes];
+    float2 sums[kSegments];  // of every segment of the cluster
+    double p[kMaxTreeNodes];
     float u[kMaxTreeNodes];
+    bool accepted[kMaxTreeNodes];  // with the drafter's probabilities: u q < p
     int32_t token[kMaxTreeNodes], parent[kMaxTreeNodes];
     int32_t path[kMaxTreeNodes];
     int32_t refused[kMaxTreeNodes];  // tokens that have no weight left
     int32_t count, refusals, found;
-    double goal;  // what the draw leaves to the segment: u_0 sum w less the weights before it
+    double goal, below;  // of the draw: u_0 sum w, and the weights before the segment
+    float2 warp_sums[kVerifyWarps];
+    int32_t passes[kVerifyWarps], some[kVerifyWarps];  // entries: the first that passes the goal, the last with weight
 };
 
 __global__ void __launch_bounds__(kVerifyThreads) speculative_verify_kernel(const SpecVerifyParams p) {
@@ -115,14 +139,28 @@ __global__ void __launch_bounds__(kVerifyThreads) speculative_verify_kernel(cons
         sh.token[j] = token;
         sh.parent[j] = j > 0 && up >= 0 && up < j ? up : -1;
         const int64_t at = static_cast<int64_t>(row0) + (ok ? up : 0);
-        sh.p[j] = ok ? static_cast<double>(weigh(__ldg(p.target + at * p.target_row + token))) : 0.0;
-        sh.q[j] = ok && p.draft ? static_cast<double>(weigh(__ldg(p.draft + at * p.draft_row + token))) : 0.0;
+        const double pj = ok ? static_cast<double>(weigh(__ldg(p.target + at * p.target_row + token))) : 0.0;
+        sh.p[j] = pj;
+        if (p.draft) {
+            const double qj = ok ? static_cast<double>(weigh(__ldg(p.draft + at * p.draft_row + token))) : 0.0;
+            sh.accepted[j] = static_cast<double>(sh.u[j]) * qj < pj;
+        }
     }
     cluster_wait();
     __syncthreads();
 
     // ---- the walk: warp 0, every lane alike ----
-    if (warp == 0) {
+    if (warp == 0 && p.draft) {  // a chain up to its first refusal
+        const uint64_t refused = ~((static_cast<uint64_t>(__ballot_sync(0xffffffffu, lane < n && (lane == 0 || sh.accepted[lane]))) |
+                                    static_cast<uint64_t>(__ballot_sync(0xffffffffu, lane + 32 < n && sh.accepted[lane + 32])) << 32));
+        const int count = refused ? __ffsll(static_cast<long long>(refused)) - 1 : 64;
+        if (lane < count) sh.path[lane] = lane;
+        if (lane + 32 < count) sh.path[lane + 32] = lane + 32;
+        if (lane == 0) {
+            sh.count = count;
+            sh.refusals = count < n ? 1 : 0;
+        }
+    } else if (warp == 0) {
         int cur = 0, count = n > 0 ? 1 : 0, refusals = 0;
         if (lane == 0) sh.path[0] = 0;
         // nodes lane and lane + 32
@@ -138,12 +176,11 @@ __global__ void __launch_bounds__(kVerifyThreads) speculative_verify_kernel(cons
                 children &= children - 1;
                 const int32_t token = sh.token[j];
                 double pj = sh.p[j];
-                if (!p.draft) {  // a token refused before has no probability left
-                    const bool gone = (lane < refusals && sh.refused[lane] == token) ||
-                                      (lane + 32 < refusals && sh.refused[lane + 32] == token);
-                    if (__any_sync(0xffffffffu, gone)) pj = 0.0;
-                }
-                if (static_cast<double>(sh.u[j]) * (p.draft ? sh.q[j] : rest) < pj) {
+                // a token refused before has no probability left
+                const bool gone = (lane < refusals && sh.refused[lane] == token) ||
+                                  (lane + 32 < refusals && sh.refused[lane + 32] == token);
+                if (__any_sync(0xffffffffu, gone)) pj = 0.0;
+                if (static_cast<double>(sh.u[j]) * rest < pj) {
                     next = j;
                     break;
                 }
@@ -185,71 +222,85 @@ __global__ void __launch_bounds__(kVerifyThreads) speculative_verify_kernel(cons
     // (64 bits: the last segments may lie wholly behind the vocabulary)
     const int lo = static_cast<int>(min(static_cast<int64_t>(seg) * p.segment, static_cast<int64_t>(p.vocab)));
     const int hi = static_cast<int>(min(static_cast<int64_t>(seg + 1) * p.segment, static_cast<int64_t>(p.vocab)));
-    auto is_refused = [&](int v) {
-        bool gone = false;
-        for (int i = 0; i < refusals; ++i) gone = gone || sh.refused[i] == v;
+    auto refused_from = [&](int v) {  // bit i: v + i, i < 4
+        uint32_t gone = 0;
+        for (int i = 0; i < refusals; ++i) {
+            const uint32_t at = static_cast<uint32_t>(sh.refused[i]) - static_cast<uint32_t>(v);
+            if (at < 4) gone |= 1u << at;
+        }
         return gone;
     };
 
     for (int attempt = 0; attempt < 2 && count > 0; ++attempt) {
         // ---- the segment's sum ----
-        float h0 = 0.f, l0 = 0.f, h1 = 0.f, l1 = 0.f;
+        float2 h = make_float2(0.f, 0.f), l = make_float2(0.f, 0.f);  // two sums, of even and odd entries
         bool here = false;  // a refused token lies in this segment
         for (int i = lane; i < refusals; i += 32) here = here || (sh.refused[i] >= lo && sh.refused[i] < hi);
         here = __any_sync(0xffffffffu, here);
-        auto add = [&](float pv, float qv, float &h, float &l) {
-            pv = weigh(pv);
-            qv = weigh(qv);
-            if (pv > qv) {
-                add_exact(h, l, pv);
-                if (draft) add_exact(h, l, -qv);
-            }
+        // h + l += max(x - y, 0), with what each rounding loses going to l
+        auto add = [&](float2 x, float2 y) {
+            const float2 minus = make_float2(-1.f, -1.f);
+            y = make_float2(weigh(y.x), weigh(y.y));
+            x = make_float2(fmaxf(weigh(x.x), y.x), fmaxf(weigh(x.y), y.y));
+            const float2 d = ffma2(y, minus, x), e = ffma2(y, minus, ffma2(d, minus, x));
+            const float2 sum = fadd2(h, d), part = ffma2(h, minus, sum);
+            const float2 rest = fadd2(ffma2(ffma2(part, minus, sum), minus, h), ffma2(part, minus, d));
+            l = fadd2(l, fadd2(rest, e));
+            h = sum;
         };
-        const bool wide = ((reinterpret_cast<uintptr_t>(target) | (draft ? reinterpret_cast<uintptr_t>(draft) : 0)) & 15) == 0;
-        if (!here && wide) {  // (lo is a multiple of 4)
-            const int full = lo + ((hi - lo) & ~3);
-#pragma unroll 4
-            for (int v = lo + 4 * lane; v < full; v += 128) {
-                const float4 x = __ldg(reinterpret_cast<const float4 *>(target + v));
+        auto one = [&](int v) {
+            const float x = __ldg(target + v), y = draft ? __ldg(draft + v) : 0.f;
+            if (!here || !(refused_from(v) & 1)) add(make_float2(x, 0.f), make_float2(y, 0.f));
+        };
+        // Four entries a load where both rows begin alike against 16 bytes (lo is a multiple of 4), from the first boundary on.
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(target) >> 2) & 3;
+        const bool wide = !draft || (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(draft) >> 2) & 3) == off;
+        if (wide) {
+            const int head = min(lo + static_cast<int>((4 - off) & 3), hi), full = head + ((hi - head) & ~3);
+#pragma unroll 2
+            for (int v = head + 4 * lane; v < full; v += 128) {
+                float4 x = __ldg(reinterpret_cast<const float4 *>(target + v));
                 const float4 y = draft ? __ldg(reinterpret_cast<const float4 *>(draft + v)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                add(x.x, y.x, h0, l0);
-                add(x.y, y.y, h1, l1);
-                add(x.z, y.z, h0, l0);
-                add(x.w, y.w, h1, l1);
+                if (here) {
+                    const uint32_t gone = refused_from(v);
+                    if (gone & 1) x.x = 0.f;
+                    if (gone & 2) x.y = 0.f;
+                    if (gone & 4) x.z = 0.f;
+                    if (gone & 8) x.w = 0.f;
+                }
+                add(make_float2(x.x, x.y), make_float2(y.x, y.y));
+                add(make_float2(x.z, x.w), make_float2(y.z, y.w));
             }
-            const int v = full + lane;
-            if (v < hi) add(__ldg(target + v), draft ? __ldg(draft + v) : 0.f, h0, l0);
+            if (lo + lane < head) one(lo + lane);
+            if (full + lane < hi) one(full + lane);
         } else {
-#pragma unroll 4
-            for (int v = lo + lane; v < hi; v += 32) {
-                const float x = __ldg(target + v), y = draft ? __ldg(draft + v) : 0.f;
-                if (!here || !is_refused(v)) add(x, y, h0, l0);
-            }
+#pragma unroll 2
+            for (int v = lo + lane; v < hi; v += 32) one(v);
         }
-        double sum = (static_cast<double>(h0) + static_cast<double>(h1)) + (static_cast<double>(l0) + static_cast<double>(l1));
+        float2 sum = plus(renormal(h.x, l.x), renormal(h.y, l.y));
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        for (int off = 16; off > 0; off >>= 1)
+            sum = plus(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, off), __shfl_xor_sync(0xffffffffu, sum.y, off)));
         if (lane < static_cast<int>(ctas)) store_remote(smem_u32(&sh.sums[seg]), lane, sum);
         cluster_arrive();
         cluster_wait();
 
         // ---- the segment that the draw falls into (warp 0 of every CTA, alike) ----
         if (warp == 0) {
-            double x[4], total = 0.0;
+            // (in fp64: one warp's few additions, each one instruction)
+            double x[4], upto = 0.0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int s = 4 * lane + i;
-                x[i] = s < segments ? sh.sums[s] : 0.0;
-                total += x[i];
+                const float2 y = 4 * lane + i < segments ? sh.sums[4 * lane + i] : make_float2(0.f, 0.f);
+                x[i] = static_cast<double>(y.x) + static_cast<double>(y.y);
+                upto += x[i];
             }
-            double upto = total;  // of this lane's segments and those before
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
+            for (int off = 1; off < 32; off <<= 1) {  // of this lane's segments and those before
                 const double y = __shfl_up_sync(0xffffffffu, upto, off);
                 if (lane >= off) upto += y;
             }
-            total = __shfl_sync(0xffffffffu, upto, 31);
-            const double goal = static_cast<double>(sh.u[0]) * total;
+            const double goal = static_cast<double>(sh.u[0]) * __shfl_sync(0xffffffffu, upto, 31);
             double before = __shfl_up_sync(0xffffffffu, upto, 1);
             if (lane == 0) before = 0.0;
             // the first segment whose sum passes the goal, and (where a rounding leaves none) the last with weight
@@ -257,23 +308,24 @@ __global__ void __launch_bounds__(kVerifyThreads) speculative_verify_kernel(cons
             double first_below = 0.0, last_below = 0.0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int s = 4 * lane + i;
+                const double with = before + x[i];
                 if (x[i] > 0.0) {
-                    last = s;
+                    last = 4 * lane + i;
                     last_below = before;
+                    if (first == 1 << 20 && with > goal) {
+                        first = 4 * lane + i;
+                        first_below = before;
+                    }
                 }
-                if (first == 1 << 20 && x[i] > 0.0 && before + x[i] > goal) {
-                    first = s;
-                    first_below = before;
-                }
-                before += x[i];
+                before = with;
             }
             const int least = __reduce_min_sync(0xffffffffu, first);
             const int most = __reduce_max_sync(0xffffffffu, last);
             const int found = least < 1 << 20 ? least : most;
             if (found < 0 ? lane == 0 : found / 4 == lane) {
                 sh.found = found;
-                sh.goal = goal - (least < 1 << 20 ? first_below : last_below);
+                sh.goal = goal;
+                sh.below = least < 1 << 20 ? first_below : last_below;
             }
         }
         __syncthreads();
@@ -291,50 +343,61 @@ __global__ void __launch_bounds__(kVerifyThreads) speculative_verify_kernel(cons
         if (rank == 0 && tid == 0) p.tokens_out[o] = -1;
         return;
     }
-    if (sh.found != seg) return;
+    if (sh.found / kVerifyWarps != static_cast<int>(rank)) return;
 
-    // ---- the token within the segment, by this warp ----
-    const double goal = sh.goal;
-    auto entry = [&](int v) { return v < hi && !(refusals > 0 && is_refused(v)) ? weight64(target, draft, v) : 0.0; };
-    // Lane l's share is the l-th run of `run` entries; the run that passes the goal is then spread over the lanes.
-    const int run = (p.segment / 32 + 3) / 4 * 4;
-    const int mine = lo + lane * run;
-    double s0 = 0.0, s1 = 0.0;
-    for (int v = mine; v < mine + run; v += 2) {
-        s0 += entry(v);
-        s1 += entry(v + 1);
-    }
-    const double share = s0 + s1;
-    double scan = share;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, scan, off);
-        if (lane >= off) scan += y;
-    }
-    const uint32_t some = __ballot_sync(0xffffffffu, share > 0.0);
-    const uint32_t pass = __ballot_sync(0xffffffffu, share > 0.0 && scan > goal);
-    const int who = pass ? __ffs(pass) - 1 : some ? 31 - __clz(some) : 0;
-    double below = __shfl_sync(0xffffffffu, scan - share, who);
+    // ---- the token within the segment, by its CTA: four entries a thread, 2048 at a time ----
+    const float2 goal = pair(sh.goal);
+    const int from = static_cast<int>(min(static_cast<int64_t>(sh.found) * p.segment, static_cast<int64_t>(p.vocab)));
+    const int to = static_cast<int>(min(static_cast<int64_t>(sh.found + 1) * p.segment, static_cast<int64_t>(p.vocab)));
+    float2 below = pair(sh.below);
     int token = -1;
-    for (int v0 = lo + who * run; v0 < lo + (who + 1) * run; v0 += 32) {
-        const int v = v0 + lane;
-        const double w = v < lo + (who + 1) * run ? entry(v) : 0.0;
-        double at = w;
+    for (int v0 = from; v0 < to; v0 += 4 * kVerifyThreads) {
+        const int v = v0 + 4 * tid;
+        const uint32_t gone = refused_from(v);
+        float2 w[4];
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, at, off);
-            if (lane >= off) at += y;
+        for (int i = 0; i < 4; ++i)
+            w[i] = v + i < to && !((gone >> i) & 1) ? weight(target, draft, v + i) : make_float2(0.f, 0.f);
+        const float2 scan = scan_lanes(plus(plus(w[0], w[1]), plus(w[2], w[3])), lane, 32);
+        if (lane == 31) sh.warp_sums[warp] = scan;
+        __syncthreads();
+        const float2 warps_upto = scan_lanes(sh.warp_sums[lane & (kVerifyWarps - 1)], lane & (kVerifyWarps - 1), kVerifyWarps);
+        auto warps = [&](int i) {
+            return make_float2(__shfl_sync(0xffffffffu, warps_upto.x, i), __shfl_sync(0xffffffffu, warps_upto.y, i));
+        };
+        const float2 before_warp = warps(max(warp - 1, 0)), before_lane = shuffle_up(scan, 1);
+        float2 at = below;
+        if (warp > 0) at = plus(at, before_warp);
+        if (lane > 0) at = plus(at, before_lane);
+        below = plus(below, warps(kVerifyWarps - 1));
+        int pass = -1, some = -1;  // of this thread's entries
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            at = plus(at, w[i]);
+            if (w[i].x > 0.f) {
+                some = v + i;
+                if (pass < 0 && above(at, goal)) pass = v + i;
+            }
         }
-        const uint32_t has = __ballot_sync(0xffffffffu, w > 0.0);
-        const uint32_t hit = __ballot_sync(0xffffffffu, w > 0.0 && below + at > goal);
-        if (hit) {
-            token = v0 + __ffs(hit) - 1;
-            break;
+        const uint32_t passes = __ballot_sync(0xffffffffu, pass >= 0), with = __ballot_sync(0xffffffffu, some >= 0);
+        const int first = __shfl_sync(0xffffffffu, pass, passes ? __ffs(passes) - 1 : 0);
+        const int last = __shfl_sync(0xffffffffu, some, with ? 31 - __clz(with) : 0);
+        if (lane == 0) {
+            sh.passes[warp] = passes ? first : -1;
+            sh.some[warp] = with ? last : -1;
         }
-        if (has) token = v0 + 31 - __clz(has);  // (the last with weight, should a rounding leave none)
-        below += __shfl_sync(0xffffffffu, at, 31);
+        __syncthreads();
+        // the first entry that passes, or (should a rounding leave none) the last with weight
+        const int pass_w = sh.passes[lane & (kVerifyWarps - 1)], some_w = sh.some[lane & (kVerifyWarps - 1)];
+        const uint32_t hit = __ballot_sync(0xffffffffu, lane < kVerifyWarps && pass_w >= 0);
+        const uint32_t any = __ballot_sync(0xffffffffu, lane < kVerifyWarps && some_w >= 0);
+        if (hit)
+            token = __shfl_sync(0xffffffffu, pass_w, __ffs(hit) - 1);
+        else if (any)
+            token = __shfl_sync(0xffffffffu, some_w, 31 - __clz(any));
+        if (hit) break;
     }
-    if (lane == 0) p.tokens_out[o] = token;
+    if (tid == 0) p.tokens_out[o] = token;
 }
 
 // ---- compaction ----------------------------------------------------------------------

@@ -363,7 +363,8 @@ int speculative_verify(int32_t *tokens_out, int32_t *path, int32_t *counts, cons
         !aligned(target_probs, 4) || !aligned(draft_probs, 4) || !aligned(tokens, 4) || !aligned(parents, 4) ||
         !aligned(uniforms, 4) || !aligned(status, 4))
         return PKV_ERR_INVALID_ARG;
-    if (current_sms() < 1) return PKV_ERR_CUDA;
+    const int sms = current_sms();
+    if (sms < 1) return PKV_ERR_CUDA;
     pkv::SpecVerifyParams p{};
     p.tokens_out = tokens_out;
     p.path = path;
@@ -381,9 +382,12 @@ int speculative_verify(int32_t *tokens_out, int32_t *path, int32_t *counts, cons
     p.max_q_len = max_q_len;
     p.total_rows = total_q_rows;
     p.vocab = vocab_size;
-    // CTAs a sequence: one for every 4096 entries, up to a portable cluster of 8.
+    // CTAs a sequence: one for every 4096 entries, up to a portable cluster of 8, as long as all run at once, two an
+    // SM (64 rows of 128000 with the drafter's take 25 us in 4 CTAs each, 33 in 8; 256 of 32000 take 27 in 2, 68 in 8).
     int cluster = 1;
-    while (cluster < pkv::kVerifyMaxCluster && static_cast<int64_t>(cluster) * 4096 < vocab_size) cluster *= 2;
+    while (cluster < pkv::kVerifyMaxCluster && static_cast<int64_t>(cluster) * 4096 < vocab_size &&
+           static_cast<int64_t>(cluster) * num_seqs <= sms)
+        cluster *= 2;
     const int32_t warps = cluster * pkv::kVerifyWarps;
     p.segment = (vocab_size + warps * 128 - 1) / (warps * 128) * 128;
     return finish(pkv::launch_speculative_verify(p, cluster, static_cast<cudaStream_t>(stream)));
