@@ -52,7 +52,8 @@ struct TreeParams {
     int32_t out_bf16;
     // The split: all (sequence, KV head, 128-row tile) units' key tiles in `ranges` equal ranges, one a CTA.
     int32_t ranges, part_rows;  // part_rows: rows of a partial (the most a row tile holds)
-    int4 *record;               // [ranges]: the split unit that begins in the range (sequence, unit, parts; 0 parts: none)
+    int4 *record;               // [ranges]: the split unit that begins in the range (first row of q, KV head, parts (0: none),
+                                // row tile x 256 + its rows)
     float2 *part_ml;            // [ranges][2][part_rows] (m, l), log2 domain, scale folded in
     float *part_o;              // the same x [128], unnormalised
 };

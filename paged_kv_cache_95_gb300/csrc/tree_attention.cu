@@ -780,7 +780,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
             if (w.t0 > 0 || w.left != w.t1 - w.t0 || w.t1 == w.s.tiles) return;
             const int64_t end = plan.begin + plan.count - w.t1 + w.s.tiles;  // behind the unit's last tile
             const int64_t cta = (end * plan.ranges + plan.total - 1) / plan.total - 1;
-            rec = make_int4(w.b, w.g * w.s.row_tiles + w.row_tile, static_cast<int>(cta) - static_cast<int>(blockIdx.x) + 1, 0);
+            rec = make_int4(w.s.row0, w.g, static_cast<int>(cta) - static_cast<int>(blockIdx.x) + 1, w.row_tile * 256 + w.rows(p));
         };
         int j = 0, sent = 0;
         bool ok = true;
@@ -1173,32 +1173,38 @@ __global__ void __launch_bounds__(kMergeRows * 32) tree_merge_kernel(const TreeP
     const int c = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
     const int4 rec = p.record[c];
     const int parts = rec.z;
-    if (parts < 2) return;
-    const Sequence s = load_sequence(p, rec.x);
-    const int g = rec.y / s.row_tiles, first_row = rec.y % s.row_tiles * kRows;
-    if (r >= min(kRows, s.n * p.group - first_row)) return;
+    if (parts < 2 || r >= (rec.w & 255)) return;
     auto part = [&](int i) -> int64_t { return (static_cast<int64_t>(c + i) * 2 + (i == 0 ? 1 : 0)) * p.part_rows + r; };
-    float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(p.part_ml + part(i)).x);
+    // Lane k holds (m, l) of the parts k, 32 + k, ..; the first 32 are read once.
+    const float2 none = make_float2(-INFINITY, 0.f), x0 = lane < parts ? __ldcg(p.part_ml + part(lane)) : none;
+    float top = x0.x;
+    for (int i = lane + 32; i < parts; i += 32) top = fmaxf(top, __ldcg(p.part_ml + part(i)).x);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
     const float mu = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-        const float2 x = __ldcg(p.part_ml + part(i));
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + part(i) * kHeadDim) + lane);
-        const float f = fast_exp2(x.x - mu);
-        sum = fmaf(f, x.y, sum);
-        o.x = fmaf(f, v.x, o.x);
-        o.y = fmaf(f, v.y, o.y);
-        o.z = fmaf(f, v.z, o.z);
-        o.w = fmaf(f, v.w, o.w);
+#pragma unroll 1
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        const float2 x = i0 == 0 ? x0 : i0 + lane < parts ? __ldcg(p.part_ml + part(i0 + lane)) : none;
+        const float mine = fast_exp2(x.x - mu);
+        sum = fmaf(mine, x.y, sum);
+        const int here = min(32, parts - i0);
+#pragma unroll 8
+        for (int i = 0; i < here; ++i) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + part(i0 + i) * kHeadDim) + lane);
+            const float f = __shfl_sync(0xffffffffu, mine, i);
+            o.x = fmaf(f, v.x, o.x);
+            o.y = fmaf(f, v.y, o.y);
+            o.z = fmaf(f, v.z, o.z);
+            o.w = fmaf(f, v.w, o.w);
+        }
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t head = (static_cast<int64_t>(s.row0) + (first_row + r) / p.group) * p.n_q + static_cast<int64_t>(g) * p.group +
-                         (first_row + r) % p.group;
+    const int at = (rec.w >> 8) * kRows + r, node = by_group(at, p.group_magic);
+    const int64_t head = (static_cast<int64_t>(rec.x) + node) * p.n_q + static_cast<int64_t>(rec.y) * p.group + (at - node * p.group);
     if (p.out_bf16)
         reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + head * kHeadDim)[lane] =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
