@@ -317,7 +317,9 @@ __device__ __noinline__ Plan make_plan(const TreeParams &p, int lane, Lengths *k
     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
     if (wrong && blockIdx.x == 0 && p.status) atomicOr(p.status, wrong);
     plan.total = total;
-    plan.ranges = static_cast<int>(min(static_cast<int64_t>(p.ranges), total));
+    // (no range of one tile while there are more: a second tile costs 0.7 us, the joining of twice the parts more; one
+    // sequence of 128 tokens and 8 KV heads takes 10.3 us for 12.0, of 1000 tokens 13.9 for 15.0, 4 tiles a range 14.1 and 15.0)
+    plan.ranges = static_cast<int>(min(static_cast<int64_t>(p.ranges), (total + 1) / 2));
     if (static_cast<int>(blockIdx.x) >= plan.ranges) return plan;
     plan.begin = divide(total * blockIdx.x, plan.ranges);
     plan.count = static_cast<int>(divide(total * (blockIdx.x + 1), plan.ranges) - plan.begin);
