@@ -355,3 +355,19 @@ def test_binding_refusals():
     for bad in (dict(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")), dict(scale=float("nan"))):
         with pytest.raises(P.PagedKVError):
             P.paged_attention_tree(**{**good, **bad})
+
+
+@pytest.mark.parametrize("fp8", POOLS)
+@pytest.mark.parametrize("heads,kv", [(6, 2), (8, 2), (7, 1)])
+def test_empty_sequences_at_every_place(heads, kv, fp8):
+    """Ranges that begin anywhere among 100 sequences, most of them empty, and go on past the 32nd and the 64th."""
+    rng = random.Random(heads)
+    nodes = [0 if rng.random() < 0.6 or 28 < b < 36 or b in (0, 63, 64, 99) else rng.choice([1, 2, 9, 33]) for b in range(100)]
+    Problem(nodes, [max(1, n + rng.choice([0, 1, 60, 150])) for n in nodes], heads, kv, fp8, seed=heads).check()
+
+
+@pytest.mark.parametrize("fp8", POOLS)
+@pytest.mark.parametrize("heads,nodes", [(128, 3), (256, 2), (130, 3), (64, 5), (96, 2), (1, 64), (2, 64)])
+def test_rows_of_a_tile(heads, nodes, fp8):
+    """One KV head: tiles of whole nodes, of parts of a node, and of rows of several nodes' parts."""
+    Problem([nodes, 1], [nodes + 70, 5], heads, 1, fp8, seed=heads).check()
