@@ -202,9 +202,12 @@ __device__ __forceinline__ float2 minus_bf16x2(float2 p, uint32_t h) {
     return d;
 }
 
-// x / group for a row x of a tree (magic: 2^32 / group rounded up; exact for 64 nodes of up to 1024 heads).
-__device__ __forceinline__ int by_group(int x, uint32_t magic) {
-    return magic == 0 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), magic));  // (0: a group of 1)
+// x / group for a row x of a sequence (magic: 2^32 / group rounded up: exact for 64 nodes of up to 1024 heads, one too many at
+// times for the rows of a sequence whose length is refused).
+__device__ __forceinline__ int by_group(int x, int group, uint32_t magic) {
+    if (magic == 0) return x;  // (a group of 1)
+    const int q = static_cast<int>(__umulhi(static_cast<uint32_t>(x), magic));
+    return q * group > x ? q - 1 : q;
 }
 
 // A sequence as the split sees it (device data: checked).  units is 0 for one without rows, or whose
@@ -394,7 +397,7 @@ __device__ __noinline__ void load_q(const TreeParams &p, int row0, int first, in
     for (int r0 = there ? rows : 8 * part; r0 < rows; r0 += 8 * parts) {
 #pragma unroll 1
         for (int i = 0; i < 8; i += 2) {  // (16 lanes a row; rows past the last are read as the last)
-            const int r = r0 + i + (lane >> 4), at = first + min(r, rows - 1), node = by_group(at, magic);
+            const int r = r0 + i + (lane >> 4), at = first + min(r, rows - 1), node = by_group(at, G, magic);
             cp_async_16(place(r, lane & 15), base + (static_cast<int64_t>(node) * p.n_q + (at - node * G)) * kHeadDim);
         }
     }
@@ -937,12 +940,13 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
             const int rows = w.rows(p), first_row = w.row_tile * kRows, g = w.g;
             const bool busy = quarter * 32 < rows;  // (warp-uniform: a warp without rows only keeps step)
             const int prefix = w.s.ctx - w.s.n;
-            const int node = by_group(first_row + r, p.group_magic);
+            const int node = by_group(first_row + r, G, p.group_magic);
             const int64_t row = static_cast<int64_t>(w.s.row0) + node;
             uint64_t mask = 0;
             if (r < rows && w.s.ctx > 0) {
                 mask = __ldg(reinterpret_cast<const unsigned long long *>(p.mask) + row);  // (not looked at before the tree's tiles)
             }
+            __syncwarp();  // (the loads from tensor memory want the whole warp)
             float sl2 = p.scale_log2;
             float m = -INFINITY, l = 0.f;
             const int t_first = w.t0 + ((j0 ^ a) & 1);
@@ -1205,7 +1209,7 @@ __global__ void __launch_bounds__(kMergeRows * 32) tree_merge_kernel(const TreeP
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int at = (rec.w >> 8) * kRows + r, node = by_group(at, p.group_magic);
+    const int at = (rec.w >> 8) * kRows + r, node = by_group(at, p.group, p.group_magic);
     const int64_t head = (static_cast<int64_t>(rec.x) + node) * p.n_q + static_cast<int64_t>(rec.y) * p.group + (at - node * p.group);
     if (p.out_bf16)
         reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + head * kHeadDim)[lane] =

@@ -371,3 +371,20 @@ def test_empty_sequences_at_every_place(heads, kv, fp8):
 def test_rows_of_a_tile(heads, nodes, fp8):
     """One KV head: tiles of whole nodes, of parts of a node, and of rows of several nodes' parts."""
     Problem([nodes, 1], [nodes + 70, 5], heads, 1, fp8, seed=heads).check()
+
+
+@pytest.mark.parametrize("heads,n", [(1022, 16500), (1002, 17400)])  # (501 heads: from row 17354 on)
+def test_a_refused_length_of_many_rows(heads, n):
+    """A sequence longer than max_q_len (zeros, and a status bit) whose row numbers pass 2^32 / heads-of-a-group squared."""
+    kv = 2
+    p = Problem([1], [20], heads, kv, seed=3)
+    q = torch.cat([p.q, torch.ones(n, heads, 128, dtype=torch.bfloat16, device="cuda")])
+    out = torch.full((n + 3, heads, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    q = torch.cat([q, q[:2]])
+    masks = torch.ones(n + 3, dtype=torch.int64, device="cuda")
+    tables, ctx = i32(p.tables * 2), i32([20, 40])
+    ws = P.paged_attention_tree(out, q, masks, i32([0, 1, n + 1]), 4, p.k, p.v, tables, ctx, p.scale)
+    assert status_of(ws) == P.PKV_STATUS_BAD_Q_LEN | P.PKV_STATUS_BAD_CONTEXT_LEN  # (40 tokens are more than 2 blocks hold)
+    want = p.want()
+    assert bool(((out[:1].double().cpu() - want).abs() <= p.bound(want, torch.bfloat16)).all())
+    assert not bool(out[1:n + 1].any()) and bool((out[n + 1:] == 7).all())
