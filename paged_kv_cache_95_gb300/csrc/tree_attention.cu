@@ -953,8 +953,14 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
 #pragma unroll 1
             for (int t = t_first; t < w.t1; t += 2) {
                 const int j = j0 + t - w.t0;
-                if constexpr (FP8) alive = alive && softmax_wait(scale_full(j % L::kStagesScale), (j / L::kStagesScale) & 1, abort_flag);
-                alive = alive && softmax_wait(s_full(j), phase(j), abort_flag);
+                if constexpr (FP8) {
+                    // (both barriers by one vote while both are complete: the hand-offs are on a tile's way, 197 us for 180)
+                    const uint32_t scale_bar = scale_full(j % L::kStagesScale), scale_phase = (j / L::kStagesScale) & 1;
+                    if (!__any_sync(0xffffffffu, mbar_test_wait(s_full(j), phase(j)) & mbar_test_wait(scale_bar, scale_phase)))
+                        alive = alive && softmax_wait(scale_bar, scale_phase, abort_flag) && softmax_wait(s_full(j), phase(j), abort_flag);
+                } else {
+                    alive = alive && softmax_wait(s_full(j), phase(j), abort_flag);
+                }
                 if (!alive) continue;
                 tc_fence_after();
                 const uint32_t t_s = lane_base + kKeys * (j % kPlaces);
@@ -1004,8 +1010,8 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                             __syncwarp();
                         }
                     }
-                    // The row's largest score in the log2 domain.  (FP8: 32 keys at a time, scaled by each key's K scale and put
-                    // back; the row's factor comes behind.  All 64 at once leave no registers for the scales: spilled
+                    // The row's largest score in the log2 domain.  (FP8: 32 keys at a time, scaled by each key's K scale, the first
+                    // 32 put back; the row's factor comes behind.  All 64 at once leave no registers for the scales: spilled
                     // ones come back through the L1 that 200 KB of shared memory leave, 403 us for 211.)
                     constexpr int kPass = FP8 ? 32 : kKeys;
                     uint32_t v[kPass];
@@ -1035,7 +1041,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                                 v[4 * i + 3] = __float_as_uint(y.y);
                             }
                         }
-                        if constexpr (FP8) tmem_st_32x32b_x32(t_s + kPass * c, v);
+                        if (FP8 && c == 0) tmem_st_32x32b_x32(t_s, reinterpret_cast<uint32_t (&)[32]>(v));
                     }
                     float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if constexpr (FP8) {
@@ -1073,8 +1079,8 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     float2 rs0 = make_float2(0.f, 0.f), rs1 = make_float2(0.f, 0.f);
                     const float2 slope = FP8 ? make_float2(sl2, sl2) : sl2v;
 #pragma unroll 1
-                    for (int c = 0; c < kKeys / kPass; ++c) {
-                        if constexpr (FP8) tmem_ld_32x32b_x32(t_s + kPass * c, v);
+                    for (int c = kKeys / kPass - 1; c >= 0; --c) {
+                        if (FP8 && c == 0) tmem_ld_32x32b_x32(t_s, reinterpret_cast<uint32_t (&)[32]>(v));
 #pragma unroll
                         for (int h = 0; h < kPass / 16; ++h) {  // 16 keys: 8 columns of heads, 8 of remainders
                             uint32_t pk[FP8 ? 8 : 16];
