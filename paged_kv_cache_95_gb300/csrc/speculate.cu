@@ -113,7 +113,7 @@ struct VerifyShared {
     int32_t passes[kVerifyWarps], some[kVerifyWarps];  // entries: the first that passes the goal, the last with weight
 };
 
-__global__ void __launch_bounds__(kVerifyThreads) speculative_verify_kernel(const SpecVerifyParams p) {
+__global__ void __launch_bounds__(kVerifyThreads, 2) speculative_verify_kernel(const SpecVerifyParams p) {
     __shared__ VerifyShared sh;
     const uint32_t rank = cluster_rank(), ctas = cluster_size();
     const int b = blockIdx.x / ctas;
@@ -257,19 +257,35 @@ __global__ void __launch_bounds__(kVerifyThreads) speculative_verify_kernel(cons
         const bool wide = !draft || (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(draft) >> 2) & 3) == off;
         if (wide) {
             const int head = min(lo + static_cast<int>((4 - off) & 3), hi), full = head + ((hi - head) & ~3);
-#pragma unroll 2
-            for (int v = head + 4 * lane; v < full; v += 128) {
-                float4 x = __ldg(reinterpret_cast<const float4 *>(target + v));
-                const float4 y = draft ? __ldg(reinterpret_cast<const float4 *>(draft + v)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                if (here) {
-                    const uint32_t gone = refused_from(v);
-                    if (gone & 1) x.x = 0.f;
-                    if (gone & 2) x.y = 0.f;
-                    if (gone & 4) x.z = 0.f;
-                    if (gone & 8) x.w = 0.f;
+            // Two loads ahead of the sums (loads of one turn, then its sums: 64 x 128000 with drafts 22.4 us for 20.2; three or four
+            // ahead gain 2 us where a warp takes 8000 entries and lose 2 where it takes 400).
+            constexpr int kAhead = 2;
+            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 x[kAhead], y[kAhead];
+            auto load = [&](int i, int v) {
+                x[i] = v < full ? __ldg(reinterpret_cast<const float4 *>(target + v)) : zero;
+                y[i] = v < full && draft ? __ldg(reinterpret_cast<const float4 *>(draft + v)) : zero;
+            };
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) load(i, head + 4 * lane + 128 * i);
+#pragma unroll 1
+            for (int v0 = head + 4 * lane; v0 < full; v0 += 128 * kAhead) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int v = v0 + 128 * i;
+                    float4 now = x[i];
+                    const float4 less = y[i];
+                    load(i, v + 128 * kAhead);
+                    if (here) {
+                        const uint32_t gone = refused_from(v);
+                        if (gone & 1) now.x = 0.f;
+                        if (gone & 2) now.y = 0.f;
+                        if (gone & 4) now.z = 0.f;
+                        if (gone & 8) now.w = 0.f;
+                    }
+                    add(make_float2(now.x, now.y), make_float2(less.x, less.y));
+                    add(make_float2(now.z, now.w), make_float2(less.z, less.w));
                 }
-                add(make_float2(x.x, x.y), make_float2(y.x, y.y));
-                add(make_float2(x.z, x.w), make_float2(y.z, y.w));
             }
             if (lo + lane < head) one(lo + lane);
             if (full + lane < hi) one(full + lane);
