@@ -912,10 +912,15 @@ PKV_API int rotary_reshape_and_cache_fp8(void *q_out, const void *q, int64_t q_r
  *   max_q_len  : host upper bound of the nodes a sequence, 1 .. PKV_MAX_TREE_NODES
  *   k_cache, v_cache, k_scale, v_scale : a bf16 pool (scales NULL) or an FP8 (E4M3) pool, as cache->dtype
  *                says; attention is over code * scale
- *   num_q_heads: any multiple of cache->num_kv_heads (to 1024)
+ *   num_q_heads: any multiple of cache->num_kv_heads (to 1024); Q is read fastest where the heads of a KV
+ *                head divide 128
  *   workspace  : 256-byte aligned, paged_attention_tree_workspace_size() bytes (for the current
  *                device; 152 SMs are assumed without a GPU), status word zeroed once (it is
  *                sticky); calls that share it must not overlap
+ * Scores and sums are fp32.  A weight is off by 2^-16 (bf16 pool), or enters times its key's V scale rounded to
+ * fp16 (FP8 pool: by 2^-12 of the product, or 2^-25 of the row's largest; V scales are meant to be above 2^-100).
+ * For an FP8 pool a query row is read as pairs of E4M3 codes: exact down to 2^-9 of its largest value, to
+ * 2^-17 of that below; a row with an infinity or a NaN is NaN.
  * A row that sees no key is zero.  A sequence with ctx < 1 or past its table
  * (PKV_STATUS_BAD_CONTEXT_LEN), ctx < n or n > max_q_len (PKV_STATUS_BAD_Q_LEN) gets zero rows; one whose
  * rows lie outside the tensors none (PKV_STATUS_BAD_Q_LEN).  A block with an invalid id
@@ -947,7 +952,8 @@ PKV_API int paged_attention_tree(void *out, int32_t out_dtype, const void *q, co
  *     max(p_i(v) - q_i(v), 0)  with draft_probs where a child was refused
  *     p_i(v)                   else, without draft_probs 0 for the refused children's tokens
  * and p_i where that is 0 everywhere (should p_i be too, the token is -1).  Products are
- * exact, sums are kept to 2^-48.  Probabilities that are NaN or below 0 count as 0, above 1
+ * exact, sums are held as pairs of fp32 numbers (over 128000 entries off by 2^-36 at most,
+ * commonly by 2^-45).  Probabilities that are NaN or below 0 count as 0, above 1
  * as 1; a draft outside [0, vocab_size), or whose parent is no node before it, is refused.
  *   tokens_out   : int32 [num_seqs][max_q_len], device: the accepted tokens, the last token, then -1
  *   path         : int32 [num_seqs][max_q_len], device: 0, the accepted nodes, then -1

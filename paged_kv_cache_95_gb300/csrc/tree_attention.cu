@@ -50,6 +50,11 @@
 // which enter P V rounded to fp16 (2^-12; as bf16 heads and remainders of V in bf16 a tile took
 // 1.4 times the instructions).  The reference m counts the exponent of a tile's largest V scale in, so that
 // weights times scales stay below 2^9.
+//
+// Measured (152 SMs, HBM 6.8 TB/s): 64 sequences of 512 .. 4096 tokens, trees of 5 .. 16 nodes, 32 heads over 8: 123 us for
+// 640 MB (94 at the copy rate); 8 of 32768, 16 nodes, 64 heads: 189 us for 1.08 GB (159); FP8, the ragged batch with trees of 16
+// .. 32 nodes: 160 us for 381 MB (56): not HBM but a tile's way bounds it, S and P V about 1000 cycles each from issue
+// to hand-off, the softmax 2000 for two tiles at once; four places of S are all that tensor memory holds.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
