@@ -22,7 +22,7 @@
 //    ahead of the pieces.  (One warp for both takes 2700 cycles for 64 keys, of which HBM leaves 1400;
 //    V by 16-byte asynchronous copies instead: what any warp reads then waits behind them, a
 //    piece's 128 rows of Q 6 us.)
-//  * 11 plans the CTA's range and fetches the pieces' Q rows, a piece ahead into two places in turn: by two
+//  * 11 fetches the pieces' Q rows, a piece ahead into two places in turn: by two
 //    TMA copies where a tile holds whole nodes (G divides 128), else row by row, which takes the warp
 //    9000 cycles for 128 rows (FP8, 64 sequences of 512 .. 4096 tokens: 221 us, 168 with the copies); the first
 //    piece's rows then come by the softmax warps, before the rings fill (behind full rings any
@@ -301,66 +301,85 @@ struct Walk {
     __device__ __forceinline__ int rows(const TreeParams &p) const { return min(kRows, s.n * p.group - row_tile * kRows); }
 };
 
-// The range of this CTA, by one warp: tiles of all sequences, then the sequence that the range starts in.  (On the way
-// of every call, with cold instruction caches: short code, and dividends that fit 32 bits divided in them.)
+// The range of this CTA, by the softmax warps, a thread a sequence: tiles of all sequences, then the sequence that the range
+// starts in.  (By one warp, 32 sequences after the other: 304 sequences of 512 tokens took 133 us for 127, 1000 of 100 tokens
+// 313 for 293; a lone sequence 0.3 us less.  On the way of every call, with cold instruction caches: short code, and dividends
+// that fit 32 bits divided in them.)
 __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
     if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
     return x / y;
 }
-__device__ __noinline__ Plan make_plan(const TreeParams &p, int lane, Lengths *known) {
-    Plan plan{};
+constexpr int kPlanThreads = 2 * kGroupWarps * 32;
+__device__ __noinline__ void make_plan(const TreeParams &p, Plan *slot, Lengths *known, int64_t *sums) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     Sequence s{};
+    int64_t upto = 0;  // this thread's tiles and those of the lanes before
     auto load = [&](int b) -> int64_t {  // tiles of all of a sequence's units
         s.tiles = 1;
         s.units = 0;
         if (b < p.num_seqs) s = load_sequence(p, b);
         return static_cast<int64_t>(s.units) * s.tiles;
     };
-    int64_t mine = 0, total = 0;
-    uint32_t wrong = 0;
-#pragma unroll 1
-    for (int b = lane; b < p.num_seqs; b += 32) {
-        total += mine = load(b);
-        wrong |= s.wrong;
-    }
-#pragma unroll 1
-    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    if (wrong && blockIdx.x == 0 && p.status) atomicOr(p.status, wrong);
-    plan.total = total;
-    // (no range of one tile while there are more: a second tile costs 0.7 us, the joining of twice the parts more; one
-    // sequence of 128 tokens and 8 KV heads takes 10.3 us for 12.0, of 1000 tokens 13.9 for 15.0, 4 tiles a range 14.1 and 15.0)
-    plan.ranges = static_cast<int>(min(static_cast<int64_t>(p.ranges), (total + 1) / 2));
-    if (static_cast<int>(blockIdx.x) >= plan.ranges) return plan;
-    plan.begin = divide(total * blockIdx.x, plan.ranges);
-    plan.count = static_cast<int>(divide(total * (blockIdx.x + 1), plan.ranges) - plan.begin);
-    int64_t before = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
-        if (p.num_seqs > 32) mine = load(b0 + lane);  // (else it is there)
-        int64_t upto = mine;
+    auto sum_warps = [&](int64_t x) {  // a warp's sum to its place, and x's scan
+        upto = x;
 #pragma unroll 1
         for (int off = 1; off < 32; off <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, upto, off);
             if (lane >= off) upto += y;
         }
-        upto += before;
-        const uint32_t past = __ballot_sync(0xffffffffu, upto > plan.begin);
-        before = __shfl_sync(0xffffffffu, upto, 31);
-        if (past) {  // the range starts in one of these 32 sequences
-            const int who = __ffs(past) - 1;
-            plan.b = b0 + who;
-            if (lane == who) {
-                const int64_t inside = plan.begin - (upto - mine);
-                plan.unit = static_cast<int>(divide(inside, s.tiles));
-                plan.tile = static_cast<int>(inside - static_cast<int64_t>(plan.unit) * s.tiles);
-                plan.s = s;
+        if (lane == 31) sums[warp] = upto;
+        softmax_sync();
+    };
+    int64_t mine = 0, all = 0;
+    uint32_t wrong = 0;
+#pragma unroll 1
+    for (int b = tid; b < p.num_seqs; b += kPlanThreads) {
+        all += mine = load(b);
+        wrong |= s.wrong;
+    }
+    if (wrong && blockIdx.x == 0 && p.status) atomicOr(p.status, wrong);
+    sum_warps(all);
+    int64_t total = 0;
+#pragma unroll 1
+    for (int w = 0; w < 2 * kGroupWarps; ++w) total += sums[w];
+    Plan plan{};
+    plan.total = total;
+    // (no range of one tile while there are more: a second tile costs 0.7 us, the joining of twice the parts more; one
+    // sequence of 128 tokens and 8 KV heads takes 10.3 us for 12.0, of 1000 tokens 13.9 for 15.0, 4 tiles a range 14.1 and 15.0)
+    plan.ranges = static_cast<int>(min(static_cast<int64_t>(p.ranges), (total + 1) / 2));
+    if (static_cast<int>(blockIdx.x) >= plan.ranges) {
+        if (tid == 0) *slot = plan;
+        return;
+    }
+    plan.begin = divide(total * blockIdx.x, plan.ranges);
+    plan.count = static_cast<int>(divide(total * (blockIdx.x + 1), plan.ranges) - plan.begin);
+    int64_t before = 0;  // tiles of the sequences before these
+#pragma unroll 1
+    for (int b0 = 0; b0 < p.num_seqs && before <= plan.begin; b0 += kPlanThreads) {
+        if (p.num_seqs > kPlanThreads) {  // (else they are there)
+            softmax_sync();
+            mine = load(b0 + tid);
+            sum_warps(mine);
+        }
+#pragma unroll 1
+        for (int w = 0; w < 2 * kGroupWarps; ++w) {
+            if (w == warp) {
+                const uint32_t past = __ballot_sync(0xffffffffu, before + upto > plan.begin);
+                if (past && before <= plan.begin) {  // the range starts in one of this warp's sequences
+                    known[lane] = {s.row0, s.n, s.ctx};
+                    if (lane == __ffs(past) - 1) {
+                        const int64_t inside = plan.begin - (before + upto - mine);
+                        plan.b = b0 + tid;
+                        plan.unit = static_cast<int>(divide(inside, s.tiles));
+                        plan.tile = static_cast<int>(inside - static_cast<int64_t>(plan.unit) * s.tiles);
+                        plan.s = s;
+                        *slot = plan;
+                    }
+                }
             }
-            known[lane] = {s.row0, s.n, s.ctx};
-            return plan;
+            before += sums[w];
         }
     }
-    plan.count = 0;  // (not reached: begin < total)
-    return plan;
 }
 
 // Sixteen E4M3 codes to fp16 (exact): a holds values 0 .. 7, b 8 .. 15.
@@ -641,11 +660,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
     }
     griddep_launch_dependents();
     griddep_wait();
-    if (warp == kWarpQ) {
-        const Plan plan = make_plan(p, lane, known);
-        // (the lane that holds the sequence; any, where the range is empty)
-        if (plan.count > 0 ? plan.s.units > 0 : lane == 0) *plan_slot = plan;
-    }
+    if (warp < 2 * kGroupWarps) make_plan(p, plan_slot, known, reinterpret_cast<int64_t *>(smem + L::kOffMl));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -388,3 +388,11 @@ def test_a_refused_length_of_many_rows(heads, n):
     want = p.want()
     assert bool(((out[:1].double().cpu() - want).abs() <= p.bound(want, torch.bfloat16)).all())
     assert not bool(out[1:n + 1].any()) and bool((out[n + 1:] == 7).all())
+
+
+@pytest.mark.parametrize("count", [256, 257, 700])
+def test_hundreds_of_sequences(count):
+    rng = random.Random(count)
+    nodes = [rng.choice([0, 0, 1, 2, 5]) for _ in range(count)]
+    nodes[-1] = 3
+    Problem(nodes, [max(1, n + rng.choice([0, 3, 64, 130])) for n in nodes], 4, 2, count == 257, seed=count).check()
