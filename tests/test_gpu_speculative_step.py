@@ -183,3 +183,28 @@ def test_a_captured_step_follows_the_device_data(fp8):
         for s in (eager, captured):
             s.accept()
         assert eager.held == captured.held
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_pool_past_32_bits(fp8):
+    """The same step, its blocks once in a small pool and once at the end of one of 2.3e9 values."""
+    s = Step(fp8, [5, 60], 12)
+    s.feed(9)
+    s.uniforms.fill_(0)  # every draft stands but the first
+    s.uniforms[[c + 1 for c, m in zip(s.host["cu"], s.n) if m > 1]] = 1 - 2.0 ** -24
+    blocks = 560_000  # of 2 KV heads x 16 x 128 values
+    shift = blocks - BLOCKS
+    small, large = s.pools, []
+    for t in small:
+        x = torch.empty(blocks, *t.shape[1:], dtype=t.dtype, device="cuda")
+        x[shift:].view(torch.uint8).copy_(t.view(torch.uint8))
+        large.append(x)
+    s.run()
+    want = [s.out.clone(), s.words.clone(), s.path.clone(), *s.bytes()]
+    s.pools, s.d_tables = large, s.d_tables + shift
+    s.slots[s.slots >= 0] += shift * 16
+    s.run()
+    got = [s.out, s.words, s.path, *(t[shift:].view(torch.uint8) for t in large)]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert any(node > i for path in s.path.tolist() for i, node in enumerate(path))  # (something moved)
