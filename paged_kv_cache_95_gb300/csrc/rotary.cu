@@ -36,11 +36,14 @@ struct Turn {
     float c[8], s[8];
 };
 
-__device__ __forceinline__ Turn load_turn(const uint64_t *frequencies, int unit, int32_t position, float magnitude) {
+template <bool INTERLEAVED>
+__device__ __forceinline__ Turn load_turn(const uint64_t *frequencies, int unit, int rotary_dim, int32_t position,
+                                          float magnitude) {
     Turn t;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint64_t turns = __ldg(reinterpret_cast<const unsigned long long *>(frequencies) + 8 * unit + i) *
+        const int pair = !INTERLEAVED ? 8 * unit + i : i < 4 ? 4 * unit + i : rotary_dim / 4 + 4 * unit + i - 4;
+        const uint64_t turns = __ldg(reinterpret_cast<const unsigned long long *>(frequencies) + pair) *
                                static_cast<uint64_t>(static_cast<int64_t>(position));
         const float half_turns = __ll2float_rn(static_cast<long long>(turns)) * 0x1p-63f;
         float s, c;
@@ -78,12 +81,13 @@ __device__ __forceinline__ void turn_pairs(float (&v)[16], const Turn &t) {
     }
 }
 
-// Where a unit's two vectors of 8 values lie in a head's row: pairs (i, i + rotary_dim / 2) in two
-// pieces; interleaved pairs and the values behind the rotated ones in one.
-template <bool INTERLEAVED>
-__device__ __forceinline__ int2 unit_places(int unit, int rotary_dim) {
-    if (!INTERLEAVED && kRotaryUnit * unit < rotary_dim) return make_int2(8 * unit, rotary_dim / 2 + 8 * unit);
-    return make_int2(16 * unit, 16 * unit + 8);
+// Where a unit's two vectors of 8 values lie in a head's row: one in each half of the rotated values (pairs (i, i +
+// rotary_dim / 2) want it so; interleaved pairs lie within a vector), or of the values behind them.  (Neighbouring lanes'
+// vectors are neighbours then.  As one piece of 32 bytes a unit 8192 tokens x 40 heads took 30.7 us interleaved, 26.6 so.)
+__device__ __forceinline__ int2 unit_places(int unit, int rotary_dim, int head_dim) {
+    const int at = 8 * unit;
+    if (2 * at < rotary_dim) return make_int2(at, rotary_dim / 2 + at);
+    return make_int2(rotary_dim / 2 + at, head_dim / 2 + at);
 }
 
 // Thread (token, s, unit) turns the unit of heads s, s + split, ...
@@ -99,11 +103,11 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryPara
     const int s = static_cast<int>(ts - token * split);
     if (token >= p.num_tokens) return;
     const bool turned = kRotaryUnit * unit < p.rotary_dim;
-    const int2 at = unit_places<INTERLEAVED>(unit, p.rotary_dim);
+    const int2 at = unit_places(unit, p.rotary_dim, p.head_dim);
     const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.x) + token * p.x_row;
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + token * p.out_row;
     Turn t;
-    if (turned) t = load_turn(p.frequencies, unit, __ldg(p.positions + token), p.magnitude);
+    if (turned) t = load_turn<INTERLEAVED>(p.frequencies, unit, p.rotary_dim, __ldg(p.positions + token), p.magnitude);
     else if (x == out && p.x_head == p.out_head) return;  // in place: nothing to copy
     for (int h0 = s; h0 < p.num_heads; h0 += kBatch * split) {
         uint4 a[kBatch], b[kBatch];
@@ -134,9 +138,10 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryPara
 // The append: a token's rows are its query heads, key heads and value heads in this order;
 // thread (token, s, unit of 8 a head) takes the unit of rows s, s + split, ...  A row's 8 units
 // are 8 neighbouring lanes, which share the maximum of an E4M3 row by shuffles.
-// E4M3: as kv_reshape_and_cache_fp8 has it, from the turned values in fp32 (one rounding, to the code).
+// E4M3: as kv_reshape_and_cache_fp8 has it, from the turned values in fp32 (one rounding, to the code).  (Ten blocks an SM, 96
+// registers: with 99, nine blocks, 16384 tokens take 69.6 us for 63.5.)
 template <bool INTERLEAVED, bool FP8>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_write_kernel(const RotaryWriteParams p, int split) {
+__global__ void __launch_bounds__(kRotaryThreads, FP8 ? 10 : 1) rotary_write_kernel(const RotaryWriteParams p, int split) {
     constexpr int kUnits = kHeadDim / kRotaryUnit;
     static_assert(kUnits == 8, "a row's units are 8 lanes");
     griddep_launch_dependents();
@@ -149,7 +154,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_write_kernel(const Rota
     if (token >= p.num_tokens) return;  // (whole groups of 8 lanes)
     const uint32_t group = 0xffu << (threadIdx.x & 24);
     const bool turned = kRotaryUnit * unit < p.rotary_dim;
-    const int2 at = unit_places<INTERLEAVED>(unit, p.rotary_dim);
+    const int2 at = unit_places(unit, p.rotary_dim, kHeadDim);
     const int64_t slot = __ldg(p.slot_mapping + token);
     const bool kept = slot >= 0 && slot < p.num_slots;  // else padding, or no slot of the pool: not written
     const int64_t block = slot / kBlockSize, place = slot - block * kBlockSize;
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_write_kernel(const Rota
     };
     load(s);  // (on their way while the sines are computed)
     Turn t;
-    if (turned) t = load_turn(p.frequencies, unit, __ldg(p.positions + token), p.magnitude);
+    if (turned) t = load_turn<INTERLEAVED>(p.frequencies, unit, p.rotary_dim, __ldg(p.positions + token), p.magnitude);
     for (int r0 = s; r0 < end; r0 += kBatch * split) {
         if (r0 != s) load(r0);
 #pragma unroll
