@@ -918,7 +918,7 @@ PKV_API int rotary_reshape_and_cache_fp8(void *q_out, const void *q, int64_t q_r
  *                device; 152 SMs are assumed without a GPU), status word zeroed once (it is
  *                sticky); calls that share it must not overlap
  * Scores and sums are fp32.  A weight is off by 2^-16 (bf16 pool), or enters times its key's V scale rounded to
- * fp16 (FP8 pool: by 2^-12 of the product, or 2^-25 of the row's largest; V scales are meant to be above 2^-100).
+ * fp16 (FP8 pool: by 2^-11 of the product, or 2^-25 of the row's largest; V scales are meant to be above 2^-100).
  * For an FP8 pool a query row is read as pairs of E4M3 codes: exact down to 2^-9 of its largest value, to
  * 2^-17 of that below; a row with an infinity or a NaN is NaN.
  * A row that sees no key is zero.  A sequence with ctx < 1 or past its table

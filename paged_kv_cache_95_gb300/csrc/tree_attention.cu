@@ -47,7 +47,7 @@
 // puts the row's largest value in [2^7, 2^8): exact down to 2^-9 of that value, 2^-17 of it below.
 // V's codes come into a ring of their own; 13-15 take every third tile each
 // and expand it to fp16 (exact) into the V ring.  K's scale multiplies the scores, V's the weights,
-// which enter P V rounded to fp16 (2^-12; as bf16 heads and remainders of V in bf16 a tile took
+// which enter P V rounded to fp16 (2^-11; as bf16 heads and remainders of V in bf16 a tile took
 // 1.4 times the instructions).  The reference m counts the exponent of a tile's largest V scale in, so that
 // weights times scales stay below 2^9.
 //

@@ -208,3 +208,30 @@ def test_a_pool_past_32_bits(fp8):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     assert any(node > i for path in s.path.tolist() for i, node in enumerate(path))  # (something moved)
+
+
+def test_two_steps_at_once():
+    """Two servers' steps on two streams, each with its own buffers: the bits of each alone."""
+    steps = [Step(fp8, [70, 15, 40], 12) for fp8 in (False, True)]
+    want = []
+    for s in steps:
+        s.feed(11)
+        s.start = [t.clone() for t in s.pools]
+        s.run()
+        want.append([s.out.clone(), s.words.clone(), *s.bytes()])
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(10):
+        for s in steps:
+            s.out.fill_(7)
+            s.words.fill_(7)
+            for t, x in zip(s.pools, s.start):
+                t.view(torch.uint8).copy_(x.view(torch.uint8))
+        torch.cuda.synchronize()
+        for s, stream in zip(steps, streams):
+            with torch.cuda.stream(stream):
+                s.run()
+        torch.cuda.synchronize()
+        for s, w in zip(steps, want):
+            rows = s.host["cu"][-1]
+            assert torch.equal(s.out[:rows], w[0][:rows]) and torch.equal(s.words, w[1])
+            assert all(torch.equal(a, b) for a, b in zip(s.bytes(), w[2:]))
