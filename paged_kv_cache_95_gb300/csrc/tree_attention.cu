@@ -1026,10 +1026,11 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                         sl2v = make_float2(1.f, 1.f);
                         if constexpr (FP8) {
                             k_scales = sbase + L::kOffOnes;
-                            // V scales that belong to no key may be anything: 1 (every warp writes the same)
+                            // V scales that belong to no key may be anything: 0, so that the largest below is of keys (every warp
+                            // writes the same)
 #pragma unroll 1
                             for (int k = lane; k < kKeys; k += 32)
-                                if (t * kKeys + k >= w.s.ctx || ((bad >> (k >> 4)) & 1)) sts32(scales + 4 * (kKeys + k), 0x3f800000u);
+                                if (t * kKeys + k >= w.s.ctx || ((bad >> (k >> 4)) & 1)) sts32(scales + 4 * (kKeys + k), 0u);
                             fence_proxy_async_smem();  // (the next copy there comes behind)
                             __syncwarp();
                         }
