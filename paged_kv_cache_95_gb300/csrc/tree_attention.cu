@@ -999,6 +999,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     }
                     const uint32_t scales = sbase + L::kOffScale + (j % (FP8 ? L::kStagesScale : 1)) * 2 * kKeys * 4;
                     float2 sl2v = make_float2(sl2, sl2);  // (bf16)
+                    uint32_t most_v = 0;  // FP8: the largest V scale (its bits) of the keys that the row sees
                     uint32_t k_scales = scales;
                     // Tiles that not every row sees whole: the scores are scaled and the hidden ones -inf before the pass below,
                     // which then scales them by 1.  (A loop of its own, once or twice a sequence: in the pass, whose code the
@@ -1019,6 +1020,8 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                             for (int k = 0; k < 16; ++k) {
                                 const float f = FP8 ? lds_f32(scales + 4 * (16 * c + k)) : sl2;
                                 x[k] = (bits >> k) & 1 ? __float_as_uint(__uint_as_float(x[k]) * f) : 0xff800000u;
+                                if (FP8 && ((bits >> k) & 1))
+                                    most_v = max(most_v, __float_as_uint(lds_f32(scales + 4 * (kKeys + 16 * c + k))) & 0x7fffffffu);
                             }
                             tmem_st_32x32b_x16(t_s + 16 * c, x);
                         }
@@ -1026,8 +1029,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                         sl2v = make_float2(1.f, 1.f);
                         if constexpr (FP8) {
                             k_scales = sbase + L::kOffOnes;
-                            // V scales that belong to no key may be anything: 0, so that the largest below is of keys (every warp
-                            // writes the same)
+                            // V scales that belong to no key may be anything: 0 (every warp writes the same)
 #pragma unroll 1
                             for (int k = lane; k < kKeys; k += 32)
                                 if (t * kKeys + k >= w.s.ctx || ((bad >> (k >> 4)) & 1)) sts32(scales + 4 * (kKeys + k), 0u);
@@ -1070,12 +1072,14 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     }
                     float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     if constexpr (FP8) {
-                        // and the exponent of the tile's largest V scale (a sum of weights of scales below 2^-90 would
-                        // leave fp32)
-                        const float2 sv = lds_f32x2(scales + (kKeys + 2 * lane) * 4);
-                        const uint32_t most = __reduce_max_sync(
-                            0xffffffffu, max(__float_as_uint(sv.x) & 0x7fffffffu, __float_as_uint(sv.y) & 0x7fffffffu));
-                        mt = fmaf(mt, sl2, static_cast<float>(min(max(static_cast<int>(most >> 23) - 127, -90), 100)));
+                        // and the exponent of the largest V scale of the tile's keys (a sum of weights of scales below 2^-90 would
+                        // leave fp32); where the rows do not see the same keys, of those that this one sees
+                        if (k_scales == scales) {
+                            const float2 sv = lds_f32x2(scales + (kKeys + 2 * lane) * 4);
+                            most_v = __reduce_max_sync(0xffffffffu,
+                                                       max(__float_as_uint(sv.x) & 0x7fffffffu, __float_as_uint(sv.y) & 0x7fffffffu));
+                        }
+                        mt = fmaf(mt, sl2, static_cast<float>(min(max(static_cast<int>(most_v >> 23) - 127, -90), 100)));
                         tmem_wait_st();
                     }
                     float alpha = 1.f;

@@ -62,3 +62,24 @@ def test_small_v_scales_beside_a_bad_block(by):
     p.tables[0][5] = -1
     got, _ = p.call()
     off(got, want, bound)
+
+
+# ---- V scales of keys that a row does not see ---------------------------------------------
+
+@pytest.mark.parametrize("up", [12, 24, 60])
+@pytest.mark.parametrize("ctx", [30, 64, 131])
+def test_a_hidden_node_with_a_far_larger_v_scale(up, ctx):
+    """Rows that do not see the node are as exact as without it (the bound leaves it out); rows that see it, as with it."""
+    nodes, hidden = 5, 2
+    masks = [1 << i for i in range(nodes)]
+    masks[4] |= 1 << hidden
+    p = Problem([nodes], [ctx], 8, 2, True, seed=ctx, masks=masks)
+    at = ctx - nodes + hidden
+    where = (p.tables[0][at // 16], slice(None), at % 16)
+    small = p.bound(p.want())
+    shrink(p, 2.0 ** up, where)
+    got, _ = p.call()
+    want = p.want()
+    blind = [i for i in range(nodes) if i != hidden and i != 4]
+    off(got[blind], want[blind], small[blind])
+    off(got, want, p.bound(want))
