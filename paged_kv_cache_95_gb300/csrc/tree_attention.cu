@@ -47,9 +47,8 @@
 // puts the row's largest value in [2^7, 2^8): exact down to 2^-9 of that value, 2^-17 of it below.
 // V's codes come into a ring of their own; 13-15 take every third tile each
 // and expand it to fp16 (exact) into the V ring.  K's scale multiplies the scores, V's the weights,
-// which enter P V rounded to fp16 (2^-11; as bf16 heads and remainders of V in bf16 a tile took
-// 1.4 times the instructions).  The reference m counts the exponent of a tile's largest V scale in, so that
-// weights times scales stay below 2^9.
+// which enter P V as fp16 heads and remainders (2^-22, as in the FP8 decode).  The reference m counts the exponent of
+// a tile's largest V scale in, so that weights times scales stay below 2^15.
 //
 // Measured (152 SMs, HBM 6.8 TB/s): 64 sequences of 512 .. 4096 tokens, trees of 5 .. 16 nodes, 32 heads over 8: 123 us for
 // 640 MB (94 at the copy rate); 8 of 32768, 16 nodes, 64 heads: 189 us for 1.08 GB (159); FP8, the ragged batch with trees of 16
@@ -79,12 +78,8 @@ constexpr uint32_t kVTile = kKeys * 256;         // 16 KB: 64 bf16 rows of V
 constexpr uint32_t kBlkBytes = 4096;             // one paged (block, head) tile of bf16 values
 constexpr uint32_t kCodeBytes = 2048;            // the same of codes
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;
-
-__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
+// FP8: weights times V scales are held 2^6 up, below 2^15 (fp16 ends at 2^16): what fp16 drops is then 2^-31 of the largest.
+constexpr int kUp = 6;
 
 template <bool FP8>
 struct Layout {
@@ -197,6 +192,16 @@ __device__ __forceinline__ bool softmax_wait(uint32_t bar, uint32_t parity, vola
 // The softmax warps of both groups.
 __device__ __forceinline__ void softmax_sync() {
     asm volatile("bar.sync 1, %0;" ::"n"(2 * kGroupWarps * 32) : "memory");
+}
+
+// P - head for a pair, head = the packed fp16 pair `h`: exact, since head is P rounded.
+__device__ __forceinline__ float2 minus_f16x2(float2 p, uint32_t h) {
+    float2 d;
+    asm("{\n\t.reg .b16 lo, hi, m;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b16 m, 0xBC00;\n\t"
+        "fma.rn.f32.f16 %0, lo, m, %3;\n\tfma.rn.f32.f16 %1, hi, m, %4;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "r"(h), "f"(p.x), "f"(p.y));
+    return d;
 }
 
 // P - head for a pair, head = the packed bf16 pair `h`: exact, since head is P truncated.
@@ -921,11 +926,11 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                     const uint32_t vb = sbase + L::kOffV + st * kVTile, d = tmem + kTmemO + 128 * (j & 1);
                     const uint32_t first = t - w.t0 < 2 ? 0u : 1u;
 #pragma unroll
-                    for (int s4 = 0; s4 < 4; ++s4) {  // keys 16 s4 ..: [8 columns heads | 8 remainders], FP8 8 columns in all
+                    for (int s4 = 0; s4 < 4; ++s4) {  // keys 16 s4 ..: [8 columns heads | 8 remainders]
                         const uint32_t at = tmem + kKeys * (j % kPlaces) + 16 * s4;
                         const uint64_t bd = sw128_desc(vb + s4 * kBlkBytes, 1024, 2048);
                         umma_bf16_tmem_a(d, at, bd, FP8 ? kIdescPV16 : kIdescPV, s4 > 0 ? 1u : first);
-                        if constexpr (!FP8) umma_bf16_tmem_a(d, at + 8, bd, kIdescPV, 1u);
+                        umma_bf16_tmem_a(d, at + 8, bd, FP8 ? kIdescPV16 : kIdescPV, 1u);
                     }
                     umma_commit(pv_done(j));
                     umma_commit(v_empty(st));
@@ -1079,7 +1084,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                             most_v = __reduce_max_sync(0xffffffffu,
                                                        max(__float_as_uint(sv.x) & 0x7fffffffu, __float_as_uint(sv.y) & 0x7fffffffu));
                         }
-                        mt = fmaf(mt, sl2, static_cast<float>(min(max(static_cast<int>(most_v >> 23) - 127, -90), 100)));
+                        mt = fmaf(mt, sl2, static_cast<float>(min(max(static_cast<int>(most_v >> 23) - 127 - kUp, -90), 100)));
                         tmem_wait_st();
                     }
                     float alpha = 1.f;
@@ -1112,7 +1117,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                         if (FP8 && c == 0) tmem_ld_32x32b_x32(t_s, reinterpret_cast<uint32_t (&)[32]>(v));
 #pragma unroll
                         for (int h = 0; h < kPass / 16; ++h) {  // 16 keys: 8 columns of heads, 8 of remainders
-                            uint32_t pk[FP8 ? 8 : 16];
+                            uint32_t pk[16];
 #pragma unroll
                             for (int e = 0; e < 8; e += 2) {
                                 const int k = 16 * h + 2 * e;
@@ -1127,6 +1132,9 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                                     py = fmul2(py, make_float2(__uint_as_float(f.z), __uint_as_float(f.w)));
                                     pk[e] = pack_f16x2(px.x, px.y);
                                     pk[e + 1] = pack_f16x2(py.x, py.y);
+                                    const float2 ex = minus_f16x2(px, pk[e]), ey = minus_f16x2(py, pk[e + 1]);
+                                    pk[8 + e] = pack_f16x2(ex.x, ex.y);
+                                    pk[9 + e] = pack_f16x2(ey.x, ey.y);
                                 } else {
                                     pk[e] = __byte_perm(__float_as_uint(px.x), __float_as_uint(px.y), 0x7632);
                                     pk[e + 1] = __byte_perm(__float_as_uint(py.x), __float_as_uint(py.y), 0x7632);
@@ -1135,10 +1143,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                                     pk[9 + e] = pack_bf16x2(ey.x, ey.y);
                                 }
                             }
-                            if constexpr (FP8)
-                                tmem_st_32x32b_x8(t_s + kPass * c + 16 * h, pk);
-                            else
-                                tmem_st_32x32b_x16(t_s + kPass * c + 16 * h, pk);
+                            tmem_st_32x32b_x16(t_s + kPass * c + 16 * h, pk);
                         }
                     }
                     const float2 rs = fadd2(rs0, rs1);

@@ -83,3 +83,84 @@ def test_a_hidden_node_with_a_far_larger_v_scale(up, ctx):
     blind = [i for i in range(nodes) if i != hidden and i != 4]
     off(got[blind], want[blind], small[blind])
     off(got, want, p.bound(want))
+
+
+# ---- weights ------------------------------------------------------------------------------
+
+class Exact(Problem):
+    """Rows of Q with one value other than 0 (a power of two) and whole numbers of up to 15 as its keys' codes, so that q k is
+    exact whatever the accumulator; K scales, V scales and V as they come."""
+
+    def __init__(self, nodes, ctx, heads, kv, seed, spread=8.0):
+        super().__init__(nodes, ctx, heads, kv, True, seed=seed)
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed + 1)
+        self.q.zero_()
+        self.q[..., 3] = 1.0
+        whole = torch.randint(-15, 16, self.k.shape[:3], generator=g, device="cuda").float()
+        hole = self.k.view(torch.uint8)[..., 0] == 0x7F
+        s = torch.where(hole, 1.0, self.scales["k_scale"])
+        put(self.k, (..., 3), torch.where(hole, float("nan"), whole))
+        self.kd[..., 3] = (whole * s).double()
+        self.scale = spread / 15  # scores in +-spread
+
+    def tight(self, want):
+        """A score of up to 8 (12 in the log2 domain) is off by 2^-24 of it for each of three roundings (the K scale, the row's
+        factor, the reference): 12 x 3 x 2^-24 x ln 2 < 2^-19 of a weight; exp2 by 2^-21; its product with the V scale by
+        2^-24, its two fp16 parts by 2^-22 or 2^-31 of the row's largest times the tile's largest V scale (here at most 2^7
+        above the least); a sum of n fp32 terms, each entering as two, by 2 n 2^-23.  A mean by these of sum w |v|, once
+        for the numerator and once for the sum."""
+        n = max(self.ctx)
+        each = 2.0 ** -19 + 2.0 ** -21 + 2.0 ** -24 + 2.0 ** -22 + n * 2.0 ** -22
+        mean = R.tree_attention(self.q, self.masks, self.cu, self.kd, self.vd.abs(), self.tables, self.ctx, self.scale)
+        live = torch.unique(torch.tensor([b for t, c in zip(self.tables, self.ctx) for b in t[:-(-c // 16)]])).cuda()
+        return each * (mean + want.abs()) + n * 2.0 ** -30 * float(self.vd[live].abs().max()) + want.abs() * 2.0 ** -23
+
+
+@pytest.mark.parametrize("nodes,ctx", [([1], [7]), ([3], [24]), ([4, 9], [64, 40]), ([16], [150]), ([5], [300])])
+def test_weights_keep_22_bits(nodes, ctx):
+    """As the FP8 decode and verify of the same pool do.  (With one fp16 value a weight, off by up to 2^-11, rows of few keys are past
+    the bound.)"""
+    p = Exact(nodes, ctx, 8, 2, seed=sum(ctx))
+    got, ws = p.call()
+    want = p.want()
+    off(got, want, p.tight(want))
+
+
+@pytest.mark.parametrize("ctx", [40, 150])
+def test_a_chain_holds_what_verify_holds(ctx):
+    """The same rows through both entry points: off the definition by the same bound."""
+    p = Exact([4, 4], [ctx, ctx + 9], 4, 2, seed=ctx)
+    p.masks = [1, 3, 7, 15] * 2
+    got, _ = p.call(extra=0)
+    out = torch.empty_like(got)
+    P.paged_attention_verify(out, p.q, 4, p.k, p.v, i32(p.tables), i32(p.ctx), p.scale, kernel=P.PKV_VERIFY_DECODE_KERNEL,
+                             **p.scales)
+    want = p.want()
+    off(out, want, p.tight(want))
+    off(got, want, p.tight(want))
+
+
+@pytest.mark.parametrize("gap", [0, 8, 16, 20])
+def test_a_heavy_key_with_a_small_v_scale(gap):
+    """A key with nearly all of the weight and a V scale 2^-gap of its tile's largest keeps 2^-(31 - gap) of its value."""
+    p = Exact([1], [20], 4, 1, seed=gap)
+    b, i = p.tables[0][0], 5
+    low = torch.full((1, 16), -15.0, device="cuda")
+    put(p.k, (b, slice(None), slice(None), 3), low)
+    put(p.k, (p.tables[0][1], slice(None), slice(0, 4), 3), low[:, :4])
+    put(p.k, (b, slice(None), i, 3), -low[:, 0])
+    s = p.scales["k_scale"]
+    s[p.tables[0]] = torch.where(torch.isnan(s[p.tables[0]]), s[p.tables[0]], 1.0)
+    p.kd[p.tables[0]] = 0
+    p.kd[p.tables[0], ..., 3] = -15
+    p.kd[b, :, i, 3] = 15
+    p.scale = 1.0  # the others weigh e^-30
+    vs = p.scales["v_scale"]
+    vs[p.tables[0]] = torch.where(torch.isnan(vs[p.tables[0]]), vs[p.tables[0]], 1.0)
+    vs[b, :, i] = 1.2987013 * 2.0 ** -gap
+    p.vd[b, :, i] = p.v[b, :, i].double() * float(vs[b, 0, i])
+    got, _ = p.call()
+    want = p.vd[b, 0, i].cpu().expand(1, 4, 128)
+    # the others: 19 of e^-30 x 448; the key's: two fp16 parts
+    off(got, want, 19 * math.exp(-30) * 448 + (2.0 ** -20 + 2.0 ** -(30 - gap)) * want.abs() + 1e-12)
