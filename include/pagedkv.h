@@ -920,8 +920,8 @@ PKV_API int rotary_reshape_and_cache_fp8(void *q_out, const void *q, int64_t q_r
  * Scores and sums are fp32.  A weight is off by 2^-16 (bf16 pool), or enters times its key's V scale rounded to
  * fp16 (FP8 pool: by 2^-11 of the product, or 2^-25 of the row's largest; V scales are meant to be above 2^-100).
  * For an FP8 pool a query row is read as pairs of E4M3 codes: exact down to 2^-9 of its largest value, to
- * 2^-17 of that below; a row with an infinity or a NaN is NaN.
- * A row that sees no key is zero.  A sequence with ctx < 1 or past its table
+ * 2^-17 of that below; a row with an infinity or a NaN is NaN (where it sees a key).
+ * A row that sees no key is zero, whatever its query.  A sequence with ctx < 1 or past its table
  * (PKV_STATUS_BAD_CONTEXT_LEN), ctx < n or n > max_q_len (PKV_STATUS_BAD_Q_LEN) gets zero rows; one whose
  * rows lie outside the tensors none (PKV_STATUS_BAD_Q_LEN).  A block with an invalid id
  * contributes nothing (PKV_STATUS_BAD_BLOCK_ID).  Slots that belong to no key may hold anything; a

@@ -474,12 +474,13 @@ __device__ __noinline__ void load_q(const TreeParams &p, int row0, int first, in
                     e4m3x4_to_f16x2x2(hi[k], f0, f1);
                     lo[k] = f16x2_to_e4m3x2(sub_f16x2(x[0], f0)) | (f16x2_to_e4m3x2(sub_f16x2(x[1], f1)) << 16);
                 }
+                // (a row with an infinity has no finite scores: codes of NaN, as one of 448 would not say)
+                if (most == 0x7f800000u) hi[0] = hi[1] = hi[2] = hi[3] = 0x7f7f7f7fu;
                 const uint32_t to = dst + r * 128 + (((2 * c + h) ^ (r & 7)) << 4);
                 sts128(to, make_uint4(hi[0], hi[1], hi[2], hi[3]));
                 sts128(to + kHalfTile, make_uint4(lo[0], lo[1], lo[2], lo[3]));
             }
-            // (a row with an infinity has no finite scores: NaN, as a code of 448 would not say)
-            if (c == 0) factor[r] = most == 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            if (c == 0) factor[r] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         }
     }
     fence_proxy_async_smem();

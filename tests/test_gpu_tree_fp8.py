@@ -164,3 +164,20 @@ def test_a_heavy_key_with_a_small_v_scale(gap):
     want = p.vd[b, 0, i].cpu().expand(1, 4, 128)
     # the others: 19 of e^-30 x 448; the key's: two fp16 parts
     off(got, want, 19 * math.exp(-30) * 448 + (2.0 ** -20 + 2.0 ** -(30 - gap)) * want.abs() + 1e-12)
+
+
+# ---- rows of Q ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fp8,what", [(False, float("nan")), (True, float("nan")), (True, float("inf")), (True, float("-inf"))])
+def test_rows_of_q_that_are_not_finite(fp8, what):
+    """Such a row is NaN, or zero where it sees no key; the others are what they were."""
+    masks = [0, 1 << 1, 0, 1 << 3]
+    p = Problem([4, 3], [4, 150], 4, 2, fp8, seed=21, masks=masks + [1, 3, 5])
+    whole, _ = p.call()
+    p.q[0, 1, 5], p.q[1, 2, 127], p.q[5, 0, 64] = what, what, what
+    got, _ = p.call()
+    nan = torch.zeros(7, 4, dtype=torch.bool)
+    nan[1, 2] = nan[5, 0] = True
+    assert torch.equal(torch.isnan(got).all(-1).cpu(), nan)
+    keep = ~nan.cuda()
+    assert torch.equal(got[keep], whole[keep]) and not got[0].any() and not got[2].any()
