@@ -751,7 +751,6 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                 }
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
         // (given up: the copies still on their way land before the CTA ends)
         if (!ok && lane == 0)
 #pragma unroll 1
