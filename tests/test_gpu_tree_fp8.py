@@ -181,3 +181,137 @@ def test_rows_of_q_that_are_not_finite(fp8, what):
     assert torch.equal(torch.isnan(got).all(-1).cpu(), nan)
     keep = ~nan.cuda()
     assert torch.equal(got[keep], whole[keep]) and not got[0].any() and not got[2].any()
+
+
+@pytest.mark.parametrize("by", [-100, -30, 40, 100])
+def test_rows_of_q_of_any_size(by):
+    """Powers of two that the softmax scale undoes change no bit: a row's codes are those of its largest value."""
+    p = Problem([5, 16], [300, 90], 8, 2, True, seed=22)
+    want, _ = p.check()
+    p.q *= 2.0 ** by
+    got, _ = p.call(scale=p.scale * 2.0 ** -by)
+    assert torch.equal(got, want)
+
+
+def test_rows_of_q_that_are_zero_or_nearly():
+    p = Problem([4, 2], [200, 64], 4, 2, True, seed=23)
+    p.q[0], p.q[4, 1] = 0.0, 0.0
+    p.q[1] *= 2.0 ** -120
+    p.q[2, 0] *= 2.0 ** -133  # the least bf16 numbers
+    p.check()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 8.0])
+def test_softmax_scales(scale):
+    p = Problem([16, 30], [500, 30], 4, 2, True, seed=4)
+    p.check(scale=scale / SCALE * p.scale)
+
+
+def test_large_scores_and_equal_ones():
+    """Weights that pass the running reference in every tile, far and by little; and a row of equal scores."""
+    p = Exact([4, 4], [1500, 1400], 8, 2, seed=12)
+    s = p.scales["k_scale"]
+    s[:] = torch.where(torch.isnan(s), s, 1.0)
+    p.kd.zero_()
+    ramp = torch.linspace(0, 60, 1500, device="cuda")
+    for b, up in ((0, ramp), (1, ramp.flip(0)[:1400])):
+        for j in range(0, p.ctx[b], 16):
+            n = min(16, p.ctx[b] - j)
+            codes = (up[j:j + n] * 7).to(F8)
+            put(p.k, (p.tables[b][j // 16], slice(None), slice(0, n), 3), codes.expand(2, n))
+            p.kd[p.tables[b][j // 16], :, :n, 3] = codes.double()
+    p.scale = 1 / 7
+    p.q[3] = 0.0
+    got, _ = p.call()
+    want = p.want()
+    # (scores of up to 60: 87 x 3 x 2^-24 x ln 2 < 2^-16 of a weight in the place of 2^-19)
+    off(got, want, 2 * p.tight(want))
+
+
+def test_keys_that_are_not_finite():
+    """A code of NaN, and scales that are NaN or infinite, reach the rows that see their key and no others."""
+    p = Problem([4, 4], [300, 300], 4, 2, True, seed=13, masks=[1, 3, 5, 9] * 2)
+    p.k.view(torch.uint8)[p.tables[0][297 // 16], 0, 297 % 16, 5] = 0x7F  # the code of NaN: node 1 of sequence 0, KV head 0
+    got, _ = p.call()
+    nan = torch.isnan(got).all(-1).cpu()
+    assert nan[1, :2].all() and int(nan.sum()) == 2 and int(torch.isnan(got).any(-1).sum()) == 2
+    p.scales["k_scale"][p.tables[0][298 // 16], 1, 298 % 16] = float("nan")  # node 2, KV head 1
+    got, _ = p.call()
+    nan = torch.isnan(got).all(-1).cpu()
+    assert nan[1, :2].all() and nan[2, 2:].all() and int(nan.sum()) == 4 and int(torch.isnan(got).any(-1).sum()) == 4
+    p.v.view(torch.uint8)[p.tables[1][0], 1, 3, 7] = 0xFF  # a key of the prefix
+    got, _ = p.call()
+    assert bool(torch.isnan(got[4:, 2:, 7]).all()) and bool(torch.isfinite(got[4:, :2]).all())
+    p.scales["v_scale"][p.tables[1][2], 0, 1] = float("inf")
+    got, _ = p.call()
+    assert not bool(torch.isfinite(got[4:, :2]).any())
+
+
+def test_graph_streams_and_a_shared_workspace():
+    p, r = Problem([8, 3], [600, 40], 8, 2, True, seed=14), Problem([64], [2500], 4, 4, True, seed=15)
+    want_p, ws = p.call()
+    need = P.paged_attention_tree_workspace_size(1, 4, 64, P.cache_desc(r.k))
+    ws = torch.zeros(max(need, ws.numel()), dtype=torch.uint8, device="cuda")
+    want_r, _ = r.call()
+    out_p, out_r = torch.zeros_like(want_p), torch.zeros_like(want_r)
+    args = [(x.q, i64(x.masks), i32(x.cu), x.most, x.k, x.v, i32(x.tables), i32(x.ctx), x.scale) for x in (p, r)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        P.paged_attention_tree(out_p, *args[0], workspace=ws, **p.scales)
+        P.paged_attention_tree(out_r, *args[1], workspace=ws, **r.scales)
+    for _ in range(3):
+        out_p.zero_(), out_r.zero_()
+        graph.replay()
+        assert torch.equal(out_p, want_p) and torch.equal(out_r, want_r)
+    args[0][7].copy_(i32([600 - 100, 40]))  # lengths changed under the graph
+    graph.replay()
+    torch.cuda.synchronize()
+    p.ctx = [500, 40]
+    assert torch.equal(out_p, p.call()[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out_r.zero_()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    P.paged_attention_tree(out_r, *args[1], stream=s, **r.scales)
+    s.synchronize()
+    assert not torch.cuda.current_stream().query()
+    assert torch.equal(out_r, want_r)
+
+
+# ---- partials -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("peaks", [False, True])
+@pytest.mark.parametrize("fp8", POOLS)
+@pytest.mark.parametrize("nodes,ctx,heads", [(12, 70000, 2), (43, 5000, 3), (5, 3300, 8), (64, 9000, 4)])
+def test_every_part_counts(nodes, ctx, heads, fp8, peaks):
+    """The values say which tile of 64 keys they come from (a 1 in the place of the tile's number modulo 128), so that an output
+    is the share of few tiles: a part left out or taken twice changes its tiles' places by a tenth and more.
+
+    Equal scores: weights of 1 and whole sums below 2^24, exact but for the division and the output (2^-22).  Scores of whole
+    numbers by the tile (0 .. 4 natural units, in no order): a weight is off by 6 x 3 x 2^-24 ln 2 + 2^-21 < 2^-19 and
+    2^-16 (bf16 parts); sums run over a part (8 tiles at most: 512 keys, each entering as two values) and over up to
+    152 parts: (2 x 512 + 152) x 2^-23 < 2^-12; 2^-11 covers numerator and sum."""
+    p = Problem([nodes], [ctx], heads, 1, fp8, seed=6)
+    key = torch.arange(ctx, device="cuda")
+    tile = key // 64
+    table = torch.tensor(p.tables[0], device="cuda")
+    at = (table[key // 16], 0, key % 16)
+    units = (tile * 37 % 5).float()
+    values = torch.nn.functional.one_hot(tile % 128, 128).float()
+    keys = torch.zeros(ctx, 128, device="cuda")
+    keys[:, 0] = units
+    p.q.zero_()
+    if peaks:
+        p.q[..., 0] = 1.0
+    p.scale = 1.0
+    for pool, x in ((p.k, keys), (p.v, values)):
+        put(pool, at, x)
+    for s in p.scales.values():
+        s[at] = 1.0
+    seen = torch.ones(nodes, ctx, dtype=torch.bool)
+    seen[:, ctx - nodes:] = torch.tensor([[m >> j & 1 for j in range(nodes)] for m in p.masks]).bool()
+    weight = torch.exp(units.double() * (1.0 if peaks else 0.0)).cpu() * seen
+    want = (weight / weight.sum(-1, keepdim=True)) @ values.double().cpu()
+    got, _ = p.call()
+    off(got, want[:, None].expand(-1, heads, -1), want[:, None] * 2.0 ** (-11 if peaks else -22))
