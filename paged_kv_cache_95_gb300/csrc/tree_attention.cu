@@ -724,6 +724,7 @@ __global__ void __launch_bounds__(Layout<FP8>::kThreads, 1)
                         sts32(sbase + L::kOffBad + 4 * (j & 15) + (is_k ? 0 : 64), bad);
                         if (is_k && bad && p.status) atomicOr(p.status, kStatusBadBlockId);
                     }
+                    __syncwarp();  // (before whichever lane is elected arrives)
                 }
                 int block[kTileBlocks];
 #pragma unroll
