@@ -968,7 +968,9 @@ PKV_API int paged_attention_tree(void *out, int32_t out_dtype, const void *q, co
  *   cu_q_lens    : int32 [num_seqs + 1], device, non-decreasing, from 0
  *   max_q_len    : host upper bound of the nodes a sequence, 1 .. PKV_MAX_TREE_NODES
  *   status       : device uint32 into which PKV_STATUS_BAD_Q_LEN is ORed for a sequence whose rows
- *                  lie outside the tensors or are more than max_q_len (count 0), or NULL
+ *                  lie outside the tensors or are more than max_q_len (count 0), or NULL (not told
+ *                  apart from an empty sequence then); the first word of paged_attention_tree's
+ *                  workspace will do, one for the whole step
  *   num_seqs     : 1 .. 65535;  vocab_size : 1 .. 2^24
  * Errors: PKV_ERR_INVALID_ARG / PKV_ERR_UNSUPPORTED / PKV_ERR_CUDA.
  */
@@ -986,7 +988,8 @@ PKV_API int speculative_verify(int32_t *tokens_out, int32_t *path, int32_t *coun
  * path and counts are speculative_verify's (path[i] >= i).  Bit-exact.
  *   k_scale, v_scale : NULL for a bf16 cache; required for PKV_DTYPE_FP8_E4M3 (16-byte aligned)
  *   path             : int32 [num_seqs][path_len], device;  path_len : 1 .. PKV_MAX_TREE_NODES
- *   status           : device uint32 into which PKV_STATUS_* bits are ORed, or NULL
+ *   status           : device uint32 into which PKV_STATUS_* bits are ORed, or NULL (as for
+ *                      speculative_verify)
  * A sequence whose lengths do not fit (more path than nodes, more nodes than context, a
  * context past its table) moves nothing, a node before its place or past the tree is skipped
  * (PKV_STATUS_BAD_Q_LEN, _BAD_CONTEXT_LEN), as is one in a block with an invalid id

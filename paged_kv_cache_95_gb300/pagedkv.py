@@ -1171,7 +1171,9 @@ def speculative_verify(tokens_out, path, counts, target_probs, tokens, cu_q_lens
     [total_rows], ``uniforms`` fp32 [total_rows], a row per node; ``parents`` int32 [total_rows]
     (None: chains) or ``draft_probs`` like ``target_probs`` (chains: what each node's child was
     drawn from).  Results: ``tokens_out`` and ``path`` int32 [num_seqs, max_q_len] (padded with
-    -1) and ``counts`` int32 [num_seqs]."""
+    -1) and ``counts`` int32 [num_seqs].  ``status``: int32 [1] into which PKV_STATUS_BAD_Q_LEN is ORed
+    for a sequence whose rows do not fit (``workspace[:4].view(torch.int32)`` of
+    :func:`paged_attention_tree` is one word for a whole step); None: such a sequence only has count 0."""
     torch = _torch()
     device, stream = _device_and_stream(stream)
     (n,), cu = _flat(cu_q_lens, "cu_q_lens", torch.int32, 1, device)
@@ -1205,7 +1207,8 @@ def kv_compact_path(k_cache, v_cache, block_tables, context_lens, cu_q_lens, pat
                     status=None, stream=None) -> None:
     """Move the accepted path's rows to consecutive places: position c + path[b, i] to c + i for
     0 < i < counts[b], c = context_lens[b] less the sequence's nodes, in both caches (and, for an
-    FP8 cache, in both scale arrays).  ``path`` and ``counts``: :func:`speculative_verify`."""
+    FP8 cache, in both scale arrays).  ``path`` and ``counts``: :func:`speculative_verify`.
+    ``status``: as there; None: what does not fit is not moved, and nothing says so."""
     torch = _torch()
     device, stream = _device_and_stream(stream)
     desc, _, _, k_at, v_at, ks, vs = _kv_pool(k_cache, v_cache, k_scale, v_scale, device)
