@@ -917,8 +917,10 @@ PKV_API int rotary_reshape_and_cache_fp8(void *q_out, const void *q, int64_t q_r
  *   workspace  : 256-byte aligned, paged_attention_tree_workspace_size() bytes (for the current
  *                device; 152 SMs are assumed without a GPU), status word zeroed once (it is
  *                sticky); calls that share it must not overlap
- * Scores and sums are fp32.  A weight is off by 2^-16 (bf16 pool), or enters times its key's V scale rounded to
- * fp16 (FP8 pool: by 2^-11 of the product, or 2^-25 of the row's largest; V scales are meant to be above 2^-100).
+ * Scores and sums are fp32.  Over a bf16 pool a weight is off by 2^-16.  Over an FP8 pool a weight times its
+ * key's V scale is off by 2^-22, or by 2^-31 of the largest weight times the largest V scale of 64 positions (counted from
+ * 0; the scales of keys that the row sees), whichever is more: a key whose V scale is 2^-k of another's of the same 64
+ * keeps 31 - k bits.  V scales are meant to lie between 2^-100 and 2^100.
  * For an FP8 pool a query row is read as pairs of E4M3 codes: exact down to 2^-9 of its largest value, to
  * 2^-17 of that below; a row with an infinity or a NaN is NaN (where it sees a key).
  * A row that sees no key is zero, whatever its query.  A sequence with ctx < 1 or past its table
@@ -952,7 +954,7 @@ PKV_API int paged_attention_tree(void *out, int32_t out_dtype, const void *q, co
  *     max(p_i(v) - q_i(v), 0)  with draft_probs where a child was refused
  *     p_i(v)                   else, without draft_probs 0 for the refused children's tokens
  * and p_i where that is 0 everywhere (should p_i be too, the token is -1).  Products are
- * exact, sums are held as pairs of fp32 numbers (over 128000 entries off by 2^-36 at most,
+ * exact (with an r below 1: to 2^-52), sums are held as pairs of fp32 numbers (over 128000 entries off by 2^-36 at most,
  * commonly by 2^-45).  Probabilities that are NaN or below 0 count as 0, above 1
  * as 1; a draft outside [0, vocab_size), or whose parent is no node before it, is refused.
  *   tokens_out   : int32 [num_seqs][max_q_len], device: the accepted tokens, the last token, then -1

@@ -383,7 +383,8 @@ int speculative_verify(int32_t *tokens_out, int32_t *path, int32_t *counts, cons
     p.total_rows = total_q_rows;
     p.vocab = vocab_size;
     // CTAs a sequence: one for every 4096 entries, up to a portable cluster of 8, as long as all run at once, two an
-    // SM (64 rows of 128000 with the drafter's take 25 us in 4 CTAs each, 33 in 8; 256 of 32000 take 27 in 2, 68 in 8).
+    // SM (with the drafter's rows: 64 of 128000 take 19.5 us in 4 CTAs each, 26 in 2 or 8; 160 of 128000 46 in 1, 48 in 2, 56 in 8;
+    // 256 of 128000 55 in 1, 57 in 2, 85 in 8; 256 of 32000 20 in 1, 28 in 2; 16 of 50257 10.2 in 8, 11.0 in 4, 15.2 in 1).
     int cluster = 1;
     while (cluster < pkv::kVerifyMaxCluster && static_cast<int64_t>(cluster) * 4096 < vocab_size &&
            static_cast<int64_t>(cluster) * num_seqs <= sms)

@@ -22,9 +22,10 @@
 //    ahead of the pieces.  (One warp for both takes 2700 cycles for 64 keys, of which HBM leaves 1400;
 //    V by 16-byte asynchronous copies instead: what any warp reads then waits behind them, a
 //    piece's 128 rows of Q 6 us.)
-//  * 11 fetches the pieces' Q rows, a piece ahead into two places in turn: by two
+//  * 11 fetches the pieces' Q rows into two places in turn, a piece ahead (FP8: behind the last scales of the piece before): by two
 //    TMA copies where a tile holds whole nodes (G divides 128), else row by row, which takes the warp
-//    9000 cycles for 128 rows (FP8, 64 sequences of 512 .. 4096 tokens: 221 us, 168 with the copies); the first
+//    9000 cycles for 128 rows (FP8, 64 sequences of 512 .. 4096 tokens: 221 us, 168 with the copies; over a bf16 pool
+//    these rows come while the piece before runs: 5 query heads a KV head 118 us for the 115 of 4); the first
 //    piece's rows then come by the softmax warps, before the rings fill (behind full rings any
 //    read takes 5 us).  FP8: it also makes them codes, and fetches every tile's scales.
 //  * 9 issues S = Q K^T, 10 P V (run whole, one elected lane issues: descriptors stay in uniform
@@ -52,8 +53,10 @@
 //
 // Measured (152 SMs, HBM 6.8 TB/s): 64 sequences of 512 .. 4096 tokens, trees of 5 .. 16 nodes, 32 heads over 8: 123 us for
 // 640 MB (94 at the copy rate); 8 of 32768, 16 nodes, 64 heads: 189 us for 1.08 GB (159); FP8, the ragged batch with trees of 16
-// .. 32 nodes: 160 us for 381 MB (56): not HBM but a tile's way bounds it, S and P V about 1000 cycles each from issue
-// to hand-off, the softmax 2000 for two tiles at once; four places of S are all that tensor memory holds.
+// .. 32 nodes: 192 us for 381 MB (56), not HBM: with one piece of 256 tiles a CTA a tile takes 0.80 us (bf16 0.73, the copy
+// rate): S and P V about 1000 cycles each from issue to hand-off, the softmax 2000 for two tiles at once, four places of S, all
+// that tensor memory holds; and a piece's change takes 6 to 8 us (bf16 1.6 to 2.6): by the order of warp 11's work Q of the next
+// piece is asked for behind this one's last scales, and its codes and first scales come after that.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
